@@ -238,11 +238,11 @@ def _run_own(s, c):
 # ---------------------------------------------------------------- plain forms
 
 def _plain_gates(x, gate, c):
-    x, gate = x.float(), gate.float()
+    gate = gate.float()
     a = torch.sigmoid(gate) if c["logits"] else gate
     if not c["lerp"]:
-        return a, x
-    return a, (torch.sigmoid(-gate) if c["logits"] else 1.0 - gate) * x
+        return a, x.to(F32, copy=True)  # the callers add the first states to it
+    return a, (torch.sigmoid(-gate) if c["logits"] else 1.0 - gate) * x.float()
 
 
 def _recurrence(a, b):

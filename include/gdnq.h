@@ -455,6 +455,175 @@ gdnq_status gdnq_prefill_resume(const gdnq_prefill_params* p, const int32_t* cu_
                                 void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
+ * gdnq_scan_* -- gated linear recurrence over channels: next to the matrix
+ *   states above, the token mixer whose state is one value per channel.
+ *
+ *       h_t = a_t h_{t-1} + b_t         (elementwise over C channels)
+ *
+ *   a_t = gate_t, or sigmoid(gate_t) with GDNQ_SCAN_LOGITS;
+ *   b_t = x_t,    or (1 - a_t) x_t   with GDNQ_SCAN_LERP (1 - a is formed
+ *   without cancellation from logits).  The state is fp32 throughout; y is h
+ *   rounded once to the call's dtype.
+ *
+ *   p->batch B sequences; p->seqlen T tokens each (cu_seqlens NULL, arrays
+ *   [B,T,C]) or T packed tokens in total (cu_seqlens [B+1] int32 on the
+ *   device as for gdnq_prefill_varlen, arrays [T,C]; sequences of length 0
+ *   are allowed).  Tokens that no sequence holds (before cu_seqlens[0], from
+ *   cu_seqlens[B] on) are left as they were in y, dx and dgate.  Offsets are
+ *   clamped to [0, T]; malformed ones give unspecified results and no access
+ *   outside the buffers.  p->channels C >= 1 (even C is faster in bf16);
+ *   p->dtype (x, gate, y and their gradients) GDNQ_F32 or GDNQ_BF16; B >= 0,
+ *   T >= 0, at most 2^31 - 1 tokens and B C <= 2^31 - 1.
+ *   A NaN or infinity stays in its own channel and sequence.
+ *
+ *   gdnq_scan_forward
+ *     x, gate [.., C] dtype     h0 [B,C] fp32 or NULL (zero)
+ *     y       [.., C] dtype     h_last [B,C] fp32 or NULL (not wanted): the
+ *             state after each sequence's last token (h0 for length 0)
+ *     carry   [ceil(tokens / GDNQ_SCAN_CHUNK), C] fp32 or NULL: the state
+ *             that enters every GDNQ_SCAN_CHUNK-th token, for the backward
+ *             pass (tokens counted through the whole call, B*T or T packed)
+ *   gdnq_scan_backward: gradients from dy (and dh_last or NULL = zero), with
+ *     the forward call's x, gate, h0, carry, cu_seqlens and flags:
+ *       l_t = dy_t + a_{t+1} l_{t+1} inside a sequence, from dh_last
+ *       dx = l (1 - a, with LERP),  da = l (h_{t-1} - x, with LERP; else
+ *       l h_{t-1}),  dgate = da (a (1 - a) da with LOGITS),  dh0 = a_1 l_1
+ *     dx, dgate [.., C] dtype; dh0 [B,C] fp32 or NULL (not wanted); h0 NULL
+ *     when the forward call's was.
+ *   gdnq_scan_step: one token per sequence (p->seqlen must be 1):
+ *     x, gate, y [B,C] dtype; h [B,C] fp32 read, h_out [B,C] fp32 written
+ *     (h_out may be h itself: the state updated in place).
+ *   Outputs must not overlap inputs or each other (but h_out = h).
+ *   workspace: gdnq_scan_workspace_size(p) bytes, for forward and backward
+ *   alike; its contents need no initial value.  Calls that may overlap in
+ *   time take workspaces of their own.
+ *   Results do not depend on the order in which workgroups run: the same
+ *   call gives the same bits.
+ *   Errors: NULL, SHAPE, DTYPE, ALIGN (cu_seqlens: 4 bytes), ALIAS, FLAGS,
+ *   WORKSPACE, HIP.
+ * ------------------------------------------------------------------------ */
+enum {
+  GDNQ_SCAN_LOGITS = 1u, /* gate holds logits: a = sigmoid(gate)            */
+  GDNQ_SCAN_LERP = 2u    /* b = (1 - a) x                                   */
+};
+#define GDNQ_SCAN_CHUNK 128 /* tokens per row of carry */
+
+typedef struct {
+  int32_t batch, seqlen, channels, dtype;
+  uint32_t flags;
+} gdnq_scan_params;
+
+size_t gdnq_scan_workspace_size(const gdnq_scan_params* p, int32_t varlen);
+
+gdnq_status gdnq_scan_forward(const gdnq_scan_params* p, const int32_t* cu_seqlens, const void* x,
+                              const void* gate, const float* h0, void* y, float* h_last, float* carry,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+gdnq_status gdnq_scan_backward(const gdnq_scan_params* p, const int32_t* cu_seqlens, const void* x,
+                               const void* gate, const float* h0, const float* carry, const void* dy,
+                               const float* dh_last, void* dx, void* dgate, float* dh0,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+gdnq_status gdnq_scan_step(const gdnq_scan_params* p, const void* x, const void* gate, const float* h,
+                           float* h_out, void* y, void* stream);
+
+/* ------------------------------------------------------------------------
+ * gdnq_group_norm_* -- the norm over a mixer's heads with its activation,
+ *   channels last: every token's every group of `width` channels (a head of
+ *   o [.., H, d_v]) is normalised by itself.
+ *
+ *       hat = (x - mean) / sqrt(mean((x - mean)^2) + eps)
+ *       (mean: 0 without GDNQ_NORM_CENTER),   n = hat weight + bias
+ *       y = n act(gate),  or act(n) when gate is NULL
+ *
+ *   p->rows R >= 0 tokens, p->groups G >= 1, p->width D in 1 .. 16384 (a
+ *   multiple of 8 is faster), R G <= 2^31 - 1; p->dtype (x, gate, y and
+ *   their gradients) GDNQ_F32 or GDNQ_BF16; p->eps >= 0, finite;
+ *   p->act GDNQ_ACT_NONE, GDNQ_ACT_SILU or GDNQ_ACT_SIGMOID (with gate: not
+ *   GDNQ_ACT_NONE, which would be a plain product).
+ *     x, gate, y [R,G,D] dtype; gate or NULL
+ *     weight, bias [G,D] fp32, or [D] under GDNQ_NORM_SHARED (one for all
+ *       groups); either may be NULL (1 and 0)
+ *   Sums and statistics are fp32; y, dx and dgate are rounded once.
+ *   gdnq_group_norm_backward: dy [R,G,D] dtype in; dx (required), dgate
+ *   (exactly when gate is given) dtype, dweight and dbias fp32 in the shape
+ *   of weight and bias or NULL (not wanted; weight or bias may be NULL with
+ *   their gradient wanted) out.  R = 0 writes zeros there.  The statistics
+ *   are formed again from x; nothing is kept from the forward call.  Sums
+ *   over tokens are taken in a fixed order: the same call gives the same
+ *   bits.
+ *   workspace: gdnq_group_norm_workspace_size(p) bytes (backward only).
+ *   Errors: NULL, SHAPE, DTYPE, ALIGN, ALIAS, FLAGS, WORKSPACE, HIP.
+ * ------------------------------------------------------------------------ */
+enum { GDNQ_ACT_NONE = 0, GDNQ_ACT_SILU = 1, GDNQ_ACT_SIGMOID = 2 };
+enum {
+  GDNQ_NORM_CENTER = 1u, /* subtract the group's mean                       */
+  GDNQ_NORM_SHARED = 2u  /* weight and bias [D], shared by all groups       */
+};
+
+typedef struct {
+  int32_t rows, groups, width, dtype, act;
+  float eps;
+  uint32_t flags;
+} gdnq_norm_params;
+
+gdnq_status gdnq_group_norm(const gdnq_norm_params* p, const void* x, const void* gate, const float* weight,
+                            const float* bias, void* y, void* stream);
+
+size_t gdnq_group_norm_workspace_size(const gdnq_norm_params* p);
+
+gdnq_status gdnq_group_norm_backward(const gdnq_norm_params* p, const void* x, const void* gate,
+                                     const float* weight, const float* bias, const void* dy, void* dx,
+                                     void* dgate, float* dweight, float* dbias, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * gdnq_mx_* -- microscaled 4-bit floating point (OCP MXFP4): the codec and
+ *   the product of rows in it, beside the row codecs of the state above.
+ *
+ *   32 adjacent values share one E8M0 byte s (scale 2^(s - 127)); a value is
+ *   an E2M1 code: sign and magnitude 0, 0.5, 1, 1.5, 2, 3, 4, 6.
+ *     s - 127 = max(floor(log2(max|x|)) - 2, -127); all-zero blocks: s = 0;
+ *     code = the magnitude nearest to |x| / scale, half-way cases to the even
+ *     code, above 6 to 6.  Both steps are exact: every implementation of
+ *     these lines gives the same bits.  A block with a NaN or an infinity
+ *     gets s = 255, E8M0's NaN (its codes are unspecified): products with it
+ *     are NaN.
+ *   Layout: codes [rows, depth / 2] bytes, column 2j in the low nibble of
+ *   byte j and 2j+1 in the high one (as GDNQ_FLAG_STATE_4BIT packs them);
+ *   scales [rows, depth / 32] bytes.  depth is a multiple of 32.
+ *
+ *   gdnq_mx_quantize: x [rows, depth] (dtype GDNQ_F32 or GDNQ_BF16) to codes
+ *     and scales; rows >= 0, depth >= 32.
+ *   gdnq_mx_matmul: y = A W^T: a [rows, depth] and w [cols, depth] in the
+ *     form above, y [rows, cols] out_dtype; products are exact, sums fp32.
+ *   gdnq_mx_linear: the same with a = the codes of x [rows, depth] in_dtype,
+ *     quantized in the call's workspace.
+ *   rows >= 0; cols >= 1; 32 <= depth <= 2^20; rows depth and cols depth up
+ *   to 2^40.  in_dtype is not read by
+ *   gdnq_mx_matmul.  flags must be 0.
+ *   workspace: gdnq_mx_workspace_size(p) bytes, enough for either call.
+ *   Errors: NULL, SHAPE, DTYPE, ALIGN, ALIAS, FLAGS, WORKSPACE, HIP.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  int32_t rows, cols, depth, in_dtype, out_dtype;
+  uint32_t flags;
+} gdnq_mx_params;
+
+gdnq_status gdnq_mx_quantize(const void* x, int64_t rows, int32_t depth, int32_t dtype, uint8_t* codes,
+                             uint8_t* scales, void* stream);
+
+size_t gdnq_mx_workspace_size(const gdnq_mx_params* p);
+
+gdnq_status gdnq_mx_matmul(const gdnq_mx_params* p, const uint8_t* a_codes, const uint8_t* a_scales,
+                           const uint8_t* w_codes, const uint8_t* w_scales, void* y, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+gdnq_status gdnq_mx_linear(const gdnq_mx_params* p, const void* x, const uint8_t* w_codes,
+                           const uint8_t* w_scales, void* y, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/* ------------------------------------------------------------------------
  * gdnq_decode_set_schedule -- tuning hook of gdnq_decode_step's persistent
  *   launch (not part of the method; results do not depend on it).
  *   grid: workgroups of the persistent grid; open_waves: waves that take the

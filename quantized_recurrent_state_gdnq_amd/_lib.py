@@ -24,12 +24,19 @@ GDNQ_FLAG_STATE_4BIT = 64
 GDNQ_FLAG_NO_REQUANT = 8
 GDNQ_MAX_WINDOW = 1 << 24
 GDNQ_FLAG_SLIDING = 128
+GDNQ_SCAN_LOGITS, GDNQ_SCAN_LERP = 1, 2
+GDNQ_SCAN_CHUNK = 128
+GDNQ_ACT_NONE, GDNQ_ACT_SILU, GDNQ_ACT_SIGMOID = 0, 1, 2
+GDNQ_NORM_CENTER, GDNQ_NORM_SHARED = 1, 2
 
 # Every function the header declares.
 EXPORTS = ("gdnq_quantize_state", "gdnq_decode_step", "gdnq_prefill_workspace_size",
            "gdnq_prefill_chunked", "gdnq_prefill_chunked_noalloc", "gdnq_prefill_handoff_workspace_size", "gdnq_prefill_handoff",
            "gdnq_prefill_varlen_workspace_size", "gdnq_prefill_varlen",
            "gdnq_prefill_resume_workspace_size", "gdnq_prefill_resume",
+           "gdnq_scan_workspace_size", "gdnq_scan_forward", "gdnq_scan_backward", "gdnq_scan_step",
+           "gdnq_group_norm", "gdnq_group_norm_workspace_size", "gdnq_group_norm_backward",
+           "gdnq_mx_quantize", "gdnq_mx_workspace_size", "gdnq_mx_matmul", "gdnq_mx_linear",
            "gdnq_decode_set_schedule", "gdnq_status_string", "gdnq_last_error", "gdnq_version",
            "gdnq_sync_debug")
 
@@ -45,6 +52,22 @@ class PrefillParams(ctypes.Structure):
                 ("d_k", ctypes.c_int32), ("d_v", ctypes.c_int32), ("chunk", ctypes.c_int32),
                 ("window", ctypes.c_int32), ("in_dtype", ctypes.c_int32),
                 ("out_dtype", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
+class ScanParams(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("seqlen", ctypes.c_int32), ("channels", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
+class NormParams(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("groups", ctypes.c_int32), ("width", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("act", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("flags", ctypes.c_uint32)]
+
+
+class MxParams(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("cols", ctypes.c_int32), ("depth", ctypes.c_int32),
+                ("in_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("flags", ctypes.c_uint32)]
 
 
 class GdnqError(RuntimeError):
@@ -88,6 +111,28 @@ def _load():
     lib.gdnq_prefill_resume_workspace_size.restype = sz
     lib.gdnq_prefill_resume.argtypes = [ctypes.POINTER(PrefillParams)] + [vp] * 16 + [sz, vp]
     lib.gdnq_prefill_resume.restype = i32
+    lib.gdnq_scan_workspace_size.argtypes = [ctypes.POINTER(ScanParams), i32]
+    lib.gdnq_scan_workspace_size.restype = sz
+    lib.gdnq_scan_forward.argtypes = [ctypes.POINTER(ScanParams)] + [vp] * 8 + [sz, vp]
+    lib.gdnq_scan_forward.restype = i32
+    lib.gdnq_scan_backward.argtypes = [ctypes.POINTER(ScanParams)] + [vp] * 11 + [sz, vp]
+    lib.gdnq_scan_backward.restype = i32
+    lib.gdnq_scan_step.argtypes = [ctypes.POINTER(ScanParams)] + [vp] * 6
+    lib.gdnq_scan_step.restype = i32
+    lib.gdnq_group_norm.argtypes = [ctypes.POINTER(NormParams)] + [vp] * 6
+    lib.gdnq_group_norm.restype = i32
+    lib.gdnq_group_norm_workspace_size.argtypes = [ctypes.POINTER(NormParams)]
+    lib.gdnq_group_norm_workspace_size.restype = sz
+    lib.gdnq_group_norm_backward.argtypes = [ctypes.POINTER(NormParams)] + [vp] * 10 + [sz, vp]
+    lib.gdnq_group_norm_backward.restype = i32
+    lib.gdnq_mx_quantize.argtypes = [vp, i64, i32, i32, vp, vp, vp]
+    lib.gdnq_mx_quantize.restype = i32
+    lib.gdnq_mx_workspace_size.argtypes = [ctypes.POINTER(MxParams)]
+    lib.gdnq_mx_workspace_size.restype = sz
+    lib.gdnq_mx_matmul.argtypes = [ctypes.POINTER(MxParams)] + [vp] * 6 + [sz, vp]
+    lib.gdnq_mx_matmul.restype = i32
+    lib.gdnq_mx_linear.argtypes = [ctypes.POINTER(MxParams)] + [vp] * 5 + [sz, vp]
+    lib.gdnq_mx_linear.restype = i32
     lib.gdnq_decode_set_schedule.argtypes = [i32, i32]
     lib.gdnq_decode_set_schedule.restype = i32
     lib.gdnq_status_string.argtypes = [i32]
@@ -182,3 +227,54 @@ def prefill_resume(params, cu_seqlens, fill_in, q, k, v, alpha, beta, o, codes, 
     return lib.gdnq_prefill_resume(ctypes.byref(params), cu_seqlens, fill_in, q, k, v, alpha, beta,
                                    o, codes, scales, buf_k, buf_v, buf_alpha, buf_beta, fill_out,
                                    workspace, workspace_bytes, stream)
+
+
+def scan_workspace_size(params, varlen):
+    return lib.gdnq_scan_workspace_size(ctypes.byref(params), int(varlen))
+
+
+def scan_forward(params, cu_seqlens, x, gate, h0, y, h_last, carry, workspace, workspace_bytes, stream):
+    return lib.gdnq_scan_forward(ctypes.byref(params), cu_seqlens, x, gate, h0, y, h_last, carry, workspace,
+                                 workspace_bytes, stream)
+
+
+def scan_backward(params, cu_seqlens, x, gate, h0, carry, dy, dh_last, dx, dgate, dh0, workspace,
+                  workspace_bytes, stream):
+    return lib.gdnq_scan_backward(ctypes.byref(params), cu_seqlens, x, gate, h0, carry, dy, dh_last, dx,
+                                  dgate, dh0, workspace, workspace_bytes, stream)
+
+
+def scan_step(params, x, gate, h, h_out, y, stream):
+    return lib.gdnq_scan_step(ctypes.byref(params), x, gate, h, h_out, y, stream)
+
+
+def group_norm(params, x, gate, weight, bias, y, stream):
+    return lib.gdnq_group_norm(ctypes.byref(params), x, gate, weight, bias, y, stream)
+
+
+def group_norm_workspace_size(params):
+    return lib.gdnq_group_norm_workspace_size(ctypes.byref(params))
+
+
+def group_norm_backward(params, x, gate, weight, bias, dy, dx, dgate, dweight, dbias, workspace,
+                        workspace_bytes, stream):
+    return lib.gdnq_group_norm_backward(ctypes.byref(params), x, gate, weight, bias, dy, dx, dgate, dweight,
+                                        dbias, workspace, workspace_bytes, stream)
+
+
+def mx_quantize(x, rows, depth, dtype, codes, scales, stream):
+    return lib.gdnq_mx_quantize(x, rows, depth, dtype, codes, scales, stream)
+
+
+def mx_workspace_size(params):
+    return lib.gdnq_mx_workspace_size(ctypes.byref(params))
+
+
+def mx_matmul(params, a_codes, a_scales, w_codes, w_scales, y, workspace, workspace_bytes, stream):
+    return lib.gdnq_mx_matmul(ctypes.byref(params), a_codes, a_scales, w_codes, w_scales, y, workspace,
+                              workspace_bytes, stream)
+
+
+def mx_linear(params, x, w_codes, w_scales, y, workspace, workspace_bytes, stream):
+    return lib.gdnq_mx_linear(ctypes.byref(params), x, w_codes, w_scales, y, workspace, workspace_bytes,
+                              stream)

@@ -593,4 +593,306 @@ gdnq_status gdnq_prefill_resume(const gdnq_prefill_params* p, const int32_t* cu_
                               buf_k, buf_v, buf_alpha, buf_beta, fill_out, workspace, workspace_bytes, stream);
 }
 
+// ---------------------------------------------------------------- gated linear recurrence
+
+// Every span from `first` on is written and must be disjoint from every other
+// (NULL spans overlap nothing).
+static gdnq_status check_disjoint(const Span* s, int n, int first) {
+  for (int i = first; i < n; ++i)
+    for (int j = 0; j < n; ++j)
+      if (j != i && overlap(s[i], s[j])) return fail(GDNQ_ERR_ALIAS, "%s overlaps %s", s[i].name, s[j].name);
+  return GDNQ_OK;
+}
+
+// Optional pointers: alignment only.
+static gdnq_status check_optional(const Span* s, int n) {
+  for (int i = 0; i < n; ++i)
+    if (s[i].p && !aligned16(s[i].p)) return fail(GDNQ_ERR_ALIGN, "%s is not 16-byte aligned", s[i].name);
+  return GDNQ_OK;
+}
+
+static gdnq_status check_workspace(const void* workspace, size_t given, size_t need) {
+  if (need > 0 && (!workspace || given < need))
+    return fail(GDNQ_ERR_WORKSPACE, "workspace of %zu bytes required, %zu given", need, given);
+  if (workspace && !aligned16(workspace)) return fail(GDNQ_ERR_ALIGN, "workspace is not 16-byte aligned");
+  return GDNQ_OK;
+}
+
+static bool dtype_ok(int32_t dt) { return dt == GDNQ_F32 || dt == GDNQ_BF16; }
+
+static gdnq_status scan_validate(const gdnq_scan_params* p, bool varlen, gdnq::ScanLaunch& L) {
+  if (!p) return fail(GDNQ_ERR_NULL, "params is NULL");
+  if (p->batch < 0 || p->seqlen < 0 || p->channels < 1)
+    return fail(GDNQ_ERR_SHAPE, "batch = %d, seqlen = %d, channels = %d", p->batch, p->seqlen, p->channels);
+  if (!dtype_ok(p->dtype)) return fail(GDNQ_ERR_DTYPE, "dtype = %d", p->dtype);
+  if (p->flags & ~uint32_t(GDNQ_SCAN_LOGITS | GDNQ_SCAN_LERP))
+    return fail(GDNQ_ERR_FLAGS, "flags 0x%x: the scan takes GDNQ_SCAN_LOGITS and GDNQ_SCAN_LERP", p->flags);
+  const int64_t n = varlen ? int64_t(p->seqlen) : int64_t(p->batch) * p->seqlen;
+  if (n > 0x7fffffffLL) return fail(GDNQ_ERR_SHAPE, "%lld tokens: at most 2^31 - 1", (long long)n);
+  if (int64_t(p->batch) * p->channels > 0x7fffffffLL)
+    return fail(GDNQ_ERR_SHAPE, "batch * channels = %lld: at most 2^31 - 1", (long long)p->batch * p->channels);
+  if ((n + GDNQ_SCAN_CHUNK - 1) / GDNQ_SCAN_CHUNK * p->channels > (int64_t(1) << 36))
+    return fail(GDNQ_ERR_SHAPE, "%lld tokens of %d channels: too large", (long long)n, p->channels);
+  L = gdnq::ScanLaunch{};
+  L.B = p->batch; L.T = p->seqlen; L.C = p->channels; L.N = n;
+  L.bf16 = p->dtype == GDNQ_BF16;
+  L.logits = (p->flags & GDNQ_SCAN_LOGITS) != 0;
+  L.lerp = (p->flags & GDNQ_SCAN_LERP) != 0;
+  return GDNQ_OK;
+}
+
+static gdnq_status check_offsets(const int32_t* cu, int B, const Span* s, int n, int first) {
+  if (!cu) return GDNQ_OK;
+  if (reinterpret_cast<uintptr_t>(cu) & 3u) return fail(GDNQ_ERR_ALIGN, "cu_seqlens is not 4-byte aligned");
+  const Span cs{"cu_seqlens", cu, (size_t(B) + 1) * 4};
+  for (int i = first; i < n; ++i)
+    if (overlap(cs, s[i])) return fail(GDNQ_ERR_ALIAS, "cu_seqlens overlaps %s", s[i].name);
+  return GDNQ_OK;
+}
+
+size_t gdnq_scan_workspace_size(const gdnq_scan_params* p, int32_t varlen) {
+  gdnq::ScanLaunch L;
+  if (scan_validate(p, varlen != 0, L) != GDNQ_OK) return 0;
+  return gdnq::scan_workspace_bytes(L.N, L.C, L.bf16);
+}
+
+gdnq_status gdnq_scan_forward(const gdnq_scan_params* p, const int32_t* cu_seqlens, const void* x,
+                              const void* gate, const float* h0, void* y, float* h_last, float* carry,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+  gdnq::ScanLaunch L;
+  if (gdnq_status st = scan_validate(p, cu_seqlens != nullptr, L)) return st;
+  if (L.B == 0) return ok();
+  const size_t tok = size_t(L.N) * L.C * esize(p->dtype), bc = size_t(L.B) * L.C * 4;
+  const size_t need = gdnq::scan_workspace_bytes(L.N, L.C, L.bf16);
+  const Span sp[] = {{"x", x, tok}, {"gate", gate, tok}, {"h0", h0, bc}, {"y", y, tok}, {"h_last", h_last, bc},
+                     {"carry", carry, size_t((L.N + GDNQ_SCAN_CHUNK - 1) / GDNQ_SCAN_CHUNK) * L.C * 4},
+                     {"workspace", workspace, need}};
+  constexpr int N = sizeof(sp) / sizeof(sp[0]);
+  if (L.N > 0) {
+    if (gdnq_status st = check_ptrs(sp, 2)) return st;
+    if (gdnq_status st = check_ptrs(sp + 3, 1)) return st;
+  }
+  if (gdnq_status st = check_optional(sp, N)) return st;
+  if (gdnq_status st = check_disjoint(sp, N, 3)) return st;
+  if (gdnq_status st = check_offsets(cu_seqlens, L.B, sp, N, 3)) return st;
+  if (gdnq_status st = check_workspace(workspace, workspace_bytes, need)) return st;
+  L.cu_seqlens = cu_seqlens;
+  L.x = x; L.gate = gate; L.h0 = h0; L.y = y; L.h_last = h_last; L.carry = carry; L.workspace = workspace;
+  clear_stale_hip_error();
+  return launched(gdnq::launch_scan_forward(L, static_cast<hipStream_t>(stream)), "scan launch", stream);
+}
+
+gdnq_status gdnq_scan_backward(const gdnq_scan_params* p, const int32_t* cu_seqlens, const void* x,
+                               const void* gate, const float* h0, const float* carry, const void* dy,
+                               const float* dh_last, void* dx, void* dgate, float* dh0,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  gdnq::ScanLaunch L;
+  if (gdnq_status st = scan_validate(p, cu_seqlens != nullptr, L)) return st;
+  if (L.B == 0) return ok();
+  const size_t tok = size_t(L.N) * L.C * esize(p->dtype), bc = size_t(L.B) * L.C * 4;
+  const size_t need = gdnq::scan_workspace_bytes(L.N, L.C, L.bf16);
+  const Span sp[] = {{"x", x, tok}, {"gate", gate, tok}, {"dy", dy, tok},
+                     {"carry", carry, size_t((L.N + GDNQ_SCAN_CHUNK - 1) / GDNQ_SCAN_CHUNK) * L.C * 4},
+                     {"h0", h0, bc}, {"dh_last", dh_last, bc},
+                     {"dx", dx, tok}, {"dgate", dgate, tok}, {"dh0", dh0, bc}, {"workspace", workspace, need}};
+  constexpr int N = sizeof(sp) / sizeof(sp[0]);
+  if (L.N > 0) {
+    if (gdnq_status st = check_ptrs(sp, 4)) return st;
+    if (gdnq_status st = check_ptrs(sp + 6, 2)) return st;
+  }
+  if (gdnq_status st = check_optional(sp, N)) return st;
+  if (gdnq_status st = check_disjoint(sp, N, 6)) return st;
+  if (gdnq_status st = check_offsets(cu_seqlens, L.B, sp, N, 6)) return st;
+  if (gdnq_status st = check_workspace(workspace, workspace_bytes, need)) return st;
+  L.cu_seqlens = cu_seqlens;
+  L.x = x; L.gate = gate; L.h0 = h0; L.carry = const_cast<float*>(carry); L.dy = dy; L.dh_last = dh_last;
+  L.dx = dx; L.dgate = dgate; L.dh0 = dh0; L.workspace = workspace;
+  clear_stale_hip_error();
+  return launched(gdnq::launch_scan_backward(L, static_cast<hipStream_t>(stream)), "scan backward launch", stream);
+}
+
+gdnq_status gdnq_scan_step(const gdnq_scan_params* p, const void* x, const void* gate, const float* h,
+                           float* h_out, void* y, void* stream) {
+  gdnq::ScanLaunch L;
+  if (gdnq_status st = scan_validate(p, false, L)) return st;
+  if (L.T != 1) return fail(GDNQ_ERR_SHAPE, "seqlen = %d: a step takes one token per sequence", L.T);
+  if (L.B == 0) return ok();
+  const size_t tok = size_t(L.N) * L.C * esize(p->dtype), bc = size_t(L.B) * L.C * 4;
+  const Span sp[] = {{"x", x, tok}, {"gate", gate, tok}, {"h", h == h_out ? nullptr : h, bc}, {"h_out", h_out, bc}, {"y", y, tok}};
+  if (!h) return fail(GDNQ_ERR_NULL, "h is NULL");
+  if (gdnq_status st = check_ptrs(sp, 2)) return st;
+  if (gdnq_status st = check_ptrs(sp + 3, 2)) return st;
+  if (gdnq_status st = check_optional(sp, 5)) return st;
+  if (gdnq_status st = check_disjoint(sp, 5, 3)) return st;
+  L.x = x; L.gate = gate; L.h0 = h; L.h_last = h_out; L.y = y;
+  clear_stale_hip_error();
+  return launched(gdnq::launch_scan_step(L, static_cast<hipStream_t>(stream)), "scan step launch", stream);
+}
+
+// ---------------------------------------------------------------- group norm
+
+static gdnq_status norm_validate(const gdnq_norm_params* p, bool gate, gdnq::NormLaunch& L) {
+  if (!p) return fail(GDNQ_ERR_NULL, "params is NULL");
+  if (p->rows < 0 || p->groups < 1 || p->width < 1 || p->width > 16384)
+    return fail(GDNQ_ERR_SHAPE, "rows = %d, groups = %d, width = %d (1 .. 16384)", p->rows, p->groups, p->width);
+  if (int64_t(p->rows) * p->groups > 0x7fffffffLL || p->groups > (1 << 20))
+    return fail(GDNQ_ERR_SHAPE, "rows * groups = %lld: at most 2^31 - 1, and 2^20 groups", (long long)p->rows * p->groups);
+  if (!dtype_ok(p->dtype)) return fail(GDNQ_ERR_DTYPE, "dtype = %d", p->dtype);
+  if (!(p->eps >= 0.0f) || p->eps > 3.0e38f) return fail(GDNQ_ERR_SHAPE, "eps = %g, expected a finite value >= 0", double(p->eps));
+  if (p->act < GDNQ_ACT_NONE || p->act > GDNQ_ACT_SIGMOID) return fail(GDNQ_ERR_FLAGS, "act = %d", p->act);
+  if (gate && p->act == GDNQ_ACT_NONE) return fail(GDNQ_ERR_FLAGS, "a gate needs GDNQ_ACT_SILU or GDNQ_ACT_SIGMOID");
+  if (p->flags & ~uint32_t(GDNQ_NORM_CENTER | GDNQ_NORM_SHARED))
+    return fail(GDNQ_ERR_FLAGS, "flags 0x%x: the norm takes GDNQ_NORM_CENTER and GDNQ_NORM_SHARED", p->flags);
+  L = gdnq::NormLaunch{};
+  L.R = p->rows; L.G = p->groups; L.D = p->width; L.act = p->act; L.eps = p->eps;
+  L.bf16 = p->dtype == GDNQ_BF16;
+  L.center = (p->flags & GDNQ_NORM_CENTER) != 0;
+  L.shared = (p->flags & GDNQ_NORM_SHARED) != 0;
+  return GDNQ_OK;
+}
+
+gdnq_status gdnq_group_norm(const gdnq_norm_params* p, const void* x, const void* gate, const float* weight,
+                            const float* bias, void* y, void* stream) {
+  gdnq::NormLaunch L;
+  if (gdnq_status st = norm_validate(p, gate != nullptr, L)) return st;
+  if (L.R == 0) return ok();
+  const size_t n = size_t(L.R) * L.G * L.D * esize(p->dtype), w = size_t(L.shared ? 1 : L.G) * L.D * 4;
+  const Span sp[] = {{"x", x, n}, {"gate", gate, n}, {"weight", weight, w}, {"bias", bias, w}, {"y", y, n}};
+  if (gdnq_status st = check_ptrs(sp, 1)) return st;
+  if (gdnq_status st = check_ptrs(sp + 4, 1)) return st;
+  if (gdnq_status st = check_optional(sp, 5)) return st;
+  if (gdnq_status st = check_disjoint(sp, 5, 4)) return st;
+  L.x = x; L.gate = gate; L.weight = weight; L.bias = bias; L.y = y;
+  clear_stale_hip_error();
+  return launched(gdnq::launch_norm_forward(L, static_cast<hipStream_t>(stream)), "group norm launch", stream);
+}
+
+size_t gdnq_group_norm_workspace_size(const gdnq_norm_params* p) {
+  gdnq::NormLaunch L;
+  if (norm_validate(p, false, L) != GDNQ_OK) return 0;
+  return gdnq::norm_workspace_bytes(L.R, L.G, L.D);
+}
+
+gdnq_status gdnq_group_norm_backward(const gdnq_norm_params* p, const void* x, const void* gate,
+                                     const float* weight, const float* bias, const void* dy, void* dx,
+                                     void* dgate, float* dweight, float* dbias, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+  gdnq::NormLaunch L;
+  if (gdnq_status st = norm_validate(p, gate != nullptr, L)) return st;
+  const size_t n = size_t(L.R) * L.G * L.D * esize(p->dtype), w = size_t(L.shared ? 1 : L.G) * L.D * 4;
+  const size_t need = gdnq::norm_workspace_bytes(L.R, L.G, L.D);
+  const Span sp[] = {{"x", x, n}, {"dy", dy, n}, {"gate", gate, n}, {"weight", weight, w}, {"bias", bias, w},
+                     {"dx", dx, n}, {"dgate", dgate, n}, {"dweight", dweight, w}, {"dbias", dbias, w},
+                     {"workspace", workspace, need}};
+  constexpr int N = sizeof(sp) / sizeof(sp[0]);
+  if (L.R > 0) {
+    if (gdnq_status st = check_ptrs(sp, 2)) return st;
+    if (gdnq_status st = check_ptrs(sp + 5, 1)) return st;
+    if ((gate == nullptr) != (dgate == nullptr)) return fail(GDNQ_ERR_NULL, "gate and dgate: both or neither");
+  }
+  if (gdnq_status st = check_optional(sp, N)) return st;
+  if (gdnq_status st = check_disjoint(sp, N, 5)) return st;
+  if (gdnq_status st = check_workspace(workspace, workspace_bytes, need)) return st;
+  if (L.R == 0 && !dweight && !dbias) return ok();
+  L.x = x; L.gate = gate; L.weight = weight; L.bias = bias; L.dy = dy; L.dx = dx; L.dgate = dgate;
+  L.dweight = dweight; L.dbias = dbias; L.workspace = workspace;
+  clear_stale_hip_error();
+  return launched(gdnq::launch_norm_backward(L, static_cast<hipStream_t>(stream)), "group norm backward launch", stream);
+}
+
+// ---------------------------------------------------------------- microscaled 4-bit
+
+static gdnq_status mx_depth_ok(int64_t rows, int32_t depth) {
+  if (depth < 32 || depth % 32 || depth > (1 << 20))
+    return fail(GDNQ_ERR_SHAPE, "depth = %d: a multiple of 32, 32 .. 2^20", depth);
+  if (rows < 0 || rows > (int64_t(1) << 31) || rows * depth > (int64_t(1) << 40))
+    return fail(GDNQ_ERR_SHAPE, "rows = %lld of %d values: too large", (long long)rows, depth);
+  return GDNQ_OK;
+}
+
+static gdnq_status mx_validate(const gdnq_mx_params* p, bool linear, gdnq::MxLaunch& L) {
+  if (!p) return fail(GDNQ_ERR_NULL, "params is NULL");
+  if (p->rows < 0 || p->cols < 1) return fail(GDNQ_ERR_SHAPE, "rows = %d, cols = %d", p->rows, p->cols);
+  if (gdnq_status st = mx_depth_ok(p->rows, p->depth)) return st;
+  if (gdnq_status st = mx_depth_ok(p->cols, p->depth)) return st;
+  if ((int64_t(p->rows) + 255) / 256 * ((int64_t(p->cols) + 15) / 16) > 0x7fffffffLL)
+    return fail(GDNQ_ERR_SHAPE, "rows = %d, cols = %d: too large", p->rows, p->cols);
+  if (!dtype_ok(p->out_dtype) || (linear && !dtype_ok(p->in_dtype)))
+    return fail(GDNQ_ERR_DTYPE, "in_dtype = %d, out_dtype = %d", p->in_dtype, p->out_dtype);
+  if (p->flags) return fail(GDNQ_ERR_FLAGS, "flags 0x%x: none are defined", p->flags);
+  L = gdnq::MxLaunch{};
+  L.M = p->rows; L.N = p->cols; L.K = p->depth; L.out_bf16 = p->out_dtype == GDNQ_BF16;
+  return GDNQ_OK;
+}
+
+gdnq_status gdnq_mx_quantize(const void* x, int64_t rows, int32_t depth, int32_t dtype, uint8_t* codes,
+                             uint8_t* scales, void* stream) {
+  if (gdnq_status st = mx_depth_ok(rows, depth)) return st;
+  if (!dtype_ok(dtype)) return fail(GDNQ_ERR_DTYPE, "dtype = %d", dtype);
+  if (rows == 0) return ok();
+  const size_t n = size_t(rows) * depth;
+  const Span sp[] = {{"x", x, n * esize(dtype)}, {"codes", codes, n / 2}, {"scales", scales, n / 32}};
+  if (gdnq_status st = check_ptrs(sp, 3)) return st;
+  if (gdnq_status st = check_disjoint(sp, 3, 1)) return st;
+  clear_stale_hip_error();
+  return launched(gdnq::launch_mx_quantize(x, rows, depth, dtype == GDNQ_BF16, codes, scales,
+                                           static_cast<hipStream_t>(stream)), "mx quantize launch", stream);
+}
+
+static size_t mx_align(size_t n) { return (n + 255) / 256 * 256; }
+
+// The quantized activations of gdnq_mx_linear come first, then the product's own workspace.
+static size_t mx_quantized_bytes(const gdnq::MxLaunch& L) {
+  return mx_align(size_t(L.M) * L.K / 2) + mx_align(size_t(L.M) * L.K / 32);
+}
+
+size_t gdnq_mx_workspace_size(const gdnq_mx_params* p) {
+  gdnq::MxLaunch L;
+  if (mx_validate(p, false, L) != GDNQ_OK) return 0;
+  return mx_quantized_bytes(L) + gdnq::mx_matmul_workspace_bytes(L.M, L.N, L.K);
+}
+
+gdnq_status gdnq_mx_matmul(const gdnq_mx_params* p, const uint8_t* a_codes, const uint8_t* a_scales,
+                           const uint8_t* w_codes, const uint8_t* w_scales, void* y, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  gdnq::MxLaunch L;
+  if (gdnq_status st = mx_validate(p, false, L)) return st;
+  if (L.M == 0) return ok();
+  const size_t need = gdnq::mx_matmul_workspace_bytes(L.M, L.N, L.K);
+  const Span sp[] = {{"a_codes", a_codes, size_t(L.M) * L.K / 2}, {"a_scales", a_scales, size_t(L.M) * L.K / 32},
+                     {"w_codes", w_codes, size_t(L.N) * L.K / 2}, {"w_scales", w_scales, size_t(L.N) * L.K / 32},
+                     {"y", y, size_t(L.M) * L.N * esize(p->out_dtype)}, {"workspace", workspace, need}};
+  if (gdnq_status st = check_ptrs(sp, 5)) return st;
+  if (gdnq_status st = check_disjoint(sp, 6, 4)) return st;
+  if (gdnq_status st = check_workspace(workspace, workspace_bytes, need)) return st;
+  L.a_codes = a_codes; L.a_scales = a_scales; L.w_codes = w_codes; L.w_scales = w_scales; L.y = y;
+  L.workspace = workspace;
+  clear_stale_hip_error();
+  return launched(gdnq::launch_mx_matmul(L, static_cast<hipStream_t>(stream)), "mx product launch", stream);
+}
+
+gdnq_status gdnq_mx_linear(const gdnq_mx_params* p, const void* x, const uint8_t* w_codes,
+                           const uint8_t* w_scales, void* y, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  gdnq::MxLaunch L;
+  if (gdnq_status st = mx_validate(p, true, L)) return st;
+  if (L.M == 0) return ok();
+  const size_t quantized = mx_quantized_bytes(L), need = quantized + gdnq::mx_matmul_workspace_bytes(L.M, L.N, L.K);
+  const Span sp[] = {{"x", x, size_t(L.M) * L.K * esize(p->in_dtype)},
+                     {"w_codes", w_codes, size_t(L.N) * L.K / 2}, {"w_scales", w_scales, size_t(L.N) * L.K / 32},
+                     {"y", y, size_t(L.M) * L.N * esize(p->out_dtype)}, {"workspace", workspace, need}};
+  if (gdnq_status st = check_ptrs(sp, 4)) return st;
+  if (gdnq_status st = check_disjoint(sp, 5, 3)) return st;
+  if (gdnq_status st = check_workspace(workspace, workspace_bytes, need)) return st;
+  uint8_t* codes = static_cast<uint8_t*>(workspace);
+  uint8_t* scales = codes + mx_align(size_t(L.M) * L.K / 2);
+  L.a_codes = codes; L.a_scales = scales; L.w_codes = w_codes; L.w_scales = w_scales; L.y = y;
+  L.workspace = codes + quantized;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  clear_stale_hip_error();
+  if (hipError_t e = gdnq::launch_mx_quantize(x, L.M, L.K, p->in_dtype == GDNQ_BF16, codes, scales, s))
+    return hip_status(e, "mx quantize launch");
+  return launched(gdnq::launch_mx_matmul(L, s), "mx product launch", stream);
+}
+
 }  // extern "C"

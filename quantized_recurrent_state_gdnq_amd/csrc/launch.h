@@ -85,4 +85,66 @@ inline size_t prefill_workspace_bytes(const PrefillLaunch& L) {
   return L.ssd ? prefill_ssd_workspace_bytes(L) : prefill_gdn_workspace_bytes(L);
 }
 
+// Gated linear recurrence over channels (scan.hip).
+struct ScanLaunch {
+  const int32_t* cu_seqlens;  // B + 1 packed token offsets, or null: B sequences of T tokens
+  const void* x;
+  const void* gate;
+  const float* h0;
+  void* y;
+  float* h_last;
+  float* carry;  // the state entering every GDNQ_SCAN_CHUNK-th token
+  const void* dy;
+  const float* dh_last;
+  void* dx;
+  void* dgate;
+  float* dh0;
+  void* workspace;
+  int B, T, C;
+  int64_t N;  // tokens of the call
+  bool bf16, logits, lerp;
+};
+size_t scan_workspace_bytes(int64_t N, int C, bool bf16);
+hipError_t launch_scan_forward(const ScanLaunch& L, hipStream_t stream);
+hipError_t launch_scan_backward(const ScanLaunch& L, hipStream_t stream);
+// one token per sequence: h0 in, h_last out
+hipError_t launch_scan_step(const ScanLaunch& L, hipStream_t stream);
+
+// Group norm with its activation (group_norm.hip).
+struct NormLaunch {
+  const void* x;
+  const void* gate;
+  const float* weight;
+  const float* bias;
+  void* y;
+  const void* dy;
+  void* dx;
+  void* dgate;
+  float* dweight;
+  float* dbias;
+  void* workspace;
+  int R, G, D, act;
+  float eps;
+  bool bf16, center, shared;
+};
+size_t norm_workspace_bytes(int R, int G, int D);
+hipError_t launch_norm_forward(const NormLaunch& L, hipStream_t stream);
+hipError_t launch_norm_backward(const NormLaunch& L, hipStream_t stream);
+
+// Microscaled 4-bit codec and product (mx.hip).
+struct MxLaunch {
+  const uint8_t* a_codes;
+  const uint8_t* a_scales;
+  const uint8_t* w_codes;
+  const uint8_t* w_scales;
+  void* y;
+  void* workspace;
+  int M, N, K;
+  bool out_bf16;
+};
+hipError_t launch_mx_quantize(const void* x, int64_t rows, int K, bool bf16, uint8_t* codes, uint8_t* scales,
+                              hipStream_t stream);
+size_t mx_matmul_workspace_bytes(int M, int N, int K);
+hipError_t launch_mx_matmul(const MxLaunch& L, hipStream_t stream);
+
 }  // namespace gdnq

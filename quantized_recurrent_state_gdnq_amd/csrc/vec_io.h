@@ -1,0 +1,39 @@
+// Element types and small vectors of the channel-wise kernels (scan,
+// group norm): fp32 and bf16 in memory, fp32 in registers.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace gdnq {
+
+typedef __bf16 bf16;
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(bf16 x) { return float(x); }
+// One rounding to the nearest even (NaN stays NaN).
+__device__ __forceinline__ void store_f32(float* p, float x) { *p = x; }
+__device__ __forceinline__ void store_f32(bf16* p, float x) { *p = bf16(x); }
+
+// p = sigmoid(z) and q = 1 - p, both to a few units in the last place: with
+// u = e^-|z| the smaller of the two is u / (1 + u), and the larger is formed
+// as one minus it, so neither cancels.  The hardware's 2^x takes -|z| log2(e)
+// in two parts (product and its rounding error), its reciprocal one Newton step.
+__device__ __forceinline__ void sigmoid_pair(float z, float& p, float& q) {
+  float m = -fabsf(z);
+  m = m < -128.0f ? -128.0f : m;  // u is 0 from -104 on (infinities, the type's lowest value); NaN passes
+  const float t = m * 1.44269504f;
+  const float low = fmaf(m, 1.44269504f, -t) + m * 1.92596299e-8f;  // log2(e) = 1.44269504 + 1.926e-8
+  const float e = __builtin_amdgcn_exp2f(t);
+  const float u = fmaf(e, low * 0.693147181f, e);
+  const float d = 1.0f + u;
+  float r = __builtin_amdgcn_rcpf(d);
+  r = fmaf(fmaf(-d, r, 1.0f), r, r);
+  const float small = u * r, large = 1.0f - small;
+  p = z >= 0.0f ? large : small;
+  q = z >= 0.0f ? small : large;
+}
+
+}  // namespace gdnq

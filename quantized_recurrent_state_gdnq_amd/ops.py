@@ -558,3 +558,306 @@ class DecodeState:
                         wht=self.wht, out_dtype=out_dtype, sliding=self.sliding)
         self.fill, self._fill_next = self._fill_next, self.fill
         return o
+
+
+# ---------------------------------------------------------------- around the mixer
+
+
+def _launch(dev, fn, *args):
+    """One library call on dev's current stream, with dev the current device
+    (a launch needs that)."""
+    stream = _stream(dev)
+    if dev.index == torch.cuda.current_device():
+        _lib.check(fn(*args, stream))
+    else:
+        with torch.cuda.device(dev):
+            _lib.check(fn(*args, stream))
+
+
+def _optional(t, name, dtype, device, shape):
+    if t is not None:
+        _shape(_need(t, name, dtype, device), shape, name)
+    return t
+
+
+def _space(workspace, need, dev):
+    """The caller's workspace (any contiguous tensor of the device) or a new
+    one, and its size in bytes."""
+    if workspace is None:
+        if need == 0:
+            return None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _need(workspace, "workspace", None, dev)
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _scan_setup(x, gate, cu_seqlens, logits, lerp):
+    """The checks every scan call shares: its parameters, sequences and the
+    rows its carry has."""
+    _need(x, "x", None, None)
+    dev = x.device
+    if x.dtype not in _DT:
+        raise ValueError("x must be float32 or bfloat16")
+    if cu_seqlens is None:
+        if x.dim() != 3:
+            raise ValueError("x must be [B,T,C], or [T,C] with cu_seqlens")
+        B, T, C = x.shape
+        n = B * T
+    else:
+        _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+            raise ValueError("cu_seqlens: one dimension of B+1 offsets")
+        if x.dim() != 2:
+            raise ValueError("x must be [T,C] with cu_seqlens")
+        B, (T, C) = cu_seqlens.numel() - 1, x.shape
+        n = T
+    _shape(_need(gate, "gate", x.dtype, dev), x.shape, "gate")
+    p = _lib.ScanParams(B, T, C, _DT[x.dtype], (_lib.GDNQ_SCAN_LOGITS if logits else 0)
+                        | (_lib.GDNQ_SCAN_LERP if lerp else 0))
+    return p, B, C, (-(-n // _lib.GDNQ_SCAN_CHUNK), C)
+
+
+def scan_workspace_size(x, cu_seqlens=None):
+    """Workspace bytes of gated_scan and gated_scan_backward for these arrays."""
+    if cu_seqlens is None:
+        p = _lib.ScanParams(x.shape[0], x.shape[1], x.shape[2], _DT[x.dtype], 0)
+    else:
+        p = _lib.ScanParams(cu_seqlens.numel() - 1, x.shape[0], x.shape[1], _DT[x.dtype], 0)
+    return int(_lib.scan_workspace_size(p, cu_seqlens is not None))
+
+
+def gated_scan(x, gate, h0=None, cu_seqlens=None, *, logits=False, lerp=False, save=False, y=None, h_last=None,
+               carry=None, workspace=None):
+    """Gated linear recurrence over channels (see gdnq_scan_* in
+    include/gdnq.h): h_t = a_t h_{t-1} + b_t with a = gate (logits=True:
+    sigmoid(gate)) and b = x (lerp=True: (1 - a) x).
+
+    x, gate [B,T,C], or [T,C] with cu_seqlens (int32 on the device, B+1
+    offsets of the packed sequences), fp32 or bf16; h0 [B,C] fp32 or None.
+    Returns (y like x, h_last [B,C] fp32), and with save=True (or a given
+    carry [ceil(tokens/128), C] fp32) the carry that gated_scan_backward
+    takes."""
+    p, B, C, cshape = _scan_setup(x, gate, cu_seqlens, logits, lerp)
+    dev = x.device
+    _optional(h0, "h0", torch.float32, dev, (B, C))
+    # a packed call may hold tokens that no sequence covers: only a given y has values there
+    y = torch.empty_like(x) if y is None else _shape(_need(y, "y", x.dtype, dev), x.shape, "y")
+    if h_last is None:
+        h_last = torch.empty((B, C), dtype=torch.float32, device=dev)
+    _shape(_need(h_last, "h_last", torch.float32, dev), (B, C), "h_last")
+    if carry is None and save:
+        carry = torch.empty(cshape, dtype=torch.float32, device=dev)
+    _optional(carry, "carry", torch.float32, dev, cshape)
+    ws, ws_bytes = _space(workspace, int(_lib.scan_workspace_size(p, cu_seqlens is not None)), dev)
+    _launch(dev, _lib.scan_forward, p, _ptr(cu_seqlens), _ptr(x), _ptr(gate), _ptr(h0), _ptr(y), _ptr(h_last),
+            _ptr(carry), _ptr(ws), ws_bytes)
+    return (y, h_last) if carry is None else (y, h_last, carry)
+
+
+def gated_scan_backward(dy, x, gate, carry, h0=None, dh_last=None, cu_seqlens=None, *, logits=False, lerp=False,
+                        dx=None, dgate=None, dh0=None, workspace=None):
+    """Gradients of gated_scan from dy (like x) and dh_last ([B,C] fp32 or
+    None), with the forward call's x, gate, carry, h0, cu_seqlens and flags.
+    Returns (dx, dgate, dh0); dh0 is None when h0 is and no dh0 was given."""
+    p, B, C, cshape = _scan_setup(x, gate, cu_seqlens, logits, lerp)
+    dev = x.device
+    _shape(_need(dy, "dy", x.dtype, dev), x.shape, "dy")
+    _shape(_need(carry, "carry", torch.float32, dev), cshape, "carry")
+    _optional(h0, "h0", torch.float32, dev, (B, C))
+    _optional(dh_last, "dh_last", torch.float32, dev, (B, C))
+    dx = torch.empty_like(x) if dx is None else _shape(_need(dx, "dx", x.dtype, dev), x.shape, "dx")
+    dgate = torch.empty_like(x) if dgate is None else _shape(_need(dgate, "dgate", x.dtype, dev), x.shape, "dgate")
+    if dh0 is None and h0 is not None:
+        dh0 = torch.empty((B, C), dtype=torch.float32, device=dev)
+    _optional(dh0, "dh0", torch.float32, dev, (B, C))
+    ws, ws_bytes = _space(workspace, int(_lib.scan_workspace_size(p, cu_seqlens is not None)), dev)
+    _launch(dev, _lib.scan_backward, p, _ptr(cu_seqlens), _ptr(x), _ptr(gate), _ptr(h0), _ptr(carry), _ptr(dy),
+            _ptr(dh_last), _ptr(dx), _ptr(dgate), _ptr(dh0), _ptr(ws), ws_bytes)
+    return dx, dgate, dh0
+
+
+def gated_scan_step(x, gate, h, *, logits=False, lerp=False, h_out=None, y=None):
+    """One token of the gated recurrence for every sequence: x, gate [B,C],
+    h [B,C] fp32, updated in place unless h_out is given.  Returns y [B,C]."""
+    _need(x, "x", None, None)
+    dev = x.device
+    if x.dtype not in _DT:
+        raise ValueError("x must be float32 or bfloat16")
+    if x.dim() != 2:
+        raise ValueError("x must be [B,C]")
+    _shape(_need(gate, "gate", x.dtype, dev), x.shape, "gate")
+    _shape(_need(h, "h", torch.float32, dev), x.shape, "h")
+    h_out = h if h_out is None else _shape(_need(h_out, "h_out", torch.float32, dev), x.shape, "h_out")
+    y = torch.empty_like(x) if y is None else _shape(_need(y, "y", x.dtype, dev), x.shape, "y")
+    p = _lib.ScanParams(x.shape[0], 1, x.shape[1], _DT[x.dtype], (_lib.GDNQ_SCAN_LOGITS if logits else 0)
+                        | (_lib.GDNQ_SCAN_LERP if lerp else 0))
+    _launch(dev, _lib.scan_step, p, _ptr(x), _ptr(gate), _ptr(h), _ptr(h_out), _ptr(y))
+    return y
+
+
+_ACTS = {"none": _lib.GDNQ_ACT_NONE, "silu": _lib.GDNQ_ACT_SILU, "sigmoid": _lib.GDNQ_ACT_SIGMOID}
+
+
+def _norm_setup(x, weight, bias, gate, act, center, eps):
+    _need(x, "x", None, None)
+    dev = x.device
+    if x.dtype not in _DT:
+        raise ValueError("x must be float32 or bfloat16")
+    if x.dim() < 2:
+        raise ValueError("x must be [..,groups,width]")
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}, got {act!r}")
+    G, D = x.shape[-2:]
+    shape = None
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is not None:
+            _need(t, name, torch.float32, dev)
+            if tuple(t.shape) not in ((D,), (G, D)) or (shape is not None and tuple(t.shape) != shape):
+                raise ValueError(f"{name} must have shape {(D,)} or {(G, D)} (both alike), got {tuple(t.shape)}")
+            shape = tuple(t.shape)
+    if gate is not None:
+        _shape(_need(gate, "gate", x.dtype, dev), x.shape, "gate")
+    shape = shape or (G, D)
+    rows = 1
+    for s in x.shape[:-2]:
+        rows *= s
+    p = _lib.NormParams(rows, G, D, _DT[x.dtype], _ACTS[act], eps, (_lib.GDNQ_NORM_CENTER if center else 0)
+                        | (_lib.GDNQ_NORM_SHARED if shape == (D,) else 0))
+    return p, shape
+
+
+def group_norm(x, weight=None, bias=None, gate=None, *, act="none", center=False, eps=1e-5, y=None):
+    """Norm of every token's groups with its activation (see gdnq_group_norm
+    in include/gdnq.h): x [..,groups,width] fp32 or bf16, e.g. a mixer's
+    heads o [B,T,H,d_v]; weight, bias [groups,width] or [width] (shared by the
+    groups) fp32, or None; y = n act(gate), or act(n) without a gate (act
+    "none", "silu" or "sigmoid").  center=False: root-mean-square norm."""
+    p, _ = _norm_setup(x, weight, bias, gate, act, center, eps)
+    dev = x.device
+    y = torch.empty_like(x) if y is None else _shape(_need(y, "y", x.dtype, dev), x.shape, "y")
+    _launch(dev, _lib.group_norm, p, _ptr(x), _ptr(gate), _ptr(weight), _ptr(bias), _ptr(y))
+    return y
+
+
+def group_norm_workspace_size(x):
+    """Workspace bytes of group_norm_backward for x [..,groups,width]."""
+    G, D = x.shape[-2:]
+    rows = 1
+    for s in x.shape[:-2]:
+        rows *= s
+    return int(_lib.group_norm_workspace_size(_lib.NormParams(rows, G, D, _DT[x.dtype], 0, 0.0, 0)))
+
+
+def group_norm_backward(dy, x, weight=None, bias=None, gate=None, *, act="none", center=False, eps=1e-5, dx=None,
+                        dgate=None, dweight=None, dbias=None, workspace=None):
+    """Gradients of group_norm from dy (like x).  Returns (dx, dgate, dweight,
+    dbias); those of arguments that are None are None.  dweight and dbias are
+    fp32, shaped like weight and bias."""
+    p, shape = _norm_setup(x, weight, bias, gate, act, center, eps)
+    dev = x.device
+    _shape(_need(dy, "dy", x.dtype, dev), x.shape, "dy")
+    dx = torch.empty_like(x) if dx is None else _shape(_need(dx, "dx", x.dtype, dev), x.shape, "dx")
+    if gate is not None:
+        dgate = torch.empty_like(x) if dgate is None else dgate
+        _shape(_need(dgate, "dgate", x.dtype, dev), x.shape, "dgate")
+    elif dgate is not None:
+        raise ValueError("dgate: the call has no gate")
+    if weight is not None and dweight is None:
+        dweight = torch.empty(shape, dtype=torch.float32, device=dev)
+    if bias is not None and dbias is None:
+        dbias = torch.empty(shape, dtype=torch.float32, device=dev)
+    _optional(dweight, "dweight", torch.float32, dev, shape)
+    _optional(dbias, "dbias", torch.float32, dev, shape)
+    ws, ws_bytes = _space(workspace, int(_lib.group_norm_workspace_size(p)), dev)
+    _launch(dev, _lib.group_norm_backward, p, _ptr(x), _ptr(gate), _ptr(weight), _ptr(bias), _ptr(dy),
+            _ptr(dx), _ptr(dgate), _ptr(dweight), _ptr(dbias), _ptr(ws), ws_bytes)
+    return dx, dgate, dweight, dbias
+
+
+def _mx_rows(x):
+    rows = 1
+    for s in x.shape[:-1]:
+        rows *= s
+    return rows
+
+
+def _mx_weights(w_codes, w_scales, depth, dev):
+    _need(w_codes, "w_codes", torch.uint8, dev)
+    _need(w_scales, "w_scales", torch.uint8, dev)
+    if w_codes.dim() != 2 or w_codes.shape[1] * 2 != depth:
+        raise ValueError(f"w_codes must be [cols,{depth // 2}], got {tuple(w_codes.shape)}")
+    _shape(w_scales, (w_codes.shape[0], depth // 32), "w_scales")
+
+
+def mx_quantize(x, codes=None, scales=None):
+    """Rows in microscaled 4-bit floating point (see gdnq_mx_quantize in
+    include/gdnq.h): x [..,depth] fp32 or bf16, depth a multiple of 32.
+    Returns (codes [..,depth/2], scales [..,depth/32]) uint8: E2M1 codes two
+    per byte, the even column in the low nibble, and one E8M0 exponent per 32
+    columns."""
+    _need(x, "x", None, None)
+    dev = x.device
+    if x.dtype not in _DT:
+        raise ValueError("x must be float32 or bfloat16")
+    if x.dim() < 1 or x.shape[-1] % 32:
+        raise ValueError("x must be [..,depth] with depth a multiple of 32")
+    depth = x.shape[-1]
+    cshape, sshape = x.shape[:-1] + (depth // 2,), x.shape[:-1] + (depth // 32,)
+    codes = torch.empty(cshape, dtype=torch.uint8, device=dev) if codes is None else codes
+    scales = torch.empty(sshape, dtype=torch.uint8, device=dev) if scales is None else scales
+    _shape(_need(codes, "codes", torch.uint8, dev), cshape, "codes")
+    _shape(_need(scales, "scales", torch.uint8, dev), sshape, "scales")
+    _launch(dev, _lib.mx_quantize, _ptr(x), _mx_rows(x), depth, _DT[x.dtype], _ptr(codes), _ptr(scales))
+    return codes, scales
+
+
+def mx_workspace_size(rows, cols, depth):
+    """Workspace bytes of mx_matmul and mx_linear at these sizes."""
+    return int(_lib.mx_workspace_size(_lib.MxParams(rows, cols, depth, 0, 0, 0)))
+
+
+def _mx_out(y, lead, cols, out_dtype, dev):
+    if out_dtype not in _DT:
+        raise ValueError("out_dtype must be float32 or bfloat16")
+    if y is None:
+        return torch.empty(lead + (cols,), dtype=out_dtype, device=dev)
+    return _shape(_need(y, "y", out_dtype, dev), lead + (cols,), "y")
+
+
+def mx_matmul(a_codes, a_scales, w_codes, w_scales, *, out_dtype=torch.bfloat16, y=None, workspace=None):
+    """y [..,cols] = A W^T for rows a [..,depth] and w [cols,depth] as
+    mx_quantize gives them (see gdnq_mx_matmul in include/gdnq.h)."""
+    _need(a_codes, "a_codes", torch.uint8, None)
+    dev = a_codes.device
+    if a_codes.dim() < 1:
+        raise ValueError("a_codes must be [..,depth/2]")
+    depth = a_codes.shape[-1] * 2
+    lead = a_codes.shape[:-1]
+    _shape(_need(a_scales, "a_scales", torch.uint8, dev), lead + (depth // 32,), "a_scales")
+    _mx_weights(w_codes, w_scales, depth, dev)
+    y = _mx_out(y, lead, w_codes.shape[0], out_dtype, dev)
+    p = _lib.MxParams(_mx_rows(a_codes), w_codes.shape[0], depth, 0, _DT[out_dtype], 0)
+    ws, ws_bytes = _space(workspace, int(_lib.mx_workspace_size(p)), dev)
+    _launch(dev, _lib.mx_matmul, p, _ptr(a_codes), _ptr(a_scales), _ptr(w_codes), _ptr(w_scales), _ptr(y),
+            _ptr(ws), ws_bytes)
+    return y
+
+
+def mx_linear(x, w_codes, w_scales, *, out_dtype=None, y=None, workspace=None):
+    """y [..,cols] = Q(x) W^T: x [..,depth] fp32 or bf16 quantized as by
+    mx_quantize, times weights w [cols,depth] stored in that form.  out_dtype
+    (default x's) float32 or bfloat16."""
+    _need(x, "x", None, None)
+    dev = x.device
+    if x.dtype not in _DT:
+        raise ValueError("x must be float32 or bfloat16")
+    if x.dim() < 1:
+        raise ValueError("x must be [..,depth]")
+    depth = x.shape[-1]
+    _mx_weights(w_codes, w_scales, depth, dev)
+    out_dtype = out_dtype or (x.dtype if y is None else y.dtype)
+    y = _mx_out(y, x.shape[:-1], w_codes.shape[0], out_dtype, dev)
+    p = _lib.MxParams(_mx_rows(x), w_codes.shape[0], depth, _DT[x.dtype], _DT[out_dtype], 0)
+    ws, ws_bytes = _space(workspace, int(_lib.mx_workspace_size(p)), dev)
+    _launch(dev, _lib.mx_linear, p, _ptr(x), _ptr(w_codes), _ptr(w_scales), _ptr(y), _ptr(ws), ws_bytes)
+    return y

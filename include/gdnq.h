@@ -473,7 +473,8 @@ gdnq_status gdnq_prefill_resume(const gdnq_prefill_params* p, const int32_t* cu_
  *   clamped to [0, T]; malformed ones give unspecified results and no access
  *   outside the buffers.  p->channels C >= 1 (even C is faster in bf16);
  *   p->dtype (x, gate, y and their gradients) GDNQ_F32 or GDNQ_BF16; B >= 0,
- *   T >= 0, at most 2^31 - 1 tokens and B C <= 2^31 - 1.
+ *   T >= 0, at most 2^31 - 4097 tokens, B C <= 2^31 - 1 and
+ *   ceil(tokens / GDNQ_SCAN_CHUNK) ceil(C / 64) <= 2^31 - 1.
  *   A NaN or infinity stays in its own channel and sequence.
  *
  *   gdnq_scan_forward

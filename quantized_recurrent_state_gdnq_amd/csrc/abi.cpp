@@ -628,10 +628,11 @@ static gdnq_status scan_validate(const gdnq_scan_params* p, bool varlen, gdnq::S
   if (p->flags & ~uint32_t(GDNQ_SCAN_LOGITS | GDNQ_SCAN_LERP))
     return fail(GDNQ_ERR_FLAGS, "flags 0x%x: the scan takes GDNQ_SCAN_LOGITS and GDNQ_SCAN_LERP", p->flags);
   const int64_t n = varlen ? int64_t(p->seqlen) : int64_t(p->batch) * p->seqlen;
-  if (n > 0x7fffffffLL) return fail(GDNQ_ERR_SHAPE, "%lld tokens: at most 2^31 - 1", (long long)n);
+  if (n > 0x7fffffffLL - 4096) return fail(GDNQ_ERR_SHAPE, "%lld tokens: at most 2^31 - 4097", (long long)n);
   if (int64_t(p->batch) * p->channels > 0x7fffffffLL)
     return fail(GDNQ_ERR_SHAPE, "batch * channels = %lld: at most 2^31 - 1", (long long)p->batch * p->channels);
-  if ((n + GDNQ_SCAN_CHUNK - 1) / GDNQ_SCAN_CHUNK * p->channels > (int64_t(1) << 36))
+  // one workgroup per chunk and 64 channels
+  if ((n + GDNQ_SCAN_CHUNK - 1) / GDNQ_SCAN_CHUNK * ((int64_t(p->channels) + 63) / 64) > 0x7fffffffLL)
     return fail(GDNQ_ERR_SHAPE, "%lld tokens of %d channels: too large", (long long)n, p->channels);
   L = gdnq::ScanLaunch{};
   L.B = p->batch; L.T = p->seqlen; L.C = p->channels; L.N = n;

@@ -2,8 +2,27 @@
 // gdnq_scan_* in gdnq.h): forward with the states for the backward pass, the
 // backward pass, and the single-token step.
 //
-// One lane per channel and sequence walks the tokens in order: the plain form
-// of the definition.
+// Forward and backward are one pass over the tokens each.  The tokens of the
+// whole call (all sequences, back to back) are cut into chunks, and a
+// workgroup takes one chunk of 64 or 128 channels: lanes hold channels, waves
+// hold runs of RUN tokens, whose inputs stay in registers.
+//   1. Each wave folds its run to the pair (A, H) with h_out = A h_in + H.  A
+//      sequence's first token has A = 0 (its state comes from h0), so runs,
+//      waves and chunks may hold any number of sequence borders.
+//   2. The waves' pairs go through LDS to the chunk's pair, which is published
+//      in the workspace; the state that enters the chunk is folded from the
+//      published pairs of the chunks before it, back to the chunk that holds
+//      its first token's sequence start, or to the last group border: every
+//      GROUP-th chunk publishes its outgoing state too, so a chunk reads at
+//      most GROUP - 1 pairs and one state.  The fold's order is fixed by the
+//      sizes alone.
+//   3. Every wave walks its run again from the state it now knows and writes.
+// Waiting: chunks are taken by ticket (a counter per channel tile), so the
+// chunk before the one a workgroup waits for is always held by a workgroup
+// that runs already and, by induction over the tickets, ends: no order of
+// dispatch is assumed.  A published pair carries its own mark (the workspace
+// starts as all ones, which no published pair has), so a single relaxed
+// 8-byte atomic is the whole hand-over.
 #include <hip/hip_runtime.h>
 
 #include "../../include/gdnq.h"
@@ -14,7 +33,23 @@
 namespace gdnq {
 namespace {
 
-constexpr int CHUNK = GDNQ_SCAN_CHUNK;
+constexpr int RUN = 16;  // tokens per wave
+constexpr int FWD_WAVES = 16, BWD_WAVES = GDNQ_SCAN_CHUNK / RUN;
+constexpr int FWD_CHUNK = FWD_WAVES * RUN, BWD_CHUNK = BWD_WAVES * RUN;
+constexpr int GROUP = 16;  // chunks per published state
+static_assert(BWD_CHUNK == GDNQ_SCAN_CHUNK && FWD_CHUNK % GDNQ_SCAN_CHUNK == 0, "carry rows are chunk borders");
+
+constexpr unsigned long long EMPTY = ~0ull;
+
+// The chain of chunks in the workspace: a ticket counter per channel tile,
+// then a pair per chunk and channel, then a state per group and channel.
+struct Chain {
+  uint32_t* ticket;  // null: the call is one chunk
+  unsigned long long* pair;
+  unsigned long long* state;
+};
+
+__host__ __device__ inline size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 // a = gate or sigmoid(gate), and keep = 1 - a without cancellation.
 template <bool LOGITS>
@@ -27,80 +62,545 @@ __device__ __forceinline__ void gate_of(float g, float& a, float& keep) {
   }
 }
 
-__device__ __forceinline__ void sequence_of(const int32_t* cu, int b, int T, int64_t N, int64_t& t0, int64_t& t1) {
+// V channels of one token: in memory, and as the registers that hold them.
+template <typename E, int V>
+struct Cell;
+template <>
+struct Cell<bf16, 2> {
+  uint32_t w;
+  __device__ __forceinline__ void load(const bf16* p) { w = *reinterpret_cast<const uint32_t*>(p); }
+  __device__ __forceinline__ float get(int i) const { return i ? bf16_hi(w) : bf16_lo(w); }
+  __device__ static __forceinline__ void store(bf16* p, const float (&v)[2]) {
+    *reinterpret_cast<bf16x2*>(p) = __builtin_convertvector(f32x2{v[0], v[1]}, bf16x2);
+  }
+};
+template <typename E>
+struct Cell<E, 1> {
+  E w;
+  __device__ __forceinline__ void load(const E* p) { w = *p; }
+  __device__ __forceinline__ float get(int) const { return to_f32(w); }
+  __device__ static __forceinline__ void store(E* p, const float (&v)[1]) { store_f32(p, v[0]); }
+};
+
+// What a wave needs to know of the RUN tokens from row0 on: bit r of the
+// masks is token row0 + r; lane r holds its sequence.
+struct Rows {
+  uint32_t valid, start, end;
+  int seq;
+  __device__ __forceinline__ int seq_of(int r) const { return __builtin_amdgcn_readlane(seq, r); }
+};
+
+// The last offset that is <= row among cu[0..B] (-1: none).
+__device__ __forceinline__ int sequence_at(const int32_t* cu, int B, int row) {
+  int lo = 0, hi = B + 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (cu[mid] <= row) lo = mid + 1;
+    else hi = mid;
+  }
+  return lo - 1;
+}
+
+// first: the first token of the sequence that holds row0 (row0 + 1 if none does).
+__device__ __forceinline__ Rows rows_of(const int32_t* __restrict__ cu, int B, int T, int64_t N, int row0, int lane,
+                                        int& first) {
+  const int row = row0 + lane;
+  bool valid = lane < RUN && row < N, start, end;
+  Rows w;
   if (cu) {
-    t0 = min(max(int64_t(cu[b]), int64_t(0)), N);
-    t1 = min(max(int64_t(cu[b + 1]), t0), N);
+    const int s0 = sequence_at(cu, B, row0);
+    int s = s0;
+    start = s >= 0 && cu[max(s, 0)] == row;
+    end = false;
+    for (int j = s0 + 1; j <= B; ++j) {
+      const int c = cu[j];
+      if (c > row0 + RUN) break;
+      if (c <= row) {
+        s = j;
+        start = c == row;
+      }
+      end |= c == row + 1;
+    }
+    valid &= s >= 0 && s < B;
+    w.seq = s;
+    first = s0 >= 0 && s0 < B ? max(cu[max(s0, 0)], 0) : row0 + 1;
   } else {
-    t0 = int64_t(b) * T;
-    t1 = t0 + T;
+    const uint32_t s = uint32_t(row) / uint32_t(T), t = uint32_t(row) - s * uint32_t(T);
+    w.seq = int(s);
+    start = t == 0;
+    end = t + 1 == uint32_t(T);
+    first = row0 < N ? int(uint32_t(row0) / uint32_t(T) * uint32_t(T)) : row0 + 1;
+  }
+  w.valid = uint32_t(__builtin_amdgcn_ballot_w64(valid));
+  w.start = uint32_t(__builtin_amdgcn_ballot_w64(valid && start));
+  w.end = uint32_t(__builtin_amdgcn_ballot_w64(valid && end));
+  return w;
+}
+
+__device__ __forceinline__ unsigned long long pack_pair(float a, float h) {
+  uint32_t lo = __float_as_uint(a);
+  if (lo == 0xffffffffu) lo = 0x7fc00000u;  // another NaN: the mark stays free
+  return (static_cast<unsigned long long>(__float_as_uint(h)) << 32) | lo;
+}
+
+template <int V>
+__device__ __forceinline__ void publish(unsigned long long* p, const float (&a)[V], const float (&h)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    __hip_atomic_store(p + i, pack_pair(a[i], h[i]), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+template <int V>
+__device__ __forceinline__ void await(const unsigned long long* p, float (&a)[V], float (&h)[V]) {
+  unsigned long long w[V];
+  for (;;) {
+    bool there = true;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      w[i] = __hip_atomic_load(p + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      there &= w[i] != EMPTY;
+    }
+    if (there) break;
+    __builtin_amdgcn_s_sleep(1);
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    a[i] = __uint_as_float(uint32_t(w[i]));
+    h[i] = __uint_as_float(uint32_t(w[i] >> 32));
   }
 }
 
-template <typename E, bool LOGITS, bool LERP>
-__global__ __launch_bounds__(64) void scan_forward_kernel(ScanLaunch L) {
-  const int c = blockIdx.x * 64 + threadIdx.x;
-  if (c >= L.C) return;
-  const E* x = static_cast<const E*>(L.x) + c;
-  const E* gate = static_cast<const E*>(L.gate) + c;
-  E* y = static_cast<E*>(L.y) + c;
-  for (int b = blockIdx.y; b < L.B; b += gridDim.y) {
-    int64_t t0, t1;
-    sequence_of(L.cu_seqlens, b, L.T, L.N, t0, t1);
-    float h = L.h0 ? L.h0[int64_t(b) * L.C + c] : 0.0f;
-    for (int64_t t = t0; t < t1; ++t) {
-      if (L.carry && t % CHUNK == 0) L.carry[t / CHUNK * L.C + c] = h;
+// A tile of LDS: a pair per wave (or chunk of the group) and channel.
+template <int V>
+__device__ __forceinline__ void put(f32x2* p, const float (&a)[V], const float (&h)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) p[i] = f32x2{a[i], h[i]};
+}
+
+// (a, h) := the pair at p after (a, h).  Behind a border (cut) h does not
+// enter at all: a NaN or an infinity of one sequence is not multiplied by the
+// next one's zero.
+template <int V>
+__device__ __forceinline__ void then(const f32x2* p, bool cut, float (&a)[V], float (&h)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    h[i] = fmaf(p[i].x, cut ? 0.0f : h[i], p[i].y);
+    a[i] *= p[i].x;
+  }
+}
+
+// Which waves of the workgroup have a border in their run (bit per wave).
+template <int WAVES>
+__device__ __forceinline__ uint32_t waves_with(const uint32_t* borders, int lane) {
+  return uint32_t(__builtin_amdgcn_ballot_w64(lane < WAVES && borders[lane & (WAVES - 1)] != 0));
+}
+
+// The state that enters a chunk, by all waves of its workgroup: place is the
+// chunk's place in the order of the chain, from the first place whose pair it
+// needs (place itself: none).  Ends with a barrier; carry[] holds the states.
+template <int V, int WAVES>
+__device__ __forceinline__ void enter_chunk(const Chain& chain, int place, int from, int C, int c, bool active, int wave,
+                                            int lane, f32x2 (*pairs)[64 * V], float* carry) {
+  const int border = place / GROUP * GROUP;
+  const bool base = from < border;  // the group's incoming state, then the group's pairs
+  const int lo = base ? border : from;
+#pragma unroll
+  for (int k = 0; k < GROUP; k += WAVES) {
+    const int j = lo + k + wave;
+    if (j < place && active) {
+      float a[V], h[V];
+      await<V>(chain.pair + int64_t(j) * C + c, a, h);
+      put<V>(&pairs[k + wave][lane * V], a, h);
+    }
+  }
+  if (wave == WAVES - 1 && active) {  // (the last wave has a pair to wait for only where GROUP > WAVES)
+    float a[V], h[V] = {};
+    if (base) await<V>(chain.state + int64_t(border / GROUP - 1) * C + c, a, h);
+#pragma unroll
+    for (int i = 0; i < V; ++i) carry[lane * V + i] = h[i];
+  }
+  __syncthreads();
+  if (wave == 0 && active) {
+    float a[V] = {}, h[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) h[i] = carry[lane * V + i];
+    for (int j = lo; j < place; ++j) then<V>(&pairs[j - lo][lane * V], false, a, h);
+#pragma unroll
+    for (int i = 0; i < V; ++i) carry[lane * V + i] = h[i];
+  }
+  __syncthreads();
+}
+
+template <int V>
+__device__ __forceinline__ void add_h0(const float* h0, int seq, int C, int c, const float (&a)[V], float (&b)[V]) {
+  if (!h0) return;
+#pragma unroll
+  for (int i = 0; i < V; ++i) b[i] = fmaf(a[i], h0[int64_t(seq) * C + c + i], b[i]);
+}
+
+__device__ __forceinline__ int take_ticket(uint32_t* ticket) {
+  __shared__ int mine;
+  if (threadIdx.x == 0)
+    mine = int(__hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+  __syncthreads();
+  return mine;
+}
+
+template <typename E, int V, bool LOGITS, bool LERP>
+__global__ __launch_bounds__(FWD_WAVES * 64) void scan_forward_kernel(ScanLaunch L, Chain chain, const int32_t* __restrict__ cu,
+                                                                      const E* __restrict__ xs, const E* __restrict__ gates, int tiles) {
+  constexpr int WAVES = FWD_WAVES, CT = 64 * V;
+  __shared__ f32x2 wave_pair[WAVES][CT];
+  __shared__ f32x2 pairs[GROUP][CT];
+  __shared__ float carry[CT];
+  __shared__ uint32_t borders[WAVES];
+  __shared__ int first_row;
+  const int tile = blockIdx.x % tiles;
+  const int chunk = chain.ticket ? take_ticket(chain.ticket + tile) : 0;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int c = tile * CT + lane * V, C = L.C;
+  const bool active = c < C;
+  const int row0 = chunk * FWD_CHUNK + wave * RUN;
+
+  Cell<E, V> x[RUN], g[RUN];
+#pragma unroll
+  for (int r = 0; r < RUN; ++r) {
+    if (active && row0 + r < L.N) {
+      const int64_t at = int64_t(row0 + r) * C + c;
+      x[r].load(xs + at);
+      g[r].load(gates + at);
+    }
+  }
+  int first;
+  const Rows rows = rows_of(cu, L.B, L.T, L.N, row0, lane, first);
+  if (threadIdx.x == 0) first_row = first;
+
+  float A[V], H[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    A[i] = 1.0f;
+    H[i] = 0.0f;
+  }
+#pragma unroll
+  for (int r = 0; r < RUN; ++r) {
+    if (!(rows.valid >> r & 1)) continue;
+    float a[V], b[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float keep;
+      gate_of<LOGITS>(g[r].get(i), a[i], keep);
+      b[i] = LERP ? keep * x[r].get(i) : x[r].get(i);
+    }
+    if (rows.start >> r & 1) {
+      if (active) add_h0<V>(L.h0, rows.seq_of(r), C, c, a, b);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        A[i] = 0.0f;
+        H[i] = b[i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        H[i] = fmaf(a[i], H[i], b[i]);
+        A[i] *= a[i];
+      }
+    }
+  }
+  put<V>(&wave_pair[wave][lane * V], A, H);
+  if (lane == 0) borders[wave] = rows.start;
+  __syncthreads();
+
+  // the pair of the waves before this one
+  const uint32_t cuts = waves_with<WAVES>(borders, lane);
+  float pa[V], ph[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    pa[i] = 1.0f;
+    ph[i] = 0.0f;
+  }
+  for (int w = 0; w < wave; ++w) then<V>(&wave_pair[w][lane * V], cuts >> w & 1, pa, ph);
+  float in[V] = {};
+  if (chain.ticket) {
+    if (wave == WAVES - 1) {  // the chunk's pair
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        H[i] = fmaf(A[i], rows.start ? 0.0f : ph[i], H[i]);
+        A[i] *= pa[i];
+      }
+      if (active) publish<V>(chain.pair + int64_t(chunk) * C + c, A, H);
+    }
+    const int start = first_row;
+    const int from = start >= chunk * FWD_CHUNK ? chunk : start / FWD_CHUNK;
+    enter_chunk<V, WAVES>(chain, chunk, from, C, c, active, wave, lane, pairs, carry);
+#pragma unroll
+    for (int i = 0; i < V; ++i) in[i] = carry[lane * V + i];
+    if (wave == WAVES - 1 && chunk % GROUP == GROUP - 1 && active) {
+      float out[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) out[i] = fmaf(A[i], cuts ? 0.0f : in[i], H[i]);
+      publish<V>(chain.state + int64_t(chunk / GROUP) * C + c, in, out);
+    }
+  }
+
+  float h[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) h[i] = fmaf(pa[i], cuts & ((1u << wave) - 1) ? 0.0f : in[i], ph[i]);
+  if (L.carry && wave % (GDNQ_SCAN_CHUNK / RUN) == 0 && active && row0 < L.N) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) L.carry[int64_t(row0 / GDNQ_SCAN_CHUNK) * C + c + i] = h[i];
+  }
+  E* ys = static_cast<E*>(L.y);
+#pragma unroll
+  for (int r = 0; r < RUN; ++r) {
+    if (!(rows.valid >> r & 1)) continue;
+    float a[V], b[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float keep;
+      gate_of<LOGITS>(g[r].get(i), a[i], keep);
+      b[i] = LERP ? keep * x[r].get(i) : x[r].get(i);
+    }
+    if (rows.start >> r & 1) {
+      if (active) add_h0<V>(L.h0, rows.seq_of(r), C, c, a, b);
+#pragma unroll
+      for (int i = 0; i < V; ++i) h[i] = b[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) h[i] = fmaf(a[i], h[i], b[i]);
+    }
+    if (active) {
+      Cell<E, V>::store(ys + int64_t(row0 + r) * C + c, h);
+      if (L.h_last && (rows.end >> r & 1)) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) L.h_last[int64_t(rows.seq_of(r)) * C + c + i] = h[i];
+      }
+    }
+  }
+}
+
+// The backward pass runs the chain from the last chunk to the first with
+// m_t = a_t l_t, what token t passes on to the token before it:
+//   l_t = dy_t (+ dh_last at a sequence's last token) + m_{t+1},
+// again pairs with m_out = A m_in + H, A = 0 over a sequence border.  The
+// states h_{t-1} are formed again from the chunk's row of carry.
+template <typename E, int V, bool LOGITS, bool LERP>
+__global__ __launch_bounds__(BWD_WAVES * 64) void scan_backward_kernel(ScanLaunch L, Chain chain, const int32_t* __restrict__ cu,
+                                                                       const E* __restrict__ xs, const E* __restrict__ gates,
+                                                                       const E* __restrict__ dys, int tiles, int chunks) {
+  constexpr int WAVES = BWD_WAVES, CT = 64 * V;
+  __shared__ f32x2 wave_pair[WAVES][CT];  // of h, forwards
+  __shared__ f32x2 wave_back[WAVES][CT];  // of m, backwards
+  __shared__ f32x2 pairs[GROUP][CT];
+  __shared__ float carry[CT];
+  __shared__ uint32_t starts[WAVES], borders[WAVES];
+  __shared__ int last_row;
+  const int tile = blockIdx.x % tiles;
+  const int place = chain.ticket ? take_ticket(chain.ticket + tile) : 0, chunk = chunks - 1 - place;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int c = tile * CT + lane * V, C = L.C;
+  const bool active = c < C;
+  const int row0 = chunk * BWD_CHUNK + wave * RUN;
+
+  Cell<E, V> x[RUN], g[RUN], dy[RUN];
+#pragma unroll
+  for (int r = 0; r < RUN; ++r) {
+    if (active && row0 + r < L.N) {
+      const int64_t at = int64_t(row0 + r) * C + c;
+      x[r].load(xs + at);
+      g[r].load(gates + at);
+      dy[r].load(dys + at);
+    }
+  }
+  float h_in[V] = {};
+  if (active && row0 < L.N) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) h_in[i] = L.carry[int64_t(chunk) * C + c + i];
+  }
+  int first;
+  const Rows rows = rows_of(cu, L.B, L.T, L.N, row0, lane, first);
+  if (threadIdx.x == WAVES * 64 - 64) {
+    // the last token of the sequence that holds the chunk's last token (the
+    // chunk's own last where none does, or where it ends there)
+    const int at = chunk * BWD_CHUNK + BWD_CHUNK - 1;
+    int e = at;
+    if (at < L.N) {
+      if (cu) {
+        const int s = sequence_at(cu, L.B, at);
+        if (s >= 0 && s < L.B) e = max(int(min(int64_t(cu[s + 1]), L.N)) - 1, at);
+      } else {
+        e = int((uint32_t(at) / uint32_t(L.T) + 1) * uint32_t(L.T)) - 1;
+      }
+    }
+    last_row = e;
+  }
+
+  float A[V], H[V], M[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    A[i] = 1.0f;
+    H[i] = M[i] = 0.0f;
+  }
+#pragma unroll
+  for (int r = 0; r < RUN; ++r) {
+    if (!(rows.valid >> r & 1)) continue;
+    float a[V], b[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float keep;
+      gate_of<LOGITS>(g[r].get(i), a[i], keep);
+      b[i] = LERP ? keep * x[r].get(i) : x[r].get(i);
+    }
+    if (rows.start >> r & 1) {
+      if (active) add_h0<V>(L.h0, rows.seq_of(r), C, c, a, b);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        A[i] = 0.0f;
+        H[i] = b[i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        H[i] = fmaf(a[i], H[i], b[i]);
+        A[i] *= a[i];
+      }
+    }
+  }
+#pragma unroll
+  for (int r = RUN - 1; r >= 0; --r) {
+    if (!(rows.valid >> r & 1)) continue;
+    if (rows.start >> r & 1) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) M[i] = 0.0f;
+      continue;
+    }
+    if ((rows.end >> r & 1)) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) M[i] = L.dh_last && active ? L.dh_last[int64_t(rows.seq_of(r)) * C + c + i] : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
       float a, keep;
-      gate_of<LOGITS>(to_f32(gate[t * L.C]), a, keep);
-      const float v = to_f32(x[t * L.C]);
-      h = fmaf(a, h, LERP ? keep * v : v);
-      store_f32(y + t * L.C, h);
+      gate_of<LOGITS>(g[r].get(i), a, keep);
+      M[i] = a * (dy[r].get(i) + M[i]);
     }
-    if (L.h_last) L.h_last[int64_t(b) * L.C + c] = h;
+  }
+  put<V>(&wave_pair[wave][lane * V], A, H);
+  // a border behind the run's last token is a border of m too, but not of h
+  const bool border = rows.start != 0 || rows.end != 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) H[i] = border ? 0.0f : A[i];
+  put<V>(&wave_back[wave][lane * V], H, M);
+  if (lane == 0) {
+    starts[wave] = rows.start;
+    borders[wave] = border;
+  }
+  __syncthreads();
+
+  {
+    const uint32_t cuts = waves_with<WAVES>(starts, lane);
+    float a[V] = {};
+    for (int w = 0; w < wave; ++w) then<V>(&wave_pair[w][lane * V], cuts >> w & 1, a, h_in);
+  }
+  const uint32_t cuts = waves_with<WAVES>(borders, lane);
+  // the pair of the waves behind this one
+  float pa[V], pm[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    pa[i] = 1.0f;
+    pm[i] = 0.0f;
+  }
+  for (int w = WAVES - 1; w > wave; --w) then<V>(&wave_back[w][lane * V], cuts >> w & 1, pa, pm);
+  float in[V] = {};
+  if (chain.ticket) {
+    if (wave == 0) {  // the chunk's pair
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        M[i] = fmaf(H[i], border ? 0.0f : pm[i], M[i]);
+        H[i] *= pa[i];
+      }
+      if (active) publish<V>(chain.pair + int64_t(place) * C + c, H, M);
+    }
+    const int from = min(place, max(0, chunks - 1 - last_row / BWD_CHUNK));
+    enter_chunk<V, WAVES>(chain, place, from, C, c, active, wave, lane, pairs, carry);
+#pragma unroll
+    for (int i = 0; i < V; ++i) in[i] = carry[lane * V + i];
+    if (wave == 0 && place % GROUP == GROUP - 1 && active) {
+      float out[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) out[i] = fmaf(H[i], cuts ? 0.0f : in[i], M[i]);
+      publish<V>(chain.state + int64_t(place / GROUP) * C + c, in, out);
+    }
+  }
+  float m[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) m[i] = fmaf(pa[i], cuts >> (wave + 1) ? 0.0f : in[i], pm[i]);
+
+  float before[RUN][V];
+#pragma unroll
+  for (int r = 0; r < RUN; ++r) {
+    if (!(rows.valid >> r & 1)) continue;
+    if (rows.start >> r & 1) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) h_in[i] = L.h0 && active ? L.h0[int64_t(rows.seq_of(r)) * C + c + i] : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      before[r][i] = h_in[i];
+      float a, keep;
+      gate_of<LOGITS>(g[r].get(i), a, keep);
+      h_in[i] = fmaf(a, h_in[i], LERP ? keep * x[r].get(i) : x[r].get(i));
+    }
+  }
+  E* dxs = static_cast<E*>(L.dx);
+  E* dgs = static_cast<E*>(L.dgate);
+#pragma unroll
+  for (int r = RUN - 1; r >= 0; --r) {
+    if (!(rows.valid >> r & 1)) continue;
+    if (rows.end >> r & 1) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) m[i] = L.dh_last && active ? L.dh_last[int64_t(rows.seq_of(r)) * C + c + i] : 0.0f;
+    }
+    float dx[V], dg[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float a, keep;
+      gate_of<LOGITS>(g[r].get(i), a, keep);
+      const float lam = dy[r].get(i) + m[i];
+      const float da = lam * (LERP ? before[r][i] - x[r].get(i) : before[r][i]);
+      dx[i] = LERP ? keep * lam : lam;
+      dg[i] = LOGITS ? da * (a * keep) : da;
+      m[i] = a * lam;
+    }
+    if (active) {
+      const int64_t at = int64_t(row0 + r) * C + c;
+      Cell<E, V>::store(dxs + at, dx);
+      Cell<E, V>::store(dgs + at, dg);
+      if (L.dh0 && (rows.start >> r & 1)) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) L.dh0[int64_t(rows.seq_of(r)) * C + c + i] = m[i];
+      }
+    }
   }
 }
 
-// Chunk by chunk from the back: the chunk's states from its carry, then the
-// reverse recurrence over it.
-template <typename E, bool LOGITS, bool LERP>
-__global__ __launch_bounds__(64) void scan_backward_kernel(ScanLaunch L) {
-  __shared__ float before[CHUNK][64];
-  const int c = blockIdx.x * 64 + threadIdx.x;
-  if (c >= L.C) return;
-  const E* x = static_cast<const E*>(L.x) + c;
-  const E* gate = static_cast<const E*>(L.gate) + c;
-  const E* dy = static_cast<const E*>(L.dy) + c;
-  E* dx = static_cast<E*>(L.dx) + c;
-  E* dgate = static_cast<E*>(L.dgate) + c;
-  for (int b = blockIdx.y; b < L.B; b += gridDim.y) {
-    int64_t t0, t1;
-    sequence_of(L.cu_seqlens, b, L.T, L.N, t0, t1);
-    float m = L.dh_last ? L.dh_last[int64_t(b) * L.C + c] : 0.0f;
-    for (int64_t end = t1; end > t0;) {
-      const int64_t begin = max(t0, (end - 1) / CHUNK * CHUNK);
-      float h = begin == t0 ? (L.h0 ? L.h0[int64_t(b) * L.C + c] : 0.0f) : L.carry[begin / CHUNK * L.C + c];
-      for (int64_t t = begin; t < end; ++t) {
-        before[t - begin][threadIdx.x] = h;
-        float a, keep;
-        gate_of<LOGITS>(to_f32(gate[t * L.C]), a, keep);
-        const float v = to_f32(x[t * L.C]);
-        h = fmaf(a, h, LERP ? keep * v : v);
-      }
-      for (int64_t t = end - 1; t >= begin; --t) {
-        float a, keep;
-        gate_of<LOGITS>(to_f32(gate[t * L.C]), a, keep);
-        const float lam = to_f32(dy[t * L.C]) + m;
-        float da = before[t - begin][threadIdx.x];
-        if (LERP) da -= to_f32(x[t * L.C]);
-        da *= lam;
-        store_f32(dgate + t * L.C, LOGITS ? da * (a * keep) : da);
-        store_f32(dx + t * L.C, LERP ? keep * lam : lam);
-        m = a * lam;
-      }
-      end = begin;
-    }
-    if (L.dh0) L.dh0[int64_t(b) * L.C + c] = m;
+// out[s] = in[s] (zero where in is null) for the sequences without tokens:
+// the states pass through.  A wave looks at 64 sequences at a time.
+__global__ __launch_bounds__(256) void scan_empty_kernel(const int32_t* __restrict__ cu, const float* __restrict__ in,
+                                                         float* __restrict__ out, int B, int C, int N) {
+  const int lane = threadIdx.x & 63, s = (blockIdx.x * 4 + (threadIdx.x >> 6)) * 64 + lane;
+  bool empty = s < B;
+  if (empty && cu) empty = min(max(cu[s], 0), N) >= min(max(cu[s + 1], 0), N);
+  for (uint64_t left = __builtin_amdgcn_ballot_w64(empty); left; left &= left - 1) {
+    const int64_t at = int64_t(s - lane + __builtin_ctzll(left)) * C;
+    for (int c = lane; c < C; c += 64) out[at + c] = in ? in[at + c] : 0.0f;
   }
+}
+
+// Empties the chain: tickets 0, pairs and states all ones.
+__global__ __launch_bounds__(256) void scan_reset_kernel(uint32_t* ticket, int tiles, ulonglong2* rest, int64_t n) {
+  const int64_t i = blockIdx.x * int64_t(256) + threadIdx.x;
+  if (i < tiles) ticket[i] = 0;
+  if (i < n) rest[i] = ulonglong2{EMPTY, EMPTY};
 }
 
 template <typename E, bool LOGITS, bool LERP>
@@ -115,34 +615,70 @@ __global__ __launch_bounds__(256) void scan_step_kernel(ScanLaunch L) {
   store_f32(static_cast<E*>(L.y) + i, h);
 }
 
-// F<E, LOGITS, LERP> for the call's type and flags.
-template <template <typename, bool, bool> class F>
-hipError_t dispatch(const ScanLaunch& L, hipStream_t stream) {
-  if (L.bf16) {
-    if (L.logits) return L.lerp ? F<bf16, true, true>::go(L, stream) : F<bf16, true, false>::go(L, stream);
-    return L.lerp ? F<bf16, false, true>::go(L, stream) : F<bf16, false, false>::go(L, stream);
-  }
-  if (L.logits) return L.lerp ? F<float, true, true>::go(L, stream) : F<float, true, false>::go(L, stream);
-  return L.lerp ? F<float, false, true>::go(L, stream) : F<float, false, false>::go(L, stream);
+struct Layout {
+  int tiles;
+  int64_t chunks, words;  // 8-byte words of pairs and states
+  size_t bytes;
+};
+
+Layout layout_of(int64_t N, int C, int chunk, int V) {
+  Layout l;
+  l.tiles = (C + 64 * V - 1) / (64 * V);
+  l.chunks = (N + chunk - 1) / chunk;
+  l.words = (l.chunks + l.chunks / GROUP) * C + 1;
+  l.bytes = l.chunks > 1 ? align256(size_t(l.tiles) * 4) + size_t(l.words + 1) / 2 * 16 : 0;
+  return l;
 }
 
-template <typename E, bool LOGITS, bool LERP>
+// Clears the chain for the call, unless it is one chunk.
+hipError_t reset_chain(const Layout& l, int C, void* workspace, Chain& chain, hipStream_t stream) {
+  chain = Chain{};
+  if (l.chunks <= 1) return hipSuccess;
+  chain.ticket = static_cast<uint32_t*>(workspace);
+  chain.pair = reinterpret_cast<unsigned long long*>(static_cast<char*>(workspace) + align256(size_t(l.tiles) * 4));
+  chain.state = chain.pair + l.chunks * C;
+  const int64_t n = (l.words + 1) / 2, most = n > l.tiles ? n : l.tiles;
+  scan_reset_kernel<<<uint32_t((most + 255) / 256), 256, 0, stream>>>(chain.ticket, l.tiles,
+                                                                    reinterpret_cast<ulonglong2*>(chain.pair), n);
+  return hipGetLastError();
+}
+
+hipError_t pass_empty(const ScanLaunch& L, const float* in, float* out, hipStream_t stream) {
+  if (!out || (!L.cu_seqlens && L.N > 0)) return hipSuccess;
+  scan_empty_kernel<<<(L.B + 255) / 256, 256, 0, stream>>>(L.cu_seqlens, in, out, L.B, L.C, int(L.N));
+  return hipGetLastError();
+}
+
+template <typename E, int V, bool LOGITS, bool LERP>
 struct Forward {
   static hipError_t go(const ScanLaunch& L, hipStream_t stream) {
-    scan_forward_kernel<E, LOGITS, LERP><<<dim3((L.C + 63) / 64, min(L.B, 65535)), 64, 0, stream>>>(L);
+    if (hipError_t e = pass_empty(L, L.h0, L.h_last, stream)) return e;
+    if (L.N == 0) return hipSuccess;
+    const Layout l = layout_of(L.N, L.C, FWD_CHUNK, V);
+    Chain chain;
+    if (hipError_t e = reset_chain(l, L.C, L.workspace, chain, stream)) return e;
+    scan_forward_kernel<E, V, LOGITS, LERP><<<uint32_t(l.chunks * l.tiles), FWD_WAVES * 64, 0, stream>>>(
+        L, chain, L.cu_seqlens, static_cast<const E*>(L.x), static_cast<const E*>(L.gate), l.tiles);
     return hipGetLastError();
   }
 };
 
-template <typename E, bool LOGITS, bool LERP>
+template <typename E, int V, bool LOGITS, bool LERP>
 struct Backward {
   static hipError_t go(const ScanLaunch& L, hipStream_t stream) {
-    scan_backward_kernel<E, LOGITS, LERP><<<dim3((L.C + 63) / 64, min(L.B, 65535)), 64, 0, stream>>>(L);
+    if (hipError_t e = pass_empty(L, L.dh_last, L.dh0, stream)) return e;
+    if (L.N == 0) return hipSuccess;
+    const Layout l = layout_of(L.N, L.C, BWD_CHUNK, V);
+    Chain chain;
+    if (hipError_t e = reset_chain(l, L.C, L.workspace, chain, stream)) return e;
+    scan_backward_kernel<E, V, LOGITS, LERP><<<uint32_t(l.chunks * l.tiles), BWD_WAVES * 64, 0, stream>>>(
+        L, chain, L.cu_seqlens, static_cast<const E*>(L.x), static_cast<const E*>(L.gate), static_cast<const E*>(L.dy), l.tiles,
+        int(l.chunks));
     return hipGetLastError();
   }
 };
 
-template <typename E, bool LOGITS, bool LERP>
+template <typename E, int V, bool LOGITS, bool LERP>
 struct Step {
   static hipError_t go(const ScanLaunch& L, hipStream_t stream) {
     scan_step_kernel<E, LOGITS, LERP><<<uint32_t((int64_t(L.B) * L.C + 255) / 256), 256, 0, stream>>>(L);
@@ -150,9 +686,28 @@ struct Step {
   }
 };
 
+template <template <typename, int, bool, bool> class F, typename E, int V>
+hipError_t by_flags(const ScanLaunch& L, hipStream_t stream) {
+  if (L.logits) return L.lerp ? F<E, V, true, true>::go(L, stream) : F<E, V, true, false>::go(L, stream);
+  return L.lerp ? F<E, V, false, true>::go(L, stream) : F<E, V, false, false>::go(L, stream);
+}
+
+// Channels per lane: a wave's row is 256 bytes in fp32 and, in pairs, in
+// bf16; an odd number of bf16 channels leaves rows unaligned to pairs and
+// takes one channel per lane.
+template <template <typename, int, bool, bool> class F>
+hipError_t dispatch(const ScanLaunch& L, hipStream_t stream) {
+  if (!L.bf16) return by_flags<F, float, 1>(L, stream);
+  return L.C % 2 ? by_flags<F, bf16, 1>(L, stream) : by_flags<F, bf16, 2>(L, stream);
+}
+
 }  // namespace
 
-size_t scan_workspace_bytes(int64_t, int, bool) { return 0; }
+size_t scan_workspace_bytes(int64_t N, int C, bool is_bf16) {
+  const int V = is_bf16 && C % 2 == 0 ? 2 : 1;
+  const size_t f = layout_of(N, C, FWD_CHUNK, V).bytes, b = layout_of(N, C, BWD_CHUNK, V).bytes;
+  return f > b ? f : b;
+}
 hipError_t launch_scan_forward(const ScanLaunch& L, hipStream_t s) { return dispatch<Forward>(L, s); }
 hipError_t launch_scan_backward(const ScanLaunch& L, hipStream_t s) { return dispatch<Backward>(L, s); }
 hipError_t launch_scan_step(const ScanLaunch& L, hipStream_t s) { return dispatch<Step>(L, s); }

@@ -674,9 +674,9 @@ gdnq_status gdnq_scan_forward(const gdnq_scan_params* p, const int32_t* cu_seqle
     if (gdnq_status st = check_ptrs(sp + 3, 1)) return st;
   }
   if (gdnq_status st = check_optional(sp, N)) return st;
+  if (gdnq_status st = check_workspace(workspace, workspace_bytes, need)) return st;
   if (gdnq_status st = check_disjoint(sp, N, 3)) return st;
   if (gdnq_status st = check_offsets(cu_seqlens, L.B, sp, N, 3)) return st;
-  if (gdnq_status st = check_workspace(workspace, workspace_bytes, need)) return st;
   L.cu_seqlens = cu_seqlens;
   L.x = x; L.gate = gate; L.h0 = h0; L.y = y; L.h_last = h_last; L.carry = carry; L.workspace = workspace;
   clear_stale_hip_error();
@@ -702,9 +702,9 @@ gdnq_status gdnq_scan_backward(const gdnq_scan_params* p, const int32_t* cu_seql
     if (gdnq_status st = check_ptrs(sp + 6, 2)) return st;
   }
   if (gdnq_status st = check_optional(sp, N)) return st;
+  if (gdnq_status st = check_workspace(workspace, workspace_bytes, need)) return st;
   if (gdnq_status st = check_disjoint(sp, N, 6)) return st;
   if (gdnq_status st = check_offsets(cu_seqlens, L.B, sp, N, 6)) return st;
-  if (gdnq_status st = check_workspace(workspace, workspace_bytes, need)) return st;
   L.cu_seqlens = cu_seqlens;
   L.x = x; L.gate = gate; L.h0 = h0; L.carry = const_cast<float*>(carry); L.dy = dy; L.dh_last = dh_last;
   L.dx = dx; L.dgate = dgate; L.dh0 = dh0; L.workspace = workspace;
@@ -792,8 +792,8 @@ gdnq_status gdnq_group_norm_backward(const gdnq_norm_params* p, const void* x, c
     if ((gate == nullptr) != (dgate == nullptr)) return fail(GDNQ_ERR_NULL, "gate and dgate: both or neither");
   }
   if (gdnq_status st = check_optional(sp, N)) return st;
-  if (gdnq_status st = check_disjoint(sp, N, 5)) return st;
   if (gdnq_status st = check_workspace(workspace, workspace_bytes, need)) return st;
+  if (gdnq_status st = check_disjoint(sp, N, 5)) return st;
   if (L.R == 0 && !dweight && !dbias) return ok();
   L.x = x; L.gate = gate; L.weight = weight; L.bias = bias; L.dy = dy; L.dx = dx; L.dgate = dgate;
   L.dweight = dweight; L.dbias = dbias; L.workspace = workspace;
@@ -864,8 +864,8 @@ gdnq_status gdnq_mx_matmul(const gdnq_mx_params* p, const uint8_t* a_codes, cons
                      {"w_codes", w_codes, size_t(L.N) * L.K / 2}, {"w_scales", w_scales, size_t(L.N) * L.K / 32},
                      {"y", y, size_t(L.M) * L.N * esize(p->out_dtype)}, {"workspace", workspace, need}};
   if (gdnq_status st = check_ptrs(sp, 5)) return st;
-  if (gdnq_status st = check_disjoint(sp, 6, 4)) return st;
   if (gdnq_status st = check_workspace(workspace, workspace_bytes, need)) return st;
+  if (gdnq_status st = check_disjoint(sp, 6, 4)) return st;
   L.a_codes = a_codes; L.a_scales = a_scales; L.w_codes = w_codes; L.w_scales = w_scales; L.y = y;
   L.workspace = workspace;
   clear_stale_hip_error();
@@ -883,8 +883,8 @@ gdnq_status gdnq_mx_linear(const gdnq_mx_params* p, const void* x, const uint8_t
                      {"w_codes", w_codes, size_t(L.N) * L.K / 2}, {"w_scales", w_scales, size_t(L.N) * L.K / 32},
                      {"y", y, size_t(L.M) * L.N * esize(p->out_dtype)}, {"workspace", workspace, need}};
   if (gdnq_status st = check_ptrs(sp, 4)) return st;
-  if (gdnq_status st = check_disjoint(sp, 5, 3)) return st;
   if (gdnq_status st = check_workspace(workspace, workspace_bytes, need)) return st;
+  if (gdnq_status st = check_disjoint(sp, 5, 3)) return st;
   uint8_t* codes = static_cast<uint8_t*>(workspace);
   uint8_t* scales = codes + mx_align(size_t(L.M) * L.K / 2);
   L.a_codes = codes; L.a_scales = scales; L.w_codes = w_codes; L.w_scales = w_scales; L.y = y;

@@ -6,8 +6,17 @@
 //   dhat = dn w,  dx = rstd (dhat - [center] mean(dhat) - hat mean(dhat hat))
 //   dw = sum dn hat,  db = sum dn   (over tokens; over groups too when shared)
 //
-// One wave per (token, group), its values read again from memory in every
-// pass: the plain form.
+// Bound by memory: every array is read or written once.  A group (one head of
+// one token) is held in the registers of a team of TEAM lanes, EIGHTS times
+// eight values each, so the statistics, the second sum of the backward pass
+// and the outputs need no second read.  The variance is the mean of the
+// centred squares, in fp32.
+//   TEAM: the fewest lanes (8 .. 64) that hold the group with eight values
+//   each; above 512 values a workgroup (TEAM = BLOCK) of as many waves as that
+//   takes, above 8192 with sixteen values a lane.
+//   Values per lane are eight adjacent ones (16 bytes of bf16) when the width
+//   is a multiple of 8; else lane l holds every TEAM-th from l on, which keeps
+//   a wave's accesses adjacent whatever the alignment.
 #include <hip/hip_runtime.h>
 
 #include "../../include/gdnq.h"
@@ -17,6 +26,16 @@
 
 namespace gdnq {
 namespace {
+
+constexpr int THREADS = 256;  // of a workgroup with several teams
+constexpr int BLOCK = 0;       // the team is the workgroup
+
+template <int TEAM>
+constexpr int bounds() { return TEAM == BLOCK ? 1024 : THREADS; }
+template <int TEAM>
+constexpr int teams_of() { return TEAM == BLOCK ? 1 : THREADS / (TEAM == BLOCK ? 1 : TEAM); }
+template <int TEAM>
+__device__ __forceinline__ int team_size() { return TEAM == BLOCK ? int(blockDim.x) : TEAM; }
 
 // f(z) and f'(z)
 __device__ __forceinline__ void activation(int act, float z, float& f, float& df) {
@@ -31,122 +50,320 @@ __device__ __forceinline__ void activation(int act, float z, float& f, float& df
   df = act == GDNQ_ACT_SILU ? p * fmaf(z, q, 1.0f) : p * q;
 }
 
-template <typename E>
-__device__ __forceinline__ void statistics(const NormLaunch& L, const E* x, float& mu, float& rstd) {
-  mu = 0.0f;
-  if (L.center) {
-    float s = 0.0f;
-    for (int i = threadIdx.x; i < L.D; i += 64) s += to_f32(x[i]);
-    mu = group_sum<64>(s) / L.D;
-  }
-  float s = 0.0f;
-  for (int i = threadIdx.x; i < L.D; i += 64) {
-    const float d = to_f32(x[i]) - mu;
-    s = fmaf(d, d, s);
-  }
-  rstd = 1.0f / sqrtf(group_sum<64>(s) / L.D + L.eps);
-}
-
-template <typename E>
-__global__ __launch_bounds__(64) void norm_forward_kernel(NormLaunch L) {
-  const int64_t u = blockIdx.x;
-  const int g = L.shared ? 0 : int(u % L.G);
-  const E* x = static_cast<const E*>(L.x) + u * L.D;
-  const E* gate = L.gate ? static_cast<const E*>(L.gate) + u * L.D : nullptr;
-  E* y = static_cast<E*>(L.y) + u * L.D;
-  float mu, rstd;
-  statistics(L, x, mu, rstd);
-  for (int i = threadIdx.x; i < L.D; i += 64) {
-    const float w = L.weight ? L.weight[int64_t(g) * L.D + i] : 1.0f, b = L.bias ? L.bias[int64_t(g) * L.D + i] : 0.0f;
-    const float n = fmaf((to_f32(x[i]) - mu) * rstd, w, b);
-    float f, df;
-    activation(L.act, gate ? to_f32(gate[i]) : n, f, df);
-    store_f32(y + i, gate ? n * f : f);
+// Sum over a team: inside a wave, or over the workgroup's waves through LDS
+// (box: a place of its own for every sum of a group, so that the barrier of
+// the next one orders its use).
+template <int TEAM>
+__device__ __forceinline__ float team_sum(float x, float* box) {
+  if constexpr (TEAM != BLOCK) {
+    return group_sum<TEAM>(x);
+  } else {
+    x = group_sum<64>(x);
+    if ((threadIdx.x & 63) == 0) box[threadIdx.x >> 6] = x;
+    __syncthreads();
+    const int waves = blockDim.x >> 6, lane = threadIdx.x & 15;
+    return group_sum<16>(lane < waves ? box[lane] : 0.0f);
   }
 }
 
-template <typename E>
-__global__ __launch_bounds__(64) void norm_backward_kernel(NormLaunch L) {
-  const int64_t u = blockIdx.x;
-  const int g = L.shared ? 0 : int(u % L.G);
-  const E* x = static_cast<const E*>(L.x) + u * L.D;
-  const E* dy = static_cast<const E*>(L.dy) + u * L.D;
-  const E* gate = L.gate ? static_cast<const E*>(L.gate) + u * L.D : nullptr;
-  float mu, rstd;
-  statistics(L, x, mu, rstd);
-  if (threadIdx.x == 0) {
-    static_cast<float*>(L.workspace)[2 * u] = mu;
-    static_cast<float*>(L.workspace)[2 * u + 1] = rstd;
-  }
-  float s0 = 0.0f, s1 = 0.0f;
-  for (int pass = 0; pass < 2; ++pass) {
-    for (int i = threadIdx.x; i < L.D; i += 64) {
-      const float w = L.weight ? L.weight[int64_t(g) * L.D + i] : 1.0f, b = L.bias ? L.bias[int64_t(g) * L.D + i] : 0.0f;
-      const float hat = (to_f32(x[i]) - mu) * rstd, n = fmaf(hat, w, b), d = to_f32(dy[i]);
-      float f, df;
-      activation(L.act, gate ? to_f32(gate[i]) : n, f, df);
-      const float dhat = d * (gate ? f : df) * w;
-      if (pass == 0) {
-        s0 += dhat;
-        s1 = fmaf(dhat, hat, s1);
+// Where value j of eighth e of lane l sits in its group.
+template <int TEAM, bool WIDE>
+__device__ __forceinline__ int place(int l, int e, int j) {
+  return WIDE ? (e * team_size<TEAM>() + l) * 8 + j : (e * 8 + j) * team_size<TEAM>() + l;
+}
+
+template <typename E, int TEAM, bool WIDE>
+struct Eight {
+  // as they are in memory; outside the group 0
+  E v[8];
+  __device__ __forceinline__ void load(const E* p, int l, int e, int D) {
+    if constexpr (WIDE) {
+      const int at = place<TEAM, WIDE>(l, e, 0);
+      if (at < D) {
+        __builtin_memcpy(v, __builtin_assume_aligned(p + at, 16), sizeof(v));
       } else {
-        if (gate) store_f32(static_cast<E*>(L.dgate) + u * L.D + i, d * n * df);
-        store_f32(static_cast<E*>(L.dx) + u * L.D + i, rstd * (dhat - s0 - hat * s1));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = E(0.0f);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int at = place<TEAM, WIDE>(l, e, j);
+        v[j] = at < D ? p[at] : E(0.0f);
       }
     }
-    if (pass == 0) {
-      s0 = L.center ? group_sum<64>(s0) / L.D : 0.0f;
-      s1 = group_sum<64>(s1) / L.D;
+  }
+  __device__ __forceinline__ void store(E* p, int l, int e, int D) const {
+    if constexpr (WIDE) {
+      const int at = place<TEAM, WIDE>(l, e, 0);
+      if (at < D) __builtin_memcpy(__builtin_assume_aligned(p + at, 16), v, sizeof(v));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int at = place<TEAM, WIDE>(l, e, j);
+        if (at < D) p[at] = v[j];
+      }
     }
   }
+};
+
+template <int TEAM, bool WIDE, int EIGHTS>
+__device__ __forceinline__ void load_params(const float* p, float other, int l, int D, float (&v)[EIGHTS][8]) {
+#pragma unroll
+  for (int e = 0; e < EIGHTS; ++e)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int at = place<TEAM, WIDE>(l, e, j);
+      v[e][j] = p && at < D ? p[at] : other;
+    }
 }
 
-// One thread per channel of the weights, over all its tokens (and groups).
-template <typename E>
-__global__ __launch_bounds__(64) void norm_params_kernel(NormLaunch L) {
-  const int64_t c = blockIdx.x * int64_t(64) + threadIdx.x, channels = int64_t(L.shared ? 1 : L.G) * L.D;
-  if (c >= channels) return;
-  const int i = int(c % L.D);
-  const float w = L.weight ? L.weight[c] : 1.0f, b = L.bias ? L.bias[c] : 0.0f;
-  const float* stat = static_cast<const float*>(L.workspace);
-  float sw = 0.0f, sb = 0.0f;
-  const int64_t units = int64_t(L.R) * L.G;
-  for (int64_t u = L.shared ? 0 : c / L.D; u < units; u += L.shared ? 1 : L.G) {
-    const float hat = (to_f32(static_cast<const E*>(L.x)[u * L.D + i]) - stat[2 * u]) * stat[2 * u + 1];
-    float f, df;
-    activation(L.act, L.gate ? to_f32(static_cast<const E*>(L.gate)[u * L.D + i]) : fmaf(hat, w, b), f, df);
-    const float dn = to_f32(static_cast<const E*>(L.dy)[u * L.D + i]) * (L.gate ? f : df);
-    sw = fmaf(dn, hat, sw);
-    sb += dn;
+// mu and rstd of the group in v; afterwards v holds x - mu (0 outside).
+template <int TEAM, bool WIDE, int EIGHTS>
+__device__ __forceinline__ float normalise(const NormLaunch& L, float (&v)[EIGHTS][8], int l, float (*box)[16]) {
+  const float inv = 1.0f / L.D;
+  if (L.center) {
+    float s = 0.0f;
+#pragma unroll
+    for (int e = 0; e < EIGHTS; ++e)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s += v[e][j];
+    const float mu = team_sum<TEAM>(s, box[0]) * inv;
+#pragma unroll
+    for (int e = 0; e < EIGHTS; ++e)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[e][j] = place<TEAM, WIDE>(l, e, j) < L.D ? v[e][j] - mu : 0.0f;
   }
-  if (L.dweight) L.dweight[c] = sw;
-  if (L.dbias) L.dbias[c] = sb;
+  float s = 0.0f;
+#pragma unroll
+  for (int e = 0; e < EIGHTS; ++e)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s = fmaf(v[e][j], v[e][j], s);
+  return 1.0f / sqrtf(fmaf(team_sum<TEAM>(s, box[1]), inv, L.eps));
 }
 
-template <typename E>
-hipError_t forward(const NormLaunch& L, hipStream_t stream) {
-  norm_forward_kernel<E><<<uint32_t(int64_t(L.R) * L.G), 64, 0, stream>>>(L);
-  return hipGetLastError();
+template <typename E, int TEAM, bool WIDE, int EIGHTS>
+__global__ __launch_bounds__(bounds<TEAM>()) void norm_forward_kernel(NormLaunch L, int64_t units) {
+  __shared__ float box[2][16];
+  const int l = TEAM == BLOCK ? threadIdx.x : threadIdx.x % team_size<TEAM>();
+  const int64_t u = blockIdx.x * int64_t(teams_of<TEAM>()) + threadIdx.x / team_size<TEAM>();
+  if (u >= units) return;  // whole teams
+  const int64_t at = u * L.D;
+  Eight<E, TEAM, WIDE> x[EIGHTS], g[EIGHTS];
+#pragma unroll
+  for (int e = 0; e < EIGHTS; ++e) x[e].load(static_cast<const E*>(L.x) + at, l, e, L.D);
+  if (L.gate) {
+#pragma unroll
+    for (int e = 0; e < EIGHTS; ++e) g[e].load(static_cast<const E*>(L.gate) + at, l, e, L.D);
+  }
+  const int64_t wat = L.shared ? 0 : u % L.G * L.D;
+  float w[EIGHTS][8], b[EIGHTS][8], v[EIGHTS][8];
+  load_params<TEAM, WIDE>(L.weight ? L.weight + wat : nullptr, 1.0f, l, L.D, w);
+  load_params<TEAM, WIDE>(L.bias ? L.bias + wat : nullptr, 0.0f, l, L.D, b);
+#pragma unroll
+  for (int e = 0; e < EIGHTS; ++e)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[e][j] = to_f32(x[e].v[j]);
+  const float rstd = normalise<TEAM, WIDE>(L, v, l, box);
+#pragma unroll
+  for (int e = 0; e < EIGHTS; ++e) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float n = fmaf(v[e][j] * rstd, w[e][j], b[e][j]);
+      float f, df;
+      activation(L.act, L.gate ? to_f32(g[e].v[j]) : n, f, df);
+      x[e].v[j] = E(L.gate ? n * f : f);
+    }
+    x[e].store(static_cast<E*>(L.y) + at, l, e, L.D);
+  }
 }
 
-template <typename E>
-hipError_t backward(const NormLaunch& L, hipStream_t stream) {
-  if (L.R > 0) norm_backward_kernel<E><<<uint32_t(int64_t(L.R) * L.G), 64, 0, stream>>>(L);
-  if (L.dweight || L.dbias)
-    norm_params_kernel<E><<<uint32_t((int64_t(L.shared ? 1 : L.G) * L.D + 63) / 64), 64, 0, stream>>>(L);
-  return hipGetLastError();
+// A team takes every slots-th group from its own number on; unless all groups
+// share the weights, slots is a multiple of the number of groups, so a team's
+// groups have the same weights and it adds their gradients up in registers.
+// Row `slot` of the partial sums is the team's; the workgroup's teams are
+// added in LDS first when all groups share the weights.
+template <typename E, int TEAM, bool WIDE, int EIGHTS>
+__global__ __launch_bounds__(bounds<TEAM>()) void norm_backward_kernel(NormLaunch L, int64_t units, int64_t slots, float* partial) {
+  constexpr int TEAMS = teams_of<TEAM>();
+  __shared__ float box[4][16];
+  const int l = TEAM == BLOCK ? threadIdx.x : threadIdx.x % team_size<TEAM>(), D = L.D;
+  const int64_t slot = blockIdx.x * int64_t(TEAMS) + threadIdx.x / team_size<TEAM>();
+  const int64_t wat = L.shared ? 0 : slot % L.G * D;
+  float w[EIGHTS][8], b[EIGHTS][8], dw[EIGHTS][8] = {}, db[EIGHTS][8] = {};
+  load_params<TEAM, WIDE>(L.weight ? L.weight + wat : nullptr, 1.0f, l, D, w);
+  load_params<TEAM, WIDE>(L.bias ? L.bias + wat : nullptr, 0.0f, l, D, b);
+  for (int64_t u = slot < slots ? slot : units; u < units; u += slots) {
+    const int64_t at = u * D;
+    Eight<E, TEAM, WIDE> x[EIGHTS], g[EIGHTS], dy[EIGHTS];
+#pragma unroll
+    for (int e = 0; e < EIGHTS; ++e) x[e].load(static_cast<const E*>(L.x) + at, l, e, D);
+    if (L.gate) {
+#pragma unroll
+      for (int e = 0; e < EIGHTS; ++e) g[e].load(static_cast<const E*>(L.gate) + at, l, e, D);
+    }
+#pragma unroll
+    for (int e = 0; e < EIGHTS; ++e) dy[e].load(static_cast<const E*>(L.dy) + at, l, e, D);
+    float v[EIGHTS][8], d[EIGHTS][8];
+#pragma unroll
+    for (int e = 0; e < EIGHTS; ++e)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[e][j] = to_f32(x[e].v[j]);
+    const float rstd = normalise<TEAM, WIDE>(L, v, l, box);
+    float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+    for (int e = 0; e < EIGHTS; ++e) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float hat = v[e][j] * rstd, n = fmaf(hat, w[e][j], b[e][j]), y = to_f32(dy[e].v[j]);  // outside the group dy = 0
+        float f, df;
+        activation(L.act, L.gate ? to_f32(g[e].v[j]) : n, f, df);
+        const float dn = y * (L.gate ? f : df);
+        if (L.gate) g[e].v[j] = E(y * n * df);
+        dw[e][j] = fmaf(dn, hat, dw[e][j]);
+        db[e][j] += dn;
+        d[e][j] = dn * w[e][j];
+        v[e][j] = hat;
+        s0 += d[e][j];
+        s1 = fmaf(d[e][j], hat, s1);
+      }
+      if (L.gate) g[e].store(static_cast<E*>(L.dgate) + at, l, e, D);
+    }
+    const float inv = 1.0f / D;
+    s0 = L.center ? team_sum<TEAM>(s0, box[2]) * inv : 0.0f;
+    s1 = team_sum<TEAM>(s1, box[3]) * inv;
+#pragma unroll
+    for (int e = 0; e < EIGHTS; ++e) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[e].v[j] = E(rstd * fmaf(-v[e][j], s1, d[e][j] - s0));
+      x[e].store(static_cast<E*>(L.dx) + at, l, e, D);
+    }
+  }
+  if (!partial) return;
+  // [2][rows][D]: dw, then db
+  if constexpr (TEAMS > 1) {
+    if (L.shared) {
+      __shared__ float sums[2][TEAMS][TEAM * 8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        sums[0][threadIdx.x / TEAM][l * 8 + j] = dw[0][j];
+        sums[1][threadIdx.x / TEAM][l * 8 + j] = db[0][j];
+      }
+      __syncthreads();
+      for (int i = threadIdx.x; i < 2 * TEAM * 8; i += THREADS) {
+        const int which = i / (TEAM * 8), k = i % (TEAM * 8), c = place<TEAM, WIDE>(k / 8, 0, k % 8);
+        float s = 0.0f;
+        for (int t = 0; t < TEAMS; ++t) s += sums[which][t][k];
+        if (c < D) partial[(int64_t(which) * gridDim.x + blockIdx.x) * D + c] = s;
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < EIGHTS; ++e)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = place<TEAM, WIDE>(l, e, j);
+      if (c < D && slot < slots) {
+        partial[slot * D + c] = dw[e][j];
+        partial[(slots + slot) * D + c] = db[e][j];
+      }
+    }
+}
+
+// out[c] = sum over rows of partial[row][c]: a workgroup takes 16 adjacent
+// columns, 64 rows at a time.
+__global__ __launch_bounds__(1024) void norm_params_kernel(const float* __restrict__ partial, int64_t rows, int64_t cols,
+                                                           float* dweight, float* dbias) {
+  __shared__ float part[64][17];
+  float* out = blockIdx.y ? dbias : dweight;
+  if (!out) return;
+  partial += int64_t(blockIdx.y) * rows * cols;
+  const int i = threadIdx.x & 15, r = threadIdx.x >> 4;
+  const int64_t c = blockIdx.x * int64_t(16) + i;
+  float s = 0.0f;
+  if (c < cols)
+    for (int64_t row = r; row < rows; row += 64) s += partial[row * cols + c];
+  part[r][i] = s;
+  __syncthreads();
+  for (int n = 32; n > 0; n >>= 1) {
+    if (r < n) part[r][i] += part[r + n][i];
+    __syncthreads();
+  }
+  if (r == 0 && c < cols) out[c] = part[0][i];
+}
+
+// The team's lanes (BLOCK: threads of the workgroup).
+int team_of(int D) { return D <= 64 ? 8 : D <= 128 ? 16 : D <= 256 ? 32 : D <= 512 ? 64 : BLOCK; }
+int threads_of(int D) { return D <= 512 ? THREADS : D <= 8192 ? (D + 511) / 512 * 64 : (D + 1023) / 1024 * 64; }
+int teams_in(int D) { return team_of(D) == BLOCK ? 1 : THREADS / team_of(D); }
+
+// Teams of the backward pass: those of at most MOST workgroups (a few per
+// CU), rounded up to a multiple of the groups so that a team's groups share
+// their weights (G_of: the groups, 1 for shared weights).
+constexpr int64_t MOST = 1024;
+
+int64_t slots_of(int64_t units, int G_of, int D) {
+  const int64_t most = MOST * teams_in(D), want = units < most ? units : most;
+  return (want + G_of - 1) / G_of * G_of;
+}
+
+template <typename E, int TEAM, bool WIDE, int EIGHTS>
+struct Forward {
+  static hipError_t go(const NormLaunch& L, hipStream_t stream) {
+    const int64_t units = int64_t(L.R) * L.G;
+    constexpr int TEAMS = teams_of<TEAM>();
+    norm_forward_kernel<E, TEAM, WIDE, EIGHTS><<<uint32_t((units + TEAMS - 1) / TEAMS), threads_of(L.D), 0, stream>>>(L, units);
+    return hipGetLastError();
+  }
+};
+
+template <typename E, int TEAM, bool WIDE, int EIGHTS>
+struct Backward {
+  static hipError_t go(const NormLaunch& L, hipStream_t stream) {
+    constexpr int TEAMS = teams_of<TEAM>();
+    const int64_t units = int64_t(L.R) * L.G, slots = slots_of(units, L.shared ? 1 : L.G, L.D);
+    const int64_t grid = (slots + TEAMS - 1) / TEAMS;
+    const bool params = L.dweight || L.dbias;
+    float* partial = params ? static_cast<float*>(L.workspace) : nullptr;
+    if (units > 0) {
+      norm_backward_kernel<E, TEAM, WIDE, EIGHTS><<<uint32_t(grid), threads_of(L.D), 0, stream>>>(L, units, slots, partial);
+      if (hipError_t e = hipGetLastError()) return e;
+    }
+    if (!params) return hipSuccess;
+    // rows of D: one per workgroup with shared weights, else one per team,
+    // whose groups repeat every G rows: [teams / G][G D]
+    const int64_t rows = units == 0 ? 0 : L.shared ? grid : slots / L.G, cols = int64_t(L.shared ? 1 : L.G) * L.D;
+    norm_params_kernel<<<dim3(uint32_t((cols + 15) / 16), 2), 1024, 0, stream>>>(partial, rows, cols, L.dweight, L.dbias);
+    return hipGetLastError();
+  }
+};
+
+template <template <typename, int, bool, int> class F, typename E, bool WIDE>
+hipError_t by_width(const NormLaunch& L, hipStream_t s) {
+  switch (team_of(L.D)) {
+    case 8: return F<E, 8, WIDE, 1>::go(L, s);
+    case 16: return F<E, 16, WIDE, 1>::go(L, s);
+    case 32: return F<E, 32, WIDE, 1>::go(L, s);
+    case 64: return F<E, 64, WIDE, 1>::go(L, s);
+    default: return L.D <= 8192 ? F<E, BLOCK, WIDE, 1>::go(L, s) : F<E, BLOCK, WIDE, 2>::go(L, s);
+  }
+}
+
+template <template <typename, int, bool, int> class F>
+hipError_t dispatch(const NormLaunch& L, hipStream_t s) {
+  const bool wide = L.D % 8 == 0;
+  if (L.bf16) return wide ? by_width<F, bf16, true>(L, s) : by_width<F, bf16, false>(L, s);
+  return wide ? by_width<F, float, true>(L, s) : by_width<F, float, false>(L, s);
 }
 
 }  // namespace
 
-size_t norm_workspace_bytes(int R, int G, int) { return size_t(R) * G * 8; }
-
-hipError_t launch_norm_forward(const NormLaunch& L, hipStream_t stream) {
-  return L.bf16 ? forward<bf16>(L, stream) : forward<float>(L, stream);
+size_t norm_workspace_bytes(int R, int G, int D) {
+  return size_t(slots_of(int64_t(R) * G, G, D)) * D * 2 * 4;
 }
 
-hipError_t launch_norm_backward(const NormLaunch& L, hipStream_t stream) {
-  return L.bf16 ? backward<bf16>(L, stream) : backward<float>(L, stream);
-}
+hipError_t launch_norm_forward(const NormLaunch& L, hipStream_t stream) { return dispatch<Forward>(L, stream); }
+hipError_t launch_norm_backward(const NormLaunch& L, hipStream_t stream) { return dispatch<Backward>(L, stream); }
 
 }  // namespace gdnq

@@ -109,13 +109,20 @@ struct Eight {
 
 template <int TEAM, bool WIDE, int EIGHTS>
 __device__ __forceinline__ void load_params(const float* p, float other, int l, int D, float (&v)[EIGHTS][8]) {
+  if (!p) {
 #pragma unroll
-  for (int e = 0; e < EIGHTS; ++e)
+    for (int e = 0; e < EIGHTS; ++e)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int at = place<TEAM, WIDE>(l, e, j);
-      v[e][j] = p && at < D ? p[at] : other;
-    }
+      for (int j = 0; j < 8; ++j) v[e][j] = other;
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < EIGHTS; ++e) {
+    Eight<float, TEAM, WIDE> r;
+    r.load(p, l, e, D);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[e][j] = r.v[j];
+  }
 }
 
 // mu and rstd of the group in v; afterwards v holds x - mu (0 outside).
@@ -142,47 +149,66 @@ __device__ __forceinline__ float normalise(const NormLaunch& L, float (&v)[EIGHT
   return 1.0f / sqrtf(fmaf(team_sum<TEAM>(s, box[1]), inv, L.eps));
 }
 
+// A team takes every slots-th group from its own number on; unless all groups
+// share the weights, slots is a multiple of the number of groups, so a team's
+// groups have the same weights, read once.  The next group's values are
+// loaded while the current one is worked on.
 template <typename E, int TEAM, bool WIDE, int EIGHTS>
-__global__ __launch_bounds__(bounds<TEAM>()) void norm_forward_kernel(NormLaunch L, int64_t units) {
-  __shared__ float box[2][16];
-  const int l = TEAM == BLOCK ? threadIdx.x : threadIdx.x % team_size<TEAM>();
-  const int64_t u = blockIdx.x * int64_t(teams_of<TEAM>()) + threadIdx.x / team_size<TEAM>();
-  if (u >= units) return;  // whole teams
-  const int64_t at = u * L.D;
-  Eight<E, TEAM, WIDE> x[EIGHTS], g[EIGHTS];
+__global__ __launch_bounds__(bounds<TEAM>()) void norm_forward_kernel(NormLaunch L, int64_t units, int64_t slots) {
+  __shared__ float box[4][16];
+  int turn = 0;  // without the mean a group has one barrier: its sum's place alternates
+  const int l = TEAM == BLOCK ? threadIdx.x : threadIdx.x % team_size<TEAM>(), D = L.D;
+  const int64_t slot = blockIdx.x * int64_t(teams_of<TEAM>()) + threadIdx.x / team_size<TEAM>();
+  if (slot >= slots) return;  // whole teams
+  const E* xs = static_cast<const E*>(L.x);
+  const E* gates = static_cast<const E*>(L.gate);
+  Eight<E, TEAM, WIDE> x[EIGHTS], g[EIGHTS], xn[EIGHTS], gn[EIGHTS];
 #pragma unroll
-  for (int e = 0; e < EIGHTS; ++e) x[e].load(static_cast<const E*>(L.x) + at, l, e, L.D);
-  if (L.gate) {
+  for (int e = 0; e < EIGHTS; ++e) xn[e].load(xs + slot * D, l, e, D);
+  if (gates) {
 #pragma unroll
-    for (int e = 0; e < EIGHTS; ++e) g[e].load(static_cast<const E*>(L.gate) + at, l, e, L.D);
+    for (int e = 0; e < EIGHTS; ++e) gn[e].load(gates + slot * D, l, e, D);
   }
-  const int64_t wat = L.shared ? 0 : u % L.G * L.D;
-  float w[EIGHTS][8], b[EIGHTS][8], v[EIGHTS][8];
-  load_params<TEAM, WIDE>(L.weight ? L.weight + wat : nullptr, 1.0f, l, L.D, w);
-  load_params<TEAM, WIDE>(L.bias ? L.bias + wat : nullptr, 0.0f, l, L.D, b);
+  const int64_t wat = L.shared ? 0 : slot % L.G * D;
+  float w[EIGHTS][8], b[EIGHTS][8];
+  load_params<TEAM, WIDE>(L.weight ? L.weight + wat : nullptr, 1.0f, l, D, w);
+  load_params<TEAM, WIDE>(L.bias ? L.bias + wat : nullptr, 0.0f, l, D, b);
+  for (int64_t u = slot; u < units; u += slots, turn ^= 2) {
+    const int64_t next = min(u + slots, units - 1) * D;
+    float v[EIGHTS][8];
 #pragma unroll
-  for (int e = 0; e < EIGHTS; ++e)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[e][j] = to_f32(x[e].v[j]);
-  const float rstd = normalise<TEAM, WIDE>(L, v, l, box);
-#pragma unroll
-  for (int e = 0; e < EIGHTS; ++e) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float n = fmaf(v[e][j] * rstd, w[e][j], b[e][j]);
-      float f, df;
-      activation(L.act, L.gate ? to_f32(g[e].v[j]) : n, f, df);
-      x[e].v[j] = E(L.gate ? n * f : f);
+    for (int e = 0; e < EIGHTS; ++e) {
+      x[e] = xn[e];
+      g[e] = gn[e];
+      xn[e].load(xs + next, l, e, D);
     }
-    x[e].store(static_cast<E*>(L.y) + at, l, e, L.D);
+    if (gates) {
+#pragma unroll
+      for (int e = 0; e < EIGHTS; ++e) gn[e].load(gates + next, l, e, D);
+    }
+#pragma unroll
+    for (int e = 0; e < EIGHTS; ++e)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[e][j] = to_f32(x[e].v[j]);
+    const float rstd = normalise<TEAM, WIDE>(L, v, l, box + turn);
+#pragma unroll
+    for (int e = 0; e < EIGHTS; ++e) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float n = fmaf(v[e][j] * rstd, w[e][j], b[e][j]);
+        float f, df;
+        activation(L.act, gates ? to_f32(g[e].v[j]) : n, f, df);
+        x[e].v[j] = E(gates ? n * f : f);
+      }
+      x[e].store(static_cast<E*>(L.y) + u * D, l, e, D);
+    }
   }
 }
 
-// A team takes every slots-th group from its own number on; unless all groups
-// share the weights, slots is a multiple of the number of groups, so a team's
-// groups have the same weights and it adds their gradients up in registers.
-// Row `slot` of the partial sums is the team's; the workgroup's teams are
-// added in LDS first when all groups share the weights.
+// The teams take their groups as in the forward pass and add the gradients of
+// their weights up in registers.  Row `slot` of the partial sums is the
+// team's; the workgroup's teams are added in LDS first when all groups share
+// the weights.
 template <typename E, int TEAM, bool WIDE, int EIGHTS>
 __global__ __launch_bounds__(bounds<TEAM>()) void norm_backward_kernel(NormLaunch L, int64_t units, int64_t slots, float* partial) {
   constexpr int TEAMS = teams_of<TEAM>();
@@ -298,22 +324,25 @@ int team_of(int D) { return D <= 64 ? 8 : D <= 128 ? 16 : D <= 256 ? 32 : D <= 5
 int threads_of(int D) { return D <= 512 ? THREADS : D <= 8192 ? (D + 511) / 512 * 64 : (D + 1023) / 1024 * 64; }
 int teams_in(int D) { return team_of(D) == BLOCK ? 1 : THREADS / team_of(D); }
 
-// Teams of the backward pass: those of at most MOST workgroups (a few per
-// CU), rounded up to a multiple of the groups so that a team's groups share
-// their weights (G_of: the groups, 1 for shared weights).
-constexpr int64_t MOST = 1024;
+// Teams of a call: those of as many workgroups as the chip's 256 CUs hold at
+// once, which then take the same number of groups each, rounded up to a
+// multiple of G (the groups of a token, 1 for shared weights) so that a team's
+// groups share their weights.  Waves a CU holds by the kernels' registers: 32
+// of the forward, 16 of the backward pass.
+constexpr int FORWARD_WAVES = 32, BACKWARD_WAVES = 16;
 
-int64_t slots_of(int64_t units, int G_of, int D) {
-  const int64_t most = MOST * teams_in(D), want = units < most ? units : most;
-  return (want + G_of - 1) / G_of * G_of;
+int64_t slots_of(int64_t units, int G, int D, int waves) {
+  const int64_t groups = 256 * (waves / (threads_of(D) / 64) > 1 ? waves / (threads_of(D) / 64) : 1);
+  const int64_t most = groups * teams_in(D), want = units < most ? units : most;
+  return (want + G - 1) / G * G;
 }
 
 template <typename E, int TEAM, bool WIDE, int EIGHTS>
 struct Forward {
   static hipError_t go(const NormLaunch& L, hipStream_t stream) {
-    const int64_t units = int64_t(L.R) * L.G;
     constexpr int TEAMS = teams_of<TEAM>();
-    norm_forward_kernel<E, TEAM, WIDE, EIGHTS><<<uint32_t((units + TEAMS - 1) / TEAMS), threads_of(L.D), 0, stream>>>(L, units);
+    const int64_t units = int64_t(L.R) * L.G, slots = slots_of(units, L.shared ? 1 : L.G, L.D, FORWARD_WAVES);
+    norm_forward_kernel<E, TEAM, WIDE, EIGHTS><<<uint32_t((slots + TEAMS - 1) / TEAMS), threads_of(L.D), 0, stream>>>(L, units, slots);
     return hipGetLastError();
   }
 };
@@ -322,7 +351,7 @@ template <typename E, int TEAM, bool WIDE, int EIGHTS>
 struct Backward {
   static hipError_t go(const NormLaunch& L, hipStream_t stream) {
     constexpr int TEAMS = teams_of<TEAM>();
-    const int64_t units = int64_t(L.R) * L.G, slots = slots_of(units, L.shared ? 1 : L.G, L.D);
+    const int64_t units = int64_t(L.R) * L.G, slots = slots_of(units, L.shared ? 1 : L.G, L.D, BACKWARD_WAVES);
     const int64_t grid = (slots + TEAMS - 1) / TEAMS;
     const bool params = L.dweight || L.dbias;
     float* partial = params ? static_cast<float*>(L.workspace) : nullptr;
@@ -360,7 +389,7 @@ hipError_t dispatch(const NormLaunch& L, hipStream_t s) {
 }  // namespace
 
 size_t norm_workspace_bytes(int R, int G, int D) {
-  return size_t(slots_of(int64_t(R) * G, G, D)) * D * 2 * 4;
+  return size_t(slots_of(int64_t(R) * G, G, D, BACKWARD_WAVES)) * D * 2 * 4;
 }
 
 hipError_t launch_norm_forward(const NormLaunch& L, hipStream_t stream) { return dispatch<Forward>(L, stream); }

@@ -600,8 +600,8 @@ gdnq_status gdnq_group_norm_backward(const gdnq_norm_params* p, const void* x, c
  *     form above, y [rows, cols] out_dtype; products are exact, sums fp32.
  *   gdnq_mx_linear: the same with a = the codes of x [rows, depth] in_dtype,
  *     quantized in the call's workspace.
- *   rows >= 0; cols >= 1; 32 <= depth <= 2^20; rows depth and cols depth up
- *   to 2^40.  in_dtype is not read by
+ *   rows >= 0; cols >= 1; both <= 2^30; 32 <= depth <= 2^20; rows depth and
+ *   cols depth up to 2^40; ceil(rows / 256) ceil(cols / 16) <= 2^31 - 1.  in_dtype is not read by
  *   gdnq_mx_matmul.  flags must be 0.
  *   workspace: gdnq_mx_workspace_size(p) bytes, enough for either call.
  *   Errors: NULL, SHAPE, DTYPE, ALIGN, ALIAS, FLAGS, WORKSPACE, HIP.

@@ -813,7 +813,8 @@ static gdnq_status mx_depth_ok(int64_t rows, int32_t depth) {
 
 static gdnq_status mx_validate(const gdnq_mx_params* p, bool linear, gdnq::MxLaunch& L) {
   if (!p) return fail(GDNQ_ERR_NULL, "params is NULL");
-  if (p->rows < 0 || p->cols < 1) return fail(GDNQ_ERR_SHAPE, "rows = %d, cols = %d", p->rows, p->cols);
+  if (p->rows < 0 || p->cols < 1 || p->rows > (1 << 30) || p->cols > (1 << 30))
+    return fail(GDNQ_ERR_SHAPE, "rows = %d, cols = %d (at most 2^30)", p->rows, p->cols);
   if (gdnq_status st = mx_depth_ok(p->rows, p->depth)) return st;
   if (gdnq_status st = mx_depth_ok(p->cols, p->depth)) return st;
   if ((int64_t(p->rows) + 255) / 256 * ((int64_t(p->cols) + 15) / 16) > 0x7fffffffLL)

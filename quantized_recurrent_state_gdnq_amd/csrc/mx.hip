@@ -64,15 +64,76 @@ __global__ __launch_bounds__(256) void mx_quantize_kernel(const E* __restrict__ 
   if ((i & 3) == 0) scales[i >> 2] = uint8_t(s);
 }
 
-// A wave computes 16 columns x 16 MT rows of y, operands from memory to
-// registers.  The matrix instruction takes 128 values of depth: lane l holds
-// the 32 values (16 bytes) of one block of row l % 16 and that block's scale,
-// for each of the four lane groups l / 16.  Its first operand is W and its
-// second the rows of A, so a lane's four results are four adjacent columns.
-template <int MT, typename E>
-__global__ __launch_bounds__(64) void mx_direct_kernel(MxLaunch L) {
-  const int lane = threadIdx.x, r = lane & 15, q = lane >> 4;
-  const int n0 = blockIdx.x * 16, m0 = blockIdx.y * 16 * MT;
+// The matrix instruction takes 128 values of depth: lane l holds the 32 values
+// (16 bytes) of one block of row l % 16 of its operand, and that block's
+// scale, one block for each lane group q = l / 16.  Which four blocks those
+// are is free as long as both operands agree.  Its first operand is W and its
+// second the rows of A, so a lane's four results are four adjacent columns of
+// row l % 16.  BW, BA: the byte of the scale register that is used.
+template <int BW, int BA>
+__device__ __forceinline__ f32x4 product(const i32x4& w, const i32x4& a, const f32x4& c, int sw, int sa) {
+  const i32x8 w8 = {w[0], w[1], w[2], w[3], 0, 0, 0, 0}, a8 = {a[0], a[1], a[2], a[3], 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w8, a8, c, 4, 4, BW, sw, BA, sa);
+}
+
+// f(integral constant) for 0 .. N - 1: the scale byte must be a constant.
+template <int I>
+struct Int {
+  static constexpr int value = I;
+};
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void each(F&& f) {
+  if constexpr (I < N) {
+    f(Int<I>{});
+    each<N, I + 1>(f);
+  }
+}
+
+// Four results of a lane: columns n .. n + 3 of row m.
+template <typename E>
+__device__ __forceinline__ void store4(E* y, int M, int N, int m, int n, const f32x4& v) {
+  if (m >= M) return;
+  E* p = y + int64_t(m) * N + n;
+  if (N % 4 == 0) {  // rows start on 4 elements: aligned, and in or out together
+    if (n >= N) return;
+    if constexpr (sizeof(E) == 2) {
+      typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+      *reinterpret_cast<bf16x4*>(p) = __builtin_convertvector(v, bf16x4);
+    } else {
+      *reinterpret_cast<f32x4*>(p) = v;
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (n + i < N) store_f32(p + i, v[i]);
+}
+
+// ---------------------------------------------------------------- few rows
+//
+// Bound by the bytes of W.  A workgroup computes 16 columns x 16 MT rows, its
+// waves a run of the depth each, operands straight from memory to registers
+// (nothing is used twice but A, which the caches hold), and the waves' sums
+// are added in LDS in wave order.  A lane takes four adjacent blocks of its
+// row at a time: 64 bytes of codes and one word of scales.
+
+// Scales of blocks b .. b + 3 of a row (beyond its end 0).
+__device__ __forceinline__ int four_scales(const uint8_t* row, int b, int blocks) {
+  uint32_t w = 0;
+  if (b + 4 <= blocks) {
+    __builtin_memcpy(&w, row + b, 4);
+  } else {
+    for (int i = 0; i < 3; ++i)
+      if (b + i < blocks) w |= uint32_t(row[b + i]) << (8 * i);
+  }
+  return int(w);
+}
+
+template <int MT, int WAVES, typename E>
+__global__ __launch_bounds__(WAVES * 64) void mx_rows_kernel(MxLaunch L, int col_tiles) {
+  __shared__ f32x4 sums[WAVES][MT][64];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  const int n0 = blockIdx.x % col_tiles * 16, m0 = blockIdx.x / col_tiles * 16 * MT;
   const int blocks = L.K / 32;
   const int64_t wrow = min(n0 + r, L.N - 1);
   const uint8_t* wc = L.w_codes + wrow * (L.K / 2);
@@ -86,39 +147,211 @@ __global__ __launch_bounds__(64) void mx_direct_kernel(MxLaunch L) {
     as[t] = L.a_scales + arow * blocks;
   }
   f32x4 acc[MT] = {};
-  for (int b0 = 0; b0 < blocks; b0 += 4) {
-    const bool in = b0 + q < blocks;
-    const int b = in ? b0 + q : 0;
-    i32x4 w = *reinterpret_cast<const i32x4*>(wc + int64_t(b) * 16);
-    int sw = ws[b];
-    if (!in) {
-      w = i32x4{0, 0, 0, 0};
-      sw = 127;
+  // runs of whole steps of 16 blocks
+  const int steps = (blocks + 15) / 16;
+  const int first = steps * wave / WAVES, last = steps * (wave + 1) / WAVES;
+  for (int step = first; step < last; ++step) {
+    const int b = step * 16 + q * 4;
+    i32x4 w[4], a[MT][4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      w[s] = i32x4{0, 0, 0, 0};
+      if (b + s < blocks) w[s] = *reinterpret_cast<const i32x4*>(wc + int64_t(b + s) * 16);
     }
-    const i32x8 w8 = {w[0], w[1], w[2], w[3], 0, 0, 0, 0};
+    const int sw = four_scales(ws, b, blocks);
+    int sa[MT];
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
-      i32x4 a = *reinterpret_cast<const i32x4*>(ac[t] + int64_t(b) * 16);
-      int sa = as[t][b];
-      if (!in) {
-        a = i32x4{0, 0, 0, 0};
-        sa = 127;
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        a[t][s] = i32x4{0, 0, 0, 0};
+        if (b + s < blocks) a[t][s] = *reinterpret_cast<const i32x4*>(ac[t] + int64_t(b + s) * 16);
       }
-      const i32x8 a8 = {a[0], a[1], a[2], a[3], 0, 0, 0, 0};
-      acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w8, a8, acc[t], 4, 4, 0, sw, 0, sa);
+      sa[t] = four_scales(as[t], b, blocks);
     }
+    each<4>([&](auto s) {
+#pragma unroll
+      for (int t = 0; t < MT; ++t) acc[t] = product<s.value, s.value>(w[s.value], a[t][s.value], acc[t], sw, sa[t]);
+    });
+  }
+#pragma unroll
+  for (int t = 0; t < MT; ++t) sums[wave][t][lane] = acc[t];
+  __syncthreads();
+  for (int t = wave; t < MT; t += WAVES) {
+    f32x4 s = sums[0][t][lane];
+    for (int w = 1; w < WAVES; ++w) s += sums[w][t][lane];
+    store4<E>(static_cast<E*>(L.y), L.M, L.N, m0 + t * 16 + r, n0 + q * 4, s);
+  }
+}
+
+// ---------------------------------------------------------------- many rows
+//
+// Bound by the matrix units.  A workgroup computes BM x BN of y, its WGM x WGN
+// waves an equal part each, in steps of DEPTH values: the step's rows of both
+// operands (128 bytes each) are loaded straight into LDS, in two buffers, one
+// filled while the other is multiplied.
+//   In LDS the eight 16-byte blocks of a row are permuted by its number, so
+// that the sixteen rows a matrix instruction reads at one block lie in
+// different banks; the loads write LDS in lane order, so the permutation is
+// in the address each lane loads from.
+//   Lane group q takes blocks 2q and 2q + 1 of a step's eight.  Their scales,
+// for rows r and r + 16 of 32, are one word of LDS: [32 rows][r][q][2][2].
+//   Rows beyond the end read the last row (their results are not stored);
+// blocks beyond the depth read zeros.
+constexpr int DEPTH = 256, STEP_BYTES = DEPTH / 2, STEP_BLOCKS = DEPTH / 32;
+
+__device__ const uint8_t zeros[16] __attribute__((aligned(16))) = {};
+
+// What a row's block number is permuted by: the same for rows 16 apart.
+__device__ __forceinline__ int swizzle(int row) { return (row ^ (row >> 3 & 1)) & 7; }
+
+template <int ROWS, int THREADS>
+struct Stage {
+  static constexpr int LOADS = ROWS * STEP_BYTES / (THREADS * 16);  // eight rows, 1 KB, per wave and load
+  const uint8_t* base;  // of the tile's first row
+  uint32_t at[LOADS];   // the lane's block of its rows in a step
+  __device__ __forceinline__ void init(const uint8_t* codes, int row0, int rows, int row_bytes, int wave, int lane) {
+    base = codes + int64_t(row0) * row_bytes;
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+      const int row = (i * (THREADS / 64) + wave) * 8 + (lane >> 3);
+      at[i] = uint32_t(min(row, rows - 1 - row0)) * uint32_t(row_bytes) + (((lane & 7) ^ swizzle(row)) << 4);
+    }
+  }
+  // Loads the step from block k0 on to LDS at `to`.
+  __device__ __forceinline__ void load(uint8_t* to, int k0, int blocks, int wave, int lane) const {
+    const uint8_t* from = base + int64_t(k0) * 16;
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+      const int piece = i * (THREADS / 64) + wave;
+      const uint8_t* p = from + at[i];
+      if (k0 + STEP_BLOCKS > blocks && k0 + ((lane & 7) ^ swizzle(piece * 8 + (lane >> 3))) >= blocks) p = zeros;
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)p,
+                                       (__attribute__((address_space(3))) void*)(to + piece * 1024), 16, 0, 0);
+    }
+  }
+};
+
+// A row's eight scales of a step (beyond the depth 0).
+__device__ __forceinline__ uint64_t eight_scales(const uint8_t* row, int k0, int blocks) {
+  uint64_t w = 0;
+  if (k0 + STEP_BLOCKS <= blocks) {
+    __builtin_memcpy(&w, row + k0, 8);
+  } else {
+    for (int i = 0; i < STEP_BLOCKS - 1; ++i)
+      if (k0 + i < blocks) w |= uint64_t(row[k0 + i]) << (8 * i);
+  }
+  return w;
+}
+
+template <int BM, int BN, int WGM, int WGN, typename E>
+__global__ __launch_bounds__(WGM* WGN * 64) void mx_tile_kernel(MxLaunch L, int row_tiles, int col_tiles) {
+  constexpr int WAVES = WGM * WGN, THREADS = WAVES * 64;
+  constexpr int TM = BM / WGM / 16, TN = BN / WGN / 16;  // 16 x 16 tiles of a wave
+  static_assert(TM % 2 == 0 && TN % 2 == 0 && BM + BN <= THREADS, "pairs of tiles share a scale word; a thread a row's scales");
+  __shared__ __attribute__((aligned(1024))) uint8_t codes[2][(BM + BN) * STEP_BYTES];
+  __shared__ uint32_t scales[2][(BM + BN) * STEP_BLOCKS / 4];
+
+  // Tiles in bands: the workgroups of one XCD (every eighth) take adjacent
+  // ones, down GROUP rows of tiles and then to the right, so that its L2 holds
+  // the operands they share.
+  constexpr int GROUP = 8;
+  const int tiles = row_tiles * col_tiles, b = blockIdx.x;
+  const int per = tiles / 8, extra = tiles % 8, x = b % 8;
+  const int id = x * per + min(x, extra) + b / 8;
+  const int band = id / (GROUP * col_tiles), in_band = id % (GROUP * col_tiles);
+  const int rows_here = min(GROUP, row_tiles - band * GROUP);
+  const int m0 = (band * GROUP + in_band % rows_here) * BM, n0 = in_band / rows_here * BN;
+
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  const int wm = wave % WGM * (BM / WGM), wn = wave / WGM * (BN / WGN);
+  const int blocks = L.K / 32, row_bytes = L.K / 2;
+  Stage<BM, THREADS> sa;
+  Stage<BN, THREADS> sw;
+  sa.init(L.a_codes, m0, L.M, row_bytes, wave, lane);
+  sw.init(L.w_codes, n0, L.N, row_bytes, wave, lane);
+  // thread t stages the scales of row t of A's tile, then of W's
+  const int t = threadIdx.x;
+  const uint8_t* scale_row = t < BM ? L.a_scales + int64_t(min(m0 + t, L.M - 1)) * blocks
+                                    : L.w_scales + int64_t(min(n0 + t - BM, L.N - 1)) * blocks;
+  const bool stages_scales = t < BM + BN;
+  auto put_scales = [&](int buf, uint64_t w) {
+    uint16_t* p = reinterpret_cast<uint16_t*>(scales[buf]) + (t >> 5) * 128 + (t & 15) * 8 + (t >> 4 & 1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i * 2] = uint16_t(w >> (16 * i));
+  };
+
+  f32x4 acc[TN][TM] = {};
+  sa.load(codes[0], 0, blocks, wave, lane);
+  sw.load(codes[0] + BM * STEP_BYTES, 0, blocks, wave, lane);
+  if (stages_scales) put_scales(0, eight_scales(scale_row, 0, blocks));
+  const int steps = (blocks + STEP_BLOCKS - 1) / STEP_BLOCKS;
+  for (int step = 0; step < steps; ++step) {
+    const int buf = step & 1;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's loads into LDS
+    __syncthreads();
+    uint64_t next_scales = 0;
+    const bool more = step + 1 < steps;
+    if (more) {
+      sa.load(codes[buf ^ 1], (step + 1) * STEP_BLOCKS, blocks, wave, lane);
+      sw.load(codes[buf ^ 1] + BM * STEP_BYTES, (step + 1) * STEP_BLOCKS, blocks, wave, lane);
+      if (stages_scales) next_scales = eight_scales(scale_row, (step + 1) * STEP_BLOCKS, blocks);
+    }
+    uint32_t sca[TM / 2], scw[TN / 2];
+#pragma unroll
+    for (int i = 0; i < TM / 2; ++i) sca[i] = scales[buf][(wm / 32 + i) * 64 + r * 4 + q];
+#pragma unroll
+    for (int i = 0; i < TN / 2; ++i) scw[i] = scales[buf][(BM / 32 + wn / 32 + i) * 64 + r * 4 + q];
+    const uint8_t* ca = codes[buf] + wm * STEP_BYTES;
+    const uint8_t* cw = codes[buf] + (BM + wn) * STEP_BYTES;
+    each<2>([&](auto s) {
+      i32x4 a[TM], w[TN];
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+        a[i] = *reinterpret_cast<const i32x4*>(ca + (i * 16 + r) * STEP_BYTES + (((2 * q + s.value) ^ swizzle(r)) << 4));
+#pragma unroll
+      for (int i = 0; i < TN; ++i)
+        w[i] = *reinterpret_cast<const i32x4*>(cw + (i * 16 + r) * STEP_BYTES + (((2 * q + s.value) ^ swizzle(r)) << 4));
+      each<TN>([&](auto j) {
+        each<TM>([&](auto i) {
+          acc[j.value][i.value] = product<(j.value & 1) * 2 + s.value, (i.value & 1) * 2 + s.value>(
+              w[j.value], a[i.value], acc[j.value][i.value], int(scw[j.value / 2]), int(sca[i.value / 2]));
+        });
+      });
+    });
+    if (more && stages_scales) put_scales(buf ^ 1, next_scales);
   }
   E* y = static_cast<E*>(L.y);
 #pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    const int m = m0 + t * 16 + r;
-    if (m >= L.M) continue;
+  for (int i = 0; i < TM; ++i)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int n = n0 + q * 4 + i;
-      if (n < L.N) store_f32(y + int64_t(m) * L.N + n, acc[t][i]);
-    }
-  }
+    for (int j = 0; j < TN; ++j) store4<E>(y, L.M, L.N, m0 + wm + i * 16 + r, n0 + wn + j * 16 + q * 4, acc[j][i]);
+}
+
+template <int MT, int WAVES, typename E>
+hipError_t rows_product(const MxLaunch& L, hipStream_t stream) {
+  const int cols = (L.N + 15) / 16;
+  const int64_t grid = int64_t(cols) * ((L.M + 16 * MT - 1) / (16 * MT));
+  mx_rows_kernel<MT, WAVES, E><<<uint32_t(grid), WAVES * 64, 0, stream>>>(L, cols);
+  return hipGetLastError();
+}
+
+template <int BM, int BN, int WGM, int WGN, typename E>
+hipError_t tile_product(const MxLaunch& L, hipStream_t stream) {
+  const int rows = (L.M + BM - 1) / BM, cols = (L.N + BN - 1) / BN;
+  mx_tile_kernel<BM, BN, WGM, WGN, E><<<uint32_t(rows) * uint32_t(cols), WGM * WGN * 64, 0, stream>>>(L, rows, cols);
+  return hipGetLastError();
+}
+
+template <typename E>
+hipError_t matmul(const MxLaunch& L, hipStream_t stream) {
+  auto tiles = [&](int b) { return int64_t((L.M + b - 1) / b) * ((L.N + b - 1) / b); };
+  if (L.M <= 16) return rows_product<1, 8, E>(L, stream);
+  if (L.M <= 32) return rows_product<2, 8, E>(L, stream);
+  if (L.M <= 64) return rows_product<4, 8, E>(L, stream);
+  if (tiles(256) >= 192) return tile_product<256, 256, 2, 4, E>(L, stream);
+  if (tiles(128) >= 192) return tile_product<128, 128, 2, 2, E>(L, stream);
+  return tile_product<64, 64, 2, 2, E>(L, stream);
 }
 
 }  // namespace
@@ -138,12 +371,7 @@ hipError_t launch_mx_quantize(const void* x, int64_t rows, int K, bool is_bf16, 
 size_t mx_matmul_workspace_bytes(int, int, int) { return 0; }
 
 hipError_t launch_mx_matmul(const MxLaunch& L, hipStream_t stream) {
-  const dim3 grid((L.N + 15) / 16, (L.M + 63) / 64);
-  if (L.out_bf16)
-    mx_direct_kernel<4, bf16><<<grid, 64, 0, stream>>>(L);
-  else
-    mx_direct_kernel<4, float><<<grid, 64, 0, stream>>>(L);
-  return hipGetLastError();
+  return L.out_bf16 ? matmul<bf16>(L, stream) : matmul<float>(L, stream);
 }
 
 }  // namespace gdnq

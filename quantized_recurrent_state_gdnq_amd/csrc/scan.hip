@@ -5,17 +5,18 @@
 // Forward and backward are one pass over the tokens each.  The tokens of the
 // whole call (all sequences, back to back) are cut into chunks, and a
 // workgroup takes one chunk of 64 or 128 channels: lanes hold channels, waves
-// hold runs of RUN tokens, whose inputs stay in registers.
+// hold runs of 8 to 32 tokens, whose inputs stay in registers.
 //   1. Each wave folds its run to the pair (A, H) with h_out = A h_in + H.  A
 //      sequence's first token has A = 0 (its state comes from h0), so runs,
 //      waves and chunks may hold any number of sequence borders.
 //   2. The waves' pairs go through LDS to the chunk's pair, which is published
-//      in the workspace; the state that enters the chunk is folded from the
-//      published pairs of the chunks before it, back to the chunk that holds
-//      its first token's sequence start, or to the last group border: every
-//      GROUP-th chunk publishes its outgoing state too, so a chunk reads at
-//      most GROUP - 1 pairs and one state.  The fold's order is fixed by the
-//      sizes alone.
+//      in the workspace.  Every 16th chunk publishes the pair of its group of 16
+//      chunks as well, every 256th its outgoing state, so the state that enters
+//      a chunk is folded from at most one state, 15 groups and 15 chunks, back
+//      to the chunk that holds its first token's sequence start.  Handing a
+//      state on costs about 3 us; with a state per group instead of two levels
+//      of pairs those hops bounded long sequences.  The fold's order is fixed
+//      by the sizes alone.
 //   3. Every wave walks its run again from the state it now knows and writes.
 // Waiting: chunks are taken by ticket (a counter per channel tile), so the
 // chunk before the one a workgroup waits for is always held by a workgroup
@@ -33,34 +34,35 @@
 namespace gdnq {
 namespace {
 
-constexpr int RUN = 16;  // tokens per wave
-constexpr int FWD_WAVES = 16, BWD_WAVES = GDNQ_SCAN_CHUNK / RUN;
-constexpr int FWD_CHUNK = FWD_WAVES * RUN, BWD_CHUNK = BWD_WAVES * RUN;
-constexpr int GROUP = 16;  // chunks per published state
+// Waves of a workgroup, tokens per wave and waves per SIMD (by the registers)
+// for V channels per lane.  Two channels of bf16 and their gates take two
+// registers and a half per token: half as many waves with twice the tokens
+// measured 119 us for 32768 tokens of 2048 channels against 167 (the shape of
+// one channel, spilling) and 121 (8 waves, 16 tokens); one channel of fp32 377
+// us for 262144 tokens of 640 channels against 413 (8 waves, 32 tokens).
+template <int V>
+struct ForwardShape {
+  static constexpr int WAVES = V == 1 ? 16 : 8, RUN = V == 1 ? 16 : 32, PER_SIMD = V == 1 ? 8 : 4;
+};
+constexpr int FWD_CHUNK = 256;
+// The backward pass holds three values and a state per token.
+constexpr int BWD_WAVES = 16, BWD_RUN = 8, BWD_PER_SIMD = 8, BWD_CHUNK = BWD_WAVES * BWD_RUN;
+constexpr int GROUP = 16;  // chunks per published group, groups per published state
 static_assert(BWD_CHUNK == GDNQ_SCAN_CHUNK && FWD_CHUNK % GDNQ_SCAN_CHUNK == 0, "carry rows are chunk borders");
+
+// Words between the tiles' ticket counters: a cache line of their own each.
+constexpr int TICKET_STRIDE = 64;
 
 constexpr unsigned long long EMPTY = ~0ull;
 
-// The chain of chunks in the workspace: a ticket counter per channel tile,
-// then a pair per chunk and channel, then a state per group and channel.
+// The chain of chunks in the workspace: a ticket counter per channel tile, then
+// per channel a pair per chunk, a pair per group and a state per GROUP groups.
 struct Chain {
   uint32_t* ticket;  // null: the call is one chunk
   unsigned long long* pair;
+  unsigned long long* group;
   unsigned long long* state;
 };
-
-__host__ __device__ inline size_t align256(size_t n) { return (n + 255) / 256 * 256; }
-
-// a = gate or sigmoid(gate), and keep = 1 - a without cancellation.
-template <bool LOGITS>
-__device__ __forceinline__ void gate_of(float g, float& a, float& keep) {
-  if constexpr (LOGITS) {
-    sigmoid_pair(g, a, keep);
-  } else {
-    a = g;
-    keep = 1.0f - g;
-  }
-}
 
 // V channels of one token: in memory, and as the registers that hold them.
 template <typename E, int V>
@@ -82,7 +84,44 @@ struct Cell<E, 1> {
   __device__ static __forceinline__ void store(E* p, const float (&v)[1]) { store_f32(p, v[0]); }
 };
 
-// What a wave needs to know of the RUN tokens from row0 on: bit r of the
+// V gates of one token: a = gate or sigmoid(gate) and keep = 1 - a, from what
+// they were loaded as (load, then settle once).  From logits one value is
+// kept in fp32, the smaller of a and keep with the logit's sign, and the other
+// is one minus it: the exponential and the reciprocal are taken once however
+// many times a token is walked over (they, not the memory, bounded the
+// kernels that took them in every walk).
+template <typename E, int V, bool LOGITS>
+struct Gates;
+template <typename E, int V>
+struct Gates<E, V, false> {
+  Cell<E, V> g;
+  __device__ __forceinline__ void load(const E* p) { g.load(p); }
+  __device__ __forceinline__ void settle() {}
+  __device__ __forceinline__ void forget() {}
+  __device__ __forceinline__ void get(int i, float& a, float& keep) const {
+    a = g.get(i);
+    keep = 1.0f - a;
+  }
+};
+template <typename E, int V>
+struct Gates<E, V, true> {
+  Cell<E, V> g;
+  float t[V];
+  __device__ __forceinline__ void load(const E* p) { g.load(p); }
+  __device__ __forceinline__ void settle() {
+#pragma unroll
+    for (int i = 0; i < V; ++i) t[i] = sigmoid_tail(g.get(i));
+  }
+  __device__ __forceinline__ void get(int i, float& a, float& keep) const { sigmoid_of_tail(t[i], a, keep); }
+  // Between walks: the compiler would keep a and b of every token from the
+  // first one in registers, four values instead of two, and spill them.
+  __device__ __forceinline__ void forget() {
+#pragma unroll
+    for (int i = 0; i < V; ++i) asm volatile("" : "+v"(t[i]));
+  }
+};
+
+// What a wave needs to know of the run of tokens from row0 on: bit r of the
 // masks is token row0 + r; lane r holds its sequence.
 struct Rows {
   uint32_t valid, start, end;
@@ -102,6 +141,7 @@ __device__ __forceinline__ int sequence_at(const int32_t* cu, int B, int row) {
 }
 
 // first: the first token of the sequence that holds row0 (row0 + 1 if none does).
+template <int RUN>
 __device__ __forceinline__ Rows rows_of(const int32_t* __restrict__ cu, int B, int T, int64_t N, int row0, int lane,
                                         int& first) {
   const int row = row0 + lane;
@@ -195,40 +235,79 @@ __device__ __forceinline__ uint32_t waves_with(const uint32_t* borders, int lane
   return uint32_t(__builtin_amdgcn_ballot_w64(lane < WAVES && borders[lane & (WAVES - 1)] != 0));
 }
 
-// The state that enters a chunk, by all waves of its workgroup: place is the
+// What a chunk's fold needs, in LDS.
+template <int V>
+struct Fold {
+  f32x2 pair[GROUP][64 * V], group[GROUP][64 * V];
+  float carry[64 * V];   // the states that enter the chunk
+  f32x2 so_far[64 * V];  // the pair of the group's chunks before this one
+};
+
+// The states that enter a chunk, by all waves of its workgroup: place is the
 // chunk's place in the order of the chain, from the first place whose pair it
-// needs (place itself: none).  Ends with a barrier; carry[] holds the states.
+// needs (place itself: none).  Ends with a barrier.
 template <int V, int WAVES>
 __device__ __forceinline__ void enter_chunk(const Chain& chain, int place, int from, int C, int c, bool active, int wave,
-                                            int lane, f32x2 (*pairs)[64 * V], float* carry) {
-  const int border = place / GROUP * GROUP;
-  const bool base = from < border;  // the group's incoming state, then the group's pairs
-  const int lo = base ? border : from;
+                                            int lane, Fold<V>& f) {
+  const int border = place / GROUP * GROUP, group = place / GROUP, outer = group / GROUP * GROUP;
+  const bool base = from < outer * GROUP;
+  const int lo = max(from, border), glo = from >= border ? group : base ? outer : from / GROUP;
+  // a wave takes one of each: all of its loads are under way together
 #pragma unroll
   for (int k = 0; k < GROUP; k += WAVES) {
-    const int j = lo + k + wave;
-    if (j < place && active) {
-      float a[V], h[V];
-      await<V>(chain.pair + int64_t(j) * C + c, a, h);
-      put<V>(&pairs[k + wave][lane * V], a, h);
+    const bool p = active && lo + k + wave < place, g = active && glo + k + wave < group;
+    float a[V], h[V];
+    if (g) {
+      await<V>(chain.group + int64_t(glo + k + wave) * C + c, a, h);
+      put<V>(&f.group[k + wave][lane * V], a, h);
+    }
+    if (p) {
+      await<V>(chain.pair + int64_t(lo + k + wave) * C + c, a, h);
+      put<V>(&f.pair[k + wave][lane * V], a, h);
     }
   }
-  if (wave == WAVES - 1 && active) {  // (the last wave has a pair to wait for only where GROUP > WAVES)
+  if (wave == WAVES - 1 && active) {  // (never a pair to wait for where WAVES = GROUP)
     float a[V], h[V] = {};
-    if (base) await<V>(chain.state + int64_t(border / GROUP - 1) * C + c, a, h);
+    if (base) await<V>(chain.state + int64_t(outer / GROUP - 1) * C + c, a, h);
 #pragma unroll
-    for (int i = 0; i < V; ++i) carry[lane * V + i] = h[i];
+    for (int i = 0; i < V; ++i) f.carry[lane * V + i] = h[i];
   }
   __syncthreads();
   if (wave == 0 && active) {
-    float a[V] = {}, h[V];
+    float a[V], h[V], ga[V] = {}, gh[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) h[i] = carry[lane * V + i];
-    for (int j = lo; j < place; ++j) then<V>(&pairs[j - lo][lane * V], false, a, h);
+    for (int i = 0; i < V; ++i) {
+      a[i] = 1.0f;
+      h[i] = 0.0f;
+      gh[i] = f.carry[lane * V + i];
+    }
+    for (int j = glo; j < group; ++j) then<V>(&f.group[j - glo][lane * V], false, ga, gh);
+    for (int j = lo; j < place; ++j) then<V>(&f.pair[j - lo][lane * V], false, a, h);
+    put<V>(&f.so_far[lane * V], a, h);
 #pragma unroll
-    for (int i = 0; i < V; ++i) carry[lane * V + i] = h[i];
+    for (int i = 0; i < V; ++i) f.carry[lane * V + i] = fmaf(a[i], gh[i], h[i]);
   }
   __syncthreads();
+}
+
+// After enter_chunk, by one wave: the chunk's own pair (a, h), with or without
+// a border (cut) in it, to its group's pair and outgoing state, where due.
+template <int V>
+__device__ __forceinline__ void leave_chunk(const Chain& chain, int place, int C, int c, int lane, bool cut, const float (&a)[V],
+                                            const float (&h)[V], const Fold<V>& f) {
+  if (place % GROUP != GROUP - 1) return;
+  float ga[V], gh[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const f32x2 p = f.so_far[lane * V + i];
+    ga[i] = a[i] * p.x;
+    gh[i] = fmaf(a[i], cut ? 0.0f : p.y, h[i]);
+  }
+  publish<V>(chain.group + int64_t(place / GROUP) * C + c, ga, gh);
+  if (place % (GROUP * GROUP) != GROUP * GROUP - 1) return;
+#pragma unroll
+  for (int i = 0; i < V; ++i) gh[i] = fmaf(a[i], cut ? 0.0f : f.carry[lane * V + i], h[i]);
+  publish<V>(chain.state + int64_t(place / (GROUP * GROUP)) * C + c, ga, gh);
 }
 
 template <int V>
@@ -243,36 +322,37 @@ __device__ __forceinline__ int take_ticket(uint32_t* ticket) {
   if (threadIdx.x == 0)
     mine = int(__hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
   __syncthreads();
-  return mine;
+  return __builtin_amdgcn_readfirstlane(mine);
 }
 
 template <typename E, int V, bool LOGITS, bool LERP>
-__global__ __launch_bounds__(FWD_WAVES * 64) void scan_forward_kernel(ScanLaunch L, Chain chain, const int32_t* __restrict__ cu,
+__global__ __launch_bounds__(ForwardShape<V>::WAVES * 64, ForwardShape<V>::PER_SIMD) void scan_forward_kernel(ScanLaunch L, Chain chain, const int32_t* __restrict__ cu,
                                                                       const E* __restrict__ xs, const E* __restrict__ gates, int tiles) {
-  constexpr int WAVES = FWD_WAVES, CT = 64 * V;
+  constexpr int WAVES = ForwardShape<V>::WAVES, RUN = ForwardShape<V>::RUN, CT = 64 * V;
+  static_assert(WAVES * RUN == FWD_CHUNK, "a chunk is the workgroup's runs");
   __shared__ f32x2 wave_pair[WAVES][CT];
-  __shared__ f32x2 pairs[GROUP][CT];
-  __shared__ float carry[CT];
+  __shared__ Fold<V> fold;
   __shared__ uint32_t borders[WAVES];
   __shared__ int first_row;
   const int tile = blockIdx.x % tiles;
-  const int chunk = chain.ticket ? take_ticket(chain.ticket + tile) : 0;
+  const int chunk = chain.ticket ? take_ticket(chain.ticket + tile * TICKET_STRIDE) : 0;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int c = tile * CT + lane * V, C = L.C;
   const bool active = c < C;
   const int row0 = chunk * FWD_CHUNK + wave * RUN;
 
-  Cell<E, V> x[RUN], g[RUN];
+  Cell<E, V> x[RUN];
+  Gates<E, V, LOGITS> g[RUN];
 #pragma unroll
   for (int r = 0; r < RUN; ++r) {
     if (active && row0 + r < L.N) {
-      const int64_t at = int64_t(row0 + r) * C + c;
-      x[r].load(xs + at);
-      g[r].load(gates + at);
+      const int64_t at = int64_t(row0 + r) * C;  // the wave's: lanes differ in the channel alone
+      x[r].load(xs + at + c);
+      g[r].load(gates + at + c);
     }
   }
   int first;
-  const Rows rows = rows_of(cu, L.B, L.T, L.N, row0, lane, first);
+  const Rows rows = rows_of<RUN>(cu, L.B, L.T, L.N, row0, lane, first);
   if (threadIdx.x == 0) first_row = first;
 
   float A[V], H[V];
@@ -285,10 +365,11 @@ __global__ __launch_bounds__(FWD_WAVES * 64) void scan_forward_kernel(ScanLaunch
   for (int r = 0; r < RUN; ++r) {
     if (!(rows.valid >> r & 1)) continue;
     float a[V], b[V];
+    g[r].settle();
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       float keep;
-      gate_of<LOGITS>(g[r].get(i), a[i], keep);
+      g[r].get(i, a[i], keep);
       b[i] = LERP ? keep * x[r].get(i) : x[r].get(i);
     }
     if (rows.start >> r & 1) {
@@ -331,15 +412,10 @@ __global__ __launch_bounds__(FWD_WAVES * 64) void scan_forward_kernel(ScanLaunch
     }
     const int start = first_row;
     const int from = start >= chunk * FWD_CHUNK ? chunk : start / FWD_CHUNK;
-    enter_chunk<V, WAVES>(chain, chunk, from, C, c, active, wave, lane, pairs, carry);
+    enter_chunk<V, WAVES>(chain, chunk, from, C, c, active, wave, lane, fold);
 #pragma unroll
-    for (int i = 0; i < V; ++i) in[i] = carry[lane * V + i];
-    if (wave == WAVES - 1 && chunk % GROUP == GROUP - 1 && active) {
-      float out[V];
-#pragma unroll
-      for (int i = 0; i < V; ++i) out[i] = fmaf(A[i], cuts ? 0.0f : in[i], H[i]);
-      publish<V>(chain.state + int64_t(chunk / GROUP) * C + c, in, out);
-    }
+    for (int i = 0; i < V; ++i) in[i] = fold.carry[lane * V + i];
+    if (wave == WAVES - 1 && active) leave_chunk<V>(chain, chunk, C, c, lane, cuts != 0, A, H, fold);
   }
 
   float h[V];
@@ -351,13 +427,15 @@ __global__ __launch_bounds__(FWD_WAVES * 64) void scan_forward_kernel(ScanLaunch
   }
   E* ys = static_cast<E*>(L.y);
 #pragma unroll
+  for (int r = 0; r < RUN; ++r) g[r].forget();
+#pragma unroll
   for (int r = 0; r < RUN; ++r) {
     if (!(rows.valid >> r & 1)) continue;
     float a[V], b[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       float keep;
-      gate_of<LOGITS>(g[r].get(i), a[i], keep);
+      g[r].get(i, a[i], keep);
       b[i] = LERP ? keep * x[r].get(i) : x[r].get(i);
     }
     if (rows.start >> r & 1) {
@@ -384,31 +462,31 @@ __global__ __launch_bounds__(FWD_WAVES * 64) void scan_forward_kernel(ScanLaunch
 // again pairs with m_out = A m_in + H, A = 0 over a sequence border.  The
 // states h_{t-1} are formed again from the chunk's row of carry.
 template <typename E, int V, bool LOGITS, bool LERP>
-__global__ __launch_bounds__(BWD_WAVES * 64) void scan_backward_kernel(ScanLaunch L, Chain chain, const int32_t* __restrict__ cu,
+__global__ __launch_bounds__(BWD_WAVES * 64, BWD_PER_SIMD) void scan_backward_kernel(ScanLaunch L, Chain chain, const int32_t* __restrict__ cu,
                                                                        const E* __restrict__ xs, const E* __restrict__ gates,
                                                                        const E* __restrict__ dys, int tiles, int chunks) {
-  constexpr int WAVES = BWD_WAVES, CT = 64 * V;
+  constexpr int WAVES = BWD_WAVES, RUN = BWD_RUN, CT = 64 * V;
   __shared__ f32x2 wave_pair[WAVES][CT];  // of h, forwards
   __shared__ f32x2 wave_back[WAVES][CT];  // of m, backwards
-  __shared__ f32x2 pairs[GROUP][CT];
-  __shared__ float carry[CT];
+  __shared__ Fold<V> fold;
   __shared__ uint32_t starts[WAVES], borders[WAVES];
   __shared__ int last_row;
   const int tile = blockIdx.x % tiles;
-  const int place = chain.ticket ? take_ticket(chain.ticket + tile) : 0, chunk = chunks - 1 - place;
+  const int place = chain.ticket ? take_ticket(chain.ticket + tile * TICKET_STRIDE) : 0, chunk = chunks - 1 - place;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int c = tile * CT + lane * V, C = L.C;
   const bool active = c < C;
   const int row0 = chunk * BWD_CHUNK + wave * RUN;
 
-  Cell<E, V> x[RUN], g[RUN], dy[RUN];
+  Cell<E, V> x[RUN], dy[RUN];
+  Gates<E, V, LOGITS> g[RUN];
 #pragma unroll
   for (int r = 0; r < RUN; ++r) {
     if (active && row0 + r < L.N) {
-      const int64_t at = int64_t(row0 + r) * C + c;
-      x[r].load(xs + at);
-      g[r].load(gates + at);
-      dy[r].load(dys + at);
+      const int64_t at = int64_t(row0 + r) * C;  // the wave's: lanes differ in the channel alone
+      x[r].load(xs + at + c);
+      g[r].load(gates + at + c);
+      dy[r].load(dys + at + c);
     }
   }
   float h_in[V] = {};
@@ -417,7 +495,7 @@ __global__ __launch_bounds__(BWD_WAVES * 64) void scan_backward_kernel(ScanLaunc
     for (int i = 0; i < V; ++i) h_in[i] = L.carry[int64_t(chunk) * C + c + i];
   }
   int first;
-  const Rows rows = rows_of(cu, L.B, L.T, L.N, row0, lane, first);
+  const Rows rows = rows_of<RUN>(cu, L.B, L.T, L.N, row0, lane, first);
   if (threadIdx.x == WAVES * 64 - 64) {
     // the last token of the sequence that holds the chunk's last token (the
     // chunk's own last where none does, or where it ends there)
@@ -444,10 +522,11 @@ __global__ __launch_bounds__(BWD_WAVES * 64) void scan_backward_kernel(ScanLaunc
   for (int r = 0; r < RUN; ++r) {
     if (!(rows.valid >> r & 1)) continue;
     float a[V], b[V];
+    g[r].settle();
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       float keep;
-      gate_of<LOGITS>(g[r].get(i), a[i], keep);
+      g[r].get(i, a[i], keep);
       b[i] = LERP ? keep * x[r].get(i) : x[r].get(i);
     }
     if (rows.start >> r & 1) {
@@ -480,7 +559,7 @@ __global__ __launch_bounds__(BWD_WAVES * 64) void scan_backward_kernel(ScanLaunc
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       float a, keep;
-      gate_of<LOGITS>(g[r].get(i), a, keep);
+      g[r].get(i, a, keep);
       M[i] = a * (dy[r].get(i) + M[i]);
     }
   }
@@ -521,21 +600,18 @@ __global__ __launch_bounds__(BWD_WAVES * 64) void scan_backward_kernel(ScanLaunc
       if (active) publish<V>(chain.pair + int64_t(place) * C + c, H, M);
     }
     const int from = min(place, max(0, chunks - 1 - last_row / BWD_CHUNK));
-    enter_chunk<V, WAVES>(chain, place, from, C, c, active, wave, lane, pairs, carry);
+    enter_chunk<V, WAVES>(chain, place, from, C, c, active, wave, lane, fold);
 #pragma unroll
-    for (int i = 0; i < V; ++i) in[i] = carry[lane * V + i];
-    if (wave == 0 && place % GROUP == GROUP - 1 && active) {
-      float out[V];
-#pragma unroll
-      for (int i = 0; i < V; ++i) out[i] = fmaf(H[i], cuts ? 0.0f : in[i], M[i]);
-      publish<V>(chain.state + int64_t(place / GROUP) * C + c, in, out);
-    }
+    for (int i = 0; i < V; ++i) in[i] = fold.carry[lane * V + i];
+    if (wave == 0 && active) leave_chunk<V>(chain, place, C, c, lane, cuts != 0, H, M, fold);
   }
   float m[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) m[i] = fmaf(pa[i], cuts >> (wave + 1) ? 0.0f : in[i], pm[i]);
 
   float before[RUN][V];
+#pragma unroll
+  for (int r = 0; r < RUN; ++r) g[r].forget();
 #pragma unroll
   for (int r = 0; r < RUN; ++r) {
     if (!(rows.valid >> r & 1)) continue;
@@ -547,7 +623,7 @@ __global__ __launch_bounds__(BWD_WAVES * 64) void scan_backward_kernel(ScanLaunc
     for (int i = 0; i < V; ++i) {
       before[r][i] = h_in[i];
       float a, keep;
-      gate_of<LOGITS>(g[r].get(i), a, keep);
+      g[r].get(i, a, keep);
       h_in[i] = fmaf(a, h_in[i], LERP ? keep * x[r].get(i) : x[r].get(i));
     }
   }
@@ -564,7 +640,7 @@ __global__ __launch_bounds__(BWD_WAVES * 64) void scan_backward_kernel(ScanLaunc
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       float a, keep;
-      gate_of<LOGITS>(g[r].get(i), a, keep);
+      g[r].get(i, a, keep);
       const float lam = dy[r].get(i) + m[i];
       const float da = lam * (LERP ? before[r][i] - x[r].get(i) : before[r][i]);
       dx[i] = LERP ? keep * lam : lam;
@@ -599,7 +675,7 @@ __global__ __launch_bounds__(256) void scan_empty_kernel(const int32_t* __restri
 // Empties the chain: tickets 0, pairs and states all ones.
 __global__ __launch_bounds__(256) void scan_reset_kernel(uint32_t* ticket, int tiles, ulonglong2* rest, int64_t n) {
   const int64_t i = blockIdx.x * int64_t(256) + threadIdx.x;
-  if (i < tiles) ticket[i] = 0;
+  if (i < tiles) ticket[i * TICKET_STRIDE] = 0;
   if (i < n) rest[i] = ulonglong2{EMPTY, EMPTY};
 }
 
@@ -607,8 +683,11 @@ template <typename E, bool LOGITS, bool LERP>
 __global__ __launch_bounds__(256) void scan_step_kernel(ScanLaunch L) {
   const int64_t n = int64_t(L.B) * L.C, i = blockIdx.x * int64_t(256) + threadIdx.x;
   if (i >= n) return;
+  Gates<E, 1, LOGITS> g;
+  g.load(static_cast<const E*>(L.gate) + i);
+  g.settle();
   float a, keep;
-  gate_of<LOGITS>(to_f32(static_cast<const E*>(L.gate)[i]), a, keep);
+  g.get(0, a, keep);
   const float v = to_f32(static_cast<const E*>(L.x)[i]);
   const float h = fmaf(a, L.h0[i], LERP ? keep * v : v);
   L.h_last[i] = h;
@@ -625,8 +704,8 @@ Layout layout_of(int64_t N, int C, int chunk, int V) {
   Layout l;
   l.tiles = (C + 64 * V - 1) / (64 * V);
   l.chunks = (N + chunk - 1) / chunk;
-  l.words = (l.chunks + l.chunks / GROUP) * C + 1;
-  l.bytes = l.chunks > 1 ? align256(size_t(l.tiles) * 4) + size_t(l.words + 1) / 2 * 16 : 0;
+  l.words = (l.chunks + l.chunks / GROUP + l.chunks / (GROUP * GROUP)) * C + 1;
+  l.bytes = l.chunks > 1 ? size_t(l.tiles) * TICKET_STRIDE * 4 + size_t(l.words + 1) / 2 * 16 : 0;
   return l;
 }
 
@@ -635,8 +714,9 @@ hipError_t reset_chain(const Layout& l, int C, void* workspace, Chain& chain, hi
   chain = Chain{};
   if (l.chunks <= 1) return hipSuccess;
   chain.ticket = static_cast<uint32_t*>(workspace);
-  chain.pair = reinterpret_cast<unsigned long long*>(static_cast<char*>(workspace) + align256(size_t(l.tiles) * 4));
-  chain.state = chain.pair + l.chunks * C;
+  chain.pair = reinterpret_cast<unsigned long long*>(static_cast<char*>(workspace) + size_t(l.tiles) * TICKET_STRIDE * 4);
+  chain.group = chain.pair + l.chunks * C;
+  chain.state = chain.group + l.chunks / GROUP * C;
   const int64_t n = (l.words + 1) / 2, most = n > l.tiles ? n : l.tiles;
   scan_reset_kernel<<<uint32_t((most + 255) / 256), 256, 0, stream>>>(chain.ticket, l.tiles,
                                                                     reinterpret_cast<ulonglong2*>(chain.pair), n);
@@ -657,7 +737,7 @@ struct Forward {
     const Layout l = layout_of(L.N, L.C, FWD_CHUNK, V);
     Chain chain;
     if (hipError_t e = reset_chain(l, L.C, L.workspace, chain, stream)) return e;
-    scan_forward_kernel<E, V, LOGITS, LERP><<<uint32_t(l.chunks * l.tiles), FWD_WAVES * 64, 0, stream>>>(
+    scan_forward_kernel<E, V, LOGITS, LERP><<<uint32_t(l.chunks * l.tiles), ForwardShape<V>::WAVES * 64, 0, stream>>>(
         L, chain, L.cu_seqlens, static_cast<const E*>(L.x), static_cast<const E*>(L.gate), l.tiles);
     return hipGetLastError();
   }

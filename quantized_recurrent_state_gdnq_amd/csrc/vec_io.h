@@ -17,11 +17,12 @@ __device__ __forceinline__ float to_f32(bf16 x) { return float(x); }
 __device__ __forceinline__ void store_f32(float* p, float x) { *p = x; }
 __device__ __forceinline__ void store_f32(bf16* p, float x) { *p = bf16(x); }
 
-// p = sigmoid(z) and q = 1 - p, both to a few units in the last place: with
-// u = e^-|z| the smaller of the two is u / (1 + u), and the larger is formed
-// as one minus it, so neither cancels.  The hardware's 2^x takes -|z| log2(e)
-// in two parts (product and its rounding error), its reciprocal one Newton step.
-__device__ __forceinline__ void sigmoid_pair(float z, float& p, float& q) {
+// The smaller of p = sigmoid(z) and q = 1 - p, with the sign of z: with
+// u = e^-|z| it is u / (1 + u), and the larger is formed as one minus it, so
+// neither cancels and both are good to a few units in the last place.  The
+// hardware's 2^x takes -|z| log2(e) in two parts (product and its rounding
+// error), its reciprocal one Newton step.
+__device__ __forceinline__ float sigmoid_tail(float z) {
   float m = -fabsf(z);
   m = m < -128.0f ? -128.0f : m;  // u is 0 from -104 on (infinities, the type's lowest value); NaN passes
   const float t = m * 1.44269504f;
@@ -31,9 +32,17 @@ __device__ __forceinline__ void sigmoid_pair(float z, float& p, float& q) {
   const float d = 1.0f + u;
   float r = __builtin_amdgcn_rcpf(d);
   r = fmaf(fmaf(-d, r, 1.0f), r, r);
-  const float small = u * r, large = 1.0f - small;
-  p = z >= 0.0f ? large : small;
-  q = z >= 0.0f ? small : large;
+  return copysignf(u * r, z);
 }
+
+__device__ __forceinline__ void sigmoid_of_tail(float t, float& p, float& q) {
+  const float small = fabsf(t), large = 1.0f - small;
+  const bool up = __float_as_int(t) >= 0;  // z >= 0; a zero tail keeps its sign
+  p = up ? large : small;
+  q = up ? small : large;
+}
+
+// p = sigmoid(z) and q = 1 - p.
+__device__ __forceinline__ void sigmoid_pair(float z, float& p, float& q) { sigmoid_of_tail(sigmoid_tail(z), p, q); }
 
 }  // namespace gdnq

@@ -890,11 +890,9 @@ gdnq_status gdnq_mx_linear(const gdnq_mx_params* p, const void* x, const uint8_t
   uint8_t* scales = codes + mx_align(size_t(L.M) * L.K / 2);
   L.a_codes = codes; L.a_scales = scales; L.w_codes = w_codes; L.w_scales = w_scales; L.y = y;
   L.workspace = codes + quantized;
-  hipStream_t s = static_cast<hipStream_t>(stream);
+  L.x = x; L.in_bf16 = p->in_dtype == GDNQ_BF16;
   clear_stale_hip_error();
-  if (hipError_t e = gdnq::launch_mx_quantize(x, L.M, L.K, p->in_dtype == GDNQ_BF16, codes, scales, s))
-    return hip_status(e, "mx quantize launch");
-  return launched(gdnq::launch_mx_matmul(L, s), "mx product launch", stream);
+  return launched(gdnq::launch_mx_linear(L, static_cast<hipStream_t>(stream)), "mx linear launch", stream);
 }
 
 }  // extern "C"

@@ -2,6 +2,8 @@
 // the product of rows in it on the scaled matrix instructions.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "../../include/gdnq.h"
 #include "device_common.h"
 #include "launch.h"
@@ -31,12 +33,27 @@ __device__ __forceinline__ void load8(const bf16* p, float (&v)[8]) {
   }
 }
 
+// The scale byte of a block from the bits of its largest magnitude (the bits
+// of non-negative floats order as the values do, NaN above infinity): its
+// exponent field - 2, and 2^(127 - s), by which x / scale is an exact product.
+__device__ __forceinline__ int scale_of(uint32_t top, float& inv) {
+  const int field = int(top >> 23), s = field == 255 ? 255 : max(field - 2, 0);
+  inv = __uint_as_float(uint32_t(254 - min(s, 253)) << 23);  // s = 254 cannot occur, 255 is NaN
+  return s;
+}
+
+// The codes of eight values: the hardware's conversion rounds to the nearest,
+// ties to the even code, and saturates.
+__device__ __forceinline__ uint32_t eight_codes(const float (&v)[8], float inv) {
+  uint32_t w = 0;
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[0] * inv, v[1] * inv, 1.0f, 0);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[2] * inv, v[3] * inv, 1.0f, 1);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[4] * inv, v[5] * inv, 1.0f, 2);
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6] * inv, v[7] * inv, 1.0f, 3);
+}
+
 // Four lanes per block of 32 values, eight values (one 4-byte word of codes)
-// each.  The largest magnitude's exponent field is read from its bits (the
-// bits of non-negative floats order as the values do, NaN above infinity), so
-// s = field - 2, and x / scale is the product with the power of two
-// 2^(127 - s), exact.  The hardware's conversion rounds to the nearest, ties
-// to the even code, and saturates.
+// each.  Bound by memory.
 template <typename E>
 __global__ __launch_bounds__(256) void mx_quantize_kernel(const E* __restrict__ x, int64_t groups, uint32_t* __restrict__ codes,
                                                           uint8_t* __restrict__ scales) {
@@ -49,18 +66,9 @@ __global__ __launch_bounds__(256) void mx_quantize_kernel(const E* __restrict__ 
   for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[j]) & 0x7fffffffu);
   top = max(top, uint32_t(__builtin_amdgcn_update_dpp(0, int(top), DPP_XOR1, 0xF, 0xF, true)));
   top = max(top, uint32_t(__builtin_amdgcn_update_dpp(0, int(top), DPP_XOR2, 0xF, 0xF, true)));
-  const int field = int(top >> 23);
-  const int s = field == 255 ? 255 : max(field - 2, 0);
-  // 2^(127 - s), exponent field 254 - s; s = 254 cannot occur, 255 is NaN
-  const float inv = __uint_as_float(uint32_t(254 - min(s, 253)) << 23);
-  uint32_t w = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] *= inv;
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[0], v[1], 1.0f, 0);
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[2], v[3], 1.0f, 1);
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[4], v[5], 1.0f, 2);
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6], v[7], 1.0f, 3);
-  codes[i] = w;
+  float inv;
+  const int s = scale_of(top, inv);
+  codes[i] = eight_codes(v, inv);
   if ((i & 3) == 0) scales[i >> 2] = uint8_t(s);
 }
 
@@ -129,7 +137,25 @@ __device__ __forceinline__ int four_scales(const uint8_t* row, int b, int blocks
   return int(w);
 }
 
-template <int MT, int WAVES, typename E>
+// A block of 32 values quantized by one lane: its scale, and its codes in w.
+template <typename X>
+__device__ __forceinline__ int quantize_block(const X* x, i32x4& w) {
+  float v[32];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) load8(x + 8 * i, *reinterpret_cast<float(*)[8]>(v + 8 * i));
+  uint32_t top = 0;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) top = max(top, __float_as_uint(v[j]) & 0x7fffffffu);
+  float inv;
+  const int s = scale_of(top, inv);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = int(eight_codes(*reinterpret_cast<float(*)[8]>(v + 8 * i), inv));
+  return s;
+}
+
+// X: the type of A's rows where they are quantized here, in every workgroup,
+// instead of by a launch of their own (void: they are codes).
+template <int MT, int WAVES, typename E, typename X>
 __global__ __launch_bounds__(WAVES * 64) void mx_rows_kernel(MxLaunch L, int col_tiles) {
   __shared__ f32x4 sums[WAVES][MT][64];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
@@ -163,11 +189,19 @@ __global__ __launch_bounds__(WAVES * 64) void mx_rows_kernel(MxLaunch L, int col
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        a[t][s] = i32x4{0, 0, 0, 0};
-        if (b + s < blocks) a[t][s] = *reinterpret_cast<const i32x4*>(ac[t] + int64_t(b + s) * 16);
+      for (int s = 0; s < 4; ++s) a[t][s] = i32x4{0, 0, 0, 0};
+      if constexpr (std::is_void_v<X>) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+          if (b + s < blocks) a[t][s] = *reinterpret_cast<const i32x4*>(ac[t] + int64_t(b + s) * 16);
+        sa[t] = four_scales(as[t], b, blocks);
+      } else {
+        const X* x = static_cast<const X*>(L.x) + int64_t(min(m0 + t * 16 + r, L.M - 1)) * L.K;
+        sa[t] = 0;
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+          if (b + s < blocks) sa[t] |= quantize_block(x + (b + s) * 32, a[t][s]) << (8 * s);
       }
-      sa[t] = four_scales(as[t], b, blocks);
     }
     each<4>([&](auto s) {
 #pragma unroll
@@ -328,11 +362,11 @@ __global__ __launch_bounds__(WGM* WGN * 64) void mx_tile_kernel(MxLaunch L, int 
     for (int j = 0; j < TN; ++j) store4<E>(y, L.M, L.N, m0 + wm + i * 16 + r, n0 + wn + j * 16 + q * 4, acc[j][i]);
 }
 
-template <int MT, int WAVES, typename E>
+template <int MT, int WAVES, typename E, typename X>
 hipError_t rows_product(const MxLaunch& L, hipStream_t stream) {
   const int cols = (L.N + 15) / 16;
   const int64_t grid = int64_t(cols) * ((L.M + 16 * MT - 1) / (16 * MT));
-  mx_rows_kernel<MT, WAVES, E><<<uint32_t(grid), WAVES * 64, 0, stream>>>(L, cols);
+  mx_rows_kernel<MT, WAVES, E, X><<<uint32_t(grid), WAVES * 64, 0, stream>>>(L, cols);
   return hipGetLastError();
 }
 
@@ -346,9 +380,9 @@ hipError_t tile_product(const MxLaunch& L, hipStream_t stream) {
 template <typename E>
 hipError_t matmul(const MxLaunch& L, hipStream_t stream) {
   auto tiles = [&](int b) { return int64_t((L.M + b - 1) / b) * ((L.N + b - 1) / b); };
-  if (L.M <= 16) return rows_product<1, 8, E>(L, stream);
-  if (L.M <= 32) return rows_product<2, 8, E>(L, stream);
-  if (L.M <= 64) return rows_product<4, 8, E>(L, stream);
+  if (L.M <= 16) return rows_product<1, 8, E, void>(L, stream);
+  if (L.M <= 32) return rows_product<2, 8, E, void>(L, stream);
+  if (L.M <= 64) return rows_product<4, 8, E, void>(L, stream);
   if (tiles(256) >= 192) return tile_product<256, 256, 2, 4, E>(L, stream);
   if (tiles(128) >= 192) return tile_product<128, 128, 2, 2, E>(L, stream);
   return tile_product<64, 64, 2, 2, E>(L, stream);
@@ -372,6 +406,22 @@ size_t mx_matmul_workspace_bytes(int, int, int) { return 0; }
 
 hipError_t launch_mx_matmul(const MxLaunch& L, hipStream_t stream) {
   return L.out_bf16 ? matmul<bf16>(L, stream) : matmul<float>(L, stream);
+}
+
+// Up to FUSED_ROWS rows are quantized inside the product: one launch less (3 us
+// of a call), and 16 rows are little to quantize again in every workgroup; at 64
+// rows that took longer than the launch.
+constexpr int FUSED_ROWS = 16;
+
+hipError_t launch_mx_linear(const MxLaunch& L, hipStream_t stream) {
+  if (L.M <= FUSED_ROWS) {
+    if (L.in_bf16) return L.out_bf16 ? rows_product<1, 8, bf16, bf16>(L, stream) : rows_product<1, 8, float, bf16>(L, stream);
+    return L.out_bf16 ? rows_product<1, 8, bf16, float>(L, stream) : rows_product<1, 8, float, float>(L, stream);
+  }
+  if (hipError_t e = launch_mx_quantize(L.x, L.M, L.K, L.in_bf16, const_cast<uint8_t*>(L.a_codes),
+                                        const_cast<uint8_t*>(L.a_scales), stream))
+    return e;
+  return launch_mx_matmul(L, stream);
 }
 
 }  // namespace gdnq

@@ -659,24 +659,23 @@ __global__ __launch_bounds__(BWD_WAVES * 64, BWD_PER_SIMD) void scan_backward_ke
   }
 }
 
-// out[s] = in[s] (zero where in is null) for the sequences without tokens:
-// the states pass through.  A wave looks at 64 sequences at a time.
-__global__ __launch_bounds__(256) void scan_empty_kernel(const int32_t* __restrict__ cu, const float* __restrict__ in,
+// What has to be done before the pass: the chain is emptied (tickets 0, pairs
+// and states all ones), and out[s] = in[s] (zero where in is null) for the
+// sequences without tokens, whose states pass through.  A wave looks at 64
+// sequences at a time.
+__global__ __launch_bounds__(256) void scan_begin_kernel(uint32_t* ticket, int tiles, ulonglong2* rest, int64_t n,
+                                                         const int32_t* __restrict__ cu, const float* __restrict__ in,
                                                          float* __restrict__ out, int B, int C, int N) {
-  const int lane = threadIdx.x & 63, s = (blockIdx.x * 4 + (threadIdx.x >> 6)) * 64 + lane;
-  bool empty = s < B;
-  if (empty && cu) empty = min(max(cu[s], 0), N) >= min(max(cu[s + 1], 0), N);
-  for (uint64_t left = __builtin_amdgcn_ballot_w64(empty); left; left &= left - 1) {
-    const int64_t at = int64_t(s - lane + __builtin_ctzll(left)) * C;
-    for (int c = lane; c < C; c += 64) out[at + c] = in ? in[at + c] : 0.0f;
-  }
-}
-
-// Empties the chain: tickets 0, pairs and states all ones.
-__global__ __launch_bounds__(256) void scan_reset_kernel(uint32_t* ticket, int tiles, ulonglong2* rest, int64_t n) {
   const int64_t i = blockIdx.x * int64_t(256) + threadIdx.x;
   if (i < tiles) ticket[i * TICKET_STRIDE] = 0;
   if (i < n) rest[i] = ulonglong2{EMPTY, EMPTY};
+  bool empty = out && i < B;
+  if (empty && cu) empty = min(max(cu[i], 0), N) >= min(max(cu[i + 1], 0), N);
+  const int lane = threadIdx.x & 63;
+  for (uint64_t left = __builtin_amdgcn_ballot_w64(empty); left; left &= left - 1) {
+    const int64_t at = (i - lane + __builtin_ctzll(left)) * C;
+    for (int c = lane; c < C; c += 64) out[at + c] = in ? in[at + c] : 0.0f;
+  }
 }
 
 template <typename E, bool LOGITS, bool LERP>
@@ -709,34 +708,35 @@ Layout layout_of(int64_t N, int C, int chunk, int V) {
   return l;
 }
 
-// Clears the chain for the call, unless it is one chunk.
-hipError_t reset_chain(const Layout& l, int C, void* workspace, Chain& chain, hipStream_t stream) {
+// The chain in the workspace (none for a call of one chunk), emptied, and the
+// sequences without tokens.
+hipError_t begin(const ScanLaunch& L, const Layout& l, const float* in, float* out, Chain& chain, hipStream_t stream) {
   chain = Chain{};
-  if (l.chunks <= 1) return hipSuccess;
-  chain.ticket = static_cast<uint32_t*>(workspace);
-  chain.pair = reinterpret_cast<unsigned long long*>(static_cast<char*>(workspace) + size_t(l.tiles) * TICKET_STRIDE * 4);
-  chain.group = chain.pair + l.chunks * C;
-  chain.state = chain.group + l.chunks / GROUP * C;
-  const int64_t n = (l.words + 1) / 2, most = n > l.tiles ? n : l.tiles;
-  scan_reset_kernel<<<uint32_t((most + 255) / 256), 256, 0, stream>>>(chain.ticket, l.tiles,
-                                                                    reinterpret_cast<ulonglong2*>(chain.pair), n);
-  return hipGetLastError();
-}
-
-hipError_t pass_empty(const ScanLaunch& L, const float* in, float* out, hipStream_t stream) {
-  if (!out || (!L.cu_seqlens && L.N > 0)) return hipSuccess;
-  scan_empty_kernel<<<(L.B + 255) / 256, 256, 0, stream>>>(L.cu_seqlens, in, out, L.B, L.C, int(L.N));
+  const bool linked = l.chunks > 1;
+  if (!L.cu_seqlens && L.N > 0) out = nullptr;  // every sequence has tokens
+  if (!linked && !out) return hipSuccess;
+  if (linked) {
+    chain.ticket = static_cast<uint32_t*>(L.workspace);
+    chain.pair = reinterpret_cast<unsigned long long*>(chain.ticket + size_t(l.tiles) * TICKET_STRIDE);
+    chain.group = chain.pair + l.chunks * L.C;
+    chain.state = chain.group + l.chunks / GROUP * L.C;
+  }
+  const int64_t words = linked ? (l.words + 1) / 2 : 0, tiles = linked ? l.tiles : 0;
+  int64_t most = words > tiles ? words : tiles;
+  if (out && L.B > most) most = L.B;
+  scan_begin_kernel<<<uint32_t((most + 255) / 256), 256, 0, stream>>>(chain.ticket, int(tiles),
+                                                                    reinterpret_cast<ulonglong2*>(chain.pair), words,
+                                                                    L.cu_seqlens, in, out, L.B, L.C, int(L.N));
   return hipGetLastError();
 }
 
 template <typename E, int V, bool LOGITS, bool LERP>
 struct Forward {
   static hipError_t go(const ScanLaunch& L, hipStream_t stream) {
-    if (hipError_t e = pass_empty(L, L.h0, L.h_last, stream)) return e;
-    if (L.N == 0) return hipSuccess;
     const Layout l = layout_of(L.N, L.C, FWD_CHUNK, V);
     Chain chain;
-    if (hipError_t e = reset_chain(l, L.C, L.workspace, chain, stream)) return e;
+    if (hipError_t e = begin(L, l, L.h0, L.h_last, chain, stream)) return e;
+    if (L.N == 0) return hipSuccess;
     scan_forward_kernel<E, V, LOGITS, LERP><<<uint32_t(l.chunks * l.tiles), ForwardShape<V>::WAVES * 64, 0, stream>>>(
         L, chain, L.cu_seqlens, static_cast<const E*>(L.x), static_cast<const E*>(L.gate), l.tiles);
     return hipGetLastError();
@@ -746,11 +746,10 @@ struct Forward {
 template <typename E, int V, bool LOGITS, bool LERP>
 struct Backward {
   static hipError_t go(const ScanLaunch& L, hipStream_t stream) {
-    if (hipError_t e = pass_empty(L, L.dh_last, L.dh0, stream)) return e;
-    if (L.N == 0) return hipSuccess;
     const Layout l = layout_of(L.N, L.C, BWD_CHUNK, V);
     Chain chain;
-    if (hipError_t e = reset_chain(l, L.C, L.workspace, chain, stream)) return e;
+    if (hipError_t e = begin(L, l, L.dh_last, L.dh0, chain, stream)) return e;
+    if (L.N == 0) return hipSuccess;
     scan_backward_kernel<E, V, LOGITS, LERP><<<uint32_t(l.chunks * l.tiles), BWD_WAVES * 64, 0, stream>>>(
         L, chain, L.cu_seqlens, static_cast<const E*>(L.x), static_cast<const E*>(L.gate), static_cast<const E*>(L.dy), l.tiles,
         int(l.chunks));

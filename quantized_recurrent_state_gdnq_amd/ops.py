@@ -22,7 +22,9 @@ def _ptr(t):
 
 
 def _stream(dev):
-    return torch.cuda.current_stream(dev).cuda_stream
+    """The device's current stream as a hipStream_t.  The raw query is a tenth
+    of the time of making a Stream object, which is a fifth of a small call."""
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def _need(t, name, dtype=None, device=None):
@@ -584,9 +586,7 @@ def _space(workspace, need, dev):
     """The caller's workspace (any contiguous tensor of the device) or a new
     one, and its size in bytes."""
     if workspace is None:
-        if need == 0:
-            return None, 0
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        return (torch.empty(need, dtype=torch.uint8, device=dev), need) if need else (None, 0)
     _need(workspace, "workspace", None, dev)
     return workspace, workspace.numel() * workspace.element_size()
 

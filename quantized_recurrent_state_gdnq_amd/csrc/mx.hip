@@ -15,6 +15,7 @@ namespace {
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
   const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
@@ -222,14 +223,20 @@ __global__ __launch_bounds__(WAVES * 64) void mx_rows_kernel(MxLaunch L, int col
 //
 // Bound by the matrix units.  A workgroup computes BM x BN of y, its WGM x WGN
 // waves an equal part each, in steps of DEPTH values: the step's rows of both
-// operands (128 bytes each) are loaded straight into LDS, in two buffers, one
-// filled while the other is multiplied.
+// operands (128 bytes each) are loaded straight into LDS, in two buffers.
+//   The 32 x 32 x 64 instruction: lane l holds one block of row l % 32, of two
+// blocks h = l / 32, and the results 8 g + 4 h + 0 .. 3 of column l % 32.  It
+// reaches 9.5 PFLOP/s in a loop of its own, 16 x 16 x 128 only 4.8.  Half h
+// takes blocks 4 h + s of a step's eight, s = 0 .. 3, so a row's four scale
+// bytes of a half are one word and s selects its byte.
 //   In LDS the eight 16-byte blocks of a row are permuted by its number, so
-// that the sixteen rows a matrix instruction reads at one block lie in
-// different banks; the loads write LDS in lane order, so the permutation is
-// in the address each lane loads from.
-//   Lane group q takes blocks 2q and 2q + 1 of a step's eight.  Their scales,
-// for rows r and r + 16 of 32, are one word of LDS: [32 rows][r][q][2][2].
+// that the rows that a wave reads together at one block lie in different
+// banks; the loads write LDS in lane order, so the permutation is in the
+// address each lane loads from.
+//   The operands of instruction step s + 1 are read from LDS while those of s
+// are multiplied.  Before the last of a step's four, the next step's buffer
+// has to be filled and this one's reads done (one barrier a step); then the
+// loads for the step after go into this one.
 //   Rows beyond the end read the last row (their results are not stored);
 // blocks beyond the depth read zeros.
 constexpr int DEPTH = 256, STEP_BYTES = DEPTH / 2, STEP_BLOCKS = DEPTH / 32;
@@ -252,39 +259,58 @@ struct Stage {
       at[i] = uint32_t(min(row, rows - 1 - row0)) * uint32_t(row_bytes) + (((lane & 7) ^ swizzle(row)) << 4);
     }
   }
+  // 16 bytes a lane from p (base and the lane's offset) to LDS at `to`, in lane
+  // order.  As an empty-handed statement (it writes no register), because the
+  // compiler waits for all such loads before any read of LDS when it knows of
+  // them, whichever buffer is read; the kernel waits itself (vmcnt) before the
+  // barrier that lets the buffer be read.
+  __device__ __forceinline__ static void to_lds(const uint8_t* base, uint32_t offset, uint8_t* to) {
+    const uint32_t lds = uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)to));
+    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(offset), "s"(base) : "m0", "memory");
+  }
+  __device__ __forceinline__ static void to_lds(const uint8_t* p, uint8_t* to) {
+    const uint32_t lds = uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)to));
+    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(p) : "m0", "memory");
+  }
   // Loads the step from block k0 on to LDS at `to`.
-  __device__ __forceinline__ void load(uint8_t* to, int k0, int blocks, int wave, int lane) const {
+  __device__ __forceinline__ void load(uint8_t* to, int k0, int wave) const {
+    const uint8_t* from = base + int64_t(k0) * 16;
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) to_lds(from, at[i], to + (i * (THREADS / 64) + wave) * 1024);
+  }
+  // The same where the depth ends inside the step.
+  __device__ __forceinline__ void load_end(uint8_t* to, int k0, int blocks, int wave, int lane) const {
     const uint8_t* from = base + int64_t(k0) * 16;
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
-      const int piece = i * (THREADS / 64) + wave;
-      const uint8_t* p = from + at[i];
-      if (k0 + STEP_BLOCKS > blocks && k0 + ((lane & 7) ^ swizzle(piece * 8 + (lane >> 3))) >= blocks) p = zeros;
-      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)p,
-                                       (__attribute__((address_space(3))) void*)(to + piece * 1024), 16, 0, 0);
+      const int piece = i * (THREADS / 64) + wave, row = piece * 8 + (lane >> 3);
+      to_lds(k0 + ((lane & 7) ^ swizzle(row)) < blocks ? from + at[i] : zeros, to + piece * 1024);
     }
   }
 };
 
-// A row's eight scales of a step (beyond the depth 0).
-__device__ __forceinline__ uint64_t eight_scales(const uint8_t* row, int k0, int blocks) {
+// A row's scales of the step in which the depth ends (beyond it 0).
+__device__ __forceinline__ uint64_t last_scales(const uint8_t* row, int k0, int blocks) {
   uint64_t w = 0;
-  if (k0 + STEP_BLOCKS <= blocks) {
-    __builtin_memcpy(&w, row + k0, 8);
-  } else {
-    for (int i = 0; i < STEP_BLOCKS - 1; ++i)
-      if (k0 + i < blocks) w |= uint64_t(row[k0 + i]) << (8 * i);
-  }
+#pragma unroll 1
+  for (int i = 0; k0 + i < blocks; ++i) w |= uint64_t(row[k0 + i]) << (8 * i);
   return w;
+}
+
+template <int BW, int BA>
+__device__ __forceinline__ f32x16 wide_product(const i32x4& w, const i32x4& a, const f32x16& c, int sw, int sa) {
+  const i32x8 w8 = {w[0], w[1], w[2], w[3], 0, 0, 0, 0}, a8 = {a[0], a[1], a[2], a[3], 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w8, a8, c, 4, 4, BW, sw, BA, sa);
 }
 
 template <int BM, int BN, int WGM, int WGN, typename E>
 __global__ __launch_bounds__(WGM* WGN * 64) void mx_tile_kernel(MxLaunch L, int row_tiles, int col_tiles) {
   constexpr int WAVES = WGM * WGN, THREADS = WAVES * 64;
-  constexpr int TM = BM / WGM / 16, TN = BN / WGN / 16;  // 16 x 16 tiles of a wave
-  static_assert(TM % 2 == 0 && TN % 2 == 0 && BM + BN <= THREADS, "pairs of tiles share a scale word; a thread a row's scales");
+  constexpr int TM = BM / WGM / 32, TN = BN / WGN / 32;  // 32 x 32 tiles of a wave
+  static_assert(BM * BN <= (BM + BN) * STEP_BYTES, "the results of a pass fit the two buffers");
+  static_assert(THREADS % (BM + BN) == 0, "a thread stages a row's scales");
   __shared__ __attribute__((aligned(1024))) uint8_t codes[2][(BM + BN) * STEP_BYTES];
-  __shared__ uint32_t scales[2][(BM + BN) * STEP_BLOCKS / 4];
+  __shared__ uint64_t scales[2][BM + BN];
 
   // Tiles in bands: the workgroups of one XCD (every eighth) take adjacent
   // ones, down GROUP rows of tiles and then to the right, so that its L2 holds
@@ -297,7 +323,7 @@ __global__ __launch_bounds__(WGM* WGN * 64) void mx_tile_kernel(MxLaunch L, int 
   const int rows_here = min(GROUP, row_tiles - band * GROUP);
   const int m0 = (band * GROUP + in_band % rows_here) * BM, n0 = in_band / rows_here * BN;
 
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
   const int wm = wave % WGM * (BM / WGM), wn = wave / WGM * (BN / WGN);
   const int blocks = L.K / 32, row_bytes = L.K / 2;
   Stage<BM, THREADS> sa;
@@ -305,61 +331,134 @@ __global__ __launch_bounds__(WGM* WGN * 64) void mx_tile_kernel(MxLaunch L, int 
   sa.init(L.a_codes, m0, L.M, row_bytes, wave, lane);
   sw.init(L.w_codes, n0, L.N, row_bytes, wave, lane);
   // thread t stages the scales of row t of A's tile, then of W's
-  const int t = threadIdx.x;
+  const int t = threadIdx.x % (BM + BN);
   const uint8_t* scale_row = t < BM ? L.a_scales + int64_t(min(m0 + t, L.M - 1)) * blocks
                                     : L.w_scales + int64_t(min(n0 + t - BM, L.N - 1)) * blocks;
-  const bool stages_scales = t < BM + BN;
-  auto put_scales = [&](int buf, uint64_t w) {
-    uint16_t* p = reinterpret_cast<uint16_t*>(scales[buf]) + (t >> 5) * 128 + (t & 15) * 8 + (t >> 4 & 1);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) p[i * 2] = uint16_t(w >> (16 * i));
+  const int full = blocks / STEP_BLOCKS, steps = (blocks + STEP_BLOCKS - 1) / STEP_BLOCKS;
+  uint64_t staged = 0;
+  auto load = [&](int step) {  // a step that the depth fills
+    uint8_t* to = codes[step & 1];
+    sa.load(to, step * STEP_BLOCKS, wave);
+    sw.load(to + BM * STEP_BYTES, step * STEP_BLOCKS, wave);
+    __builtin_memcpy(&staged, scale_row + step * STEP_BLOCKS, 8);
+  };
+  auto load_any = [&](int step) {  // a step beyond the last: none
+    if (step >= steps) return;
+    if (step < full) return load(step);
+    uint8_t* to = codes[step & 1];
+    sa.load_end(to, step * STEP_BLOCKS, blocks, wave, lane);
+    sw.load_end(to + BM * STEP_BYTES, step * STEP_BLOCKS, blocks, wave, lane);
+    staged = last_scales(scale_row, step * STEP_BLOCKS, blocks);
   };
 
-  f32x4 acc[TN][TM] = {};
-  sa.load(codes[0], 0, blocks, wave, lane);
-  sw.load(codes[0] + BM * STEP_BYTES, 0, blocks, wave, lane);
-  if (stages_scales) put_scales(0, eight_scales(scale_row, 0, blocks));
-  const int steps = (blocks + STEP_BLOCKS - 1) / STEP_BLOCKS;
-  for (int step = 0; step < steps; ++step) {
-    const int buf = step & 1;
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's loads into LDS
-    __syncthreads();
-    uint64_t next_scales = 0;
-    const bool more = step + 1 < steps;
-    if (more) {
-      sa.load(codes[buf ^ 1], (step + 1) * STEP_BLOCKS, blocks, wave, lane);
-      sw.load(codes[buf ^ 1] + BM * STEP_BYTES, (step + 1) * STEP_BLOCKS, blocks, wave, lane);
-      if (stages_scales) next_scales = eight_scales(scale_row, (step + 1) * STEP_BLOCKS, blocks);
-    }
-    uint32_t sca[TM / 2], scw[TN / 2];
+  f32x16 acc[TN][TM] = {};
+  i32x4 a[2][TM], w[2][TN];
+  int sca[TM], scw[TN];
+  // operands of instruction step s of `buf`
+  auto fetch = [&](int buf, auto s) {
+    constexpr int k = s.value;
+    const int slot = ((4 * h + k) ^ swizzle(r)) << 4;
+    const uint8_t* ca = codes[buf] + (wm + r) * STEP_BYTES + slot;
+    const uint8_t* cw = codes[buf] + (BM + wn + r) * STEP_BYTES + slot;
 #pragma unroll
-    for (int i = 0; i < TM / 2; ++i) sca[i] = scales[buf][(wm / 32 + i) * 64 + r * 4 + q];
+    for (int i = 0; i < TM; ++i) a[k & 1][i] = *reinterpret_cast<const i32x4*>(ca + i * 32 * STEP_BYTES);
 #pragma unroll
-    for (int i = 0; i < TN / 2; ++i) scw[i] = scales[buf][(BM / 32 + wn / 32 + i) * 64 + r * 4 + q];
-    const uint8_t* ca = codes[buf] + wm * STEP_BYTES;
-    const uint8_t* cw = codes[buf] + (BM + wn) * STEP_BYTES;
-    each<2>([&](auto s) {
-      i32x4 a[TM], w[TN];
-#pragma unroll
-      for (int i = 0; i < TM; ++i)
-        a[i] = *reinterpret_cast<const i32x4*>(ca + (i * 16 + r) * STEP_BYTES + (((2 * q + s.value) ^ swizzle(r)) << 4));
-#pragma unroll
-      for (int i = 0; i < TN; ++i)
-        w[i] = *reinterpret_cast<const i32x4*>(cw + (i * 16 + r) * STEP_BYTES + (((2 * q + s.value) ^ swizzle(r)) << 4));
-      each<TN>([&](auto j) {
-        each<TM>([&](auto i) {
-          acc[j.value][i.value] = product<(j.value & 1) * 2 + s.value, (i.value & 1) * 2 + s.value>(
-              w[j.value], a[i.value], acc[j.value][i.value], int(scw[j.value / 2]), int(sca[i.value / 2]));
-        });
+    for (int i = 0; i < TN; ++i) w[k & 1][i] = *reinterpret_cast<const i32x4*>(cw + i * 32 * STEP_BYTES);
+  };
+  auto multiply = [&](auto s) {
+    constexpr int k = s.value;
+    each<TN>([&](auto j) {
+      each<TM>([&](auto i) {
+        acc[j.value][i.value] =
+            wide_product<k, k>(w[k & 1][j.value], a[k & 1][i.value], acc[j.value][i.value], scw[j.value], sca[i.value]);
       });
     });
-    if (more && stages_scales) put_scales(buf ^ 1, next_scales);
-  }
+  };
+  auto fetch_scales = [&](int buf) {
+    const int* p = reinterpret_cast<const int*>(scales[buf]);
+#pragma unroll
+    for (int i = 0; i < TM; ++i) sca[i] = p[(wm + i * 32 + r) * 2 + h];
+#pragma unroll
+    for (int i = 0; i < TN; ++i) scw[i] = p[(BM + wn + i * 32 + r) * 2 + h];
+  };
+  // One step; LOAD: the step after the next is loaded, 1 full, 2 any; NEXT:
+  // there is a next one.  The body of the main loop has no branch: the
+  // compiler moves matrix instructions past one, behind the barrier.
+  auto body = [&](int step, auto LOAD, auto NEXT) {
+    const int buf = step & 1;
+    fetch_scales(buf);
+    fetch(buf, Int<1>{});
+    multiply(Int<0>{});
+    __builtin_amdgcn_sched_barrier(0);  // two instruction steps' operands in registers, not four
+    fetch(buf, Int<2>{});
+    multiply(Int<1>{});
+    __builtin_amdgcn_sched_barrier(0);
+    fetch(buf, Int<3>{});
+    multiply(Int<2>{});
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (NEXT.value != 0) {
+      scales[buf ^ 1][t] = staged;
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's loads into LDS
+      __syncthreads();
+      if constexpr (LOAD.value == 1) load(step + 2);
+      if constexpr (LOAD.value == 2) load_any(step + 2);
+      fetch(buf ^ 1, Int<0>{});
+    }
+    multiply(Int<3>{});
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  load_any(0);
+  scales[0][t] = staged;
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  load_any(1);
+  fetch(0, Int<0>{});
+  int step = 0;
+  for (; step + 2 < full; ++step) body(step, Int<1>{}, Int<1>{});
+  for (; step + 1 < steps; ++step) body(step, Int<2>{}, Int<1>{});
+  body(step, Int<0>{}, Int<0>{});
+
+  // The results go through LDS (BN 2-byte or half as many 4-byte values a row
+  // at a time) so that they leave in whole rows: stored from the lanes, 16
+  // bytes a row, they took 13 us of a tile's 52.  A row's 16-byte pieces are
+  // permuted by its number.
+  constexpr int PASSES = sizeof(E) / 2, COLS = BN / PASSES, PITCH = COLS * sizeof(E), PIECES = PITCH / 16;
+  typedef E e4 __attribute__((ext_vector_type(4)));
+  uint8_t* out = codes[0];
   E* y = static_cast<E*>(L.y);
+  for (int pass = 0; pass < PASSES; ++pass) {
+    __syncthreads();
+    if (wn / COLS == pass) {
 #pragma unroll
-  for (int i = 0; i < TM; ++i)
+      for (int i = 0; i < TM; ++i)
 #pragma unroll
-    for (int j = 0; j < TN; ++j) store4<E>(y, L.M, L.N, m0 + wm + i * 16 + r, n0 + wn + j * 16 + q * 4, acc[j][i]);
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const int row = wm + i * 32 + r, at = (wn % COLS + j * 32 + g * 8 + h * 4) * int(sizeof(E));
+            const f32x4 v = {acc[j][i][4 * g], acc[j][i][4 * g + 1], acc[j][i][4 * g + 2], acc[j][i][4 * g + 3]};
+            *reinterpret_cast<e4*>(out + row * PITCH + (((at >> 4) ^ row) & (PIECES - 1)) * 16 + (at & 15)) =
+                __builtin_convertvector(v, e4);
+          }
+    }
+    __syncthreads();
+    const int n = n0 + pass * COLS;
+    if (int64_t(L.N) * sizeof(E) % 16 == 0) {  // whole pieces, aligned, in or out together
+      for (int p = threadIdx.x; p < BM * PIECES; p += THREADS) {
+        const int row = p / PIECES, piece = p % PIECES, col = n + piece * (16 / int(sizeof(E)));
+        if (m0 + row < L.M && col < L.N)
+          *reinterpret_cast<i32x4*>(y + int64_t(m0 + row) * L.N + col) =
+              *reinterpret_cast<const i32x4*>(out + row * PITCH + ((piece ^ row) & (PIECES - 1)) * 16);
+      }
+    } else {
+      for (int p = threadIdx.x; p < BM * COLS; p += THREADS) {
+        const int row = p / COLS, at = p % COLS * int(sizeof(E)), col = n + p % COLS;
+        if (m0 + row < L.M && col < L.N)
+          y[int64_t(m0 + row) * L.N + col] =
+              *reinterpret_cast<const E*>(out + row * PITCH + (((at >> 4) ^ row) & (PIECES - 1)) * 16 + (at & 15));
+      }
+    }
+  }
 }
 
 template <int MT, int WAVES, typename E, typename X>

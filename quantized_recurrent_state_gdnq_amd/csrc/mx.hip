@@ -353,7 +353,7 @@ __global__ __launch_bounds__(WGM* WGN * 64) void mx_tile_kernel(MxLaunch L, int 
 
   f32x16 acc[TN][TM] = {};
   i32x4 a[2][TM], w[2][TN];
-  int sca[TM], scw[TN];
+  int sca[TM], scw[TN], next_sca[TM], next_scw[TN];
   // operands of instruction step s of `buf`
   auto fetch = [&](int buf, auto s) {
     constexpr int k = s.value;
@@ -377,23 +377,30 @@ __global__ __launch_bounds__(WGM* WGN * 64) void mx_tile_kernel(MxLaunch L, int 
   auto fetch_scales = [&](int buf) {
     const int* p = reinterpret_cast<const int*>(scales[buf]);
 #pragma unroll
-    for (int i = 0; i < TM; ++i) sca[i] = p[(wm + i * 32 + r) * 2 + h];
+    for (int i = 0; i < TM; ++i) next_sca[i] = p[(wm + i * 32 + r) * 2 + h];
 #pragma unroll
-    for (int i = 0; i < TN; ++i) scw[i] = p[(BM + wn + i * 32 + r) * 2 + h];
+    for (int i = 0; i < TN; ++i) next_scw[i] = p[(BM + wn + i * 32 + r) * 2 + h];
   };
   // One step; LOAD: the step after the next is loaded, 1 full, 2 any; NEXT:
   // there is a next one.  The body of the main loop has no branch: the
-  // compiler moves matrix instructions past one, behind the barrier.
+  // compiler moves matrix instructions past one, behind the barrier.  (Nor may
+  // it move reads behind the products that they run beside.)
   auto body = [&](int step, auto LOAD, auto NEXT) {
     const int buf = step & 1;
-    fetch_scales(buf);
+#pragma unroll
+    for (int i = 0; i < TM; ++i) sca[i] = next_sca[i];
+#pragma unroll
+    for (int i = 0; i < TN; ++i) scw[i] = next_scw[i];
     fetch(buf, Int<1>{});
+    __builtin_amdgcn_sched_barrier(0);
     multiply(Int<0>{});
-    __builtin_amdgcn_sched_barrier(0);  // two instruction steps' operands in registers, not four
+    __builtin_amdgcn_sched_barrier(0);
     fetch(buf, Int<2>{});
+    __builtin_amdgcn_sched_barrier(0);
     multiply(Int<1>{});
     __builtin_amdgcn_sched_barrier(0);
     fetch(buf, Int<3>{});
+    __builtin_amdgcn_sched_barrier(0);
     multiply(Int<2>{});
     __builtin_amdgcn_sched_barrier(0);
     if constexpr (NEXT.value != 0) {
@@ -403,6 +410,8 @@ __global__ __launch_bounds__(WGM* WGN * 64) void mx_tile_kernel(MxLaunch L, int 
       if constexpr (LOAD.value == 1) load(step + 2);
       if constexpr (LOAD.value == 2) load_any(step + 2);
       fetch(buf ^ 1, Int<0>{});
+      fetch_scales(buf ^ 1);
+      __builtin_amdgcn_sched_barrier(0);
     }
     multiply(Int<3>{});
     __builtin_amdgcn_sched_barrier(0);
@@ -413,6 +422,7 @@ __global__ __launch_bounds__(WGM* WGN * 64) void mx_tile_kernel(MxLaunch L, int 
   __syncthreads();
   load_any(1);
   fetch(0, Int<0>{});
+  fetch_scales(0);
   int step = 0;
   for (; step + 2 < full; ++step) body(step, Int<1>{}, Int<1>{});
   for (; step + 1 < steps; ++step) body(step, Int<2>{}, Int<1>{});

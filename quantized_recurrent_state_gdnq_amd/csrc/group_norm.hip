@@ -34,6 +34,9 @@ template <int TEAM>
 constexpr int bounds() { return TEAM == BLOCK ? 1024 : THREADS; }
 template <int TEAM>
 constexpr int teams_of() { return TEAM == BLOCK ? 1 : THREADS / (TEAM == BLOCK ? 1 : TEAM); }
+// Whether the backward pass gives a workgroup one group of every token.
+template <int TEAM>
+constexpr bool by_group() { return TEAM != BLOCK && TEAM >= 16; }
 template <int TEAM>
 __device__ __forceinline__ int team_size() { return TEAM == BLOCK ? int(blockDim.x) : TEAM; }
 
@@ -205,21 +208,31 @@ __global__ __launch_bounds__(bounds<TEAM>()) void norm_forward_kernel(NormLaunch
   }
 }
 
-// The teams take their groups as in the forward pass and add the gradients of
-// their weights up in registers.  Row `slot` of the partial sums is the
-// team's; the workgroup's teams are added in LDS first when all groups share
-// the weights.
+// The teams take their groups as in the forward pass, or, with weights of
+// every channel and groups wide enough (above 64 values) to be read apart from
+// their neighbours, the teams of a workgroup take one group of the token each
+// of the next tokens.  Either way a team adds the gradients of its weights up
+// in registers, and where the workgroup's teams have the same weights they are
+// added in LDS to one row of the partial sums, else a team has a row.
 template <typename E, int TEAM, bool WIDE, int EIGHTS>
 __global__ __launch_bounds__(bounds<TEAM>()) void norm_backward_kernel(NormLaunch L, int64_t units, int64_t slots, float* partial) {
   constexpr int TEAMS = teams_of<TEAM>();
   __shared__ float box[4][16];
   const int l = TEAM == BLOCK ? threadIdx.x : threadIdx.x % team_size<TEAM>(), D = L.D;
   const int64_t slot = blockIdx.x * int64_t(TEAMS) + threadIdx.x / team_size<TEAM>();
-  const int64_t wat = L.shared ? 0 : slot % L.G * D;
+  const bool alike = L.shared || by_group<TEAM>();  // the workgroup's teams have the same weights
+  const int64_t per_group = gridDim.x / L.G;         // workgroups (by_group)
+  const int64_t group = by_group<TEAM>() && !L.shared ? blockIdx.x % L.G : slot % L.G;
+  const int64_t wat = L.shared ? 0 : group * D;
+  int64_t first = slot < slots ? slot : units, stride = slots;
+  if (by_group<TEAM>() && !L.shared) {
+    first = (blockIdx.x / L.G * TEAMS + threadIdx.x / team_size<TEAM>()) * L.G + group;
+    stride = per_group * TEAMS * L.G;
+  }
   float w[EIGHTS][8], b[EIGHTS][8], dw[EIGHTS][8] = {}, db[EIGHTS][8] = {};
   load_params<TEAM, WIDE>(L.weight ? L.weight + wat : nullptr, 1.0f, l, D, w);
   load_params<TEAM, WIDE>(L.bias ? L.bias + wat : nullptr, 0.0f, l, D, b);
-  for (int64_t u = slot < slots ? slot : units; u < units; u += slots) {
+  for (int64_t u = first; u < units; u += stride) {
     const int64_t at = u * D;
     Eight<E, TEAM, WIDE> x[EIGHTS], g[EIGHTS], dy[EIGHTS];
 #pragma unroll
@@ -268,7 +281,7 @@ __global__ __launch_bounds__(bounds<TEAM>()) void norm_backward_kernel(NormLaunc
   if (!partial) return;
   // [2][rows][D]: dw, then db
   if constexpr (TEAMS > 1) {
-    if (L.shared) {
+    if (alike) {
       __shared__ float sums[2][TEAMS][TEAM * 8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -352,7 +365,8 @@ struct Backward {
   static hipError_t go(const NormLaunch& L, hipStream_t stream) {
     constexpr int TEAMS = teams_of<TEAM>();
     const int64_t units = int64_t(L.R) * L.G, slots = slots_of(units, L.shared ? 1 : L.G, L.D, BACKWARD_WAVES);
-    const int64_t grid = (slots + TEAMS - 1) / TEAMS;
+    int64_t grid = (slots + TEAMS - 1) / TEAMS;
+    if (by_group<TEAM>() && !L.shared) grid = (grid + L.G - 1) / L.G * L.G;
     const bool params = L.dweight || L.dbias;
     float* partial = params ? static_cast<float*>(L.workspace) : nullptr;
     if (units > 0) {
@@ -360,9 +374,10 @@ struct Backward {
       if (hipError_t e = hipGetLastError()) return e;
     }
     if (!params) return hipSuccess;
-    // rows of D: one per workgroup with shared weights, else one per team,
-    // whose groups repeat every G rows: [teams / G][G D]
-    const int64_t rows = units == 0 ? 0 : L.shared ? grid : slots / L.G, cols = int64_t(L.shared ? 1 : L.G) * L.D;
+    // rows of D: one per workgroup whose teams have the same weights, else one
+    // per team; without shared weights the groups repeat every G rows: [rows / G][G D]
+    const int64_t all = L.shared || by_group<TEAM>() ? grid : slots;
+    const int64_t rows = units == 0 ? 0 : L.shared ? all : all / L.G, cols = int64_t(L.shared ? 1 : L.G) * L.D;
     norm_params_kernel<<<dim3(uint32_t((cols + 15) / 16), 2), 1024, 0, stream>>>(partial, rows, cols, L.dweight, L.dbias);
     return hipGetLastError();
   }

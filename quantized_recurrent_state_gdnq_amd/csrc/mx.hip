@@ -222,41 +222,44 @@ __global__ __launch_bounds__(WAVES * 64) void mx_rows_kernel(MxLaunch L, int col
 // ---------------------------------------------------------------- many rows
 //
 // Bound by the matrix units.  A workgroup computes BM x BN of y, its WGM x WGN
-// waves an equal part each, in steps of DEPTH values: the step's rows of both
-// operands (128 bytes each) are loaded straight into LDS, in two buffers.
+// waves an equal part each, in steps of DEPTH values (256, or 512 for small
+// tiles): the step's rows of both operands are loaded straight into LDS, in two
+// buffers.
 //   The 32 x 32 x 64 instruction: lane l holds one block of row l % 32, of two
 // blocks h = l / 32, and the results 8 g + 4 h + 0 .. 3 of column l % 32.  It
 // reaches 9.5 PFLOP/s in a loop of its own, 16 x 16 x 128 only 4.8.  Half h
-// takes blocks 4 h + s of a step's eight, s = 0 .. 3, so a row's four scale
-// bytes of a half are one word and s selects its byte.
-//   In LDS the eight 16-byte blocks of a row are permuted by its number, so
+// takes the step's blocks of that half in turn, so four scale bytes are one
+// word and the instruction step selects the byte.
+//   In LDS the 16-byte blocks of a row are permuted by its number, so
 // that the rows that a wave reads together at one block lie in different
 // banks; the loads write LDS in lane order, so the permutation is in the
 // address each lane loads from.
 //   The operands of instruction step s + 1 are read from LDS while those of s
-// are multiplied.  Before the last of a step's four, the next step's buffer
+// are multiplied.  Before the last of a step's, the next step's buffer
 // has to be filled and this one's reads done (one barrier a step); then the
 // loads for the step after go into this one.
 //   Rows beyond the end read the last row (their results are not stored);
 // blocks beyond the depth read zeros.
-constexpr int DEPTH = 256, STEP_BYTES = DEPTH / 2, STEP_BLOCKS = DEPTH / 32;
-
 __device__ const uint8_t zeros[16] __attribute__((aligned(16))) = {};
 
 // What a row's block number is permuted by: the same for rows 16 apart.
-__device__ __forceinline__ int swizzle(int row) { return (row ^ (row >> 3 & 1)) & 7; }
+template <int BLOCKS>
+__device__ __forceinline__ int swizzle(int row) {
+  return BLOCKS == 8 ? (row ^ (row >> 3 & 1)) & 7 : row & 15;
+}
 
-template <int ROWS, int THREADS>
+// One operand's ROWS rows of a step of BLOCKS blocks, 1 KB per wave and load.
+template <int ROWS, int BLOCKS, int THREADS>
 struct Stage {
-  static constexpr int LOADS = ROWS * STEP_BYTES / (THREADS * 16);  // eight rows, 1 KB, per wave and load
+  static constexpr int LOADS = ROWS * BLOCKS / THREADS, PER_KB = 64 / BLOCKS;
   const uint8_t* base;  // of the tile's first row
   uint32_t at[LOADS];   // the lane's block of its rows in a step
   __device__ __forceinline__ void init(const uint8_t* codes, int row0, int rows, int row_bytes, int wave, int lane) {
     base = codes + int64_t(row0) * row_bytes;
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
-      const int row = (i * (THREADS / 64) + wave) * 8 + (lane >> 3);
-      at[i] = uint32_t(min(row, rows - 1 - row0)) * uint32_t(row_bytes) + (((lane & 7) ^ swizzle(row)) << 4);
+      const int row = (i * (THREADS / 64) + wave) * PER_KB + lane / BLOCKS;
+      at[i] = uint32_t(min(row, rows - 1 - row0)) * uint32_t(row_bytes) + ((lane % BLOCKS ^ swizzle<BLOCKS>(row)) << 4);
     }
   }
   // 16 bytes a lane from p (base and the lane's offset) to LDS at `to`, in lane
@@ -283,19 +286,11 @@ struct Stage {
     const uint8_t* from = base + int64_t(k0) * 16;
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
-      const int piece = i * (THREADS / 64) + wave, row = piece * 8 + (lane >> 3);
-      to_lds(k0 + ((lane & 7) ^ swizzle(row)) < blocks ? from + at[i] : zeros, to + piece * 1024);
+      const int piece = i * (THREADS / 64) + wave, row = piece * PER_KB + lane / BLOCKS;
+      to_lds(k0 + (lane % BLOCKS ^ swizzle<BLOCKS>(row)) < blocks ? from + at[i] : zeros, to + piece * 1024);
     }
   }
 };
-
-// A row's scales of the step in which the depth ends (beyond it 0).
-__device__ __forceinline__ uint64_t last_scales(const uint8_t* row, int k0, int blocks) {
-  uint64_t w = 0;
-#pragma unroll 1
-  for (int i = 0; k0 + i < blocks; ++i) w |= uint64_t(row[k0 + i]) << (8 * i);
-  return w;
-}
 
 template <int BW, int BA>
 __device__ __forceinline__ f32x16 wide_product(const i32x4& w, const i32x4& a, const f32x16& c, int sw, int sa) {
@@ -303,14 +298,16 @@ __device__ __forceinline__ f32x16 wide_product(const i32x4& w, const i32x4& a, c
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w8, a8, c, 4, 4, BW, sw, BA, sa);
 }
 
-template <int BM, int BN, int WGM, int WGN, typename E>
+template <int BM, int BN, int WGM, int WGN, int DEPTH, typename E>
 __global__ __launch_bounds__(WGM* WGN * 64) void mx_tile_kernel(MxLaunch L, int row_tiles, int col_tiles) {
   constexpr int WAVES = WGM * WGN, THREADS = WAVES * 64;
   constexpr int TM = BM / WGM / 32, TN = BN / WGN / 32;  // 32 x 32 tiles of a wave
+  constexpr int STEP_BYTES = DEPTH / 2, STEP_BLOCKS = DEPTH / 32;  // of a row
+  constexpr int INSTRUCTIONS = STEP_BLOCKS / 2, WORDS = STEP_BLOCKS / 8;  // of a step; a half's words of scales
   static_assert(BM * BN <= (BM + BN) * STEP_BYTES, "the results of a pass fit the two buffers");
   static_assert(THREADS % (BM + BN) == 0, "a thread stages a row's scales");
   __shared__ __attribute__((aligned(1024))) uint8_t codes[2][(BM + BN) * STEP_BYTES];
-  __shared__ uint64_t scales[2][BM + BN];
+  __shared__ uint64_t scales[2][BM + BN][WORDS];
 
   // Tiles in bands: the workgroups of one XCD (every eighth) take adjacent
   // ones, down GROUP rows of tiles and then to the right, so that its L2 holds
@@ -326,8 +323,8 @@ __global__ __launch_bounds__(WGM* WGN * 64) void mx_tile_kernel(MxLaunch L, int 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
   const int wm = wave % WGM * (BM / WGM), wn = wave / WGM * (BN / WGN);
   const int blocks = L.K / 32, row_bytes = L.K / 2;
-  Stage<BM, THREADS> sa;
-  Stage<BN, THREADS> sw;
+  Stage<BM, STEP_BLOCKS, THREADS> sa;
+  Stage<BN, STEP_BLOCKS, THREADS> sw;
   sa.init(L.a_codes, m0, L.M, row_bytes, wave, lane);
   sw.init(L.w_codes, n0, L.N, row_bytes, wave, lane);
   // thread t stages the scales of row t of A's tile, then of W's
@@ -335,12 +332,12 @@ __global__ __launch_bounds__(WGM* WGN * 64) void mx_tile_kernel(MxLaunch L, int 
   const uint8_t* scale_row = t < BM ? L.a_scales + int64_t(min(m0 + t, L.M - 1)) * blocks
                                     : L.w_scales + int64_t(min(n0 + t - BM, L.N - 1)) * blocks;
   const int full = blocks / STEP_BLOCKS, steps = (blocks + STEP_BLOCKS - 1) / STEP_BLOCKS;
-  uint64_t staged = 0;
+  uint64_t staged[WORDS] = {};
   auto load = [&](int step) {  // a step that the depth fills
     uint8_t* to = codes[step & 1];
     sa.load(to, step * STEP_BLOCKS, wave);
     sw.load(to + BM * STEP_BYTES, step * STEP_BLOCKS, wave);
-    __builtin_memcpy(&staged, scale_row + step * STEP_BLOCKS, 8);
+    __builtin_memcpy(staged, scale_row + step * STEP_BLOCKS, sizeof(staged));
   };
   auto load_any = [&](int step) {  // a step beyond the last: none
     if (step >= steps) return;
@@ -348,16 +345,26 @@ __global__ __launch_bounds__(WGM* WGN * 64) void mx_tile_kernel(MxLaunch L, int 
     uint8_t* to = codes[step & 1];
     sa.load_end(to, step * STEP_BLOCKS, blocks, wave, lane);
     sw.load_end(to + BM * STEP_BYTES, step * STEP_BLOCKS, blocks, wave, lane);
-    staged = last_scales(scale_row, step * STEP_BLOCKS, blocks);
+#pragma unroll
+    for (int k = 0; k < WORDS; ++k) {
+      staged[k] = 0;
+#pragma unroll 1
+      for (int i = step * STEP_BLOCKS + 8 * k, n = 0; n < 8 && i + n < blocks; ++n)
+        staged[k] |= uint64_t(scale_row[i + n]) << (8 * n);
+    }
+  };
+  auto put_scales = [&](int buf) {
+#pragma unroll
+    for (int k = 0; k < WORDS; ++k) scales[buf][t][k] = staged[k];
   };
 
   f32x16 acc[TN][TM] = {};
   i32x4 a[2][TM], w[2][TN];
-  int sca[TM], scw[TN], next_sca[TM], next_scw[TN];
+  int sca[TM][WORDS], scw[TN][WORDS], next_sca[TM][WORDS], next_scw[TN][WORDS];
   // operands of instruction step s of `buf`
   auto fetch = [&](int buf, auto s) {
     constexpr int k = s.value;
-    const int slot = ((4 * h + k) ^ swizzle(r)) << 4;
+    const int slot = ((INSTRUCTIONS * h + k) ^ swizzle<STEP_BLOCKS>(r)) << 4;
     const uint8_t* ca = codes[buf] + (wm + r) * STEP_BYTES + slot;
     const uint8_t* cw = codes[buf] + (BM + wn + r) * STEP_BYTES + slot;
 #pragma unroll
@@ -370,16 +377,21 @@ __global__ __launch_bounds__(WGM* WGN * 64) void mx_tile_kernel(MxLaunch L, int 
     each<TN>([&](auto j) {
       each<TM>([&](auto i) {
         acc[j.value][i.value] =
-            wide_product<k, k>(w[k & 1][j.value], a[k & 1][i.value], acc[j.value][i.value], scw[j.value], sca[i.value]);
+            wide_product<k & 3, k & 3>(w[k & 1][j.value], a[k & 1][i.value], acc[j.value][i.value], scw[j.value][k / 4],
+                                       sca[i.value][k / 4]);
       });
     });
   };
   auto fetch_scales = [&](int buf) {
     const int* p = reinterpret_cast<const int*>(scales[buf]);
 #pragma unroll
-    for (int i = 0; i < TM; ++i) next_sca[i] = p[(wm + i * 32 + r) * 2 + h];
+    for (int i = 0; i < TM; ++i)
 #pragma unroll
-    for (int i = 0; i < TN; ++i) next_scw[i] = p[(BM + wn + i * 32 + r) * 2 + h];
+      for (int k = 0; k < WORDS; ++k) next_sca[i][k] = p[((wm + i * 32 + r) * 2 + h) * WORDS + k];
+#pragma unroll
+    for (int i = 0; i < TN; ++i)
+#pragma unroll
+      for (int k = 0; k < WORDS; ++k) next_scw[i][k] = p[((BM + wn + i * 32 + r) * 2 + h) * WORDS + k];
   };
   // One step; LOAD: the step after the next is loaded, 1 full, 2 any; NEXT:
   // there is a next one.  The body of the main loop has no branch: the
@@ -388,23 +400,20 @@ __global__ __launch_bounds__(WGM* WGN * 64) void mx_tile_kernel(MxLaunch L, int 
   auto body = [&](int step, auto LOAD, auto NEXT) {
     const int buf = step & 1;
 #pragma unroll
-    for (int i = 0; i < TM; ++i) sca[i] = next_sca[i];
+    for (int k = 0; k < WORDS; ++k) {
 #pragma unroll
-    for (int i = 0; i < TN; ++i) scw[i] = next_scw[i];
-    fetch(buf, Int<1>{});
-    __builtin_amdgcn_sched_barrier(0);
-    multiply(Int<0>{});
-    __builtin_amdgcn_sched_barrier(0);
-    fetch(buf, Int<2>{});
-    __builtin_amdgcn_sched_barrier(0);
-    multiply(Int<1>{});
-    __builtin_amdgcn_sched_barrier(0);
-    fetch(buf, Int<3>{});
-    __builtin_amdgcn_sched_barrier(0);
-    multiply(Int<2>{});
-    __builtin_amdgcn_sched_barrier(0);
+      for (int i = 0; i < TM; ++i) sca[i][k] = next_sca[i][k];
+#pragma unroll
+      for (int i = 0; i < TN; ++i) scw[i][k] = next_scw[i][k];
+    }
+    each<INSTRUCTIONS - 1>([&](auto s) {
+      fetch(buf, Int<s.value + 1>{});
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(s);
+      __builtin_amdgcn_sched_barrier(0);
+    });
     if constexpr (NEXT.value != 0) {
-      scales[buf ^ 1][t] = staged;
+      put_scales(buf ^ 1);
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's loads into LDS
       __syncthreads();
       if constexpr (LOAD.value == 1) load(step + 2);
@@ -413,11 +422,11 @@ __global__ __launch_bounds__(WGM* WGN * 64) void mx_tile_kernel(MxLaunch L, int 
       fetch_scales(buf ^ 1);
       __builtin_amdgcn_sched_barrier(0);
     }
-    multiply(Int<3>{});
+    multiply(Int<INSTRUCTIONS - 1>{});
     __builtin_amdgcn_sched_barrier(0);
   };
   load_any(0);
-  scales[0][t] = staged;
+  put_scales(0);
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
   load_any(1);
@@ -479,22 +488,38 @@ hipError_t rows_product(const MxLaunch& L, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <int BM, int BN, int WGM, int WGN, typename E>
+template <int BM, int BN, int WGM, int WGN, int DEPTH, typename E>
 hipError_t tile_product(const MxLaunch& L, hipStream_t stream) {
   const int rows = (L.M + BM - 1) / BM, cols = (L.N + BN - 1) / BN;
-  mx_tile_kernel<BM, BN, WGM, WGN, E><<<uint32_t(rows) * uint32_t(cols), WGM * WGN * 64, 0, stream>>>(L, rows, cols);
+  mx_tile_kernel<BM, BN, WGM, WGN, DEPTH, E><<<uint32_t(rows) * uint32_t(cols), WGM * WGN * 64, 0, stream>>>(L, rows, cols);
   return hipGetLastError();
 }
 
+// Which kernel, by the number of workgroups each would have (us for a product
+// of M x N x K with the choice, and with the one it was taken over):
+//   few rows, 16 of them and 16 waves: at most one workgroup per CU
+//     (16 x 4096 x 4096: 4.6, 64 x 64 tiles 6.3; 64 x 1024 x 8192: 6.9, 10.0);
+//   few rows, 32 of them: also up to 448 where the depth is small enough that
+//     reading A in each of them costs little (32 x 4096 x 4096: 5.7, 6.3; 192 x
+//     1111 x 2080: 4.3, 7.1; but 192 x 1024 x 8192: 15.6, 10.3);
+//   64 x 64 tiles, of which a CU holds two: up to 512, in steps of 512, since a
+//     step takes its loads' latency (64 x 4096 x 4096: 6.5, in steps of 256
+//     8.1, 128 x 128 tiles 11.9; 512 x 4096 x 4096: 11.6, 128 x 128 13.0);
+//   128 x 128 tiles: up to 256 in steps of 512, one on a CU (1001 x 4096 x
+//     4096: 15.1, 17.8), else in steps of 256, two on a CU (2048 x 4096 x
+//     4096: 28.3, 31.3);
+//   256 x 256 tiles from 192 on (4096 x 4096 x 4096: 42.7, 52.4; 2048 x 4096 x
+//     4096, 128 of them: 33.1, 28.3).
 template <typename E>
 hipError_t matmul(const MxLaunch& L, hipStream_t stream) {
-  auto tiles = [&](int b) { return int64_t((L.M + b - 1) / b) * ((L.N + b - 1) / b); };
-  if (L.M <= 16) return rows_product<1, 8, E, void>(L, stream);
-  if (L.M <= 32) return rows_product<2, 8, E, void>(L, stream);
-  if (L.M <= 64) return rows_product<4, 8, E, void>(L, stream);
-  if (tiles(256) >= 192) return tile_product<256, 256, 2, 4, E>(L, stream);
-  if (tiles(128) >= 192) return tile_product<128, 128, 2, 2, E>(L, stream);
-  return tile_product<64, 64, 2, 2, E>(L, stream);
+  auto count = [&](int64_t m, int64_t n) { return (L.M + m - 1) / m * ((L.N + n - 1) / n); };
+  if (count(16, 16) <= 256) return rows_product<1, 16, E, void>(L, stream);
+  const int64_t rows = count(32, 16);
+  if (rows <= 256 || (rows <= 448 && rows * L.K <= 1 << 20)) return rows_product<2, 8, E, void>(L, stream);
+  if (count(64, 64) <= 512) return tile_product<64, 64, 2, 2, 512, E>(L, stream);
+  if (count(256, 256) >= 192) return tile_product<256, 256, 2, 4, 256, E>(L, stream);
+  if (count(128, 128) <= 256) return tile_product<128, 128, 2, 2, 512, E>(L, stream);
+  return tile_product<128, 128, 2, 2, 256, E>(L, stream);
 }
 
 }  // namespace
@@ -524,8 +549,8 @@ constexpr int FUSED_ROWS = 16;
 
 hipError_t launch_mx_linear(const MxLaunch& L, hipStream_t stream) {
   if (L.M <= FUSED_ROWS) {
-    if (L.in_bf16) return L.out_bf16 ? rows_product<1, 8, bf16, bf16>(L, stream) : rows_product<1, 8, float, bf16>(L, stream);
-    return L.out_bf16 ? rows_product<1, 8, bf16, float>(L, stream) : rows_product<1, 8, float, float>(L, stream);
+    if (L.in_bf16) return L.out_bf16 ? rows_product<1, 16, bf16, bf16>(L, stream) : rows_product<1, 16, float, bf16>(L, stream);
+    return L.out_bf16 ? rows_product<1, 16, bf16, float>(L, stream) : rows_product<1, 16, float, float>(L, stream);
   }
   if (hipError_t e = launch_mx_quantize(L.x, L.M, L.K, L.in_bf16, const_cast<uint8_t*>(L.a_codes),
                                         const_cast<uint8_t*>(L.a_scales), stream))

@@ -40,7 +40,8 @@ constexpr bool by_group() { return TEAM != BLOCK && TEAM >= 16; }
 template <int TEAM>
 __device__ __forceinline__ int team_size() { return TEAM == BLOCK ? int(blockDim.x) : TEAM; }
 
-// f(z) and f'(z)
+// f(z) and f'(z); E: the type of the call.
+template <typename E>
 __device__ __forceinline__ void activation(int act, float z, float& f, float& df) {
   if (act == GDNQ_ACT_NONE) {
     f = z;
@@ -48,7 +49,7 @@ __device__ __forceinline__ void activation(int act, float z, float& f, float& df
     return;
   }
   float p, q;
-  sigmoid_pair(z, p, q);
+  sigmoid_pair<E>(z, p, q);
   f = act == GDNQ_ACT_SILU ? z * p : p;
   df = act == GDNQ_ACT_SILU ? p * fmaf(z, q, 1.0f) : p * q;
 }
@@ -200,7 +201,7 @@ __global__ __launch_bounds__(bounds<TEAM>()) void norm_forward_kernel(NormLaunch
       for (int j = 0; j < 8; ++j) {
         const float n = fmaf(v[e][j] * rstd, w[e][j], b[e][j]);
         float f, df;
-        activation(L.act, gates ? to_f32(g[e].v[j]) : n, f, df);
+        activation<E>(L.act, gates ? to_f32(g[e].v[j]) : n, f, df);
         x[e].v[j] = E(gates ? n * f : f);
       }
       x[e].store(static_cast<E*>(L.y) + u * D, l, e, D);
@@ -256,7 +257,7 @@ __global__ __launch_bounds__(bounds<TEAM>()) void norm_backward_kernel(NormLaunc
       for (int j = 0; j < 8; ++j) {
         const float hat = v[e][j] * rstd, n = fmaf(hat, w[e][j], b[e][j]), y = to_f32(dy[e].v[j]);  // outside the group dy = 0
         float f, df;
-        activation(L.act, L.gate ? to_f32(g[e].v[j]) : n, f, df);
+        activation<E>(L.act, L.gate ? to_f32(g[e].v[j]) : n, f, df);
         const float dn = y * (L.gate ? f : df);
         if (L.gate) g[e].v[j] = E(y * n * df);
         dw[e][j] = fmaf(dn, hat, dw[e][j]);
@@ -321,8 +322,10 @@ __global__ __launch_bounds__(1024) void norm_params_kernel(const float* __restri
   const int i = threadIdx.x & 15, r = threadIdx.x >> 4;
   const int64_t c = blockIdx.x * int64_t(16) + i;
   float s = 0.0f;
-  if (c < cols)
+  if (c < cols) {
+#pragma unroll 8
     for (int64_t row = r; row < rows; row += 64) s += partial[row * cols + c];
+  }
   part[r][i] = s;
   __syncthreads();
   for (int n = 32; n > 0; n >>= 1) {

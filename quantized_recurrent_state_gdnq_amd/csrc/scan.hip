@@ -110,7 +110,7 @@ struct Gates<E, V, true> {
   __device__ __forceinline__ void load(const E* p) { g.load(p); }
   __device__ __forceinline__ void settle() {
 #pragma unroll
-    for (int i = 0; i < V; ++i) t[i] = sigmoid_tail(g.get(i));
+    for (int i = 0; i < V; ++i) t[i] = sigmoid_tail<E>(g.get(i));
   }
   __device__ __forceinline__ void get(int i, float& a, float& keep) const { sigmoid_of_tail(t[i], a, keep); }
   // Between walks: the compiler would keep a and b of every token from the

@@ -19,20 +19,30 @@ __device__ __forceinline__ void store_f32(bf16* p, float x) { *p = bf16(x); }
 
 // The smaller of p = sigmoid(z) and q = 1 - p, with the sign of z: with
 // u = e^-|z| it is u / (1 + u), and the larger is formed as one minus it, so
-// neither cancels and both are good to a few units in the last place.  The
-// hardware's 2^x takes -|z| log2(e) in two parts (product and its rounding
-// error), its reciprocal one Newton step.
+// neither cancels.  E is the type z was stored in.
+//   fp32: good to a few units in the last place: the hardware's 2^x takes
+// -|z| log2(e) in two parts (product and its rounding error), its reciprocal
+// one Newton step.
+//   bf16: neither, 12 instruction slots instead of 21 (2^x and the reciprocal
+// are four each): off by up to |z| 2^-24 and a few units, where the results
+// are rounded to 2^-8 or are sums of many such terms.
+template <typename E>
 __device__ __forceinline__ float sigmoid_tail(float z) {
-  float m = -fabsf(z);
-  m = m < -128.0f ? -128.0f : m;  // u is 0 from -104 on (infinities, the type's lowest value); NaN passes
-  const float t = m * 1.44269504f;
-  const float low = fmaf(m, 1.44269504f, -t) + m * 1.92596299e-8f;  // log2(e) = 1.44269504 + 1.926e-8
-  const float e = __builtin_amdgcn_exp2f(t);
-  const float u = fmaf(e, low * 0.693147181f, e);
-  const float d = 1.0f + u;
-  float r = __builtin_amdgcn_rcpf(d);
-  r = fmaf(fmaf(-d, r, 1.0f), r, r);
-  return copysignf(u * r, z);
+  if constexpr (sizeof(E) == 2) {
+    const float u = __builtin_amdgcn_exp2f(-fabsf(z) * 1.44269504f);
+    return copysignf(u * __builtin_amdgcn_rcpf(1.0f + u), z);
+  } else {
+    float m = -fabsf(z);
+    m = m < -128.0f ? -128.0f : m;  // u is 0 from -104 on (infinities, the type's lowest value); NaN passes
+    const float t = m * 1.44269504f;
+    const float low = fmaf(m, 1.44269504f, -t) + m * 1.92596299e-8f;  // log2(e) = 1.44269504 + 1.926e-8
+    const float e = __builtin_amdgcn_exp2f(t);
+    const float u = fmaf(e, low * 0.693147181f, e);
+    const float d = 1.0f + u;
+    float r = __builtin_amdgcn_rcpf(d);
+    r = fmaf(fmaf(-d, r, 1.0f), r, r);
+    return copysignf(u * r, z);
+  }
 }
 
 __device__ __forceinline__ void sigmoid_of_tail(float t, float& p, float& q) {
@@ -43,6 +53,9 @@ __device__ __forceinline__ void sigmoid_of_tail(float t, float& p, float& q) {
 }
 
 // p = sigmoid(z) and q = 1 - p.
-__device__ __forceinline__ void sigmoid_pair(float z, float& p, float& q) { sigmoid_of_tail(sigmoid_tail(z), p, q); }
+template <typename E>
+__device__ __forceinline__ void sigmoid_pair(float z, float& p, float& q) {
+  sigmoid_of_tail(sigmoid_tail<E>(z), p, q);
+}
 
 }  // namespace gdnq

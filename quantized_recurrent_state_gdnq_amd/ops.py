@@ -576,10 +576,16 @@ def _launch(dev, fn, *args):
             _lib.check(fn(*args, stream))
 
 
+def _checked(t, name, dtype, device, shape):
+    """A tensor of exactly this type, device and shape, contiguous (one test
+    where all holds: a call makes a few of these)."""
+    if t is not None and t.dtype == dtype and t.device == device and t.shape == shape and t.is_contiguous():
+        return t
+    return _shape(_need(t, name, dtype, device), shape, name)
+
+
 def _optional(t, name, dtype, device, shape):
-    if t is not None:
-        _shape(_need(t, name, dtype, device), shape, name)
-    return t
+    return None if t is None else _checked(t, name, dtype, device, shape)
 
 
 def _space(workspace, need, dev):
@@ -611,7 +617,7 @@ def _scan_setup(x, gate, cu_seqlens, logits, lerp):
             raise ValueError("x must be [T,C] with cu_seqlens")
         B, (T, C) = cu_seqlens.numel() - 1, x.shape
         n = T
-    _shape(_need(gate, "gate", x.dtype, dev), x.shape, "gate")
+    _checked(gate, "gate", x.dtype, dev, x.shape)
     p = _lib.ScanParams(B, T, C, _DT[x.dtype], (_lib.GDNQ_SCAN_LOGITS if logits else 0)
                         | (_lib.GDNQ_SCAN_LERP if lerp else 0))
     return p, B, C, (-(-n // _lib.GDNQ_SCAN_CHUNK), C)
@@ -641,10 +647,10 @@ def gated_scan(x, gate, h0=None, cu_seqlens=None, *, logits=False, lerp=False, s
     dev = x.device
     _optional(h0, "h0", torch.float32, dev, (B, C))
     # a packed call may hold tokens that no sequence covers: only a given y has values there
-    y = torch.empty_like(x) if y is None else _shape(_need(y, "y", x.dtype, dev), x.shape, "y")
+    y = torch.empty_like(x) if y is None else _checked(y, "y", x.dtype, dev, x.shape)
     if h_last is None:
         h_last = torch.empty((B, C), dtype=torch.float32, device=dev)
-    _shape(_need(h_last, "h_last", torch.float32, dev), (B, C), "h_last")
+    _checked(h_last, "h_last", torch.float32, dev, (B, C))
     if carry is None and save:
         carry = torch.empty(cshape, dtype=torch.float32, device=dev)
     _optional(carry, "carry", torch.float32, dev, cshape)
@@ -661,12 +667,12 @@ def gated_scan_backward(dy, x, gate, carry, h0=None, dh_last=None, cu_seqlens=No
     Returns (dx, dgate, dh0); dh0 is None when h0 is and no dh0 was given."""
     p, B, C, cshape = _scan_setup(x, gate, cu_seqlens, logits, lerp)
     dev = x.device
-    _shape(_need(dy, "dy", x.dtype, dev), x.shape, "dy")
-    _shape(_need(carry, "carry", torch.float32, dev), cshape, "carry")
+    _checked(dy, "dy", x.dtype, dev, x.shape)
+    _checked(carry, "carry", torch.float32, dev, cshape)
     _optional(h0, "h0", torch.float32, dev, (B, C))
     _optional(dh_last, "dh_last", torch.float32, dev, (B, C))
-    dx = torch.empty_like(x) if dx is None else _shape(_need(dx, "dx", x.dtype, dev), x.shape, "dx")
-    dgate = torch.empty_like(x) if dgate is None else _shape(_need(dgate, "dgate", x.dtype, dev), x.shape, "dgate")
+    dx = torch.empty_like(x) if dx is None else _checked(dx, "dx", x.dtype, dev, x.shape)
+    dgate = torch.empty_like(x) if dgate is None else _checked(dgate, "dgate", x.dtype, dev, x.shape)
     if dh0 is None and h0 is not None:
         dh0 = torch.empty((B, C), dtype=torch.float32, device=dev)
     _optional(dh0, "dh0", torch.float32, dev, (B, C))
@@ -685,10 +691,10 @@ def gated_scan_step(x, gate, h, *, logits=False, lerp=False, h_out=None, y=None)
         raise ValueError("x must be float32 or bfloat16")
     if x.dim() != 2:
         raise ValueError("x must be [B,C]")
-    _shape(_need(gate, "gate", x.dtype, dev), x.shape, "gate")
-    _shape(_need(h, "h", torch.float32, dev), x.shape, "h")
-    h_out = h if h_out is None else _shape(_need(h_out, "h_out", torch.float32, dev), x.shape, "h_out")
-    y = torch.empty_like(x) if y is None else _shape(_need(y, "y", x.dtype, dev), x.shape, "y")
+    _checked(gate, "gate", x.dtype, dev, x.shape)
+    _checked(h, "h", torch.float32, dev, x.shape)
+    h_out = h if h_out is None else _checked(h_out, "h_out", torch.float32, dev, x.shape)
+    y = torch.empty_like(x) if y is None else _checked(y, "y", x.dtype, dev, x.shape)
     p = _lib.ScanParams(x.shape[0], 1, x.shape[1], _DT[x.dtype], (_lib.GDNQ_SCAN_LOGITS if logits else 0)
                         | (_lib.GDNQ_SCAN_LERP if lerp else 0))
     _launch(dev, _lib.scan_step, p, _ptr(x), _ptr(gate), _ptr(h), _ptr(h_out), _ptr(y))
@@ -716,7 +722,7 @@ def _norm_setup(x, weight, bias, gate, act, center, eps):
                 raise ValueError(f"{name} must have shape {(D,)} or {(G, D)} (both alike), got {tuple(t.shape)}")
             shape = tuple(t.shape)
     if gate is not None:
-        _shape(_need(gate, "gate", x.dtype, dev), x.shape, "gate")
+        _checked(gate, "gate", x.dtype, dev, x.shape)
     shape = shape or (G, D)
     rows = 1
     for s in x.shape[:-2]:
@@ -734,7 +740,7 @@ def group_norm(x, weight=None, bias=None, gate=None, *, act="none", center=False
     "none", "silu" or "sigmoid").  center=False: root-mean-square norm."""
     p, _ = _norm_setup(x, weight, bias, gate, act, center, eps)
     dev = x.device
-    y = torch.empty_like(x) if y is None else _shape(_need(y, "y", x.dtype, dev), x.shape, "y")
+    y = torch.empty_like(x) if y is None else _checked(y, "y", x.dtype, dev, x.shape)
     _launch(dev, _lib.group_norm, p, _ptr(x), _ptr(gate), _ptr(weight), _ptr(bias), _ptr(y))
     return y
 
@@ -755,11 +761,11 @@ def group_norm_backward(dy, x, weight=None, bias=None, gate=None, *, act="none",
     fp32, shaped like weight and bias."""
     p, shape = _norm_setup(x, weight, bias, gate, act, center, eps)
     dev = x.device
-    _shape(_need(dy, "dy", x.dtype, dev), x.shape, "dy")
-    dx = torch.empty_like(x) if dx is None else _shape(_need(dx, "dx", x.dtype, dev), x.shape, "dx")
+    _checked(dy, "dy", x.dtype, dev, x.shape)
+    dx = torch.empty_like(x) if dx is None else _checked(dx, "dx", x.dtype, dev, x.shape)
     if gate is not None:
         dgate = torch.empty_like(x) if dgate is None else dgate
-        _shape(_need(dgate, "dgate", x.dtype, dev), x.shape, "dgate")
+        _checked(dgate, "dgate", x.dtype, dev, x.shape)
     elif dgate is not None:
         raise ValueError("dgate: the call has no gate")
     if weight is not None and dweight is None:
@@ -805,8 +811,8 @@ def mx_quantize(x, codes=None, scales=None):
     cshape, sshape = x.shape[:-1] + (depth // 2,), x.shape[:-1] + (depth // 32,)
     codes = torch.empty(cshape, dtype=torch.uint8, device=dev) if codes is None else codes
     scales = torch.empty(sshape, dtype=torch.uint8, device=dev) if scales is None else scales
-    _shape(_need(codes, "codes", torch.uint8, dev), cshape, "codes")
-    _shape(_need(scales, "scales", torch.uint8, dev), sshape, "scales")
+    _checked(codes, "codes", torch.uint8, dev, cshape)
+    _checked(scales, "scales", torch.uint8, dev, sshape)
     _launch(dev, _lib.mx_quantize, _ptr(x), _mx_rows(x), depth, _DT[x.dtype], _ptr(codes), _ptr(scales))
     return codes, scales
 
@@ -821,7 +827,7 @@ def _mx_out(y, lead, cols, out_dtype, dev):
         raise ValueError("out_dtype must be float32 or bfloat16")
     if y is None:
         return torch.empty(lead + (cols,), dtype=out_dtype, device=dev)
-    return _shape(_need(y, "y", out_dtype, dev), lead + (cols,), "y")
+    return _checked(y, "y", out_dtype, dev, lead + (cols,))
 
 
 def mx_matmul(a_codes, a_scales, w_codes, w_scales, *, out_dtype=torch.bfloat16, y=None, workspace=None):
@@ -833,7 +839,7 @@ def mx_matmul(a_codes, a_scales, w_codes, w_scales, *, out_dtype=torch.bfloat16,
         raise ValueError("a_codes must be [..,depth/2]")
     depth = a_codes.shape[-1] * 2
     lead = a_codes.shape[:-1]
-    _shape(_need(a_scales, "a_scales", torch.uint8, dev), lead + (depth // 32,), "a_scales")
+    _checked(a_scales, "a_scales", torch.uint8, dev, lead + (depth // 32,))
     _mx_weights(w_codes, w_scales, depth, dev)
     y = _mx_out(y, lead, w_codes.shape[0], out_dtype, dev)
     p = _lib.MxParams(_mx_rows(a_codes), w_codes.shape[0], depth, 0, _DT[out_dtype], 0)

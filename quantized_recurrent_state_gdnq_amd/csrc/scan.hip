@@ -72,6 +72,8 @@ struct Cell<bf16, 2> {
   uint32_t w;
   __device__ __forceinline__ void load(const bf16* p) { w = *reinterpret_cast<const uint32_t*>(p); }
   __device__ __forceinline__ float get(int i) const { return i ? bf16_hi(w) : bf16_lo(w); }
+  // Between walks: the compiler would keep both values apart, in two registers.
+  __device__ __forceinline__ void forget() { asm volatile("" : "+v"(w)); }
   __device__ static __forceinline__ void store(bf16* p, const float (&v)[2]) {
     *reinterpret_cast<bf16x2*>(p) = __builtin_convertvector(f32x2{v[0], v[1]}, bf16x2);
   }
@@ -81,6 +83,7 @@ struct Cell<E, 1> {
   E w;
   __device__ __forceinline__ void load(const E* p) { w = *p; }
   __device__ __forceinline__ float get(int) const { return to_f32(w); }
+  __device__ __forceinline__ void forget() {}
   __device__ static __forceinline__ void store(E* p, const float (&v)[1]) { store_f32(p, v[0]); }
 };
 
@@ -127,7 +130,31 @@ struct Rows {
   uint32_t valid, start, end;
   int seq;
   __device__ __forceinline__ int seq_of(int r) const { return __builtin_amdgcn_readlane(seq, r); }
+  // All of them in the middle of one sequence.
+  template <int RUN>
+  __device__ __forceinline__ bool plain() const {
+    return valid == uint32_t((uint64_t(1) << RUN) - 1) && (start | end) == 0;
+  }
 };
+
+// f(Plain or Mixed): most runs are plain, and their walks need no question per
+// token, whose branches cost as much as the arithmetic (32768 x 2048 bf16: 98
+// us, 114 with them).  With gates from logits the two kinds of walk together
+// keep more values in registers than there are, and spill (156 us against
+// 112), so there all are Mixed.
+struct Plain {
+  static constexpr bool value = true;
+};
+struct Mixed {
+  static constexpr bool value = false;
+};
+template <bool LOGITS, typename F>
+__device__ __forceinline__ void by_kind(bool plain, F&& f) {
+  if constexpr (!LOGITS) {
+    if (plain) return f(Plain{});
+  }
+  f(Mixed{});
+}
 
 // The last offset that is <= row among cu[0..B] (-1: none).
 __device__ __forceinline__ int sequence_at(const int32_t* cu, int B, int row) {
@@ -343,13 +370,17 @@ __global__ __launch_bounds__(ForwardShape<V>::WAVES * 64, ForwardShape<V>::PER_S
 
   Cell<E, V> x[RUN];
   Gates<E, V, LOGITS> g[RUN];
+  const int cl = active ? c : 0, last = int(L.N) - 1;
 #pragma unroll
   for (int r = 0; r < RUN; ++r) {
-    if (active && row0 + r < L.N) {
-      const int64_t at = int64_t(row0 + r) * C;  // the wave's: lanes differ in the channel alone
-      x[r].load(xs + at + c);
-      g[r].load(gates + at + c);
-    }
+    // Lanes differ in the channel alone.  Plain walks wait for one token's loads
+    // at a time, if no branch parts them: beyond the end these read the last
+    // token.  Under a branch they are issued a token at a time, which Mixed
+    // walks take better (prefill with logits 113 us, 119 without the branch).
+    if (LOGITS && row0 + r > last) continue;
+    const int64_t at = int64_t(min(row0 + r, last)) * C;
+    x[r].load(xs + at + cl);
+    g[r].load(gates + at + cl);
   }
   int first;
   const Rows rows = rows_of<RUN>(cu, L.B, L.T, L.N, row0, lane, first);
@@ -361,32 +392,39 @@ __global__ __launch_bounds__(ForwardShape<V>::WAVES * 64, ForwardShape<V>::PER_S
     A[i] = 1.0f;
     H[i] = 0.0f;
   }
-#pragma unroll
-  for (int r = 0; r < RUN; ++r) {
-    if (!(rows.valid >> r & 1)) continue;
-    float a[V], b[V];
-    g[r].settle();
+  // a and b of token r of the run
+  auto input = [&](int r, float (&a)[V], float (&b)[V]) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       float keep;
       g[r].get(i, a[i], keep);
       b[i] = LERP ? keep * x[r].get(i) : x[r].get(i);
     }
-    if (rows.start >> r & 1) {
-      if (active) add_h0<V>(L.h0, rows.seq_of(r), C, c, a, b);
+  };
+  auto fold_run = [&](auto PLAIN) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        A[i] = 0.0f;
-        H[i] = b[i];
-      }
-    } else {
+    for (int r = 0; r < RUN; ++r) {
+      if (!PLAIN.value && !(rows.valid >> r & 1)) continue;
+      float a[V], b[V];
+      g[r].settle();
+      input(r, a, b);
+      if (!PLAIN.value && (rows.start >> r & 1)) {
+        if (active) add_h0<V>(L.h0, rows.seq_of(r), C, c, a, b);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        H[i] = fmaf(a[i], H[i], b[i]);
-        A[i] *= a[i];
+        for (int i = 0; i < V; ++i) {
+          A[i] = 0.0f;
+          H[i] = b[i];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          H[i] = fmaf(a[i], H[i], b[i]);
+          A[i] *= a[i];
+        }
       }
     }
-  }
+  };
+  by_kind<LOGITS>(rows.template plain<RUN>(), fold_run);
   put<V>(&wave_pair[wave][lane * V], A, H);
   if (lane == 0) borders[wave] = rows.start;
   __syncthreads();
@@ -427,33 +465,32 @@ __global__ __launch_bounds__(ForwardShape<V>::WAVES * 64, ForwardShape<V>::PER_S
   }
   E* ys = static_cast<E*>(L.y);
 #pragma unroll
-  for (int r = 0; r < RUN; ++r) g[r].forget();
-#pragma unroll
   for (int r = 0; r < RUN; ++r) {
-    if (!(rows.valid >> r & 1)) continue;
-    float a[V], b[V];
+    g[r].forget();
+    if (!LOGITS) x[r].forget();
+  }
+  auto write_run = [&](auto PLAIN) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      float keep;
-      g[r].get(i, a[i], keep);
-      b[i] = LERP ? keep * x[r].get(i) : x[r].get(i);
-    }
-    if (rows.start >> r & 1) {
-      if (active) add_h0<V>(L.h0, rows.seq_of(r), C, c, a, b);
+    for (int r = 0; r < RUN; ++r) {
+      if (!PLAIN.value && !(rows.valid >> r & 1)) continue;
+      float a[V], b[V];
+      input(r, a, b);
+      if (!PLAIN.value && (rows.start >> r & 1)) {
+        add_h0<V>(L.h0, rows.seq_of(r), C, c, a, b);
 #pragma unroll
-      for (int i = 0; i < V; ++i) h[i] = b[i];
-    } else {
+        for (int i = 0; i < V; ++i) h[i] = b[i];
+      } else {
 #pragma unroll
-      for (int i = 0; i < V; ++i) h[i] = fmaf(a[i], h[i], b[i]);
-    }
-    if (active) {
+        for (int i = 0; i < V; ++i) h[i] = fmaf(a[i], h[i], b[i]);
+      }
       Cell<E, V>::store(ys + int64_t(row0 + r) * C + c, h);
-      if (L.h_last && (rows.end >> r & 1)) {
+      if (!PLAIN.value && L.h_last && (rows.end >> r & 1)) {
 #pragma unroll
         for (int i = 0; i < V; ++i) L.h_last[int64_t(rows.seq_of(r)) * C + c + i] = h[i];
       }
     }
-  }
+  };
+  if (active) by_kind<LOGITS>(rows.template plain<RUN>(), write_run);
 }
 
 // The backward pass runs the chain from the last chunk to the first with
@@ -480,20 +517,18 @@ __global__ __launch_bounds__(BWD_WAVES * 64, BWD_PER_SIMD) void scan_backward_ke
 
   Cell<E, V> x[RUN], dy[RUN];
   Gates<E, V, LOGITS> g[RUN];
+  const int cl = active ? c : 0, last = int(L.N) - 1;
 #pragma unroll
-  for (int r = 0; r < RUN; ++r) {
-    if (active && row0 + r < L.N) {
-      const int64_t at = int64_t(row0 + r) * C;  // the wave's: lanes differ in the channel alone
-      x[r].load(xs + at + c);
-      g[r].load(gates + at + c);
-      dy[r].load(dys + at + c);
-    }
+  for (int r = 0; r < RUN; ++r) {  // as in the forward pass
+    if (LOGITS && row0 + r > last) continue;
+    const int64_t at = int64_t(min(row0 + r, last)) * C;
+    x[r].load(xs + at + cl);
+    g[r].load(gates + at + cl);
+    dy[r].load(dys + at + cl);
   }
-  float h_in[V] = {};
-  if (active && row0 < L.N) {
+  float h_in[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) h_in[i] = L.carry[int64_t(chunk) * C + c + i];
-  }
+  for (int i = 0; i < V; ++i) h_in[i] = L.carry[int64_t(chunk) * C + cl + i];
   int first;
   const Rows rows = rows_of<RUN>(cu, L.B, L.T, L.N, row0, lane, first);
   if (threadIdx.x == WAVES * 64 - 64) {
@@ -518,51 +553,65 @@ __global__ __launch_bounds__(BWD_WAVES * 64, BWD_PER_SIMD) void scan_backward_ke
     A[i] = 1.0f;
     H[i] = M[i] = 0.0f;
   }
+  // m behind a sequence's last token
+  auto last_gradient = [&](int r, float (&m)[V]) {
 #pragma unroll
-  for (int r = 0; r < RUN; ++r) {
-    if (!(rows.valid >> r & 1)) continue;
-    float a[V], b[V];
-    g[r].settle();
+    for (int i = 0; i < V; ++i) m[i] = L.dh_last ? L.dh_last[int64_t(rows.seq_of(r)) * C + cl + i] : 0.0f;
+  };
+  // a and b of token r of the run
+  auto input = [&](int r, float (&a)[V], float (&b)[V]) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       float keep;
       g[r].get(i, a[i], keep);
       b[i] = LERP ? keep * x[r].get(i) : x[r].get(i);
     }
-    if (rows.start >> r & 1) {
-      if (active) add_h0<V>(L.h0, rows.seq_of(r), C, c, a, b);
+  };
+  auto fold_run = [&](auto PLAIN) {
+#pragma unroll
+    for (int r = 0; r < RUN; ++r) {
+      if (!PLAIN.value && !(rows.valid >> r & 1)) continue;
+      float a[V], b[V];
+      g[r].settle();
+      input(r, a, b);
+      if (!PLAIN.value && (rows.start >> r & 1)) {
+        if (active) add_h0<V>(L.h0, rows.seq_of(r), C, c, a, b);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          A[i] = 0.0f;
+          H[i] = b[i];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          H[i] = fmaf(a[i], H[i], b[i]);
+          A[i] *= a[i];
+        }
+      }
+    }
+  };
+  by_kind<LOGITS>(rows.template plain<RUN>(), fold_run);
+  auto fold_back = [&](auto PLAIN) {
+#pragma unroll
+    for (int r = RUN - 1; r >= 0; --r) {
+      if constexpr (!PLAIN.value) {
+        if (!(rows.valid >> r & 1)) continue;
+        if (rows.start >> r & 1) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) M[i] = 0.0f;
+          continue;
+        }
+        if (rows.end >> r & 1) last_gradient(r, M);
+      }
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        A[i] = 0.0f;
-        H[i] = b[i];
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        H[i] = fmaf(a[i], H[i], b[i]);
-        A[i] *= a[i];
+        float a, keep;
+        g[r].get(i, a, keep);
+        M[i] = a * (dy[r].get(i) + M[i]);
       }
     }
-  }
-#pragma unroll
-  for (int r = RUN - 1; r >= 0; --r) {
-    if (!(rows.valid >> r & 1)) continue;
-    if (rows.start >> r & 1) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) M[i] = 0.0f;
-      continue;
-    }
-    if ((rows.end >> r & 1)) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) M[i] = L.dh_last && active ? L.dh_last[int64_t(rows.seq_of(r)) * C + c + i] : 0.0f;
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      float a, keep;
-      g[r].get(i, a, keep);
-      M[i] = a * (dy[r].get(i) + M[i]);
-    }
-  }
+  };
+  by_kind<LOGITS>(rows.template plain<RUN>(), fold_back);
   put<V>(&wave_pair[wave][lane * V], A, H);
   // a border behind the run's last token is a border of m too, but not of h
   const bool border = rows.start != 0 || rows.end != 0;
@@ -611,52 +660,58 @@ __global__ __launch_bounds__(BWD_WAVES * 64, BWD_PER_SIMD) void scan_backward_ke
 
   float before[RUN][V];
 #pragma unroll
-  for (int r = 0; r < RUN; ++r) g[r].forget();
-#pragma unroll
   for (int r = 0; r < RUN; ++r) {
-    if (!(rows.valid >> r & 1)) continue;
-    if (rows.start >> r & 1) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) h_in[i] = L.h0 && active ? L.h0[int64_t(rows.seq_of(r)) * C + c + i] : 0.0f;
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      before[r][i] = h_in[i];
-      float a, keep;
-      g[r].get(i, a, keep);
-      h_in[i] = fmaf(a, h_in[i], LERP ? keep * x[r].get(i) : x[r].get(i));
-    }
+    g[r].forget();
+    if (!LOGITS) x[r].forget();
+    if (!LOGITS) dy[r].forget();
   }
   E* dxs = static_cast<E*>(L.dx);
   E* dgs = static_cast<E*>(L.dgate);
+  auto write_run = [&](auto PLAIN) {
 #pragma unroll
-  for (int r = RUN - 1; r >= 0; --r) {
-    if (!(rows.valid >> r & 1)) continue;
-    if (rows.end >> r & 1) {
+    for (int r = 0; r < RUN; ++r) {
+      if constexpr (!PLAIN.value) {
+        if (!(rows.valid >> r & 1)) continue;
+        if (rows.start >> r & 1) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) m[i] = L.dh_last && active ? L.dh_last[int64_t(rows.seq_of(r)) * C + c + i] : 0.0f;
+          for (int i = 0; i < V; ++i) h_in[i] = L.h0 ? L.h0[int64_t(rows.seq_of(r)) * C + c + i] : 0.0f;
+        }
+      }
+      float a[V], b[V];
+      input(r, a, b);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        before[r][i] = h_in[i];
+        h_in[i] = fmaf(a[i], h_in[i], b[i]);
+      }
     }
-    float dx[V], dg[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      float a, keep;
-      g[r].get(i, a, keep);
-      const float lam = dy[r].get(i) + m[i];
-      const float da = lam * (LERP ? before[r][i] - x[r].get(i) : before[r][i]);
-      dx[i] = LERP ? keep * lam : lam;
-      dg[i] = LOGITS ? da * (a * keep) : da;
-      m[i] = a * lam;
-    }
-    if (active) {
+    for (int r = RUN - 1; r >= 0; --r) {
+      if constexpr (!PLAIN.value) {
+        if (!(rows.valid >> r & 1)) continue;
+        if (rows.end >> r & 1) last_gradient(r, m);
+      }
+      float dx[V], dg[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        float a, keep;
+        g[r].get(i, a, keep);
+        const float lam = dy[r].get(i) + m[i];
+        const float da = lam * (LERP ? before[r][i] - x[r].get(i) : before[r][i]);
+        dx[i] = LERP ? keep * lam : lam;
+        dg[i] = LOGITS ? da * (a * keep) : da;
+        m[i] = a * lam;
+      }
       const int64_t at = int64_t(row0 + r) * C + c;
       Cell<E, V>::store(dxs + at, dx);
       Cell<E, V>::store(dgs + at, dg);
-      if (L.dh0 && (rows.start >> r & 1)) {
+      if (!PLAIN.value && L.dh0 && (rows.start >> r & 1)) {
 #pragma unroll
         for (int i = 0; i < V; ++i) L.dh0[int64_t(rows.seq_of(r)) * C + c + i] = m[i];
       }
     }
-  }
+  };
+  if (active) by_kind<LOGITS>(rows.template plain<RUN>(), write_run);
 }
 
 // What has to be done before the pass: the chain is emptied (tickets 0, pairs

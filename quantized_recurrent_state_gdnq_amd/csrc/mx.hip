@@ -277,9 +277,11 @@ struct Stage {
   }
   // Loads the step from block k0 on to LDS at `to`.
   __device__ __forceinline__ void load(uint8_t* to, int k0, int wave) const {
-    const uint8_t* from = base + int64_t(k0) * 16;
 #pragma unroll
-    for (int i = 0; i < LOADS; ++i) to_lds(from, at[i], to + (i * (THREADS / 64) + wave) * 1024);
+    for (int i = 0; i < LOADS; ++i) load_one(to, k0, wave, i);
+  }
+  __device__ __forceinline__ void load_one(uint8_t* to, int k0, int wave, int i) const {
+    to_lds(base + int64_t(k0) * 16, at[i], to + (i * (THREADS / 64) + wave) * 1024);
   }
   // The same where the depth ends inside the step.
   __device__ __forceinline__ void load_end(uint8_t* to, int k0, int blocks, int wave, int lane) const {
@@ -305,7 +307,8 @@ __global__ __launch_bounds__(WGM* WGN * 64) void mx_tile_kernel(MxLaunch L, int 
   constexpr int STEP_BYTES = DEPTH / 2, STEP_BLOCKS = DEPTH / 32;  // of a row
   constexpr int INSTRUCTIONS = STEP_BLOCKS / 2, WORDS = STEP_BLOCKS / 8;  // of a step; a half's words of scales
   static_assert(BM * BN <= (BM + BN) * STEP_BYTES, "the results of a pass fit the two buffers");
-  static_assert(THREADS % (BM + BN) == 0, "a thread stages a row's scales");
+  constexpr int SCALE_ROWS = BM + BN > THREADS ? (BM + BN) / THREADS : 1;  // that a thread stages
+  static_assert((SCALE_ROWS * THREADS) % (BM + BN) == 0, "every row's scales are staged");
   __shared__ __attribute__((aligned(1024))) uint8_t codes[2][(BM + BN) * STEP_BYTES];
   __shared__ uint64_t scales[2][BM + BN][WORDS];
 
@@ -327,60 +330,63 @@ __global__ __launch_bounds__(WGM* WGN * 64) void mx_tile_kernel(MxLaunch L, int 
   Stage<BN, STEP_BLOCKS, THREADS> sw;
   sa.init(L.a_codes, m0, L.M, row_bytes, wave, lane);
   sw.init(L.w_codes, n0, L.N, row_bytes, wave, lane);
-  // thread t stages the scales of row t of A's tile, then of W's
+  // thread t stages the scales of rows t, t + THREADS .. of A's tile, then W's
   const int t = threadIdx.x % (BM + BN);
-  const uint8_t* scale_row = t < BM ? L.a_scales + int64_t(min(m0 + t, L.M - 1)) * blocks
-                                    : L.w_scales + int64_t(min(n0 + t - BM, L.N - 1)) * blocks;
+  const uint8_t* scale_row[SCALE_ROWS];
+#pragma unroll
+  for (int q = 0; q < SCALE_ROWS; ++q) {
+    const int row = t + q * THREADS;
+    scale_row[q] = row < BM ? L.a_scales + int64_t(min(m0 + row, L.M - 1)) * blocks
+                            : L.w_scales + int64_t(min(n0 + row - BM, L.N - 1)) * blocks;
+  }
   const int full = blocks / STEP_BLOCKS, steps = (blocks + STEP_BLOCKS - 1) / STEP_BLOCKS;
-  uint64_t staged[WORDS] = {};
-  auto load = [&](int step) {  // a step that the depth fills
-    uint8_t* to = codes[step & 1];
-    sa.load(to, step * STEP_BLOCKS, wave);
-    sw.load(to + BM * STEP_BYTES, step * STEP_BLOCKS, wave);
-    __builtin_memcpy(staged, scale_row + step * STEP_BLOCKS, sizeof(staged));
+  uint64_t staged[SCALE_ROWS][WORDS] = {};
+  auto load_scales = [&](int step) {
+#pragma unroll
+    for (int q = 0; q < SCALE_ROWS; ++q) __builtin_memcpy(staged[q], scale_row[q] + step * STEP_BLOCKS, sizeof(staged[q]));
   };
   auto load_any = [&](int step) {  // a step beyond the last: none
     if (step >= steps) return;
-    if (step < full) return load(step);
     uint8_t* to = codes[step & 1];
+    if (step < full) {
+      sa.load(to, step * STEP_BLOCKS, wave);
+      sw.load(to + BM * STEP_BYTES, step * STEP_BLOCKS, wave);
+      load_scales(step);
+      return;
+    }
     sa.load_end(to, step * STEP_BLOCKS, blocks, wave, lane);
     sw.load_end(to + BM * STEP_BYTES, step * STEP_BLOCKS, blocks, wave, lane);
 #pragma unroll
-    for (int k = 0; k < WORDS; ++k) {
-      staged[k] = 0;
+    for (int q = 0; q < SCALE_ROWS; ++q)
+#pragma unroll
+      for (int k = 0; k < WORDS; ++k) {
+        staged[q][k] = 0;
 #pragma unroll 1
-      for (int i = step * STEP_BLOCKS + 8 * k, n = 0; n < 8 && i + n < blocks; ++n)
-        staged[k] |= uint64_t(scale_row[i + n]) << (8 * n);
-    }
+        for (int i = step * STEP_BLOCKS + 8 * k, n = 0; n < 8 && i + n < blocks; ++n)
+          staged[q][k] |= uint64_t(scale_row[q][i + n]) << (8 * n);
+      }
   };
   auto put_scales = [&](int buf) {
 #pragma unroll
-    for (int k = 0; k < WORDS; ++k) scales[buf][t][k] = staged[k];
+    for (int q = 0; q < SCALE_ROWS; ++q)
+#pragma unroll
+      for (int k = 0; k < WORDS; ++k) scales[buf][t + q * THREADS][k] = staged[q][k];
   };
 
   f32x16 acc[TN][TM] = {};
   i32x4 a[2][TM], w[2][TN];
   int sca[TM][WORDS], scw[TN][WORDS], next_sca[TM][WORDS], next_scw[TN][WORDS];
-  // operands of instruction step s of `buf`
-  auto fetch = [&](int buf, auto s) {
+  constexpr int PRODUCTS = TM * TN, READS = TM + TN;  // of a wave, in an instruction step
+  constexpr int LOADS = decltype(sa)::LOADS + decltype(sw)::LOADS;
+  // operand n of instruction step s of `buf`
+  auto fetch = [&](int buf, auto s, int n) {
     constexpr int k = s.value;
     const int slot = ((INSTRUCTIONS * h + k) ^ swizzle<STEP_BLOCKS>(r)) << 4;
-    const uint8_t* ca = codes[buf] + (wm + r) * STEP_BYTES + slot;
-    const uint8_t* cw = codes[buf] + (BM + wn + r) * STEP_BYTES + slot;
-#pragma unroll
-    for (int i = 0; i < TM; ++i) a[k & 1][i] = *reinterpret_cast<const i32x4*>(ca + i * 32 * STEP_BYTES);
-#pragma unroll
-    for (int i = 0; i < TN; ++i) w[k & 1][i] = *reinterpret_cast<const i32x4*>(cw + i * 32 * STEP_BYTES);
-  };
-  auto multiply = [&](auto s) {
-    constexpr int k = s.value;
-    each<TN>([&](auto j) {
-      each<TM>([&](auto i) {
-        acc[j.value][i.value] =
-            wide_product<k & 3, k & 3>(w[k & 1][j.value], a[k & 1][i.value], acc[j.value][i.value], scw[j.value][k / 4],
-                                       sca[i.value][k / 4]);
-      });
-    });
+    const uint8_t* at = codes[buf] + r * STEP_BYTES + slot;
+    if (n < TM)
+      a[k & 1][n] = *reinterpret_cast<const i32x4*>(at + (wm + n * 32) * STEP_BYTES);
+    else
+      w[k & 1][n - TM] = *reinterpret_cast<const i32x4*>(at + (BM + wn + (n - TM) * 32) * STEP_BYTES);
   };
   auto fetch_scales = [&](int buf) {
     const int* p = reinterpret_cast<const int*>(scales[buf]);
@@ -393,10 +399,38 @@ __global__ __launch_bounds__(WGM* WGN * 64) void mx_tile_kernel(MxLaunch L, int 
 #pragma unroll
       for (int k = 0; k < WORDS; ++k) next_scw[i][k] = p[((BM + wn + i * 32 + r) * 2 + h) * WORDS + k];
   };
+  // The products of instruction step s.  Between them, and kept there: the reads
+  // of step f's operands (READ) and the loads of a full `load` (LOAD), a share
+  // before each product.  All at once ahead of the products they held these up
+  // until the queues of LDS and of the loads had room (16384 x 8192 x 4096: 346
+  // us, with waves of 128 x 128 333, with the reads and loads between 321).
+  auto products = [&](auto s, int buf, auto f, auto READ, int load, auto LOAD) {
+    constexpr int k = s.value;
+    each<PRODUCTS>([&](auto q) {
+      constexpr int j = q.value / TM, i = q.value % TM;
+      if constexpr (READ.value != 0) {
+        constexpr int SHARE = (READS + PRODUCTS - 1) / PRODUCTS;
+#pragma unroll
+        for (int n = q.value * SHARE; n < min((q.value + 1) * SHARE, READS); ++n) fetch(buf, f, n);
+      }
+      if constexpr (LOAD.value != 0) {
+        constexpr int SHARE = (LOADS + PRODUCTS - 1) / PRODUCTS;
+        uint8_t* to = codes[load & 1];
+#pragma unroll
+        for (int n = q.value * SHARE; n < min((q.value + 1) * SHARE, LOADS); ++n) {
+          if (n < sa.LOADS)
+            sa.load_one(to, load * STEP_BLOCKS, wave, n);
+          else
+            sw.load_one(to + BM * STEP_BYTES, load * STEP_BLOCKS, wave, n - sa.LOADS);
+        }
+      }
+      acc[j][i] = wide_product<k & 3, k & 3>(w[k & 1][j], a[k & 1][i], acc[j][i], scw[j][k / 4], sca[i][k / 4]);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
   // One step; LOAD: the step after the next is loaded, 1 full, 2 any; NEXT:
   // there is a next one.  The body of the main loop has no branch: the
-  // compiler moves matrix instructions past one, behind the barrier.  (Nor may
-  // it move reads behind the products that they run beside.)
+  // compiler moves matrix instructions past one, behind the barrier.
   auto body = [&](int step, auto LOAD, auto NEXT) {
     const int buf = step & 1;
 #pragma unroll
@@ -406,31 +440,25 @@ __global__ __launch_bounds__(WGM* WGN * 64) void mx_tile_kernel(MxLaunch L, int 
 #pragma unroll
       for (int i = 0; i < TN; ++i) scw[i][k] = next_scw[i][k];
     }
-    each<INSTRUCTIONS - 1>([&](auto s) {
-      fetch(buf, Int<s.value + 1>{});
-      __builtin_amdgcn_sched_barrier(0);
-      multiply(s);
-      __builtin_amdgcn_sched_barrier(0);
-    });
+    each<INSTRUCTIONS - 1>([&](auto s) { products(s, buf, Int<s.value + 1>{}, Int<1>{}, 0, Int<0>{}); });
     if constexpr (NEXT.value != 0) {
       put_scales(buf ^ 1);
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's loads into LDS
       __syncthreads();
-      if constexpr (LOAD.value == 1) load(step + 2);
+      if constexpr (LOAD.value == 1) load_scales(step + 2);
       if constexpr (LOAD.value == 2) load_any(step + 2);
-      fetch(buf ^ 1, Int<0>{});
       fetch_scales(buf ^ 1);
       __builtin_amdgcn_sched_barrier(0);
     }
-    multiply(Int<INSTRUCTIONS - 1>{});
-    __builtin_amdgcn_sched_barrier(0);
+    products(Int<INSTRUCTIONS - 1>{}, buf ^ 1, Int<0>{}, NEXT, step + 2, Int<LOAD.value == 1>{});
   };
   load_any(0);
   put_scales(0);
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
   load_any(1);
-  fetch(0, Int<0>{});
+#pragma unroll
+  for (int n = 0; n < READS; ++n) fetch(0, Int<0>{}, n);
   fetch_scales(0);
   int step = 0;
   for (; step + 2 < full; ++step) body(step, Int<1>{}, Int<1>{});
@@ -442,6 +470,7 @@ __global__ __launch_bounds__(WGM* WGN * 64) void mx_tile_kernel(MxLaunch L, int 
   // bytes a row, they took 13 us of a tile's 52.  A row's 16-byte pieces are
   // permuted by its number.
   constexpr int PASSES = sizeof(E) / 2, COLS = BN / PASSES, PITCH = COLS * sizeof(E), PIECES = PITCH / 16;
+  static_assert(BM * PIECES % THREADS == 0, "the loop below ends with whole rows of threads");
   typedef E e4 __attribute__((ext_vector_type(4)));
   uint8_t* out = codes[0];
   E* y = static_cast<E*>(L.y);
@@ -463,8 +492,9 @@ __global__ __launch_bounds__(WGM* WGN * 64) void mx_tile_kernel(MxLaunch L, int 
     __syncthreads();
     const int n = n0 + pass * COLS;
     if (int64_t(L.N) * sizeof(E) % 16 == 0) {  // whole pieces, aligned, in or out together
-      for (int p = threadIdx.x; p < BM * PIECES; p += THREADS) {
-        const int row = p / PIECES, piece = p % PIECES, col = n + piece * (16 / int(sizeof(E)));
+#pragma unroll 8
+      for (int i = 0; i < BM * PIECES; i += THREADS) {
+        const int p = i + threadIdx.x, row = p / PIECES, piece = p % PIECES, col = n + piece * (16 / int(sizeof(E)));
         if (m0 + row < L.M && col < L.N)
           *reinterpret_cast<i32x4*>(y + int64_t(m0 + row) * L.N + col) =
               *reinterpret_cast<const i32x4*>(out + row * PITCH + ((piece ^ row) & (PIECES - 1)) * 16);
@@ -517,7 +547,7 @@ hipError_t matmul(const MxLaunch& L, hipStream_t stream) {
   const int64_t rows = count(32, 16);
   if (rows <= 256 || (rows <= 448 && rows * L.K <= 1 << 20)) return rows_product<2, 8, E, void>(L, stream);
   if (count(64, 64) <= 512) return tile_product<64, 64, 2, 2, 512, E>(L, stream);
-  if (count(256, 256) >= 192) return tile_product<256, 256, 2, 4, 256, E>(L, stream);
+  if (count(256, 256) >= 192) return tile_product<256, 256, 2, 2, 256, E>(L, stream);
   if (count(128, 128) <= 256) return tile_product<128, 128, 2, 2, 512, E>(L, stream);
   return tile_product<128, 128, 2, 2, 256, E>(L, stream);
 }

@@ -474,7 +474,7 @@ gdnq_status gdnq_prefill_resume(const gdnq_prefill_params* p, const int32_t* cu_
  *   outside the buffers.  p->channels C >= 1 (even C is faster in bf16);
  *   p->dtype (x, gate, y and their gradients) GDNQ_F32 or GDNQ_BF16; B >= 0,
  *   T >= 0, at most 2^31 - 4097 tokens, B C <= 2^31 - 1 and
- *   ceil(tokens / GDNQ_SCAN_CHUNK) ceil(C / 64) <= 2^31 - 1.
+ *   ceil(tokens / GDNQ_SCAN_CHUNK) ceil(C / 64) < 2^22.
  *   A NaN or infinity stays in its own channel and sequence.
  *
  *   gdnq_scan_forward
@@ -538,8 +538,9 @@ gdnq_status gdnq_scan_step(const gdnq_scan_params* p, const void* x, const void*
  *       y = n act(gate),  or act(n) when gate is NULL
  *
  *   p->rows R >= 0 tokens, p->groups G >= 1, p->width D in 1 .. 16384 (a
- *   multiple of 8 is faster), R G <= 2^31 - 1; p->dtype (x, gate, y and
- *   their gradients) GDNQ_F32 or GDNQ_BF16; p->eps >= 0, finite;
+ *   multiple of 8 is faster), R G <= 2^31 - 1, G D < 2^26 without
+ *   GDNQ_NORM_SHARED; p->dtype (x, gate, y and their gradients) GDNQ_F32 or
+ *   GDNQ_BF16; p->eps >= 0, finite;
  *   p->act GDNQ_ACT_NONE, GDNQ_ACT_SILU or GDNQ_ACT_SIGMOID (with gate: not
  *   GDNQ_ACT_NONE, which would be a plain product).
  *     x, gate, y [R,G,D] dtype; gate or NULL
@@ -600,9 +601,9 @@ gdnq_status gdnq_group_norm_backward(const gdnq_norm_params* p, const void* x, c
  *     form above, y [rows, cols] out_dtype; products are exact, sums fp32.
  *   gdnq_mx_linear: the same with a = the codes of x [rows, depth] in_dtype,
  *     quantized in the call's workspace.
- *   rows >= 0; cols >= 1; both <= 2^30; 32 <= depth <= 2^20; rows depth and
- *   cols depth up to 2^40; ceil(rows / 256) ceil(cols / 16) <= 2^31 - 1.  in_dtype is not read by
- *   gdnq_mx_matmul.  flags must be 0.
+ *   0 <= rows <= 2^30; 1 <= cols <= 2^25; 32 <= depth <= 2^20; rows depth
+ *   and cols depth up to 2^40; ceil(rows / 256) ceil(cols / 256) < 2^24.
+ *   in_dtype is not read by gdnq_mx_matmul.  flags must be 0.
  *   workspace: gdnq_mx_workspace_size(p) bytes, enough for either call.
  *   Errors: NULL, SHAPE, DTYPE, ALIGN, ALIAS, FLAGS, WORKSPACE, HIP.
  * ------------------------------------------------------------------------ */

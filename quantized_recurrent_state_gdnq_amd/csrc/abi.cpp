@@ -631,8 +631,8 @@ static gdnq_status scan_validate(const gdnq_scan_params* p, bool varlen, gdnq::S
   if (n > 0x7fffffffLL - 4096) return fail(GDNQ_ERR_SHAPE, "%lld tokens: at most 2^31 - 4097", (long long)n);
   if (int64_t(p->batch) * p->channels > 0x7fffffffLL)
     return fail(GDNQ_ERR_SHAPE, "batch * channels = %lld: at most 2^31 - 1", (long long)p->batch * p->channels);
-  // one workgroup per chunk and 64 channels
-  if ((n + GDNQ_SCAN_CHUNK - 1) / GDNQ_SCAN_CHUNK * ((int64_t(p->channels) + 63) / 64) > 0x7fffffffLL)
+  // a workgroup of up to 1024 threads per chunk and 64 channels, and a launch has fewer than 2^32 threads
+  if ((n + GDNQ_SCAN_CHUNK - 1) / GDNQ_SCAN_CHUNK * ((int64_t(p->channels) + 63) / 64) >= 1 << 22)
     return fail(GDNQ_ERR_SHAPE, "%lld tokens of %d channels: too large", (long long)n, p->channels);
   L = gdnq::ScanLaunch{};
   L.B = p->batch; L.T = p->seqlen; L.C = p->channels; L.N = n;
@@ -738,6 +738,9 @@ static gdnq_status norm_validate(const gdnq_norm_params* p, bool gate, gdnq::Nor
     return fail(GDNQ_ERR_SHAPE, "rows = %d, groups = %d, width = %d (1 .. 16384)", p->rows, p->groups, p->width);
   if (int64_t(p->rows) * p->groups > 0x7fffffffLL || p->groups > (1 << 20))
     return fail(GDNQ_ERR_SHAPE, "rows * groups = %lld: at most 2^31 - 1, and 2^20 groups", (long long)p->rows * p->groups);
+  // a workgroup of 1024 threads adds 16 weights' gradients, and a launch has fewer than 2^32 threads
+  if (!(p->flags & GDNQ_NORM_SHARED) && int64_t(p->groups) * p->width >= 1 << 26)
+    return fail(GDNQ_ERR_SHAPE, "groups * width = %lld: less than 2^26 unless weights are shared", (long long)p->groups * p->width);
   if (!dtype_ok(p->dtype)) return fail(GDNQ_ERR_DTYPE, "dtype = %d", p->dtype);
   if (!(p->eps >= 0.0f) || p->eps > 3.0e38f) return fail(GDNQ_ERR_SHAPE, "eps = %g, expected a finite value >= 0", double(p->eps));
   if (p->act < GDNQ_ACT_NONE || p->act > GDNQ_ACT_SIGMOID) return fail(GDNQ_ERR_FLAGS, "act = %d", p->act);
@@ -813,11 +816,12 @@ static gdnq_status mx_depth_ok(int64_t rows, int32_t depth) {
 
 static gdnq_status mx_validate(const gdnq_mx_params* p, bool linear, gdnq::MxLaunch& L) {
   if (!p) return fail(GDNQ_ERR_NULL, "params is NULL");
-  if (p->rows < 0 || p->cols < 1 || p->rows > (1 << 30) || p->cols > (1 << 30))
-    return fail(GDNQ_ERR_SHAPE, "rows = %d, cols = %d (at most 2^30)", p->rows, p->cols);
+  // at most 1024 threads per 16 columns of few rows, 256 per tile of 256 x 256, fewer than 2^32 in a launch
+  if (p->rows < 0 || p->cols < 1 || p->rows > (1 << 30) || p->cols > (1 << 25))
+    return fail(GDNQ_ERR_SHAPE, "rows = %d (at most 2^30), cols = %d (at most 2^25)", p->rows, p->cols);
   if (gdnq_status st = mx_depth_ok(p->rows, p->depth)) return st;
   if (gdnq_status st = mx_depth_ok(p->cols, p->depth)) return st;
-  if ((int64_t(p->rows) + 255) / 256 * ((int64_t(p->cols) + 15) / 16) > 0x7fffffffLL)
+  if ((int64_t(p->rows) + 255) / 256 * ((int64_t(p->cols) + 255) / 256) >= 1 << 24)
     return fail(GDNQ_ERR_SHAPE, "rows = %d, cols = %d: too large", p->rows, p->cols);
   if (!dtype_ok(p->out_dtype) || (linear && !dtype_ok(p->in_dtype)))
     return fail(GDNQ_ERR_DTYPE, "in_dtype = %d, out_dtype = %d", p->in_dtype, p->out_dtype);

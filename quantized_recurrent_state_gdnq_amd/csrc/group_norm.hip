@@ -18,7 +18,9 @@
 // a multiple of 8 (WIDE) they are aligned and all in the group or all out; else
 // they are loaded unaligned, and the lane in which the group ends takes its
 // values one by one.  (Every TEAM-th value instead, which needs no unaligned
-// access, took 13.1 + 19.7 us for the odd fp32 training step's two passes.)
+// access, took 365 us for forward and backward of 20000 x 5 groups of 333 bf16,
+// against 242, and 1499 for 20000 x 4999, against 622; for 4099 x 7 of 171 fp32
+// it was faster, 13.1 + 19.7 against 14.2 + 22.2.)
 #include <hip/hip_runtime.h>
 
 #include "../../include/gdnq.h"

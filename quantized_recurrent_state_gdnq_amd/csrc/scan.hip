@@ -36,10 +36,10 @@ namespace {
 
 // Waves of a workgroup, tokens per wave and waves per SIMD (by the registers)
 // for V channels per lane.  Two channels of bf16 and their gates take two
-// registers and a half per token: half as many waves with twice the tokens
-// measured 119 us for 32768 tokens of 2048 channels against 167 (the shape of
-// one channel, spilling) and 121 (8 waves, 16 tokens); one channel of fp32 377
-// us for 262144 tokens of 640 channels against 413 (8 waves, 32 tokens).
+// registers and a half per token, so half as many waves hold twice the tokens:
+// 98 us for 32768 tokens of 2048 channels with given gates, 114 with 8 waves of
+// 16 tokens; the shape of one channel spills.  One channel of fp32: 377 us for
+// 262144 tokens of 640 channels, 413 with 8 waves of 32 tokens.
 template <int V>
 struct ForwardShape {
   static constexpr int WAVES = V == 1 ? 16 : 8, RUN = V == 1 ? 16 : 32, PER_SIMD = V == 1 ? 8 : 4;

@@ -204,3 +204,40 @@ def test_mx_quantize():
     refused(q(addr(1), 4, 64, 1, addr(1), addr(3), None), ALIAS, "overlaps")
     refused(q(addr(1), 4, 64, 1, addr(2) + 4, addr(3), None), ALIGN, "codes")
     assert q(None, 0, 64, 1, None, None, None) == 0
+
+
+# ---------------------------------------------------------------- launches
+
+# A launch has fewer than 2^32 threads: sizes that would need more are refused,
+# those just below are taken (a size of 0 bytes or tokens elsewhere keeps them
+# from being launched).
+
+@pytest.mark.parametrize("T,C,fits", [
+    (128 * (2 ** 22 - 1), 64, True), (128 * (2 ** 22 - 1) + 1, 64, False), (2 ** 30, 1, False), (2 ** 29, 65, False)])
+def test_scan_launch_limit(T, C, fits):
+    p = scan_p(B=1, T=T, C=C)
+    assert (_lib.scan_workspace_size(p, False) > 0) == fits
+    if not fits:
+        refused(forward(p), SHAPE, "too large")
+        refused(backward(p), SHAPE, "too large")
+
+
+@pytest.mark.parametrize("G,D,flags,fits", [
+    (2 ** 13 - 1, 2 ** 13, 0, True), (2 ** 13, 2 ** 13, 0, False), (2 ** 20, 64, 0, False), (2 ** 20, 64, 2, True)])
+def test_norm_launch_limit(G, D, flags, fits):
+    p = norm_p(R=0, G=G, D=D, flags=flags)
+    if fits:
+        assert norm(p) == 0
+    else:
+        refused(norm(p), SHAPE, "2^26")
+        refused(norm_backward(p), SHAPE, "2^26")
+
+
+@pytest.mark.parametrize("M,N,fits", [
+    (1, 2 ** 25, True), (1, 2 ** 25 + 1, False), (2 ** 30, 3 * 256, True), (2 ** 30, 4 * 256, False), (2 ** 15, 2 ** 25, False)])
+def test_mx_launch_limit(M, N, fits):
+    p = mx_p(M=M, N=N, K=32)
+    assert (_lib.mx_workspace_size(p) > 0) == fits
+    if not fits:
+        assert matmul(p) == SHAPE
+        assert linear(p) == SHAPE

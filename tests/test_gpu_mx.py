@@ -84,6 +84,29 @@ def test_codec_every_mantissa_and_tie():
     assert_codes(xb.double().numpy(), *ops.mx_quantize(xb.to(DEV)))
 
 
+def test_codec_of_more_values_than_one_launch_takes():
+    """2^34 values are a launch; the rows on both sides of its end against the
+    same rows alone."""
+    rows, K = 2 ** 14 + 8, 2 ** 20
+    if torch.cuda.mem_get_info()[0] < 64 << 30:
+        pytest.skip("needs 64 GiB of free device memory")
+    x = torch.zeros(rows, K, dtype=torch.bfloat16, device=DEV)
+    some = [0, 1, 2 ** 14 - 2, 2 ** 14 - 1, 2 ** 14, 2 ** 14 + 1, rows - 1]
+    g = torch.Generator(device=DEV).manual_seed(5)
+    part = torch.randn(len(some), K, generator=g, device=DEV).bfloat16()
+    x[some] = part
+    codes = torch.full((rows, K // 2), 0xEE, dtype=torch.uint8, device=DEV)
+    scales = torch.full((rows, K // 32), 0xEE, dtype=torch.uint8, device=DEV)
+    ops.mx_quantize(x, codes, scales)
+    del x
+    want_codes, want_scales = ops.mx_quantize(part)
+    assert torch.equal(codes[some], want_codes) and torch.equal(scales[some], want_scales)
+    for r in (2, 2 ** 13, 2 ** 14 - 3, 2 ** 14 + 2, rows - 2):
+        assert not codes[r].any() and not scales[r].any()
+    del codes, scales
+    torch.cuda.empty_cache()
+
+
 def test_codec_extremes():
     tiny = 2.0 ** -149
     rows = [[0.0] * 32, [tiny] * 32, [2.0 ** -126] + [2.0 ** -128] * 31, [2.0 ** -125] + [tiny] * 31,
@@ -142,6 +165,14 @@ def test_product_rows(rows):
 @pytest.mark.parametrize("rows", [20, 300])
 def test_product_depths(K, rows):
     check_product(random_rows(rows, K, rows, torch.bfloat16), random_rows(272, K, 7), torch.float32)
+
+
+# sizes of the larger tiles: 128 x 128 (two on a CU), 256 x 256, each with whole and ragged steps and edges
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows,cols,K", [(2049, 2301, 32), (2304, 2176, 1024), (2049, 2301, 1312), (3585, 3331, 32),
+                                         (3329, 3584, 288), (3584, 3584, 512), (3500, 3333, 992), (3585, 3600, 1280)])
+def test_product_large_tiles(rows, cols, K, out_dtype):
+    check_product(random_rows(rows, K, rows, torch.bfloat16), random_rows(cols, K, cols + 1), out_dtype)
 
 
 def test_scales_pair_with_their_blocks():

@@ -152,6 +152,51 @@ def test_channels(C, dtype):
     run_case(3, 150, C, dtype, False, True, True, seed=C)
 
 
+def exact(x, a, dy, h0, dh_last, bounds):
+    """The recurrence and its gradients for gates of 1 and -1 and small
+    integers, whose every sum and product is exact, in int64."""
+    y, dx, dg = np.zeros_like(x), np.zeros_like(x), np.zeros_like(x)
+    h_last, dh0 = h0.copy(), dh_last.copy()
+    for i, (t0, t1) in enumerate(zip(bounds[:-1], bounds[1:])):
+        if t0 == t1:
+            continue
+        p = np.cumprod(a[t0:t1], 0)
+        h = p * (h0[i] + np.cumsum(p * x[t0:t1], 0))
+        before = np.concatenate([h0[i][None], h[:-1]])
+        d = dy[t0:t1].copy()
+        d[-1] += dh_last[i]
+        lam = p * np.cumsum((p * d)[::-1], 0)[::-1]
+        y[t0:t1], dx[t0:t1], dg[t0:t1] = h, lam, lam * before
+        h_last[i], dh0[i] = h[-1], a[t0] * lam[0]
+    return dict(y=y, h_last=h_last, dx=dx, dgate=dg, dh0=dh0)
+
+
+# Sequences longer than 256 chunks (65536 tokens forward, 32768 backward), that
+# nothing is forgotten in: the states handed on have to be whole.
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("C", [1, 2, 66])
+@pytest.mark.parametrize("lengths", [[33000], [70001], [140000], [10, 65700, 0, 66500, 33]])
+def test_long_memory(lengths, C, dtype):
+    bounds = np.concatenate([[0], np.cumsum(lengths)])
+    n, B = int(bounds[-1]), len(lengths)
+    rng = np.random.default_rng(n + C)
+    x, dy = rng.integers(-1, 2, (n, C)), rng.integers(-1, 2, (n, C))
+    a = np.where(rng.random((n, C)) < 0.001, -1, 1)
+    h0, dh_last = rng.integers(-9, 10, (B, C)), rng.integers(-9, 10, (B, C))
+
+    def gpu(v, t):
+        return torch.from_numpy(v).to(DEV).to(t)
+    cu = gpu(bounds, torch.int32)
+    xs, gs, dys, h0s, dhs = gpu(x, dtype), gpu(a, dtype), gpu(dy, dtype), gpu(h0, torch.float32), gpu(dh_last, torch.float32)
+    y, h, carry = ops.gated_scan(xs, gs, h0s, cu, save=True)
+    dx, dgate, dh0 = ops.gated_scan_backward(dys, xs, gs, carry, h0s, dhs, cu)
+    want = exact(x, a, dy, h0, dh_last, bounds)
+    assert max(np.abs(v).max() for v in want.values()) < 2 ** 24
+    for name, got, t in (("y", y, dtype), ("h_last", h, torch.float32), ("dx", dx, dtype), ("dgate", dgate, dtype),
+                         ("dh0", dh0, torch.float32)):
+        assert torch.equal(got.cpu(), torch.from_numpy(want[name]).float().to(t)), name
+
+
 def test_batches():
     run_case(700, 3, 5, torch.float32, True, False, True, seed=3)
     run_case(33, 128, 130, torch.bfloat16, True, True, True, seed=4)

@@ -12,10 +12,10 @@
 // and the outputs need no second read.  The variance is the mean of the
 // centred squares, in fp32.
 // Measured, gated bf16: 32768 x 16 groups of 128 forward 82 us (4.9 TB/s),
-// backward 127 (5.3 TB/s); 16384 groups of 5120 forward 117 (4.3 TB/s).
+// backward 127 (5.3 TB/s); 16384 groups of 5120 forward 100 (5.0 TB/s).
 //   TEAM: the fewest lanes (8 .. 64) that hold the group with eight values
 //   each; above 512 values a workgroup (TEAM = BLOCK) of as many waves as that
-//   takes, above 8192 with sixteen values a lane.
+//   takes, with eight or sixteen values a lane (see eights_of).
 //   A lane holds eight adjacent values (16 bytes of bf16).  Where the width is
 // a multiple of 8 (WIDE) they are aligned and all in the group or all out; else
 // they are loaded unaligned, and the lane in which the group ends takes its
@@ -357,43 +357,54 @@ __global__ __launch_bounds__(1024) void norm_params_kernel(const float* __restri
 
 // The team's lanes (BLOCK: threads of the workgroup).
 int team_of(int D) { return D <= 64 ? 8 : D <= 128 ? 16 : D <= 256 ? 32 : D <= 512 ? 64 : BLOCK; }
-int threads_of(int D) { return D <= 512 ? THREADS : D <= 8192 ? (D + 511) / 512 * 64 : (D + 1023) / 1024 * 64; }
+int threads_of(int D, int eights) { return D <= 512 ? THREADS : (D + 512 * eights - 1) / (512 * eights) * 64; }
 int teams_in(int D) { return team_of(D) == BLOCK ? 1 : THREADS / team_of(D); }
 
 // Teams of a call: those of as many workgroups as the chip's 256 CUs hold at
 // once, which then take the same number of groups each, rounded up to a
 // multiple of G (the groups of a token, 1 for shared weights) so that a team's
 // groups share their weights.  Waves a CU holds by the kernels' registers: 32
-// of the forward, 16 of the backward pass.
-constexpr int FORWARD_WAVES = 32, BACKWARD_WAVES = 16;
+// of the forward, 16 of the backward pass and with two eights a lane.
+template <int EIGHTS>
+constexpr int FORWARD_WAVES = EIGHTS == 1 ? 32 : 16;
+constexpr int BACKWARD_WAVES = 16;
 
-int64_t slots_of(int64_t units, int G, int D, int waves) {
-  const int64_t groups = 256 * (waves / (threads_of(D) / 64) > 1 ? waves / (threads_of(D) / 64) : 1);
+// Eights of a lane where a group takes a workgroup: two above 8192 values; in
+// the forward pass of aligned bf16 always, for fewer waves at a barrier (16384 x
+// 5120: 100 us, 119 with one; unaligned 16384 x 5121 127 with one, 158 with two;
+// 8192 x 5120 fp32 98 and 103; the backward pass spills with two).
+int eights_of(int D) { return D <= 8192 ? 1 : 2; }
+
+int64_t slots_of(int64_t units, int G, int D, int eights, int waves) {
+  const int own = threads_of(D, eights) / 64;
+  const int64_t groups = 256 * (waves > own ? waves / own : 1);
   const int64_t most = groups * teams_in(D), want = units < most ? units : most;
   return (want + G - 1) / G * G;
 }
 
 template <typename E, int TEAM, bool WIDE, int EIGHTS>
 struct Forward {
+  static constexpr bool TWO = WIDE && sizeof(E) == 2;  // eights for a workgroup's group
   static hipError_t go(const NormLaunch& L, hipStream_t stream) {
     constexpr int TEAMS = teams_of<TEAM>();
-    const int64_t units = int64_t(L.R) * L.G, slots = slots_of(units, L.shared ? 1 : L.G, L.D, FORWARD_WAVES);
-    norm_forward_kernel<E, TEAM, WIDE, EIGHTS><<<uint32_t((slots + TEAMS - 1) / TEAMS), threads_of(L.D), 0, stream>>>(L, units, slots);
+    const int64_t units = int64_t(L.R) * L.G, slots = slots_of(units, L.shared ? 1 : L.G, L.D, EIGHTS, FORWARD_WAVES<EIGHTS>);
+    norm_forward_kernel<E, TEAM, WIDE, EIGHTS><<<uint32_t((slots + TEAMS - 1) / TEAMS), threads_of(L.D, EIGHTS), 0, stream>>>(L, units, slots);
     return hipGetLastError();
   }
 };
 
 template <typename E, int TEAM, bool WIDE, int EIGHTS>
 struct Backward {
+  static constexpr bool TWO = false;
   static hipError_t go(const NormLaunch& L, hipStream_t stream) {
     constexpr int TEAMS = teams_of<TEAM>();
-    const int64_t units = int64_t(L.R) * L.G, slots = slots_of(units, L.shared ? 1 : L.G, L.D, BACKWARD_WAVES);
+    const int64_t units = int64_t(L.R) * L.G, slots = slots_of(units, L.shared ? 1 : L.G, L.D, EIGHTS, BACKWARD_WAVES);
     int64_t grid = (slots + TEAMS - 1) / TEAMS;
     if (by_group<TEAM>() && !L.shared) grid = (grid + L.G - 1) / L.G * L.G;
     const bool params = L.dweight || L.dbias;
     float* partial = params ? static_cast<float*>(L.workspace) : nullptr;
     if (units > 0) {
-      norm_backward_kernel<E, TEAM, WIDE, EIGHTS><<<uint32_t(grid), threads_of(L.D), 0, stream>>>(L, units, slots, partial);
+      norm_backward_kernel<E, TEAM, WIDE, EIGHTS><<<uint32_t(grid), threads_of(L.D, EIGHTS), 0, stream>>>(L, units, slots, partial);
       if (hipError_t e = hipGetLastError()) return e;
     }
     if (!params) return hipSuccess;
@@ -413,7 +424,11 @@ hipError_t by_width(const NormLaunch& L, hipStream_t s) {
     case 16: return F<E, 16, WIDE, 1>::go(L, s);
     case 32: return F<E, 32, WIDE, 1>::go(L, s);
     case 64: return F<E, 64, WIDE, 1>::go(L, s);
-    default: return L.D <= 8192 ? F<E, BLOCK, WIDE, 1>::go(L, s) : F<E, BLOCK, WIDE, 2>::go(L, s);
+    default:
+      if constexpr (!F<E, BLOCK, WIDE, 1>::TWO) {
+        if (eights_of(L.D) == 1) return F<E, BLOCK, WIDE, 1>::go(L, s);
+      }
+      return F<E, BLOCK, WIDE, 2>::go(L, s);
   }
 }
 
@@ -427,7 +442,7 @@ hipError_t dispatch(const NormLaunch& L, hipStream_t s) {
 }  // namespace
 
 size_t norm_workspace_bytes(int R, int G, int D) {
-  return size_t(slots_of(int64_t(R) * G, G, D, BACKWARD_WAVES)) * D * 2 * 4;
+  return size_t(slots_of(int64_t(R) * G, G, D, eights_of(D), BACKWARD_WAVES)) * D * 2 * 4;
 }
 
 hipError_t launch_norm_forward(const NormLaunch& L, hipStream_t stream) { return dispatch<Forward>(L, stream); }

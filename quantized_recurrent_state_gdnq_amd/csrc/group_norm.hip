@@ -15,14 +15,13 @@
 // backward 127 (5.3 TB/s); 16384 groups of 5120 forward 100 (5.0 TB/s).
 //   TEAM: the fewest lanes (8 .. 64) that hold the group with eight values
 //   each; above 512 values a workgroup (TEAM = BLOCK) of as many waves as that
-//   takes, with eight or sixteen values a lane (see eights_of).
+//   takes, with eight or sixteen values a lane (see forward_eights).
 //   A lane holds eight adjacent values (16 bytes of bf16).  Where the width is
 // a multiple of 8 (WIDE) they are aligned and all in the group or all out; else
-// they are loaded unaligned, and the lane in which the group ends takes its
-// values one by one.  (Every TEAM-th value instead, which needs no unaligned
-// access, took 365 us for forward and backward of 20000 x 5 groups of 333 bf16,
-// against 242, and 1499 for 20000 x 4999, against 622; for 4099 x 7 of 171 fp32
-// it was faster, 13.1 + 19.7 against 14.2 + 22.2.)
+// they are loaded unaligned, and the lane in which the group ends takes its last
+// eight values, of which those of the lane before count once (forward and
+// backward of 20000 x 4999 bf16: 583 us; 666 where that lane takes its own few
+// one by one; 1499 where every lane takes every TEAM-th value, aligned).
 #include <hip/hip_runtime.h>
 
 #include "../../include/gdnq.h"
@@ -76,10 +75,17 @@ __device__ __forceinline__ float team_sum(float x, float* box) {
   }
 }
 
-// Where value j of eighth e of lane l sits in its group.
-template <int TEAM>
-__device__ __forceinline__ int place(int l, int e, int j) {
-  return (e * team_size<TEAM>() + l) * 8 + j;
+// Where eighth e of lane l starts in its group: a lane in which the group ends
+// starts early, so that its eight values are the group's last ones.
+template <int TEAM, bool WIDE>
+__device__ __forceinline__ int place(int l, int e, int D) {
+  const int at = (e * team_size<TEAM>() + l) * 8;
+  return !WIDE && at < D && D >= 8 ? min(at, D - 8) : at;
+}
+// Whether value j there is the lane's own: not also one of the lane before.
+template <int TEAM, bool WIDE>
+__device__ __forceinline__ bool own(int l, int e, int j, int D) {
+  return WIDE || place<TEAM, WIDE>(l, e, D) + j >= (e * team_size<TEAM>() + l) * 8;
 }
 
 template <typename E, int TEAM, bool WIDE>
@@ -87,7 +93,7 @@ struct Eight {
   // as they are in memory; outside the group 0
   E v[8];
   __device__ __forceinline__ void load(const E* p, int l, int e, int D) {
-    const int at = place<TEAM>(l, e, 0);
+    const int at = place<TEAM, WIDE>(l, e, D);
     if (at + (WIDE ? 0 : 7) < D) {
       if constexpr (WIDE) p = static_cast<const E*>(__builtin_assume_aligned(p, 16));
       __builtin_memcpy(v, p + at, sizeof(v));
@@ -97,7 +103,7 @@ struct Eight {
     for (int j = 0; j < 8; ++j) v[j] = !WIDE && at + j < D ? p[at + j] : E(0.0f);
   }
   __device__ __forceinline__ void store(E* p, int l, int e, int D) const {
-    const int at = place<TEAM>(l, e, 0);
+    const int at = place<TEAM, WIDE>(l, e, D);
     if (at + (WIDE ? 0 : 7) < D) {
       if constexpr (WIDE) p = static_cast<E*>(__builtin_assume_aligned(p, 16));
       __builtin_memcpy(p + at, v, sizeof(v));
@@ -138,18 +144,18 @@ __device__ __forceinline__ float normalise(const NormLaunch& L, float (&v)[EIGHT
 #pragma unroll
     for (int e = 0; e < EIGHTS; ++e)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s += v[e][j];
+      for (int j = 0; j < 8; ++j) s += own<TEAM, WIDE>(l, e, j, L.D) ? v[e][j] : 0.0f;
     const float mu = team_sum<TEAM>(s, box[0]) * inv;
 #pragma unroll
     for (int e = 0; e < EIGHTS; ++e)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[e][j] = place<TEAM>(l, e, j) < L.D ? v[e][j] - mu : 0.0f;
+      for (int j = 0; j < 8; ++j) v[e][j] = place<TEAM, WIDE>(l, e, L.D) + j < L.D ? v[e][j] - mu : 0.0f;
   }
   float s = 0.0f;
 #pragma unroll
   for (int e = 0; e < EIGHTS; ++e)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s = fmaf(v[e][j], v[e][j], s);
+    for (int j = 0; j < 8; ++j) s = fmaf(v[e][j], own<TEAM, WIDE>(l, e, j, L.D) ? v[e][j] : 0.0f, s);
   return 1.0f / sqrtf(fmaf(team_sum<TEAM>(s, box[1]), inv, L.eps));
 }
 
@@ -284,8 +290,9 @@ __global__ __launch_bounds__(bounds<TEAM>()) void norm_backward_kernel(NormLaunc
         db[e][j] += dn;
         d[e][j] = dn * w[e][j];
         v[e][j] = hat;
-        s0 += d[e][j];
-        s1 = fmaf(d[e][j], hat, s1);
+        const float mine = own<TEAM, WIDE>(l, e, j, D) ? d[e][j] : 0.0f;
+        s0 += mine;
+        s1 = fmaf(mine, hat, s1);
       }
       if (L.gate) g[e].store(static_cast<E*>(L.dgate) + at, l, e, D);
     }
@@ -311,10 +318,10 @@ __global__ __launch_bounds__(bounds<TEAM>()) void norm_backward_kernel(NormLaunc
       }
       __syncthreads();
       for (int i = threadIdx.x; i < 2 * TEAM * 8; i += THREADS) {
-        const int which = i / (TEAM * 8), k = i % (TEAM * 8), c = place<TEAM>(k / 8, 0, k % 8);
+        const int which = i / (TEAM * 8), k = i % (TEAM * 8), c = place<TEAM, WIDE>(k / 8, 0, D) + k % 8;
         float s = 0.0f;
         for (int t = 0; t < TEAMS; ++t) s += sums[which][t][k];
-        if (c < D) partial[(int64_t(which) * gridDim.x + blockIdx.x) * D + c] = s;
+        if (c < D && own<TEAM, WIDE>(k / 8, 0, k % 8, D)) partial[(int64_t(which) * gridDim.x + blockIdx.x) * D + c] = s;
       }
       return;
     }
@@ -323,8 +330,8 @@ __global__ __launch_bounds__(bounds<TEAM>()) void norm_backward_kernel(NormLaunc
   for (int e = 0; e < EIGHTS; ++e)
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int c = place<TEAM>(l, e, j);
-      if (c < D && slot < slots) {
+      const int c = place<TEAM, WIDE>(l, e, D) + j;
+      if (c < D && slot < slots && own<TEAM, WIDE>(l, e, j, D)) {
         partial[slot * D + c] = dw[e][j];
         partial[(slots + slot) * D + c] = db[e][j];
       }
@@ -363,17 +370,23 @@ int teams_in(int D) { return team_of(D) == BLOCK ? 1 : THREADS / team_of(D); }
 // Teams of a call: those of as many workgroups as the chip's 256 CUs hold at
 // once, which then take the same number of groups each, rounded up to a
 // multiple of G (the groups of a token, 1 for shared weights) so that a team's
-// groups share their weights.  Waves a CU holds by the kernels' registers: 32
-// of the forward, 16 of the backward pass and with two eights a lane.
-template <int EIGHTS>
-constexpr int FORWARD_WAVES = EIGHTS == 1 ? 32 : 16;
+// groups share their weights.  Waves a CU holds by the kernels' registers (a
+// grid of more than that runs a part of its workgroups after the others:
+// 20000 x 4999 bf16 forward 199 us with 32, 156 with 28):
+template <typename E, int TEAM, bool WIDE, int EIGHTS>
+constexpr int FORWARD_WAVES = EIGHTS == 2 ? 16 : WIDE && (TEAM != BLOCK || sizeof(E) == 2) ? 32 : 28;
 constexpr int BACKWARD_WAVES = 16;
 
-// Eights of a lane where a group takes a workgroup: two above 8192 values; in
-// the forward pass of aligned bf16 always, for fewer waves at a barrier (16384 x
-// 5120: 100 us, 119 with one; unaligned 16384 x 5121 127 with one, 158 with two;
-// 8192 x 5120 fp32 98 and 103; the backward pass spills with two).
-int eights_of(int D) { return D <= 8192 ? 1 : 2; }
+// Eights of a lane where a group takes a workgroup: two above 8192 values, and
+// in the forward pass
+//   of aligned bf16 always, for fewer waves at a barrier (16384 x 5120: 96 us,
+//   117 with one; 8192 x 5120 fp32 103 and 96);
+//   of unaligned groups above 7168, of whose 15 waves a CU holds only one group
+//   (16384 x 7169: 188 us, 234 with one; 16384 x 5121 158 and 130).
+// The backward pass spills with two.
+template <typename E, bool WIDE>
+int forward_eights(int D) { return (WIDE && sizeof(E) == 2) || D > (WIDE ? 8192 : 7168) ? 2 : 1; }
+int backward_eights(int D) { return D <= 8192 ? 1 : 2; }
 
 int64_t slots_of(int64_t units, int G, int D, int eights, int waves) {
   const int own = threads_of(D, eights) / 64;
@@ -384,10 +397,11 @@ int64_t slots_of(int64_t units, int G, int D, int eights, int waves) {
 
 template <typename E, int TEAM, bool WIDE, int EIGHTS>
 struct Forward {
-  static constexpr bool TWO = WIDE && sizeof(E) == 2;  // eights for a workgroup's group
+  static constexpr bool ONE = !WIDE || sizeof(E) == 4;  // whether groups of a workgroup may have one eight a lane
+  static int eights(int D) { return forward_eights<E, WIDE>(D); }
   static hipError_t go(const NormLaunch& L, hipStream_t stream) {
     constexpr int TEAMS = teams_of<TEAM>();
-    const int64_t units = int64_t(L.R) * L.G, slots = slots_of(units, L.shared ? 1 : L.G, L.D, EIGHTS, FORWARD_WAVES<EIGHTS>);
+    const int64_t units = int64_t(L.R) * L.G, slots = slots_of(units, L.shared ? 1 : L.G, L.D, EIGHTS, FORWARD_WAVES<E, TEAM, WIDE, EIGHTS>);
     norm_forward_kernel<E, TEAM, WIDE, EIGHTS><<<uint32_t((slots + TEAMS - 1) / TEAMS), threads_of(L.D, EIGHTS), 0, stream>>>(L, units, slots);
     return hipGetLastError();
   }
@@ -395,7 +409,8 @@ struct Forward {
 
 template <typename E, int TEAM, bool WIDE, int EIGHTS>
 struct Backward {
-  static constexpr bool TWO = false;
+  static constexpr bool ONE = true;
+  static int eights(int D) { return backward_eights(D); }
   static hipError_t go(const NormLaunch& L, hipStream_t stream) {
     constexpr int TEAMS = teams_of<TEAM>();
     const int64_t units = int64_t(L.R) * L.G, slots = slots_of(units, L.shared ? 1 : L.G, L.D, EIGHTS, BACKWARD_WAVES);
@@ -425,8 +440,8 @@ hipError_t by_width(const NormLaunch& L, hipStream_t s) {
     case 32: return F<E, 32, WIDE, 1>::go(L, s);
     case 64: return F<E, 64, WIDE, 1>::go(L, s);
     default:
-      if constexpr (!F<E, BLOCK, WIDE, 1>::TWO) {
-        if (eights_of(L.D) == 1) return F<E, BLOCK, WIDE, 1>::go(L, s);
+      if constexpr (F<E, BLOCK, WIDE, 1>::ONE) {
+        if (F<E, BLOCK, WIDE, 1>::eights(L.D) == 1) return F<E, BLOCK, WIDE, 1>::go(L, s);
       }
       return F<E, BLOCK, WIDE, 2>::go(L, s);
   }
@@ -442,7 +457,7 @@ hipError_t dispatch(const NormLaunch& L, hipStream_t s) {
 }  // namespace
 
 size_t norm_workspace_bytes(int R, int G, int D) {
-  return size_t(slots_of(int64_t(R) * G, G, D, eights_of(D), BACKWARD_WAVES)) * D * 2 * 4;
+  return size_t(slots_of(int64_t(R) * G, G, D, backward_eights(D), BACKWARD_WAVES)) * D * 2 * 4;
 }
 
 hipError_t launch_norm_forward(const NormLaunch& L, hipStream_t stream) { return dispatch<Forward>(L, stream); }

@@ -123,16 +123,22 @@ __device__ __forceinline__ void store4(E* y, int M, int N, int m, int n, const f
 // Bound by the bytes of W.  A workgroup computes 16 columns x 16 MT rows, its
 // waves a run of the depth each, operands straight from memory to registers
 // (nothing is used twice but A, which the caches hold), and the waves' sums
-// are added in LDS in wave order.  A lane takes four adjacent blocks of its
-// row at a time: 64 bytes of codes and one word of scales.
+// are added in LDS in wave order.  A lane takes N adjacent blocks of its row at
+// a time: four, 64 bytes and one word of scales (single blocks with their own
+// scale loads took 7.8 us for 32 x 4096 x 4096, against 5.8); where rows are
+// quantized here two, so that more waves share that (1 x 4096 x 4096: 6.0 us,
+// with four 7.6; 16 x 4096 x 4096: 8.0, 8.9).  As many rows in codes take two as
+// well (5.4 us for 16, with four 5.0): both calls then add in the same order.
 
-// Scales of blocks b .. b + 3 of a row (beyond its end 0).
-__device__ __forceinline__ int four_scales(const uint8_t* row, int b, int blocks) {
+// Scales of blocks b .. b + N - 1 of a row (beyond its end 0).
+template <int N>
+__device__ __forceinline__ int scales_at(const uint8_t* row, int b, int blocks) {
   uint32_t w = 0;
-  if (b + 4 <= blocks) {
-    __builtin_memcpy(&w, row + b, 4);
+  if (b + N <= blocks) {
+    __builtin_memcpy(&w, row + b, N);
   } else {
-    for (int i = 0; i < 3; ++i)
+#pragma unroll
+    for (int i = 0; i < N - 1; ++i)
       if (b + i < blocks) w |= uint32_t(row[b + i]) << (8 * i);
   }
   return int(w);
@@ -156,7 +162,7 @@ __device__ __forceinline__ int quantize_block(const X* x, i32x4& w) {
 
 // X: the type of A's rows where they are quantized here, in every workgroup,
 // instead of by a launch of their own (void: they are codes).
-template <int MT, int WAVES, typename E, typename X>
+template <int MT, int WAVES, int N, typename E, typename X>
 __global__ __launch_bounds__(WAVES * 64) void mx_rows_kernel(MxLaunch L, int col_tiles) {
   __shared__ f32x4 sums[WAVES][MT][64];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
@@ -174,37 +180,38 @@ __global__ __launch_bounds__(WAVES * 64) void mx_rows_kernel(MxLaunch L, int col
     as[t] = L.a_scales + arow * blocks;
   }
   f32x4 acc[MT] = {};
-  // runs of whole steps of 16 blocks
-  const int steps = (blocks + 15) / 16;
+  // runs of whole steps
+  constexpr int STEP = 4 * N;
+  const int steps = (blocks + STEP - 1) / STEP;
   const int first = steps * wave / WAVES, last = steps * (wave + 1) / WAVES;
   for (int step = first; step < last; ++step) {
-    const int b = step * 16 + q * 4;
-    i32x4 w[4], a[MT][4];
+    const int b = step * STEP + q * N;
+    i32x4 w[N], a[MT][N];
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
+    for (int s = 0; s < N; ++s) {
       w[s] = i32x4{0, 0, 0, 0};
       if (b + s < blocks) w[s] = *reinterpret_cast<const i32x4*>(wc + int64_t(b + s) * 16);
     }
-    const int sw = four_scales(ws, b, blocks);
+    const int sw = scales_at<N>(ws, b, blocks);
     int sa[MT];
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
 #pragma unroll
-      for (int s = 0; s < 4; ++s) a[t][s] = i32x4{0, 0, 0, 0};
+      for (int s = 0; s < N; ++s) a[t][s] = i32x4{0, 0, 0, 0};
       if constexpr (std::is_void_v<X>) {
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
+        for (int s = 0; s < N; ++s)
           if (b + s < blocks) a[t][s] = *reinterpret_cast<const i32x4*>(ac[t] + int64_t(b + s) * 16);
-        sa[t] = four_scales(as[t], b, blocks);
+        sa[t] = scales_at<N>(as[t], b, blocks);
       } else {
         const X* x = static_cast<const X*>(L.x) + int64_t(min(m0 + t * 16 + r, L.M - 1)) * L.K;
         sa[t] = 0;
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
+        for (int s = 0; s < N; ++s)
           if (b + s < blocks) sa[t] |= quantize_block(x + (b + s) * 32, a[t][s]) << (8 * s);
       }
     }
-    each<4>([&](auto s) {
+    each<N>([&](auto s) {
 #pragma unroll
       for (int t = 0; t < MT; ++t) acc[t] = product<s.value, s.value>(w[s.value], a[t][s.value], acc[t], sw, sa[t]);
     });
@@ -515,11 +522,11 @@ __global__ __launch_bounds__(WGM* WGN * 64) void mx_tile_kernel(MxLaunch L, int 
   }
 }
 
-template <int MT, int WAVES, typename E, typename X>
+template <int MT, int WAVES, int N, typename E, typename X>
 hipError_t rows_product(const MxLaunch& L, hipStream_t stream) {
   const int cols = (L.N + 15) / 16;
   const int64_t grid = int64_t(cols) * ((L.M + 16 * MT - 1) / (16 * MT));
-  mx_rows_kernel<MT, WAVES, E, X><<<uint32_t(grid), WAVES * 64, 0, stream>>>(L, cols);
+  mx_rows_kernel<MT, WAVES, N, E, X><<<uint32_t(grid), WAVES * 64, 0, stream>>>(L, cols);
   return hipGetLastError();
 }
 
@@ -529,6 +536,11 @@ hipError_t tile_product(const MxLaunch& L, hipStream_t stream) {
   mx_tile_kernel<BM, BN, WGM, WGN, DEPTH, E><<<uint32_t(rows) * uint32_t(cols), WGM * WGN * 64, 0, stream>>>(L, rows, cols);
   return hipGetLastError();
 }
+
+// Up to FUSED_ROWS rows are quantized inside the product: one launch less (3 us
+// of a call), and 16 rows are little to quantize again in every workgroup; at 64
+// rows that took longer than the launch.
+constexpr int FUSED_ROWS = 16;
 
 // Which kernel, by the number of workgroups each would have (us for a product
 // of M x N x K with the choice, and with the one it was taken over):
@@ -548,9 +560,10 @@ hipError_t tile_product(const MxLaunch& L, hipStream_t stream) {
 template <typename E>
 hipError_t matmul(const MxLaunch& L, hipStream_t stream) {
   auto count = [&](int64_t m, int64_t n) { return (L.M + m - 1) / m * ((L.N + n - 1) / n); };
-  if (count(16, 16) <= 256) return rows_product<1, 16, E, void>(L, stream);
+  if (count(16, 16) <= 256)
+    return L.M <= FUSED_ROWS ? rows_product<1, 16, 2, E, void>(L, stream) : rows_product<1, 16, 4, E, void>(L, stream);
   const int64_t rows = count(32, 16);
-  if (rows <= 256 || (rows <= 448 && rows * L.K <= 1 << 20)) return rows_product<2, 8, E, void>(L, stream);
+  if (rows <= 256 || (rows <= 448 && rows * L.K <= 1 << 20)) return rows_product<2, 8, 4, E, void>(L, stream);
   if (count(64, 64) <= 512) return tile_product<64, 64, 2, 2, 512, E>(L, stream);
   if (count(256, 256) >= 192) return tile_product<256, 256, 2, 2, 256, E>(L, stream);
   if (count(128, 128) <= 256) return tile_product<128, 128, 2, 2, 512, E>(L, stream);
@@ -583,15 +596,10 @@ hipError_t launch_mx_matmul(const MxLaunch& L, hipStream_t stream) {
   return L.out_bf16 ? matmul<bf16>(L, stream) : matmul<float>(L, stream);
 }
 
-// Up to FUSED_ROWS rows are quantized inside the product: one launch less (3 us
-// of a call), and 16 rows are little to quantize again in every workgroup; at 64
-// rows that took longer than the launch.
-constexpr int FUSED_ROWS = 16;
-
 hipError_t launch_mx_linear(const MxLaunch& L, hipStream_t stream) {
   if (L.M <= FUSED_ROWS) {
-    if (L.in_bf16) return L.out_bf16 ? rows_product<1, 16, bf16, bf16>(L, stream) : rows_product<1, 16, float, bf16>(L, stream);
-    return L.out_bf16 ? rows_product<1, 16, bf16, float>(L, stream) : rows_product<1, 16, float, float>(L, stream);
+    if (L.in_bf16) return L.out_bf16 ? rows_product<1, 16, 2, bf16, bf16>(L, stream) : rows_product<1, 16, 2, float, bf16>(L, stream);
+    return L.out_bf16 ? rows_product<1, 16, 2, bf16, float>(L, stream) : rows_product<1, 16, 2, float, float>(L, stream);
   }
   if (hipError_t e = launch_mx_quantize(L.x, L.M, L.K, L.in_bf16, const_cast<uint8_t*>(L.a_codes),
                                         const_cast<uint8_t*>(L.a_scales), stream))

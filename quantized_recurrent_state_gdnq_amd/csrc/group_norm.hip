@@ -12,7 +12,7 @@
 // and the outputs need no second read.  The variance is the mean of the
 // centred squares, in fp32.
 // Measured, gated bf16: 32768 x 16 groups of 128 forward 82 us (4.9 TB/s),
-// backward 127 (5.3 TB/s); 16384 groups of 5120 forward 100 (5.0 TB/s).
+// backward 127 (5.3 TB/s); 16384 groups of 5120 forward 96 (5.2 TB/s).
 //   TEAM: the fewest lanes (8 .. 64) that hold the group with eight values
 //   each; above 512 values a workgroup (TEAM = BLOCK) of as many waves as that
 //   takes, with eight or sixteen values a lane (see forward_eights).

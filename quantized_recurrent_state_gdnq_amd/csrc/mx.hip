@@ -228,7 +228,7 @@ __global__ __launch_bounds__(WAVES * 64) void mx_rows_kernel(MxLaunch L, int col
 
 // ---------------------------------------------------------------- many rows
 //
-// Bound by the matrix units: 16384 x 8192 x 4096 takes 313 us, 3.5 PFLOP/s.  A
+// Bound by the matrix units: 16384 x 8192 x 4096 takes 318 us, 3.5 PFLOP/s.  A
 // step of 256 x 256 x 256 takes 1.76 us, at the instruction's own rate 0.85;
 // without its loads into LDS 1.39; the clock falls to 2.0 GHz meanwhile.  A tile
 // costs 11 us beside its steps, more than half of it to write its results.

@@ -28,7 +28,7 @@
 // Bound by memory in fp32: 262144 x 640 forward 365 us, 5.6 TB/s.  In bf16 the
 // vector instructions weigh as much: 32768 x 2048 forward with given gates 98
 // us (4.1 TB/s), with logits 108; 32768 x 5120 with logits, 48 sequences:
-// forward 239, backward 370 us (4.3 and 4.7 TB/s).
+// forward 237, backward 368 us (4.4 and 4.7 TB/s).
 #include <hip/hip_runtime.h>
 
 #include "../../include/gdnq.h"

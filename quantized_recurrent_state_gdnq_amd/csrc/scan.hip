@@ -249,16 +249,19 @@ __device__ __forceinline__ void put(f32x2* p, const float (&a)[V], const float (
   for (int i = 0; i < V; ++i) p[i] = f32x2{a[i], h[i]};
 }
 
-// (a, h) := the pair at p after (a, h).  Behind a border (cut) h does not
-// enter at all: a NaN or an infinity of one sequence is not multiplied by the
-// next one's zero.
+// (a, h) := the pair (pa, ph) after (a, h).  Behind a border (cut) neither
+// enters: the pair is the border's own, (0, ph).  As products with its zero a
+// NaN or an infinity of one sequence would reach the next one.
+__device__ __forceinline__ void join(float pa, float ph, bool cut, float& a, float& h) {
+  h = cut ? ph : fmaf(pa, h, ph);
+  a = cut ? 0.0f : a * pa;
+}
+
+// The same with the pair of every channel at p.
 template <int V>
 __device__ __forceinline__ void then(const f32x2* p, bool cut, float (&a)[V], float (&h)[V]) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    h[i] = fmaf(p[i].x, cut ? 0.0f : h[i], p[i].y);
-    a[i] *= p[i].x;
-  }
+  for (int i = 0; i < V; ++i) join(p[i].x, p[i].y, cut, a[i], h[i]);
 }
 
 // Which waves of the workgroup have a border in their run (bit per wave).
@@ -331,14 +334,14 @@ __device__ __forceinline__ void leave_chunk(const Chain& chain, int place, int C
   float ga[V], gh[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const f32x2 p = f.so_far[lane * V + i];
-    ga[i] = a[i] * p.x;
-    gh[i] = fmaf(a[i], cut ? 0.0f : p.y, h[i]);
+    ga[i] = f.so_far[lane * V + i].x;
+    gh[i] = f.so_far[lane * V + i].y;
+    join(a[i], h[i], cut, ga[i], gh[i]);
   }
   publish<V>(chain.group + int64_t(place / GROUP) * C + c, ga, gh);
   if (place % (GROUP * GROUP) != GROUP * GROUP - 1) return;
 #pragma unroll
-  for (int i = 0; i < V; ++i) gh[i] = fmaf(a[i], cut ? 0.0f : f.carry[lane * V + i], h[i]);
+  for (int i = 0; i < V; ++i) gh[i] = cut ? h[i] : fmaf(a[i], f.carry[lane * V + i], h[i]);
   publish<V>(chain.state + int64_t(place / (GROUP * GROUP)) * C + c, ga, gh);
 }
 
@@ -448,8 +451,8 @@ __global__ __launch_bounds__(ForwardShape<V>::WAVES * 64, ForwardShape<V>::PER_S
     if (wave == WAVES - 1) {  // the chunk's pair
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        H[i] = fmaf(A[i], rows.start ? 0.0f : ph[i], H[i]);
-        A[i] *= pa[i];
+        H[i] = rows.start ? H[i] : fmaf(A[i], ph[i], H[i]);
+        A[i] = cuts ? 0.0f : A[i] * pa[i];
       }
       if (active) publish<V>(chain.pair + int64_t(chunk) * C + c, A, H);
     }
@@ -463,7 +466,7 @@ __global__ __launch_bounds__(ForwardShape<V>::WAVES * 64, ForwardShape<V>::PER_S
 
   float h[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) h[i] = fmaf(pa[i], cuts & ((1u << wave) - 1) ? 0.0f : in[i], ph[i]);
+  for (int i = 0; i < V; ++i) h[i] = cuts & ((1u << wave) - 1) ? ph[i] : fmaf(pa[i], in[i], ph[i]);
   if (L.carry && wave % (GDNQ_SCAN_CHUNK / RUN) == 0 && active && row0 < L.N) {
 #pragma unroll
     for (int i = 0; i < V; ++i) L.carry[int64_t(row0 / GDNQ_SCAN_CHUNK) * C + c + i] = h[i];
@@ -648,8 +651,8 @@ __global__ __launch_bounds__(BWD_WAVES * 64, BWD_PER_SIMD) void scan_backward_ke
     if (wave == 0) {  // the chunk's pair
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        M[i] = fmaf(H[i], border ? 0.0f : pm[i], M[i]);
-        H[i] *= pa[i];
+        M[i] = border ? M[i] : fmaf(H[i], pm[i], M[i]);
+        H[i] = cuts ? 0.0f : H[i] * pa[i];
       }
       if (active) publish<V>(chain.pair + int64_t(place) * C + c, H, M);
     }
@@ -661,7 +664,7 @@ __global__ __launch_bounds__(BWD_WAVES * 64, BWD_PER_SIMD) void scan_backward_ke
   }
   float m[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) m[i] = fmaf(pa[i], cuts >> (wave + 1) ? 0.0f : in[i], pm[i]);
+  for (int i = 0; i < V; ++i) m[i] = cuts >> (wave + 1) ? pm[i] : fmaf(pa[i], in[i], pm[i]);
 
   float before[RUN][V];
 #pragma unroll

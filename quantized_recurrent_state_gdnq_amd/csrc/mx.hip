@@ -277,14 +277,17 @@ struct Stage {
   // order.  As an empty-handed statement (it writes no register), because the
   // compiler waits for all such loads before any read of LDS when it knows of
   // them, whichever buffer is read; the kernel waits itself (vmcnt) before the
-  // barrier that lets the buffer be read.
+  // barrier that lets the buffer be read.  The s_nop is the wait that a load
+  // into LDS needs behind a scalar write of M0, where the chip takes its place
+  // in LDS from; inside a statement the compiler adds none.  The compiler warns
+  // that M0 is a reserved register: nothing else in this file uses it.
   __device__ __forceinline__ static void to_lds(const uint8_t* base, uint32_t offset, uint8_t* to) {
     const uint32_t lds = uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)to));
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(offset), "s"(base) : "m0", "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(offset), "s"(base) : "m0", "memory");
   }
   __device__ __forceinline__ static void to_lds(const uint8_t* p, uint8_t* to) {
     const uint32_t lds = uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)to));
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(p) : "m0", "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(p) : "m0", "memory");
   }
   // Loads the step from block k0 on to LDS at `to`.
   __device__ __forceinline__ void load(uint8_t* to, int k0, int wave) const {

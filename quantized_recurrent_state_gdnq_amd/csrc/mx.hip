@@ -128,7 +128,8 @@ __device__ __forceinline__ void store4(E* y, int M, int N, int m, int n, const f
 // scale loads took 7.8 us for 32 x 4096 x 4096, against 5.8); where rows are
 // quantized here two, so that more waves share that (1 x 4096 x 4096: 6.0 us,
 // with four 7.6; 16 x 4096 x 4096: 8.0, 8.9).  As many rows in codes take two as
-// well (5.4 us for 16, with four 5.0): both calls then add in the same order.
+// well (5.4 us for 16, with four 5.0), so that mx_linear and mx_matmul of the
+// same rows add in the same order.
 
 // Scales of blocks b .. b + N - 1 of a row (beyond its end 0).
 template <int N>
@@ -540,15 +541,24 @@ hipError_t tile_product(const MxLaunch& L, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Up to FUSED_ROWS rows are quantized inside the product: one launch less (3 us
-// of a call), and 16 rows are little to quantize again in every workgroup; at 64
-// rows that took longer than the launch.
+// Up to FUSED_ROWS rows are quantized inside the product where it has at most
+// one workgroup per CU: one launch less, and 16 rows are little to quantize
+// again in every workgroup; at 64 rows that took longer than the launch.  (us
+// on the GPU, one launch and two, 1 and 16 rows: 4096 columns x 512: 3.7 and 3.9,
+// 4.4 and 4.6; x 4096: 6.0 and 7.9, 6.1 and 7.5; x 8192: 10.4 and 15.1, 9.3 and
+// 11.3, where the second launch's 2 us of host time still make up for it.  With
+// more columns a CU quantizes the rows again and again: 16384 x 4096: 19.4 and
+// 28.2, 13.2 and 13.0; 32768 x 4096: 34.9 and 55.0, 17.7 and 17.7.)
 constexpr int FUSED_ROWS = 16;
+bool fused(const MxLaunch& L) { return L.M <= FUSED_ROWS && L.N <= 256 * 16; }
 
 // Which kernel, by the number of workgroups each would have (us for a product
 // of M x N x K with the choice, and with the one it was taken over):
 //   few rows, 16 of them and 16 waves: at most one workgroup per CU
 //     (16 x 4096 x 4096: 4.6, 64 x 64 tiles 6.3; 64 x 1024 x 8192: 6.9, 10.0);
+//     for up to 16 rows two per CU from a depth of 1024 on (1 and 16 rows x 8192 x
+//     4096: 6.8 and 8.4, by the rules below 9.9 and 10.0; x 8192 x 1024: 3.5 and
+//     4.0, 4.0 and 4.1; but x 4112 x 512: 2.9 and 3.0, 2.8 and 2.9);
 //   few rows, 32 of them: also up to 448 where the depth is small enough that
 //     reading A in each of them costs little (32 x 4096 x 4096: 5.7, 6.3; 192 x
 //     1111 x 2080: 4.3, 7.1; but 192 x 1024 x 8192: 15.6, 10.3);
@@ -563,8 +573,8 @@ constexpr int FUSED_ROWS = 16;
 template <typename E>
 hipError_t matmul(const MxLaunch& L, hipStream_t stream) {
   auto count = [&](int64_t m, int64_t n) { return (L.M + m - 1) / m * ((L.N + n - 1) / n); };
-  if (count(16, 16) <= 256)
-    return L.M <= FUSED_ROWS ? rows_product<1, 16, 2, E, void>(L, stream) : rows_product<1, 16, 4, E, void>(L, stream);
+  if (L.M <= FUSED_ROWS && count(16, 16) <= (L.K >= 1024 ? 512 : 256)) return rows_product<1, 16, 2, E, void>(L, stream);
+  if (count(16, 16) <= 256) return rows_product<1, 16, 4, E, void>(L, stream);
   const int64_t rows = count(32, 16);
   if (rows <= 256 || (rows <= 448 && rows * L.K <= 1 << 20)) return rows_product<2, 8, 4, E, void>(L, stream);
   if (count(64, 64) <= 512) return tile_product<64, 64, 2, 2, 512, E>(L, stream);
@@ -600,7 +610,7 @@ hipError_t launch_mx_matmul(const MxLaunch& L, hipStream_t stream) {
 }
 
 hipError_t launch_mx_linear(const MxLaunch& L, hipStream_t stream) {
-  if (L.M <= FUSED_ROWS) {
+  if (fused(L)) {
     if (L.in_bf16) return L.out_bf16 ? rows_product<1, 16, 2, bf16, bf16>(L, stream) : rows_product<1, 16, 2, float, bf16>(L, stream);
     return L.out_bf16 ? rows_product<1, 16, 2, bf16, float>(L, stream) : rows_product<1, 16, 2, float, float>(L, stream);
   }

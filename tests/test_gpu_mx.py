@@ -242,3 +242,11 @@ def test_refusals():
     with pytest.raises(_lib.GdnqError, match="ALIAS"):
         codes = torch.zeros(8, 64, device=DEV)
         ops.mx_quantize(codes, codes.view(torch.uint8).view(-1)[:256].view(8, 32))
+
+
+@pytest.mark.parametrize("rows", [1, 2, 9, 16])
+@pytest.mark.parametrize("cols,K", [(4096, 544), (4112, 544), (4097, 1056), (8192, 1024), (8193, 1056), (8208, 992), (33000, 96)])
+def test_few_rows_many_columns(rows, cols, K):
+    """On both sides of the numbers of columns at which the kernel changes;
+    fp32 results show the order of the sums, which is the same in both calls."""
+    check_product(random_rows(rows, K, rows, torch.bfloat16), random_rows(cols, K, cols + 1), torch.float32)

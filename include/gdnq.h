@@ -604,7 +604,8 @@ gdnq_status gdnq_group_norm_backward(const gdnq_norm_params* p, const void* x, c
  *   0 <= rows <= 2^30; 1 <= cols <= 2^25; 32 <= depth <= 2^20; rows depth
  *   and cols depth up to 2^40; ceil(rows / 256) ceil(cols / 256) < 2^24.
  *   in_dtype is not read by gdnq_mx_matmul.  flags must be 0.
- *   workspace: gdnq_mx_workspace_size(p) bytes, enough for either call.
+ *   workspace: gdnq_mx_workspace_size(p) bytes for gdnq_mx_linear;
+ *   gdnq_mx_matmul needs none (NULL, 0).
  *   Errors: NULL, SHAPE, DTYPE, ALIGN, ALIAS, FLAGS, WORKSPACE, HIP.
  * ------------------------------------------------------------------------ */
 typedef struct {

@@ -847,7 +847,7 @@ gdnq_status gdnq_mx_quantize(const void* x, int64_t rows, int32_t depth, int32_t
 
 static size_t mx_align(size_t n) { return (n + 255) / 256 * 256; }
 
-// The quantized activations of gdnq_mx_linear come first, then the product's own workspace.
+// The quantized activations of gdnq_mx_linear.
 static size_t mx_quantized_bytes(const gdnq::MxLaunch& L) {
   return mx_align(size_t(L.M) * L.K / 2) + mx_align(size_t(L.M) * L.K / 32);
 }
@@ -855,7 +855,7 @@ static size_t mx_quantized_bytes(const gdnq::MxLaunch& L) {
 size_t gdnq_mx_workspace_size(const gdnq_mx_params* p) {
   gdnq::MxLaunch L;
   if (mx_validate(p, false, L) != GDNQ_OK) return 0;
-  return mx_quantized_bytes(L) + gdnq::mx_matmul_workspace_bytes(L.M, L.N, L.K);
+  return mx_quantized_bytes(L);
 }
 
 gdnq_status gdnq_mx_matmul(const gdnq_mx_params* p, const uint8_t* a_codes, const uint8_t* a_scales,
@@ -864,15 +864,13 @@ gdnq_status gdnq_mx_matmul(const gdnq_mx_params* p, const uint8_t* a_codes, cons
   gdnq::MxLaunch L;
   if (gdnq_status st = mx_validate(p, false, L)) return st;
   if (L.M == 0) return ok();
-  const size_t need = gdnq::mx_matmul_workspace_bytes(L.M, L.N, L.K);
   const Span sp[] = {{"a_codes", a_codes, size_t(L.M) * L.K / 2}, {"a_scales", a_scales, size_t(L.M) * L.K / 32},
                      {"w_codes", w_codes, size_t(L.N) * L.K / 2}, {"w_scales", w_scales, size_t(L.N) * L.K / 32},
-                     {"y", y, size_t(L.M) * L.N * esize(p->out_dtype)}, {"workspace", workspace, need}};
+                     {"y", y, size_t(L.M) * L.N * esize(p->out_dtype)}};
   if (gdnq_status st = check_ptrs(sp, 5)) return st;
-  if (gdnq_status st = check_workspace(workspace, workspace_bytes, need)) return st;
-  if (gdnq_status st = check_disjoint(sp, 6, 4)) return st;
+  if (gdnq_status st = check_workspace(workspace, workspace_bytes, 0)) return st;
+  if (gdnq_status st = check_disjoint(sp, 5, 4)) return st;
   L.a_codes = a_codes; L.a_scales = a_scales; L.w_codes = w_codes; L.w_scales = w_scales; L.y = y;
-  L.workspace = workspace;
   clear_stale_hip_error();
   return launched(gdnq::launch_mx_matmul(L, static_cast<hipStream_t>(stream)), "mx product launch", stream);
 }
@@ -883,7 +881,7 @@ gdnq_status gdnq_mx_linear(const gdnq_mx_params* p, const void* x, const uint8_t
   gdnq::MxLaunch L;
   if (gdnq_status st = mx_validate(p, true, L)) return st;
   if (L.M == 0) return ok();
-  const size_t quantized = mx_quantized_bytes(L), need = quantized + gdnq::mx_matmul_workspace_bytes(L.M, L.N, L.K);
+  const size_t need = mx_quantized_bytes(L);
   const Span sp[] = {{"x", x, size_t(L.M) * L.K * esize(p->in_dtype)},
                      {"w_codes", w_codes, size_t(L.N) * L.K / 2}, {"w_scales", w_scales, size_t(L.N) * L.K / 32},
                      {"y", y, size_t(L.M) * L.N * esize(p->out_dtype)}, {"workspace", workspace, need}};
@@ -893,7 +891,6 @@ gdnq_status gdnq_mx_linear(const gdnq_mx_params* p, const void* x, const uint8_t
   uint8_t* codes = static_cast<uint8_t*>(workspace);
   uint8_t* scales = codes + mx_align(size_t(L.M) * L.K / 2);
   L.a_codes = codes; L.a_scales = scales; L.w_codes = w_codes; L.w_scales = w_scales; L.y = y;
-  L.workspace = codes + quantized;
   L.x = x; L.in_bf16 = p->in_dtype == GDNQ_BF16;
   clear_stale_hip_error();
   return launched(gdnq::launch_mx_linear(L, static_cast<hipStream_t>(stream)), "mx linear launch", stream);

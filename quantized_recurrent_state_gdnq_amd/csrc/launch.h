@@ -139,13 +139,11 @@ struct MxLaunch {
   const uint8_t* w_scales;
   const void* x;  // launch_mx_linear: the rows, whose codes go to a_codes, a_scales
   void* y;
-  void* workspace;
   int M, N, K;
   bool in_bf16, out_bf16;
 };
 hipError_t launch_mx_quantize(const void* x, int64_t rows, int K, bool bf16, uint8_t* codes, uint8_t* scales,
                               hipStream_t stream);
-size_t mx_matmul_workspace_bytes(int M, int N, int K);
 hipError_t launch_mx_matmul(const MxLaunch& L, hipStream_t stream);
 hipError_t launch_mx_linear(const MxLaunch& L, hipStream_t stream);
 

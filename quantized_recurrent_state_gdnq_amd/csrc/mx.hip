@@ -603,8 +603,6 @@ hipError_t launch_mx_quantize(const void* x, int64_t rows, int K, bool is_bf16, 
   return hipSuccess;
 }
 
-size_t mx_matmul_workspace_bytes(int, int, int) { return 0; }
-
 hipError_t launch_mx_matmul(const MxLaunch& L, hipStream_t stream) {
   return L.out_bf16 ? matmul<bf16>(L, stream) : matmul<float>(L, stream);
 }

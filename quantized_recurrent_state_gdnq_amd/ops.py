@@ -818,7 +818,7 @@ def mx_quantize(x, codes=None, scales=None):
 
 
 def mx_workspace_size(rows, cols, depth):
-    """Workspace bytes of mx_matmul and mx_linear at these sizes."""
+    """Workspace bytes of mx_linear at these sizes (mx_matmul needs none)."""
     return int(_lib.mx_workspace_size(_lib.MxParams(rows, cols, depth, 0, 0, 0)))
 
 
@@ -843,7 +843,7 @@ def mx_matmul(a_codes, a_scales, w_codes, w_scales, *, out_dtype=torch.bfloat16,
     _mx_weights(w_codes, w_scales, depth, dev)
     y = _mx_out(y, lead, w_codes.shape[0], out_dtype, dev)
     p = _lib.MxParams(_mx_rows(a_codes), w_codes.shape[0], depth, 0, _DT[out_dtype], 0)
-    ws, ws_bytes = _space(workspace, int(_lib.mx_workspace_size(p)), dev)
+    ws, ws_bytes = _space(workspace, 0, dev)
     _launch(dev, _lib.mx_matmul, p, _ptr(a_codes), _ptr(a_scales), _ptr(w_codes), _ptr(w_scales), _ptr(y),
             _ptr(ws), ws_bytes)
     return y

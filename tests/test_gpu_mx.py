@@ -250,3 +250,15 @@ def test_few_rows_many_columns(rows, cols, K):
     """On both sides of the numbers of columns at which the kernel changes;
     fp32 results show the order of the sums, which is the same in both calls."""
     check_product(random_rows(rows, K, rows, torch.bfloat16), random_rows(cols, K, cols + 1), torch.float32)
+
+
+def test_product_allocates_its_result_alone():
+    ac, asc = ops.mx_quantize(torch.zeros(2048, 4096, device=DEV))
+    wc, wsc = ops.mx_quantize(torch.zeros(64, 4096, device=DEV))
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    y = ops.mx_matmul(ac, asc, wc, wsc)
+    assert torch.cuda.max_memory_allocated() - before == y.numel() * 2  # 256 KiB; the rows' codes are 4 MiB
+    given = torch.empty(64, dtype=torch.uint8, device=DEV)  # one that is given is not used, whatever its size
+    assert torch.equal(ops.mx_matmul(ac, asc, wc, wsc, workspace=given), y)

@@ -588,6 +588,13 @@ def _optional(t, name, dtype, device, shape):
     return None if t is None else _checked(t, name, dtype, device, shape)
 
 
+def _sizes(a, b, c=0):
+    """The C parameters hold 32 bits, and ctypes would go on with the low ones
+    of a larger size."""
+    if a > 0x7fffffff or b > 0x7fffffff or c > 0x7fffffff:
+        raise ValueError(f"sizes {a}, {b}, {c}: at most 2^31 - 1 each")
+
+
 def _space(workspace, need, dev):
     """The caller's workspace (any contiguous tensor of the device) or a new
     one, and its size in bytes."""
@@ -618,6 +625,7 @@ def _scan_setup(x, gate, cu_seqlens, logits, lerp):
         B, (T, C) = cu_seqlens.numel() - 1, x.shape
         n = T
     _checked(gate, "gate", x.dtype, dev, x.shape)
+    _sizes(B, T, C)
     p = _lib.ScanParams(B, T, C, _DT[x.dtype], (_lib.GDNQ_SCAN_LOGITS if logits else 0)
                         | (_lib.GDNQ_SCAN_LERP if lerp else 0))
     return p, B, C, (-(-n // _lib.GDNQ_SCAN_CHUNK), C)
@@ -625,11 +633,9 @@ def _scan_setup(x, gate, cu_seqlens, logits, lerp):
 
 def scan_workspace_size(x, cu_seqlens=None):
     """Workspace bytes of gated_scan and gated_scan_backward for these arrays."""
-    if cu_seqlens is None:
-        p = _lib.ScanParams(x.shape[0], x.shape[1], x.shape[2], _DT[x.dtype], 0)
-    else:
-        p = _lib.ScanParams(cu_seqlens.numel() - 1, x.shape[0], x.shape[1], _DT[x.dtype], 0)
-    return int(_lib.scan_workspace_size(p, cu_seqlens is not None))
+    B, T, C = x.shape if cu_seqlens is None else (cu_seqlens.numel() - 1, *x.shape)
+    _sizes(B, T, C)
+    return int(_lib.scan_workspace_size(_lib.ScanParams(B, T, C, _DT[x.dtype], 0), cu_seqlens is not None))
 
 
 def gated_scan(x, gate, h0=None, cu_seqlens=None, *, logits=False, lerp=False, save=False, y=None, h_last=None,
@@ -695,7 +701,9 @@ def gated_scan_step(x, gate, h, *, logits=False, lerp=False, h_out=None, y=None)
     _checked(h, "h", torch.float32, dev, x.shape)
     h_out = h if h_out is None else _checked(h_out, "h_out", torch.float32, dev, x.shape)
     y = torch.empty_like(x) if y is None else _checked(y, "y", x.dtype, dev, x.shape)
-    p = _lib.ScanParams(x.shape[0], 1, x.shape[1], _DT[x.dtype], (_lib.GDNQ_SCAN_LOGITS if logits else 0)
+    B, C = x.shape
+    _sizes(B, C)
+    p = _lib.ScanParams(B, 1, C, _DT[x.dtype], (_lib.GDNQ_SCAN_LOGITS if logits else 0)
                         | (_lib.GDNQ_SCAN_LERP if lerp else 0))
     _launch(dev, _lib.scan_step, p, _ptr(x), _ptr(gate), _ptr(h), _ptr(h_out), _ptr(y))
     return y
@@ -727,6 +735,7 @@ def _norm_setup(x, weight, bias, gate, act, center, eps):
     rows = 1
     for s in x.shape[:-2]:
         rows *= s
+    _sizes(rows, G, D)
     p = _lib.NormParams(rows, G, D, _DT[x.dtype], _ACTS[act], eps, (_lib.GDNQ_NORM_CENTER if center else 0)
                         | (_lib.GDNQ_NORM_SHARED if shape == (D,) else 0))
     return p, shape
@@ -751,6 +760,7 @@ def group_norm_workspace_size(x):
     rows = 1
     for s in x.shape[:-2]:
         rows *= s
+    _sizes(rows, G, D)
     return int(_lib.group_norm_workspace_size(_lib.NormParams(rows, G, D, _DT[x.dtype], 0, 0.0, 0)))
 
 
@@ -808,6 +818,7 @@ def mx_quantize(x, codes=None, scales=None):
     if x.dim() < 1 or x.shape[-1] % 32:
         raise ValueError("x must be [..,depth] with depth a multiple of 32")
     depth = x.shape[-1]
+    _sizes(0, depth)  # the rows are 64 bits
     cshape, sshape = x.shape[:-1] + (depth // 2,), x.shape[:-1] + (depth // 32,)
     codes = torch.empty(cshape, dtype=torch.uint8, device=dev) if codes is None else codes
     scales = torch.empty(sshape, dtype=torch.uint8, device=dev) if scales is None else scales
@@ -819,6 +830,7 @@ def mx_quantize(x, codes=None, scales=None):
 
 def mx_workspace_size(rows, cols, depth):
     """Workspace bytes of mx_linear at these sizes (mx_matmul needs none)."""
+    _sizes(rows, cols, depth)
     return int(_lib.mx_workspace_size(_lib.MxParams(rows, cols, depth, 0, 0, 0)))
 
 
@@ -842,7 +854,9 @@ def mx_matmul(a_codes, a_scales, w_codes, w_scales, *, out_dtype=torch.bfloat16,
     _checked(a_scales, "a_scales", torch.uint8, dev, lead + (depth // 32,))
     _mx_weights(w_codes, w_scales, depth, dev)
     y = _mx_out(y, lead, w_codes.shape[0], out_dtype, dev)
-    p = _lib.MxParams(_mx_rows(a_codes), w_codes.shape[0], depth, 0, _DT[out_dtype], 0)
+    rows, cols = _mx_rows(a_codes), w_codes.shape[0]
+    _sizes(rows, cols, depth)
+    p = _lib.MxParams(rows, cols, depth, 0, _DT[out_dtype], 0)
     ws, ws_bytes = _space(workspace, 0, dev)
     _launch(dev, _lib.mx_matmul, p, _ptr(a_codes), _ptr(a_scales), _ptr(w_codes), _ptr(w_scales), _ptr(y),
             _ptr(ws), ws_bytes)
@@ -863,7 +877,9 @@ def mx_linear(x, w_codes, w_scales, *, out_dtype=None, y=None, workspace=None):
     _mx_weights(w_codes, w_scales, depth, dev)
     out_dtype = out_dtype or (x.dtype if y is None else y.dtype)
     y = _mx_out(y, x.shape[:-1], w_codes.shape[0], out_dtype, dev)
-    p = _lib.MxParams(_mx_rows(x), w_codes.shape[0], depth, _DT[x.dtype], _DT[out_dtype], 0)
+    rows, cols = _mx_rows(x), w_codes.shape[0]
+    _sizes(rows, cols, depth)
+    p = _lib.MxParams(rows, cols, depth, _DT[x.dtype], _DT[out_dtype], 0)
     ws, ws_bytes = _space(workspace, int(_lib.mx_workspace_size(p)), dev)
     _launch(dev, _lib.mx_linear, p, _ptr(x), _ptr(w_codes), _ptr(w_scales), _ptr(y), _ptr(ws), ws_bytes)
     return y

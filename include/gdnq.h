@@ -538,8 +538,8 @@ gdnq_status gdnq_scan_step(const gdnq_scan_params* p, const void* x, const void*
  *       y = n act(gate),  or act(n) when gate is NULL
  *
  *   p->rows R >= 0 tokens, p->groups G >= 1, p->width D in 1 .. 16384 (a
- *   multiple of 8 is faster), R G <= 2^31 - 1, G D < 2^26 without
- *   GDNQ_NORM_SHARED; p->dtype (x, gate, y and their gradients) GDNQ_F32 or
+ *   multiple of 8 is faster), R G <= 2^31 - 1, G <= 2^20, G D <= 2^26 - 16
+ *   without GDNQ_NORM_SHARED; p->dtype (x, gate, y and their gradients) GDNQ_F32 or
  *   GDNQ_BF16; p->eps >= 0, finite;
  *   p->act GDNQ_ACT_NONE, GDNQ_ACT_SILU or GDNQ_ACT_SIGMOID (with gate: not
  *   GDNQ_ACT_NONE, which would be a plain product).

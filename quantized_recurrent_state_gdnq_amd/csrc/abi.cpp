@@ -739,8 +739,8 @@ static gdnq_status norm_validate(const gdnq_norm_params* p, bool gate, gdnq::Nor
   if (int64_t(p->rows) * p->groups > 0x7fffffffLL || p->groups > (1 << 20))
     return fail(GDNQ_ERR_SHAPE, "rows * groups = %lld: at most 2^31 - 1, and 2^20 groups", (long long)p->rows * p->groups);
   // a workgroup of 1024 threads adds 16 weights' gradients, and a launch has fewer than 2^32 threads
-  if (!(p->flags & GDNQ_NORM_SHARED) && int64_t(p->groups) * p->width >= 1 << 26)
-    return fail(GDNQ_ERR_SHAPE, "groups * width = %lld: less than 2^26 unless weights are shared", (long long)p->groups * p->width);
+  if (!(p->flags & GDNQ_NORM_SHARED) && int64_t(p->groups) * p->width > (1 << 26) - 16)
+    return fail(GDNQ_ERR_SHAPE, "groups * width = %lld: at most 2^26 - 16 unless weights are shared", (long long)p->groups * p->width);
   if (!dtype_ok(p->dtype)) return fail(GDNQ_ERR_DTYPE, "dtype = %d", p->dtype);
   if (!(p->eps >= 0.0f) || p->eps > 3.0e38f) return fail(GDNQ_ERR_SHAPE, "eps = %g, expected a finite value >= 0", double(p->eps));
   if (p->act < GDNQ_ACT_NONE || p->act > GDNQ_ACT_SIGMOID) return fail(GDNQ_ERR_FLAGS, "act = %d", p->act);

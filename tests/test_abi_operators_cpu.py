@@ -241,3 +241,18 @@ def test_mx_launch_limit(M, N, fits):
     if not fits:
         assert matmul(p) == SHAPE
         assert linear(p) == SHAPE
+
+
+@pytest.mark.parametrize("G,D,fits", [(8193, 8191, False), (17159, 3911, False), (8188, 8196, True)])
+def test_norm_backward_launch_limit(G, D, fits):
+    """Just below 2^26 weights: the launch that adds their gradients has 1024
+    threads per 16 of them, rounded up."""
+    assert 2 ** 26 - 16 <= G * D < 2 ** 26
+    assert fits == (-(-G * D // 16) * 1024 < 2 ** 32)
+    p = norm_p(R=0, G=G, D=D)
+    if fits:
+        assert norm(p) == 0
+    else:
+        refused(norm(p), SHAPE, "2^26")
+        refused(norm_backward(p), SHAPE, "2^26")
+        assert _lib.group_norm_workspace_size(p) == 0

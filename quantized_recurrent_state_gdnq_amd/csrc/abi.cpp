@@ -774,7 +774,7 @@ gdnq_status gdnq_group_norm(const gdnq_norm_params* p, const void* x, const void
 size_t gdnq_group_norm_workspace_size(const gdnq_norm_params* p) {
   gdnq::NormLaunch L;
   if (norm_validate(p, false, L) != GDNQ_OK) return 0;
-  return gdnq::norm_workspace_bytes(L.R, L.G, L.D);
+  return gdnq::norm_workspace_bytes(L.R, L.G, L.D, L.shared);
 }
 
 gdnq_status gdnq_group_norm_backward(const gdnq_norm_params* p, const void* x, const void* gate,
@@ -784,7 +784,7 @@ gdnq_status gdnq_group_norm_backward(const gdnq_norm_params* p, const void* x, c
   gdnq::NormLaunch L;
   if (gdnq_status st = norm_validate(p, gate != nullptr, L)) return st;
   const size_t n = size_t(L.R) * L.G * L.D * esize(p->dtype), w = size_t(L.shared ? 1 : L.G) * L.D * 4;
-  const size_t need = gdnq::norm_workspace_bytes(L.R, L.G, L.D);
+  const size_t need = gdnq::norm_workspace_bytes(L.R, L.G, L.D, L.shared);
   const Span sp[] = {{"x", x, n}, {"dy", dy, n}, {"gate", gate, n}, {"weight", weight, w}, {"bias", bias, w},
                      {"dx", dx, n}, {"dgate", dgate, n}, {"dweight", dweight, w}, {"dbias", dbias, w},
                      {"workspace", workspace, need}};

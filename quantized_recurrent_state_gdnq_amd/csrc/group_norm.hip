@@ -456,8 +456,8 @@ hipError_t dispatch(const NormLaunch& L, hipStream_t s) {
 
 }  // namespace
 
-size_t norm_workspace_bytes(int R, int G, int D) {
-  return size_t(slots_of(int64_t(R) * G, G, D, backward_eights(D), BACKWARD_WAVES)) * D * 2 * 4;
+size_t norm_workspace_bytes(int R, int G, int D, bool shared) {
+  return size_t(slots_of(int64_t(R) * G, shared ? 1 : G, D, backward_eights(D), BACKWARD_WAVES)) * D * 2 * 4;
 }
 
 hipError_t launch_norm_forward(const NormLaunch& L, hipStream_t stream) { return dispatch<Forward>(L, stream); }

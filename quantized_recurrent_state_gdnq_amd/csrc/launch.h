@@ -127,7 +127,7 @@ struct NormLaunch {
   float eps;
   bool bf16, center, shared;
 };
-size_t norm_workspace_bytes(int R, int G, int D);
+size_t norm_workspace_bytes(int R, int G, int D, bool shared);
 hipError_t launch_norm_forward(const NormLaunch& L, hipStream_t stream);
 hipError_t launch_norm_backward(const NormLaunch& L, hipStream_t stream);
 

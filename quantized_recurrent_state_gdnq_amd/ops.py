@@ -755,13 +755,15 @@ def group_norm(x, weight=None, bias=None, gate=None, *, act="none", center=False
 
 
 def group_norm_workspace_size(x):
-    """Workspace bytes of group_norm_backward for x [..,groups,width]."""
+    """Workspace bytes of group_norm_backward for x [..,groups,width], enough
+    for weights of the groups' own and for shared ones."""
     G, D = x.shape[-2:]
     rows = 1
     for s in x.shape[:-2]:
         rows *= s
     _sizes(rows, G, D)
-    return int(_lib.group_norm_workspace_size(_lib.NormParams(rows, G, D, _DT[x.dtype], 0, 0.0, 0)))
+    return max(int(_lib.group_norm_workspace_size(_lib.NormParams(rows, G, D, _DT[x.dtype], 0, 0.0, flags)))
+               for flags in (0, _lib.GDNQ_NORM_SHARED))
 
 
 def group_norm_backward(dy, x, weight=None, bias=None, gate=None, *, act="none", center=False, eps=1e-5, dx=None,

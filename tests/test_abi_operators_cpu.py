@@ -6,8 +6,9 @@ dereferences; every call below fails validation or has nothing to do, so no
 kernel is launched."""
 
 import pytest
+import torch
 
-from quantized_recurrent_state_gdnq_amd import _lib
+from quantized_recurrent_state_gdnq_amd import _lib, ops
 
 L = _lib.lib
 NULL, SHAPE, DTYPE, ALIGN, ALIAS, WORKSPACE, FLAGS = 1, 2, 3, 4, 5, 6, 8
@@ -256,3 +257,23 @@ def test_norm_backward_launch_limit(G, D, fits):
         refused(norm(p), SHAPE, "2^26")
         refused(norm_backward(p), SHAPE, "2^26")
         assert _lib.group_norm_workspace_size(p) == 0
+
+
+def test_norm_workspace_of_shared_weights():
+    """Teams that share the weights need no more rows of partial sums than the
+    chip holds teams: 256 CUs, 16 waves each, 8 teams of 8 lanes a wave, 64
+    values of two gradients."""
+    p = norm_p(R=4, G=2 ** 20, D=64, flags=2)
+    assert 0 < _lib.group_norm_workspace_size(p) <= 256 * 16 * 8 * 64 * 2 * 4
+    # and no fewer than one row for own weights
+    assert _lib.group_norm_workspace_size(norm_p(R=4, G=2 ** 19, D=64)) >= 2 ** 19 * 64 * 2 * 4
+    assert _lib.group_norm_workspace_size(norm_p(R=1, G=2 ** 20, D=64, flags=2)) > 0
+
+
+def test_norm_workspace_of_a_tensor():
+    """Of either kind of weights: where groups may not have their own, of shared ones."""
+    x = torch.empty((4, 2 ** 20, 64), dtype=torch.bfloat16, device="meta")
+    shared = _lib.group_norm_workspace_size(norm_p(R=4, G=2 ** 20, D=64, flags=2))
+    assert ops.group_norm_workspace_size(x) == shared
+    x = torch.empty((4, 30, 64), dtype=torch.bfloat16, device="meta")
+    assert ops.group_norm_workspace_size(x) == _lib.group_norm_workspace_size(norm_p(R=4, G=30, D=64))

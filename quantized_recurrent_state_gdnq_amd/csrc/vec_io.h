@@ -24,8 +24,11 @@ __device__ __forceinline__ void store_f32(bf16* p, float x) { *p = bf16(x); }
 // -|z| log2(e) in two parts (product and its rounding error), its reciprocal
 // one Newton step.
 //   bf16: neither, 12 instruction slots instead of 21 (2^x and the reciprocal
-// are four each): off by up to |z| 2^-24 and a few units, where the results
-// are rounded to 2^-8 or are sums of many such terms.
+// are four each): the smaller side is off by up to 1.25 |z| 2^-24 of itself and a
+// few units.  Results in bf16 are rounded to 2^-8; the fp32 ones of such calls
+// (states, their gradients, weights' gradients) carry it, beside inputs that
+// were rounded to 2^-8 (20 units for a gate of e^-16).
+//   Either way a smaller side under 2^-126 (|z| above 87.3) is 0.
 template <typename E>
 __device__ __forceinline__ float sigmoid_tail(float z) {
   if constexpr (sizeof(E) == 2) {
@@ -33,7 +36,7 @@ __device__ __forceinline__ float sigmoid_tail(float z) {
     return copysignf(u * __builtin_amdgcn_rcpf(1.0f + u), z);
   } else {
     float m = -fabsf(z);
-    m = m < -128.0f ? -128.0f : m;  // u is 0 from -104 on (infinities, the type's lowest value); NaN passes
+    m = m < -128.0f ? -128.0f : m;  // u is 0 there (infinities, the type's lowest value); NaN passes
     const float t = m * 1.44269504f;
     const float low = fmaf(m, 1.44269504f, -t) + m * 1.92596299e-8f;  // log2(e) = 1.44269504 + 1.926e-8
     const float e = __builtin_amdgcn_exp2f(t);

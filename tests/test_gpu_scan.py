@@ -430,3 +430,24 @@ def test_refusals():
     with pytest.raises(_lib.GdnqError, match="ALIGN"):
         flat = torch.zeros(2 * 4 * 8 + 1, device=DEV)
         ops.gated_scan(x, flat[1:].view(2, 4, 8))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_large_logits(dtype):
+    """a and 1 - a alone in a state (fp32, whatever the call's type), over all
+    logits whose smaller side is a normal number.  K units; in bf16 calls the
+    exponent z log2(e) is a rounded product with a rounded constant (1.44269504,
+    off by 0.23 u of itself), which adds 1.25 |z| units to the smaller side."""
+    z = torch.linspace(-87, 87, 4096).to(dtype)
+    zero, one = torch.zeros_like(z)[None], torch.ones_like(z)[None]
+    state = torch.ones((1, z.numel()), device=DEV)
+    a, keep = state.clone(), torch.zeros_like(state)
+    ops.gated_scan_step(zero.to(DEV), z[None].to(DEV), a, logits=True)
+    ops.gated_scan_step(one.to(DEV), z[None].to(DEV), keep, logits=True, lerp=True)
+    v = np64(z)
+    for got, want, small in ((a, 1 / (1 + np.exp(-v)), v < 0), (keep, 1 / (1 + np.exp(v)), v > 0)):
+        units = K + (1.25 * np.abs(v) if dtype == torch.bfloat16 else 0.0)
+        tail = np.exp(-np.abs(v)) / (1 + np.exp(-np.abs(v)))
+        tol = np.where(small, units * U * want, units * U * tail + K * U)
+        err = np.abs(got[0].double().cpu().numpy() - want)
+        assert (err <= tol).all(), (np.max(err / tol), v[np.argmax(err / tol)])

@@ -463,15 +463,18 @@ gdnq_status gdnq_prefill_resume(const gdnq_prefill_params* p, const int32_t* cu_
  *   a_t = gate_t, or sigmoid(gate_t) with GDNQ_SCAN_LOGITS;
  *   b_t = x_t,    or (1 - a_t) x_t   with GDNQ_SCAN_LERP (1 - a is formed
  *   without cancellation from logits).  The state is fp32 throughout; y is h
- *   rounded once to the call's dtype.
+ *   rounded once to the call's dtype.  Gates that are given as they are lie in
+ *   [-1, 1], or their products over up to 4096 adjacent tokens of a sequence
+ *   have to stay finite in fp32: pieces of a sequence are joined by these
+ *   products, and one that overflows makes a finite state NaN or infinite.
  *
  *   p->batch B sequences; p->seqlen T tokens each (cu_seqlens NULL, arrays
  *   [B,T,C]) or T packed tokens in total (cu_seqlens [B+1] int32 on the
  *   device as for gdnq_prefill_varlen, arrays [T,C]; sequences of length 0
  *   are allowed).  Tokens that no sequence holds (before cu_seqlens[0], from
- *   cu_seqlens[B] on) are left as they were in y, dx and dgate.  Offsets are
- *   clamped to [0, T]; malformed ones give unspecified results and no access
- *   outside the buffers.  p->channels C >= 1 (even C is faster in bf16);
+ *   cu_seqlens[B] on) are left as they were in y, dx and dgate.  Offsets that
+ *   fall or lie outside [0, T] give unspecified results and no access outside
+ *   the buffers.  p->channels C >= 1 (even C is faster in bf16);
  *   p->dtype (x, gate, y and their gradients) GDNQ_F32 or GDNQ_BF16; B >= 0,
  *   T >= 0, at most 2^31 - 4097 tokens, B C <= 2^31 - 1 and
  *   ceil(tokens / GDNQ_SCAN_CHUNK) ceil(C / 64) < 2^22.

@@ -641,8 +641,8 @@ def scan_workspace_size(x, cu_seqlens=None):
 def gated_scan(x, gate, h0=None, cu_seqlens=None, *, logits=False, lerp=False, save=False, y=None, h_last=None,
                carry=None, workspace=None):
     """Gated linear recurrence over channels (see gdnq_scan_* in
-    include/gdnq.h): h_t = a_t h_{t-1} + b_t with a = gate (logits=True:
-    sigmoid(gate)) and b = x (lerp=True: (1 - a) x).
+    include/gdnq.h): h_t = a_t h_{t-1} + b_t with a = gate, in [-1, 1]
+    (logits=True: sigmoid(gate)), and b = x (lerp=True: (1 - a) x).
 
     x, gate [B,T,C], or [T,C] with cu_seqlens (int32 on the device, B+1
     offsets of the packed sequences), fp32 or bf16; h0 [B,C] fp32 or None.

@@ -6,13 +6,23 @@
 //   dhat = dn w,  dx = rstd (dhat - [center] mean(dhat) - hat mean(dhat hat))
 //   dw = sum dn hat,  db = sum dn   (over tokens; over groups too when shared)
 //
-// Bound by memory: every array is read or written once.  A group (one head of
-// one token) is held in the registers of a team of TEAM lanes, EIGHTS times
-// eight values each, so the statistics, the second sum of the backward pass
-// and the outputs need no second read.  The variance is the mean of the
-// centred squares, in fp32.
+// Every array is read or written once.  A group (one head of one token) is
+// held in the registers of a team of TEAM lanes, EIGHTS times eight values
+// each, so the statistics, the second sum of the backward pass and the outputs
+// need no second read.  The variance is the mean of the centred squares, in
+// fp32.
 // Measured, gated bf16: 32768 x 16 groups of 128 forward 82 us (4.9 TB/s),
-// backward 127 (5.3 TB/s); 16384 groups of 5120 forward 96 (5.2 TB/s).
+// backward 127 (5.3 TB/s); 16384 groups of 5120 forward 96 (5.2 TB/s).  Bound
+// by memory from groups of about 48 aligned values on; not
+//   below: a team has eight lanes of eight values, so of groups of 8 seven lanes
+//     in eight idle (100 M values in bf16, forward and backward: groups of 8 603
+//     and 999 us, of 16 284 and 486, of 24 189 and 338, of 48 101 and 182);
+//   in the backward pass above 8192 values, where two eights of everything do
+//     not fit the registers and 119 to 278 of a lane's are kept in scratch (100
+//     M values in bf16: groups of 12288 715 us, of 16384 675, of 16383 965; 50 M
+//     in fp32: 427, 420 and 465);
+//   in the backward pass of unaligned bf16 (100 M values: groups of 171 283 us,
+//     of 333 294, of 4999 370).
 //   TEAM: the fewest lanes (8 .. 64) that hold the group with eight values
 //   each; above 512 values a workgroup (TEAM = BLOCK) of as many waves as that
 //   takes, with eight or sixteen values a lane (see forward_eights).
@@ -370,11 +380,15 @@ int teams_in(int D) { return team_of(D) == BLOCK ? 1 : THREADS / team_of(D); }
 // Teams of a call: those of as many workgroups as the chip's 256 CUs hold at
 // once, which then take the same number of groups each, rounded up to a
 // multiple of G (the groups of a token, 1 for shared weights) so that a team's
-// groups share their weights.  Waves a CU holds by the kernels' registers (a
-// grid of more than that runs a part of its workgroups after the others:
-// 20000 x 4999 bf16 forward 199 us with 32, 156 with 28):
+// groups share their weights.  FORWARD_WAVES, waves of a CU in the forward
+// grid, are as measured.  A grid of more than the registers hold runs a part of
+// its workgroups after the others: 20000 x 4999 bf16 199 us with 32, 156 with
+// 28; 20000 x 8 groups of 256 fp32 97 with 32, 94 with 28.  As many as they
+// hold is not always better: above 512 values in aligned bf16 they hold 20
+// (16384 x 5120: 115 us, with 16 96), up to 512 in unaligned bf16 32 (40000 x 16
+// groups of 100: 94, with 28 95).
 template <typename E, int TEAM, bool WIDE, int EIGHTS>
-constexpr int FORWARD_WAVES = EIGHTS == 2 ? 16 : WIDE && (TEAM != BLOCK || sizeof(E) == 2) ? 32 : 28;
+constexpr int FORWARD_WAVES = EIGHTS == 2 ? 16 : WIDE && sizeof(E) == 2 ? 32 : 28;
 constexpr int BACKWARD_WAVES = 16;
 
 // Eights of a lane where a group takes a workgroup: two above 8192 values, and
@@ -383,7 +397,8 @@ constexpr int BACKWARD_WAVES = 16;
 //   117 with one; 8192 x 5120 fp32 103 and 96);
 //   of unaligned groups above 7168, of whose 15 waves a CU holds only one group
 //   (16384 x 7169: 188 us, 234 with one; 16384 x 5121 158 and 130).
-// The backward pass spills with two.
+// The backward pass spills with two, so it takes them only above 8192 values,
+// where one would need more than 1024 threads.
 template <typename E, bool WIDE>
 int forward_eights(int D) { return (WIDE && sizeof(E) == 2) || D > (WIDE ? 8192 : 7168) ? 2 : 1; }
 int backward_eights(int D) { return D <= 8192 ? 1 : 2; }

@@ -229,10 +229,12 @@ __global__ __launch_bounds__(WAVES * 64) void mx_rows_kernel(MxLaunch L, int col
 
 // ---------------------------------------------------------------- many rows
 //
-// Bound by the matrix units: 16384 x 8192 x 4096 takes 318 us, 3.5 PFLOP/s.  A
-// step of 256 x 256 x 256 takes 1.76 us, at the instruction's own rate 0.85;
-// without its loads into LDS 1.39; the clock falls to 2.0 GHz meanwhile.  A tile
-// costs 11 us beside its steps, more than half of it to write its results.
+// Bound by the matrix units: 16384 x 8192 x 4096 takes 314 us of a call, 3.5
+// PFLOP/s (under the profiler 325 to 348).  A step of 256 x 256 x 256 takes 1.76
+// us, at the instruction's own rate 0.85; without its loads into LDS 1.39; the
+// clock falls to 2.0 GHz meanwhile.  A tile costs 11 us beside its 16 steps, more
+// than half of it to write its results; a CU works on one tile at a time, and
+// nothing of that is hidden.
 //   A workgroup computes BM x BN of y, its WGM x WGN
 // waves an equal part each, in steps of DEPTH values (256, or 512 for small
 // tiles): the step's rows of both operands are loaded straight into LDS, in two
@@ -561,7 +563,8 @@ bool fused(const MxLaunch& L) { return L.M <= FUSED_ROWS && L.N <= 256 * 16; }
 //     4.0, 4.0 and 4.1; but x 4112 x 512: 2.9 and 3.0, 2.8 and 2.9);
 //   few rows, 32 of them: also up to 448 where the depth is small enough that
 //     reading A in each of them costs little (32 x 4096 x 4096: 5.7, 6.3; 192 x
-//     1111 x 2080: 4.3, 7.1; but 192 x 1024 x 8192: 15.6, 10.3);
+//     1111 x 2080: 4.3, 7.1; but 192 x 1024 x 8192: 15.6, 10.3; the border
+//     between them rests on these three);
 //   64 x 64 tiles, of which a CU holds two: up to 512, in steps of 512, since a
 //     step takes its loads' latency (64 x 4096 x 4096: 6.5, in steps of 256
 //     8.1, 128 x 128 tiles 11.9; 512 x 4096 x 4096: 11.6, 128 x 128 13.0);

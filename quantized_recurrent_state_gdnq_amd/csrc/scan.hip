@@ -25,10 +25,14 @@
 // starts as all ones, which no published pair has), so a single relaxed
 // 8-byte atomic is the whole hand-over.
 //
-// Bound by memory in fp32: 262144 x 640 forward 365 us, 5.6 TB/s.  In bf16 the
-// vector instructions weigh as much: 32768 x 2048 forward with given gates 98
-// us (4.1 TB/s), with logits 108; 32768 x 5120 with logits, 48 sequences:
-// forward 237, backward 368 us (4.4 and 4.7 TB/s).
+// Bound by memory in fp32: 262144 x 640 forward 365 us, 5.6 TB/s; 65536 x 1024
+// backward 222, 6.0 TB/s.  In bf16 the vector instructions weigh as much: 32768
+// x 2048 forward 98 us a call with given gates (4.1 TB/s), 109 with logits (the
+// kernel 104 of it, 115 to 117 under the profiler); 65536 x 2048 backward with
+// given gates 258 (5.2 TB/s); 32768 x 5120 with logits, 48 sequences: forward
+// 236, backward 370 (4.4 and 4.7 TB/s).  An odd number of channels takes one a
+// lane: 65536 x 1023 forward 142, backward 196 (2.8 and 3.4 TB/s).  All but the
+// calls' by the profiler's medians.
 #include <hip/hip_runtime.h>
 
 #include "../../include/gdnq.h"
@@ -741,6 +745,8 @@ __global__ __launch_bounds__(256) void scan_begin_kernel(uint32_t* ticket, int t
   }
 }
 
+// One value a lane: 64 x 4096 takes 2.8 us, little more than a launch; 1024 x
+// 8192 in bf16 17.9 us (117 MB, in part from the last-level cache), fp32 21.7 (168 MB).
 template <typename E, bool LOGITS, bool LERP>
 __global__ __launch_bounds__(256) void scan_step_kernel(ScanLaunch L) {
   const int64_t n = int64_t(L.B) * L.C, i = blockIdx.x * int64_t(256) + threadIdx.x;

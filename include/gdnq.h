@@ -630,6 +630,85 @@ gdnq_status gdnq_mx_linear(const gdnq_mx_params* p, const void* x, const uint8_t
                            void* stream);
 
 /* ------------------------------------------------------------------------
+ * gdnq_delta_* -- the gated delta rule as a model is trained with it, and
+ *   served with its state in fp32: whole or packed sequences in chunks, their
+ *   gradients, and one token per sequence.  No quantization, no window.
+ *
+ *       S_t = alpha_t S_{t-1} (I - beta_t k_t k_t^T) + beta_t v_t k_t^T
+ *       o_t = S_t q_t                       (q, k as given; S [d_v, d_k] fp32)
+ *
+ *   p->batch B sequences; p->seqlen T tokens each (cu_seqlens NULL, arrays
+ *   [B,T,..]) or T packed tokens in total (cu_seqlens [B+1] int32 on the device
+ *   as for gdnq_prefill_varlen, arrays [T,..]; sequences of length 0 are
+ *   allowed).  Tokens that no sequence holds are left as they were in every
+ *   output.  Offsets that fall or lie outside [0, T] give unspecified results
+ *   and no access outside the buffers.
+ *   p->key_heads G, p->heads H, a multiple of G: value head h reads the q and k
+ *   of key head h / (H / G), whose gradients are summed over its value heads.
+ *   d_k a multiple of 8, 8 .. 128 (gdnq_delta_step: .. 256); d_v a multiple of
+ *   8, 8 .. 1024.  Multiples of 16 are faster, and d_k of 64 or 128.
+ *     q, k        [.., G, d_k] bf16       v  [.., H, d_v] bf16
+ *     alpha, beta [.., H] fp32: alpha in [0, 1]; with GDNQ_DELTA_LOG alpha holds
+ *                 log alpha, at most 0, and dalpha is the gradient of that.  A
+ *                 chunked call takes a decay under 2^-64 (also alpha = 0) as
+ *                 2^-64, less than a state's rounding.
+ *     h0          [B,H,d_v,d_k] fp32 or NULL (zero)
+ *   gdnq_delta_forward
+ *     o           [.., H, d_v] out_dtype (GDNQ_F32 or GDNQ_BF16)
+ *     h_last      [B,H,d_v,d_k] fp32 or NULL (not wanted): the state after each
+ *                 sequence (h0 for length 0)
+ *     carry       gdnq_delta_carry_size bytes or NULL: what the backward pass
+ *                 needs of this call (states entering the chunks, writes)
+ *   gdnq_delta_backward: gradients from dout [.., H, d_v] bf16 and dh_last
+ *     ([B,H,d_v,d_k] fp32 or NULL = zero), with the forward call's q, k, alpha,
+ *     beta, cu_seqlens, flags and carry:
+ *     dq, dk [.., G, d_k] bf16, dv [.., H, d_v] bf16, dalpha, dbeta [.., H] fp32,
+ *     dh0 [B,H,d_v,d_k] fp32 or NULL (not wanted)
+ *   gdnq_delta_step: one token per sequence (p->seqlen must be 1): q, k [B,G,d_k],
+ *     v, o [B,H,d_v] (in_dtype and out_dtype GDNQ_F32 or GDNQ_BF16), alpha, beta
+ *     [B,H] fp32, h read and h_out written [B,H,d_v,d_k] fp32 (h_out may be h
+ *     itself: the state updated in place).
+ *   in_dtype of the chunked calls must be GDNQ_BF16; gdnq_delta_backward does
+ *   not read out_dtype.  Products of fp32 values take them in two bf16 parts (16
+ *   bits and more), sums and states are fp32; o, dq, dk and dv are rounded once.
+ *   Results do not depend on the order in which workgroups run.  A NaN or
+ *   infinity stays in its own sequence and head, and reaches back at most to the
+ *   first token of its chunk of 64.
+ *   Outputs must not overlap inputs or each other (but h_out = h).
+ *   workspace: gdnq_delta_workspace_size(p, varlen, backward) bytes; its contents
+ *   need no initial value.  Calls that may overlap in time take workspaces of
+ *   their own.
+ *   B >= 0, T >= 0, at most 2^31 - 1 tokens, 64-token chunks (of all sequences;
+ *   packed: T / 64 + B) times H < 2^24, B H ceil(d_v / 64) < 2^24.
+ *   Errors: NULL, SHAPE, DTYPE, ALIGN (cu_seqlens: 4 bytes), ALIAS, FLAGS,
+ *   WORKSPACE, HIP.
+ * ------------------------------------------------------------------------ */
+enum { GDNQ_DELTA_LOG = 1u /* alpha holds log alpha */ };
+
+typedef struct {
+  int32_t batch, seqlen, key_heads, heads, d_k, d_v, in_dtype, out_dtype;
+  uint32_t flags;
+} gdnq_delta_params;
+
+size_t gdnq_delta_workspace_size(const gdnq_delta_params* p, int32_t varlen, int32_t backward);
+size_t gdnq_delta_carry_size(const gdnq_delta_params* p, int32_t varlen);
+
+gdnq_status gdnq_delta_forward(const gdnq_delta_params* p, const int32_t* cu_seqlens, const void* q,
+                               const void* k, const void* v, const float* alpha, const float* beta,
+                               const float* h0, void* o, float* h_last, void* carry, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+gdnq_status gdnq_delta_backward(const gdnq_delta_params* p, const int32_t* cu_seqlens, const void* q,
+                                const void* k, const float* alpha, const float* beta, const void* carry,
+                                const void* dout, const float* dh_last, void* dq, void* dk, void* dv,
+                                float* dalpha, float* dbeta, float* dh0, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+gdnq_status gdnq_delta_step(const gdnq_delta_params* p, const void* q, const void* k, const void* v,
+                            const float* alpha, const float* beta, const float* h, float* h_out, void* o,
+                            void* stream);
+
+/* ------------------------------------------------------------------------
  * gdnq_decode_set_schedule -- tuning hook of gdnq_decode_step's persistent
  *   launch (not part of the method; results do not depend on it).
  *   grid: workgroups of the persistent grid; open_waves: waves that take the

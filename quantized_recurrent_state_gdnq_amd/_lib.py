@@ -28,6 +28,7 @@ GDNQ_SCAN_LOGITS, GDNQ_SCAN_LERP = 1, 2
 GDNQ_SCAN_CHUNK = 128
 GDNQ_ACT_NONE, GDNQ_ACT_SILU, GDNQ_ACT_SIGMOID = 0, 1, 2
 GDNQ_NORM_CENTER, GDNQ_NORM_SHARED = 1, 2
+GDNQ_DELTA_LOG = 1
 
 # Every function the header declares.
 EXPORTS = ("gdnq_quantize_state", "gdnq_decode_step", "gdnq_prefill_workspace_size",
@@ -37,6 +38,8 @@ EXPORTS = ("gdnq_quantize_state", "gdnq_decode_step", "gdnq_prefill_workspace_si
            "gdnq_scan_workspace_size", "gdnq_scan_forward", "gdnq_scan_backward", "gdnq_scan_step",
            "gdnq_group_norm", "gdnq_group_norm_workspace_size", "gdnq_group_norm_backward",
            "gdnq_mx_quantize", "gdnq_mx_workspace_size", "gdnq_mx_matmul", "gdnq_mx_linear",
+           "gdnq_delta_workspace_size", "gdnq_delta_carry_size", "gdnq_delta_forward", "gdnq_delta_backward",
+           "gdnq_delta_step",
            "gdnq_decode_set_schedule", "gdnq_status_string", "gdnq_last_error", "gdnq_version",
            "gdnq_sync_debug")
 
@@ -67,6 +70,12 @@ class NormParams(ctypes.Structure):
 
 class MxParams(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int32), ("cols", ctypes.c_int32), ("depth", ctypes.c_int32),
+                ("in_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
+class DeltaParams(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("seqlen", ctypes.c_int32), ("key_heads", ctypes.c_int32),
+                ("heads", ctypes.c_int32), ("d_k", ctypes.c_int32), ("d_v", ctypes.c_int32),
                 ("in_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("flags", ctypes.c_uint32)]
 
 
@@ -133,6 +142,16 @@ def _load():
     lib.gdnq_mx_matmul.restype = i32
     lib.gdnq_mx_linear.argtypes = [ctypes.POINTER(MxParams)] + [vp] * 5 + [sz, vp]
     lib.gdnq_mx_linear.restype = i32
+    lib.gdnq_delta_workspace_size.argtypes = [ctypes.POINTER(DeltaParams), i32, i32]
+    lib.gdnq_delta_workspace_size.restype = sz
+    lib.gdnq_delta_carry_size.argtypes = [ctypes.POINTER(DeltaParams), i32]
+    lib.gdnq_delta_carry_size.restype = sz
+    lib.gdnq_delta_forward.argtypes = [ctypes.POINTER(DeltaParams)] + [vp] * 11 + [sz, vp]
+    lib.gdnq_delta_forward.restype = i32
+    lib.gdnq_delta_backward.argtypes = [ctypes.POINTER(DeltaParams)] + [vp] * 15 + [sz, vp]
+    lib.gdnq_delta_backward.restype = i32
+    lib.gdnq_delta_step.argtypes = [ctypes.POINTER(DeltaParams)] + [vp] * 9
+    lib.gdnq_delta_step.restype = i32
     lib.gdnq_decode_set_schedule.argtypes = [i32, i32]
     lib.gdnq_decode_set_schedule.restype = i32
     lib.gdnq_status_string.argtypes = [i32]
@@ -278,3 +297,26 @@ def mx_matmul(params, a_codes, a_scales, w_codes, w_scales, y, workspace, worksp
 def mx_linear(params, x, w_codes, w_scales, y, workspace, workspace_bytes, stream):
     return lib.gdnq_mx_linear(ctypes.byref(params), x, w_codes, w_scales, y, workspace, workspace_bytes,
                               stream)
+
+
+def delta_workspace_size(params, varlen, backward):
+    return lib.gdnq_delta_workspace_size(ctypes.byref(params), int(varlen), int(backward))
+
+
+def delta_carry_size(params, varlen):
+    return lib.gdnq_delta_carry_size(ctypes.byref(params), int(varlen))
+
+
+def delta_forward(params, cu_seqlens, q, k, v, alpha, beta, h0, o, h_last, carry, workspace, workspace_bytes, stream):
+    return lib.gdnq_delta_forward(ctypes.byref(params), cu_seqlens, q, k, v, alpha, beta, h0, o, h_last, carry,
+                                  workspace, workspace_bytes, stream)
+
+
+def delta_backward(params, cu_seqlens, q, k, alpha, beta, carry, dout, dh_last, dq, dk, dv, dalpha, dbeta, dh0,
+                   workspace, workspace_bytes, stream):
+    return lib.gdnq_delta_backward(ctypes.byref(params), cu_seqlens, q, k, alpha, beta, carry, dout, dh_last, dq, dk,
+                                   dv, dalpha, dbeta, dh0, workspace, workspace_bytes, stream)
+
+
+def delta_step(params, q, k, v, alpha, beta, h, h_out, o, stream):
+    return lib.gdnq_delta_step(ctypes.byref(params), q, k, v, alpha, beta, h, h_out, o, stream)

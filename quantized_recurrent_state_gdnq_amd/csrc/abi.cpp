@@ -896,4 +896,129 @@ gdnq_status gdnq_mx_linear(const gdnq_mx_params* p, const void* x, const uint8_t
   return launched(gdnq::launch_mx_linear(L, static_cast<hipStream_t>(stream)), "mx linear launch", stream);
 }
 
+// ---------------------------------------------------------------- trained delta rule
+
+static gdnq_status delta_validate(const gdnq_delta_params* p, bool varlen, bool step, gdnq::DeltaLaunch& L) {
+  if (!p) return fail(GDNQ_ERR_NULL, "params is NULL");
+  if (p->batch < 0 || p->seqlen < 0) return fail(GDNQ_ERR_SHAPE, "batch = %d, seqlen = %d", p->batch, p->seqlen);
+  if (p->key_heads < 1 || p->heads < 1 || p->heads % p->key_heads)
+    return fail(GDNQ_ERR_SHAPE, "heads = %d, key_heads = %d: a positive multiple expected", p->heads, p->key_heads);
+  const int most = step ? 256 : 128;
+  if (p->d_k < 8 || p->d_k % 8 || p->d_k > most || p->d_v < 8 || p->d_v % 8 || p->d_v > 1024)
+    return fail(GDNQ_ERR_SHAPE, "d_k = %d, d_v = %d: multiples of 8, d_k up to %d, d_v up to 1024", p->d_k, p->d_v, most);
+  if (step ? !dtype_ok(p->in_dtype) : p->in_dtype != GDNQ_BF16) return fail(GDNQ_ERR_DTYPE, "in_dtype = %d", p->in_dtype);
+  if (!dtype_ok(p->out_dtype)) return fail(GDNQ_ERR_DTYPE, "out_dtype = %d", p->out_dtype);
+  if (p->flags & ~uint32_t(GDNQ_DELTA_LOG)) return fail(GDNQ_ERR_FLAGS, "flags 0x%x: the delta rule takes GDNQ_DELTA_LOG", p->flags);
+  L = gdnq::DeltaLaunch{};
+  L.B = p->batch; L.T = p->seqlen; L.G = p->key_heads; L.H = p->heads; L.dk = p->d_k; L.dv = p->d_v;
+  L.N = varlen ? int64_t(p->seqlen) : int64_t(p->batch) * p->seqlen;
+  L.in_bf16 = p->in_dtype == GDNQ_BF16;
+  L.out_bf16 = p->out_dtype == GDNQ_BF16;
+  L.log_decay = (p->flags & GDNQ_DELTA_LOG) != 0;
+  if (L.N > 0x7fffffffLL) return fail(GDNQ_ERR_SHAPE, "%lld tokens: at most 2^31 - 1", (long long)L.N);
+  // a workgroup of 256 threads per chunk and head, and per 64 rows of a state (a
+  // step: per four), and a launch has fewer than 2^32 threads
+  const int64_t slots = varlen ? L.N / 64 + L.B : int64_t(L.B) * ((L.T + 63) / 64);
+  const int64_t groups = step ? (L.dv + 31) / 32 : (L.dv + 63) / 64;
+  if (slots > (1 << 24) || slots * L.H >= 1 << 24 || int64_t(L.B) * L.H >= 1 << 24 || int64_t(L.B) * L.H * groups >= 1 << 24)
+    return fail(GDNQ_ERR_SHAPE, "%lld chunks, %d sequences of %d heads: too large", (long long)slots, L.B, L.H);
+  return GDNQ_OK;
+}
+
+size_t gdnq_delta_workspace_size(const gdnq_delta_params* p, int32_t varlen, int32_t backward) {
+  gdnq::DeltaLaunch L;
+  if (delta_validate(p, varlen != 0, false, L) != GDNQ_OK) return 0;
+  if (varlen) L.cu_seqlens = reinterpret_cast<const int32_t*>(4);  // only asked for being given
+  return backward ? gdnq::delta_backward_workspace_bytes(L) : gdnq::delta_forward_workspace_bytes(L);
+}
+
+size_t gdnq_delta_carry_size(const gdnq_delta_params* p, int32_t varlen) {
+  gdnq::DeltaLaunch L;
+  if (delta_validate(p, varlen != 0, false, L) != GDNQ_OK) return 0;
+  if (varlen) L.cu_seqlens = reinterpret_cast<const int32_t*>(4);
+  return gdnq::delta_carry_bytes(L);
+}
+
+gdnq_status gdnq_delta_forward(const gdnq_delta_params* p, const int32_t* cu_seqlens, const void* q,
+                               const void* k, const void* v, const float* alpha, const float* beta,
+                               const float* h0, void* o, float* h_last, void* carry, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  gdnq::DeltaLaunch L;
+  if (gdnq_status st = delta_validate(p, cu_seqlens != nullptr, false, L)) return st;
+  if (L.B == 0) return ok();
+  L.cu_seqlens = cu_seqlens;
+  const size_t key = size_t(L.N) * L.G * L.dk * 2, val = size_t(L.N) * L.H * L.dv, gate = size_t(L.N) * L.H * 4;
+  const size_t states = size_t(L.B) * L.H * L.dv * L.dk * 4, need = gdnq::delta_forward_workspace_bytes(L);
+  const Span sp[] = {{"q", q, key}, {"k", k, key}, {"v", v, val * 2}, {"alpha", alpha, gate}, {"beta", beta, gate},
+                     {"h0", h0, states}, {"o", o, val * esize(p->out_dtype)}, {"h_last", h_last, states},
+                     {"carry", carry, gdnq::delta_carry_bytes(L)}, {"workspace", workspace, need}};
+  constexpr int N = sizeof(sp) / sizeof(sp[0]);
+  if (L.N > 0) {
+    if (gdnq_status st = check_ptrs(sp, 5)) return st;
+    if (gdnq_status st = check_ptrs(sp + 6, 1)) return st;
+  }
+  if (gdnq_status st = check_optional(sp, N)) return st;
+  if (gdnq_status st = check_workspace(workspace, workspace_bytes, need)) return st;
+  if (gdnq_status st = check_disjoint(sp, N, 6)) return st;
+  if (gdnq_status st = check_offsets(cu_seqlens, L.B, sp, N, 6)) return st;
+  L.q = q; L.k = k; L.v = v; L.alpha = alpha; L.beta = beta; L.h0 = h0; L.o = o; L.h_last = h_last; L.carry = carry;
+  L.workspace = workspace;
+  L.rows_at = gdnq::delta_carry_rows_at(L);
+  clear_stale_hip_error();
+  return launched(gdnq::launch_delta_forward(L, static_cast<hipStream_t>(stream)), "delta rule launch", stream);
+}
+
+gdnq_status gdnq_delta_backward(const gdnq_delta_params* p, const int32_t* cu_seqlens, const void* q,
+                                const void* k, const float* alpha, const float* beta, const void* carry,
+                                const void* dout, const float* dh_last, void* dq, void* dk, void* dv,
+                                float* dalpha, float* dbeta, float* dh0, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  gdnq::DeltaLaunch L;
+  if (gdnq_status st = delta_validate(p, cu_seqlens != nullptr, false, L)) return st;
+  if (L.B == 0) return ok();
+  L.cu_seqlens = cu_seqlens;
+  const size_t key = size_t(L.N) * L.G * L.dk * 2, val = size_t(L.N) * L.H * L.dv * 2, gate = size_t(L.N) * L.H * 4;
+  const size_t states = size_t(L.B) * L.H * L.dv * L.dk * 4, need = gdnq::delta_backward_workspace_bytes(L);
+  const Span sp[] = {{"q", q, key}, {"k", k, key}, {"alpha", alpha, gate}, {"beta", beta, gate},
+                     {"carry", carry, gdnq::delta_carry_bytes(L)}, {"dout", dout, val}, {"dh_last", dh_last, states},
+                     {"dq", dq, key}, {"dk", dk, key}, {"dv", dv, val}, {"dalpha", dalpha, gate}, {"dbeta", dbeta, gate},
+                     {"dh0", dh0, states}, {"workspace", workspace, need}};
+  constexpr int N = sizeof(sp) / sizeof(sp[0]);
+  if (L.N > 0) {
+    if (gdnq_status st = check_ptrs(sp, 6)) return st;
+    if (gdnq_status st = check_ptrs(sp + 7, 5)) return st;
+  }
+  if (gdnq_status st = check_optional(sp, N)) return st;
+  if (gdnq_status st = check_workspace(workspace, workspace_bytes, need)) return st;
+  if (gdnq_status st = check_disjoint(sp, N, 7)) return st;
+  if (gdnq_status st = check_offsets(cu_seqlens, L.B, sp, N, 7)) return st;
+  L.q = q; L.k = k; L.alpha = alpha; L.beta = beta; L.carry = const_cast<void*>(carry); L.dout = dout; L.dh_last = dh_last;
+  L.dq = dq; L.dk_out = dk; L.dv_out = dv; L.dalpha = dalpha; L.dbeta = dbeta; L.dh0 = dh0; L.workspace = workspace;
+  L.rows_at = gdnq::delta_carry_rows_at(L);
+  clear_stale_hip_error();
+  return launched(gdnq::launch_delta_backward(L, static_cast<hipStream_t>(stream)), "delta rule backward launch", stream);
+}
+
+gdnq_status gdnq_delta_step(const gdnq_delta_params* p, const void* q, const void* k, const void* v,
+                            const float* alpha, const float* beta, const float* h, float* h_out, void* o,
+                            void* stream) {
+  gdnq::DeltaLaunch L;
+  if (gdnq_status st = delta_validate(p, false, true, L)) return st;
+  if (L.T != 1) return fail(GDNQ_ERR_SHAPE, "seqlen = %d: a step takes one token per sequence", L.T);
+  if (L.B == 0) return ok();
+  const size_t key = size_t(L.B) * L.G * L.dk * esize(p->in_dtype), val = size_t(L.B) * L.H * L.dv, gate = size_t(L.B) * L.H * 4;
+  const size_t states = size_t(L.B) * L.H * L.dv * L.dk * 4;
+  const Span sp[] = {{"q", q, key}, {"k", k, key}, {"v", v, val * esize(p->in_dtype)}, {"alpha", alpha, gate},
+                     {"beta", beta, gate}, {"h", h == h_out ? nullptr : h, states}, {"h_out", h_out, states},
+                     {"o", o, val * esize(p->out_dtype)}};
+  if (!h) return fail(GDNQ_ERR_NULL, "h is NULL");
+  if (gdnq_status st = check_ptrs(sp, 5)) return st;
+  if (gdnq_status st = check_ptrs(sp + 6, 2)) return st;
+  if (gdnq_status st = check_optional(sp, 8)) return st;
+  if (gdnq_status st = check_disjoint(sp, 8, 6)) return st;
+  L.q = q; L.k = k; L.v = v; L.alpha = alpha; L.beta = beta; L.h0 = h; L.h_last = h_out; L.o = o;
+  clear_stale_hip_error();
+  return launched(gdnq::launch_delta_step(L, static_cast<hipStream_t>(stream)), "delta rule step launch", stream);
+}
+
 }  // extern "C"

@@ -1,0 +1,149 @@
+// Shared parts of the trained delta rule (delta_rule.hip, delta_rule_backward.hip):
+// where chunks lie, what the workspace and the carry hold, and the layouts of
+// the matrix operands.
+//
+// A chunk is 64 tokens of one sequence, counted from the sequence's start.  With
+//   c_i   the running product of alpha inside the chunk, rho_ij = c_i / c_j,
+//   At_ij = rho_ij k_i.k_j (j < i),   M_ij = rho_ij q_i.k_j (j <= i),
+//   B     = diag(beta),   S the state that enters the chunk,
+// the chunk is
+//   w = (I + At B)^-1 (V - c K S^T),   u = B w      (w: what each token writes, u: times beta)
+//   O = c Q S^T + M u,                 S' = c_64 S + u^T (c_64 / c) K
+// and its gradient, from dS' and dO,
+//   du = M^T dO + (c_64 / c) K dS'^T,  z = (I + B At)^-T du,  dx = B z
+//   dS = c_64 dS' + dO^T c Q - dx^T c K,   dV = dx,   dbeta = w . z
+// (the rest at the gradient kernel).  Only S and dS pass from chunk to chunk,
+// and each of their rows by itself: a wave carries 16 rows.
+//
+// Operands of the products are bf16: q, k, v and dO as they are, fp32 values in
+// two parts, hi = bf16(x) and lo = bf16(x - hi), 16 to 17 significant bits; the
+// product of two lo parts (2^-18 of the term) is left out.  Sums are fp32.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "device_common.h"
+#include "launch.h"
+#include "mfma.h"
+#include "vec_io.h"
+
+namespace gdnq {
+
+constexpr int DELTA_CHUNK = 64;
+// A triangle of 64 x 64 as the first operand of a product: of its 16 x 32
+// blocks six are not zero.  A block is 64 lanes of 16 bytes; hi parts, then lo.
+constexpr int TRI_BLOCKS = 6, TRI_PART = TRI_BLOCKS * 1024, TRI_BYTES = 2 * TRI_PART;
+// Of one chunk of one value head in the workspace: two such triangles, then
+// five rows of 64: c, c_64 / c, beta, and log2 c as a whole number and a rest.
+constexpr int DELTA_SCALARS = 2 * TRI_BYTES;
+constexpr int DELTA_CHUNK_BYTES = DELTA_SCALARS + 5 * 256;
+
+inline int64_t delta_slots(const DeltaLaunch& L) {
+  return L.cu_seqlens ? L.N / DELTA_CHUNK + L.B : int64_t(L.B) * ((L.T + DELTA_CHUNK - 1) / DELTA_CHUNK);
+}
+__host__ __device__ inline int64_t delta_align(int64_t n) { return (n + 255) / 256 * 256; }
+// A state in two bf16 parts, [2][d_v][d_k].
+__host__ __device__ inline int64_t delta_state_bytes(const DeltaLaunch& L) { return int64_t(L.dv) * L.dk * 4; }
+
+#ifdef __HIPCC__
+
+struct DeltaSpan {
+  int64_t first, slot;  // first token in the call, first chunk slot
+  int tokens;
+};
+
+// The offsets of sequence b: malformed ones are clamped into [0, N].
+__device__ __forceinline__ int64_t delta_offset(const DeltaLaunch& L, int b) {
+  return min(max(int64_t(L.cu_seqlens[b]), int64_t(0)), L.N);
+}
+
+// Slots of packed sequences need no map: sequence b's start at cu[b] / 64 + b,
+// and those of the next lie far enough behind, since floor(y / 64) -
+// floor(x / 64) + 1 >= ceil((y - x) / 64).
+__device__ __forceinline__ DeltaSpan delta_sequence(const DeltaLaunch& L, int b) {
+  if (!L.cu_seqlens) {
+    const int chunks = (L.T + DELTA_CHUNK - 1) / DELTA_CHUNK;
+    return {int64_t(b) * L.T, int64_t(b) * chunks, L.T};
+  }
+  const int64_t first = delta_offset(L, b), end = delta_offset(L, b + 1);
+  return {first, first / DELTA_CHUNK + b, int(max(end - first, int64_t(0)))};
+}
+
+// The tokens of a slot: how many (0: none) and the first.
+__device__ __forceinline__ int delta_slot_tokens(const DeltaLaunch& L, int64_t slot, int64_t& first) {
+  int b;
+  if (!L.cu_seqlens) {
+    const int chunks = (L.T + DELTA_CHUNK - 1) / DELTA_CHUNK;
+    b = int(slot / chunks);
+  } else {
+    int low = 0, high = L.B - 1;  // the last sequence that starts at or before the slot
+    while (low < high) {
+      const int mid = (low + high + 1) / 2;
+      if (delta_offset(L, mid) / DELTA_CHUNK + mid <= slot)
+        low = mid;
+      else
+        high = mid - 1;
+    }
+    b = low;
+  }
+  const DeltaSpan s = delta_sequence(L, b);
+  const int64_t at = (slot - s.slot) * DELTA_CHUNK;
+  first = s.first + at;
+  return at < 0 ? 0 : int(min(int64_t(DELTA_CHUNK), s.tokens - at > 0 ? s.tokens - at : int64_t(0)));
+}
+
+// Rows of D bf16 in LDS in 16-byte blocks, permuted by the row's number so
+// that neither sixteen rows at one block nor the 4 rows x 32 (or 4 x 8) bytes of
+// a transposing read meet in a bank.
+template <int D>
+__device__ __forceinline__ int lds_block(int row, int block) {
+  if constexpr (D == 128)
+    return row * 256 + ((block ^ ((row & 3) << 2 | (row >> 2 & 3))) << 4);
+  else
+    return row * 128 + ((block ^ ((row >> 1 & 1) << 2 | (row >> 2 & 3))) << 4);
+}
+
+__device__ __forceinline__ bf16x8 lds_frag(const uint8_t* p) { return *reinterpret_cast<const bf16x8*>(p); }
+
+// 4 x 16 values of 16 bits per 16 lanes, transposed: lane 4 t + p gives the
+// address of four adjacent values of row t, lane i gets column i of four rows.
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ bf16x8 lds_transposed(const uint8_t* a, const uint8_t* b) {
+  typedef __attribute__((address_space(3))) s16x4* lds4;
+  const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(a));
+  const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(b));
+  typedef short s16x8 __attribute__((ext_vector_type(8)));
+  return __builtin_bit_cast(bf16x8, s16x8{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]});
+}
+
+// Two products of fp32 values in parts.
+__device__ __forceinline__ f32x4 mfma_exact_split(const bf16x8& a, const bf16x8& bh, const bf16x8& bl, f32x4 c) {
+  return mfma16(a, bh, mfma16(a, bl, c));
+}
+__device__ __forceinline__ f32x4 mfma_split_split(const bf16x8& ah, const bf16x8& al, const bf16x8& bh, const bf16x8& bl,
+                                                  f32x4 c) {
+  return mfma16(ah, bh, mfma16(ah, bl, mfma16(al, bh, c)));
+}
+
+__device__ __forceinline__ void split8(const f32x4& a, const f32x4& b, bf16x8& hi, bf16x8& lo) {
+  const float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+  split2(x, hi, lo);
+}
+
+// 2^(a - b) of numbers given as whole part and rest.
+__device__ __forceinline__ float exp2_difference(float ar, int aw, float br, int bw) {
+  return ldexpf(__builtin_amdgcn_exp2f(ar - br), aw - bw);
+}
+
+// In the chains a wave's tile it of 16 tokens holds, in row 4 g + e, token
+// 32 (it / 2) + 8 g + 4 (it % 2) + e, and tile t of 16 state columns likewise:
+// so the results of two tiles are, in their lanes, the second operand of a
+// product over those 32, in order.
+__device__ __forceinline__ int chain_row(int tile, int row) {
+  return (tile >> 1) * 32 + (row >> 2) * 8 + (tile & 1) * 4 + (row & 3);
+}
+
+#endif  // __HIPCC__
+
+}  // namespace gdnq

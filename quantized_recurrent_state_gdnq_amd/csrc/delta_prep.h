@@ -1,0 +1,190 @@
+// What the chains of the trained delta rule need of every chunk and does not
+// depend on the state: the inverse of I + At B (forward) or the transposed one
+// of I + B At (backward), the triangle M or its transpose, and the decays.
+// One workgroup of four waves per chunk and value head.
+#pragma once
+
+#include "delta_common.h"
+
+namespace gdnq {
+
+// D += A B of 16 x 16 fp32 tiles in LDS (A) and in result layout (B): the
+// contraction index of step s is 4 g + s, which a result tile holds in register s.
+constexpr int PREP_PITCH = 68;
+__device__ __forceinline__ f32x4 tile_product(const float* a, const f32x4& b, f32x4 d, int lane) {
+  const int r = lane & 15, g = lane >> 4;
+  const f32x4 x = *reinterpret_cast<const f32x4*>(a + r * PREP_PITCH + g * 4);
+#pragma unroll
+  for (int s = 0; s < 4; ++s) d = __builtin_amdgcn_mfma_f32_16x16x4f32(x[s], b[s], d, 0, 0, 0);
+  return d;
+}
+__device__ __forceinline__ f32x4 load_tile(const float* a, int lane) {
+  const int c = lane & 15, g = lane >> 4;
+  f32x4 x;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) x[e] = a[(4 * g + e) * PREP_PITCH + c];
+  return x;
+}
+__device__ __forceinline__ void store_tile(float* a, const f32x4& x, int lane, float sign) {
+  const int c = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) a[(4 * g + e) * PREP_PITCH + c] = sign * x[e];
+}
+
+// (I + a)^-1 of a strictly lower triangle in LDS into n (zero above the
+// diagonal), fp32: the diagonal 16 x 16 blocks by substitution, a lane per
+// column, then [n1 0; -n2 a21 n1, n2] twice.
+__device__ __forceinline__ void invert_triangle(const float* a, float* n, int wave, int lane) {
+  constexpr int P = PREP_PITCH;
+  if (lane < 16) {
+    const float* block = a + wave * 16 * (P + 1);
+    float* to = n + wave * 16 * (P + 1);
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float sum = i == lane ? 1.0f : 0.0f;
+#pragma unroll
+      for (int j = 0; j < i; ++j) sum = fmaf(-block[i * P + j], x[j], sum);
+      x[i] = sum;
+      to[i * P + lane] = sum;
+    }
+  }
+  if (wave >= 2) {  // the tiles above the diagonal that are read
+    float* to = n + (wave - 2) * (32 * P + 32) + 16;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) to[(lane / 16 * 4 + e) * P + lane % 16] = 0.0f;
+  }
+  __syncthreads();
+  if (wave < 2) {
+    const int at = wave * 32;
+    f32x4 p = tile_product(a + (at + 16) * P + at, load_tile(n + at * P + at, lane), f32x4{0, 0, 0, 0}, lane);
+    p = tile_product(n + (at + 16) * P + at + 16, p, f32x4{0, 0, 0, 0}, lane);
+    store_tile(n + (at + 16) * P + at, p, lane, -1.0f);
+  }
+  __syncthreads();
+  const int rt = 2 + (wave >> 1), ct = wave & 1;
+  f32x4 sum = {0, 0, 0, 0};
+#pragma unroll
+  for (int m = 2; m < 4; ++m) {
+    if (m > rt) break;
+    f32x4 p = {0, 0, 0, 0};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (k < ct) continue;
+      p = tile_product(a + m * 16 * P + k * 16, load_tile(n + k * 16 * P + ct * 16, lane), p, lane);
+    }
+    sum = tile_product(n + rt * 16 * P + m * 16, p, sum, lane);
+  }
+  store_tile(n + rt * 16 * P + ct * 16, sum, lane, -1.0f);
+  __syncthreads();
+}
+
+template <int DK, bool BACK>
+__global__ __launch_bounds__(256) void delta_prep_kernel(DeltaLaunch L) {
+  constexpr int P = PREP_PITCH, KB = DK / 32;
+  __shared__ __attribute__((aligned(16))) float a[64 * P], m[64 * P], n[64 * P];
+  __shared__ float rest[64], beta[64];
+  __shared__ int whole[64];
+  const int64_t slot = blockIdx.x / L.H;
+  const int h = blockIdx.x % L.H, kh = h / (L.H / L.G);
+  int64_t first;
+  const int tokens = delta_slot_tokens(L, slot, first);
+  if (tokens == 0) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+  uint8_t* out = static_cast<uint8_t*>(L.workspace) + (slot * L.H + h) * DELTA_CHUNK_BYTES;
+
+  // The decays, as log2 in 64 bits and then as a whole number and a rest, so
+  // that the ratio of two tokens is good to fp32 whatever lies before them.  A
+  // token's decay is at least 2^-64: what is left of a state then is below any
+  // sum's rounding, and the gradient of a zero alpha can be told from it.
+  if (wave == 0) {
+    double x = 0.0;
+    float bt = 0.0f;
+    if (lane < tokens) {
+      const int64_t at = (first + lane) * L.H + h;
+      x = L.log_decay ? double(L.alpha[at]) * 1.4426950408889634074 : log2(double(L.alpha[at]));
+      x = x < -64.0 ? -64.0 : x;
+      bt = L.beta[at];
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const double y = __shfl_up(x, d);
+      if (lane >= d) x += y;
+    }
+    const double w = rint(x);
+    const float r = float(x - w);
+    const int wi = int(w);
+    rest[lane] = r;
+    whole[lane] = wi;
+    beta[lane] = bt;
+    float* sc = reinterpret_cast<float*>(out + DELTA_SCALARS);
+    sc[lane] = exp2_difference(r, wi, 0.0f, 0);
+    sc[64 + lane] = exp2_difference(__shfl(r, 63), __shfl(wi, 63), r, wi);
+    sc[128 + lane] = bt;
+    reinterpret_cast<int*>(sc)[192 + lane] = wi;
+    sc[256 + lane] = r;
+  }
+  // Wave it: the rows of tile it, against the tiles up to it.
+  const bf16* kp = static_cast<const bf16*>(L.k) + int64_t(kh) * L.dk;
+  const bf16* qp = static_cast<const bf16*>(L.q) + int64_t(kh) * L.dk;
+  auto frag = [&](const bf16* p, int row, int j) {
+    bf16x8 x = {};
+    const int at = j * 32 + g * 8;
+    if (row < tokens && at < L.dk) x = *reinterpret_cast<const bf16x8*>(p + (first + row) * (int64_t(L.G) * L.dk) + at);
+    return x;
+  };
+  f32x4 kk[4] = {}, qk[4] = {};
+#pragma unroll
+  for (int j = 0; j < KB; ++j) {
+    const bf16x8 kr = frag(kp, wave * 16 + c, j), qr = frag(qp, wave * 16 + c, j);
+#pragma unroll
+    for (int jt = 0; jt < 4; ++jt) {
+      if (jt > wave) break;
+      const bf16x8 kc = frag(kp, jt * 16 + c, j);
+      kk[jt] = mfma16(kr, kc, kk[jt]);
+      qk[jt] = mfma16(qr, kc, qk[jt]);
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int jt = 0; jt < 4; ++jt) {
+    if (jt > (wave | 1)) break;  // with the tile above the diagonal that is read
+    const int j = jt * 16 + c;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = wave * 16 + g * 4 + e;
+      float rho = 0.0f;
+      if (j <= i) rho = exp2_difference(rest[i], whole[i], rest[j], whole[j]);
+      m[i * P + j] = rho * qk[jt][e];
+      a[i * P + j] = j < i ? rho * kk[jt][e] * beta[BACK ? i : j] : 0.0f;
+    }
+  }
+  __syncthreads();
+  invert_triangle(a, n, wave, lane);
+
+  // Out as first operands: six blocks of each, rows in the chains' order.
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const int f = wave * 3 + i, block = f % TRI_BLOCKS;
+    const float* from = f < TRI_BLOCKS ? n : m;
+    int it, j;
+    if (!BACK) {
+      it = block < 2 ? block : (block + 2) / 2;
+      j = block < 2 ? 0 : block & 1;
+    } else {  // transposed: tiles 0 and 1 have both blocks, 2 and 3 the second
+      it = block < 4 ? block / 2 : block - 2;
+      j = block < 4 ? block & 1 : 1;
+    }
+    const int row = chain_row(it, c), at = j * 32 + g * 8;
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = BACK ? from[(at + e) * P + row] : from[row * P + at + e];
+    bf16x8 hi, lo;
+    split2(x, hi, lo);
+    uint8_t* to = out + (f < TRI_BLOCKS ? 0 : TRI_BYTES) + block * 1024 + lane * 16;
+    *reinterpret_cast<bf16x8*>(to) = hi;
+    *reinterpret_cast<bf16x8*>(to + TRI_PART) = lo;
+  }
+}
+
+}  // namespace gdnq

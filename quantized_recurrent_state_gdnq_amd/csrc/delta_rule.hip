@@ -1,0 +1,341 @@
+// The gated delta rule with its state in fp32: chunks of 64 tokens on the
+// matrix units (forward), and one token per sequence.  The backward pass is in
+// delta_rule_backward.hip; the formulas are in delta_common.h.
+#include "delta_common.h"
+#include "delta_prep.h"
+
+namespace gdnq {
+namespace {
+
+// ---------------------------------------------------------------- the chain
+//
+// A workgroup of four waves takes 64 rows (d_v) of one head's state through
+// its chunks, 16 rows a wave, in registers as S^T in tiles of 16 columns (d_k)
+// x 16 rows.  No wave needs another's results: the second operand of every
+// product is the wave's own (see chain_row), the first ones (K, Q and the
+// triangles) come from LDS, where the workgroup puts the next chunk's while
+// this one's are used.
+template <int DK, bool SAVE, typename O>
+__global__ __launch_bounds__(256, 1) void delta_chain_kernel(DeltaLaunch L, int row_groups) {
+  constexpr int BLOCKS = DK / 8, KB = DK / 32, TILES = DK / 16;
+  constexpr int MAT = 64 * DK * 2, LOADS = 64 * BLOCKS / 256;
+  struct Buffer {
+    uint8_t k[MAT], q[MAT], n[TRI_BYTES], m[TRI_BYTES];
+  };
+  __shared__ __attribute__((aligned(1024))) Buffer buffers[2];
+  const int h = blockIdx.x / row_groups % L.H, b = blockIdx.x / row_groups / L.H, group = blockIdx.x % row_groups;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+  const int col = group * 64 + wave * 16 + c;
+  const bool mine = col < L.dv;
+  const int kh = h / (L.H / L.G);
+  const DeltaSpan s = delta_sequence(L, b);
+  const int chunks = (s.tokens + 63) / 64;
+  const bf16* kp = static_cast<const bf16*>(L.k);
+  const bf16* qp = static_cast<const bf16*>(L.q);
+  const bf16* vp = static_cast<const bf16*>(L.v);
+  const int64_t krow = int64_t(L.G) * L.dk, vrow = int64_t(L.H) * L.dv;
+
+  f32x4 S[TILES];
+  const int64_t state_row = ((int64_t(b) * L.H + h) * L.dv + col) * L.dk;
+#pragma unroll
+  for (int t = 0; t < TILES; ++t) {
+    const int at = chain_row(t, g * 4);
+    S[t] = f32x4{0, 0, 0, 0};
+    if (L.h0 && mine && at < L.dk) S[t] = *reinterpret_cast<const f32x4*>(L.h0 + state_row + at);
+  }
+
+  uint4 rk[LOADS], rq[LOADS], rn[3], rm[3];
+  f32x4 gamma[4], tail[4], beta[4];
+  bf16 v[4][4];
+  auto fetch = [&](int chunk) {
+    const int64_t first = s.first + int64_t(chunk) * 64;
+    const int n = min(64, s.tokens - chunk * 64);
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+      const int p = i * 256 + threadIdx.x, row = p / BLOCKS, block = p % BLOCKS;
+      rk[i] = rq[i] = uint4{0, 0, 0, 0};
+      if (row < n && block * 8 < L.dk) {
+        const int64_t at = (first + row) * krow + int64_t(kh) * L.dk + block * 8;
+        rk[i] = *reinterpret_cast<const uint4*>(kp + at);
+        rq[i] = *reinterpret_cast<const uint4*>(qp + at);
+      }
+    }
+    const uint8_t* ws = static_cast<const uint8_t*>(L.workspace) + ((s.slot + chunk) * L.H + h) * DELTA_CHUNK_BYTES;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      rn[i] = *reinterpret_cast<const uint4*>(ws + (i * 256 + threadIdx.x) * 16);
+      rm[i] = *reinterpret_cast<const uint4*>(ws + TRI_BYTES + (i * 256 + threadIdx.x) * 16);
+    }
+  };
+  // What a lane needs of its four tokens a tile: read a chunk ahead, too.
+  auto fetch_rows = [&](int chunk) {
+    const int64_t first = s.first + int64_t(chunk) * 64;
+    const int n = min(64, s.tokens - chunk * 64);
+    const float* sc = reinterpret_cast<const float*>(static_cast<const uint8_t*>(L.workspace) +
+                                                     ((s.slot + chunk) * L.H + h) * DELTA_CHUNK_BYTES + DELTA_SCALARS);
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      const int row = chain_row(it, g * 4);
+      gamma[it] = *reinterpret_cast<const f32x4*>(sc + row);
+      tail[it] = *reinterpret_cast<const f32x4*>(sc + 64 + row);
+      beta[it] = *reinterpret_cast<const f32x4*>(sc + 128 + row);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        v[it][e] = mine && row + e < n ? vp[(first + row + e) * vrow + int64_t(h) * L.dv + col] : bf16(0.0f);
+    }
+  };
+  auto put = [&](Buffer& to) {
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+      const int p = i * 256 + threadIdx.x, at = lds_block<DK>(p / BLOCKS, p % BLOCKS);
+      *reinterpret_cast<uint4*>(to.k + at) = rk[i];
+      *reinterpret_cast<uint4*>(to.q + at) = rq[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      *reinterpret_cast<uint4*>(to.n + (i * 256 + threadIdx.x) * 16) = rn[i];
+      *reinterpret_cast<uint4*>(to.m + (i * 256 + threadIdx.x) * 16) = rm[i];
+    }
+  };
+
+  if (chunks > 0) {
+    fetch(0);
+    fetch_rows(0);
+    put(buffers[0]);
+  }
+  __syncthreads();
+  for (int chunk = 0; chunk < chunks; ++chunk) {
+    const Buffer& buf = buffers[chunk & 1];
+    if (chunk + 1 < chunks) fetch(chunk + 1);
+    bf16x8 sh[KB], sl[KB];
+#pragma unroll
+    for (int j = 0; j < KB; ++j) split8(S[2 * j], S[2 * j + 1], sh[j], sl[j]);
+    if constexpr (SAVE) {
+      bf16* to = reinterpret_cast<bf16*>(static_cast<uint8_t*>(L.carry) + ((s.slot + chunk) * L.H + h) * delta_state_bytes(L));
+#pragma unroll
+      for (int j = 0; j < KB; ++j) {
+        const int at = j * 32 + g * 8;
+        if (mine && at < L.dk) {
+          *reinterpret_cast<bf16x8*>(to + int64_t(col) * L.dk + at) = sh[j];
+          *reinterpret_cast<bf16x8*>(to + int64_t(L.dv + col) * L.dk + at) = sl[j];
+        }
+      }
+    }
+    f32x4 x[4], o[4];
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      const int row = chain_row(it, c);
+      x[it] = o[it] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < KB; ++j) {
+        const int at = lds_block<DK>(row, j * 4 + g);
+        x[it] = mfma_exact_split(lds_frag(buf.k + at), sh[j], sl[j], x[it]);
+        o[it] = mfma_exact_split(lds_frag(buf.q + at), sh[j], sl[j], o[it]);
+      }
+    }
+#pragma unroll
+    for (int it = 0; it < 4; ++it)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[it][e] = float(v[it][e]) - gamma[it][e] * x[it][e];
+    bf16x8 hi[2], lo[2];
+    auto triangle = [&](const uint8_t* tri, f32x4 (&d)[4]) {
+#pragma unroll
+      for (int it = 0; it < 4; ++it)
+#pragma unroll
+        for (int j = 0; j <= it / 2; ++j) {
+          const uint8_t* at = tri + (it < 2 ? it : 2 * it - 2 + j) * 1024 + lane * 16;
+          d[it] = mfma_split_split(lds_frag(at), lds_frag(at + TRI_PART), hi[j], lo[j], d[it]);
+        }
+    };
+    split8(x[0], x[1], hi[0], lo[0]);
+    split8(x[2], x[3], hi[1], lo[1]);
+    f32x4 w[4] = {};
+    triangle(buf.n, w);
+    const int64_t first = s.first + int64_t(chunk) * 64;
+    const int n = min(64, s.tokens - chunk * 64);
+    if constexpr (SAVE) {
+      float* to = reinterpret_cast<float*>(static_cast<uint8_t*>(L.carry) + L.rows_at);
+#pragma unroll
+      for (int it = 0; it < 4; ++it)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int row = chain_row(it, g * 4 + e);
+          if (mine && row < n) to[(first + row) * vrow + int64_t(h) * L.dv + col] = w[it][e];
+        }
+    }
+    f32x4 tu[4];
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      w[it] *= beta[it];
+      tu[it] = w[it] * tail[it];
+      o[it] *= gamma[it];
+    }
+    split8(w[0], w[1], hi[0], lo[0]);
+    split8(w[2], w[3], hi[1], lo[1]);
+    bf16x8 th[2], tl[2];
+    split8(tu[0], tu[1], th[0], tl[0]);
+    split8(tu[2], tu[3], th[1], tl[1]);
+    const float whole = __shfl(gamma[3][3], 63);  // the last token's: row 63 is tile 3's, g = 3, e = 3
+#pragma unroll
+    for (int t = 0; t < TILES; ++t) {
+      S[t] *= whole;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        // tokens 32 j + 8 g + .. of the columns in tile t's order
+        const int row = j * 32 + g * 8 + (c >> 2), block = (t >> 1) * 4 + (c & 3), half = (t & 1) * 8;
+        const bf16x8 a = lds_transposed(buf.k + lds_block<DK>(row, block) + half, buf.k + lds_block<DK>(row + 4, block) + half);
+        S[t] = mfma_exact_split(a, th[j], tl[j], S[t]);
+      }
+    }
+    triangle(buf.m, o);
+    if (mine) {
+      O* op = static_cast<O*>(L.o);
+#pragma unroll
+      for (int it = 0; it < 4; ++it)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int row = chain_row(it, g * 4 + e);
+          if (row < n) store_f32(op + (first + row) * vrow + int64_t(h) * L.dv + col, o[it][e]);
+        }
+    }
+    if (chunk + 1 < chunks) {
+      fetch_rows(chunk + 1);
+      put(buffers[(chunk + 1) & 1]);
+    }
+    __syncthreads();
+  }
+  if (L.h_last && mine) {
+#pragma unroll
+    for (int t = 0; t < TILES; ++t) {
+      const int at = chain_row(t, g * 4);
+      if (at < L.dk) *reinterpret_cast<f32x4*>(L.h_last + state_row + at) = S[t];
+    }
+  }
+}
+
+// ---------------------------------------------------------------- one token
+//
+// Bound by the state's bytes: read once, written once.  LANES lanes hold a row,
+// eight columns each, and R rows are in flight in a lane.
+template <int LANES, int R, typename E>
+__global__ __launch_bounds__(256) void delta_step_kernel(DeltaLaunch L) {
+  constexpr int ROWS = 256 / LANES;  // rows of a pass
+  const int lane = threadIdx.x % LANES, at = lane * 8;
+  const bool here = at < L.dk;
+  const int row0 = blockIdx.x % L.row_groups * (ROWS * R) + threadIdx.x / LANES;
+  const int64_t bh = blockIdx.x / L.row_groups;
+  const int h = int(bh % L.H);
+  const int64_t b = bh / L.H, key = (b * L.G + h / (L.H / L.G)) * L.dk + at;
+  const float* from = L.h0 + bh * L.dv * L.dk + at;
+  float* to = L.h_last + bh * L.dv * L.dk + at;
+  f32x4 s[R][2];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int row = row0 + r * ROWS;
+    s[r][0] = s[r][1] = f32x4{0, 0, 0, 0};
+    if (here && row < L.dv) {
+      s[r][0] = *reinterpret_cast<const f32x4*>(from + int64_t(row) * L.dk);
+      s[r][1] = *reinterpret_cast<const f32x4*>(from + int64_t(row) * L.dk + 4);
+    }
+  }
+  float k[8] = {}, q[8] = {};
+  if (here) {
+    const E* kp = static_cast<const E*>(L.k) + key;
+    const E* qp = static_cast<const E*>(L.q) + key;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) k[e] = to_f32(kp[e]), q[e] = to_f32(qp[e]);
+  }
+  float kq = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) kq = fmaf(k[e], q[e], kq);
+  kq = group_sum<LANES>(kq);
+  float a = L.alpha[bh];
+  if (L.log_decay) a = expf(a);
+  const float beta = L.beta[bh];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int row = row0 + r * ROWS;
+    float sk = 0, sq = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float x = s[r][e / 4][e % 4] * a;
+      s[r][e / 4][e % 4] = x;
+      sk = fmaf(x, k[e], sk);
+      sq = fmaf(x, q[e], sq);
+    }
+    sk = group_sum<LANES>(sk);
+    sq = group_sum<LANES>(sq);
+    if (row < L.dv) {
+      const float u = beta * (to_f32(static_cast<const E*>(L.v)[bh * L.dv + row]) - sk);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[r][e / 4][e % 4] = fmaf(u, k[e], s[r][e / 4][e % 4]);
+      if (here) {
+        *reinterpret_cast<f32x4*>(to + int64_t(row) * L.dk) = s[r][0];
+        *reinterpret_cast<f32x4*>(to + int64_t(row) * L.dk + 4) = s[r][1];
+      }
+      if (lane == 0) {
+        const float o = fmaf(u, kq, sq);
+        if (L.out_bf16)
+          store_f32(static_cast<bf16*>(L.o) + bh * L.dv + row, o);
+        else
+          store_f32(static_cast<float*>(L.o) + bh * L.dv + row, o);
+      }
+    }
+  }
+}
+
+template <int DK>
+hipError_t forward(const DeltaLaunch& L, hipStream_t stream) {
+  const int64_t heads = delta_slots(L) * L.H;
+  if (heads > 0) {
+    delta_prep_kernel<DK, false><<<uint32_t(heads), 256, 0, stream>>>(L);
+    if (hipError_t e = hipGetLastError()) return e;
+  }
+  const int groups = (L.dv + 63) / 64;
+  const uint32_t grid = uint32_t(groups) * uint32_t(L.H) * uint32_t(L.B);
+  if (L.carry)
+    L.out_bf16 ? delta_chain_kernel<DK, true, bf16><<<grid, 256, 0, stream>>>(L, groups)
+               : delta_chain_kernel<DK, true, float><<<grid, 256, 0, stream>>>(L, groups);
+  else
+    L.out_bf16 ? delta_chain_kernel<DK, false, bf16><<<grid, 256, 0, stream>>>(L, groups)
+               : delta_chain_kernel<DK, false, float><<<grid, 256, 0, stream>>>(L, groups);
+  return hipGetLastError();
+}
+
+template <int LANES, typename E>
+hipError_t step(DeltaLaunch L, hipStream_t stream) {
+  constexpr int ROWS = 256 / LANES;
+  auto groups = [&](int r) { return (L.dv + ROWS * r - 1) / (ROWS * r); };
+  const int64_t heads = int64_t(L.B) * L.H;
+  if (heads * groups(4) >= 1024) {
+    L.row_groups = groups(4);
+    delta_step_kernel<LANES, 4, E><<<uint32_t(heads * L.row_groups), 256, 0, stream>>>(L);
+  } else {
+    L.row_groups = groups(1);
+    delta_step_kernel<LANES, 1, E><<<uint32_t(heads * L.row_groups), 256, 0, stream>>>(L);
+  }
+  return hipGetLastError();
+}
+
+template <typename E>
+hipError_t step_of(const DeltaLaunch& L, hipStream_t stream) {
+  if (L.dk <= 64) return step<8, E>(L, stream);
+  if (L.dk <= 128) return step<16, E>(L, stream);
+  return step<32, E>(L, stream);
+}
+
+}  // namespace
+
+size_t delta_carry_rows_at(const DeltaLaunch& L) { return size_t(delta_align(delta_slots(L) * L.H * delta_state_bytes(L))); }
+size_t delta_carry_bytes(const DeltaLaunch& L) { return delta_carry_rows_at(L) + size_t(L.N) * L.H * L.dv * 4; }
+size_t delta_forward_workspace_bytes(const DeltaLaunch& L) { return size_t(delta_slots(L)) * L.H * DELTA_CHUNK_BYTES; }
+
+hipError_t launch_delta_forward(const DeltaLaunch& L, hipStream_t stream) {
+  return L.dk <= 64 ? forward<64>(L, stream) : forward<128>(L, stream);
+}
+
+hipError_t launch_delta_step(const DeltaLaunch& L, hipStream_t stream) {
+  return L.in_bf16 ? step_of<bf16>(L, stream) : step_of<float>(L, stream);
+}
+
+}  // namespace gdnq

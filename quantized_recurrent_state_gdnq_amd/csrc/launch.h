@@ -147,4 +147,41 @@ hipError_t launch_mx_quantize(const void* x, int64_t rows, int K, bool bf16, uin
 hipError_t launch_mx_matmul(const MxLaunch& L, hipStream_t stream);
 hipError_t launch_mx_linear(const MxLaunch& L, hipStream_t stream);
 
+// The trained delta rule: its state in fp32, chunked (delta_rule.hip) with
+// gradients (delta_rule_backward.hip), and one token per sequence.
+struct DeltaLaunch {
+  const int32_t* cu_seqlens;  // B + 1 packed token offsets, or null: B sequences of T tokens
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* alpha;
+  const float* beta;
+  const float* h0;  // one token: the state read
+  void* o;
+  float* h_last;    // one token: the state written
+  void* carry;      // states entering every chunk, then what every token writes
+  const void* dout;
+  const float* dh_last;
+  void* dq;
+  void* dk_out;
+  void* dv_out;
+  float* dalpha;
+  float* dbeta;
+  float* dh0;
+  void* workspace;
+  int B, T, G, H, dk, dv;
+  int64_t N;        // tokens of the call
+  size_t rows_at;   // where the tokens' part of the carry begins
+  int row_groups;
+  bool in_bf16, out_bf16, log_decay;
+};
+size_t delta_carry_rows_at(const DeltaLaunch& L);
+size_t delta_carry_bytes(const DeltaLaunch& L);
+size_t delta_forward_workspace_bytes(const DeltaLaunch& L);
+size_t delta_backward_workspace_bytes(const DeltaLaunch& L);
+hipError_t launch_delta_forward(const DeltaLaunch& L, hipStream_t stream);
+hipError_t launch_delta_backward(const DeltaLaunch& L, hipStream_t stream);
+// one token per sequence: h0 in, h_last out
+hipError_t launch_delta_step(const DeltaLaunch& L, hipStream_t stream);
+
 }  // namespace gdnq

@@ -885,3 +885,123 @@ def mx_linear(x, w_codes, w_scales, *, out_dtype=None, y=None, workspace=None):
     ws, ws_bytes = _space(workspace, int(_lib.mx_workspace_size(p)), dev)
     _launch(dev, _lib.mx_linear, p, _ptr(x), _ptr(w_codes), _ptr(w_scales), _ptr(y), _ptr(ws), ws_bytes)
     return y
+
+
+# ---------------------------------------------------------------- the delta rule with its state in fp32
+
+
+def _delta_setup(q, k, v, alpha, beta, cu_seqlens, log_decay, out_dtype, dtypes=(torch.bfloat16,)):
+    """The checks every delta rule call shares: its parameters and the shape
+    of its states."""
+    _need(q, "q", None, None)
+    dev = q.device
+    if q.dtype not in dtypes:
+        raise ValueError(f"q must be one of {[str(d) for d in dtypes]}, got {q.dtype}")
+    if out_dtype not in _DT:
+        raise ValueError("out_dtype must be float32 or bfloat16")
+    step = len(dtypes) > 1
+    packed = cu_seqlens is not None
+    dims = 3 if step or packed else 4
+    if q.dim() != dims or v.dim() != dims:
+        raise ValueError("q must be [B,T,G,d_k] and v [B,T,H,d_v], or [T,..] with cu_seqlens (one token: [B,..])")
+    if packed:
+        _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+            raise ValueError("cu_seqlens: one dimension of B+1 offsets")
+    lead, (G, d_k), (H, d_v) = q.shape[:-2], q.shape[-2:], v.shape[-2:]
+    _checked(k, "k", q.dtype, dev, q.shape)
+    _checked(v, "v", q.dtype, dev, lead + (H, d_v))
+    _checked(alpha, "alpha", torch.float32, dev, lead + (H,))
+    _checked(beta, "beta", torch.float32, dev, lead + (H,))
+    B, T = (cu_seqlens.numel() - 1, q.shape[0]) if packed else (q.shape[0], 1 if step else q.shape[1])
+    _sizes(B, T)
+    _sizes(G, H, max(d_k, d_v))
+    p = _lib.DeltaParams(B, T, G, H, d_k, d_v, _DT[q.dtype], _DT[out_dtype],
+                         _lib.GDNQ_DELTA_LOG if log_decay else 0)
+    return p, (B, H, d_v, d_k), packed
+
+
+def delta_rule_workspace_size(q, v, cu_seqlens=None, *, backward=False):
+    """Workspace bytes of delta_rule (or delta_rule_backward) for these arrays."""
+    B, T = (q.shape[0], q.shape[1]) if cu_seqlens is None else (cu_seqlens.numel() - 1, q.shape[0])
+    _sizes(B, T)
+    p = _lib.DeltaParams(B, T, q.shape[-2], v.shape[-2], q.shape[-1], v.shape[-1], _DT[q.dtype], 0, 0)
+    return int(_lib.delta_workspace_size(p, cu_seqlens is not None, backward))
+
+
+def delta_rule(q, k, v, alpha, beta, h0=None, cu_seqlens=None, *, log_decay=False, save=False, out_dtype=None, o=None,
+               h_last=None, carry=None, workspace=None):
+    """The gated delta rule with its state in fp32 (see gdnq_delta_* in
+    include/gdnq.h): S_t = alpha_t S_{t-1}(I - beta_t k_t k_t^T) + beta_t v_t
+    k_t^T, o_t = S_t q_t.
+
+    q, k [B,T,G,d_k], v [B,T,H,d_v] bf16 and alpha, beta [B,T,H] fp32, or
+    [T,..] with cu_seqlens (int32 on the device, B+1 offsets of the packed
+    sequences); value head h uses key head h // (H / G).  log_decay=True: alpha
+    holds its logarithm.  h0 [B,H,d_v,d_k] fp32 or None.  Returns (o like v, or
+    of out_dtype, h_last [B,H,d_v,d_k] fp32), and with save=True (or a given
+    carry) the carry, a uint8 tensor that delta_rule_backward takes."""
+    out_dtype = out_dtype or (torch.bfloat16 if o is None else o.dtype)
+    p, states, packed = _delta_setup(q, k, v, alpha, beta, cu_seqlens, log_decay, out_dtype)
+    dev = q.device
+    _optional(h0, "h0", torch.float32, dev, states)
+    # a packed call may hold tokens that no sequence covers: only a given o has values there
+    if o is None:
+        o = torch.empty(v.shape, dtype=out_dtype, device=dev)
+    _checked(o, "o", out_dtype, dev, v.shape)
+    if h_last is None:
+        h_last = torch.empty(states, dtype=torch.float32, device=dev)
+    _checked(h_last, "h_last", torch.float32, dev, states)
+    if save or carry is not None:
+        size = (int(_lib.delta_carry_size(p, packed)),)
+        carry = torch.empty(size, dtype=torch.uint8, device=dev) if carry is None else carry
+        _checked(carry, "carry", torch.uint8, dev, size)
+    ws, ws_bytes = _space(workspace, int(_lib.delta_workspace_size(p, packed, False)), dev)
+    _launch(dev, _lib.delta_forward, p, _ptr(cu_seqlens), _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), _ptr(h0),
+            _ptr(o), _ptr(h_last), _ptr(carry), _ptr(ws), ws_bytes)
+    return (o, h_last) if carry is None else (o, h_last, carry)
+
+
+def delta_rule_backward(do, q, k, v, alpha, beta, carry, h0=None, dh_last=None, cu_seqlens=None, *, log_decay=False,
+                        dq=None, dk=None, dv=None, dalpha=None, dbeta=None, dh0=None, workspace=None):
+    """Gradients of delta_rule from do (like v, bf16) and dh_last
+    ([B,H,d_v,d_k] fp32 or None), with the forward call's arguments and its
+    carry.  Returns (dq, dk, dv, dalpha, dbeta, dh0): dq, dk, dv bf16 like q, k,
+    v; dalpha (of what alpha holds) and dbeta fp32; dh0 is None when h0 is and
+    no dh0 was given."""
+    p, states, packed = _delta_setup(q, k, v, alpha, beta, cu_seqlens, log_decay, torch.bfloat16)
+    dev = q.device
+    _checked(do, "do", torch.bfloat16, dev, v.shape)
+    _checked(carry, "carry", torch.uint8, dev, (int(_lib.delta_carry_size(p, packed)),))
+    _optional(h0, "h0", torch.float32, dev, states)
+    _optional(dh_last, "dh_last", torch.float32, dev, states)
+    dq = torch.empty_like(q) if dq is None else _checked(dq, "dq", q.dtype, dev, q.shape)
+    dk = torch.empty_like(q) if dk is None else _checked(dk, "dk", q.dtype, dev, q.shape)
+    dv = torch.empty_like(v) if dv is None else _checked(dv, "dv", q.dtype, dev, v.shape)
+    dalpha = torch.empty_like(alpha) if dalpha is None else _checked(dalpha, "dalpha", alpha.dtype, dev, alpha.shape)
+    dbeta = torch.empty_like(beta) if dbeta is None else _checked(dbeta, "dbeta", beta.dtype, dev, beta.shape)
+    if dh0 is None and h0 is not None:
+        dh0 = torch.empty(states, dtype=torch.float32, device=dev)
+    _optional(dh0, "dh0", torch.float32, dev, states)
+    ws, ws_bytes = _space(workspace, int(_lib.delta_workspace_size(p, packed, True)), dev)
+    _launch(dev, _lib.delta_backward, p, _ptr(cu_seqlens), _ptr(q), _ptr(k), _ptr(alpha), _ptr(beta), _ptr(carry),
+            _ptr(do), _ptr(dh_last), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dalpha), _ptr(dbeta), _ptr(dh0), _ptr(ws),
+            ws_bytes)
+    return dq, dk, dv, dalpha, dbeta, dh0
+
+
+def delta_rule_step(q, k, v, alpha, beta, h, *, log_decay=False, out_dtype=None, h_out=None, o=None):
+    """One token of the delta rule for every sequence: q, k [B,G,d_k], v
+    [B,H,d_v] fp32 or bf16, alpha, beta [B,H] fp32, h [B,H,d_v,d_k] fp32, updated
+    in place unless h_out is given.  Returns o [B,H,d_v] like v, or of
+    out_dtype."""
+    out_dtype = out_dtype or (v.dtype if o is None else o.dtype)
+    p, states, _ = _delta_setup(q, k, v, alpha, beta, None, log_decay, out_dtype, (torch.float32, torch.bfloat16))
+    dev = q.device
+    _checked(h, "h", torch.float32, dev, states)
+    h_out = h if h_out is None else _checked(h_out, "h_out", torch.float32, dev, states)
+    if o is None:
+        o = torch.empty(v.shape, dtype=out_dtype, device=dev)
+    _checked(o, "o", out_dtype, dev, v.shape)
+    _launch(dev, _lib.delta_step, p, _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), _ptr(h), _ptr(h_out), _ptr(o))
+    return o

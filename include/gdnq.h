@@ -709,6 +709,104 @@ gdnq_status gdnq_delta_step(const gdnq_delta_params* p, const void* q, const voi
                             void* stream);
 
 /* ------------------------------------------------------------------------
+ * gdnq_qk_norm_* -- the norm of every head's queries and keys, with the
+ *   position rotation in the same pass: what the calls above take as q and k.
+ *
+ *       n = x / sqrt(mean(x^2) + eps) weight      (GDNQ_QK_L2: sum, not mean)
+ *       y: the first p->rotary columns of n in pairs (a, b), turned by the
+ *          angle t = position inv_freq[pair]:  (a cos t - b sin t, a sin t + b cos t);
+ *          the other columns as they are
+ *   Pair i is columns (i, i + rotary / 2), or (2i, 2i + 1) with
+ *   GDNQ_QK_INTERLEAVED.
+ *
+ *   p->rows R >= 0 tokens, p->q_heads, p->k_heads >= 1, R (q_heads + k_heads) <=
+ *   2^31 - 1, p->width D in 1 .. 512 (a multiple of 8 is faster), p->rotary even,
+ *   0 .. D (a multiple of 16 is faster); p->dtype (q, k, results and gradients)
+ *   GDNQ_F32 or GDNQ_BF16; p->eps >= 0, finite.
+ *     q, k       rows of [q_heads, D] and [k_heads, D], dense, q_stride and
+ *                k_stride elements apart (at least a row: views of a fused
+ *                projection's rows).  These two need only their type's
+ *                alignment; rows of whole 16-byte pieces are faster.
+ *     q_weight, k_weight  [D] fp32, shared by the heads, or NULL (1)
+ *     positions  [R] int32, or int64 with GDNQ_QK_POS64; inv_freq [rotary / 2]
+ *                fp32; both NULL exactly when rotary is 0
+ *     q_out, k_out [R, heads, D]
+ *   Angles are formed and reduced in 64 bits: good to fp32 for positions up to
+ *   2^31 in magnitude.  Sums are fp32, results are rounded once.
+ *   gdnq_qk_norm_backward: dq_out, dk_out [R, heads, D] in; dq, dk [R, heads, D]
+ *   and dq_weight, dk_weight [D] fp32 (NULL: not wanted) out.  The statistics are
+ *   formed again; nothing is kept from the forward call.  R = 0 writes zeros to
+ *   the weights' gradients.  Sums over tokens are taken in a fixed order.
+ *   workspace: gdnq_qk_norm_workspace_size(p) bytes (backward only).
+ *   Errors: NULL, SHAPE, DTYPE, ALIGN, ALIAS, FLAGS, WORKSPACE, HIP.
+ * ------------------------------------------------------------------------ */
+enum {
+  GDNQ_QK_L2 = 1u,          /* divide by the root of the sum, not the mean   */
+  GDNQ_QK_INTERLEAVED = 2u, /* pairs of adjacent columns                     */
+  GDNQ_QK_POS64 = 4u        /* positions are int64                           */
+};
+
+typedef struct {
+  int32_t rows, q_heads, k_heads, width, rotary, dtype;
+  float eps;
+  uint32_t flags;
+  int64_t q_stride, k_stride; /* elements between the rows of q and of k */
+} gdnq_qk_params;
+
+gdnq_status gdnq_qk_norm(const gdnq_qk_params* p, const void* q, const void* k, const float* q_weight,
+                         const float* k_weight, const void* positions, const float* inv_freq, void* q_out,
+                         void* k_out, void* stream);
+
+size_t gdnq_qk_norm_workspace_size(const gdnq_qk_params* p);
+
+gdnq_status gdnq_qk_norm_backward(const gdnq_qk_params* p, const void* q, const void* k,
+                                  const float* q_weight, const float* k_weight, const void* positions,
+                                  const float* inv_freq, const void* dq_out, const void* dk_out, void* dq,
+                                  void* dk, float* dq_weight, float* dk_weight, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * gdnq_int8_* -- rows in 8-bit integers with a scale each, and the product of
+ *   such rows: beside gdnq_mx_*, a projection whose weights have a scale for
+ *   every channel and whose activations have one for every token.
+ *
+ *   The codec is the one above, on rows of any length: scale = max|x| / 127,
+ *   code = clamp(round_half_even(x / scale), -127, 127) (IEEE fp32 divisions);
+ *   a row of zeros, or whose scale rounds to 0, has codes 0.  A row with a NaN
+ *   or an infinity gets scale NaN and codes 0: products with it are NaN.
+ *   gdnq_int8_quantize: x [rows, depth] (dtype GDNQ_F32 or GDNQ_BF16) to codes
+ *     [rows, depth] int8 and scales [rows] fp32.
+ *   gdnq_int8_matmul: y[m,n] = (sum_k a[m,k] w[n,k]) a_scales[m] w_scales[n] +
+ *     bias[n]: a [rows, depth], w [cols, depth] int8 (-128 is allowed), bias
+ *     [cols] fp32 or NULL, y [rows, cols] out_dtype.  The sum is exact, the rest
+ *     fp32, rounded once.
+ *   gdnq_int8_linear: the same with a = the codes of x [rows, depth] in_dtype,
+ *     quantized in the call's workspace.
+ *   0 <= rows <= 2^30; 1 <= cols <= 2^25; depth a multiple of 16, 16 .. 2^17 - 16
+ *   (the sums fit 32 bits); ceil(rows / 256) ceil(cols / 256) < 2^24.  in_dtype
+ *   is not read by gdnq_int8_matmul.  flags must be 0.
+ *   workspace: gdnq_int8_workspace_size(p) bytes for gdnq_int8_linear.
+ *   Errors: NULL, SHAPE, DTYPE, ALIGN, ALIAS, FLAGS, WORKSPACE, HIP.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  int32_t rows, cols, depth, in_dtype, out_dtype;
+  uint32_t flags;
+} gdnq_int8_params;
+
+gdnq_status gdnq_int8_quantize(const void* x, int64_t rows, int32_t depth, int32_t dtype, int8_t* codes,
+                               float* scales, void* stream);
+
+gdnq_status gdnq_int8_matmul(const gdnq_int8_params* p, const int8_t* a_codes, const float* a_scales,
+                             const int8_t* w_codes, const float* w_scales, const float* bias, void* y,
+                             void* stream);
+
+size_t gdnq_int8_workspace_size(const gdnq_int8_params* p);
+
+gdnq_status gdnq_int8_linear(const gdnq_int8_params* p, const void* x, const int8_t* w_codes,
+                             const float* w_scales, const float* bias, void* y, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
  * gdnq_decode_set_schedule -- tuning hook of gdnq_decode_step's persistent
  *   launch (not part of the method; results do not depend on it).
  *   grid: workgroups of the persistent grid; open_waves: waves that take the

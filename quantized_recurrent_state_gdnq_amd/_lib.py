@@ -29,6 +29,7 @@ GDNQ_SCAN_CHUNK = 128
 GDNQ_ACT_NONE, GDNQ_ACT_SILU, GDNQ_ACT_SIGMOID = 0, 1, 2
 GDNQ_NORM_CENTER, GDNQ_NORM_SHARED = 1, 2
 GDNQ_DELTA_LOG = 1
+GDNQ_QK_L2, GDNQ_QK_INTERLEAVED, GDNQ_QK_POS64 = 1, 2, 4
 
 # Every function the header declares.
 EXPORTS = ("gdnq_quantize_state", "gdnq_decode_step", "gdnq_prefill_workspace_size",
@@ -39,7 +40,8 @@ EXPORTS = ("gdnq_quantize_state", "gdnq_decode_step", "gdnq_prefill_workspace_si
            "gdnq_group_norm", "gdnq_group_norm_workspace_size", "gdnq_group_norm_backward",
            "gdnq_mx_quantize", "gdnq_mx_workspace_size", "gdnq_mx_matmul", "gdnq_mx_linear",
            "gdnq_delta_workspace_size", "gdnq_delta_carry_size", "gdnq_delta_forward", "gdnq_delta_backward",
-           "gdnq_delta_step",
+           "gdnq_delta_step", "gdnq_qk_norm", "gdnq_qk_norm_workspace_size", "gdnq_qk_norm_backward",
+           "gdnq_int8_quantize", "gdnq_int8_matmul", "gdnq_int8_workspace_size", "gdnq_int8_linear",
            "gdnq_decode_set_schedule", "gdnq_status_string", "gdnq_last_error", "gdnq_version",
            "gdnq_sync_debug")
 
@@ -76,6 +78,18 @@ class MxParams(ctypes.Structure):
 class DeltaParams(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int32), ("seqlen", ctypes.c_int32), ("key_heads", ctypes.c_int32),
                 ("heads", ctypes.c_int32), ("d_k", ctypes.c_int32), ("d_v", ctypes.c_int32),
+                ("in_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
+class QkParams(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("q_heads", ctypes.c_int32), ("k_heads", ctypes.c_int32),
+                ("width", ctypes.c_int32), ("rotary", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("flags", ctypes.c_uint32), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64)]
+
+
+class Int8Params(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("cols", ctypes.c_int32), ("depth", ctypes.c_int32),
                 ("in_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("flags", ctypes.c_uint32)]
 
 
@@ -152,6 +166,20 @@ def _load():
     lib.gdnq_delta_backward.restype = i32
     lib.gdnq_delta_step.argtypes = [ctypes.POINTER(DeltaParams)] + [vp] * 9
     lib.gdnq_delta_step.restype = i32
+    lib.gdnq_qk_norm.argtypes = [ctypes.POINTER(QkParams)] + [vp] * 9
+    lib.gdnq_qk_norm.restype = i32
+    lib.gdnq_qk_norm_workspace_size.argtypes = [ctypes.POINTER(QkParams)]
+    lib.gdnq_qk_norm_workspace_size.restype = sz
+    lib.gdnq_qk_norm_backward.argtypes = [ctypes.POINTER(QkParams)] + [vp] * 13 + [sz, vp]
+    lib.gdnq_qk_norm_backward.restype = i32
+    lib.gdnq_int8_quantize.argtypes = [vp, i64, i32, i32, vp, vp, vp]
+    lib.gdnq_int8_quantize.restype = i32
+    lib.gdnq_int8_matmul.argtypes = [ctypes.POINTER(Int8Params)] + [vp] * 7
+    lib.gdnq_int8_matmul.restype = i32
+    lib.gdnq_int8_workspace_size.argtypes = [ctypes.POINTER(Int8Params)]
+    lib.gdnq_int8_workspace_size.restype = sz
+    lib.gdnq_int8_linear.argtypes = [ctypes.POINTER(Int8Params)] + [vp] * 6 + [sz, vp]
+    lib.gdnq_int8_linear.restype = i32
     lib.gdnq_decode_set_schedule.argtypes = [i32, i32]
     lib.gdnq_decode_set_schedule.restype = i32
     lib.gdnq_status_string.argtypes = [i32]
@@ -320,3 +348,34 @@ def delta_backward(params, cu_seqlens, q, k, alpha, beta, carry, dout, dh_last, 
 
 def delta_step(params, q, k, v, alpha, beta, h, h_out, o, stream):
     return lib.gdnq_delta_step(ctypes.byref(params), q, k, v, alpha, beta, h, h_out, o, stream)
+
+
+def qk_norm(params, q, k, q_weight, k_weight, positions, inv_freq, q_out, k_out, stream):
+    return lib.gdnq_qk_norm(ctypes.byref(params), q, k, q_weight, k_weight, positions, inv_freq, q_out, k_out, stream)
+
+
+def qk_norm_workspace_size(params):
+    return lib.gdnq_qk_norm_workspace_size(ctypes.byref(params))
+
+
+def qk_norm_backward(params, q, k, q_weight, k_weight, positions, inv_freq, dq_out, dk_out, dq, dk, dq_weight,
+                     dk_weight, workspace, workspace_bytes, stream):
+    return lib.gdnq_qk_norm_backward(ctypes.byref(params), q, k, q_weight, k_weight, positions, inv_freq, dq_out,
+                                     dk_out, dq, dk, dq_weight, dk_weight, workspace, workspace_bytes, stream)
+
+
+def int8_quantize(x, rows, depth, dtype, codes, scales, stream):
+    return lib.gdnq_int8_quantize(x, rows, depth, dtype, codes, scales, stream)
+
+
+def int8_matmul(params, a_codes, a_scales, w_codes, w_scales, bias, y, stream):
+    return lib.gdnq_int8_matmul(ctypes.byref(params), a_codes, a_scales, w_codes, w_scales, bias, y, stream)
+
+
+def int8_workspace_size(params):
+    return lib.gdnq_int8_workspace_size(ctypes.byref(params))
+
+
+def int8_linear(params, x, w_codes, w_scales, bias, y, workspace, workspace_bytes, stream):
+    return lib.gdnq_int8_linear(ctypes.byref(params), x, w_codes, w_scales, bias, y, workspace, workspace_bytes,
+                                stream)

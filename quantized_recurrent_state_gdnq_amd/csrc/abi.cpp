@@ -1021,4 +1021,201 @@ gdnq_status gdnq_delta_step(const gdnq_delta_params* p, const void* q, const voi
   return launched(gdnq::launch_delta_step(L, static_cast<hipStream_t>(stream)), "delta rule step launch", stream);
 }
 
+// ---------------------------------------------------------------- norms of queries and keys
+
+static gdnq_status qk_validate(const gdnq_qk_params* p, gdnq::QkLaunch& L) {
+  if (!p) return fail(GDNQ_ERR_NULL, "params is NULL");
+  if (p->rows < 0 || p->q_heads < 1 || p->k_heads < 1 || p->width < 1 || p->width > 512)
+    return fail(GDNQ_ERR_SHAPE, "rows = %d, q_heads = %d, k_heads = %d, width = %d (1 .. 512)", p->rows, p->q_heads, p->k_heads, p->width);
+  // in 64 bits: the heads' sum alone may pass 32
+  const int64_t heads = int64_t(p->q_heads) + p->k_heads;
+  if (heads > (1 << 20) || heads * p->rows > 0x7fffffffLL)
+    return fail(GDNQ_ERR_SHAPE, "%lld heads of %d rows: at most 2^20 and 2^31 - 1 in all", (long long)heads, p->rows);
+  if (p->rotary < 0 || p->rotary % 2 || p->rotary > p->width)
+    return fail(GDNQ_ERR_SHAPE, "rotary = %d: even, 0 .. width %d", p->rotary, p->width);
+  if (p->rows > 1 && (p->q_stride < int64_t(p->q_heads) * p->width || p->k_stride < int64_t(p->k_heads) * p->width ||
+                      p->q_stride > (int64_t(1) << 31) || p->k_stride > (int64_t(1) << 31)))
+    return fail(GDNQ_ERR_SHAPE, "q_stride = %lld, k_stride = %lld: a row or more, up to 2^31", (long long)p->q_stride, (long long)p->k_stride);
+  if (!dtype_ok(p->dtype)) return fail(GDNQ_ERR_DTYPE, "dtype = %d", p->dtype);
+  if (!(p->eps >= 0.0f) || p->eps > 3.0e38f) return fail(GDNQ_ERR_SHAPE, "eps = %g, expected a finite value >= 0", double(p->eps));
+  if (p->flags & ~uint32_t(GDNQ_QK_L2 | GDNQ_QK_INTERLEAVED | GDNQ_QK_POS64))
+    return fail(GDNQ_ERR_FLAGS, "flags 0x%x: GDNQ_QK_L2, GDNQ_QK_INTERLEAVED and GDNQ_QK_POS64", p->flags);
+  L = gdnq::QkLaunch{};
+  L.R = p->rows; L.Hq = p->q_heads; L.Hk = p->k_heads; L.D = p->width; L.rotary = p->rotary; L.eps = p->eps;
+  L.q_stride = p->q_stride; L.k_stride = p->k_stride;
+  L.bf16 = p->dtype == GDNQ_BF16;
+  L.l2 = (p->flags & GDNQ_QK_L2) != 0;
+  L.interleaved = (p->flags & GDNQ_QK_INTERLEAVED) != 0;
+  L.pos64 = (p->flags & GDNQ_QK_POS64) != 0;
+  return GDNQ_OK;
+}
+
+// q and k: present, aligned to their type; the rotation's arguments.
+static gdnq_status qk_inputs(const gdnq_qk_params* p, const gdnq::QkLaunch& L, const void* q, const void* k,
+                             const void* positions, const float* inv_freq) {
+  const size_t es = esize(p->dtype);
+  if (L.R > 0) {
+    if (!q) return fail(GDNQ_ERR_NULL, "q is NULL");
+    if (!k) return fail(GDNQ_ERR_NULL, "k is NULL");
+    if (L.rotary && !positions) return fail(GDNQ_ERR_NULL, "positions is NULL");
+    if (L.rotary && !inv_freq) return fail(GDNQ_ERR_NULL, "inv_freq is NULL");
+  }
+  if (!L.rotary && (positions || inv_freq)) return fail(GDNQ_ERR_SHAPE, "positions and inv_freq: none without rotary columns");
+  if (reinterpret_cast<uintptr_t>(q) % es || reinterpret_cast<uintptr_t>(k) % es)
+    return fail(GDNQ_ERR_ALIGN, "q and k: %zu bytes", es);
+  if (reinterpret_cast<uintptr_t>(positions) % (L.pos64 ? 8 : 4)) return fail(GDNQ_ERR_ALIGN, "positions");
+  return GDNQ_OK;
+}
+
+gdnq_status gdnq_qk_norm(const gdnq_qk_params* p, const void* q, const void* k, const float* q_weight,
+                         const float* k_weight, const void* positions, const float* inv_freq, void* q_out,
+                         void* k_out, void* stream) {
+  gdnq::QkLaunch L;
+  if (gdnq_status st = qk_validate(p, L)) return st;
+  if (gdnq_status st = qk_inputs(p, L, q, k, positions, inv_freq)) return st;
+  if (L.R == 0) return ok();
+  const size_t es = esize(p->dtype), nq = size_t(L.Hq) * L.D, nk = size_t(L.Hk) * L.D;
+  const Span sp[] = {{"q", q, ((L.R - 1) * size_t(L.q_stride) + nq) * es}, {"k", k, ((L.R - 1) * size_t(L.k_stride) + nk) * es},
+                     {"q_weight", q_weight, size_t(L.D) * 4}, {"k_weight", k_weight, size_t(L.D) * 4},
+                     {"positions", positions, size_t(L.R) * (L.pos64 ? 8 : 4)}, {"inv_freq", inv_freq, size_t(L.rotary) * 2},
+                     {"q_out", q_out, L.R * nq * es}, {"k_out", k_out, L.R * nk * es}};
+  if (gdnq_status st = check_ptrs(sp + 6, 2)) return st;
+  if (gdnq_status st = check_optional(sp + 2, 2)) return st;
+  if (gdnq_status st = check_optional(sp + 5, 1)) return st;
+  if (gdnq_status st = check_disjoint(sp, 8, 6)) return st;
+  L.q = q; L.k = k; L.q_weight = q_weight; L.k_weight = k_weight; L.positions = positions; L.inv_freq = inv_freq;
+  L.q_out = q_out; L.k_out = k_out;
+  clear_stale_hip_error();
+  return launched(gdnq::launch_qk_forward(L, static_cast<hipStream_t>(stream)), "qk norm launch", stream);
+}
+
+size_t gdnq_qk_norm_workspace_size(const gdnq_qk_params* p) {
+  gdnq::QkLaunch L;
+  if (qk_validate(p, L) != GDNQ_OK) return 0;
+  return gdnq::qk_workspace_bytes(L);
+}
+
+gdnq_status gdnq_qk_norm_backward(const gdnq_qk_params* p, const void* q, const void* k,
+                                  const float* q_weight, const float* k_weight, const void* positions,
+                                  const float* inv_freq, const void* dq_out, const void* dk_out, void* dq,
+                                  void* dk, float* dq_weight, float* dk_weight, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  gdnq::QkLaunch L;
+  if (gdnq_status st = qk_validate(p, L)) return st;
+  if (gdnq_status st = qk_inputs(p, L, q, k, positions, inv_freq)) return st;
+  const size_t es = esize(p->dtype), nq = size_t(L.Hq) * L.D, nk = size_t(L.Hk) * L.D, need = gdnq::qk_workspace_bytes(L);
+  const size_t apart = L.R > 0 ? size_t(L.R - 1) : 0, some = L.R > 0 ? 1 : 0;
+  const Span sp[] = {{"q", q, (apart * size_t(L.q_stride) + some * nq) * es}, {"k", k, (apart * size_t(L.k_stride) + some * nk) * es},
+                     {"q_weight", q_weight, size_t(L.D) * 4}, {"k_weight", k_weight, size_t(L.D) * 4},
+                     {"positions", positions, size_t(L.R) * (L.pos64 ? 8 : 4)}, {"inv_freq", inv_freq, size_t(L.rotary) * 2},
+                     {"dq_out", dq_out, L.R * nq * es}, {"dk_out", dk_out, L.R * nk * es},
+                     {"dq", dq, L.R * nq * es}, {"dk", dk, L.R * nk * es}, {"dq_weight", dq_weight, size_t(L.D) * 4},
+                     {"dk_weight", dk_weight, size_t(L.D) * 4}, {"workspace", workspace, need}};
+  constexpr int N = sizeof(sp) / sizeof(sp[0]);
+  if (L.R > 0)
+    if (gdnq_status st = check_ptrs(sp + 6, 4)) return st;
+  if (gdnq_status st = check_optional(sp + 2, 2)) return st;
+  if (gdnq_status st = check_optional(sp + 5, N - 5)) return st;
+  if (gdnq_status st = check_workspace(workspace, workspace_bytes, need)) return st;
+  if (gdnq_status st = check_disjoint(sp, N, 8)) return st;
+  if (L.R == 0 && !dq_weight && !dk_weight) return ok();
+  L.q = q; L.k = k; L.q_weight = q_weight; L.k_weight = k_weight; L.positions = positions; L.inv_freq = inv_freq;
+  L.dq_out = dq_out; L.dk_out = dk_out; L.dq = dq; L.dk = dk; L.dq_weight = dq_weight; L.dk_weight = dk_weight;
+  L.workspace = workspace;
+  clear_stale_hip_error();
+  return launched(gdnq::launch_qk_backward(L, static_cast<hipStream_t>(stream)), "qk norm backward launch", stream);
+}
+
+// ---------------------------------------------------------------- 8-bit rows
+
+static gdnq_status int8_depth_ok(int64_t rows, int32_t depth) {
+  if (depth < 16 || depth % 16 || depth > (1 << 17) - 16)
+    return fail(GDNQ_ERR_SHAPE, "depth = %d: a multiple of 16, 16 .. 2^17 - 16", depth);
+  if (rows < 0 || rows > (int64_t(1) << 31)) return fail(GDNQ_ERR_SHAPE, "rows = %lld", (long long)rows);
+  return GDNQ_OK;
+}
+
+static gdnq_status int8_validate(const gdnq_int8_params* p, bool linear, gdnq::Int8Launch& L) {
+  if (!p) return fail(GDNQ_ERR_NULL, "params is NULL");
+  // at most 1024 threads per 16 columns of few rows, 256 per tile of 256 x 256, fewer than 2^32 in a launch
+  if (p->rows < 0 || p->cols < 1 || p->rows > (1 << 30) || p->cols > (1 << 25))
+    return fail(GDNQ_ERR_SHAPE, "rows = %d (at most 2^30), cols = %d (at most 2^25)", p->rows, p->cols);
+  if (gdnq_status st = int8_depth_ok(p->rows, p->depth)) return st;
+  if ((int64_t(p->rows) + 255) / 256 * ((int64_t(p->cols) + 255) / 256) >= 1 << 24)
+    return fail(GDNQ_ERR_SHAPE, "rows = %d, cols = %d: too large", p->rows, p->cols);
+  if (!dtype_ok(p->out_dtype) || (linear && !dtype_ok(p->in_dtype)))
+    return fail(GDNQ_ERR_DTYPE, "in_dtype = %d, out_dtype = %d", p->in_dtype, p->out_dtype);
+  if (p->flags) return fail(GDNQ_ERR_FLAGS, "flags 0x%x: none are defined", p->flags);
+  L = gdnq::Int8Launch{};
+  L.M = p->rows; L.N = p->cols; L.K = p->depth; L.out_bf16 = p->out_dtype == GDNQ_BF16;
+  return GDNQ_OK;
+}
+
+gdnq_status gdnq_int8_quantize(const void* x, int64_t rows, int32_t depth, int32_t dtype, int8_t* codes,
+                               float* scales, void* stream) {
+  if (gdnq_status st = int8_depth_ok(rows, depth)) return st;
+  if (!dtype_ok(dtype)) return fail(GDNQ_ERR_DTYPE, "dtype = %d", dtype);
+  if (rows == 0) return ok();
+  const size_t n = size_t(rows) * depth;
+  const Span sp[] = {{"x", x, n * esize(dtype)}, {"codes", codes, n}, {"scales", scales, size_t(rows) * 4}};
+  if (gdnq_status st = check_ptrs(sp, 3)) return st;
+  if (gdnq_status st = check_disjoint(sp, 3, 1)) return st;
+  clear_stale_hip_error();
+  return launched(gdnq::launch_int8_quantize(x, rows, depth, dtype == GDNQ_BF16, codes, scales,
+                                             static_cast<hipStream_t>(stream)), "int8 quantize launch", stream);
+}
+
+// The quantized activations of gdnq_int8_linear.
+static size_t int8_quantized_bytes(const gdnq::Int8Launch& L) {
+  return mx_align(size_t(L.M) * L.K) + mx_align(size_t(L.M) * 4);
+}
+
+size_t gdnq_int8_workspace_size(const gdnq_int8_params* p) {
+  gdnq::Int8Launch L;
+  if (int8_validate(p, false, L) != GDNQ_OK) return 0;
+  return int8_quantized_bytes(L);
+}
+
+gdnq_status gdnq_int8_matmul(const gdnq_int8_params* p, const int8_t* a_codes, const float* a_scales,
+                             const int8_t* w_codes, const float* w_scales, const float* bias, void* y,
+                             void* stream) {
+  gdnq::Int8Launch L;
+  if (gdnq_status st = int8_validate(p, false, L)) return st;
+  if (L.M == 0) return ok();
+  const Span sp[] = {{"a_codes", a_codes, size_t(L.M) * L.K}, {"a_scales", a_scales, size_t(L.M) * 4},
+                     {"w_codes", w_codes, size_t(L.N) * L.K}, {"w_scales", w_scales, size_t(L.N) * 4},
+                     {"y", y, size_t(L.M) * L.N * esize(p->out_dtype)}, {"bias", bias, size_t(L.N) * 4}};
+  if (gdnq_status st = check_ptrs(sp, 5)) return st;
+  if (gdnq_status st = check_optional(sp, 6)) return st;
+  if (gdnq_status st = check_disjoint(sp, 5, 4)) return st;
+  if (overlap(sp[4], sp[5])) return fail(GDNQ_ERR_ALIAS, "y overlaps bias");
+  L.a_codes = a_codes; L.a_scales = a_scales; L.w_codes = w_codes; L.w_scales = w_scales; L.bias = bias; L.y = y;
+  clear_stale_hip_error();
+  return launched(gdnq::launch_int8_matmul(L, static_cast<hipStream_t>(stream)), "int8 product launch", stream);
+}
+
+gdnq_status gdnq_int8_linear(const gdnq_int8_params* p, const void* x, const int8_t* w_codes,
+                             const float* w_scales, const float* bias, void* y, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  gdnq::Int8Launch L;
+  if (gdnq_status st = int8_validate(p, true, L)) return st;
+  if (L.M == 0) return ok();
+  const size_t need = int8_quantized_bytes(L);
+  const Span sp[] = {{"x", x, size_t(L.M) * L.K * esize(p->in_dtype)}, {"w_codes", w_codes, size_t(L.N) * L.K},
+                     {"w_scales", w_scales, size_t(L.N) * 4}, {"bias", bias, size_t(L.N) * 4},
+                     {"y", y, size_t(L.M) * L.N * esize(p->out_dtype)}, {"workspace", workspace, need}};
+  if (gdnq_status st = check_ptrs(sp, 3)) return st;
+  if (gdnq_status st = check_ptrs(sp + 4, 1)) return st;
+  if (gdnq_status st = check_optional(sp, 5)) return st;
+  if (gdnq_status st = check_workspace(workspace, workspace_bytes, need)) return st;
+  if (gdnq_status st = check_disjoint(sp, 6, 4)) return st;
+  int8_t* codes = static_cast<int8_t*>(workspace);
+  float* scales = reinterpret_cast<float*>(codes + mx_align(size_t(L.M) * L.K));
+  L.a_codes = codes; L.a_scales = scales; L.w_codes = w_codes; L.w_scales = w_scales; L.bias = bias; L.y = y;
+  clear_stale_hip_error();
+  hipError_t e = gdnq::launch_int8_quantize(x, L.M, L.K, p->in_dtype == GDNQ_BF16, codes, scales, static_cast<hipStream_t>(stream));
+  if (e == hipSuccess) e = gdnq::launch_int8_matmul(L, static_cast<hipStream_t>(stream));
+  return launched(e, "int8 linear launch", stream);
+}
+
 }  // extern "C"

@@ -184,4 +184,46 @@ hipError_t launch_delta_backward(const DeltaLaunch& L, hipStream_t stream);
 // one token per sequence: h0 in, h_last out
 hipError_t launch_delta_step(const DeltaLaunch& L, hipStream_t stream);
 
+// Norms of queries and keys with the position rotation (qk_norm.hip).
+struct QkLaunch {
+  const void* q;  // rows of Hq (Hk) heads, q_stride (k_stride) elements apart
+  const void* k;
+  const float* q_weight;
+  const float* k_weight;
+  const void* positions;  // int32, or int64 with pos64
+  const float* inv_freq;
+  void* q_out;
+  void* k_out;
+  const void* dq_out;
+  const void* dk_out;
+  void* dq;
+  void* dk;
+  float* dq_weight;
+  float* dk_weight;
+  void* workspace;
+  int64_t R, q_stride, k_stride;
+  int Hq, Hk, D, rotary;
+  int group;  // tokens of a workgroup at a time
+  float eps;
+  bool bf16, l2, interleaved, pos64;
+};
+size_t qk_workspace_bytes(const QkLaunch& L);
+hipError_t launch_qk_forward(const QkLaunch& L, hipStream_t stream);
+hipError_t launch_qk_backward(const QkLaunch& L, hipStream_t stream);
+
+// The row codec on rows of any length, and the product of such rows (int8.hip).
+struct Int8Launch {
+  const int8_t* a_codes;
+  const float* a_scales;
+  const int8_t* w_codes;
+  const float* w_scales;
+  const float* bias;
+  void* y;
+  int M, N, K;
+  bool out_bf16;
+};
+hipError_t launch_int8_quantize(const void* x, int64_t rows, int K, bool bf16, int8_t* codes, float* scales,
+                                hipStream_t stream);
+hipError_t launch_int8_matmul(const Int8Launch& L, hipStream_t stream);
+
 }  // namespace gdnq

@@ -1005,3 +1005,213 @@ def delta_rule_step(q, k, v, alpha, beta, h, *, log_decay=False, out_dtype=None,
     _checked(o, "o", out_dtype, dev, v.shape)
     _launch(dev, _lib.delta_step, p, _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), _ptr(h), _ptr(h_out), _ptr(o))
     return o
+
+
+# ---------------------------------------------------------------- queries and keys
+
+
+def _head_rows(t, name, dtype, dev):
+    """A tensor [..,heads,width] whose rows [heads,width] are dense and evenly
+    apart, as views of a fused projection's rows are: (leading shape, rows,
+    elements from row to row)."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dtype != dtype or t.device != dev:
+        raise ValueError(f"{name} must be {dtype} on {dev}, got {t.dtype} on {t.device}")
+    if t.dim() < 2:
+        raise ValueError(f"{name} must be [..,heads,width]")
+    H, D = t.shape[-2:]
+    lead, strides = t.shape[:-2], t.stride()
+    if t.is_contiguous():
+        rows = 1
+        for s in lead:
+            rows *= s
+        return lead, rows, H * D
+    rows, step = 1, None
+    for size, stride in zip(reversed(lead), reversed(strides[:-2])):
+        if size == 1:
+            continue
+        if step is None:
+            step = stride
+        elif stride != step * rows:
+            raise ValueError(f"{name}: its rows must be evenly apart")
+        rows *= size
+    if (D > 1 and strides[-1] != 1) or (H > 1 and strides[-2] != D):
+        raise ValueError(f"{name}: its heads must be dense")
+    return lead, rows, H * D if step is None else step
+
+
+def _qk_setup(q, k, q_weight, k_weight, positions, inv_freq, norm, eps, interleaved):
+    """The checks the forward and backward calls share."""
+    if q is None or not q.is_cuda:
+        raise ValueError("q must be a GPU tensor")
+    dev = q.device
+    if q.dtype not in _DT:
+        raise ValueError("q must be float32 or bfloat16")
+    if norm not in ("rms", "l2"):
+        raise ValueError(f"norm must be 'rms' or 'l2', got {norm!r}")
+    lead, rows, q_stride = _head_rows(q, "q", q.dtype, dev)
+    k_lead, _, k_stride = _head_rows(k, "k", q.dtype, dev)
+    D = q.shape[-1]
+    if k_lead != lead or k.shape[-1] != D:
+        raise ValueError(f"k must be {tuple(lead)} + [heads,{D}], got {tuple(k.shape)}")
+    for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
+        _optional(t, name, torch.float32, dev, (D,))
+    if (positions is None) != (inv_freq is None):
+        raise ValueError("positions and inv_freq: both or neither")
+    rotary = flags = 0
+    if positions is not None:
+        if positions.dtype not in (torch.int32, torch.int64):
+            raise ValueError("positions must be int32 or int64")
+        _checked(positions, "positions", positions.dtype, dev, lead)
+        _need(inv_freq, "inv_freq", torch.float32, dev)
+        if inv_freq.dim() != 1:
+            raise ValueError("inv_freq: one dimension, a value for every pair of rotated columns")
+        rotary = 2 * inv_freq.numel()
+        if positions.dtype == torch.int64:
+            flags = _lib.GDNQ_QK_POS64
+        if rotary == 0:  # nothing turns
+            positions = inv_freq = None
+    flags |= (_lib.GDNQ_QK_L2 if norm == "l2" else 0) | (_lib.GDNQ_QK_INTERLEAVED if interleaved else 0)
+    _sizes(rows, q.shape[-2], k.shape[-2])
+    _sizes(D, rotary)
+    return _lib.QkParams(rows, q.shape[-2], k.shape[-2], D, rotary, _DT[q.dtype], eps, flags, q_stride, k_stride), \
+        positions, inv_freq
+
+
+def qk_norm(q, k, q_weight=None, k_weight=None, positions=None, inv_freq=None, *, norm="rms", eps=1e-6,
+            interleaved=False, q_out=None, k_out=None):
+    """Norms of every head's queries and keys with the position rotation (see
+    gdnq_qk_norm in include/gdnq.h): what delta_rule and the prefill and
+    decode calls take as q and k.
+
+    q [..,q_heads,width], k [..,k_heads,width] fp32 or bf16, whose rows may be
+    views of a fused projection's; q_weight, k_weight [width] fp32 or None;
+    positions [..] int32 or int64 and inv_freq [rotary / 2] fp32, or None for no
+    rotation.  norm "rms" or "l2"; pairs are (i, i + rotary / 2), or (2i, 2i + 1)
+    with interleaved=True.  Returns (q, k), contiguous."""
+    p, positions, inv_freq = _qk_setup(q, k, q_weight, k_weight, positions, inv_freq, norm, eps, interleaved)
+    dev = q.device
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=dev) if q_out is None else _checked(q_out, "q_out", q.dtype, dev, q.shape)
+    k_out = torch.empty(k.shape, dtype=q.dtype, device=dev) if k_out is None else _checked(k_out, "k_out", q.dtype, dev, k.shape)
+    _launch(dev, _lib.qk_norm, p, _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(positions), _ptr(inv_freq),
+            _ptr(q_out), _ptr(k_out))
+    return q_out, k_out
+
+
+def qk_norm_workspace_size(q, k, rotary=0):
+    """Workspace bytes of qk_norm_backward for these arrays."""
+    rows = 1
+    for s in q.shape[:-2]:
+        rows *= s
+    _sizes(rows, q.shape[-2], k.shape[-2])
+    D = q.shape[-1]
+    return int(_lib.qk_norm_workspace_size(_lib.QkParams(rows, q.shape[-2], k.shape[-2], D, rotary, _DT[q.dtype], 0.0, 0,
+                                                         q.shape[-2] * D, k.shape[-2] * D)))
+
+
+def qk_norm_backward(dq_out, dk_out, q, k, q_weight=None, k_weight=None, positions=None, inv_freq=None, *, norm="rms",
+                     eps=1e-6, interleaved=False, dq=None, dk=None, dq_weight=None, dk_weight=None, workspace=None):
+    """Gradients of qk_norm from dq_out and dk_out (like its results, contiguous),
+    with its arguments.  Returns (dq, dk, dq_weight, dk_weight), contiguous; those
+    of weights that are None are None unless given."""
+    p, positions, inv_freq = _qk_setup(q, k, q_weight, k_weight, positions, inv_freq, norm, eps, interleaved)
+    dev = q.device
+    _checked(dq_out, "dq_out", q.dtype, dev, q.shape)
+    _checked(dk_out, "dk_out", q.dtype, dev, k.shape)
+    dq = torch.empty(q.shape, dtype=q.dtype, device=dev) if dq is None else _checked(dq, "dq", q.dtype, dev, q.shape)
+    dk = torch.empty(k.shape, dtype=q.dtype, device=dev) if dk is None else _checked(dk, "dk", q.dtype, dev, k.shape)
+    D = q.shape[-1]
+    if q_weight is not None and dq_weight is None:
+        dq_weight = torch.empty(D, dtype=torch.float32, device=dev)
+    if k_weight is not None and dk_weight is None:
+        dk_weight = torch.empty(D, dtype=torch.float32, device=dev)
+    _optional(dq_weight, "dq_weight", torch.float32, dev, (D,))
+    _optional(dk_weight, "dk_weight", torch.float32, dev, (D,))
+    ws, ws_bytes = _space(workspace, int(_lib.qk_norm_workspace_size(p)), dev)
+    _launch(dev, _lib.qk_norm_backward, p, _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(positions),
+            _ptr(inv_freq), _ptr(dq_out), _ptr(dk_out), _ptr(dq), _ptr(dk), _ptr(dq_weight), _ptr(dk_weight), _ptr(ws),
+            ws_bytes)
+    return dq, dk, dq_weight, dk_weight
+
+
+# ---------------------------------------------------------------- 8-bit projections
+
+
+def int8_quantize(x, codes=None, scales=None):
+    """Rows in 8-bit integers with a scale each (see gdnq_int8_quantize in
+    include/gdnq.h): x [..,depth] fp32 or bf16, depth a multiple of 16.  Returns
+    (codes [..,depth] int8, scales [..] fp32)."""
+    _need(x, "x", None, None)
+    dev = x.device
+    if x.dtype not in _DT:
+        raise ValueError("x must be float32 or bfloat16")
+    if x.dim() < 1 or x.shape[-1] % 16:
+        raise ValueError("x must be [..,depth] with depth a multiple of 16")
+    depth = x.shape[-1]
+    _sizes(0, depth)  # the rows are 64 bits
+    codes = torch.empty(x.shape, dtype=torch.int8, device=dev) if codes is None else codes
+    scales = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if scales is None else scales
+    _checked(codes, "codes", torch.int8, dev, x.shape)
+    _checked(scales, "scales", torch.float32, dev, x.shape[:-1])
+    _launch(dev, _lib.int8_quantize, _ptr(x), _mx_rows(x), depth, _DT[x.dtype], _ptr(codes), _ptr(scales))
+    return codes, scales
+
+
+def _int8_weights(w_codes, w_scales, bias, depth, dev):
+    _need(w_codes, "w_codes", torch.int8, dev)
+    if w_codes.dim() != 2 or w_codes.shape[1] != depth:
+        raise ValueError(f"w_codes must be [cols,{depth}], got {tuple(w_codes.shape)}")
+    cols = w_codes.shape[0]
+    _checked(w_scales, "w_scales", torch.float32, dev, (cols,))
+    _optional(bias, "bias", torch.float32, dev, (cols,))
+    return cols
+
+
+def int8_workspace_size(rows, cols, depth):
+    """Workspace bytes of int8_linear at these sizes (int8_matmul needs none)."""
+    _sizes(rows, cols, depth)
+    return int(_lib.int8_workspace_size(_lib.Int8Params(rows, cols, depth, 0, 0, 0)))
+
+
+def int8_matmul(a_codes, a_scales, w_codes, w_scales, bias=None, *, out_dtype=torch.bfloat16, y=None):
+    """y [..,cols] = (A W^T) a_scales w_scales + bias for rows a [..,depth] and w
+    [cols,depth] as int8_quantize gives them, bias [cols] fp32 or None (see
+    gdnq_int8_matmul in include/gdnq.h)."""
+    _need(a_codes, "a_codes", torch.int8, None)
+    dev = a_codes.device
+    if a_codes.dim() < 1:
+        raise ValueError("a_codes must be [..,depth]")
+    depth, lead = a_codes.shape[-1], a_codes.shape[:-1]
+    _checked(a_scales, "a_scales", torch.float32, dev, lead)
+    cols = _int8_weights(w_codes, w_scales, bias, depth, dev)
+    y = _mx_out(y, lead, cols, out_dtype, dev)
+    rows = _mx_rows(a_codes)
+    _sizes(rows, cols, depth)
+    p = _lib.Int8Params(rows, cols, depth, 0, _DT[out_dtype], 0)
+    _launch(dev, _lib.int8_matmul, p, _ptr(a_codes), _ptr(a_scales), _ptr(w_codes), _ptr(w_scales), _ptr(bias), _ptr(y))
+    return y
+
+
+def int8_linear(x, w_codes, w_scales, bias=None, *, out_dtype=None, y=None, workspace=None):
+    """y [..,cols] = Q(x) W^T + bias: x [..,depth] fp32 or bf16 quantized as by
+    int8_quantize, times weights w [cols,depth] stored in that form.  out_dtype
+    (default x's) float32 or bfloat16."""
+    _need(x, "x", None, None)
+    dev = x.device
+    if x.dtype not in _DT:
+        raise ValueError("x must be float32 or bfloat16")
+    if x.dim() < 1:
+        raise ValueError("x must be [..,depth]")
+    depth = x.shape[-1]
+    cols = _int8_weights(w_codes, w_scales, bias, depth, dev)
+    out_dtype = out_dtype or (x.dtype if y is None else y.dtype)
+    y = _mx_out(y, x.shape[:-1], cols, out_dtype, dev)
+    rows = _mx_rows(x)
+    _sizes(rows, cols, depth)
+    p = _lib.Int8Params(rows, cols, depth, _DT[x.dtype], _DT[out_dtype], 0)
+    ws, ws_bytes = _space(workspace, int(_lib.int8_workspace_size(p)), dev)
+    _launch(dev, _lib.int8_linear, p, _ptr(x), _ptr(w_codes), _ptr(w_scales), _ptr(bias), _ptr(y), _ptr(ws), ws_bytes)
+    return y

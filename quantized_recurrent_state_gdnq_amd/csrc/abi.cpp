@@ -963,7 +963,6 @@ gdnq_status gdnq_delta_forward(const gdnq_delta_params* p, const int32_t* cu_seq
   if (gdnq_status st = check_offsets(cu_seqlens, L.B, sp, N, 6)) return st;
   L.q = q; L.k = k; L.v = v; L.alpha = alpha; L.beta = beta; L.h0 = h0; L.o = o; L.h_last = h_last; L.carry = carry;
   L.workspace = workspace;
-  L.rows_at = gdnq::delta_carry_rows_at(L);
   clear_stale_hip_error();
   return launched(gdnq::launch_delta_forward(L, static_cast<hipStream_t>(stream)), "delta rule launch", stream);
 }
@@ -994,7 +993,6 @@ gdnq_status gdnq_delta_backward(const gdnq_delta_params* p, const int32_t* cu_se
   if (gdnq_status st = check_offsets(cu_seqlens, L.B, sp, N, 7)) return st;
   L.q = q; L.k = k; L.alpha = alpha; L.beta = beta; L.carry = const_cast<void*>(carry); L.dout = dout; L.dh_last = dh_last;
   L.dq = dq; L.dk_out = dk; L.dv_out = dv; L.dalpha = dalpha; L.dbeta = dbeta; L.dh0 = dh0; L.workspace = workspace;
-  L.rows_at = gdnq::delta_carry_rows_at(L);
   clear_stale_hip_error();
   return launched(gdnq::launch_delta_backward(L, static_cast<hipStream_t>(stream)), "delta rule backward launch", stream);
 }

@@ -30,21 +30,27 @@
 
 namespace gdnq {
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
 constexpr int DELTA_CHUNK = 64;
 // A triangle of 64 x 64 as the first operand of a product: of its 16 x 32
 // blocks six are not zero.  A block is 64 lanes of 16 bytes; hi parts, then lo.
 constexpr int TRI_BLOCKS = 6, TRI_PART = TRI_BLOCKS * 1024, TRI_BYTES = 2 * TRI_PART;
 // Of one chunk of one value head in the workspace: two such triangles, then
-// five rows of 64: c, c_64 / c, beta, and log2 c as a whole number and a rest.
+// rows of 64: c, beta c_64 / c, c_64 / c, beta c (the chains' kilobyte), beta, and
+// log2 c as a whole number and a rest.
 constexpr int DELTA_SCALARS = 2 * TRI_BYTES;
-constexpr int DELTA_CHUNK_BYTES = DELTA_SCALARS + 5 * 256;
+enum { ROW_C, ROW_TAIL_BETA, ROW_TAIL, ROW_C_BETA, ROW_BETA, ROW_WHOLE, ROW_REST, ROWS };
+constexpr int DELTA_CHUNK_BYTES = DELTA_SCALARS + 8 * 256;
 
 inline int64_t delta_slots(const DeltaLaunch& L) {
   return L.cu_seqlens ? L.N / DELTA_CHUNK + L.B : int64_t(L.B) * ((L.T + DELTA_CHUNK - 1) / DELTA_CHUNK);
 }
 __host__ __device__ inline int64_t delta_align(int64_t n) { return (n + 255) / 256 * 256; }
-// A state in two bf16 parts, [2][d_v][d_k].
+// A state in two bf16 parts, [2][d_v][d_k], and behind it a chunk's w or z,
+// [2][d_v][64]: what a chain leaves of a chunk and head.
 __host__ __device__ inline int64_t delta_state_bytes(const DeltaLaunch& L) { return int64_t(L.dv) * L.dk * 4; }
+__host__ __device__ inline int64_t delta_left_bytes(const DeltaLaunch& L) { return int64_t(L.dv) * (L.dk * 4 + DELTA_CHUNK * 4); }
 
 #ifdef __HIPCC__
 
@@ -104,6 +110,13 @@ __device__ __forceinline__ int lds_block(int row, int block) {
     return row * 128 + ((block ^ ((row >> 1 & 1) << 2 | (row >> 2 & 3))) << 4);
 }
 
+// Loads are made whatever the token or column, from a clamped address, and cut
+// to zero where they are used: a branch around a load waits for it on the spot.
+__device__ __forceinline__ u32x4 only_if(bool keep, const u32x4& x) {
+  const uint32_t m = keep ? ~0u : 0u;
+  return x & m;
+}
+
 __device__ __forceinline__ bf16x8 lds_frag(const uint8_t* p) { return *reinterpret_cast<const bf16x8*>(p); }
 
 // 4 x 16 values of 16 bits per 16 lanes, transposed: lane 4 t + p gives the
@@ -143,6 +156,122 @@ __device__ __forceinline__ float exp2_difference(float ar, int aw, float br, int
 __device__ __forceinline__ int chain_row(int tile, int row) {
   return (tile >> 1) * 32 + (row >> 2) * 8 + (tile & 1) * 4 + (row & 3);
 }
+
+// What the workgroup of a chain (256 threads, 64 rows of a state) has in LDS of
+// a chunk: K, Q, the two triangles, 64 columns of V (or dO), and the kilobyte of
+// decays.  All of it comes straight from memory, 16 bytes a lane and 1 KB a wave
+// at a time, in the order of LDS: the permutation of the blocks is in the address
+// that each lane loads from.
+template <int DK>
+struct ChainBuffer {
+  uint8_t k[64 * DK * 2], q[64 * DK * 2], tri[2 * TRI_BYTES], v[64 * 128], rows[1024];
+};
+
+__device__ const uint8_t delta_zeros[16] __attribute__((aligned(16))) = {};
+
+// As a statement that writes no register: the compiler, which would wait for
+// all such loads before any read of LDS, does not know of it, and the kernel
+// waits itself (vmcnt) before the barrier that lets the buffer be read.  The
+// s_nop is the wait that a load into LDS needs behind a scalar write of M0, where
+// the chip takes its place from.
+__device__ __forceinline__ void to_lds(const void* base, uint32_t offset, void* to) {
+  const uint32_t lds = uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)to));
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(offset), "s"(base) : "m0", "memory");
+}
+__device__ __forceinline__ void to_lds(const void* p, void* to) {
+  const uint32_t lds = uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)to));
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(p) : "m0", "memory");
+}
+
+// The row and block that lane place p of a matrix of rows of D bf16 is: the
+// inverse of lds_block.
+template <int D>
+__device__ __forceinline__ void lds_place(int p, int& row, int& block) {
+  row = p / (D / 8);
+  block = (lds_block<D>(row, p % (D / 8)) >> 4) % (D / 8);
+}
+
+template <int DK>
+struct ChainLoader {
+  static constexpr int LOADS = 64 * (DK / 8) / 256;
+  uint32_t at_k[LOADS], at_v[2];  // byte offsets in a whole chunk
+  const uint8_t *k, *q, *v;       // of the call's first token, this head, this group of columns
+  const uint8_t* space;           // the workspace at this head
+  int64_t krow, vrow, chunk_stride;
+  int dk, cols, wave, lane;
+  bool exact;                     // no columns of K to be zero
+
+  __device__ __forceinline__ void init(const DeltaLaunch& L, const void* values, int h, int group, int wave_, int lane_) {
+    wave = wave_;
+    lane = lane_;
+    dk = L.dk;
+    exact = L.dk == DK;
+    const int kh = h / (L.H / L.G);
+    krow = int64_t(L.G) * L.dk * 2;
+    vrow = int64_t(L.H) * L.dv * 2;
+    k = static_cast<const uint8_t*>(L.k) + int64_t(kh) * L.dk * 2;
+    q = static_cast<const uint8_t*>(L.q) + int64_t(kh) * L.dk * 2;
+    v = static_cast<const uint8_t*>(values) + (int64_t(h) * L.dv + group * 64) * 2;
+    cols = min(64, L.dv - group * 64);
+    space = static_cast<const uint8_t*>(L.workspace) + int64_t(h) * DELTA_CHUNK_BYTES;
+    chunk_stride = int64_t(L.H) * DELTA_CHUNK_BYTES;
+    int row, block;
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+      lds_place<DK>((i * 4 + wave) * 64 + lane, row, block);
+      at_k[i] = uint32_t(row) * uint32_t(krow) + block * 16;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      lds_place<64>((i * 4 + wave) * 64 + lane, row, block);
+      at_v[i] = uint32_t(row) * uint32_t(vrow) + min(block * 8, cols - 8) * 2;  // columns beyond the last: no matter
+    }
+  }
+
+  // n tokens from `first` on, chunk slot `slot`.  Rows behind the last token are
+  // the last one's again (beta = 0 there), or zeros where ZERO_V.
+  template <bool ZERO_V>
+  __device__ __forceinline__ void load(ChainBuffer<DK>& to, int64_t first, int n, int64_t slot) const {
+    const uint8_t* ws = space + slot * chunk_stride;
+    const uint8_t *kf = k + first * krow, *qf = q + first * krow, *vf = v + first * vrow;
+#pragma unroll
+    for (int i = 0; i < 6; ++i) to_lds(ws, (i * 4 + wave) * 1024 + lane * 16, to.tri + (i * 4 + wave) * 1024);
+    if (wave == 0) to_lds(ws + DELTA_SCALARS, lane * 16, to.rows);
+    if (exact && n == 64) {
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i) {
+        to_lds(kf, at_k[i], to.k + (i * 4 + wave) * 1024);
+        to_lds(qf, at_k[i], to.q + (i * 4 + wave) * 1024);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) to_lds(vf, at_v[i], to.v + (i * 4 + wave) * 1024);
+      return;
+    }
+    int row, block;
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+      lds_place<DK>((i * 4 + wave) * 64 + lane, row, block);
+      const int64_t at = min(row, n - 1) * krow + block * 16;
+      to_lds(block * 8 < dk ? kf + at : delta_zeros, to.k + (i * 4 + wave) * 1024);
+      to_lds(block * 8 < dk ? qf + at : delta_zeros, to.q + (i * 4 + wave) * 1024);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      lds_place<64>((i * 4 + wave) * 64 + lane, row, block);
+      const uint8_t* p = vf + min(row, n - 1) * vrow + min(block * 8, cols - 8) * 2;
+      to_lds(ZERO_V && row >= n ? delta_zeros : p, to.v + (i * 4 + wave) * 1024);
+    }
+  }
+};
+
+// Four tokens of tile it of a lane's column, out of the 64 columns in LDS.
+__device__ __forceinline__ s16x4 chain_column(const uint8_t* v, int it, int wave, int lane) {
+  const int c = lane & 15, g = lane >> 4;
+  typedef __attribute__((address_space(3))) s16x4* lds4;
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+      (lds4)(v + lds_block<64>(chain_row(it, g * 4) + (c >> 2), wave * 2 + ((c & 3) >> 1)) + (c & 1) * 8));
+}
+__device__ __forceinline__ float bf16_value(short x) { return __uint_as_float(uint32_t(uint16_t(x)) << 16); }
 
 #endif  // __HIPCC__
 

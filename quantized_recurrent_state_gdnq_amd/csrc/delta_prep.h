@@ -1,6 +1,7 @@
 // What the chains of the trained delta rule need of every chunk and does not
 // depend on the state: the inverse of I + At B (forward) or the transposed one
-// of I + B At (backward), the triangle M or its transpose, and the decays.
+// of I + B At (backward), the triangle M B (so that the chain needs w alone) or
+// the transpose of M, and the decays.
 // One workgroup of four waves per chunk and value head.
 #pragma once
 
@@ -117,21 +118,23 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaLaunch L) {
     rest[lane] = r;
     whole[lane] = wi;
     beta[lane] = bt;
-    float* sc = reinterpret_cast<float*>(out + DELTA_SCALARS);
-    sc[lane] = exp2_difference(r, wi, 0.0f, 0);
-    sc[64 + lane] = exp2_difference(__shfl(r, 63), __shfl(wi, 63), r, wi);
-    sc[128 + lane] = bt;
-    reinterpret_cast<int*>(sc)[192 + lane] = wi;
-    sc[256 + lane] = r;
+    float* sc = reinterpret_cast<float*>(out + DELTA_SCALARS) + lane;
+    const float c1 = exp2_difference(r, wi, 0.0f, 0), tail = exp2_difference(__shfl(r, 63), __shfl(wi, 63), r, wi);
+    sc[ROW_C * 64] = c1;
+    sc[ROW_TAIL_BETA * 64] = tail * bt;
+    sc[ROW_TAIL * 64] = tail;
+    sc[ROW_C_BETA * 64] = c1 * bt;
+    sc[ROW_BETA * 64] = bt;
+    reinterpret_cast<int*>(sc)[ROW_WHOLE * 64] = wi;
+    sc[ROW_REST * 64] = r;
   }
   // Wave it: the rows of tile it, against the tiles up to it.
   const bf16* kp = static_cast<const bf16*>(L.k) + int64_t(kh) * L.dk;
   const bf16* qp = static_cast<const bf16*>(L.q) + int64_t(kh) * L.dk;
   auto frag = [&](const bf16* p, int row, int j) {
-    bf16x8 x = {};
     const int at = j * 32 + g * 8;
-    if (row < tokens && at < L.dk) x = *reinterpret_cast<const bf16x8*>(p + (first + row) * (int64_t(L.G) * L.dk) + at);
-    return x;
+    const u32x4 x = *reinterpret_cast<const u32x4*>(p + (first + min(row, tokens - 1)) * (int64_t(L.G) * L.dk) + min(at, L.dk - 8));
+    return __builtin_bit_cast(bf16x8, only_if(row < tokens && at < L.dk, x));
   };
   f32x4 kk[4] = {}, qk[4] = {};
 #pragma unroll
@@ -155,7 +158,7 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaLaunch L) {
       const int i = wave * 16 + g * 4 + e;
       float rho = 0.0f;
       if (j <= i) rho = exp2_difference(rest[i], whole[i], rest[j], whole[j]);
-      m[i * P + j] = rho * qk[jt][e];
+      m[i * P + j] = BACK ? rho * qk[jt][e] : rho * qk[jt][e] * beta[j];
       a[i * P + j] = j < i ? rho * kk[jt][e] * beta[BACK ? i : j] : 0.0f;
     }
   }

@@ -1,6 +1,8 @@
 // The gated delta rule with its state in fp32: chunks of 64 tokens on the
 // matrix units (forward), and one token per sequence.  The backward pass is in
 // delta_rule_backward.hip; the formulas are in delta_common.h.
+#include <type_traits>
+
 #include "delta_common.h"
 #include "delta_prep.h"
 
@@ -17,23 +19,17 @@ namespace {
 // this one's are used.
 template <int DK, bool SAVE, typename O>
 __global__ __launch_bounds__(256, 1) void delta_chain_kernel(DeltaLaunch L, int row_groups) {
-  constexpr int BLOCKS = DK / 8, KB = DK / 32, TILES = DK / 16;
-  constexpr int MAT = 64 * DK * 2, LOADS = 64 * BLOCKS / 256;
-  struct Buffer {
-    uint8_t k[MAT], q[MAT], n[TRI_BYTES], m[TRI_BYTES];
-  };
-  __shared__ __attribute__((aligned(1024))) Buffer buffers[2];
+  constexpr int KB = DK / 32, TILES = DK / 16;
+  __shared__ __attribute__((aligned(1024))) ChainBuffer<DK> buffers[2];
   const int h = blockIdx.x / row_groups % L.H, b = blockIdx.x / row_groups / L.H, group = blockIdx.x % row_groups;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
   const int col = group * 64 + wave * 16 + c;
   const bool mine = col < L.dv;
-  const int kh = h / (L.H / L.G);
   const DeltaSpan s = delta_sequence(L, b);
   const int chunks = (s.tokens + 63) / 64;
-  const bf16* kp = static_cast<const bf16*>(L.k);
-  const bf16* qp = static_cast<const bf16*>(L.q);
-  const bf16* vp = static_cast<const bf16*>(L.v);
-  const int64_t krow = int64_t(L.G) * L.dk, vrow = int64_t(L.H) * L.dv;
+  ChainLoader<DK> loader;
+  loader.init(L, L.v, h, group, wave, lane);
+  const int64_t vrow = int64_t(L.H) * L.dv;
 
   f32x4 S[TILES];
   const int64_t state_row = ((int64_t(b) * L.H + h) * L.dv + col) * L.dk;
@@ -43,84 +39,34 @@ __global__ __launch_bounds__(256, 1) void delta_chain_kernel(DeltaLaunch L, int 
     S[t] = f32x4{0, 0, 0, 0};
     if (L.h0 && mine && at < L.dk) S[t] = *reinterpret_cast<const f32x4*>(L.h0 + state_row + at);
   }
-
-  uint4 rk[LOADS], rq[LOADS], rn[3], rm[3];
-  f32x4 gamma[4], tail[4], beta[4];
-  bf16 v[4][4];
-  auto fetch = [&](int chunk) {
-    const int64_t first = s.first + int64_t(chunk) * 64;
-    const int n = min(64, s.tokens - chunk * 64);
-#pragma unroll
-    for (int i = 0; i < LOADS; ++i) {
-      const int p = i * 256 + threadIdx.x, row = p / BLOCKS, block = p % BLOCKS;
-      rk[i] = rq[i] = uint4{0, 0, 0, 0};
-      if (row < n && block * 8 < L.dk) {
-        const int64_t at = (first + row) * krow + int64_t(kh) * L.dk + block * 8;
-        rk[i] = *reinterpret_cast<const uint4*>(kp + at);
-        rq[i] = *reinterpret_cast<const uint4*>(qp + at);
-      }
-    }
-    const uint8_t* ws = static_cast<const uint8_t*>(L.workspace) + ((s.slot + chunk) * L.H + h) * DELTA_CHUNK_BYTES;
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      rn[i] = *reinterpret_cast<const uint4*>(ws + (i * 256 + threadIdx.x) * 16);
-      rm[i] = *reinterpret_cast<const uint4*>(ws + TRI_BYTES + (i * 256 + threadIdx.x) * 16);
-    }
-  };
-  // What a lane needs of its four tokens a tile: read a chunk ahead, too.
-  auto fetch_rows = [&](int chunk) {
-    const int64_t first = s.first + int64_t(chunk) * 64;
-    const int n = min(64, s.tokens - chunk * 64);
-    const float* sc = reinterpret_cast<const float*>(static_cast<const uint8_t*>(L.workspace) +
-                                                     ((s.slot + chunk) * L.H + h) * DELTA_CHUNK_BYTES + DELTA_SCALARS);
-#pragma unroll
-    for (int it = 0; it < 4; ++it) {
-      const int row = chain_row(it, g * 4);
-      gamma[it] = *reinterpret_cast<const f32x4*>(sc + row);
-      tail[it] = *reinterpret_cast<const f32x4*>(sc + 64 + row);
-      beta[it] = *reinterpret_cast<const f32x4*>(sc + 128 + row);
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        v[it][e] = mine && row + e < n ? vp[(first + row + e) * vrow + int64_t(h) * L.dv + col] : bf16(0.0f);
-    }
-  };
-  auto put = [&](Buffer& to) {
-#pragma unroll
-    for (int i = 0; i < LOADS; ++i) {
-      const int p = i * 256 + threadIdx.x, at = lds_block<DK>(p / BLOCKS, p % BLOCKS);
-      *reinterpret_cast<uint4*>(to.k + at) = rk[i];
-      *reinterpret_cast<uint4*>(to.q + at) = rq[i];
-    }
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      *reinterpret_cast<uint4*>(to.n + (i * 256 + threadIdx.x) * 16) = rn[i];
-      *reinterpret_cast<uint4*>(to.m + (i * 256 + threadIdx.x) * 16) = rm[i];
-    }
-  };
-
-  if (chunks > 0) {
-    fetch(0);
-    fetch_rows(0);
-    put(buffers[0]);
-  }
+  if (chunks > 0) loader.template load<false>(buffers[0], s.first, min(64, s.tokens), s.slot);
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
   for (int chunk = 0; chunk < chunks; ++chunk) {
-    const Buffer& buf = buffers[chunk & 1];
-    if (chunk + 1 < chunks) fetch(chunk + 1);
+    const ChainBuffer<DK>& buf = buffers[chunk & 1];
+    const int64_t first = s.first + int64_t(chunk) * 64;
+    const int n = min(64, s.tokens - chunk * 64);
+    if (chunk + 1 < chunks)
+      loader.template load<false>(buffers[(chunk + 1) & 1], first + 64, min(64, s.tokens - chunk * 64 - 64), s.slot + chunk + 1);
+    bf16* left = nullptr;  // this chunk's part of the carry
+    if constexpr (SAVE)
+      left = reinterpret_cast<bf16*>(static_cast<uint8_t*>(L.carry) + ((s.slot + chunk) * L.H + h) * delta_left_bytes(L));
     bf16x8 sh[KB], sl[KB];
 #pragma unroll
-    for (int j = 0; j < KB; ++j) split8(S[2 * j], S[2 * j + 1], sh[j], sl[j]);
-    if constexpr (SAVE) {
-      bf16* to = reinterpret_cast<bf16*>(static_cast<uint8_t*>(L.carry) + ((s.slot + chunk) * L.H + h) * delta_state_bytes(L));
-#pragma unroll
-      for (int j = 0; j < KB; ++j) {
+    for (int j = 0; j < KB; ++j) {
+      split8(S[2 * j], S[2 * j + 1], sh[j], sl[j]);
+      if constexpr (SAVE) {
         const int at = j * 32 + g * 8;
         if (mine && at < L.dk) {
-          *reinterpret_cast<bf16x8*>(to + int64_t(col) * L.dk + at) = sh[j];
-          *reinterpret_cast<bf16x8*>(to + int64_t(L.dv + col) * L.dk + at) = sl[j];
+          *reinterpret_cast<bf16x8*>(left + col * L.dk + at) = sh[j];
+          *reinterpret_cast<bf16x8*>(left + (L.dv + col) * L.dk + at) = sl[j];
         }
       }
     }
+    const float* rows = reinterpret_cast<const float*>(buf.rows);
+    // x = V - c K S^T by tokens (rows), and O^T = (c Q S^T)^T by tokens in lanes,
+    // so that a lane has four adjacent values of a token to store: the operands
+    // are the same registers, in the other order.
     f32x4 x[4], o[4];
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
@@ -130,52 +76,38 @@ __global__ __launch_bounds__(256, 1) void delta_chain_kernel(DeltaLaunch L, int 
       for (int j = 0; j < KB; ++j) {
         const int at = lds_block<DK>(row, j * 4 + g);
         x[it] = mfma_exact_split(lds_frag(buf.k + at), sh[j], sl[j], x[it]);
-        o[it] = mfma_exact_split(lds_frag(buf.q + at), sh[j], sl[j], o[it]);
+        const bf16x8 q8 = lds_frag(buf.q + at);
+        o[it] = mfma16(sh[j], q8, mfma16(sl[j], q8, o[it]));
       }
     }
 #pragma unroll
-    for (int it = 0; it < 4; ++it)
+    for (int it = 0; it < 4; ++it) {
+      const s16x4 v = chain_column(buf.v, it, wave, lane);
+      const f32x4 decay = *reinterpret_cast<const f32x4*>(rows + ROW_C * 64 + chain_row(it, g * 4));
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[it][e] = float(v[it][e]) - gamma[it][e] * x[it][e];
+      for (int e = 0; e < 4; ++e) x[it][e] = bf16_value(v[e]) - decay[e] * x[it][e];
+      o[it] *= rows[ROW_C * 64 + chain_row(it, c)];
+    }
+    // The six blocks of a triangle: tiles 0 and 1 with the first 32 tokens, 2 and
+    // 3 with both halves.
     bf16x8 hi[2], lo[2];
-    auto triangle = [&](const uint8_t* tri, f32x4 (&d)[4]) {
-#pragma unroll
-      for (int it = 0; it < 4; ++it)
-#pragma unroll
-        for (int j = 0; j <= it / 2; ++j) {
-          const uint8_t* at = tri + (it < 2 ? it : 2 * it - 2 + j) * 1024 + lane * 16;
-          d[it] = mfma_split_split(lds_frag(at), lds_frag(at + TRI_PART), hi[j], lo[j], d[it]);
-        }
-    };
     split8(x[0], x[1], hi[0], lo[0]);
     split8(x[2], x[3], hi[1], lo[1]);
     f32x4 w[4] = {};
-    triangle(buf.n, w);
-    const int64_t first = s.first + int64_t(chunk) * 64;
-    const int n = min(64, s.tokens - chunk * 64);
-    if constexpr (SAVE) {
-      float* to = reinterpret_cast<float*>(static_cast<uint8_t*>(L.carry) + L.rows_at);
 #pragma unroll
-      for (int it = 0; it < 4; ++it)
+    for (int it = 0; it < 4; ++it)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int row = chain_row(it, g * 4 + e);
-          if (mine && row < n) to[(first + row) * vrow + int64_t(h) * L.dv + col] = w[it][e];
-        }
-    }
+      for (int j = 0; j <= it / 2; ++j) {
+        const uint8_t* at = buf.tri + (it < 2 ? it : 2 * it - 2 + j) * 1024 + lane * 16;
+        w[it] = mfma_split_split(lds_frag(at), lds_frag(at + TRI_PART), hi[j], lo[j], w[it]);
+      }
     f32x4 tu[4];
 #pragma unroll
-    for (int it = 0; it < 4; ++it) {
-      w[it] *= beta[it];
-      tu[it] = w[it] * tail[it];
-      o[it] *= gamma[it];
-    }
-    split8(w[0], w[1], hi[0], lo[0]);
-    split8(w[2], w[3], hi[1], lo[1]);
+    for (int it = 0; it < 4; ++it) tu[it] = w[it] * *reinterpret_cast<const f32x4*>(rows + ROW_TAIL_BETA * 64 + chain_row(it, g * 4));
     bf16x8 th[2], tl[2];
     split8(tu[0], tu[1], th[0], tl[0]);
     split8(tu[2], tu[3], th[1], tl[1]);
-    const float whole = __shfl(gamma[3][3], 63);  // the last token's: row 63 is tile 3's, g = 3, e = 3
+    const float whole = rows[ROW_C * 64 + 63];
 #pragma unroll
     for (int t = 0; t < TILES; ++t) {
       S[t] *= whole;
@@ -187,22 +119,39 @@ __global__ __launch_bounds__(256, 1) void delta_chain_kernel(DeltaLaunch L, int 
         S[t] = mfma_exact_split(a, th[j], tl[j], S[t]);
       }
     }
-    triangle(buf.m, o);
-    if (mine) {
-      O* op = static_cast<O*>(L.o);
+    split8(w[0], w[1], hi[0], lo[0]);
+    split8(w[2], w[3], hi[1], lo[1]);
 #pragma unroll
-      for (int it = 0; it < 4; ++it)
+    for (int it = 0; it < 4; ++it)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int row = chain_row(it, g * 4 + e);
-          if (row < n) store_f32(op + (first + row) * vrow + int64_t(h) * L.dv + col, o[it][e]);
-        }
-    }
-    if (chunk + 1 < chunks) {
-      fetch_rows(chunk + 1);
-      put(buffers[(chunk + 1) & 1]);
-    }
+      for (int j = 0; j <= it / 2; ++j) {
+        const uint8_t* at = buf.tri + TRI_BYTES + (it < 2 ? it : 2 * it - 2 + j) * 1024 + lane * 16;
+        o[it] = mfma_split_split(hi[j], lo[j], lds_frag(at), lds_frag(at + TRI_PART), o[it]);
+      }
+    // the next chunk is in LDS, and nobody reads this one any more; the stores
+    // below are behind this wait, so that the next chunk's covers them
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
+    if constexpr (SAVE) {
+      if (mine) {
+        bf16* wp = left + 2 * L.dv * L.dk;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          *reinterpret_cast<bf16x8*>(wp + col * 64 + j * 32 + g * 8) = hi[j];
+          *reinterpret_cast<bf16x8*>(wp + (L.dv + col) * 64 + j * 32 + g * 8) = lo[j];
+        }
+      }
+    }
+    const int oc = group * 64 + wave * 16 + g * 4;
+    if (oc < L.dv) {
+      O* op = static_cast<O*>(L.o) + first * vrow + int64_t(h) * L.dv + oc;
+      typedef O o4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+      for (int it = 0; it < 4; ++it) {
+        const int row = chain_row(it, c);
+        if (row < n) *reinterpret_cast<o4*>(op + row * vrow) = __builtin_convertvector(o[it], o4);
+      }
+    }
   }
   if (L.h_last && mine) {
 #pragma unroll
@@ -326,8 +275,7 @@ hipError_t step_of(const DeltaLaunch& L, hipStream_t stream) {
 
 }  // namespace
 
-size_t delta_carry_rows_at(const DeltaLaunch& L) { return size_t(delta_align(delta_slots(L) * L.H * delta_state_bytes(L))); }
-size_t delta_carry_bytes(const DeltaLaunch& L) { return delta_carry_rows_at(L) + size_t(L.N) * L.H * L.dv * 4; }
+size_t delta_carry_bytes(const DeltaLaunch& L) { return size_t(delta_slots(L)) * L.H * delta_left_bytes(L); }
 size_t delta_forward_workspace_bytes(const DeltaLaunch& L) { return size_t(delta_slots(L)) * L.H * DELTA_CHUNK_BYTES; }
 
 hipError_t launch_delta_forward(const DeltaLaunch& L, hipStream_t stream) {

@@ -1,46 +1,33 @@
 // Gradients of the chunked delta rule (formulas in delta_common.h and below).
+#include <type_traits>
+
 #include "delta_common.h"
 #include "delta_prep.h"
 
 namespace gdnq {
 namespace {
 
-struct BackwardSpace {
-  int64_t states, rows, bytes;  // dS' of every chunk in two bf16 parts; z of every token
-};
-__host__ __device__ inline BackwardSpace backward_space(const DeltaLaunch& L, int64_t slots) {
-  BackwardSpace s;
-  s.states = delta_align(slots * L.H * DELTA_CHUNK_BYTES);
-  s.rows = s.states + delta_align(slots * L.H * delta_state_bytes(L));
-  s.bytes = s.rows + L.N * L.H * L.dv * 4;
-  return s;
+// The workspace goes on with dS' and z of every chunk and head, as the carry
+// holds S and w.
+__host__ __device__ inline int64_t backward_left_at(const DeltaLaunch& L, int64_t slots) {
+  return delta_align(slots * L.H * DELTA_CHUNK_BYTES);
 }
 
 // ---------------------------------------------------------------- the chain of dS
 //
-// As the forward chain, from the last chunk to the first: dS' leaves it for the
-// gradient kernel, z and dV are its results.
+// As the forward chain, from the last chunk to the first.
 template <int DK>
-__global__ __launch_bounds__(256, 1) void delta_chain_back_kernel(DeltaLaunch L, int row_groups, int64_t states_at,
-                                                                  int64_t rows_at) {
-  constexpr int BLOCKS = DK / 8, KB = DK / 32, TILES = DK / 16;
-  constexpr int MAT = 64 * DK * 2, LOADS = 64 * BLOCKS / 256;
-  struct Buffer {
-    uint8_t k[MAT], q[MAT], n[TRI_BYTES], m[TRI_BYTES];
-  };
-  __shared__ __attribute__((aligned(1024))) Buffer buffers[2];
+__global__ __launch_bounds__(256, 1) void delta_chain_back_kernel(DeltaLaunch L, int row_groups, int64_t left_at) {
+  constexpr int KB = DK / 32, TILES = DK / 16;
+  __shared__ __attribute__((aligned(1024))) ChainBuffer<DK> buffers[2];
   const int h = blockIdx.x / row_groups % L.H, b = blockIdx.x / row_groups / L.H, group = blockIdx.x % row_groups;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
   const int col = group * 64 + wave * 16 + c;
   const bool mine = col < L.dv;
-  const int kh = h / (L.H / L.G);
   const DeltaSpan s = delta_sequence(L, b);
   const int chunks = (s.tokens + 63) / 64;
-  const bf16* kp = static_cast<const bf16*>(L.k);
-  const bf16* qp = static_cast<const bf16*>(L.q);
-  const bf16* dp = static_cast<const bf16*>(L.dout);
-  uint8_t* space = static_cast<uint8_t*>(L.workspace);
-  const int64_t krow = int64_t(L.G) * L.dk, vrow = int64_t(L.H) * L.dv;
+  ChainLoader<DK> loader;
+  loader.init(L, L.dout, h, group, wave, lane);
 
   f32x4 S[TILES];  // dS^T
   const int64_t state_row = ((int64_t(b) * L.H + h) * L.dv + col) * L.dk;
@@ -50,80 +37,28 @@ __global__ __launch_bounds__(256, 1) void delta_chain_back_kernel(DeltaLaunch L,
     S[t] = f32x4{0, 0, 0, 0};
     if (L.dh_last && mine && at < L.dk) S[t] = *reinterpret_cast<const f32x4*>(L.dh_last + state_row + at);
   }
-
-  uint4 rk[LOADS], rq[LOADS], rn[3], rm[3];
-  f32x4 gamma[4], tail[4], beta[4];
-  bf16 d[4][4];
-  auto fetch = [&](int chunk) {
-    const int64_t first = s.first + int64_t(chunk) * 64;
-    const int n = min(64, s.tokens - chunk * 64);
-#pragma unroll
-    for (int i = 0; i < LOADS; ++i) {
-      const int p = i * 256 + threadIdx.x, row = p / BLOCKS, block = p % BLOCKS;
-      rk[i] = rq[i] = uint4{0, 0, 0, 0};
-      if (row < n && block * 8 < L.dk) {
-        const int64_t at = (first + row) * krow + int64_t(kh) * L.dk + block * 8;
-        rk[i] = *reinterpret_cast<const uint4*>(kp + at);
-        rq[i] = *reinterpret_cast<const uint4*>(qp + at);
-      }
-    }
-    const uint8_t* ws = space + ((s.slot + chunk) * L.H + h) * DELTA_CHUNK_BYTES;
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      rn[i] = *reinterpret_cast<const uint4*>(ws + (i * 256 + threadIdx.x) * 16);
-      rm[i] = *reinterpret_cast<const uint4*>(ws + TRI_BYTES + (i * 256 + threadIdx.x) * 16);
-    }
-  };
-  auto fetch_rows = [&](int chunk) {
-    const int64_t first = s.first + int64_t(chunk) * 64;
-    const int n = min(64, s.tokens - chunk * 64);
-    const float* sc = reinterpret_cast<const float*>(space + ((s.slot + chunk) * L.H + h) * DELTA_CHUNK_BYTES + DELTA_SCALARS);
-#pragma unroll
-    for (int it = 0; it < 4; ++it) {
-      const int row = chain_row(it, g * 4);
-      gamma[it] = *reinterpret_cast<const f32x4*>(sc + row);
-      tail[it] = *reinterpret_cast<const f32x4*>(sc + 64 + row);
-      beta[it] = *reinterpret_cast<const f32x4*>(sc + 128 + row);
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        d[it][e] = mine && row + e < n ? dp[(first + row + e) * vrow + int64_t(h) * L.dv + col] : bf16(0.0f);
-    }
-  };
-  auto put = [&](Buffer& to) {
-#pragma unroll
-    for (int i = 0; i < LOADS; ++i) {
-      const int p = i * 256 + threadIdx.x, at = lds_block<DK>(p / BLOCKS, p % BLOCKS);
-      *reinterpret_cast<uint4*>(to.k + at) = rk[i];
-      *reinterpret_cast<uint4*>(to.q + at) = rq[i];
-    }
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      *reinterpret_cast<uint4*>(to.n + (i * 256 + threadIdx.x) * 16) = rn[i];
-      *reinterpret_cast<uint4*>(to.m + (i * 256 + threadIdx.x) * 16) = rm[i];
-    }
-  };
-
-  if (chunks > 0) {
-    fetch(chunks - 1);
-    fetch_rows(chunks - 1);
-    put(buffers[0]);
-  }
+  if (chunks > 0)
+    loader.template load<true>(buffers[0], s.first + int64_t(chunks - 1) * 64, s.tokens - (chunks - 1) * 64, s.slot + chunks - 1);
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
   for (int done = 0; done < chunks; ++done) {
     const int chunk = chunks - 1 - done;
-    const Buffer& buf = buffers[done & 1];
-    if (chunk > 0) fetch(chunk - 1);
+    const ChainBuffer<DK>& buf = buffers[done & 1];
+    if (chunk > 0) loader.template load<true>(buffers[(done + 1) & 1], s.first + int64_t(chunk - 1) * 64, 64, s.slot + chunk - 1);
+    bf16* left = reinterpret_cast<bf16*>(static_cast<uint8_t*>(L.workspace) + left_at +
+                                         ((s.slot + chunk) * L.H + h) * delta_left_bytes(L));
     bf16x8 sh[KB], sl[KB];
-    bf16* to = reinterpret_cast<bf16*>(space + states_at + ((s.slot + chunk) * L.H + h) * delta_state_bytes(L));
 #pragma unroll
     for (int j = 0; j < KB; ++j) {
       split8(S[2 * j], S[2 * j + 1], sh[j], sl[j]);
       const int at = j * 32 + g * 8;
       if (mine && at < L.dk) {
-        *reinterpret_cast<bf16x8*>(to + int64_t(col) * L.dk + at) = sh[j];
-        *reinterpret_cast<bf16x8*>(to + int64_t(L.dv + col) * L.dk + at) = sl[j];
+        *reinterpret_cast<bf16x8*>(left + col * L.dk + at) = sh[j];
+        *reinterpret_cast<bf16x8*>(left + (L.dv + col) * L.dk + at) = sl[j];
       }
     }
+    const float* rows = reinterpret_cast<const float*>(buf.rows);
+    auto row4 = [&](int which, int it) { return *reinterpret_cast<const f32x4*>(rows + which * 64 + chain_row(it, g * 4)); };
     f32x4 u[4];
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
@@ -131,21 +66,31 @@ __global__ __launch_bounds__(256, 1) void delta_chain_back_kernel(DeltaLaunch L,
       u[it] = f32x4{0, 0, 0, 0};
 #pragma unroll
       for (int j = 0; j < KB; ++j) u[it] = mfma_exact_split(lds_frag(buf.k + lds_block<DK>(row, j * 4 + g)), sh[j], sl[j], u[it]);
-      u[it] *= tail[it];
+      u[it] *= row4(ROW_TAIL, it);
     }
-    bf16x8 dh[2], dl[2], hi[2], lo[2];
+    // dO, and c dO in parts
+    bf16x8 d[2], dh[2], dl[2], hi[2], lo[2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < 2; ++j) {
+      const s16x4 d0 = chain_column(buf.v, 2 * j, wave, lane), d1 = chain_column(buf.v, 2 * j + 1, wave, lane);
+      typedef short s16x8 __attribute__((ext_vector_type(8)));
+      d[j] = __builtin_bit_cast(bf16x8, s16x8{d0[0], d0[1], d0[2], d0[3], d1[0], d1[1], d1[2], d1[3]});
+      f32x4 a = row4(ROW_C, 2 * j), b4 = row4(ROW_C, 2 * j + 1);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) dh[j][e] = d[2 * j + e / 4][e % 4];
+      for (int e = 0; e < 4; ++e) {
+        a[e] *= bf16_value(d0[e]);
+        b4[e] *= bf16_value(d1[e]);
+      }
+      split8(a, b4, dh[j], dl[j]);
+    }
     // transposed triangles: tiles 0 and 1 take both halves of the tokens, 2 and 3 the second
-    auto block_at = [&](const uint8_t* tri, int it, int j) { return tri + (it < 2 ? it * 2 + j : it + 2) * 1024 + lane * 16; };
+    auto block_at = [&](int it, int j) { return buf.tri + (it < 2 ? it * 2 + j : it + 2) * 1024 + lane * 16; };
 #pragma unroll
     for (int it = 0; it < 4; ++it)
 #pragma unroll
       for (int j = it / 2; j < 2; ++j) {
-        const uint8_t* at = block_at(buf.m, it, j);
-        u[it] = mfma16(lds_frag(at), dh[j], mfma16(lds_frag(at + TRI_PART), dh[j], u[it]));
+        const uint8_t* at = block_at(it, j) + TRI_BYTES;
+        u[it] = mfma16(lds_frag(at), d[j], mfma16(lds_frag(at + TRI_PART), d[j], u[it]));
       }
     split8(u[0], u[1], hi[0], lo[0]);
     split8(u[2], u[3], hi[1], lo[1]);
@@ -154,34 +99,17 @@ __global__ __launch_bounds__(256, 1) void delta_chain_back_kernel(DeltaLaunch L,
     for (int it = 0; it < 4; ++it)
 #pragma unroll
       for (int j = it / 2; j < 2; ++j) {
-        const uint8_t* at = block_at(buf.n, it, j);
+        const uint8_t* at = block_at(it, j);
         z[it] = mfma_split_split(lds_frag(at), lds_frag(at + TRI_PART), hi[j], lo[j], z[it]);
       }
-    const int64_t first = s.first + int64_t(chunk) * 64;
-    const int n = min(64, s.tokens - chunk * 64);
-    float* zp = reinterpret_cast<float*>(space + rows_at);
-    bf16* vp = static_cast<bf16*>(L.dv_out);
-    f32x4 gd[4];
+    bf16x8 zh[2], zl[2];
+    split8(z[0], z[1], zh[0], zl[0]);
+    split8(z[2], z[3], zh[1], zl[1]);
 #pragma unroll
-    for (int it = 0; it < 4; ++it) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int row = chain_row(it, g * 4 + e);
-        const int64_t at = (first + row) * vrow + int64_t(h) * L.dv + col;
-        const float dx = beta[it][e] * z[it][e];
-        if (mine && row < n) {
-          zp[at] = z[it][e];
-          store_f32(vp + at, dx);
-        }
-        z[it][e] = -gamma[it][e] * dx;
-        gd[it][e] = gamma[it][e] * float(d[it][e]);
-      }
-    }
+    for (int it = 0; it < 4; ++it) z[it] *= -row4(ROW_C_BETA, it);
     split8(z[0], z[1], hi[0], lo[0]);
     split8(z[2], z[3], hi[1], lo[1]);
-    split8(gd[0], gd[1], dh[0], dl[0]);
-    split8(gd[2], gd[3], dh[1], dl[1]);
-    const float whole = __shfl(gamma[3][3], 63);
+    const float whole = rows[ROW_C * 64 + 63];
 #pragma unroll
     for (int t = 0; t < TILES; ++t) {
       S[t] *= whole;
@@ -189,15 +117,20 @@ __global__ __launch_bounds__(256, 1) void delta_chain_back_kernel(DeltaLaunch L,
       for (int j = 0; j < 2; ++j) {
         const int row = j * 32 + g * 8 + (c >> 2), block = (t >> 1) * 4 + (c & 3), half = (t & 1) * 8;
         const int a = lds_block<DK>(row, block) + half, b4 = lds_block<DK>(row + 4, block) + half;
-        S[t] = mfma_exact_split(lds_transposed(buf.k + a, buf.k + b4), hi[j], lo[j], S[t]);
         S[t] = mfma_exact_split(lds_transposed(buf.q + a, buf.q + b4), dh[j], dl[j], S[t]);
+        S[t] = mfma_exact_split(lds_transposed(buf.k + a, buf.k + b4), hi[j], lo[j], S[t]);
       }
     }
-    if (chunk > 0) {
-      fetch_rows(chunk - 1);
-      put(buffers[(done + 1) & 1]);
-    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
+    if (mine) {
+      bf16* zp = left + 2 * L.dv * L.dk;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        *reinterpret_cast<bf16x8*>(zp + col * 64 + j * 32 + g * 8) = zh[j];
+        *reinterpret_cast<bf16x8*>(zp + (L.dv + col) * 64 + j * 32 + g * 8) = zl[j];
+      }
+    }
   }
   if (L.dh0 && mine) {
 #pragma unroll
@@ -223,10 +156,10 @@ __global__ __launch_bounds__(256, 1) void delta_chain_back_kernel(DeltaLaunch L,
 // over the key head's value heads in turn (so that their sum needs no atomics
 // and no memory).  S and dS' pass through LDS 32 rows (d_v) at a time.
 template <int DK>
-__global__ __launch_bounds__(256, 1) void delta_gradient_kernel(DeltaLaunch L, int64_t states_at, int64_t rows_at) {
+__global__ __launch_bounds__(256, 1) void delta_gradient_kernel(DeltaLaunch L, int64_t left_at) {
   constexpr int BLOCKS = DK / 8, KB = DK / 32, TILES = DK / 16;
   constexpr int MAT = 64 * DK * 2, LOADS = 64 * BLOCKS / 256, SLAB = 32 * DK * 2, SLAB_LOADS = 4 * 32 * BLOCKS / 256;
-  __shared__ __attribute__((aligned(1024))) uint8_t ks[MAT], qs[MAT], slab[4 * SLAB], us[2 * 4096], pairs[4 * 8192];
+  __shared__ __attribute__((aligned(1024))) uint8_t ks[MAT], qs[MAT], slab[4 * SLAB], wz[4 * 4096], pairs[4 * 8192];
   __shared__ float rest[64], gamma[64], tail[64], beta[64], below[4][64], row_in[64], row_out[64], pair_sum[64], dots[4];
   __shared__ int whole[64];
   const int64_t slot = blockIdx.x / L.G;
@@ -243,13 +176,10 @@ __global__ __launch_bounds__(256, 1) void delta_gradient_kernel(DeltaLaunch L, i
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
       const int p = i * 256 + threadIdx.x, row = p / BLOCKS, block = p % BLOCKS, to = lds_block<DK>(row, block);
-      uint4 k = {0, 0, 0, 0}, q = {0, 0, 0, 0};
-      if (row < n && block * 8 < L.dk) {
-        k = *reinterpret_cast<const uint4*>(kp + (first + row) * krow + block * 8);
-        q = *reinterpret_cast<const uint4*>(qp + (first + row) * krow + block * 8);
-      }
-      *reinterpret_cast<uint4*>(ks + to) = k;
-      *reinterpret_cast<uint4*>(qs + to) = q;
+      const bool keep = row < n && block * 8 < L.dk;
+      const int64_t at = (first + min(row, n - 1)) * krow + min(block * 8, L.dk - 8);
+      *reinterpret_cast<u32x4*>(ks + to) = only_if(keep, *reinterpret_cast<const u32x4*>(kp + at));
+      *reinterpret_cast<u32x4*>(qs + to) = only_if(keep, *reinterpret_cast<const u32x4*>(qp + at));
     }
   }
   __syncthreads();
@@ -272,8 +202,7 @@ __global__ __launch_bounds__(256, 1) void delta_gradient_kernel(DeltaLaunch L, i
   const bool here = token < n;
   const int64_t at_row = (first + (here ? token : 0)) * vrow;
   const bf16* dop = static_cast<const bf16*>(L.dout) + at_row;
-  const float* wp = reinterpret_cast<const float*>(static_cast<const uint8_t*>(L.carry) + L.rows_at) + at_row;
-  const float* zp = reinterpret_cast<const float*>(space + rows_at) + at_row;
+  bf16* dvp = static_cast<bf16*>(L.dv_out) + at_row;
   // 4 x 16 (row, column) blocks of a transposing read
   const int tr_row = g * 8 + (c >> 2), tr_half = (c & 1) * 8;
 
@@ -282,16 +211,16 @@ __global__ __launch_bounds__(256, 1) void delta_gradient_kernel(DeltaLaunch L, i
     const int h = kh * share + hs;
     const int64_t chunk = slot * L.H + h;
     if (threadIdx.x < 64) {
-      const float* sc = reinterpret_cast<const float*>(space + chunk * DELTA_CHUNK_BYTES + DELTA_SCALARS);
-      gamma[lane] = sc[lane];
-      tail[lane] = sc[64 + lane];
-      beta[lane] = sc[128 + lane];
-      whole[lane] = reinterpret_cast<const int*>(sc)[192 + lane];
-      rest[lane] = sc[256 + lane];
+      const float* sc = reinterpret_cast<const float*>(space + chunk * DELTA_CHUNK_BYTES + DELTA_SCALARS) + lane;
+      gamma[lane] = sc[ROW_C * 64];
+      tail[lane] = sc[ROW_TAIL * 64];
+      beta[lane] = sc[ROW_BETA * 64];
+      whole[lane] = reinterpret_cast<const int*>(sc)[ROW_WHOLE * 64];
+      rest[lane] = sc[ROW_REST * 64];
     }
-    const bf16* states = reinterpret_cast<const bf16*>(static_cast<const uint8_t*>(L.carry) + chunk * delta_state_bytes(L));
-    const bf16* dstates = reinterpret_cast<const bf16*>(space + states_at + chunk * delta_state_bytes(L));
-    f32x4 ds[TILES] = {}, xs[TILES] = {}, ud[TILES] = {};  // dO S, dx S, u dS'
+    const bf16* states = reinterpret_cast<const bf16*>(static_cast<const uint8_t*>(L.carry) + chunk * delta_left_bytes(L));
+    const bf16* dstates = reinterpret_cast<const bf16*>(space + left_at + chunk * delta_left_bytes(L));
+    f32x4 ds[TILES] = {}, xs[TILES] = {}, ud[TILES] = {};  // dO S, z S, w dS'
     f32x4 dm[4] = {}, da[4] = {};
     float db = 0.0f, dot = 0.0f;
     __syncthreads();
@@ -301,29 +230,39 @@ __global__ __launch_bounds__(256, 1) void delta_gradient_kernel(DeltaLaunch L, i
 #pragma unroll
       for (int i = 0; i < SLAB_LOADS; ++i) {
         const int p = i * 256 + threadIdx.x, part = p / (32 * BLOCKS), row = p / BLOCKS % 32, block = p % BLOCKS;
-        uint4 x = {0, 0, 0, 0};
-        if (v0 + row < L.dv && block * 8 < L.dk)
-          x = *reinterpret_cast<const uint4*>((part < 2 ? states : dstates) +
-                                              (int64_t(part & 1) * L.dv + v0 + row) * L.dk + block * 8);
-        *reinterpret_cast<uint4*>(slab + part * SLAB + lds_block<DK>(row, block)) = x;
+        const bool keep = v0 + row < L.dv && block * 8 < L.dk;
+        const u32x4 x = *reinterpret_cast<const u32x4*>((part < 2 ? states : dstates) +
+                                                        (int64_t(part & 1) * L.dv + min(v0 + row, L.dv - 1)) * L.dk +
+                                                        min(block * 8, L.dk - 8));
+        *reinterpret_cast<u32x4*>(slab + part * SLAB + lds_block<DK>(row, block)) = only_if(keep, x);
       }
-      bf16x8 o8 = {}, xh, xl, uh, ul;
-      const int at = v0 + g * 8;
-      f32x4 w0 = {}, w1 = {}, z0 = {}, z1 = {};
-      if (here && at < L.dv) {
-        o8 = *reinterpret_cast<const bf16x8*>(dop + int64_t(h) * L.dv + at);
-        w0 = *reinterpret_cast<const f32x4*>(wp + int64_t(h) * L.dv + at);
-        w1 = *reinterpret_cast<const f32x4*>(wp + int64_t(h) * L.dv + at + 4);
-        z0 = *reinterpret_cast<const f32x4*>(zp + int64_t(h) * L.dv + at);
-        z1 = *reinterpret_cast<const f32x4*>(zp + int64_t(h) * L.dv + at + 4);
-      }
+      // w hi, w lo, z hi, z lo: 32 rows of 64 tokens each
 #pragma unroll
-      for (int e = 0; e < 4; ++e) db = fmaf(w0[e], z0[e], fmaf(w1[e], z1[e], db));
-      split8(z0 * bt, z1 * bt, xh, xl);
-      split8(w0 * bt, w1 * bt, uh, ul);
-      *reinterpret_cast<bf16x8*>(us + wave * 1024 + lane * 16) = uh;
-      *reinterpret_cast<bf16x8*>(us + 4096 + wave * 1024 + lane * 16) = ul;
+      for (int i = 0; i < 4; ++i) {
+        const int row = threadIdx.x / 8, block = threadIdx.x % 8;
+        const u32x4 x = *reinterpret_cast<const u32x4*>((i < 2 ? states : dstates) + 2 * int64_t(L.dv) * L.dk +
+                                                        (int64_t(i & 1) * L.dv + min(v0 + row, L.dv - 1)) * 64 + block * 8);
+        *reinterpret_cast<u32x4*>(wz + i * 4096 + lds_block<64>(row, block)) = only_if(v0 + row < L.dv, x);
+      }
+      const bool keep = here && v0 + g * 8 < L.dv;
+      const int64_t at = int64_t(h) * L.dv + min(v0 + g * 8, L.dv - 8);
+      const bf16x8 o8 = __builtin_bit_cast(bf16x8, only_if(keep, *reinterpret_cast<const u32x4*>(dop + at)));
       __syncthreads();
+      // the wave's tokens of w and z, in parts: rows of the first operand
+      auto tokens16 = [&](const uint8_t* part, int tile) {
+        const int block = tile * 2 + ((c & 3) >> 1);
+        return lds_transposed(part + lds_block<64>(tr_row, block) + tr_half, part + lds_block<64>(tr_row + 4, block) + tr_half);
+      };
+      const bf16x8 wh = tokens16(wz, wave), wl = tokens16(wz + 4096, wave);
+      const bf16x8 zh = tokens16(wz + 8192, wave), zl = tokens16(wz + 12288, wave);
+      bf16x8 dv8;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float z = float(zh[e]) + float(zl[e]);
+        db = fmaf(float(wh[e]) + float(wl[e]), z, db);
+        dv8[e] = bf16(bt * z);
+      }
+      if (keep) *reinterpret_cast<bf16x8*>(dvp + at) = dv8;
 #pragma unroll
       for (int t = 0; t < TILES; ++t) {
         const int block = t * 2 + ((c & 3) >> 1);
@@ -332,15 +271,15 @@ __global__ __launch_bounds__(256, 1) void delta_gradient_kernel(DeltaLaunch L, i
         const bf16x8 dh = lds_transposed(slab + 2 * SLAB + a, slab + 2 * SLAB + b);
         const bf16x8 dl = lds_transposed(slab + 3 * SLAB + a, slab + 3 * SLAB + b);
         ds[t] = mfma_exact_split(o8, sh, sl, ds[t]);
-        xs[t] = mfma_split_split(xh, xl, sh, sl, xs[t]);
-        ud[t] = mfma_split_split(uh, ul, dh, dl, ud[t]);
+        xs[t] = mfma_split_split(zh, zl, sh, sl, xs[t]);
+        ud[t] = mfma_split_split(wh, wl, dh, dl, ud[t]);
       }
 #pragma unroll
       for (int jt = 0; jt < 4; ++jt) {
         if (jt > wave) break;
-        const bf16x8 h8 = lds_frag(us + jt * 1024 + lane * 16), l8 = lds_frag(us + 4096 + jt * 1024 + lane * 16);
+        const bf16x8 h8 = tokens16(wz, jt), l8 = tokens16(wz + 4096, jt);
         dm[jt] = mfma_exact_split(o8, h8, l8, dm[jt]);
-        da[jt] = mfma_split_split(xh, xl, h8, l8, da[jt]);
+        da[jt] = mfma_split_split(zh, zl, h8, l8, da[jt]);
       }
       // <S, dS'> of the slab's 32 rows
 #pragma unroll
@@ -370,8 +309,8 @@ __global__ __launch_bounds__(256, 1) void delta_gradient_kernel(DeltaLaunch L, i
       for (int e = 0; e < 4; ++e) {
         const int i = wave * 16 + g * 4 + e;
         const float rho = j <= i ? exp2_difference(rest[i], whole[i], rest[j], whole[j]) : 0.0f;
-        m4[e] = rho * dm[jt][e];
-        a4[e] = j < i ? -rho * da[jt][e] : 0.0f;
+        m4[e] = rho * beta[j] * dm[jt][e];
+        a4[e] = j < i ? -rho * beta[j] * beta[i] * da[jt][e] : 0.0f;
         passing[jt][e] = j <= i ? m4[e] * qk[jt][e] + a4[e] * kk[jt][e] : 0.0f;
       }
       const int to = lds_block<64>(j, wave * 2 + (g >> 1)) + (g & 1) * 8;
@@ -446,13 +385,13 @@ __global__ __launch_bounds__(256, 1) void delta_gradient_kernel(DeltaLaunch L, i
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int row = wave * 16 + g * 4 + e;
-      const float gm = gamma[row], tl = tail[row];
+      const float gm = gamma[row], gb = gm * beta[row], tb = tail[row] * beta[row];
       float in = 0.0f, out = 0.0f;
 #pragma unroll
       for (int t = 0; t < TILES; ++t) {
         const int at = lds_block<DK>(row, t * 2 + (c >> 3)) + (c & 7) * 2;
         const float q = float(*reinterpret_cast<const bf16*>(qs + at)), k = float(*reinterpret_cast<const bf16*>(ks + at));
-        const float a = gm * ds[t][e], x = gm * xs[t][e], u = tl * ud[t][e];
+        const float a = gm * ds[t][e], x = gb * xs[t][e], u = tb * ud[t][e];
         in = fmaf(q, a, fmaf(-k, x, in));
         out = fmaf(k, u, out);
         dq[t][e] += a;
@@ -503,21 +442,24 @@ __global__ __launch_bounds__(256, 1) void delta_gradient_kernel(DeltaLaunch L, i
 template <int DK>
 hipError_t backward(const DeltaLaunch& L, hipStream_t stream) {
   const int64_t slots = delta_slots(L);
-  const BackwardSpace s = backward_space(L, slots);
+  const int64_t left_at = backward_left_at(L, slots);
   if (slots > 0) {
     delta_prep_kernel<DK, true><<<uint32_t(slots * L.H), 256, 0, stream>>>(L);
     if (hipError_t e = hipGetLastError()) return e;
   }
   const int groups = (L.dv + 63) / 64;
-  delta_chain_back_kernel<DK><<<uint32_t(groups) * uint32_t(L.H) * uint32_t(L.B), 256, 0, stream>>>(L, groups, s.states, s.rows);
+  delta_chain_back_kernel<DK><<<uint32_t(groups) * uint32_t(L.H) * uint32_t(L.B), 256, 0, stream>>>(L, groups, left_at);
   if (hipError_t e = hipGetLastError()) return e;
-  if (slots > 0) delta_gradient_kernel<DK><<<uint32_t(slots * L.G), 256, 0, stream>>>(L, s.states, s.rows);
+  if (slots > 0) delta_gradient_kernel<DK><<<uint32_t(slots * L.G), 256, 0, stream>>>(L, left_at);
   return hipGetLastError();
 }
 
 }  // namespace
 
-size_t delta_backward_workspace_bytes(const DeltaLaunch& L) { return size_t(backward_space(L, delta_slots(L)).bytes); }
+size_t delta_backward_workspace_bytes(const DeltaLaunch& L) {
+  const int64_t slots = delta_slots(L);
+  return size_t(backward_left_at(L, slots) + slots * L.H * delta_left_bytes(L));
+}
 
 hipError_t launch_delta_backward(const DeltaLaunch& L, hipStream_t stream) {
   return L.dk <= 64 ? backward<64>(L, stream) : backward<128>(L, stream);

@@ -159,7 +159,7 @@ struct DeltaLaunch {
   const float* h0;  // one token: the state read
   void* o;
   float* h_last;    // one token: the state written
-  void* carry;      // states entering every chunk, then what every token writes
+  void* carry;      // of every chunk and head, the state entering it and what its tokens write
   const void* dout;
   const float* dh_last;
   void* dq;
@@ -171,11 +171,9 @@ struct DeltaLaunch {
   void* workspace;
   int B, T, G, H, dk, dv;
   int64_t N;        // tokens of the call
-  size_t rows_at;   // where the tokens' part of the carry begins
   int row_groups;
   bool in_bf16, out_bf16, log_decay;
 };
-size_t delta_carry_rows_at(const DeltaLaunch& L);
 size_t delta_carry_bytes(const DeltaLaunch& L);
 size_t delta_forward_workspace_bytes(const DeltaLaunch& L);
 size_t delta_backward_workspace_bytes(const DeltaLaunch& L);

@@ -152,175 +152,217 @@ __global__ __launch_bounds__(256, 1) void delta_chain_back_kernel(DeltaLaunch L,
 //                 + sum over j < t of k_j.((c_64 / c) u dS')_j  + c_64 <S, dS'>
 // A sum over what passes token t, with nothing subtracted: what lies before or
 // behind it wholly is not in it.
-//   One workgroup per chunk and key head, wave it the 16 tokens of tile it,
-// over the key head's value heads in turn (so that their sum needs no atomics
-// and no memory).  S and dS' pass through LDS 32 rows (d_v) at a time.
+//   One workgroup of eight waves per chunk and key head, over the key head's
+// value heads in turn (so that their sum needs no atomics and no memory): wave
+// (it, half) has the 16 tokens of tile it, half of the columns (d_k) and dM or
+// dAt.  S, dS', w, z and dO pass through LDS 32 rows (d_v) at a time, the next
+// ones loaded while these are used.  dQ and dK are formed transposed (tokens in
+// lanes), so that a token's factors are a lane's and results leave four at a time.
 template <int DK>
-__global__ __launch_bounds__(256, 1) void delta_gradient_kernel(DeltaLaunch L, int64_t left_at) {
-  constexpr int BLOCKS = DK / 8, KB = DK / 32, TILES = DK / 16;
-  constexpr int MAT = 64 * DK * 2, LOADS = 64 * BLOCKS / 256, SLAB = 32 * DK * 2, SLAB_LOADS = 4 * 32 * BLOCKS / 256;
-  __shared__ __attribute__((aligned(1024))) uint8_t ks[MAT], qs[MAT], slab[4 * SLAB], wz[4 * 4096], pairs[4 * 8192];
-  __shared__ float rest[64], gamma[64], tail[64], beta[64], below[4][64], row_in[64], row_out[64], pair_sum[64], dots[4];
+struct GradientSlab {
+  uint8_t states[4][32 * DK * 2], tokens[4][4096], d[4096];  // S hi, lo, dS' hi, lo; w hi, lo, z hi, lo; dO
+};
+
+// Rows of 32 bf16 in LDS.
+__device__ __forceinline__ int slab_block(int row, int block) { return row * 64 + ((block ^ (row >> 2 & 3)) << 4); }
+
+template <int DK>
+struct GradientLoader {
+  const uint8_t *left[2], *d;  // of the carry and the workspace at this chunk and head; dO of the chunk's first token
+  int64_t vrow;
+  int dk, dv, n, wave, lane;
+  __device__ __forceinline__ void load(GradientSlab<DK>& to, int v0) const {
+    constexpr int PIECES = 4 * 32 * DK * 2 / 1024;
+    int row, block;
+#pragma unroll
+    for (int i = 0; i < PIECES / 8; ++i) {
+      const int piece = i * 8 + wave, part = piece / (PIECES / 4);
+      lds_place<DK>(piece % (PIECES / 4) * 64 + lane, row, block);
+      const uint8_t* p = left[part >> 1] + (int64_t((part & 1) * dv + v0 + row) * dk + block * 8) * 2;
+      to_lds(v0 + row < dv && block * 8 < dk ? p : delta_zeros, &to.states[0][0] + piece * 1024);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int piece = i * 8 + wave, part = piece / 4;
+      lds_place<64>(piece % 4 * 64 + lane, row, block);
+      const uint8_t* p = left[part >> 1] + (int64_t(2 * dv) * dk + int64_t((part & 1) * dv + v0 + row) * 64 + block * 8) * 2;
+      to_lds(v0 + row < dv ? p : delta_zeros, &to.tokens[0][0] + piece * 1024);
+    }
+    if (wave < 4) {
+      row = (wave * 64 + lane) / 4;
+      block = (slab_block(row, lane & 3) >> 4) & 3;
+      const uint8_t* p = d + row * vrow + (v0 + block * 8) * 2;
+      to_lds(row < n && v0 + block * 8 < dv ? p : delta_zeros, to.d + wave * 1024);
+    }
+  }
+};
+
+template <int DK>
+__global__ __launch_bounds__(512, 2) void delta_gradient_kernel(DeltaLaunch L, int64_t left_at) {
+  constexpr int BLOCKS = DK / 8, KB = DK / 32, TILES = DK / 32;  // tiles of a wave
+  constexpr int MAT = 64 * DK * 2;
+  static_assert(sizeof(GradientSlab<DK>) >= 4 * 8192, "the triangles take a slab's place");
+  __shared__ __attribute__((aligned(1024))) GradientSlab<DK> slabs[2];
+  __shared__ __attribute__((aligned(1024))) uint8_t ks[MAT], qs[MAT];
+  __shared__ float rest[64], gamma[64], tail[64], beta[64], below[2][4][64], row_in[2][64], row_out[2][64], pair_sum[2][64];
+  __shared__ float dots[8];
   __shared__ int whole[64];
+  uint8_t* pairs = reinterpret_cast<uint8_t*>(&slabs[1]);
   const int64_t slot = blockIdx.x / L.G;
   const int kh = blockIdx.x % L.G, share = L.H / L.G;
   int64_t first;
   const int n = delta_slot_tokens(L, slot, first);
   if (n == 0) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+  const int it = wave >> 1, half = wave & 1;
   const int64_t krow = int64_t(L.G) * L.dk, vrow = int64_t(L.H) * L.dv;
   const uint8_t* space = static_cast<const uint8_t*>(L.workspace);
+  GradientLoader<DK> loader;
+  loader.vrow = vrow * 2;
+  loader.dk = L.dk;
+  loader.dv = L.dv;
+  loader.n = n;
+  loader.wave = wave;
+  loader.lane = lane;
+  auto set_head = [&](int h) {
+    const int64_t chunk = slot * L.H + h;
+    loader.left[0] = static_cast<const uint8_t*>(L.carry) + chunk * delta_left_bytes(L);
+    loader.left[1] = space + left_at + chunk * delta_left_bytes(L);
+    loader.d = static_cast<const uint8_t*>(L.dout) + (first * vrow + int64_t(h) * L.dv) * 2;
+  };
+  set_head(kh * share);
+  loader.load(slabs[0], 0);
   {
-    const bf16* kp = static_cast<const bf16*>(L.k) + int64_t(kh) * L.dk;
-    const bf16* qp = static_cast<const bf16*>(L.q) + int64_t(kh) * L.dk;
+    const uint8_t* kp = static_cast<const uint8_t*>(L.k) + (first * krow + int64_t(kh) * L.dk) * 2;
+    const uint8_t* qp = static_cast<const uint8_t*>(L.q) + (first * krow + int64_t(kh) * L.dk) * 2;
 #pragma unroll
-    for (int i = 0; i < LOADS; ++i) {
-      const int p = i * 256 + threadIdx.x, row = p / BLOCKS, block = p % BLOCKS, to = lds_block<DK>(row, block);
+    for (int i = 0; i < MAT / 8192; ++i) {
+      int row, block;
+      lds_place<DK>((i * 8 + wave) * 64 + lane, row, block);
+      const int64_t at = (row * krow + block * 8) * 2;
       const bool keep = row < n && block * 8 < L.dk;
-      const int64_t at = (first + min(row, n - 1)) * krow + min(block * 8, L.dk - 8);
-      *reinterpret_cast<u32x4*>(ks + to) = only_if(keep, *reinterpret_cast<const u32x4*>(kp + at));
-      *reinterpret_cast<u32x4*>(qs + to) = only_if(keep, *reinterpret_cast<const u32x4*>(qp + at));
+      to_lds(keep ? kp + at : delta_zeros, ks + (i * 8 + wave) * 1024);
+      to_lds(keep ? qp + at : delta_zeros, qs + (i * 8 + wave) * 1024);
     }
   }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
-  // q.k and k.k of the wave's rows with the tokens up to them: exact products
-  f32x4 qk[4] = {}, kk[4] = {};
+  // q.k (or k.k) of the wave's rows with the tokens up to them: exact products
+  f32x4 xk[4] = {};
 #pragma unroll
   for (int j = 0; j < KB; ++j) {
-    const int at = lds_block<DK>(wave * 16 + c, j * 4 + g);
-    const bf16x8 qr = lds_frag(qs + at), kr = lds_frag(ks + at);
+    const bf16x8 row8 = lds_frag((half ? ks : qs) + lds_block<DK>(it * 16 + c, j * 4 + g));
 #pragma unroll
-    for (int jt = 0; jt < 4; ++jt) {
-      if (jt > wave) break;
-      const bf16x8 kc = lds_frag(ks + lds_block<DK>(jt * 16 + c, j * 4 + g));
-      qk[jt] = mfma16(qr, kc, qk[jt]);
-      kk[jt] = mfma16(kr, kc, kk[jt]);
-    }
+    for (int jt = 0; jt < 4; ++jt)
+      if (jt <= it) xk[jt] = mfma16(row8, lds_frag(ks + lds_block<DK>(jt * 16 + c, j * 4 + g)), xk[jt]);
   }
-  // the first operand's row of this lane, and a row of it out of memory
-  const int token = wave * 16 + c;
-  const bool here = token < n;
-  const int64_t at_row = (first + (here ? token : 0)) * vrow;
-  const bf16* dop = static_cast<const bf16*>(L.dout) + at_row;
-  bf16* dvp = static_cast<bf16*>(L.dv_out) + at_row;
+  const int token = it * 16 + c;
   // 4 x 16 (row, column) blocks of a transposing read
-  const int tr_row = g * 8 + (c >> 2), tr_half = (c & 1) * 8;
+  const int tr_row = g * 8 + (c >> 2), tr_half = (c & 1) * 8, tr_block = (c & 3) >> 1;
+  const int col0 = half * TILES * 16;  // of the wave's columns
 
   f32x4 dq[TILES] = {}, dk[TILES] = {};
   for (int hs = 0; hs < share; ++hs) {
     const int h = kh * share + hs;
-    const int64_t chunk = slot * L.H + h;
     if (threadIdx.x < 64) {
-      const float* sc = reinterpret_cast<const float*>(space + chunk * DELTA_CHUNK_BYTES + DELTA_SCALARS) + lane;
+      const float* sc = reinterpret_cast<const float*>(space + (slot * L.H + h) * DELTA_CHUNK_BYTES + DELTA_SCALARS) + lane;
       gamma[lane] = sc[ROW_C * 64];
       tail[lane] = sc[ROW_TAIL * 64];
       beta[lane] = sc[ROW_BETA * 64];
       whole[lane] = reinterpret_cast<const int*>(sc)[ROW_WHOLE * 64];
       rest[lane] = sc[ROW_REST * 64];
     }
-    const bf16* states = reinterpret_cast<const bf16*>(static_cast<const uint8_t*>(L.carry) + chunk * delta_left_bytes(L));
-    const bf16* dstates = reinterpret_cast<const bf16*>(space + left_at + chunk * delta_left_bytes(L));
     f32x4 ds[TILES] = {}, xs[TILES] = {}, ud[TILES] = {};  // dO S, z S, w dS'
-    f32x4 dm[4] = {}, da[4] = {};
+    f32x4 pair[4] = {};                                    // dO w^T or z w^T
     float db = 0.0f, dot = 0.0f;
+    bf16* dvp = static_cast<bf16*>(L.dv_out) + (first + token) * vrow + int64_t(h) * L.dv + g * 8;
     __syncthreads();
     const float bt = beta[token];
-    for (int v0 = 0; v0 < L.dv; v0 += 32) {
-      // parts: S hi, S lo, dS' hi, dS' lo
-#pragma unroll
-      for (int i = 0; i < SLAB_LOADS; ++i) {
-        const int p = i * 256 + threadIdx.x, part = p / (32 * BLOCKS), row = p / BLOCKS % 32, block = p % BLOCKS;
-        const bool keep = v0 + row < L.dv && block * 8 < L.dk;
-        const u32x4 x = *reinterpret_cast<const u32x4*>((part < 2 ? states : dstates) +
-                                                        (int64_t(part & 1) * L.dv + min(v0 + row, L.dv - 1)) * L.dk +
-                                                        min(block * 8, L.dk - 8));
-        *reinterpret_cast<u32x4*>(slab + part * SLAB + lds_block<DK>(row, block)) = only_if(keep, x);
-      }
-      // w hi, w lo, z hi, z lo: 32 rows of 64 tokens each
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = threadIdx.x / 8, block = threadIdx.x % 8;
-        const u32x4 x = *reinterpret_cast<const u32x4*>((i < 2 ? states : dstates) + 2 * int64_t(L.dv) * L.dk +
-                                                        (int64_t(i & 1) * L.dv + min(v0 + row, L.dv - 1)) * 64 + block * 8);
-        *reinterpret_cast<u32x4*>(wz + i * 4096 + lds_block<64>(row, block)) = only_if(v0 + row < L.dv, x);
-      }
-      const bool keep = here && v0 + g * 8 < L.dv;
-      const int64_t at = int64_t(h) * L.dv + min(v0 + g * 8, L.dv - 8);
-      const bf16x8 o8 = __builtin_bit_cast(bf16x8, only_if(keep, *reinterpret_cast<const u32x4*>(dop + at)));
-      __syncthreads();
-      // the wave's tokens of w and z, in parts: rows of the first operand
-      auto tokens16 = [&](const uint8_t* part, int tile) {
-        const int block = tile * 2 + ((c & 3) >> 1);
-        return lds_transposed(part + lds_block<64>(tr_row, block) + tr_half, part + lds_block<64>(tr_row + 4, block) + tr_half);
+    for (int v0 = 0, turn = 0; v0 < L.dv; v0 += 32, turn ^= 1) {
+      const GradientSlab<DK>& slab = slabs[turn];
+      if (v0 + 32 < L.dv) loader.load(slabs[turn ^ 1], v0 + 32);
+      auto tokens16 = [&](int part, int tile) {
+        const int block = tile * 2 + tr_block;
+        const uint8_t* p = slab.tokens[part] + tr_half;
+        return lds_transposed(p + lds_block<64>(tr_row, block), p + lds_block<64>(tr_row + 4, block));
       };
-      const bf16x8 wh = tokens16(wz, wave), wl = tokens16(wz + 4096, wave);
-      const bf16x8 zh = tokens16(wz + 8192, wave), zl = tokens16(wz + 12288, wave);
-      bf16x8 dv8;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float z = float(zh[e]) + float(zl[e]);
-        db = fmaf(float(wh[e]) + float(wl[e]), z, db);
-        dv8[e] = bf16(bt * z);
-      }
-      if (keep) *reinterpret_cast<bf16x8*>(dvp + at) = dv8;
+      const bf16x8 wh = tokens16(0, it), wl = tokens16(1, it), zh = tokens16(2, it), zl = tokens16(3, it);
+      const bf16x8 o8 = lds_frag(slab.d + slab_block(token, g));
 #pragma unroll
       for (int t = 0; t < TILES; ++t) {
-        const int block = t * 2 + ((c & 3) >> 1);
+        const int block = (half * TILES + t) * 2 + tr_block;
         const int a = lds_block<DK>(tr_row, block) + tr_half, b = lds_block<DK>(tr_row + 4, block) + tr_half;
-        const bf16x8 sh = lds_transposed(slab + a, slab + b), sl = lds_transposed(slab + SLAB + a, slab + SLAB + b);
-        const bf16x8 dh = lds_transposed(slab + 2 * SLAB + a, slab + 2 * SLAB + b);
-        const bf16x8 dl = lds_transposed(slab + 3 * SLAB + a, slab + 3 * SLAB + b);
-        ds[t] = mfma_exact_split(o8, sh, sl, ds[t]);
-        xs[t] = mfma_split_split(zh, zl, sh, sl, xs[t]);
-        ud[t] = mfma_split_split(wh, wl, dh, dl, ud[t]);
+        const bf16x8 sh = lds_transposed(slab.states[0] + a, slab.states[0] + b);
+        const bf16x8 sl = lds_transposed(slab.states[1] + a, slab.states[1] + b);
+        ds[t] = mfma16(sh, o8, mfma16(sl, o8, ds[t]));
+        xs[t] = mfma_split_split(sh, sl, zh, zl, xs[t]);
+        const bf16x8 dh = lds_transposed(slab.states[2] + a, slab.states[2] + b);
+        const bf16x8 dl = lds_transposed(slab.states[3] + a, slab.states[3] + b);
+        ud[t] = mfma_split_split(dh, dl, wh, wl, ud[t]);
       }
 #pragma unroll
       for (int jt = 0; jt < 4; ++jt) {
-        if (jt > wave) break;
-        const bf16x8 h8 = tokens16(wz, jt), l8 = tokens16(wz + 4096, jt);
-        dm[jt] = mfma_exact_split(o8, h8, l8, dm[jt]);
-        da[jt] = mfma_split_split(zh, zl, h8, l8, da[jt]);
+        if (jt > it) continue;
+        const bf16x8 h8 = tokens16(0, jt), l8 = tokens16(1, jt);
+        if (half)
+          pair[jt] = mfma_split_split(zh, zl, h8, l8, pair[jt]);
+        else
+          pair[jt] = mfma_exact_split(o8, h8, l8, pair[jt]);
+      }
+      bf16x8 dv8;
+      if (half) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float z = float(zh[e]) + float(zl[e]);
+          db = fmaf(float(wh[e]) + float(wl[e]), z, db);
+          dv8[e] = bf16(bt * z);
+        }
       }
       // <S, dS'> of the slab's 32 rows
-#pragma unroll
-      for (int i = 0; i < 32 * BLOCKS / 256; ++i) {
-        const int p = (i * 256 + threadIdx.x) * 16;
-        const bf16x8 sh = lds_frag(slab + p), sl = lds_frag(slab + SLAB + p);
-        const bf16x8 dh = lds_frag(slab + 2 * SLAB + p), dl = lds_frag(slab + 3 * SLAB + p);
+      if (threadIdx.x < 32 * BLOCKS) {
+        const int p = threadIdx.x * 16;
+        const bf16x8 sh = lds_frag(slab.states[0] + p), sl = lds_frag(slab.states[1] + p);
+        const bf16x8 dh = lds_frag(slab.states[2] + p), dl = lds_frag(slab.states[3] + p);
 #pragma unroll
         for (int e = 0; e < 8; ++e) dot = fmaf(float(sh[e]) + float(sl[e]), float(dh[e]) + float(dl[e]), dot);
       }
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       __syncthreads();
+      if (half && token < n && v0 + g * 8 < L.dv) *reinterpret_cast<bf16x8*>(dvp + v0) = dv8;
     }
-    db = xor32_sum(xor16_sum(db));
-    if (here && g == 0) L.dbeta[(first + token) * L.H + h] = db;
+    if (hs + 1 < share) {
+      set_head(h + 1);
+      loader.load(slabs[0], 0);
+    }
+    if (half) {
+      db = xor32_sum(xor16_sum(db));
+      if (token < n && g == 0) L.dbeta[(first + token) * L.H + h] = db;
+    }
     dot = wave_allreduce_sum(dot);
     if (lane == 0) dots[wave] = dot;
 
     // The triangles times rho, in two parts, by columns: row j of `pairs` holds
     // the 64 tokens i.  And what passes each token (sums from the last row up).
     f32x4 passing[4] = {};
+    uint8_t* triangle = pairs + half * 16384;
 #pragma unroll
     for (int jt = 0; jt < 4; ++jt) {
-      if (jt > (wave | 1)) break;
+      if (jt > (it | 1)) continue;
       const int j = jt * 16 + c;
-      float m4[4], a4[4];
+      float x4[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int i = wave * 16 + g * 4 + e;
-        const float rho = j <= i ? exp2_difference(rest[i], whole[i], rest[j], whole[j]) : 0.0f;
-        m4[e] = rho * beta[j] * dm[jt][e];
-        a4[e] = j < i ? -rho * beta[j] * beta[i] * da[jt][e] : 0.0f;
-        passing[jt][e] = j <= i ? m4[e] * qk[jt][e] + a4[e] * kk[jt][e] : 0.0f;
+        const int i = it * 16 + g * 4 + e;
+        float rho = j <= i ? exp2_difference(rest[i], whole[i], rest[j], whole[j]) * beta[j] : 0.0f;
+        if (half) rho = j < i ? -rho * beta[i] : 0.0f;
+        x4[e] = rho * pair[jt][e];
+        passing[jt][e] = x4[e] * xk[jt][e];
       }
-      const int to = lds_block<64>(j, wave * 2 + (g >> 1)) + (g & 1) * 8;
+      const int to = lds_block<64>(j, it * 2 + (g >> 1)) + (g & 1) * 8;
       bf16x4 hi, lo;
-      split2(m4, hi, lo);
-      *reinterpret_cast<bf16x4*>(pairs + to) = hi;
-      *reinterpret_cast<bf16x4*>(pairs + 8192 + to) = lo;
-      split2(a4, hi, lo);
-      *reinterpret_cast<bf16x4*>(pairs + 16384 + to) = hi;
-      *reinterpret_cast<bf16x4*>(pairs + 24576 + to) = lo;
+      split2(x4, hi, lo);
+      *reinterpret_cast<bf16x4*>(triangle + to) = hi;
+      *reinterpret_cast<bf16x4*>(triangle + 8192 + to) = lo;
       // sums over the rows from e on, then with those of the lane groups below
 #pragma unroll
       for (int e = 2; e >= 0; --e) passing[jt][e] += passing[jt][e + 1];
@@ -329,112 +371,114 @@ __global__ __launch_bounds__(256, 1) void delta_gradient_kernel(DeltaLaunch L, i
       const float behind = (g < 3 ? up1 : 0.0f) + (g < 2 ? up2 : 0.0f) + (g < 1 ? up3 : 0.0f);
 #pragma unroll
       for (int e = 0; e < 4; ++e) passing[jt][e] += behind;
-      if (g == 0) below[wave][j] = passing[jt][0];
+      if (g == 0) below[half][it][j] = passing[jt][0];
     }
     __syncthreads();
     {
       f32x4 sum = {0, 0, 0, 0};
 #pragma unroll
       for (int jt = 0; jt < 4; ++jt) {
-        if (jt > wave) break;
+        if (jt > it) continue;
         float later = 0.0f;
-        for (int it = wave + 1; it < 4; ++it) later += below[it][jt * 16 + c];
+        for (int i = it + 1; i < 4; ++i) later += below[half][i][jt * 16 + c];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (jt * 16 + c < wave * 16 + g * 4 + e) sum[e] += passing[jt][e] + later;
+          if (jt * 16 + c < it * 16 + g * 4 + e) sum[e] += passing[jt][e] + later;
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         sum[e] = group_sum<16>(sum[e]);
-        if (c == 0) pair_sum[wave * 16 + g * 4 + e] = sum[e];
+        if (c == 0) pair_sum[half][it * 16 + g * 4 + e] = sum[e];
       }
+    }
+    // what the state gives, and its share of the decays' gradient
+    {
+      const float gm = gamma[token], gb = gm * bt, tb = tail[token] * bt;
+      float in = 0.0f, out = 0.0f;
+#pragma unroll
+      for (int t = 0; t < TILES; ++t) {
+        const int at = lds_block<DK>(token, (col0 >> 3) + t * 2 + (g >> 1)) + (g & 1) * 8;
+        const bf16x4 q = *reinterpret_cast<const bf16x4*>(qs + at), k = *reinterpret_cast<const bf16x4*>(ks + at);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float a = gm * ds[t][e], x = gb * xs[t][e], u = tb * ud[t][e];
+          in = fmaf(float(q[e]), a, fmaf(-float(k[e]), x, in));
+          out = fmaf(float(k[e]), u, out);
+          dq[t][e] += a;
+          dk[t][e] += u - x;
+        }
+      }
+      in = xor32_sum(xor16_sum(in));
+      out = xor32_sum(xor16_sum(out));
+      if (g == 0) row_in[half][token] = in, row_out[half][token] = out;
     }
     // dM K, dAt K (rows i), dM^T Q, dAt^T K (rows j)
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
-      if (kb <= wave / 2) {  // j up to the wave's rows
-        const int block = wave * 2 + ((c & 3) >> 1);
+      bf16x8 k8[TILES], q8[TILES];
+#pragma unroll
+      for (int t = 0; t < TILES; ++t) {
+        const int block = (half * TILES + t) * 2 + tr_block;
+        const int ka = lds_block<DK>(kb * 32 + tr_row, block) + tr_half, kb4 = lds_block<DK>(kb * 32 + tr_row + 4, block) + tr_half;
+        k8[t] = lds_transposed(ks + ka, ks + kb4);
+        q8[t] = lds_transposed(qs + ka, qs + kb4);
+      }
+      if (kb <= it / 2) {  // j up to the wave's rows
+        const int block = it * 2 + tr_block;
         const int a = lds_block<64>(kb * 32 + tr_row, block) + tr_half, b = lds_block<64>(kb * 32 + tr_row + 4, block) + tr_half;
         const bf16x8 mh = lds_transposed(pairs + a, pairs + b), ml = lds_transposed(pairs + 8192 + a, pairs + 8192 + b);
         const bf16x8 ah = lds_transposed(pairs + 16384 + a, pairs + 16384 + b);
         const bf16x8 al = lds_transposed(pairs + 24576 + a, pairs + 24576 + b);
 #pragma unroll
         for (int t = 0; t < TILES; ++t) {
-          const int block = t * 2 + ((c & 3) >> 1);
-          const int ka = lds_block<DK>(kb * 32 + tr_row, block) + tr_half, kb4 = lds_block<DK>(kb * 32 + tr_row + 4, block) + tr_half;
-          const bf16x8 k8 = lds_transposed(ks + ka, ks + kb4);
-          dq[t] = mfma16(mh, k8, mfma16(ml, k8, dq[t]));
-          dk[t] = mfma16(ah, k8, mfma16(al, k8, dk[t]));
+          dq[t] = mfma_exact_split(k8[t], mh, ml, dq[t]);
+          dk[t] = mfma_exact_split(k8[t], ah, al, dk[t]);
         }
       }
-      if (kb >= wave / 2) {  // i from the wave's rows on
-        const int at = lds_block<64>(wave * 16 + c, kb * 4 + g);
+      if (kb >= it / 2) {  // i from the wave's rows on
+        const int at = lds_block<64>(token, kb * 4 + g);
         const bf16x8 mh = lds_frag(pairs + at), ml = lds_frag(pairs + 8192 + at);
         const bf16x8 ah = lds_frag(pairs + 16384 + at), al = lds_frag(pairs + 24576 + at);
 #pragma unroll
         for (int t = 0; t < TILES; ++t) {
-          const int block = t * 2 + ((c & 3) >> 1);
-          const int ka = lds_block<DK>(kb * 32 + tr_row, block) + tr_half, kb4 = lds_block<DK>(kb * 32 + tr_row + 4, block) + tr_half;
-          const bf16x8 q8 = lds_transposed(qs + ka, qs + kb4), k8 = lds_transposed(ks + ka, ks + kb4);
-          dk[t] = mfma16(mh, q8, mfma16(ml, q8, dk[t]));
-          dk[t] = mfma16(ah, k8, mfma16(al, k8, dk[t]));
+          dk[t] = mfma_exact_split(q8[t], mh, ml, dk[t]);
+          dk[t] = mfma_exact_split(k8[t], ah, al, dk[t]);
         }
       }
     }
-    // what the state gives, and its share of the decays' gradient
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int row = wave * 16 + g * 4 + e;
-      const float gm = gamma[row], gb = gm * beta[row], tb = tail[row] * beta[row];
-      float in = 0.0f, out = 0.0f;
-#pragma unroll
-      for (int t = 0; t < TILES; ++t) {
-        const int at = lds_block<DK>(row, t * 2 + (c >> 3)) + (c & 7) * 2;
-        const float q = float(*reinterpret_cast<const bf16*>(qs + at)), k = float(*reinterpret_cast<const bf16*>(ks + at));
-        const float a = gm * ds[t][e], x = gb * xs[t][e], u = tb * ud[t][e];
-        in = fmaf(q, a, fmaf(-k, x, in));
-        out = fmaf(k, u, out);
-        dq[t][e] += a;
-        dk[t][e] += u - x;
-      }
-      in = group_sum<16>(in);
-      out = group_sum<16>(out);
-      if (c == 0) row_in[row] = in, row_out[row] = out;
-    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     if (wave == 0) {
       // sums over i >= t, and over j < t (not of all up to t less the token's own:
       // its own is far larger where the token forgets much)
-      float in = row_in[63 - lane], out = lane ? row_out[lane - 1] : 0.0f;
+      float in = row_in[0][63 - lane] + row_in[1][63 - lane], out = lane ? row_out[0][lane - 1] + row_out[1][lane - 1] : 0.0f;
 #pragma unroll
       for (int d = 1; d < 64; d *= 2) {
         const float a = __shfl_up(in, d), b = __shfl_up(out, d);
         if (lane >= d) in += a, out += b;
       }
       in = __shfl(in, 63 - lane);
-      float da_t = pair_sum[lane] + in + out + gamma[63] * (dots[0] + dots[1] + dots[2] + dots[3]);
+      float all = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) all += dots[i];
+      float da_t = pair_sum[0][lane] + pair_sum[1][lane] + in + out + gamma[63] * all;
       if (lane < n) {
         const int64_t at = (first + lane) * L.H + h;
-        if (!L.log_decay) {
-          const float a = L.alpha[at];
-          da_t /= fmaxf(a, 5.42101086e-20f);  // the least decay, 2^-64
-        }
+        if (!L.log_decay) da_t /= fmaxf(L.alpha[at], 5.42101086e-20f);  // the least decay, 2^-64
         L.dalpha[at] = da_t;
       }
     }
     __syncthreads();
   }
-  bf16* dqp = static_cast<bf16*>(L.dq) + int64_t(kh) * L.dk;
-  bf16* dkp = static_cast<bf16*>(L.dk_out) + int64_t(kh) * L.dk;
+  if (token >= n) return;
+  bf16* dqp = static_cast<bf16*>(L.dq) + (first + token) * krow + int64_t(kh) * L.dk;
+  bf16* dkp = static_cast<bf16*>(L.dk_out) + (first + token) * krow + int64_t(kh) * L.dk;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const int row = wave * 16 + g * 4 + e;
-    if (row >= n) continue;
-#pragma unroll
-    for (int t = 0; t < TILES; ++t) {
-      if (t * 16 + c >= L.dk) continue;
-      store_f32(dqp + (first + row) * krow + t * 16 + c, dq[t][e]);
-      store_f32(dkp + (first + row) * krow + t * 16 + c, dk[t][e]);
+  for (int t = 0; t < TILES; ++t) {
+    const int at = col0 + t * 16 + g * 4;
+    if (at < L.dk) {
+      *reinterpret_cast<bf16x4*>(dqp + at) = __builtin_convertvector(dq[t], bf16x4);
+      *reinterpret_cast<bf16x4*>(dkp + at) = __builtin_convertvector(dk[t], bf16x4);
     }
   }
 }
@@ -450,7 +494,7 @@ hipError_t backward(const DeltaLaunch& L, hipStream_t stream) {
   const int groups = (L.dv + 63) / 64;
   delta_chain_back_kernel<DK><<<uint32_t(groups) * uint32_t(L.H) * uint32_t(L.B), 256, 0, stream>>>(L, groups, left_at);
   if (hipError_t e = hipGetLastError()) return e;
-  if (slots > 0) delta_gradient_kernel<DK><<<uint32_t(slots * L.G), 256, 0, stream>>>(L, left_at);
+  if (slots > 0) delta_gradient_kernel<DK><<<uint32_t(slots * L.G), 512, 0, stream>>>(L, left_at);
   return hipGetLastError();
 }
 

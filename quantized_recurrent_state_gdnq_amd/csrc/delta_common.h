@@ -23,6 +23,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "device_common.h"
 #include "launch.h"
 #include "mfma.h"
@@ -53,6 +55,16 @@ __host__ __device__ inline int64_t delta_state_bytes(const DeltaLaunch& L) { ret
 __host__ __device__ inline int64_t delta_left_bytes(const DeltaLaunch& L) { return int64_t(L.dv) * (L.dk * 4 + DELTA_CHUNK * 4); }
 
 #ifdef __HIPCC__
+
+template <int V>
+using Int = std::integral_constant<int, V>;
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void each(F&& f) {
+  if constexpr (I < N) {
+    f(Int<I>{});
+    each<N, I + 1>(static_cast<F&&>(f));
+  }
+}
 
 struct DeltaSpan {
   int64_t first, slot;  // first token in the call, first chunk slot
@@ -228,41 +240,94 @@ struct ChainLoader {
     }
   }
 
-  // n tokens from `first` on, chunk slot `slot`.  Rows behind the last token are
-  // the last one's again (beta = 0 there), or zeros where ZERO_V.
-  template <bool ZERO_V>
-  __device__ __forceinline__ void load(ChainBuffer<DK>& to, int64_t first, int n, int64_t slot) const {
-    const uint8_t* ws = space + slot * chunk_stride;
-    const uint8_t *kf = k + first * krow, *qf = q + first * krow, *vf = v + first * vrow;
+  // The next chunk to load: n tokens from `first` on, chunk slot `slot`.
+  struct Next {
+    const uint8_t *ws, *k, *q, *v;
+    int n;
+    bool whole;
+  };
+  __device__ __forceinline__ Next next(int64_t first, int n, int64_t slot) const {
+    return {space + slot * chunk_stride, k + first * krow, q + first * krow, v + first * vrow, n, exact && n == 64};
+  }
+
+  // A whole chunk's loads are made in STEPS parts of one or two, between the
+  // products of the chunk before: all at once they hold the wave up until the
+  // queue has room (2600 of a chunk's 8100 cycles).
+  static constexpr int STEPS = LOADS + 5;
+  template <int STEP>
+  __device__ __forceinline__ void step(ChainBuffer<DK>& to, const Next& x) const {
+    if constexpr (STEP < LOADS) {
+      to_lds(x.k, at_k[STEP], to.k + (STEP * 4 + wave) * 1024);
+      to_lds(x.q, at_k[STEP], to.q + (STEP * 4 + wave) * 1024);
+    } else if constexpr (STEP == LOADS) {
 #pragma unroll
-    for (int i = 0; i < 6; ++i) to_lds(ws, (i * 4 + wave) * 1024 + lane * 16, to.tri + (i * 4 + wave) * 1024);
-    if (wave == 0) to_lds(ws + DELTA_SCALARS, lane * 16, to.rows);
-    if (exact && n == 64) {
+      for (int i = 0; i < 2; ++i) to_lds(x.v, at_v[i], to.v + (i * 4 + wave) * 1024);
+    } else if constexpr (STEP < LOADS + 4) {
 #pragma unroll
-      for (int i = 0; i < LOADS; ++i) {
-        to_lds(kf, at_k[i], to.k + (i * 4 + wave) * 1024);
-        to_lds(qf, at_k[i], to.q + (i * 4 + wave) * 1024);
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) to_lds(vf, at_v[i], to.v + (i * 4 + wave) * 1024);
-      return;
+      for (int i = (STEP - LOADS - 1) * 2; i < (STEP - LOADS) * 2; ++i)
+        to_lds(x.ws, (i * 4 + wave) * 1024 + lane * 16, to.tri + (i * 4 + wave) * 1024);
+    } else {
+      if (wave == 0) to_lds(x.ws + DELTA_SCALARS, lane * 16, to.rows);
     }
+  }
+
+  // Any chunk at once.  Rows behind the last token are the last one's again (beta
+  // is 0 there), or zeros where ZERO_V; columns behind the last are zero.
+  template <bool ZERO_V>
+  __device__ __forceinline__ void load(ChainBuffer<DK>& to, const Next& x) const {
+    step<LOADS + 1>(to, x);
+    step<LOADS + 2>(to, x);
+    step<LOADS + 3>(to, x);
+    step<LOADS + 4>(to, x);
     int row, block;
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
       lds_place<DK>((i * 4 + wave) * 64 + lane, row, block);
-      const int64_t at = min(row, n - 1) * krow + block * 16;
-      to_lds(block * 8 < dk ? kf + at : delta_zeros, to.k + (i * 4 + wave) * 1024);
-      to_lds(block * 8 < dk ? qf + at : delta_zeros, to.q + (i * 4 + wave) * 1024);
+      const int64_t at = min(row, x.n - 1) * krow + block * 16;
+      to_lds(block * 8 < dk ? x.k + at : delta_zeros, to.k + (i * 4 + wave) * 1024);
+      to_lds(block * 8 < dk ? x.q + at : delta_zeros, to.q + (i * 4 + wave) * 1024);
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       lds_place<64>((i * 4 + wave) * 64 + lane, row, block);
-      const uint8_t* p = vf + min(row, n - 1) * vrow + min(block * 8, cols - 8) * 2;
-      to_lds(ZERO_V && row >= n ? delta_zeros : p, to.v + (i * 4 + wave) * 1024);
+      const uint8_t* p = x.v + min(row, x.n - 1) * vrow + min(block * 8, cols - 8) * 2;
+      to_lds(ZERO_V && row >= x.n ? delta_zeros : p, to.v + (i * 4 + wave) * 1024);
     }
   }
 };
+
+// What the chains read of K or Q: rows of 16 tokens in chain order with their
+// columns (the first operand, or the second, of a product over d_k), and 16
+// columns in chain order with their tokens (of one over the tokens).  All of a
+// phase's operands are read ahead of it, and kept there (the sched_barriers):
+// left to the compiler each was read just before its product, and waited for.
+template <int DK>
+__device__ __forceinline__ void chain_rows(const uint8_t* m, int lane, bf16x8 (&f)[4][DK / 32]) {
+#pragma unroll
+  for (int j = 0; j < DK / 32; ++j)
+#pragma unroll
+    for (int it = 0; it < 4; ++it) f[it][j] = lds_frag(m + lds_block<DK>(chain_row(it, lane & 15), j * 4 + (lane >> 4)));
+}
+template <int DK>
+__device__ __forceinline__ void chain_columns(const uint8_t* m, int lane, bf16x8 (&f)[DK / 16][2]) {
+  const int c = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int t = 0; t < DK / 16; ++t) {
+      const int row = j * 32 + g * 8 + (c >> 2), block = (t >> 1) * 4 + (c & 3), half = (t & 1) * 8;
+      f[t][j] = lds_transposed(m + lds_block<DK>(row, block) + half, m + lds_block<DK>(row + 4, block) + half);
+    }
+}
+// The six blocks of a triangle, hi and lo.
+__device__ __forceinline__ void chain_triangle(const uint8_t* tri, int lane, bf16x8 (&h)[TRI_BLOCKS], bf16x8 (&l)[TRI_BLOCKS]) {
+#pragma unroll
+  for (int i = 0; i < TRI_BLOCKS; ++i) {
+    h[i] = lds_frag(tri + i * 1024 + lane * 16);
+    l[i] = lds_frag(tri + TRI_PART + i * 1024 + lane * 16);
+  }
+}
+__device__ __forceinline__ void phase() { __builtin_amdgcn_sched_barrier(0); }
 
 // Four tokens of tile it of a lane's column, out of the 64 columns in LDS.
 __device__ __forceinline__ s16x4 chain_column(const uint8_t* v, int it, int wave, int lane) {

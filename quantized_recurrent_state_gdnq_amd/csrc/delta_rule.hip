@@ -39,18 +39,27 @@ __global__ __launch_bounds__(256, 1) void delta_chain_kernel(DeltaLaunch L, int 
     S[t] = f32x4{0, 0, 0, 0};
     if (L.h0 && mine && at < L.dk) S[t] = *reinterpret_cast<const f32x4*>(L.h0 + state_row + at);
   }
-  if (chunks > 0) loader.template load<false>(buffers[0], s.first, min(64, s.tokens), s.slot);
+  if (chunks > 0) loader.template load<false>(buffers[0], loader.next(s.first, min(64, s.tokens), s.slot));
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
   for (int chunk = 0; chunk < chunks; ++chunk) {
     const ChainBuffer<DK>& buf = buffers[chunk & 1];
     const int64_t first = s.first + int64_t(chunk) * 64;
     const int n = min(64, s.tokens - chunk * 64);
-    if (chunk + 1 < chunks)
-      loader.template load<false>(buffers[(chunk + 1) & 1], first + 64, min(64, s.tokens - chunk * 64 - 64), s.slot + chunk + 1);
+    ChainBuffer<DK>& following = buffers[(chunk + 1) & 1];
+    const auto next = loader.next(first + 64, min(64, s.tokens - chunk * 64 - 64), s.slot + chunk + 1);
+    const bool paced = next.n > 0 && next.whole;
+    if (next.n > 0 && !next.whole) loader.template load<false>(following, next);
+    auto ahead = [&](auto step) {
+      phase();
+      if (paced) loader.template step<step.value>(following, next);
+    };
     bf16* left = nullptr;  // this chunk's part of the carry
     if constexpr (SAVE)
       left = reinterpret_cast<bf16*>(static_cast<uint8_t*>(L.carry) + ((s.slot + chunk) * L.H + h) * delta_left_bytes(L));
+    bf16x8 kf[4][KB], qf[4][KB];
+    chain_rows<DK>(buf.k, lane, kf);
+    phase();
     bf16x8 sh[KB], sl[KB];
 #pragma unroll
     for (int j = 0; j < KB; ++j) {
@@ -64,70 +73,99 @@ __global__ __launch_bounds__(256, 1) void delta_chain_kernel(DeltaLaunch L, int 
       }
     }
     const float* rows = reinterpret_cast<const float*>(buf.rows);
+    auto row4 = [&](int which, int it) { return *reinterpret_cast<const f32x4*>(rows + which * 64 + chain_row(it, g * 4)); };
+    phase();
+    chain_rows<DK>(buf.q, lane, qf);
+    s16x4 v[4];
+    f32x4 decay[4];
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      v[it] = chain_column(buf.v, it, wave, lane);
+      decay[it] = row4(ROW_C, it);
+    }
+    phase();
     // x = V - c K S^T by tokens (rows), and O^T = (c Q S^T)^T by tokens in lanes,
     // so that a lane has four adjacent values of a token to store: the operands
     // are the same registers, in the other order.
-    f32x4 x[4], o[4];
+    f32x4 x[4] = {}, o[4] = {};
+    each<KB>([&](auto j) {
 #pragma unroll
-    for (int it = 0; it < 4; ++it) {
-      const int row = chain_row(it, c);
-      x[it] = o[it] = f32x4{0, 0, 0, 0};
+      for (int it = 0; it < 4; ++it) x[it] = mfma16(kf[it][j.value], sl[j.value], x[it]);
 #pragma unroll
-      for (int j = 0; j < KB; ++j) {
-        const int at = lds_block<DK>(row, j * 4 + g);
-        x[it] = mfma_exact_split(lds_frag(buf.k + at), sh[j], sl[j], x[it]);
-        const bf16x8 q8 = lds_frag(buf.q + at);
-        o[it] = mfma16(sh[j], q8, mfma16(sl[j], q8, o[it]));
-      }
-    }
+      for (int it = 0; it < 4; ++it) x[it] = mfma16(kf[it][j.value], sh[j.value], x[it]);
+      ahead(Int<j.value>{});  // the first LOADS = KB steps
+    });
+    phase();
+    bf16x8 nh[TRI_BLOCKS], nl[TRI_BLOCKS];
+    chain_triangle(buf.tri, lane, nh, nl);
+    phase();
+    each<KB>([&](auto j) {
 #pragma unroll
-    for (int it = 0; it < 4; ++it) {
-      const s16x4 v = chain_column(buf.v, it, wave, lane);
-      const f32x4 decay = *reinterpret_cast<const f32x4*>(rows + ROW_C * 64 + chain_row(it, g * 4));
+      for (int it = 0; it < 4; ++it) o[it] = mfma16(sl[j.value], qf[it][j.value], o[it]);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[it][e] = bf16_value(v[e]) - decay[e] * x[it][e];
-      o[it] *= rows[ROW_C * 64 + chain_row(it, c)];
-    }
-    // The six blocks of a triangle: tiles 0 and 1 with the first 32 tokens, 2 and
-    // 3 with both halves.
+      for (int it = 0; it < 4; ++it) o[it] = mfma16(sh[j.value], qf[it][j.value], o[it]);
+      if constexpr (j.value % (KB / 2) == KB / 2 - 1) ahead(Int<KB + (j.value + 1) / (KB / 2) - 1>{});
+    });
+#pragma unroll
+    for (int it = 0; it < 4; ++it)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[it][e] = bf16_value(v[it][e]) - decay[it][e] * x[it][e];
     bf16x8 hi[2], lo[2];
     split8(x[0], x[1], hi[0], lo[0]);
     split8(x[2], x[3], hi[1], lo[1]);
-    f32x4 w[4] = {};
+    ahead(Int<KB + 2>{});
+    phase();
+    bf16x8 kt[TILES][2];
+    chain_columns<DK>(buf.k, lane, kt);
+    f32x4 tail[4];
 #pragma unroll
-    for (int it = 0; it < 4; ++it)
-#pragma unroll
-      for (int j = 0; j <= it / 2; ++j) {
-        const uint8_t* at = buf.tri + (it < 2 ? it : 2 * it - 2 + j) * 1024 + lane * 16;
-        w[it] = mfma_split_split(lds_frag(at), lds_frag(at + TRI_PART), hi[j], lo[j], w[it]);
-      }
-    f32x4 tu[4];
-#pragma unroll
-    for (int it = 0; it < 4; ++it) tu[it] = w[it] * *reinterpret_cast<const f32x4*>(rows + ROW_TAIL_BETA * 64 + chain_row(it, g * 4));
-    bf16x8 th[2], tl[2];
-    split8(tu[0], tu[1], th[0], tl[0]);
-    split8(tu[2], tu[3], th[1], tl[1]);
+    for (int it = 0; it < 4; ++it) tail[it] = row4(ROW_TAIL_BETA, it);
     const float whole = rows[ROW_C * 64 + 63];
+    phase();
+    // The six blocks of a triangle: tiles 0 and 1 with the first 32 tokens, 2 and
+    // 3 with both halves.
+    f32x4 w[4] = {};
+    auto part = [&](const bf16x8 (&n)[TRI_BLOCKS], const bf16x8 (&y)[2]) {
 #pragma unroll
-    for (int t = 0; t < TILES; ++t) {
-      S[t] *= whole;
+      for (int it = 0; it < 4; ++it) w[it] = mfma16(n[it < 2 ? it : 2 * it - 2], y[0], w[it]);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        // tokens 32 j + 8 g + .. of the columns in tile t's order
-        const int row = j * 32 + g * 8 + (c >> 2), block = (t >> 1) * 4 + (c & 3), half = (t & 1) * 8;
-        const bf16x8 a = lds_transposed(buf.k + lds_block<DK>(row, block) + half, buf.k + lds_block<DK>(row + 4, block) + half);
-        S[t] = mfma_exact_split(a, th[j], tl[j], S[t]);
-      }
+      for (int it = 2; it < 4; ++it) w[it] = mfma16(n[2 * it - 1], y[1], w[it]);
+    };
+    part(nl, hi);
+    ahead(Int<KB + 3>{});
+    part(nh, lo);
+    part(nh, hi);
+    ahead(Int<KB + 4>{});
+    bf16x8 th[2], tl[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      split8(w[2 * j] * tail[2 * j], w[2 * j + 1] * tail[2 * j + 1], th[j], tl[j]);
+      split8(w[2 * j], w[2 * j + 1], hi[j], lo[j]);
     }
-    split8(w[0], w[1], hi[0], lo[0]);
-    split8(w[2], w[3], hi[1], lo[1]);
 #pragma unroll
-    for (int it = 0; it < 4; ++it)
+    for (int it = 0; it < 4; ++it) o[it] *= rows[ROW_C * 64 + chain_row(it, c)];
 #pragma unroll
-      for (int j = 0; j <= it / 2; ++j) {
-        const uint8_t* at = buf.tri + TRI_BYTES + (it < 2 ? it : 2 * it - 2 + j) * 1024 + lane * 16;
-        o[it] = mfma_split_split(hi[j], lo[j], lds_frag(at), lds_frag(at + TRI_PART), o[it]);
-      }
+    for (int t = 0; t < TILES; ++t) S[t] *= whole;
+    phase();
+    bf16x8 mh[TRI_BLOCKS], ml[TRI_BLOCKS];
+    chain_triangle(buf.tri + TRI_BYTES, lane, mh, ml);
+    phase();
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+#pragma unroll
+      for (int t = 0; t < TILES; ++t) S[t] = mfma16(kt[t][j], tl[j], S[t]);
+#pragma unroll
+      for (int t = 0; t < TILES; ++t) S[t] = mfma16(kt[t][j], th[j], S[t]);
+    }
+    auto inside = [&](const bf16x8 (&y)[2], const bf16x8 (&m)[TRI_BLOCKS]) {
+#pragma unroll
+      for (int it = 0; it < 4; ++it) o[it] = mfma16(y[0], m[it < 2 ? it : 2 * it - 2], o[it]);
+#pragma unroll
+      for (int it = 2; it < 4; ++it) o[it] = mfma16(y[1], m[2 * it - 1], o[it]);
+    };
+    inside(lo, mh);
+    inside(hi, ml);
+    inside(hi, mh);
     // the next chunk is in LDS, and nobody reads this one any more; the stores
     // below are behind this wait, so that the next chunk's covers them
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");

@@ -38,15 +38,25 @@ __global__ __launch_bounds__(256, 1) void delta_chain_back_kernel(DeltaLaunch L,
     if (L.dh_last && mine && at < L.dk) S[t] = *reinterpret_cast<const f32x4*>(L.dh_last + state_row + at);
   }
   if (chunks > 0)
-    loader.template load<true>(buffers[0], s.first + int64_t(chunks - 1) * 64, s.tokens - (chunks - 1) * 64, s.slot + chunks - 1);
+    loader.template load<true>(buffers[0], loader.next(s.first + int64_t(chunks - 1) * 64, s.tokens - (chunks - 1) * 64, s.slot + chunks - 1));
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
   for (int done = 0; done < chunks; ++done) {
     const int chunk = chunks - 1 - done;
     const ChainBuffer<DK>& buf = buffers[done & 1];
-    if (chunk > 0) loader.template load<true>(buffers[(done + 1) & 1], s.first + int64_t(chunk - 1) * 64, 64, s.slot + chunk - 1);
+    ChainBuffer<DK>& following = buffers[(done + 1) & 1];
+    const auto next = loader.next(s.first + int64_t(chunk - 1) * 64, 64, s.slot + chunk - 1);
+    const bool paced = chunk > 0 && next.whole;
+    if (chunk > 0 && !next.whole) loader.template load<true>(following, next);
+    auto ahead = [&](auto step) {
+      phase();
+      if (paced) loader.template step<step.value>(following, next);
+    };
     bf16* left = reinterpret_cast<bf16*>(static_cast<uint8_t*>(L.workspace) + left_at +
                                          ((s.slot + chunk) * L.H + h) * delta_left_bytes(L));
+    bf16x8 kf[4][KB];
+    chain_rows<DK>(buf.k, lane, kf);
+    phase();
     bf16x8 sh[KB], sl[KB];
 #pragma unroll
     for (int j = 0; j < KB; ++j) {
@@ -59,67 +69,98 @@ __global__ __launch_bounds__(256, 1) void delta_chain_back_kernel(DeltaLaunch L,
     }
     const float* rows = reinterpret_cast<const float*>(buf.rows);
     auto row4 = [&](int which, int it) { return *reinterpret_cast<const f32x4*>(rows + which * 64 + chain_row(it, g * 4)); };
-    f32x4 u[4];
+    phase();
+    bf16x8 mh[TRI_BLOCKS], ml[TRI_BLOCKS];
+    chain_triangle(buf.tri + TRI_BYTES, lane, mh, ml);
+    s16x4 d4[4];
+    f32x4 tail[4], decay[4], decay_beta[4];
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
-      const int row = chain_row(it, c);
-      u[it] = f32x4{0, 0, 0, 0};
-#pragma unroll
-      for (int j = 0; j < KB; ++j) u[it] = mfma_exact_split(lds_frag(buf.k + lds_block<DK>(row, j * 4 + g)), sh[j], sl[j], u[it]);
-      u[it] *= row4(ROW_TAIL, it);
+      d4[it] = chain_column(buf.v, it, wave, lane);
+      tail[it] = row4(ROW_TAIL, it);
+      decay[it] = row4(ROW_C, it);
+      decay_beta[it] = row4(ROW_C_BETA, it);
     }
+    const float whole = rows[ROW_C * 64 + 63];
+    phase();
+    f32x4 u[4] = {};
+    each<KB>([&](auto j) {
+#pragma unroll
+      for (int it = 0; it < 4; ++it) u[it] = mfma16(kf[it][j.value], sl[j.value], u[it]);
+#pragma unroll
+      for (int it = 0; it < 4; ++it) u[it] = mfma16(kf[it][j.value], sh[j.value], u[it]);
+      ahead(Int<j.value>{});  // the first LOADS = KB steps
+    });
+    phase();
+    bf16x8 nh[TRI_BLOCKS], nl[TRI_BLOCKS], kt[TILES][2];
+    chain_triangle(buf.tri, lane, nh, nl);
+    chain_columns<DK>(buf.q, lane, kt);
+    phase();
     // dO, and c dO in parts
     bf16x8 d[2], dh[2], dl[2], hi[2], lo[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const s16x4 d0 = chain_column(buf.v, 2 * j, wave, lane), d1 = chain_column(buf.v, 2 * j + 1, wave, lane);
+      const s16x4 d0 = d4[2 * j], d1 = d4[2 * j + 1];
       typedef short s16x8 __attribute__((ext_vector_type(8)));
       d[j] = __builtin_bit_cast(bf16x8, s16x8{d0[0], d0[1], d0[2], d0[3], d1[0], d1[1], d1[2], d1[3]});
-      f32x4 a = row4(ROW_C, 2 * j), b4 = row4(ROW_C, 2 * j + 1);
+    }
+#pragma unroll
+    for (int it = 0; it < 4; ++it) u[it] *= tail[it];
+    // transposed triangles: tiles 0 and 1 take both halves of the tokens, 2 and 3 the second
+    auto part = [&](f32x4 (&y)[4], const bf16x8 (&m)[TRI_BLOCKS], const bf16x8 (&x)[2]) {
+#pragma unroll
+      for (int it = 0; it < 4; ++it) y[it] = mfma16(m[it < 2 ? it * 2 + 1 : it + 2], x[1], y[it]);
+#pragma unroll
+      for (int it = 0; it < 2; ++it) y[it] = mfma16(m[it * 2], x[0], y[it]);
+    };
+    part(u, ml, d);
+    ahead(Int<KB>{});
+    part(u, mh, d);
+    ahead(Int<KB + 1>{});
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      f32x4 a, b4;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        a[e] *= bf16_value(d0[e]);
-        b4[e] *= bf16_value(d1[e]);
+        a[e] = decay[2 * j][e] * bf16_value(d4[2 * j][e]);
+        b4[e] = decay[2 * j + 1][e] * bf16_value(d4[2 * j + 1][e]);
       }
       split8(a, b4, dh[j], dl[j]);
     }
-    // transposed triangles: tiles 0 and 1 take both halves of the tokens, 2 and 3 the second
-    auto block_at = [&](int it, int j) { return buf.tri + (it < 2 ? it * 2 + j : it + 2) * 1024 + lane * 16; };
-#pragma unroll
-    for (int it = 0; it < 4; ++it)
-#pragma unroll
-      for (int j = it / 2; j < 2; ++j) {
-        const uint8_t* at = block_at(it, j) + TRI_BYTES;
-        u[it] = mfma16(lds_frag(at), d[j], mfma16(lds_frag(at + TRI_PART), d[j], u[it]));
-      }
     split8(u[0], u[1], hi[0], lo[0]);
     split8(u[2], u[3], hi[1], lo[1]);
     f32x4 z[4] = {};
+    part(z, nl, hi);
+    ahead(Int<KB + 2>{});
+    part(z, nh, lo);
+    ahead(Int<KB + 3>{});
+    part(z, nh, hi);
+    ahead(Int<KB + 4>{});
+    // the part of dS that does not wait for z
 #pragma unroll
-    for (int it = 0; it < 4; ++it)
+    for (int t = 0; t < TILES; ++t) S[t] *= whole;
 #pragma unroll
-      for (int j = it / 2; j < 2; ++j) {
-        const uint8_t* at = block_at(it, j);
-        z[it] = mfma_split_split(lds_frag(at), lds_frag(at + TRI_PART), hi[j], lo[j], z[it]);
-      }
+    for (int j = 0; j < 2; ++j) {
+#pragma unroll
+      for (int t = 0; t < TILES; ++t) S[t] = mfma16(kt[t][j], dl[j], S[t]);
+#pragma unroll
+      for (int t = 0; t < TILES; ++t) S[t] = mfma16(kt[t][j], dh[j], S[t]);
+    }
+    phase();
+    chain_columns<DK>(buf.k, lane, kt);
+    phase();
     bf16x8 zh[2], zl[2];
-    split8(z[0], z[1], zh[0], zl[0]);
-    split8(z[2], z[3], zh[1], zl[1]);
 #pragma unroll
-    for (int it = 0; it < 4; ++it) z[it] *= -row4(ROW_C_BETA, it);
-    split8(z[0], z[1], hi[0], lo[0]);
-    split8(z[2], z[3], hi[1], lo[1]);
-    const float whole = rows[ROW_C * 64 + 63];
+    for (int j = 0; j < 2; ++j) {
+      split8(z[2 * j], z[2 * j + 1], zh[j], zl[j]);
+      split8(z[2 * j] * -decay_beta[2 * j], z[2 * j + 1] * -decay_beta[2 * j + 1], hi[j], lo[j]);
+    }
 #pragma unroll
-    for (int t = 0; t < TILES; ++t) {
-      S[t] *= whole;
+    for (int j = 0; j < 2; ++j) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int row = j * 32 + g * 8 + (c >> 2), block = (t >> 1) * 4 + (c & 3), half = (t & 1) * 8;
-        const int a = lds_block<DK>(row, block) + half, b4 = lds_block<DK>(row + 4, block) + half;
-        S[t] = mfma_exact_split(lds_transposed(buf.q + a, buf.q + b4), dh[j], dl[j], S[t]);
-        S[t] = mfma_exact_split(lds_transposed(buf.k + a, buf.k + b4), hi[j], lo[j], S[t]);
-      }
+      for (int t = 0; t < TILES; ++t) S[t] = mfma16(kt[t][j], lo[j], S[t]);
+#pragma unroll
+      for (int t = 0; t < TILES; ++t) S[t] = mfma16(kt[t][j], hi[j], S[t]);
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();

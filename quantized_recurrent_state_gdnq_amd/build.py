@@ -25,6 +25,11 @@ ARCH = "gfx950"
 GPU_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-mcode-object-version=5", "-I", INCLUDE, "-I", CSRC,
           "-Wall", "-Wno-unused-function"]
+# Results of matrix instructions in vector registers where they fit: a state that
+# is scaled and split between products would be moved out of the accumulation
+# registers and back in every chunk.
+SOURCE_FLAGS = {"delta_rule.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+                "delta_rule_backward.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
 
 
 def sources():
@@ -34,7 +39,7 @@ def sources():
 
 def _compile(src):
     obj = os.path.join(BUILD, os.path.basename(src) + ".o")
-    cmd = [HIPCC] + COMMON + GPU_FLAGS + ["-c", src, "-o", obj]
+    cmd = [HIPCC] + COMMON + GPU_FLAGS + SOURCE_FLAGS.get(os.path.basename(src), []) + ["-c", src, "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")

@@ -296,28 +296,37 @@ struct ChainLoader {
   }
 };
 
-// What the chains read of K or Q: rows of 16 tokens in chain order with their
-// columns (the first operand, or the second, of a product over d_k), and 16
-// columns in chain order with their tokens (of one over the tokens).  All of a
-// phase's operands are read ahead of it, and kept there (the sched_barriers):
-// left to the compiler each was read just before its product, and waited for.
+// What the chains read of K or Q: the 64 tokens in chain order with 32 columns
+// each (an operand of a product over d_k), and 64 columns in chain order with
+// their tokens (of one over the tokens).  Operands are read some products ahead
+// of their own, and kept there (the sched_barriers): left to the compiler each
+// was read just before its product, and waited for.
 template <int DK>
-__device__ __forceinline__ void chain_rows(const uint8_t* m, int lane, bf16x8 (&f)[4][DK / 32]) {
+__device__ __forceinline__ void chain_rows(const uint8_t* m, int lane, int j, bf16x8 (&f)[4]) {
 #pragma unroll
-  for (int j = 0; j < DK / 32; ++j)
-#pragma unroll
-    for (int it = 0; it < 4; ++it) f[it][j] = lds_frag(m + lds_block<DK>(chain_row(it, lane & 15), j * 4 + (lane >> 4)));
+  for (int it = 0; it < 4; ++it) f[it] = lds_frag(m + lds_block<DK>(chain_row(it, lane & 15), j * 4 + (lane >> 4)));
 }
 template <int DK>
-__device__ __forceinline__ void chain_columns(const uint8_t* m, int lane, bf16x8 (&f)[DK / 16][2]) {
+__device__ __forceinline__ void chain_columns(const uint8_t* m, int lane, int tiles, bf16x8 (&f)[4][2]) {
   const int c = lane & 15, g = lane >> 4;
 #pragma unroll
   for (int j = 0; j < 2; ++j)
 #pragma unroll
-    for (int t = 0; t < DK / 16; ++t) {
-      const int row = j * 32 + g * 8 + (c >> 2), block = (t >> 1) * 4 + (c & 3), half = (t & 1) * 8;
+    for (int t = 0; t < 4; ++t) {
+      const int row = j * 32 + g * 8 + (c >> 2), block = ((tiles * 4 + t) >> 1) * 4 + (c & 3), half = (t & 1) * 8;
       f[t][j] = lds_transposed(m + lds_block<DK>(row, block) + half, m + lds_block<DK>(row + 4, block) + half);
     }
+}
+// Four tiles of S^T += columns^T x, x in parts.
+__device__ __forceinline__ void chain_update(f32x4* S, const bf16x8 (&f)[4][2], const bf16x8 (&h)[2], const bf16x8 (&l)[2]) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int t = 0; t < 4; ++t) S[t] = mfma16(f[t][j], l[j], S[t]);
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int t = 0; t < 4; ++t) S[t] = mfma16(f[t][j], h[j], S[t]);
 }
 // The six blocks of a triangle, hi and lo.
 __device__ __forceinline__ void chain_triangle(const uint8_t* tri, int lane, bf16x8 (&h)[TRI_BLOCKS], bf16x8 (&l)[TRI_BLOCKS]) {

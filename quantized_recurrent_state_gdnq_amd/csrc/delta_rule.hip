@@ -57,8 +57,11 @@ __global__ __launch_bounds__(256, 1) void delta_chain_kernel(DeltaLaunch L, int 
     bf16* left = nullptr;  // this chunk's part of the carry
     if constexpr (SAVE)
       left = reinterpret_cast<bf16*>(static_cast<uint8_t*>(L.carry) + ((s.slot + chunk) * L.H + h) * delta_left_bytes(L));
-    bf16x8 kf[4][KB], qf[4][KB];
-    chain_rows<DK>(buf.k, lane, kf);
+    // K, then Q, 32 columns at a time, two ahead
+    bf16x8 ring[3][4];
+    auto read = [&](auto i) { chain_rows<DK>(i.value < KB ? buf.k : buf.q, lane, i.value % KB, ring[i.value % 3]); };
+    read(Int<0>{});
+    read(Int<1>{});
     phase();
     bf16x8 sh[KB], sl[KB];
 #pragma unroll
@@ -75,52 +78,58 @@ __global__ __launch_bounds__(256, 1) void delta_chain_kernel(DeltaLaunch L, int 
     const float* rows = reinterpret_cast<const float*>(buf.rows);
     auto row4 = [&](int which, int it) { return *reinterpret_cast<const f32x4*>(rows + which * 64 + chain_row(it, g * 4)); };
     phase();
-    chain_rows<DK>(buf.q, lane, qf);
-    s16x4 v[4];
-    f32x4 decay[4];
-#pragma unroll
-    for (int it = 0; it < 4; ++it) {
-      v[it] = chain_column(buf.v, it, wave, lane);
-      decay[it] = row4(ROW_C, it);
-    }
-    phase();
     // x = V - c K S^T by tokens (rows), and O^T = (c Q S^T)^T by tokens in lanes,
     // so that a lane has four adjacent values of a token to store: the operands
     // are the same registers, in the other order.
-    f32x4 x[4] = {}, o[4] = {};
-    each<KB>([&](auto j) {
+    f32x4 x[4] = {}, o[4] = {}, decay[4];
+    s16x4 v[4];
+    bf16x8 hi[2], lo[2], nh[TRI_BLOCKS], nl[TRI_BLOCKS];
+    each<2 * KB>([&](auto i) {
+      constexpr int j = i.value % KB;
+      if constexpr (i.value + 2 < 2 * KB) read(Int<i.value + 2>{});
+      if constexpr (i.value == KB - 1) {
 #pragma unroll
-      for (int it = 0; it < 4; ++it) x[it] = mfma16(kf[it][j.value], sl[j.value], x[it]);
+        for (int it = 0; it < 4; ++it) {
+          v[it] = chain_column(buf.v, it, wave, lane);
+          decay[it] = row4(ROW_C, it);
+        }
+      }
+      if constexpr (i.value == 2 * KB - 2) chain_triangle(buf.tri, lane, nh, nl);
+      phase();
+      const bf16x8(&f)[4] = ring[i.value % 3];
+      if constexpr (i.value < KB) {
 #pragma unroll
-      for (int it = 0; it < 4; ++it) x[it] = mfma16(kf[it][j.value], sh[j.value], x[it]);
-      ahead(Int<j.value>{});  // the first LOADS = KB steps
+        for (int it = 0; it < 4; ++it) x[it] = mfma16(f[it], sl[j], x[it]);
+#pragma unroll
+        for (int it = 0; it < 4; ++it) x[it] = mfma16(f[it], sh[j], x[it]);
+      } else {
+#pragma unroll
+        for (int it = 0; it < 4; ++it) o[it] = mfma16(sl[j], f[it], o[it]);
+#pragma unroll
+        for (int it = 0; it < 4; ++it) o[it] = mfma16(sh[j], f[it], o[it]);
+      }
+      if constexpr (i.value >= 2 * KB - 2) {  // beside the last of these products
+        constexpr int half = i.value - (2 * KB - 2);
+#pragma unroll
+        for (int it = 2 * half; it < 2 * half + 2; ++it)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[it][e] = bf16_value(v[it][e]) - decay[it][e] * x[it][e];
+        split8(x[2 * half], x[2 * half + 1], hi[half], lo[half]);
+      }
+      // the loader's first KB + 2 steps
+      if constexpr (i.value < KB) ahead(Int<i.value>{});
+      if constexpr (i.value >= 2 * KB - 2) ahead(Int<i.value - KB + 2>{});
     });
     phase();
-    bf16x8 nh[TRI_BLOCKS], nl[TRI_BLOCKS];
-    chain_triangle(buf.tri, lane, nh, nl);
-    phase();
-    each<KB>([&](auto j) {
-#pragma unroll
-      for (int it = 0; it < 4; ++it) o[it] = mfma16(sl[j.value], qf[it][j.value], o[it]);
-#pragma unroll
-      for (int it = 0; it < 4; ++it) o[it] = mfma16(sh[j.value], qf[it][j.value], o[it]);
-      if constexpr (j.value % (KB / 2) == KB / 2 - 1) ahead(Int<KB + (j.value + 1) / (KB / 2) - 1>{});
-    });
-#pragma unroll
-    for (int it = 0; it < 4; ++it)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[it][e] = bf16_value(v[it][e]) - decay[it][e] * x[it][e];
-    bf16x8 hi[2], lo[2];
-    split8(x[0], x[1], hi[0], lo[0]);
-    split8(x[2], x[3], hi[1], lo[1]);
-    ahead(Int<KB + 2>{});
-    phase();
-    bf16x8 kt[TILES][2];
-    chain_columns<DK>(buf.k, lane, kt);
+    bf16x8 kt[2][4][2];
+    chain_columns<DK>(buf.k, lane, 0, kt[0]);
     f32x4 tail[4];
 #pragma unroll
     for (int it = 0; it < 4; ++it) tail[it] = row4(ROW_TAIL_BETA, it);
     const float whole = rows[ROW_C * 64 + 63];
+    float decay_o[4];
+#pragma unroll
+    for (int it = 0; it < 4; ++it) decay_o[it] = rows[ROW_C * 64 + chain_row(it, c)];
     phase();
     // The six blocks of a triangle: tiles 0 and 1 with the first 32 tokens, 2 and
     // 3 with both halves.
@@ -132,31 +141,26 @@ __global__ __launch_bounds__(256, 1) void delta_chain_kernel(DeltaLaunch L, int 
       for (int it = 2; it < 4; ++it) w[it] = mfma16(n[2 * it - 1], y[1], w[it]);
     };
     part(nl, hi);
-    ahead(Int<KB + 3>{});
     part(nh, lo);
     part(nh, hi);
-    ahead(Int<KB + 4>{});
-    bf16x8 th[2], tl[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      split8(w[2 * j] * tail[2 * j], w[2 * j + 1] * tail[2 * j + 1], th[j], tl[j]);
-      split8(w[2 * j], w[2 * j + 1], hi[j], lo[j]);
-    }
-#pragma unroll
-    for (int it = 0; it < 4; ++it) o[it] *= rows[ROW_C * 64 + chain_row(it, c)];
 #pragma unroll
     for (int t = 0; t < TILES; ++t) S[t] *= whole;
+#pragma unroll
+    for (int it = 0; it < 4; ++it) o[it] *= decay_o[it];
+    ahead(Int<KB + 2>{});
     phase();
-    bf16x8 mh[TRI_BLOCKS], ml[TRI_BLOCKS];
+    bf16x8 mh[TRI_BLOCKS], ml[TRI_BLOCKS], th[2], tl[2];
+    if constexpr (TILES > 4) chain_columns<DK>(buf.k, lane, 1, kt[1]);
     chain_triangle(buf.tri + TRI_BYTES, lane, mh, ml);
     phase();
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < 2; ++j) split8(w[2 * j] * tail[2 * j], w[2 * j + 1] * tail[2 * j + 1], th[j], tl[j]);
+    chain_update(S, kt[0], th, tl);
 #pragma unroll
-      for (int t = 0; t < TILES; ++t) S[t] = mfma16(kt[t][j], tl[j], S[t]);
-#pragma unroll
-      for (int t = 0; t < TILES; ++t) S[t] = mfma16(kt[t][j], th[j], S[t]);
-    }
+    for (int j = 0; j < 2; ++j) split8(w[2 * j], w[2 * j + 1], hi[j], lo[j]);
+    ahead(Int<KB + 3>{});
+    if constexpr (TILES > 4) chain_update(S + 4, kt[1], th, tl);
+    ahead(Int<KB + 4>{});
     auto inside = [&](const bf16x8 (&y)[2], const bf16x8 (&m)[TRI_BLOCKS]) {
 #pragma unroll
       for (int it = 0; it < 4; ++it) o[it] = mfma16(y[0], m[it < 2 ? it : 2 * it - 2], o[it]);
@@ -166,6 +170,7 @@ __global__ __launch_bounds__(256, 1) void delta_chain_kernel(DeltaLaunch L, int 
     inside(lo, mh);
     inside(hi, ml);
     inside(hi, mh);
+    phase();
     // the next chunk is in LDS, and nobody reads this one any more; the stores
     // below are behind this wait, so that the next chunk's covers them
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");

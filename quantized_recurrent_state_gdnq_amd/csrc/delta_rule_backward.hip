@@ -54,8 +54,10 @@ __global__ __launch_bounds__(256, 1) void delta_chain_back_kernel(DeltaLaunch L,
     };
     bf16* left = reinterpret_cast<bf16*>(static_cast<uint8_t*>(L.workspace) + left_at +
                                          ((s.slot + chunk) * L.H + h) * delta_left_bytes(L));
-    bf16x8 kf[4][KB];
-    chain_rows<DK>(buf.k, lane, kf);
+    bf16x8 ring[3][4];
+    auto read = [&](auto i) { chain_rows<DK>(buf.k, lane, i.value, ring[i.value % 3]); };
+    read(Int<0>{});
+    read(Int<1>{});
     phase();
     bf16x8 sh[KB], sl[KB];
 #pragma unroll
@@ -70,42 +72,36 @@ __global__ __launch_bounds__(256, 1) void delta_chain_back_kernel(DeltaLaunch L,
     const float* rows = reinterpret_cast<const float*>(buf.rows);
     auto row4 = [&](int which, int it) { return *reinterpret_cast<const f32x4*>(rows + which * 64 + chain_row(it, g * 4)); };
     phase();
-    bf16x8 mh[TRI_BLOCKS], ml[TRI_BLOCKS];
-    chain_triangle(buf.tri + TRI_BYTES, lane, mh, ml);
-    s16x4 d4[4];
-    f32x4 tail[4], decay[4], decay_beta[4];
+    f32x4 u[4] = {}, tail[4], decay[4];
+    bf16x8 mh[TRI_BLOCKS], ml[TRI_BLOCKS], d[2];
+    each<KB>([&](auto i) {
+      if constexpr (i.value + 2 < KB) read(Int<i.value + 2>{});
+      if constexpr (i.value == KB - 2) {
+        chain_triangle(buf.tri + TRI_BYTES, lane, mh, ml);
 #pragma unroll
-    for (int it = 0; it < 4; ++it) {
-      d4[it] = chain_column(buf.v, it, wave, lane);
-      tail[it] = row4(ROW_TAIL, it);
-      decay[it] = row4(ROW_C, it);
-      decay_beta[it] = row4(ROW_C_BETA, it);
-    }
-    const float whole = rows[ROW_C * 64 + 63];
-    phase();
-    f32x4 u[4] = {};
-    each<KB>([&](auto j) {
+        for (int j = 0; j < 2; ++j) {
+          const s16x4 d0 = chain_column(buf.v, 2 * j, wave, lane), d1 = chain_column(buf.v, 2 * j + 1, wave, lane);
+          typedef short s16x8 __attribute__((ext_vector_type(8)));
+          d[j] = __builtin_bit_cast(bf16x8, s16x8{d0[0], d0[1], d0[2], d0[3], d1[0], d1[1], d1[2], d1[3]});
+        }
 #pragma unroll
-      for (int it = 0; it < 4; ++it) u[it] = mfma16(kf[it][j.value], sl[j.value], u[it]);
+        for (int it = 0; it < 4; ++it) {
+          tail[it] = row4(ROW_TAIL, it);
+          decay[it] = row4(ROW_C, it);
+        }
+      }
+      phase();
+      const bf16x8(&f)[4] = ring[i.value % 3];
 #pragma unroll
-      for (int it = 0; it < 4; ++it) u[it] = mfma16(kf[it][j.value], sh[j.value], u[it]);
-      ahead(Int<j.value>{});  // the first LOADS = KB steps
+      for (int it = 0; it < 4; ++it) u[it] = mfma16(f[it], sl[i.value], u[it]);
+#pragma unroll
+      for (int it = 0; it < 4; ++it) u[it] = mfma16(f[it], sh[i.value], u[it]);
+      ahead(Int<i.value>{});  // the loader's first KB steps
     });
+    const float whole = rows[ROW_C * 64 + 63];
+    bf16x8 kt[2][4][2], dh[2], dl[2], hi[2], lo[2];
+    chain_columns<DK>(buf.q, lane, 0, kt[0]);
     phase();
-    bf16x8 nh[TRI_BLOCKS], nl[TRI_BLOCKS], kt[TILES][2];
-    chain_triangle(buf.tri, lane, nh, nl);
-    chain_columns<DK>(buf.q, lane, kt);
-    phase();
-    // dO, and c dO in parts
-    bf16x8 d[2], dh[2], dl[2], hi[2], lo[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const s16x4 d0 = d4[2 * j], d1 = d4[2 * j + 1];
-      typedef short s16x8 __attribute__((ext_vector_type(8)));
-      d[j] = __builtin_bit_cast(bf16x8, s16x8{d0[0], d0[1], d0[2], d0[3], d1[0], d1[1], d1[2], d1[3]});
-    }
-#pragma unroll
-    for (int it = 0; it < 4; ++it) u[it] *= tail[it];
     // transposed triangles: tiles 0 and 1 take both halves of the tokens, 2 and 3 the second
     auto part = [&](f32x4 (&y)[4], const bf16x8 (&m)[TRI_BLOCKS], const bf16x8 (&x)[2]) {
 #pragma unroll
@@ -113,55 +109,60 @@ __global__ __launch_bounds__(256, 1) void delta_chain_back_kernel(DeltaLaunch L,
 #pragma unroll
       for (int it = 0; it < 2; ++it) y[it] = mfma16(m[it * 2], x[0], y[it]);
     };
+#pragma unroll
+    for (int it = 0; it < 4; ++it) u[it] *= tail[it];
     part(u, ml, d);
-    ahead(Int<KB>{});
     part(u, mh, d);
-    ahead(Int<KB + 1>{});
+    // beside these products: c dO in parts
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       f32x4 a, b4;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        a[e] = decay[2 * j][e] * bf16_value(d4[2 * j][e]);
-        b4[e] = decay[2 * j + 1][e] * bf16_value(d4[2 * j + 1][e]);
+        a[e] = decay[2 * j][e] * float(d[j][e]);
+        b4[e] = decay[2 * j + 1][e] * float(d[j][4 + e]);
       }
       split8(a, b4, dh[j], dl[j]);
     }
-    split8(u[0], u[1], hi[0], lo[0]);
-    split8(u[2], u[3], hi[1], lo[1]);
-    f32x4 z[4] = {};
-    part(z, nl, hi);
-    ahead(Int<KB + 2>{});
-    part(z, nh, lo);
-    ahead(Int<KB + 3>{});
-    part(z, nh, hi);
-    ahead(Int<KB + 4>{});
-    // the part of dS that does not wait for z
 #pragma unroll
     for (int t = 0; t < TILES; ++t) S[t] *= whole;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-#pragma unroll
-      for (int t = 0; t < TILES; ++t) S[t] = mfma16(kt[t][j], dl[j], S[t]);
-#pragma unroll
-      for (int t = 0; t < TILES; ++t) S[t] = mfma16(kt[t][j], dh[j], S[t]);
-    }
+    ahead(Int<KB>{});
     phase();
-    chain_columns<DK>(buf.k, lane, kt);
+    bf16x8 nh[TRI_BLOCKS], nl[TRI_BLOCKS];
+    chain_triangle(buf.tri, lane, nh, nl);
+    if constexpr (TILES > 4) chain_columns<DK>(buf.q, lane, 1, kt[1]);
     phase();
+    // the part of dS that does not wait for z, half of it while u is split
+    chain_update(S, kt[0], dh, dl);
+    split8(u[0], u[1], hi[0], lo[0]);
+    split8(u[2], u[3], hi[1], lo[1]);
+    ahead(Int<KB + 1>{});
+    phase();
+    chain_columns<DK>(buf.k, lane, 0, kt[0]);
+    f32x4 decay_beta[4];
+#pragma unroll
+    for (int it = 0; it < 4; ++it) decay_beta[it] = row4(ROW_C_BETA, it);
+    phase();
+    f32x4 z[4] = {};
+    part(z, nl, hi);
+    part(z, nh, lo);
+    part(z, nh, hi);
+    ahead(Int<KB + 2>{});
     bf16x8 zh[2], zl[2];
+    if constexpr (TILES > 4) chain_update(S + 4, kt[1], dh, dl);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      split8(z[2 * j], z[2 * j + 1], zh[j], zl[j]);
+    for (int j = 0; j < 2; ++j)
       split8(z[2 * j] * -decay_beta[2 * j], z[2 * j + 1] * -decay_beta[2 * j + 1], hi[j], lo[j]);
-    }
+    ahead(Int<KB + 3>{});
+    phase();
+    if constexpr (TILES > 4) chain_columns<DK>(buf.k, lane, 1, kt[1]);
+    phase();
+    chain_update(S, kt[0], hi, lo);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-#pragma unroll
-      for (int t = 0; t < TILES; ++t) S[t] = mfma16(kt[t][j], lo[j], S[t]);
-#pragma unroll
-      for (int t = 0; t < TILES; ++t) S[t] = mfma16(kt[t][j], hi[j], S[t]);
-    }
+    for (int j = 0; j < 2; ++j) split8(z[2 * j], z[2 * j + 1], zh[j], zl[j]);
+    ahead(Int<KB + 4>{});
+    if constexpr (TILES > 4) chain_update(S + 4, kt[1], hi, lo);
+    phase();
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     if (mine) {

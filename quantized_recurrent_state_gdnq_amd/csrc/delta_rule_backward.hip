@@ -194,12 +194,14 @@ __global__ __launch_bounds__(256, 1) void delta_chain_back_kernel(DeltaLaunch L,
 //                 + sum over j < t of k_j.((c_64 / c) u dS')_j  + c_64 <S, dS'>
 // A sum over what passes token t, with nothing subtracted: what lies before or
 // behind it wholly is not in it.
-//   One workgroup of eight waves per chunk and key head, over the key head's
-// value heads in turn (so that their sum needs no atomics and no memory): wave
-// (it, half) has the 16 tokens of tile it, half of the columns (d_k) and dM or
-// dAt.  S, dS', w, z and dO pass through LDS 32 rows (d_v) at a time, the next
-// ones loaded while these are used.  dQ and dK are formed transposed (tokens in
-// lanes), so that a token's factors are a lane's and results leave four at a time.
+//   A workgroup of sixteen waves takes a chunk and key head after another, and
+// the key head's value heads in turn (so that their sum needs no atomics and no
+// memory): wave (it, quarter) has the 16 tokens of tile it, a quarter of the
+// columns (d_k) and half of dM or of dAt.  S, dS', w, z and dO pass through LDS 32
+// rows (d_v) at a time, the next ones (of the next head, or chunk) loaded while
+// these are used; bound by these loads, 208 KB a chunk and head at 128 x 128.  dQ
+// and dK are formed transposed (tokens in lanes), so that a token's factors are a
+// lane's and results leave four at a time.
 template <int DK>
 struct GradientSlab {
   uint8_t states[4][32 * DK * 2], tokens[4][4096], d[4096];  // S hi, lo, dS' hi, lo; w hi, lo, z hi, lo; dO
@@ -210,25 +212,62 @@ __device__ __forceinline__ int slab_block(int row, int block) { return row * 64 
 
 template <int DK>
 struct GradientLoader {
-  const uint8_t *left[2], *d;  // of the carry and the workspace at this chunk and head; dO of the chunk's first token
+  static constexpr int PIECES = 4 * 32 * DK * 2 / 1024;  // kilobytes of the states, of which a wave takes every 16th
+  const uint8_t *left[2], *d, *rows;  // of the carry and the workspace at a chunk and head; dO of its first token; its decays
   int64_t vrow;
   int dk, dv, n, wave, lane;
-  __device__ __forceinline__ void load(GradientSlab<DK>& to, int v0) const {
-    constexpr int PIECES = 4 * 32 * DK * 2 / 1024;
+  bool exact;                  // whole columns and slabs
+  uint32_t at_state, at_row, at_d;  // a lane's offsets then
+  __device__ __forceinline__ void init(const DeltaLaunch& L, int wave_, int lane_) {
+    wave = wave_;
+    lane = lane_;
+    dk = L.dk;
+    dv = L.dv;
+    vrow = int64_t(L.H) * L.dv * 2;
+    exact = L.dk == DK && L.dv % 32 == 0;
     int row, block;
+    lds_place<DK>(wave % (PIECES / 4) * 64 + lane, row, block);  // 16 pieces on it is the same place of another part
+    at_state = uint32_t(row * DK + block * 8) * 2;
+    lds_place<64>(wave % 4 * 64 + lane, row, block);
+    at_row = uint32_t(row * 64 + block * 8) * 2;
+    row = (wave % 4 * 64 + lane) / 4;
+    block = (slab_block(row, lane & 3) >> 4) & 3;
+    at_d = uint32_t(row) * uint32_t(vrow) + block * 16;
+  }
+  __device__ __forceinline__ void set(const DeltaLaunch& L, int64_t left_at, int64_t slot, int64_t first, int tokens, int h) {
+    const int64_t chunk = slot * L.H + h;
+    const uint8_t* space = static_cast<const uint8_t*>(L.workspace);
+    left[0] = static_cast<const uint8_t*>(L.carry) + chunk * delta_left_bytes(L);
+    left[1] = space + left_at + chunk * delta_left_bytes(L);
+    rows = space + chunk * DELTA_CHUNK_BYTES + DELTA_SCALARS;
+    d = static_cast<const uint8_t*>(L.dout) + (first * L.H + h) * int64_t(L.dv) * 2;
+    n = tokens;
+  }
+  __device__ __forceinline__ void load(GradientSlab<DK>& to, int v0) const {
+    if (exact && n == 64) {
 #pragma unroll
-    for (int i = 0; i < PIECES / 8; ++i) {
-      const int piece = i * 8 + wave, part = piece / (PIECES / 4);
+      for (int i = 0; i < PIECES / 16; ++i) {
+        const int piece = i * 16 + wave, part = piece / (PIECES / 4);
+        to_lds((part < 2 ? left[0] : left[1]) + ((part & 1) * dv + v0) * (DK * 2), at_state, &to.states[0][0] + piece * 1024);
+      }
+      const int part = wave / 4;
+      to_lds((part < 2 ? left[0] : left[1]) + (2 * dv * DK + ((part & 1) * dv + v0) * 64) * 2, at_row, &to.tokens[0][0] + wave * 1024);
+      if (wave < 4) to_lds(d + v0 * 2, at_d, to.d + wave * 1024);
+      return;
+    }
+    int row, block;
+#pragma unroll 1
+    for (int i = 0; i < PIECES / 16; ++i) {
+      const int piece = i * 16 + wave, part = piece / (PIECES / 4);
       lds_place<DK>(piece % (PIECES / 4) * 64 + lane, row, block);
-      const uint8_t* p = left[part >> 1] + (int64_t((part & 1) * dv + v0 + row) * dk + block * 8) * 2;
+      const uint8_t* p = (part < 2 ? left[0] : left[1]) + (int64_t((part & 1) * dv + v0 + row) * dk + block * 8) * 2;
       to_lds(v0 + row < dv && block * 8 < dk ? p : delta_zeros, &to.states[0][0] + piece * 1024);
     }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int piece = i * 8 + wave, part = piece / 4;
-      lds_place<64>(piece % 4 * 64 + lane, row, block);
-      const uint8_t* p = left[part >> 1] + (int64_t(2 * dv) * dk + int64_t((part & 1) * dv + v0 + row) * 64 + block * 8) * 2;
-      to_lds(v0 + row < dv ? p : delta_zeros, &to.tokens[0][0] + piece * 1024);
+    {
+      const int part = wave / 4;
+      lds_place<64>(wave % 4 * 64 + lane, row, block);
+      const uint8_t* p = (part < 2 ? left[0] : left[1]) + (int64_t(2 * dv) * dk + int64_t((part & 1) * dv + v0 + row) * 64 + block * 8) * 2;
+      to_lds(v0 + row < dv ? p : delta_zeros, &to.tokens[0][0] + wave * 1024);
     }
     if (wave < 4) {
       row = (wave * 64 + lane) / 4;
@@ -237,291 +276,310 @@ struct GradientLoader {
       to_lds(row < n && v0 + block * 8 < dv ? p : delta_zeros, to.d + wave * 1024);
     }
   }
+  // Before a head's first slab: its decays, too.
+  __device__ __forceinline__ void load_first(GradientSlab<DK>& to, float* decays) const {
+    load(to, 0);
+    if (wave == 4 || wave == 5) to_lds(rows, (wave - 4) * 1024 + lane * 16, decays + (wave - 4) * 256);
+  }
 };
 
 template <int DK>
-__global__ __launch_bounds__(512, 2) void delta_gradient_kernel(DeltaLaunch L, int64_t left_at) {
-  constexpr int BLOCKS = DK / 8, KB = DK / 32, TILES = DK / 32;  // tiles of a wave
+__global__ __launch_bounds__(1024) void delta_gradient_kernel(DeltaLaunch L, int64_t left_at, int64_t items) {
+  constexpr int BLOCKS = DK / 8, KB = DK / 32, TILES = DK / 64;  // tiles of a wave
   constexpr int MAT = 64 * DK * 2;
   static_assert(sizeof(GradientSlab<DK>) >= 4 * 8192, "the triangles take a slab's place");
   __shared__ __attribute__((aligned(1024))) GradientSlab<DK> slabs[2];
   __shared__ __attribute__((aligned(1024))) uint8_t ks[MAT], qs[MAT];
-  __shared__ float rest[64], gamma[64], tail[64], beta[64], below[2][4][64], row_in[2][64], row_out[2][64], pair_sum[2][64];
-  __shared__ float dots[8];
-  __shared__ int whole[64];
+  __shared__ __attribute__((aligned(1024))) float decays[2][512];
+  __shared__ float up[64], down[64], below[2][4][64], row_in[4][64], row_out[4][64], pair_sum[4][64], dots[16];
   uint8_t* pairs = reinterpret_cast<uint8_t*>(&slabs[1]);
-  const int64_t slot = blockIdx.x / L.G;
-  const int kh = blockIdx.x % L.G, share = L.H / L.G;
-  int64_t first;
-  const int n = delta_slot_tokens(L, slot, first);
-  if (n == 0) return;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-  const int it = wave >> 1, half = wave & 1;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int it = wave >> 2, quarter = wave & 3, kind = quarter >> 1, jt0 = (quarter & 1) * 2;  // kind 0: dM, 1: dAt
+  const int share = L.H / L.G;
   const int64_t krow = int64_t(L.G) * L.dk, vrow = int64_t(L.H) * L.dv;
-  const uint8_t* space = static_cast<const uint8_t*>(L.workspace);
   GradientLoader<DK> loader;
-  loader.vrow = vrow * 2;
-  loader.dk = L.dk;
-  loader.dv = L.dv;
-  loader.n = n;
-  loader.wave = wave;
-  loader.lane = lane;
-  auto set_head = [&](int h) {
-    const int64_t chunk = slot * L.H + h;
-    loader.left[0] = static_cast<const uint8_t*>(L.carry) + chunk * delta_left_bytes(L);
-    loader.left[1] = space + left_at + chunk * delta_left_bytes(L);
-    loader.d = static_cast<const uint8_t*>(L.dout) + (first * vrow + int64_t(h) * L.dv) * 2;
-  };
-  set_head(kh * share);
-  loader.load(slabs[0], 0);
-  {
-    const uint8_t* kp = static_cast<const uint8_t*>(L.k) + (first * krow + int64_t(kh) * L.dk) * 2;
-    const uint8_t* qp = static_cast<const uint8_t*>(L.q) + (first * krow + int64_t(kh) * L.dk) * 2;
-#pragma unroll
-    for (int i = 0; i < MAT / 8192; ++i) {
-      int row, block;
-      lds_place<DK>((i * 8 + wave) * 64 + lane, row, block);
-      const int64_t at = (row * krow + block * 8) * 2;
-      const bool keep = row < n && block * 8 < L.dk;
-      to_lds(keep ? kp + at : delta_zeros, ks + (i * 8 + wave) * 1024);
-      to_lds(keep ? qp + at : delta_zeros, qs + (i * 8 + wave) * 1024);
-    }
-  }
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  __syncthreads();
-  // q.k (or k.k) of the wave's rows with the tokens up to them: exact products
-  f32x4 xk[4] = {};
-#pragma unroll
-  for (int j = 0; j < KB; ++j) {
-    const bf16x8 row8 = lds_frag((half ? ks : qs) + lds_block<DK>(it * 16 + c, j * 4 + g));
-#pragma unroll
-    for (int jt = 0; jt < 4; ++jt)
-      if (jt <= it) xk[jt] = mfma16(row8, lds_frag(ks + lds_block<DK>(jt * 16 + c, j * 4 + g)), xk[jt]);
-  }
-  const int token = it * 16 + c;
-  // 4 x 16 (row, column) blocks of a transposing read
-  const int tr_row = g * 8 + (c >> 2), tr_half = (c & 1) * 8, tr_block = (c & 3) >> 1;
-  const int col0 = half * TILES * 16;  // of the wave's columns
+  loader.init(L, wave, lane);
+  const int col0 = quarter * TILES * 16;  // of the wave's columns
 
-  f32x4 dq[TILES] = {}, dk[TILES] = {};
-  for (int hs = 0; hs < share; ++hs) {
-    const int h = kh * share + hs;
-    if (threadIdx.x < 64) {
-      const float* sc = reinterpret_cast<const float*>(space + (slot * L.H + h) * DELTA_CHUNK_BYTES + DELTA_SCALARS) + lane;
-      gamma[lane] = sc[ROW_C * 64];
-      tail[lane] = sc[ROW_TAIL * 64];
-      beta[lane] = sc[ROW_BETA * 64];
-      whole[lane] = reinterpret_cast<const int*>(sc)[ROW_WHOLE * 64];
-      rest[lane] = sc[ROW_REST * 64];
+  // the item's slot, key head, first token and tokens; slots without tokens are passed over
+  int64_t item = blockIdx.x, first = 0;
+  int n = 0;
+  auto find = [&](int64_t& i, int64_t& at) {
+    int tokens = 0;
+    for (; i < items; i += gridDim.x)
+      if ((tokens = delta_slot_tokens(L, i / L.G, at)) > 0) break;
+    return tokens;
+  };
+  n = find(item, first);
+  int parity = 0;  // of the decays
+  if (item < items) {
+    loader.set(L, left_at, item / L.G, first, n, int(item % L.G) * share);
+    loader.load_first(slabs[0], decays[0]);
+  }
+  while (item < items) {
+    const int64_t slot = item / L.G;
+    const int kh = int(item % L.G);
+    int64_t next = item + gridDim.x, next_first = 0;
+    const int next_n = find(next, next_first);
+    {
+      const uint8_t* kp = static_cast<const uint8_t*>(L.k) + (first * krow + int64_t(kh) * L.dk) * 2;
+      const uint8_t* qp = static_cast<const uint8_t*>(L.q) + (first * krow + int64_t(kh) * L.dk) * 2;
+      int row, block;
+      lds_place<DK>(wave * 64 + lane, row, block);
+      if (wave < MAT / 1024) {
+        const int64_t at = (row * krow + block * 8) * 2;
+        const bool keep = row < n && block * 8 < L.dk;
+        to_lds(keep ? kp + at : delta_zeros, ks + wave * 1024);
+        to_lds(keep ? qp + at : delta_zeros, qs + wave * 1024);
+      }
     }
-    f32x4 ds[TILES] = {}, xs[TILES] = {}, ud[TILES] = {};  // dO S, z S, w dS'
-    f32x4 pair[4] = {};                                    // dO w^T or z w^T
-    float db = 0.0f, dot = 0.0f;
-    bf16* dvp = static_cast<bf16*>(L.dv_out) + (first + token) * vrow + int64_t(h) * L.dv + g * 8;
-    __syncthreads();
-    const float bt = beta[token];
-    for (int v0 = 0, turn = 0; v0 < L.dv; v0 += 32, turn ^= 1) {
-      const GradientSlab<DK>& slab = slabs[turn];
-      if (v0 + 32 < L.dv) loader.load(slabs[turn ^ 1], v0 + 32);
-      auto tokens16 = [&](int part, int tile) {
-        const int block = tile * 2 + tr_block;
-        const uint8_t* p = slab.tokens[part] + tr_half;
-        return lds_transposed(p + lds_block<64>(tr_row, block), p + lds_block<64>(tr_row + 4, block));
-      };
-      const bf16x8 wh = tokens16(0, it), wl = tokens16(1, it), zh = tokens16(2, it), zl = tokens16(3, it);
-      const bf16x8 o8 = lds_frag(slab.d + slab_block(token, g));
-#pragma unroll
-      for (int t = 0; t < TILES; ++t) {
-        const int block = (half * TILES + t) * 2 + tr_block;
-        const int a = lds_block<DK>(tr_row, block) + tr_half, b = lds_block<DK>(tr_row + 4, block) + tr_half;
-        const bf16x8 sh = lds_transposed(slab.states[0] + a, slab.states[0] + b);
-        const bf16x8 sl = lds_transposed(slab.states[1] + a, slab.states[1] + b);
-        ds[t] = mfma16(sh, o8, mfma16(sl, o8, ds[t]));
-        xs[t] = mfma_split_split(sh, sl, zh, zl, xs[t]);
-        const bf16x8 dh = lds_transposed(slab.states[2] + a, slab.states[2] + b);
-        const bf16x8 dl = lds_transposed(slab.states[3] + a, slab.states[3] + b);
-        ud[t] = mfma_split_split(dh, dl, wh, wl, ud[t]);
-      }
-#pragma unroll
-      for (int jt = 0; jt < 4; ++jt) {
-        if (jt > it) continue;
-        const bf16x8 h8 = tokens16(0, jt), l8 = tokens16(1, jt);
-        if (half)
-          pair[jt] = mfma_split_split(zh, zl, h8, l8, pair[jt]);
-        else
-          pair[jt] = mfma_exact_split(o8, h8, l8, pair[jt]);
-      }
-      bf16x8 dv8;
-      if (half) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float z = float(zh[e]) + float(zl[e]);
-          db = fmaf(float(wh[e]) + float(wl[e]), z, db);
-          dv8[e] = bf16(bt * z);
-        }
-      }
-      // <S, dS'> of the slab's 32 rows
-      if (threadIdx.x < 32 * BLOCKS) {
-        const int p = threadIdx.x * 16;
-        const bf16x8 sh = lds_frag(slab.states[0] + p), sl = lds_frag(slab.states[1] + p);
-        const bf16x8 dh = lds_frag(slab.states[2] + p), dl = lds_frag(slab.states[3] + p);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) dot = fmaf(float(sh[e]) + float(sl[e]), float(dh[e]) + float(dl[e]), dot);
-      }
+    f32x4 dq[TILES] = {}, dk[TILES] = {};
+    for (int hs = 0; hs < share; ++hs, parity ^= 1) {
+      // places in LDS are formed again for every head: kept over all of it, they
+      // would not fit the registers beside the sums
+      int ln = lane;
+      asm volatile("" : "+v"(ln));
+      const int c = ln & 15, g = ln >> 4, token = it * 16 + c;
+      // 4 x 16 (row, column) blocks of a transposing read
+      const int tr_row = g * 8 + (c >> 2), tr_half = (c & 1) * 8, tr_block = (c & 3) >> 1;
+      const int h = kh * share + hs;
+      const float* row = decays[parity];
+      f32x4 ds[TILES] = {}, xs[TILES] = {}, ud[TILES] = {};  // dO S, z S, w dS'
+      f32x4 pair[2] = {};                                    // dO w^T or z w^T
+      float db = 0.0f, dot = 0.0f;
+      bf16* dvp = static_cast<bf16*>(L.dv_out) + (first + token) * vrow + int64_t(h) * L.dv + g * 8;
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       __syncthreads();
-      if (half && token < n && v0 + g * 8 < L.dv) *reinterpret_cast<bf16x8*>(dvp + v0) = dv8;
-    }
-    if (hs + 1 < share) {
-      set_head(h + 1);
-      loader.load(slabs[0], 0);
-    }
-    if (half) {
-      db = xor32_sum(xor16_sum(db));
-      if (token < n && g == 0) L.dbeta[(first + token) * L.H + h] = db;
-    }
-    dot = wave_allreduce_sum(dot);
-    if (lane == 0) dots[wave] = dot;
+      const float bt = row[ROW_BETA * 64 + token];
+      // rho_ij beta_j = 2^(whole_i - whole_j) up_i down_j
+      if (wave == 15) up[lane] = __builtin_amdgcn_exp2f(row[ROW_REST * 64 + lane]);
+      if (wave == 14) down[lane] = __builtin_amdgcn_exp2f(-row[ROW_REST * 64 + lane]) * row[ROW_BETA * 64 + lane];
+      for (int v0 = 0, turn = 0; v0 < L.dv; v0 += 32, turn ^= 1) {
+        const GradientSlab<DK>& slab = slabs[turn];
+        if (v0 + 32 < L.dv) loader.load(slabs[turn ^ 1], v0 + 32);
+        auto tokens16 = [&](int part, int tile) {
+          const int block = tile * 2 + tr_block;
+          const uint8_t* p = slab.tokens[part] + tr_half;
+          return lds_transposed(p + lds_block<64>(tr_row, block), p + lds_block<64>(tr_row + 4, block));
+        };
+        const bf16x8 wh = tokens16(0, it), wl = tokens16(1, it), zh = tokens16(2, it), zl = tokens16(3, it);
+        const bf16x8 o8 = lds_frag(slab.d + slab_block(token, g));
+#pragma unroll
+        for (int t = 0; t < TILES; ++t) {
+          const int block = (quarter * TILES + t) * 2 + tr_block;
+          const int a = lds_block<DK>(tr_row, block) + tr_half, b = lds_block<DK>(tr_row + 4, block) + tr_half;
+          const bf16x8 sh = lds_transposed(slab.states[0] + a, slab.states[0] + b);
+          const bf16x8 sl = lds_transposed(slab.states[1] + a, slab.states[1] + b);
+          ds[t] = mfma16(sh, o8, mfma16(sl, o8, ds[t]));
+          xs[t] = mfma_split_split(sh, sl, zh, zl, xs[t]);
+          const bf16x8 dh = lds_transposed(slab.states[2] + a, slab.states[2] + b);
+          const bf16x8 dl = lds_transposed(slab.states[3] + a, slab.states[3] + b);
+          ud[t] = mfma_split_split(dh, dl, wh, wl, ud[t]);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          if (jt0 + j > it) continue;
+          const bf16x8 h8 = tokens16(0, jt0 + j), l8 = tokens16(1, jt0 + j);
+          if (kind)
+            pair[j] = mfma_split_split(zh, zl, h8, l8, pair[j]);
+          else
+            pair[j] = mfma_exact_split(o8, h8, l8, pair[j]);
+        }
+        bf16x8 dv8;
+        if (quarter == 3) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float z = float(zh[e]) + float(zl[e]);
+            db = fmaf(float(wh[e]) + float(wl[e]), z, db);
+            dv8[e] = bf16(bt * z);
+          }
+        }
+        // <S, dS'> of the slab's 32 rows
+        if (threadIdx.x < 32 * BLOCKS) {
+          const int p = threadIdx.x * 16;
+          const bf16x8 sh = lds_frag(slab.states[0] + p), sl = lds_frag(slab.states[1] + p);
+          const bf16x8 dh = lds_frag(slab.states[2] + p), dl = lds_frag(slab.states[3] + p);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dot = fmaf(float(sh[e]) + float(sl[e]), float(dh[e]) + float(dl[e]), dot);
+        }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        if (quarter == 3 && token < n && v0 + g * 8 < L.dv) *reinterpret_cast<bf16x8*>(dvp + v0) = dv8;
+      }
+      // the first slab of the next head, or of the next chunk
+      if (hs + 1 < share) {
+        loader.set(L, left_at, slot, first, n, h + 1);
+        loader.load_first(slabs[0], decays[parity ^ 1]);
+      } else if (next < items) {
+        loader.set(L, left_at, next / L.G, next_first, next_n, int(next % L.G) * share);
+        loader.load_first(slabs[0], decays[parity ^ 1]);
+      }
+      if (quarter == 3) {
+        db = xor32_sum(xor16_sum(db));
+        if (token < n && g == 0) L.dbeta[(first + token) * L.H + h] = db;
+      }
+      dot = wave_allreduce_sum(dot);
+      if (lane == 0) dots[wave] = dot;
 
-    // The triangles times rho, in two parts, by columns: row j of `pairs` holds
-    // the 64 tokens i.  And what passes each token (sums from the last row up).
-    f32x4 passing[4] = {};
-    uint8_t* triangle = pairs + half * 16384;
+      // The triangles times rho, in two parts, by columns: row j of `pairs` holds
+      // the 64 tokens i.  And what passes each token (sums from the last row up):
+      // each element times q.k or k.k, exact products.
+      f32x4 passing[2] = {};
+      uint8_t* triangle = pairs + kind * 16384;
+      const int* whole = reinterpret_cast<const int*>(row + ROW_WHOLE * 64);
 #pragma unroll
-    for (int jt = 0; jt < 4; ++jt) {
-      if (jt > (it | 1)) continue;
-      const int j = jt * 16 + c;
-      float x4[4];
+      for (int jn = 0; jn < 2; ++jn) {
+        const int jt = jt0 + jn, j = jt * 16 + c;
+        if (jt > (it | 1)) continue;
+        f32x4 xk = {0, 0, 0, 0};
+        if (jt <= it) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int i = it * 16 + g * 4 + e;
-        float rho = j <= i ? exp2_difference(rest[i], whole[i], rest[j], whole[j]) * beta[j] : 0.0f;
-        if (half) rho = j < i ? -rho * beta[i] : 0.0f;
-        x4[e] = rho * pair[jt][e];
-        passing[jt][e] = x4[e] * xk[jt][e];
-      }
-      const int to = lds_block<64>(j, it * 2 + (g >> 1)) + (g & 1) * 8;
-      bf16x4 hi, lo;
-      split2(x4, hi, lo);
-      *reinterpret_cast<bf16x4*>(triangle + to) = hi;
-      *reinterpret_cast<bf16x4*>(triangle + 8192 + to) = lo;
-      // sums over the rows from e on, then with those of the lane groups below
-#pragma unroll
-      for (int e = 2; e >= 0; --e) passing[jt][e] += passing[jt][e + 1];
-      const float own = passing[jt][0];
-      const float up1 = __shfl_down(own, 16), up2 = __shfl_down(own, 32), up3 = __shfl_down(own, 48);
-      const float behind = (g < 3 ? up1 : 0.0f) + (g < 2 ? up2 : 0.0f) + (g < 1 ? up3 : 0.0f);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) passing[jt][e] += behind;
-      if (g == 0) below[half][it][j] = passing[jt][0];
-    }
-    __syncthreads();
-    {
-      f32x4 sum = {0, 0, 0, 0};
-#pragma unroll
-      for (int jt = 0; jt < 4; ++jt) {
-        if (jt > it) continue;
-        float later = 0.0f;
-        for (int i = it + 1; i < 4; ++i) later += below[half][i][jt * 16 + c];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (jt * 16 + c < it * 16 + g * 4 + e) sum[e] += passing[jt][e] + later;
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        sum[e] = group_sum<16>(sum[e]);
-        if (c == 0) pair_sum[half][it * 16 + g * 4 + e] = sum[e];
-      }
-    }
-    // what the state gives, and its share of the decays' gradient
-    {
-      const float gm = gamma[token], gb = gm * bt, tb = tail[token] * bt;
-      float in = 0.0f, out = 0.0f;
-#pragma unroll
-      for (int t = 0; t < TILES; ++t) {
-        const int at = lds_block<DK>(token, (col0 >> 3) + t * 2 + (g >> 1)) + (g & 1) * 8;
-        const bf16x4 q = *reinterpret_cast<const bf16x4*>(qs + at), k = *reinterpret_cast<const bf16x4*>(ks + at);
+          for (int b = 0; b < KB; ++b)
+            xk = mfma16(lds_frag((kind ? ks : qs) + lds_block<DK>(token, b * 4 + g)), lds_frag(ks + lds_block<DK>(j, b * 4 + g)), xk);
+        }
+        float x4[4];
+        const float dj = down[j];
+        const int wj = whole[j];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float a = gm * ds[t][e], x = gb * xs[t][e], u = tb * ud[t][e];
-          in = fmaf(float(q[e]), a, fmaf(-float(k[e]), x, in));
-          out = fmaf(float(k[e]), u, out);
-          dq[t][e] += a;
-          dk[t][e] += u - x;
+          const int i = it * 16 + g * 4 + e;
+          float rho = j <= i ? ldexpf(up[i] * dj, whole[i] - wj) : 0.0f;
+          if (kind) rho = j < i ? -rho * row[ROW_BETA * 64 + i] : 0.0f;
+          x4[e] = rho * pair[jn][e];
+          passing[jn][e] = x4[e] * xk[e];
+        }
+        const int to = lds_block<64>(j, it * 2 + (g >> 1)) + (g & 1) * 8;
+        bf16x4 hi, lo;
+        split2(x4, hi, lo);
+        *reinterpret_cast<bf16x4*>(triangle + to) = hi;
+        *reinterpret_cast<bf16x4*>(triangle + 8192 + to) = lo;
+        // sums over the rows from e on, then with those of the lane groups below
+#pragma unroll
+        for (int e = 2; e >= 0; --e) passing[jn][e] += passing[jn][e + 1];
+        const float own = passing[jn][0];
+        const float up1 = __shfl_down(own, 16), up2 = __shfl_down(own, 32), up3 = __shfl_down(own, 48);
+        const float behind = (g < 3 ? up1 : 0.0f) + (g < 2 ? up2 : 0.0f) + (g < 1 ? up3 : 0.0f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) passing[jn][e] += behind;
+        if (g == 0) below[kind][it][j] = passing[jn][0];
+      }
+      // what the state gives, and its share of the decays' gradient
+      {
+        const float gm = row[ROW_C * 64 + token], gb = row[ROW_C_BETA * 64 + token], tb = row[ROW_TAIL_BETA * 64 + token];
+        float in = 0.0f, out = 0.0f;
+#pragma unroll
+        for (int t = 0; t < TILES; ++t) {
+          const int at = lds_block<DK>(token, (col0 >> 3) + t * 2 + (g >> 1)) + (g & 1) * 8;
+          const bf16x4 q = *reinterpret_cast<const bf16x4*>(qs + at), k = *reinterpret_cast<const bf16x4*>(ks + at);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float a = gm * ds[t][e], x = gb * xs[t][e], u = tb * ud[t][e];
+            in = fmaf(float(q[e]), a, fmaf(-float(k[e]), x, in));
+            out = fmaf(float(k[e]), u, out);
+            dq[t][e] += a;
+            dk[t][e] += u - x;
+          }
+        }
+        in = xor32_sum(xor16_sum(in));
+        out = xor32_sum(xor16_sum(out));
+        if (g == 0) row_in[quarter][token] = in, row_out[quarter][token] = out;
+      }
+      __syncthreads();
+      {
+        f32x4 sum = {0, 0, 0, 0};
+#pragma unroll
+        for (int jn = 0; jn < 2; ++jn) {
+          const int jt = jt0 + jn;
+          if (jt > it) continue;
+          float later = 0.0f;
+          for (int i = it + 1; i < 4; ++i) later += below[kind][i][jt * 16 + c];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (jt * 16 + c < it * 16 + g * 4 + e) sum[e] += passing[jn][e] + later;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          sum[e] = group_sum<16>(sum[e]);
+          if (c == 0) pair_sum[quarter][it * 16 + g * 4 + e] = sum[e];
         }
       }
-      in = xor32_sum(xor16_sum(in));
-      out = xor32_sum(xor16_sum(out));
-      if (g == 0) row_in[half][token] = in, row_out[half][token] = out;
-    }
-    // dM K, dAt K (rows i), dM^T Q, dAt^T K (rows j)
+      // dM K, dAt K (rows i), dM^T Q, dAt^T K (rows j)
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-      bf16x8 k8[TILES], q8[TILES];
+      for (int kb = 0; kb < 2; ++kb) {
+        bf16x8 k8[TILES], q8[TILES];
+#pragma unroll
+        for (int t = 0; t < TILES; ++t) {
+          const int block = (quarter * TILES + t) * 2 + tr_block;
+          const int ka = lds_block<DK>(kb * 32 + tr_row, block) + tr_half, kb4 = lds_block<DK>(kb * 32 + tr_row + 4, block) + tr_half;
+          k8[t] = lds_transposed(ks + ka, ks + kb4);
+          q8[t] = lds_transposed(qs + ka, qs + kb4);
+        }
+        if (kb <= it / 2) {  // j up to the wave's rows
+          const int block = it * 2 + tr_block;
+          const int a = lds_block<64>(kb * 32 + tr_row, block) + tr_half, b = lds_block<64>(kb * 32 + tr_row + 4, block) + tr_half;
+          const bf16x8 mh = lds_transposed(pairs + a, pairs + b), ml = lds_transposed(pairs + 8192 + a, pairs + 8192 + b);
+          const bf16x8 ah = lds_transposed(pairs + 16384 + a, pairs + 16384 + b);
+          const bf16x8 al = lds_transposed(pairs + 24576 + a, pairs + 24576 + b);
+#pragma unroll
+          for (int t = 0; t < TILES; ++t) {
+            dq[t] = mfma_exact_split(k8[t], mh, ml, dq[t]);
+            dk[t] = mfma_exact_split(k8[t], ah, al, dk[t]);
+          }
+        }
+        if (kb >= it / 2) {  // i from the wave's rows on
+          const int at = lds_block<64>(token, kb * 4 + g);
+          const bf16x8 mh = lds_frag(pairs + at), ml = lds_frag(pairs + 8192 + at);
+          const bf16x8 ah = lds_frag(pairs + 16384 + at), al = lds_frag(pairs + 24576 + at);
+#pragma unroll
+          for (int t = 0; t < TILES; ++t) {
+            dk[t] = mfma_exact_split(q8[t], mh, ml, dk[t]);
+            dk[t] = mfma_exact_split(k8[t], ah, al, dk[t]);
+          }
+        }
+      }
+      __syncthreads();
+      if (wave == 0) {
+        // sums over i >= t, and over j < t (not of all up to t less the token's own:
+        // its own is far larger where the token forgets much)
+        float in = 0.0f, out = 0.0f, all = 0.0f, inside = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          in += row_in[i][63 - lane];
+          out += lane ? row_out[i][lane - 1] : 0.0f;
+          inside += pair_sum[i][lane];
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) all += dots[i];
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+          const float a = __shfl_up(in, d), b = __shfl_up(out, d);
+          if (lane >= d) in += a, out += b;
+        }
+        in = __shfl(in, 63 - lane);
+        float da_t = inside + in + out + row[ROW_C * 64 + 63] * all;
+        if (lane < n) {
+          const int64_t at = (first + lane) * L.H + h;
+          if (!L.log_decay) da_t /= fmaxf(L.alpha[at], 5.42101086e-20f);  // the least decay, 2^-64
+          L.dalpha[at] = da_t;
+        }
+      }
+    }
+    const int token = it * 16 + (lane & 15), g = lane >> 4;
+    if (token < n) {
+      bf16* dqp = static_cast<bf16*>(L.dq) + (first + token) * krow + int64_t(kh) * L.dk;
+      bf16* dkp = static_cast<bf16*>(L.dk_out) + (first + token) * krow + int64_t(kh) * L.dk;
 #pragma unroll
       for (int t = 0; t < TILES; ++t) {
-        const int block = (half * TILES + t) * 2 + tr_block;
-        const int ka = lds_block<DK>(kb * 32 + tr_row, block) + tr_half, kb4 = lds_block<DK>(kb * 32 + tr_row + 4, block) + tr_half;
-        k8[t] = lds_transposed(ks + ka, ks + kb4);
-        q8[t] = lds_transposed(qs + ka, qs + kb4);
-      }
-      if (kb <= it / 2) {  // j up to the wave's rows
-        const int block = it * 2 + tr_block;
-        const int a = lds_block<64>(kb * 32 + tr_row, block) + tr_half, b = lds_block<64>(kb * 32 + tr_row + 4, block) + tr_half;
-        const bf16x8 mh = lds_transposed(pairs + a, pairs + b), ml = lds_transposed(pairs + 8192 + a, pairs + 8192 + b);
-        const bf16x8 ah = lds_transposed(pairs + 16384 + a, pairs + 16384 + b);
-        const bf16x8 al = lds_transposed(pairs + 24576 + a, pairs + 24576 + b);
-#pragma unroll
-        for (int t = 0; t < TILES; ++t) {
-          dq[t] = mfma_exact_split(k8[t], mh, ml, dq[t]);
-          dk[t] = mfma_exact_split(k8[t], ah, al, dk[t]);
-        }
-      }
-      if (kb >= it / 2) {  // i from the wave's rows on
-        const int at = lds_block<64>(token, kb * 4 + g);
-        const bf16x8 mh = lds_frag(pairs + at), ml = lds_frag(pairs + 8192 + at);
-        const bf16x8 ah = lds_frag(pairs + 16384 + at), al = lds_frag(pairs + 24576 + at);
-#pragma unroll
-        for (int t = 0; t < TILES; ++t) {
-          dk[t] = mfma_exact_split(q8[t], mh, ml, dk[t]);
-          dk[t] = mfma_exact_split(k8[t], ah, al, dk[t]);
+        const int at = col0 + t * 16 + g * 4;
+        if (at < L.dk) {
+          *reinterpret_cast<bf16x4*>(dqp + at) = __builtin_convertvector(dq[t], bf16x4);
+          *reinterpret_cast<bf16x4*>(dkp + at) = __builtin_convertvector(dk[t], bf16x4);
         }
       }
     }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    if (wave == 0) {
-      // sums over i >= t, and over j < t (not of all up to t less the token's own:
-      // its own is far larger where the token forgets much)
-      float in = row_in[0][63 - lane] + row_in[1][63 - lane], out = lane ? row_out[0][lane - 1] + row_out[1][lane - 1] : 0.0f;
-#pragma unroll
-      for (int d = 1; d < 64; d *= 2) {
-        const float a = __shfl_up(in, d), b = __shfl_up(out, d);
-        if (lane >= d) in += a, out += b;
-      }
-      in = __shfl(in, 63 - lane);
-      float all = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) all += dots[i];
-      float da_t = pair_sum[0][lane] + pair_sum[1][lane] + in + out + gamma[63] * all;
-      if (lane < n) {
-        const int64_t at = (first + lane) * L.H + h;
-        if (!L.log_decay) da_t /= fmaxf(L.alpha[at], 5.42101086e-20f);  // the least decay, 2^-64
-        L.dalpha[at] = da_t;
-      }
-    }
-    __syncthreads();
-  }
-  if (token >= n) return;
-  bf16* dqp = static_cast<bf16*>(L.dq) + (first + token) * krow + int64_t(kh) * L.dk;
-  bf16* dkp = static_cast<bf16*>(L.dk_out) + (first + token) * krow + int64_t(kh) * L.dk;
-#pragma unroll
-  for (int t = 0; t < TILES; ++t) {
-    const int at = col0 + t * 16 + g * 4;
-    if (at < L.dk) {
-      *reinterpret_cast<bf16x4*>(dqp + at) = __builtin_convertvector(dq[t], bf16x4);
-      *reinterpret_cast<bf16x4*>(dkp + at) = __builtin_convertvector(dk[t], bf16x4);
-    }
+    item = next;
+    first = next_first;
+    n = next_n;
   }
 }
 
@@ -536,7 +594,8 @@ hipError_t backward(const DeltaLaunch& L, hipStream_t stream) {
   const int groups = (L.dv + 63) / 64;
   delta_chain_back_kernel<DK><<<uint32_t(groups) * uint32_t(L.H) * uint32_t(L.B), 256, 0, stream>>>(L, groups, left_at);
   if (hipError_t e = hipGetLastError()) return e;
-  if (slots > 0) delta_gradient_kernel<DK><<<uint32_t(slots * L.G), 512, 0, stream>>>(L, left_at);
+  const int64_t items = slots * L.G;
+  if (items > 0) delta_gradient_kernel<DK><<<uint32_t(items < 256 ? items : 256), 1024, 0, stream>>>(L, left_at, items);
   return hipGetLastError();
 }
 

@@ -312,6 +312,30 @@ __global__ __launch_bounds__(1024) void delta_gradient_kernel(DeltaLaunch L, int
   };
   n = find(item, first);
   int parity = 0;  // of the decays
+  // d log alpha of the head before, whose sums lie in LDS until the next head's
+  // slabs are done: by a wave with the least other work, while slabs are loaded.
+  int64_t last_first = 0;
+  int last_n = 0, last_h = 0;
+  auto finish = [&](const float* row) {
+    // sums over i >= t, and over j < t (not of all up to t less the token's own:
+    // its own is far larger where the token forgets much)
+    float in = 0.0f, out = 0.0f, all = 0.0f, inside = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      in += row_in[i][63 - lane];
+      out += lane ? row_out[i][lane - 1] : 0.0f;
+      inside += pair_sum[i][lane];
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) all += dots[i];
+    in = __shfl(wave_scan_incl(in), 63 - lane);
+    float da = inside + in + wave_scan_incl(out) + row[ROW_C * 64 + 63] * all;
+    if (lane < last_n) {
+      const int64_t at = (last_first + lane) * L.H + last_h;
+      if (!L.log_decay) da /= fmaxf(L.alpha[at], 5.42101086e-20f);  // the least decay, 2^-64
+      L.dalpha[at] = da;
+    }
+  };
   if (item < items) {
     loader.set(L, left_at, item / L.G, first, n, int(item % L.G) * share);
     loader.load_first(slabs[0], decays[0]);
@@ -321,18 +345,6 @@ __global__ __launch_bounds__(1024) void delta_gradient_kernel(DeltaLaunch L, int
     const int kh = int(item % L.G);
     int64_t next = item + gridDim.x, next_first = 0;
     const int next_n = find(next, next_first);
-    {
-      const uint8_t* kp = static_cast<const uint8_t*>(L.k) + (first * krow + int64_t(kh) * L.dk) * 2;
-      const uint8_t* qp = static_cast<const uint8_t*>(L.q) + (first * krow + int64_t(kh) * L.dk) * 2;
-      int row, block;
-      lds_place<DK>(wave * 64 + lane, row, block);
-      if (wave < MAT / 1024) {
-        const int64_t at = (row * krow + block * 8) * 2;
-        const bool keep = row < n && block * 8 < L.dk;
-        to_lds(keep ? kp + at : delta_zeros, ks + wave * 1024);
-        to_lds(keep ? qp + at : delta_zeros, qs + wave * 1024);
-      }
-    }
     f32x4 dq[TILES] = {}, dk[TILES] = {};
     for (int hs = 0; hs < share; ++hs, parity ^= 1) {
       // places in LDS are formed again for every head: kept over all of it, they
@@ -350,6 +362,19 @@ __global__ __launch_bounds__(1024) void delta_gradient_kernel(DeltaLaunch L, int
       bf16* dvp = static_cast<bf16*>(L.dv_out) + (first + token) * vrow + int64_t(h) * L.dv + g * 8;
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       __syncthreads();
+      if (hs == 0) {
+        const uint8_t* kp = static_cast<const uint8_t*>(L.k) + (first * krow + int64_t(kh) * L.dk) * 2;
+        const uint8_t* qp = static_cast<const uint8_t*>(L.q) + (first * krow + int64_t(kh) * L.dk) * 2;
+        int r, block;
+        lds_place<DK>(wave * 64 + ln, r, block);
+        if (wave < MAT / 1024) {
+          const int64_t at = (r * krow + block * 8) * 2;
+          const bool keep = r < n && block * 8 < L.dk;
+          to_lds(keep ? kp + at : delta_zeros, ks + wave * 1024);
+          to_lds(keep ? qp + at : delta_zeros, qs + wave * 1024);
+        }
+      }
+      if (wave == 3 && last_n > 0) finish(decays[parity ^ 1]);
       const float bt = row[ROW_BETA * 64 + token];
       // rho_ij beta_j = 2^(whole_i - whole_j) up_i down_j
       if (wave == 15) up[lane] = __builtin_amdgcn_exp2f(row[ROW_REST * 64 + lane]);
@@ -537,32 +562,9 @@ __global__ __launch_bounds__(1024) void delta_gradient_kernel(DeltaLaunch L, int
           }
         }
       }
-      __syncthreads();
-      if (wave == 0) {
-        // sums over i >= t, and over j < t (not of all up to t less the token's own:
-        // its own is far larger where the token forgets much)
-        float in = 0.0f, out = 0.0f, all = 0.0f, inside = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          in += row_in[i][63 - lane];
-          out += lane ? row_out[i][lane - 1] : 0.0f;
-          inside += pair_sum[i][lane];
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) all += dots[i];
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-          const float a = __shfl_up(in, d), b = __shfl_up(out, d);
-          if (lane >= d) in += a, out += b;
-        }
-        in = __shfl(in, 63 - lane);
-        float da_t = inside + in + out + row[ROW_C * 64 + 63] * all;
-        if (lane < n) {
-          const int64_t at = (first + lane) * L.H + h;
-          if (!L.log_decay) da_t /= fmaxf(L.alpha[at], 5.42101086e-20f);  // the least decay, 2^-64
-          L.dalpha[at] = da_t;
-        }
-      }
+      last_first = first;
+      last_n = n;
+      last_h = h;
     }
     const int token = it * 16 + (lane & 15), g = lane >> 4;
     if (token < n) {
@@ -581,6 +583,8 @@ __global__ __launch_bounds__(1024) void delta_gradient_kernel(DeltaLaunch L, int
     first = next_first;
     n = next_n;
   }
+  __syncthreads();
+  if (wave == 3 && last_n > 0) finish(decays[parity ^ 1]);
 }
 
 template <int DK>

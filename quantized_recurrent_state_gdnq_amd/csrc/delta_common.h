@@ -89,11 +89,11 @@ __device__ __forceinline__ DeltaSpan delta_sequence(const DeltaLaunch& L, int b)
 }
 
 // The tokens of a slot: how many (0: none) and the first.
-__device__ __forceinline__ int delta_slot_tokens(const DeltaLaunch& L, int64_t slot, int64_t& first) {
+__device__ __forceinline__ int delta_slot_tokens(const DeltaLaunch& L, int slot, int64_t& first) {
   int b;
   if (!L.cu_seqlens) {
     const int chunks = (L.T + DELTA_CHUNK - 1) / DELTA_CHUNK;
-    b = int(slot / chunks);
+    b = slot / chunks;
   } else {
     int low = 0, high = L.B - 1;  // the last sequence that starts at or before the slot
     while (low < high) {

@@ -86,13 +86,13 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaLaunch L) {
   __shared__ __attribute__((aligned(16))) float a[64 * P], m[64 * P], n[64 * P];
   __shared__ float rest[64], beta[64];
   __shared__ int whole[64];
-  const int64_t slot = blockIdx.x / L.H;
-  const int h = blockIdx.x % L.H, kh = h / (L.H / L.G);
+  const int slot = int(blockIdx.x) / L.H;
+  const int h = int(blockIdx.x) % L.H, kh = h / (L.H / L.G);
   int64_t first;
   const int tokens = delta_slot_tokens(L, slot, first);
   if (tokens == 0) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-  uint8_t* out = static_cast<uint8_t*>(L.workspace) + (slot * L.H + h) * DELTA_CHUNK_BYTES;
+  uint8_t* out = static_cast<uint8_t*>(L.workspace) + (int64_t(slot) * L.H + h) * DELTA_CHUNK_BYTES;
 
   // The decays, as log2 in 64 bits and then as a whole number and a rest, so
   // that the ratio of two tokens is good to fp32 whatever lies before them.  A

@@ -276,42 +276,69 @@ struct GradientLoader {
       to_lds(row < n && v0 + block * 8 < dv ? p : delta_zeros, to.d + wave * 1024);
     }
   }
-  // Before a head's first slab: its decays, too.
-  __device__ __forceinline__ void load_first(GradientSlab<DK>& to, float* decays) const {
-    load(to, 0);
-    if (wave == 4 || wave == 5) to_lds(rows, (wave - 4) * 1024 + lane * 16, decays + (wave - 4) * 256);
-  }
 };
 
+// The sum of eight products of values in two parts.
+__device__ __forceinline__ float dot8(const bf16x8& ah, const bf16x8& al, const bf16x8& bh, const bf16x8& bl, float s) {
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    const bf16x2 a0 = {ah[e], ah[e + 1]}, a1 = {al[e], al[e + 1]}, b0 = {bh[e], bh[e + 1]}, b1 = {bl[e], bl[e + 1]};
+    s = __builtin_amdgcn_fdot2_f32_bf16(a1, b0, s, false);
+    s = __builtin_amdgcn_fdot2_f32_bf16(a0, b1, s, false);
+    s = __builtin_amdgcn_fdot2_f32_bf16(a0, b0, s, false);
+  }
+  return s;
+}
+
 template <int DK>
-__global__ __launch_bounds__(1024) void delta_gradient_kernel(DeltaLaunch L, int64_t left_at, int64_t items) {
+__global__ __launch_bounds__(1024) void delta_gradient_kernel(DeltaLaunch L, int64_t left_at, int items) {
   constexpr int BLOCKS = DK / 8, KB = DK / 32, TILES = DK / 64;  // tiles of a wave
   constexpr int MAT = 64 * DK * 2;
   static_assert(sizeof(GradientSlab<DK>) >= 4 * 8192, "the triangles take a slab's place");
   __shared__ __attribute__((aligned(1024))) GradientSlab<DK> slabs[2];
   __shared__ __attribute__((aligned(1024))) uint8_t ks[MAT], qs[MAT];
-  __shared__ __attribute__((aligned(1024))) float decays[2][512];
-  __shared__ float up[64], down[64], below[2][4][64], row_in[4][64], row_out[4][64], pair_sum[4][64], dots[16];
-  uint8_t* pairs = reinterpret_cast<uint8_t*>(&slabs[1]);
+  __shared__ __attribute__((aligned(1024))) float decays[3][512];
+  __shared__ float below[2][4][64], row_in[4][64], row_out[4][64], pair_sum[4][64], dots[16];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int it = wave >> 2, quarter = wave & 3, kind = quarter >> 1, jt0 = (quarter & 1) * 2;  // kind 0: dM, 1: dAt
   const int share = L.H / L.G;
   const int64_t krow = int64_t(L.G) * L.dk, vrow = int64_t(L.H) * L.dv;
   GradientLoader<DK> loader;
   loader.init(L, wave, lane);
+  int c = lane & 15, g = lane >> 4;
   const int col0 = quarter * TILES * 16;  // of the wave's columns
 
+  // Places in LDS.  Blocks are permuted by an exclusive or with bits of the row
+  // that 16 rows repeat, so the places of other tiles and blocks are these with
+  // constants added (rows) or xored (blocks).
+  const int tr_row = g * 8 + (c >> 2), tr_block = (c & 3) >> 1, tr_half = (c & 1) * 8;  // 4 x 16 of a transposing read
+  int tr_a = lds_block<DK>(tr_row, quarter * TILES * 2 + tr_block) + tr_half;
+  int tr_b = lds_block<DK>(tr_row + 4, quarter * TILES * 2 + tr_block) + tr_half;
+  int tr64_a = lds_block<64>(tr_row, tr_block) + tr_half, tr64_b = lds_block<64>(tr_row + 4, tr_block) + tr_half;
+  int row_d = lds_block<DK>(c, g), row_64 = lds_block<64>(c, g);  // block g of a tile's row c
+  int row_4 = lds_block<DK>(c, quarter * TILES * 2 + (g >> 1)) + (g & 1) * 8;  // four of the wave's columns
+  constexpr int TILE_D = 16 * DK * 2, TILE_64 = 16 * 128;  // bytes of a tile's rows
+  // What follows from these is formed again in each part of each head: kept, it
+  // would not fit the registers, and a reload from memory waits for all the loads
+  // into LDS that were made before it.
+  auto part = [&] {
+    asm volatile("" : "+v"(c), "+v"(g), "+v"(tr_a), "+v"(tr_b), "+v"(tr64_a), "+v"(tr64_b), "+v"(row_d), "+v"(row_64), "+v"(row_4));
+  };
+  auto columns = [&](const uint8_t* m, int t) { return lds_transposed(m + (tr_a ^ (t << 5)), m + (tr_b ^ (t << 5))); };
+  auto columns64 = [&](const uint8_t* m, int tile) { return lds_transposed(m + (tr64_a ^ (tile << 5)), m + (tr64_b ^ (tile << 5))); };
+
   // the item's slot, key head, first token and tokens; slots without tokens are passed over
-  int64_t item = blockIdx.x, first = 0;
-  int n = 0;
-  auto find = [&](int64_t& i, int64_t& at) {
+  int item = blockIdx.x, n = 0;
+  int64_t first = 0;
+  auto find = [&](int& i, int64_t& at) {
     int tokens = 0;
     for (; i < items; i += gridDim.x)
       if ((tokens = delta_slot_tokens(L, i / L.G, at)) > 0) break;
     return tokens;
   };
   n = find(item, first);
-  int parity = 0;  // of the decays
+  // of the decays (the head before's, this one's, the next one's), of the slabs
+  int before = 2, now = 0, turn = 0;
   // d log alpha of the head before, whose sums lie in LDS until the next head's
   // slabs are done: by a wave with the least other work, while slabs are loaded.
   int64_t last_first = 0;
@@ -337,36 +364,32 @@ __global__ __launch_bounds__(1024) void delta_gradient_kernel(DeltaLaunch L, int
     }
   };
   if (item < items) {
-    loader.set(L, left_at, item / L.G, first, n, int(item % L.G) * share);
-    loader.load_first(slabs[0], decays[0]);
+    loader.set(L, left_at, item / L.G, first, n, item % L.G * share);
+    loader.load(slabs[0], 0);
+    if (wave < 2) to_lds(loader.rows, wave * 1024 + lane * 16, decays[0] + wave * 256);
   }
   while (item < items) {
-    const int64_t slot = item / L.G;
-    const int kh = int(item % L.G);
-    int64_t next = item + gridDim.x, next_first = 0;
+    const int slot = item / L.G, kh = item % L.G;
+    int next = item + gridDim.x;
+    int64_t next_first = 0;
     const int next_n = find(next, next_first);
     f32x4 dq[TILES] = {}, dk[TILES] = {};
-    for (int hs = 0; hs < share; ++hs, parity ^= 1) {
-      // places in LDS are formed again for every head: kept over all of it, they
-      // would not fit the registers beside the sums
-      int ln = lane;
-      asm volatile("" : "+v"(ln));
-      const int c = ln & 15, g = ln >> 4, token = it * 16 + c;
-      // 4 x 16 (row, column) blocks of a transposing read
-      const int tr_row = g * 8 + (c >> 2), tr_half = (c & 1) * 8, tr_block = (c & 3) >> 1;
+    for (int hs = 0; hs < share; ++hs) {
+      const int after = 3 - before - now;
+      part();
+      int token = it * 16 + c;
       const int h = kh * share + hs;
-      const float* row = decays[parity];
+      const float* row = decays[now];
       f32x4 ds[TILES] = {}, xs[TILES] = {}, ud[TILES] = {};  // dO S, z S, w dS'
       f32x4 pair[2] = {};                                    // dO w^T or z w^T
       float db = 0.0f, dot = 0.0f;
-      bf16* dvp = static_cast<bf16*>(L.dv_out) + (first + token) * vrow + int64_t(h) * L.dv + g * 8;
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       __syncthreads();
       if (hs == 0) {
         const uint8_t* kp = static_cast<const uint8_t*>(L.k) + (first * krow + int64_t(kh) * L.dk) * 2;
         const uint8_t* qp = static_cast<const uint8_t*>(L.q) + (first * krow + int64_t(kh) * L.dk) * 2;
         int r, block;
-        lds_place<DK>(wave * 64 + ln, r, block);
+        lds_place<DK>(wave * 64 + lane, r, block);
         if (wave < MAT / 1024) {
           const int64_t at = (r * krow + block * 8) * 2;
           const bool keep = r < n && block * 8 < L.dk;
@@ -374,31 +397,29 @@ __global__ __launch_bounds__(1024) void delta_gradient_kernel(DeltaLaunch L, int
           to_lds(keep ? qp + at : delta_zeros, qs + wave * 1024);
         }
       }
-      if (wave == 3 && last_n > 0) finish(decays[parity ^ 1]);
+      if (wave == 3 && last_n > 0) finish(decays[before]);
       const float bt = row[ROW_BETA * 64 + token];
-      // rho_ij beta_j = 2^(whole_i - whole_j) up_i down_j
-      if (wave == 15) up[lane] = __builtin_amdgcn_exp2f(row[ROW_REST * 64 + lane]);
-      if (wave == 14) down[lane] = __builtin_amdgcn_exp2f(-row[ROW_REST * 64 + lane]) * row[ROW_BETA * 64 + lane];
-      for (int v0 = 0, turn = 0; v0 < L.dv; v0 += 32, turn ^= 1) {
+      for (int v0 = 0; v0 < L.dv; v0 += 32, turn ^= 1) {
         const GradientSlab<DK>& slab = slabs[turn];
-        if (v0 + 32 < L.dv) loader.load(slabs[turn ^ 1], v0 + 32);
-        auto tokens16 = [&](int part, int tile) {
-          const int block = tile * 2 + tr_block;
-          const uint8_t* p = slab.tokens[part] + tr_half;
-          return lds_transposed(p + lds_block<64>(tr_row, block), p + lds_block<64>(tr_row + 4, block));
-        };
+        // the next slab: of this head, of the next, or of the next chunk
+        const bool more = v0 + 32 < L.dv;
+        if (!more) {
+          if (hs + 1 < share)
+            loader.set(L, left_at, slot, first, n, h + 1);
+          else if (next < items)
+            loader.set(L, left_at, next / L.G, next_first, next_n, next % L.G * share);
+          if (wave < 2) to_lds(loader.rows, wave * 1024 + lane * 16, decays[after] + wave * 256);
+        }
+        loader.load(slabs[turn ^ 1], more ? v0 + 32 : 0);  // behind the last chunk the same again
+        auto tokens16 = [&](int part, int tile) { return columns64(slab.tokens[part], tile); };
         const bf16x8 wh = tokens16(0, it), wl = tokens16(1, it), zh = tokens16(2, it), zl = tokens16(3, it);
-        const bf16x8 o8 = lds_frag(slab.d + slab_block(token, g));
+        const bf16x8 o8 = lds_frag(slab.d + it * 1024 + slab_block(c, g));
 #pragma unroll
         for (int t = 0; t < TILES; ++t) {
-          const int block = (quarter * TILES + t) * 2 + tr_block;
-          const int a = lds_block<DK>(tr_row, block) + tr_half, b = lds_block<DK>(tr_row + 4, block) + tr_half;
-          const bf16x8 sh = lds_transposed(slab.states[0] + a, slab.states[0] + b);
-          const bf16x8 sl = lds_transposed(slab.states[1] + a, slab.states[1] + b);
+          const bf16x8 sh = columns(slab.states[0], t), sl = columns(slab.states[1], t);
           ds[t] = mfma16(sh, o8, mfma16(sl, o8, ds[t]));
           xs[t] = mfma_split_split(sh, sl, zh, zl, xs[t]);
-          const bf16x8 dh = lds_transposed(slab.states[2] + a, slab.states[2] + b);
-          const bf16x8 dl = lds_transposed(slab.states[3] + a, slab.states[3] + b);
+          const bf16x8 dh = columns(slab.states[2], t), dl = columns(slab.states[3], t);
           ud[t] = mfma_split_split(dh, dl, wh, wl, ud[t]);
         }
 #pragma unroll
@@ -412,33 +433,23 @@ __global__ __launch_bounds__(1024) void delta_gradient_kernel(DeltaLaunch L, int
         }
         bf16x8 dv8;
         if (quarter == 3) {
+          db = dot8(wh, wl, zh, zl, db);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float z = float(zh[e]) + float(zl[e]);
-            db = fmaf(float(wh[e]) + float(wl[e]), z, db);
-            dv8[e] = bf16(bt * z);
-          }
+          for (int e = 0; e < 8; ++e) dv8[e] = bf16(bt * (float(zh[e]) + float(zl[e])));
         }
         // <S, dS'> of the slab's 32 rows
-        if (threadIdx.x < 32 * BLOCKS) {
-          const int p = threadIdx.x * 16;
-          const bf16x8 sh = lds_frag(slab.states[0] + p), sl = lds_frag(slab.states[1] + p);
-          const bf16x8 dh = lds_frag(slab.states[2] + p), dl = lds_frag(slab.states[3] + p);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) dot = fmaf(float(sh[e]) + float(sl[e]), float(dh[e]) + float(dl[e]), dot);
+        if (wave < 32 * BLOCKS / 64) {
+          const int p = wave * 1024 + lane * 16;
+          dot = dot8(lds_frag(slab.states[0] + p), lds_frag(slab.states[1] + p), lds_frag(slab.states[2] + p),
+                     lds_frag(slab.states[3] + p), dot);
         }
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        if (more || v0 == 0) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // K and Q came with the first
         __syncthreads();
-        if (quarter == 3 && token < n && v0 + g * 8 < L.dv) *reinterpret_cast<bf16x8*>(dvp + v0) = dv8;
+        if (quarter == 3 && token < n && v0 + g * 8 < L.dv) *reinterpret_cast<bf16x8*>(static_cast<bf16*>(L.dv_out) + (first + token) * vrow + int64_t(h) * L.dv + g * 8 + v0) = dv8;
       }
-      // the first slab of the next head, or of the next chunk
-      if (hs + 1 < share) {
-        loader.set(L, left_at, slot, first, n, h + 1);
-        loader.load_first(slabs[0], decays[parity ^ 1]);
-      } else if (next < items) {
-        loader.set(L, left_at, next / L.G, next_first, next_n, int(next % L.G) * share);
-        loader.load_first(slabs[0], decays[parity ^ 1]);
-      }
+      part();
+      token = it * 16 + c;
+      uint8_t* pairs = reinterpret_cast<uint8_t*>(&slabs[turn ^ 1]);  // the last slab's place
       if (quarter == 3) {
         db = xor32_sum(xor16_sum(db));
         if (token < n && g == 0) L.dbeta[(first + token) * L.H + h] = db;
@@ -449,31 +460,49 @@ __global__ __launch_bounds__(1024) void delta_gradient_kernel(DeltaLaunch L, int
       // The triangles times rho, in two parts, by columns: row j of `pairs` holds
       // the 64 tokens i.  And what passes each token (sums from the last row up):
       // each element times q.k or k.k, exact products.
-      f32x4 passing[2] = {};
+      //   rho_ij beta_j = a_i b_j with a_i = 2^(log2 c_i - r), b_j = beta_j 2^(r -
+      // log2 c_j); r is that of the row tile's first token, before which the columns
+      // of a tile off the diagonal lie, so neither passes 1.
+      f32x4 passing[2] = {}, ai = {};
       uint8_t* triangle = pairs + kind * 16384;
       const int* whole = reinterpret_cast<const int*>(row + ROW_WHOLE * 64);
+      const float* rest = row + ROW_REST * 64;
+      const float rr = rest[it * 16];
+      const int rw = whole[it * 16];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = it * 16 + g * 4 + e;
+        ai[e] = exp2_difference(rest[i], whole[i], rr, rw);
+        if (kind) ai[e] *= -row[ROW_BETA * 64 + i];
+      }
 #pragma unroll
       for (int jn = 0; jn < 2; ++jn) {
         const int jt = jt0 + jn, j = jt * 16 + c;
         if (jt > (it | 1)) continue;
-        f32x4 xk = {0, 0, 0, 0};
+        float x4[4] = {};
         if (jt <= it) {
+          f32x4 xk = {0, 0, 0, 0};
 #pragma unroll
           for (int b = 0; b < KB; ++b)
-            xk = mfma16(lds_frag((kind ? ks : qs) + lds_block<DK>(token, b * 4 + g)), lds_frag(ks + lds_block<DK>(j, b * 4 + g)), xk);
-        }
-        float x4[4];
-        const float dj = down[j];
-        const int wj = whole[j];
+            xk = mfma16(lds_frag((kind ? ks : qs) + it * TILE_D + (row_d ^ (b << 6))), lds_frag(ks + jt * TILE_D + (row_d ^ (b << 6))), xk);
+          const float bj = row[ROW_BETA * 64 + j];
+          if (jt < it) {
+            const float b = bj * exp2_difference(rr, rw, rest[j], whole[j]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int i = it * 16 + g * 4 + e;
-          float rho = j <= i ? ldexpf(up[i] * dj, whole[i] - wj) : 0.0f;
-          if (kind) rho = j < i ? -rho * row[ROW_BETA * 64 + i] : 0.0f;
-          x4[e] = rho * pair[jn][e];
-          passing[jn][e] = x4[e] * xk[e];
+            for (int e = 0; e < 4; ++e) x4[e] = ai[e] * b * pair[jn][e];
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int i = g * 4 + e;
+              float rho = bj * exp2_difference(rest[it * 16 + i], whole[it * 16 + i], rest[j], whole[j]);
+              if (kind) rho *= -row[ROW_BETA * 64 + it * 16 + i];
+              x4[e] = c < i || (c == i && !kind) ? rho * pair[jn][e] : 0.0f;
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) passing[jn][e] = x4[e] * xk[e];
         }
-        const int to = lds_block<64>(j, it * 2 + (g >> 1)) + (g & 1) * 8;
+        const int to = jt * TILE_64 + ((lds_block<64>(c, g >> 1) + (g & 1) * 8) ^ (it << 5));
         bf16x4 hi, lo;
         split2(x4, hi, lo);
         *reinterpret_cast<bf16x4*>(triangle + to) = hi;
@@ -488,13 +517,14 @@ __global__ __launch_bounds__(1024) void delta_gradient_kernel(DeltaLaunch L, int
         for (int e = 0; e < 4; ++e) passing[jn][e] += behind;
         if (g == 0) below[kind][it][j] = passing[jn][0];
       }
+      part();
       // what the state gives, and its share of the decays' gradient
       {
         const float gm = row[ROW_C * 64 + token], gb = row[ROW_C_BETA * 64 + token], tb = row[ROW_TAIL_BETA * 64 + token];
         float in = 0.0f, out = 0.0f;
 #pragma unroll
         for (int t = 0; t < TILES; ++t) {
-          const int at = lds_block<DK>(token, (col0 >> 3) + t * 2 + (g >> 1)) + (g & 1) * 8;
+          const int at = it * TILE_D + (row_4 ^ (t << 5));
           const bf16x4 q = *reinterpret_cast<const bf16x4*>(qs + at), k = *reinterpret_cast<const bf16x4*>(ks + at);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -510,6 +540,7 @@ __global__ __launch_bounds__(1024) void delta_gradient_kernel(DeltaLaunch L, int
         if (g == 0) row_in[quarter][token] = in, row_out[quarter][token] = out;
       }
       __syncthreads();
+      part();
       {
         f32x4 sum = {0, 0, 0, 0};
 #pragma unroll
@@ -520,7 +551,7 @@ __global__ __launch_bounds__(1024) void delta_gradient_kernel(DeltaLaunch L, int
           for (int i = it + 1; i < 4; ++i) later += below[kind][i][jt * 16 + c];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (jt * 16 + c < it * 16 + g * 4 + e) sum[e] += passing[jn][e] + later;
+            if (jt < it || c < g * 4 + e) sum[e] += passing[jn][e] + later;
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -528,23 +559,19 @@ __global__ __launch_bounds__(1024) void delta_gradient_kernel(DeltaLaunch L, int
           if (c == 0) pair_sum[quarter][it * 16 + g * 4 + e] = sum[e];
         }
       }
+      part();
       // dM K, dAt K (rows i), dM^T Q, dAt^T K (rows j)
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) {
         bf16x8 k8[TILES], q8[TILES];
 #pragma unroll
         for (int t = 0; t < TILES; ++t) {
-          const int block = (quarter * TILES + t) * 2 + tr_block;
-          const int ka = lds_block<DK>(kb * 32 + tr_row, block) + tr_half, kb4 = lds_block<DK>(kb * 32 + tr_row + 4, block) + tr_half;
-          k8[t] = lds_transposed(ks + ka, ks + kb4);
-          q8[t] = lds_transposed(qs + ka, qs + kb4);
+          k8[t] = columns(ks + kb * 2 * TILE_D, t);
+          q8[t] = columns(qs + kb * 2 * TILE_D, t);
         }
         if (kb <= it / 2) {  // j up to the wave's rows
-          const int block = it * 2 + tr_block;
-          const int a = lds_block<64>(kb * 32 + tr_row, block) + tr_half, b = lds_block<64>(kb * 32 + tr_row + 4, block) + tr_half;
-          const bf16x8 mh = lds_transposed(pairs + a, pairs + b), ml = lds_transposed(pairs + 8192 + a, pairs + 8192 + b);
-          const bf16x8 ah = lds_transposed(pairs + 16384 + a, pairs + 16384 + b);
-          const bf16x8 al = lds_transposed(pairs + 24576 + a, pairs + 24576 + b);
+          const uint8_t* p = pairs + kb * 2 * TILE_64;
+          const bf16x8 mh = columns64(p, it), ml = columns64(p + 8192, it), ah = columns64(p + 16384, it), al = columns64(p + 24576, it);
 #pragma unroll
           for (int t = 0; t < TILES; ++t) {
             dq[t] = mfma_exact_split(k8[t], mh, ml, dq[t]);
@@ -552,9 +579,8 @@ __global__ __launch_bounds__(1024) void delta_gradient_kernel(DeltaLaunch L, int
           }
         }
         if (kb >= it / 2) {  // i from the wave's rows on
-          const int at = lds_block<64>(token, kb * 4 + g);
-          const bf16x8 mh = lds_frag(pairs + at), ml = lds_frag(pairs + 8192 + at);
-          const bf16x8 ah = lds_frag(pairs + 16384 + at), al = lds_frag(pairs + 24576 + at);
+          const uint8_t* p = pairs + it * TILE_64 + (row_64 ^ (kb << 6));
+          const bf16x8 mh = lds_frag(p), ml = lds_frag(p + 8192), ah = lds_frag(p + 16384), al = lds_frag(p + 24576);
 #pragma unroll
           for (int t = 0; t < TILES; ++t) {
             dk[t] = mfma_exact_split(q8[t], mh, ml, dk[t]);
@@ -565,8 +591,10 @@ __global__ __launch_bounds__(1024) void delta_gradient_kernel(DeltaLaunch L, int
       last_first = first;
       last_n = n;
       last_h = h;
+      before = now;
+      now = after;
     }
-    const int token = it * 16 + (lane & 15), g = lane >> 4;
+    const int token = it * 16 + c;
     if (token < n) {
       bf16* dqp = static_cast<bf16*>(L.dq) + (first + token) * krow + int64_t(kh) * L.dk;
       bf16* dkp = static_cast<bf16*>(L.dk_out) + (first + token) * krow + int64_t(kh) * L.dk;
@@ -583,8 +611,9 @@ __global__ __launch_bounds__(1024) void delta_gradient_kernel(DeltaLaunch L, int
     first = next_first;
     n = next_n;
   }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
-  if (wave == 3 && last_n > 0) finish(decays[parity ^ 1]);
+  if (wave == 3 && last_n > 0) finish(decays[before]);
 }
 
 template <int DK>
@@ -599,7 +628,7 @@ hipError_t backward(const DeltaLaunch& L, hipStream_t stream) {
   delta_chain_back_kernel<DK><<<uint32_t(groups) * uint32_t(L.H) * uint32_t(L.B), 256, 0, stream>>>(L, groups, left_at);
   if (hipError_t e = hipGetLastError()) return e;
   const int64_t items = slots * L.G;
-  if (items > 0) delta_gradient_kernel<DK><<<uint32_t(items < 256 ? items : 256), 1024, 0, stream>>>(L, left_at, items);
+  if (items > 0) delta_gradient_kernel<DK><<<uint32_t(items < 256 ? items : 256), 1024, 0, stream>>>(L, left_at, int(items));
   return hipGetLastError();
 }
 

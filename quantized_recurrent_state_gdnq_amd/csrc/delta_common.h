@@ -54,7 +54,38 @@ __host__ __device__ inline int64_t delta_align(int64_t n) { return (n + 255) / 2
 __host__ __device__ inline int64_t delta_state_bytes(const DeltaLaunch& L) { return int64_t(L.dv) * L.dk * 4; }
 __host__ __device__ inline int64_t delta_left_bytes(const DeltaLaunch& L) { return int64_t(L.dv) * (L.dk * 4 + DELTA_CHUNK * 4); }
 
+// Few chains of many chunks are cut into segments that run at once.  A segment
+// maps the state that enters it linearly, S' = S P + R: a first pass carries R
+// from zero and P from the identity (d_k more rows, without V and O), a second
+// one joins them, and the chains then start from the states that enter.  That is
+// 2.3 times the work (without the outputs, 82 of 132 products a chunk and row),
+// so it pays where chains leave three in four of the 256 CUs idle: 65536 tokens,
+// 8 heads, 16 workgroups: MEASURED_LONG.
+//   In the workspace for each sequence, segment and head: R (then the state
+// behind the segment) [d_v][d_k] fp32, P [2][d_k][d_k] in two bf16 parts.
+inline void delta_split(DeltaLaunch& L, int64_t at) {
+  const int64_t chains = int64_t(L.B) * L.H * ((L.dv + 63) / 64);
+  const int64_t chunks = ((L.cu_seqlens ? L.N : int64_t(L.T)) + DELTA_CHUNK - 1) / DELTA_CHUNK;
+  L.segments = 1;
+  L.seg_chunks = 0x7fffffff;
+  L.seg_at = delta_align(at);
+  if (chains == 0 || chains > 64) return;
+  const int64_t want = 256 / chains;
+  if (chunks < 8 * want) return;
+  L.seg_chunks = int((chunks + want - 1) / want);
+  L.segments = int((chunks + L.seg_chunks - 1) / L.seg_chunks);
+}
+__host__ __device__ inline int64_t delta_segment_bytes(const DeltaLaunch& L) { return int64_t(L.dk) * (L.dv + L.dk) * 4; }
+// The bytes up to the end of what the segments take.
+inline int64_t delta_split_bytes(const DeltaLaunch& L) {
+  return L.segments > 1 ? L.seg_at + int64_t(L.B) * L.segments * L.H * delta_segment_bytes(L) : L.seg_at;
+}
+
 #ifdef __HIPCC__
+
+__device__ __forceinline__ uint8_t* delta_segment(const DeltaLaunch& L, int b, int seg, int h) {
+  return static_cast<uint8_t*>(L.workspace) + L.seg_at + ((int64_t(b) * L.segments + seg) * L.H + h) * delta_segment_bytes(L);
+}
 
 template <int V>
 using Int = std::integral_constant<int, V>;
@@ -346,6 +377,129 @@ __device__ __forceinline__ s16x4 chain_column(const uint8_t* v, int it, int wave
       (lds4)(v + lds_block<64>(chain_row(it, g * 4) + (c >> 2), wave * 2 + ((c & 3) >> 1)) + (c & 1) * 8));
 }
 __device__ __forceinline__ float bf16_value(short x) { return __uint_as_float(uint32_t(uint16_t(x)) << 16); }
+
+// Where the workgroup of a chain is: rows [64 group, ..) of head h, segment seg of
+// sequence b.  Of a first pass the groups behind those of V carry the identity.
+struct ChainPlace {
+  int b, seg, h, group, first, end;  // chunks
+  bool identity;
+};
+__device__ __forceinline__ ChainPlace chain_place(const DeltaLaunch& L, int groups, int chunks, int b, int rest) {
+  ChainPlace p;
+  p.b = b;
+  p.group = rest % groups;
+  p.h = rest / groups % L.H;
+  p.seg = rest / groups / L.H;
+  const int dv_groups = (L.dv + 63) / 64;
+  p.identity = p.group >= dv_groups;
+  if (p.identity) p.group -= dv_groups;
+  p.first = int(min(int64_t(p.seg) * L.seg_chunks, int64_t(chunks)));
+  p.end = int(min(int64_t(p.first) + L.seg_chunks, int64_t(chunks)));
+  return p;
+}
+// A chain's state tiles from a matrix of fp32 rows (or none: zero), or the identity.
+template <int TILES>
+__device__ __forceinline__ void chain_load_state(f32x4 (&S)[TILES], const float* rows, int dk, int row, bool here, int g) {
+#pragma unroll
+  for (int t = 0; t < TILES; ++t) {
+    const int at = chain_row(t, g * 4);
+    S[t] = f32x4{0, 0, 0, 0};
+    if (rows && here && at < dk) S[t] = *reinterpret_cast<const f32x4*>(rows + int64_t(row) * dk + at);
+  }
+}
+template <int TILES>
+__device__ __forceinline__ void chain_identity(f32x4 (&S)[TILES], int row, int g) {
+#pragma unroll
+  for (int t = 0; t < TILES; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) S[t][e] = chain_row(t, g * 4) + e == row ? 1.0f : 0.0f;
+}
+// What a first pass leaves: R in fp32, or P in two parts.
+template <int TILES>
+__device__ __forceinline__ void chain_leave(const DeltaLaunch& L, const ChainPlace& p, const f32x4 (&S)[TILES], int row, int g) {
+  uint8_t* to = delta_segment(L, p.b, p.seg, p.h);
+  if (!p.identity) {
+    if (row >= L.dv) return;
+#pragma unroll
+    for (int t = 0; t < TILES; ++t) {
+      const int at = chain_row(t, g * 4);
+      if (at < L.dk) *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(to) + int64_t(row) * L.dk + at) = S[t];
+    }
+    return;
+  }
+  if (row >= L.dk) return;
+  bf16* pm = reinterpret_cast<bf16*>(to + int64_t(L.dv) * L.dk * 4);
+#pragma unroll
+  for (int j = 0; j < TILES / 2; ++j) {
+    const int at = j * 32 + g * 8;
+    bf16x8 hi, lo;
+    split8(S[2 * j], S[2 * j + 1], hi, lo);
+    if (at < L.dk) {
+      *reinterpret_cast<bf16x8*>(pm + row * L.dk + at) = hi;
+      *reinterpret_cast<bf16x8*>(pm + (L.dk + row) * L.dk + at) = lo;
+    }
+  }
+}
+
+// The segments of a sequence and head joined: S = S P + R from the first on (or,
+// for the gradient, from the last), each R replaced by the state behind it.  A
+// workgroup takes 64 rows of S, in the chains' layout; P goes through LDS.
+template <int DK, bool BACK>
+__global__ __launch_bounds__(256) void delta_join_kernel(DeltaLaunch L, int groups) {
+  constexpr int TILES = DK / 16, KB = DK / 32, PIECES = 2 * DK * DK * 2 / 1024;
+  __shared__ __attribute__((aligned(1024))) uint8_t ps[2][2][DK * DK * 2];
+  const int group = int(blockIdx.x) % groups, h = int(blockIdx.x) / groups % L.H, b = int(blockIdx.x) / groups / L.H;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+  const int row = group * 64 + wave * 16 + c;
+  const bool mine = row < L.dv;
+  const int chunks = (delta_sequence(L, b).tokens + 63) / 64;
+  const int steps = int((int64_t(chunks) + L.seg_chunks - 1) / L.seg_chunks) - 1;
+  if (steps <= 0) return;
+  auto load = [&](int step) {
+    const uint8_t* from = delta_segment(L, b, BACK ? steps - step : step, h) + int64_t(L.dv) * L.dk * 4;
+#pragma unroll 4
+    for (int i = 0; i < PIECES / 4; ++i) {
+      const int piece = i * 4 + wave, part = piece / (PIECES / 2);
+      int r, block;
+      lds_place<DK>(piece % (PIECES / 2) * 64 + lane, r, block);
+      const uint8_t* p = from + (int64_t(part * L.dk + r) * L.dk + block * 8) * 2;
+      to_lds(r < L.dk && block * 8 < L.dk ? p : delta_zeros, &ps[step & 1][0][0] + piece * 1024);
+    }
+  };
+  f32x4 S[TILES];
+  const float* start = BACK ? L.dh_last : L.h0;
+  if (start) start += (int64_t(b) * L.H + h) * L.dv * L.dk;
+  chain_load_state<TILES>(S, start, L.dk, row, mine, g);
+  load(0);
+  for (int step = 0; step < steps; ++step) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (step + 1 < steps) load(step + 1);
+    float* state = reinterpret_cast<float*>(delta_segment(L, b, BACK ? steps - step : step, h));
+    f32x4 R[TILES];
+    chain_load_state<TILES>(R, state, L.dk, row, mine, g);
+    bf16x8 sh[KB], sl[KB];
+#pragma unroll
+    for (int j = 0; j < KB; ++j) split8(S[2 * j], S[2 * j + 1], sh[j], sl[j]);
+#pragma unroll
+    for (int t = 0; t < TILES; ++t) {
+      f32x4 s = {0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < KB; ++j) {
+        const int r = j * 32 + g * 8 + (c >> 2), block = (t >> 1) * 4 + (c & 3), half = (t & 1) * 8;
+        const int x = lds_block<DK>(r, block) + half, y = lds_block<DK>(r + 4, block) + half;
+        const uint8_t *ph = ps[step & 1][0], *pl = ps[step & 1][1];
+        s = mfma_split_split(lds_transposed(ph + x, ph + y), lds_transposed(pl + x, pl + y), sh[j], sl[j], s);
+      }
+      S[t] = R[t] + s;
+    }
+#pragma unroll
+    for (int t = 0; t < TILES; ++t) {
+      const int at = chain_row(t, g * 4);
+      if (mine && at < L.dk) *reinterpret_cast<f32x4*>(state + int64_t(row) * L.dk + at) = S[t];
+    }
+  }
+}
 
 #endif  // __HIPCC__
 

@@ -17,39 +17,51 @@ namespace {
 // product is the wave's own (see chain_row), the first ones (K, Q and the
 // triangles) come from LDS, where the workgroup puts the next chunk's while
 // this one's are used.
-template <int DK, bool SAVE, typename O>
+//   PASS: the first pass over segments, which has no outputs.
+template <int DK, bool SAVE, bool PASS, typename O>
 __global__ __launch_bounds__(256, 1) void delta_chain_kernel(DeltaLaunch L, int row_groups) {
   constexpr int KB = DK / 32, TILES = DK / 16;
   __shared__ __attribute__((aligned(1024))) ChainBuffer<DK> buffers[2];
-  const int h = blockIdx.x / row_groups % L.H, b = blockIdx.x / row_groups / L.H, group = blockIdx.x % row_groups;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-  const int col = group * 64 + wave * 16 + c;
-  const bool mine = col < L.dv;
+  const int per = row_groups * L.H * (L.segments - PASS), b = int(blockIdx.x) / per;
   const DeltaSpan s = delta_sequence(L, b);
   const int chunks = (s.tokens + 63) / 64;
+  const ChainPlace place = chain_place(L, row_groups, chunks, b, int(blockIdx.x) % per);
+  // a segment without chunks, or one that no other follows
+  if (place.seg > 0 && place.first >= chunks) return;
+  if (PASS && place.end >= chunks) return;
+  const int h = place.h, group = place.group, end = place.end;
+  const int col = group * 64 + wave * 16 + c;
+  const bool mine = col < L.dv;
   ChainLoader<DK> loader;
-  loader.init(L, L.v, h, group, wave, lane);
+  loader.init(L, L.v, h, PASS && place.identity ? 0 : group, wave, lane);
   const int64_t vrow = int64_t(L.H) * L.dv;
 
   f32x4 S[TILES];
   const int64_t state_row = ((int64_t(b) * L.H + h) * L.dv + col) * L.dk;
-#pragma unroll
-  for (int t = 0; t < TILES; ++t) {
-    const int at = chain_row(t, g * 4);
-    S[t] = f32x4{0, 0, 0, 0};
-    if (L.h0 && mine && at < L.dk) S[t] = *reinterpret_cast<const f32x4*>(L.h0 + state_row + at);
+  if constexpr (PASS) {
+    if (place.identity)
+      chain_identity<TILES>(S, col, g);
+    else
+      chain_load_state<TILES>(S, nullptr, L.dk, col, mine, g);
+  } else {
+    const float* start = L.h0 ? L.h0 + state_row - int64_t(col) * L.dk : nullptr;
+    if (place.seg > 0) start = reinterpret_cast<const float*>(delta_segment(L, b, place.seg - 1, h));
+    chain_load_state<TILES>(S, start, L.dk, col, mine, g);
   }
-  if (chunks > 0) loader.template load<false>(buffers[0], loader.next(s.first, min(64, s.tokens), s.slot));
+  if (place.first < end)
+    loader.template load<false>(buffers[place.first & 1], loader.next(s.first + int64_t(place.first) * 64,
+                                                                     min(64, s.tokens - place.first * 64), s.slot + place.first));
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
-  for (int chunk = 0; chunk < chunks; ++chunk) {
+  for (int chunk = place.first; chunk < end; ++chunk) {
     const ChainBuffer<DK>& buf = buffers[chunk & 1];
     const int64_t first = s.first + int64_t(chunk) * 64;
     const int n = min(64, s.tokens - chunk * 64);
     ChainBuffer<DK>& following = buffers[(chunk + 1) & 1];
     const auto next = loader.next(first + 64, min(64, s.tokens - chunk * 64 - 64), s.slot + chunk + 1);
-    const bool paced = next.n > 0 && next.whole;
-    if (next.n > 0 && !next.whole) loader.template load<false>(following, next);
+    const bool paced = chunk + 1 < end && next.whole;
+    if (chunk + 1 < end && !next.whole) loader.template load<false>(following, next);
     auto ahead = [&](auto step) {
       phase();
       if (paced) loader.template step<step.value>(following, next);
@@ -84,17 +96,28 @@ __global__ __launch_bounds__(256, 1) void delta_chain_kernel(DeltaLaunch L, int 
     f32x4 x[4] = {}, o[4] = {}, decay[4];
     s16x4 v[4];
     bf16x8 hi[2], lo[2], nh[TRI_BLOCKS], nl[TRI_BLOCKS];
-    each<2 * KB>([&](auto i) {
+    auto errors = [&](auto half) {
+#pragma unroll
+      for (int it = 2 * half.value; it < 2 * half.value + 2; ++it)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float value = PASS && place.identity ? 0.0f : bf16_value(v[it][e]);
+          x[it][e] = value - decay[it][e] * x[it][e];
+        }
+      split8(x[2 * half.value], x[2 * half.value + 1], hi[half.value], lo[half.value]);
+    };
+    constexpr int PRODUCTS = PASS ? KB : 2 * KB;
+    each<PRODUCTS>([&](auto i) {
       constexpr int j = i.value % KB;
-      if constexpr (i.value + 2 < 2 * KB) read(Int<i.value + 2>{});
-      if constexpr (i.value == KB - 1) {
+      if constexpr (i.value + 2 < PRODUCTS) read(Int<i.value + 2>{});
+      if constexpr (i.value == (PASS ? KB - 2 : KB - 1)) {
 #pragma unroll
         for (int it = 0; it < 4; ++it) {
           v[it] = chain_column(buf.v, it, wave, lane);
           decay[it] = row4(ROW_C, it);
         }
       }
-      if constexpr (i.value == 2 * KB - 2) chain_triangle(buf.tri, lane, nh, nl);
+      if constexpr (i.value == PRODUCTS - 2) chain_triangle(buf.tri, lane, nh, nl);
       phase();
       const bf16x8(&f)[4] = ring[i.value % 3];
       if constexpr (i.value < KB) {
@@ -108,18 +131,17 @@ __global__ __launch_bounds__(256, 1) void delta_chain_kernel(DeltaLaunch L, int 
 #pragma unroll
         for (int it = 0; it < 4; ++it) o[it] = mfma16(sh[j], f[it], o[it]);
       }
-      if constexpr (i.value >= 2 * KB - 2) {  // beside the last of these products
-        constexpr int half = i.value - (2 * KB - 2);
-#pragma unroll
-        for (int it = 2 * half; it < 2 * half + 2; ++it)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[it][e] = bf16_value(v[it][e]) - decay[it][e] * x[it][e];
-        split8(x[2 * half], x[2 * half + 1], hi[half], lo[half]);
-      }
+      if constexpr (!PASS && i.value >= 2 * KB - 2) errors(Int<i.value - (2 * KB - 2)>{});  // beside the last of these products
       // the loader's first KB + 2 steps
       if constexpr (i.value < KB) ahead(Int<i.value>{});
-      if constexpr (i.value >= 2 * KB - 2) ahead(Int<i.value - KB + 2>{});
+      if constexpr (!PASS && i.value >= 2 * KB - 2) ahead(Int<i.value - KB + 2>{});
     });
+    if constexpr (PASS) {
+      errors(Int<0>{});
+      errors(Int<1>{});
+      ahead(Int<KB>{});
+      ahead(Int<KB + 1>{});
+    }
     phase();
     bf16x8 kt[2][4][2];
     chain_columns<DK>(buf.k, lane, 0, kt[0]);
@@ -151,13 +173,15 @@ __global__ __launch_bounds__(256, 1) void delta_chain_kernel(DeltaLaunch L, int 
     phase();
     bf16x8 mh[TRI_BLOCKS], ml[TRI_BLOCKS], th[2], tl[2];
     if constexpr (TILES > 4) chain_columns<DK>(buf.k, lane, 1, kt[1]);
-    chain_triangle(buf.tri + TRI_BYTES, lane, mh, ml);
+    if constexpr (!PASS) chain_triangle(buf.tri + TRI_BYTES, lane, mh, ml);
     phase();
 #pragma unroll
     for (int j = 0; j < 2; ++j) split8(w[2 * j] * tail[2 * j], w[2 * j + 1] * tail[2 * j + 1], th[j], tl[j]);
     chain_update(S, kt[0], th, tl);
+    if constexpr (!PASS) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) split8(w[2 * j], w[2 * j + 1], hi[j], lo[j]);
+      for (int j = 0; j < 2; ++j) split8(w[2 * j], w[2 * j + 1], hi[j], lo[j]);
+    }
     ahead(Int<KB + 3>{});
     if constexpr (TILES > 4) chain_update(S + 4, kt[1], th, tl);
     ahead(Int<KB + 4>{});
@@ -167,9 +191,11 @@ __global__ __launch_bounds__(256, 1) void delta_chain_kernel(DeltaLaunch L, int 
 #pragma unroll
       for (int it = 2; it < 4; ++it) o[it] = mfma16(y[1], m[2 * it - 1], o[it]);
     };
-    inside(lo, mh);
-    inside(hi, ml);
-    inside(hi, mh);
+    if constexpr (!PASS) {
+      inside(lo, mh);
+      inside(hi, ml);
+      inside(hi, mh);
+    }
     phase();
     // the next chunk is in LDS, and nobody reads this one any more; the stores
     // below are behind this wait, so that the next chunk's covers them
@@ -186,7 +212,7 @@ __global__ __launch_bounds__(256, 1) void delta_chain_kernel(DeltaLaunch L, int 
       }
     }
     const int oc = group * 64 + wave * 16 + g * 4;
-    if (oc < L.dv) {
+    if (!PASS && oc < L.dv) {
       O* op = static_cast<O*>(L.o) + first * vrow + int64_t(h) * L.dv + oc;
       typedef O o4 __attribute__((ext_vector_type(4)));
 #pragma unroll
@@ -196,7 +222,8 @@ __global__ __launch_bounds__(256, 1) void delta_chain_kernel(DeltaLaunch L, int 
       }
     }
   }
-  if (L.h_last && mine) {
+  if constexpr (PASS) chain_leave<TILES>(L, place, S, col, g);
+  if (!PASS && L.h_last && mine && end == chunks) {
 #pragma unroll
     for (int t = 0; t < TILES; ++t) {
       const int at = chain_row(t, g * 4);
@@ -284,13 +311,20 @@ hipError_t forward(const DeltaLaunch& L, hipStream_t stream) {
     if (hipError_t e = hipGetLastError()) return e;
   }
   const int groups = (L.dv + 63) / 64;
-  const uint32_t grid = uint32_t(groups) * uint32_t(L.H) * uint32_t(L.B);
+  if (L.segments > 1) {
+    const int all = groups + (L.dk + 63) / 64;
+    delta_chain_kernel<DK, false, true, bf16><<<uint32_t(all * L.H * (L.segments - 1) * L.B), 256, 0, stream>>>(L, all);
+    if (hipError_t e = hipGetLastError()) return e;
+    delta_join_kernel<DK, false><<<uint32_t(groups * L.H * L.B), 256, 0, stream>>>(L, groups);
+    if (hipError_t e = hipGetLastError()) return e;
+  }
+  const uint32_t grid = uint32_t(groups) * uint32_t(L.H) * uint32_t(L.B) * uint32_t(L.segments);
   if (L.carry)
-    L.out_bf16 ? delta_chain_kernel<DK, true, bf16><<<grid, 256, 0, stream>>>(L, groups)
-               : delta_chain_kernel<DK, true, float><<<grid, 256, 0, stream>>>(L, groups);
+    L.out_bf16 ? delta_chain_kernel<DK, true, false, bf16><<<grid, 256, 0, stream>>>(L, groups)
+               : delta_chain_kernel<DK, true, false, float><<<grid, 256, 0, stream>>>(L, groups);
   else
-    L.out_bf16 ? delta_chain_kernel<DK, false, bf16><<<grid, 256, 0, stream>>>(L, groups)
-               : delta_chain_kernel<DK, false, float><<<grid, 256, 0, stream>>>(L, groups);
+    L.out_bf16 ? delta_chain_kernel<DK, false, false, bf16><<<grid, 256, 0, stream>>>(L, groups)
+               : delta_chain_kernel<DK, false, false, float><<<grid, 256, 0, stream>>>(L, groups);
   return hipGetLastError();
 }
 
@@ -319,10 +353,14 @@ hipError_t step_of(const DeltaLaunch& L, hipStream_t stream) {
 }  // namespace
 
 size_t delta_carry_bytes(const DeltaLaunch& L) { return size_t(delta_slots(L)) * L.H * delta_left_bytes(L); }
-size_t delta_forward_workspace_bytes(const DeltaLaunch& L) { return size_t(delta_slots(L)) * L.H * DELTA_CHUNK_BYTES; }
+static DeltaLaunch forward_split(DeltaLaunch L) {
+  delta_split(L, delta_slots(L) * L.H * DELTA_CHUNK_BYTES);
+  return L;
+}
+size_t delta_forward_workspace_bytes(const DeltaLaunch& L) { return size_t(delta_split_bytes(forward_split(L))); }
 
 hipError_t launch_delta_forward(const DeltaLaunch& L, hipStream_t stream) {
-  return L.dk <= 64 ? forward<64>(L, stream) : forward<128>(L, stream);
+  return L.dk <= 64 ? forward<64>(forward_split(L), stream) : forward<128>(forward_split(L), stream);
 }
 
 hipError_t launch_delta_step(const DeltaLaunch& L, hipStream_t stream) {

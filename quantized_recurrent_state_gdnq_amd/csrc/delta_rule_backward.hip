@@ -16,38 +16,47 @@ __host__ __device__ inline int64_t backward_left_at(const DeltaLaunch& L, int64_
 // ---------------------------------------------------------------- the chain of dS
 //
 // As the forward chain, from the last chunk to the first.
-template <int DK>
+template <int DK, bool PASS>
 __global__ __launch_bounds__(256, 1) void delta_chain_back_kernel(DeltaLaunch L, int row_groups, int64_t left_at) {
   constexpr int KB = DK / 32, TILES = DK / 16;
   __shared__ __attribute__((aligned(1024))) ChainBuffer<DK> buffers[2];
-  const int h = blockIdx.x / row_groups % L.H, b = blockIdx.x / row_groups / L.H, group = blockIdx.x % row_groups;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-  const int col = group * 64 + wave * 16 + c;
-  const bool mine = col < L.dv;
+  const int per = row_groups * L.H * L.segments, b = int(blockIdx.x) / per;
   const DeltaSpan s = delta_sequence(L, b);
   const int chunks = (s.tokens + 63) / 64;
+  const ChainPlace place = chain_place(L, row_groups, chunks, b, int(blockIdx.x) % per);
+  // a segment without chunks, or one that none comes before
+  if (place.seg > 0 && place.first >= chunks) return;
+  if (PASS && place.seg == 0) return;
+  const int h = place.h, group = place.group, count = place.end - place.first, last = place.end - 1;
+  const int col = group * 64 + wave * 16 + c;
+  const bool mine = col < L.dv && !(PASS && place.identity);
   ChainLoader<DK> loader;
-  loader.init(L, L.dout, h, group, wave, lane);
+  loader.init(L, L.dout, h, PASS && place.identity ? 0 : group, wave, lane);
 
   f32x4 S[TILES];  // dS^T
   const int64_t state_row = ((int64_t(b) * L.H + h) * L.dv + col) * L.dk;
-#pragma unroll
-  for (int t = 0; t < TILES; ++t) {
-    const int at = chain_row(t, g * 4);
-    S[t] = f32x4{0, 0, 0, 0};
-    if (L.dh_last && mine && at < L.dk) S[t] = *reinterpret_cast<const f32x4*>(L.dh_last + state_row + at);
+  if constexpr (PASS) {
+    if (place.identity)
+      chain_identity<TILES>(S, col, g);
+    else
+      chain_load_state<TILES>(S, nullptr, L.dk, col, mine, g);
+  } else {
+    const float* start = L.dh_last ? L.dh_last + state_row - int64_t(col) * L.dk : nullptr;
+    if (place.end < chunks) start = reinterpret_cast<const float*>(delta_segment(L, b, place.seg + 1, h));
+    chain_load_state<TILES>(S, start, L.dk, col, mine, g);
   }
-  if (chunks > 0)
-    loader.template load<true>(buffers[0], loader.next(s.first + int64_t(chunks - 1) * 64, s.tokens - (chunks - 1) * 64, s.slot + chunks - 1));
+  if (count > 0)
+    loader.template load<true>(buffers[0], loader.next(s.first + int64_t(last) * 64, min(64, s.tokens - last * 64), s.slot + last));
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
-  for (int done = 0; done < chunks; ++done) {
-    const int chunk = chunks - 1 - done;
+  for (int done = 0; done < count; ++done) {
+    const int chunk = last - done;
     const ChainBuffer<DK>& buf = buffers[done & 1];
     ChainBuffer<DK>& following = buffers[(done + 1) & 1];
     const auto next = loader.next(s.first + int64_t(chunk - 1) * 64, 64, s.slot + chunk - 1);
-    const bool paced = chunk > 0 && next.whole;
-    if (chunk > 0 && !next.whole) loader.template load<true>(following, next);
+    const bool paced = chunk > place.first && next.whole;
+    if (chunk > place.first && !next.whole) loader.template load<true>(following, next);
     auto ahead = [&](auto step) {
       phase();
       if (paced) loader.template step<step.value>(following, next);
@@ -64,7 +73,7 @@ __global__ __launch_bounds__(256, 1) void delta_chain_back_kernel(DeltaLaunch L,
     for (int j = 0; j < KB; ++j) {
       split8(S[2 * j], S[2 * j + 1], sh[j], sl[j]);
       const int at = j * 32 + g * 8;
-      if (mine && at < L.dk) {
+      if (!PASS && mine && at < L.dk) {
         *reinterpret_cast<bf16x8*>(left + col * L.dk + at) = sh[j];
         *reinterpret_cast<bf16x8*>(left + (L.dv + col) * L.dk + at) = sl[j];
       }
@@ -83,6 +92,7 @@ __global__ __launch_bounds__(256, 1) void delta_chain_back_kernel(DeltaLaunch L,
           const s16x4 d0 = chain_column(buf.v, 2 * j, wave, lane), d1 = chain_column(buf.v, 2 * j + 1, wave, lane);
           typedef short s16x8 __attribute__((ext_vector_type(8)));
           d[j] = __builtin_bit_cast(bf16x8, s16x8{d0[0], d0[1], d0[2], d0[3], d1[0], d1[1], d1[2], d1[3]});
+          if (PASS && place.identity) d[j] = bf16x8{};
         }
 #pragma unroll
         for (int it = 0; it < 4; ++it) {
@@ -159,13 +169,14 @@ __global__ __launch_bounds__(256, 1) void delta_chain_back_kernel(DeltaLaunch L,
     phase();
     chain_update(S, kt[0], hi, lo);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) split8(z[2 * j], z[2 * j + 1], zh[j], zl[j]);
+    for (int j = 0; j < 2; ++j)
+      if constexpr (!PASS) split8(z[2 * j], z[2 * j + 1], zh[j], zl[j]);
     ahead(Int<KB + 4>{});
     if constexpr (TILES > 4) chain_update(S + 4, kt[1], hi, lo);
     phase();
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    if (mine) {
+    if (!PASS && mine) {
       bf16* zp = left + 2 * L.dv * L.dk;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -174,7 +185,8 @@ __global__ __launch_bounds__(256, 1) void delta_chain_back_kernel(DeltaLaunch L,
       }
     }
   }
-  if (L.dh0 && mine) {
+  if constexpr (PASS) chain_leave<TILES>(L, place, S, col, g);
+  if (!PASS && L.dh0 && mine && place.seg == 0) {
 #pragma unroll
     for (int t = 0; t < TILES; ++t) {
       const int at = chain_row(t, g * 4);
@@ -625,7 +637,14 @@ hipError_t backward(const DeltaLaunch& L, hipStream_t stream) {
     if (hipError_t e = hipGetLastError()) return e;
   }
   const int groups = (L.dv + 63) / 64;
-  delta_chain_back_kernel<DK><<<uint32_t(groups) * uint32_t(L.H) * uint32_t(L.B), 256, 0, stream>>>(L, groups, left_at);
+  if (L.segments > 1) {
+    const int all = groups + (L.dk + 63) / 64;
+    delta_chain_back_kernel<DK, true><<<uint32_t(all * L.H * L.segments * L.B), 256, 0, stream>>>(L, all, left_at);
+    if (hipError_t e = hipGetLastError()) return e;
+    delta_join_kernel<DK, true><<<uint32_t(groups * L.H * L.B), 256, 0, stream>>>(L, groups);
+    if (hipError_t e = hipGetLastError()) return e;
+  }
+  delta_chain_back_kernel<DK, false><<<uint32_t(groups * L.H * L.segments) * uint32_t(L.B), 256, 0, stream>>>(L, groups, left_at);
   if (hipError_t e = hipGetLastError()) return e;
   const int64_t items = slots * L.G;
   if (items > 0) delta_gradient_kernel<DK><<<uint32_t(items < 256 ? items : 256), 1024, 0, stream>>>(L, left_at, int(items));
@@ -634,13 +653,15 @@ hipError_t backward(const DeltaLaunch& L, hipStream_t stream) {
 
 }  // namespace
 
-size_t delta_backward_workspace_bytes(const DeltaLaunch& L) {
+static DeltaLaunch backward_split(DeltaLaunch L) {
   const int64_t slots = delta_slots(L);
-  return size_t(backward_left_at(L, slots) + slots * L.H * delta_left_bytes(L));
+  delta_split(L, backward_left_at(L, slots) + slots * L.H * delta_left_bytes(L));
+  return L;
 }
+size_t delta_backward_workspace_bytes(const DeltaLaunch& L) { return size_t(delta_split_bytes(backward_split(L))); }
 
 hipError_t launch_delta_backward(const DeltaLaunch& L, hipStream_t stream) {
-  return L.dk <= 64 ? backward<64>(L, stream) : backward<128>(L, stream);
+  return L.dk <= 64 ? backward<64>(backward_split(L), stream) : backward<128>(backward_split(L), stream);
 }
 
 }  // namespace gdnq

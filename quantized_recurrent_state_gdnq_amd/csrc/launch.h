@@ -172,6 +172,10 @@ struct DeltaLaunch {
   int B, T, G, H, dk, dv;
   int64_t N;        // tokens of the call
   int row_groups;
+  // Long sequences in few heads: SEG chunks a segment, up to `segments` of a sequence (1: not split),
+  // and where the workspace holds what passes between them.
+  int seg_chunks, segments;
+  int64_t seg_at;
   bool in_bf16, out_bf16, log_decay;
 };
 size_t delta_carry_bytes(const DeltaLaunch& L);

@@ -211,6 +211,23 @@ def test_long():
     check((1, 2500), 1, 2, 128, 128, log=True)
 
 
+# few heads of many tokens are cut into segments that run at once: what passes
+# between them is a product more (of 64 decays near 1, so that it matters)
+@pytest.mark.parametrize("G,H,dk,dv", [(32, 64, 72, 24), (64, 64, 128, 64), (16, 64, 64, 8)])
+def test_segments(G, H, dk, dv):
+    check((1, 2111), G, H, dk, dv, decay=-7.0, log=True, scale=2.0)
+
+
+@pytest.mark.parametrize("lengths", [[0, 2500, 70, 1100], [40, 3000, 0, 1], [600, 700, 64, 900]])
+def test_packed_segments(lengths):
+    check((sum(lengths) + 3,), 8, 16, 64, 40, lengths=lengths, start=2, decay=-7.0, scale=2.0)
+
+
+@pytest.mark.parametrize("state,dh", [(False, True), (True, False)])
+def test_segments_without_states(state, dh):
+    check((1, 2200), 64, 64, 16, 16, decay=-7.0, state=state, dh=dh, scale=2.0)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("B,G,H,dk,dv", [(1, 1, 1, 64, 64), (3, 2, 6, 128, 128), (2, 1, 2, 72, 40), (2, 1, 1, 256, 8),
                                          (40, 4, 8, 128, 136), (5, 1, 1, 8, 1024), (1, 1, 1, 136, 64)])

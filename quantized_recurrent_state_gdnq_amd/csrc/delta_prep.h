@@ -9,58 +9,54 @@
 
 namespace gdnq {
 
-// D += A B of 16 x 16 fp32 tiles in LDS (A) and in result layout (B): the
-// contraction index of step s is 4 g + s, which a result tile holds in register s.
-constexpr int PREP_PITCH = 68;
+// A lower triangle of 64 x 64 fp32 in LDS: its ten 16 x 16 tiles, rows of 20.
+constexpr int PREP_PITCH = 20, PREP_TILE = 16 * PREP_PITCH, PREP_FLOATS = 10 * PREP_TILE;
+__device__ __forceinline__ constexpr int prep_tile(int it, int jt) { return (it * (it + 1) / 2 + jt) * PREP_TILE; }
+
+// D += A B of such tiles: A in LDS, B in result layout; the contraction index of
+// step s is 4 g + s, which a result tile holds in register s.
 __device__ __forceinline__ f32x4 tile_product(const float* a, const f32x4& b, f32x4 d, int lane) {
-  const int r = lane & 15, g = lane >> 4;
-  const f32x4 x = *reinterpret_cast<const f32x4*>(a + r * PREP_PITCH + g * 4);
+  const f32x4 x = *reinterpret_cast<const f32x4*>(a + (lane & 15) * PREP_PITCH + (lane >> 4) * 4);
 #pragma unroll
   for (int s = 0; s < 4; ++s) d = __builtin_amdgcn_mfma_f32_16x16x4f32(x[s], b[s], d, 0, 0, 0);
   return d;
 }
 __device__ __forceinline__ f32x4 load_tile(const float* a, int lane) {
-  const int c = lane & 15, g = lane >> 4;
   f32x4 x;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) x[e] = a[(4 * g + e) * PREP_PITCH + c];
+  for (int e = 0; e < 4; ++e) x[e] = a[(4 * (lane >> 4) + e) * PREP_PITCH + (lane & 15)];
   return x;
 }
 __device__ __forceinline__ void store_tile(float* a, const f32x4& x, int lane, float sign) {
-  const int c = lane & 15, g = lane >> 4;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) a[(4 * g + e) * PREP_PITCH + c] = sign * x[e];
+  for (int e = 0; e < 4; ++e) a[(4 * (lane >> 4) + e) * PREP_PITCH + (lane & 15)] = sign * x[e];
 }
 
-// (I + a)^-1 of a strictly lower triangle in LDS into n (zero above the
-// diagonal), fp32: the diagonal 16 x 16 blocks by substitution, a lane per
-// column, then [n1 0; -n2 a21 n1, n2] twice.
+// (I + a)^-1 of a strictly lower triangle into n, fp32: the diagonal tiles by
+// substitution, a lane per column, then [n1 0; -n2 a21 n1, n2] twice.
 __device__ __forceinline__ void invert_triangle(const float* a, float* n, int wave, int lane) {
-  constexpr int P = PREP_PITCH;
   if (lane < 16) {
-    const float* block = a + wave * 16 * (P + 1);
-    float* to = n + wave * 16 * (P + 1);
+    const float* block = a + prep_tile(wave, wave);
+    float* to = n + prep_tile(wave, wave) + lane;
     float x[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
+      float row[16];
+#pragma unroll
+      for (int j = 0; j < i; j += 4) *reinterpret_cast<f32x4*>(row + j) = *reinterpret_cast<const f32x4*>(block + i * PREP_PITCH + j);
       float sum = i == lane ? 1.0f : 0.0f;
 #pragma unroll
-      for (int j = 0; j < i; ++j) sum = fmaf(-block[i * P + j], x[j], sum);
+      for (int j = 0; j < i; ++j) sum = fmaf(-row[j], x[j], sum);
       x[i] = sum;
-      to[i * P + lane] = sum;
+      to[i * PREP_PITCH] = sum;
     }
-  }
-  if (wave >= 2) {  // the tiles above the diagonal that are read
-    float* to = n + (wave - 2) * (32 * P + 32) + 16;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) to[(lane / 16 * 4 + e) * P + lane % 16] = 0.0f;
   }
   __syncthreads();
   if (wave < 2) {
-    const int at = wave * 32;
-    f32x4 p = tile_product(a + (at + 16) * P + at, load_tile(n + at * P + at, lane), f32x4{0, 0, 0, 0}, lane);
-    p = tile_product(n + (at + 16) * P + at + 16, p, f32x4{0, 0, 0, 0}, lane);
-    store_tile(n + (at + 16) * P + at, p, lane, -1.0f);
+    const int t = wave * 2;
+    f32x4 p = tile_product(a + prep_tile(t + 1, t), load_tile(n + prep_tile(t, t), lane), f32x4{0, 0, 0, 0}, lane);
+    p = tile_product(n + prep_tile(t + 1, t + 1), p, f32x4{0, 0, 0, 0}, lane);
+    store_tile(n + prep_tile(t + 1, t), p, lane, -1.0f);
   }
   __syncthreads();
   const int rt = 2 + (wave >> 1), ct = wave & 1;
@@ -72,18 +68,35 @@ __device__ __forceinline__ void invert_triangle(const float* a, float* n, int wa
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       if (k < ct) continue;
-      p = tile_product(a + m * 16 * P + k * 16, load_tile(n + k * 16 * P + ct * 16, lane), p, lane);
+      p = tile_product(a + prep_tile(m, k), load_tile(n + prep_tile(k, ct), lane), p, lane);
     }
-    sum = tile_product(n + rt * 16 * P + m * 16, p, sum, lane);
+    sum = tile_product(n + prep_tile(rt, m), p, sum, lane);
   }
-  store_tile(n + rt * 16 * P + ct * 16, sum, lane, -1.0f);
+  store_tile(n + prep_tile(rt, ct), sum, lane, -1.0f);
   __syncthreads();
+}
+
+// Inclusive prefix sum of the lanes in 64 bits, as wave_scan_incl.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_rows64(double x) {
+  const int2 v = __builtin_bit_cast(int2, x);
+  return __builtin_bit_cast(double, int2{__builtin_amdgcn_update_dpp(0, v.x, CTRL, ROWS, 0xF, false),
+                                         __builtin_amdgcn_update_dpp(0, v.y, CTRL, ROWS, 0xF, false)});
+}
+__device__ __forceinline__ double wave_scan64(double x) {
+  x += dpp_rows64<0x111, 0xF>(x);
+  x += dpp_rows64<0x112, 0xF>(x);
+  x += dpp_rows64<0x114, 0xF>(x);
+  x += dpp_rows64<0x118, 0xF>(x);
+  x += dpp_rows64<0x142, 0xA>(x);
+  x += dpp_rows64<0x143, 0xC>(x);
+  return x;
 }
 
 template <int DK, bool BACK>
 __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaLaunch L) {
-  constexpr int P = PREP_PITCH, KB = DK / 32;
-  __shared__ __attribute__((aligned(16))) float a[64 * P], m[64 * P], n[64 * P];
+  constexpr int KB = DK / 32;
+  __shared__ __attribute__((aligned(16))) float a[PREP_FLOATS], n[PREP_FLOATS];
   __shared__ float rest[64], beta[64];
   __shared__ int whole[64];
   const int slot = int(blockIdx.x) / L.H;
@@ -107,11 +120,7 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaLaunch L) {
       x = x < -64.0 ? -64.0 : x;
       bt = L.beta[at];
     }
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const double y = __shfl_up(x, d);
-      if (lane >= d) x += y;
-    }
+    x = wave_scan64(x);
     const double w = rint(x);
     const float r = float(x - w);
     const int wi = int(w);
@@ -149,27 +158,33 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaLaunch L) {
     }
   }
   __syncthreads();
+  f32x4 m[4];
 #pragma unroll
   for (int jt = 0; jt < 4; ++jt) {
-    if (jt > (wave | 1)) break;  // with the tile above the diagonal that is read
+    if (jt > wave) break;
     const int j = jt * 16 + c;
+    f32x4 at;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int i = wave * 16 + g * 4 + e;
-      float rho = 0.0f;
-      if (j <= i) rho = exp2_difference(rest[i], whole[i], rest[j], whole[j]);
-      m[i * P + j] = BACK ? rho * qk[jt][e] : rho * qk[jt][e] * beta[j];
-      a[i * P + j] = j < i ? rho * kk[jt][e] * beta[BACK ? i : j] : 0.0f;
+      const float rho = j <= i ? exp2_difference(rest[i], whole[i], rest[j], whole[j]) : 0.0f;
+      m[jt][e] = BACK ? rho * qk[jt][e] : rho * qk[jt][e] * beta[j];
+      at[e] = j < i ? rho * kk[jt][e] * beta[BACK ? i : j] : 0.0f;
     }
+    store_tile(a + prep_tile(wave, jt), at, lane, 1.0f);
   }
   __syncthreads();
   invert_triangle(a, n, wave, lane);
+#pragma unroll
+  for (int jt = 0; jt < 4; ++jt)
+    if (jt <= wave) store_tile(a + prep_tile(wave, jt), m[jt], lane, 1.0f);  // M in a's place
+  __syncthreads();
 
   // Out as first operands: six blocks of each, rows in the chains' order.
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
     const int f = wave * 3 + i, block = f % TRI_BLOCKS;
-    const float* from = f < TRI_BLOCKS ? n : m;
+    const float* from = f < TRI_BLOCKS ? n : a;
     int it, j;
     if (!BACK) {
       it = block < 2 ? block : (block + 2) / 2;
@@ -181,7 +196,10 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaLaunch L) {
     const int row = chain_row(it, c), at = j * 32 + g * 8;
     float x[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = BACK ? from[(at + e) * P + row] : from[row * P + at + e];
+    for (int e = 0; e < 8; ++e) {
+      const int r = BACK ? at + e : row, k = BACK ? row : at + e;  // at + e all lie in one tile
+      x[e] = (at >> 4) > (row >> 4) == BACK || (at >> 4) == (row >> 4) ? from[prep_tile(r >> 4, k >> 4) + (r & 15) * PREP_PITCH + (k & 15)] : 0.0f;
+    }
     bf16x8 hi, lo;
     split2(x, hi, lo);
     uint8_t* to = out + (f < TRI_BLOCKS ? 0 : TRI_BYTES) + block * 1024 + lane * 16;

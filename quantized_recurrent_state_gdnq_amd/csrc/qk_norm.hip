@@ -26,7 +26,17 @@ namespace gdnq {
 namespace {
 
 constexpr int THREADS = 256;
-enum { NONE = 0, PAIRS = 1, HALVES = 2, LANES = 3 };  // how partners lie: none, 2i and 2i+1, through LDS, in another lane
+// How partners lie: none, 2i and 2i+1, through LDS, in another lane, and in the
+// lane half a team away where the whole row turns and fills the team.
+enum { NONE = 0, PAIRS = 1, HALVES = 2, LANES = 3, WHOLE = 4 };
+
+// The value of lane l ^ (TEAM / 2).
+template <int TEAM>
+__device__ __forceinline__ float across(float x) {
+  if constexpr (TEAM == 8) return dpp<0x1B>(dpp<DPP_ROW_HALF_MIRROR>(x));  // 7 - l, then reversed in its four
+  if constexpr (TEAM == 16) return dpp<0x128>(x);                          // the row of 16 turned by 8
+  return __shfl_xor(x, TEAM / 2);
+}
 
 // The turn of position p: angle = p f is exact or nearly so in 64 bits, and is
 // brought into [-pi, pi] there; the rest is rounded to fp32 once.
@@ -39,20 +49,18 @@ __device__ __forceinline__ void turn(double angle, float& c, float& s) {
 template <typename E, int TEAM, bool WIDE>
 struct Row {
   static __device__ __forceinline__ int column(int l, int j) { return WIDE ? l * 8 + j : j * TEAM + l; }
-  static __device__ __forceinline__ void load(const E* p, int l, int D, float (&v)[8]) {
+  // as they are in memory; outside the row 0
+  static __device__ __forceinline__ void fetch(const E* p, int l, int D, E (&x)[8]) {
     if constexpr (WIDE) {
-      E x[8];
       if (l * 8 < D) {
         __builtin_memcpy(x, __builtin_assume_aligned(p + l * 8, 16), sizeof(x));
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] = E(0.0f);
       }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = to_f32(x[j]);
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = column(l, j) < D ? to_f32(p[column(l, j)]) : 0.0f;
+      for (int j = 0; j < 8; ++j) x[j] = column(l, j) < D ? p[column(l, j)] : E(0.0f);
     }
   }
   static __device__ __forceinline__ void store(E* p, int l, int D, const float (&v)[8]) {
@@ -78,6 +86,13 @@ struct Row {
 template <int TEAM, bool WIDE, int MODE, typename R>
 __device__ __forceinline__ void rotate(float (&v)[8], int l, int r, const float* cs, const float* sn, float sign, float* box) {
   if constexpr (MODE == NONE) return;
+  if constexpr (MODE == WHOLE) {
+    const int pair = (l & (TEAM / 2 - 1)) * 8;
+    const float s = l < TEAM / 2 ? -sign : sign;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = fmaf(v[j], cs[pair + j], sn[pair + j] * s * across<TEAM>(v[j]));
+    return;
+  }
   const int half = r / 2;
   float other[8];
   if constexpr (MODE == PAIRS) {
@@ -117,6 +132,16 @@ __device__ __forceinline__ void rotate(float (&v)[8], int l, int r, const float*
   }
 }
 
+// The rows of a workgroup's tokens, `heads` each, in turns of `teams`.
+struct Units {
+  int token, h;
+  __device__ __forceinline__ Units(int team, int heads) : token(team / heads), h(team % heads) {}
+  __device__ __forceinline__ void next(int teams, int heads) {
+    h += teams;
+    while (h >= heads) h -= heads, ++token;
+  }
+};
+
 // The tokens' tables, [token][pair].
 __device__ __forceinline__ void tables(const QkLaunch& L, int64_t first, int tokens, float* cs, float* sn) {
   const int half = L.rotary / 2;
@@ -142,27 +167,40 @@ __global__ __launch_bounds__(THREADS) void qk_forward_kernel(QkLaunch L) {
     tables(L, first, tokens, cs, sn);
     __syncthreads();
   }
-  const int heads = L.Hq + L.Hk, units = tokens * heads;
+  const int heads = L.Hq + L.Hk;
   const float scale = L.l2 ? 1.0f : 1.0f / D;
   float wq[8], wk[8];
   R::weights(L.q_weight, l, D, wq);
   R::weights(L.k_weight, l, D, wk);
-  for (int u = team; u < units; u += TEAMS) {
-    const int token = u / heads, h = u % heads;
-    const bool is_q = h < L.Hq;
-    const int64_t row = first + token;
-    const E* from = is_q ? static_cast<const E*>(L.q) + row * L.q_stride + int64_t(h) * D
-                         : static_cast<const E*>(L.k) + row * L.k_stride + int64_t(h - L.Hq) * D;
-    E* to = is_q ? static_cast<E*>(L.q_out) + (row * L.Hq + h) * D : static_cast<E*>(L.k_out) + (row * L.Hk + h - L.Hq) * D;
+  auto from = [&](const Units& u) {
+    return u.h < L.Hq ? static_cast<const E*>(L.q) + (first + u.token) * L.q_stride + u.h * D
+                      : static_cast<const E*>(L.k) + (first + u.token) * L.k_stride + (u.h - L.Hq) * D;
+  };
+  // a row is loaded while the one before is worked on
+  Units u(team, heads);
+  E x[8], ahead[8];
+  if (u.token < tokens) R::fetch(from(u), l, D, x);
+  while (u.token < tokens) {
+    Units n = u;
+    n.next(TEAMS, heads);
+    if (n.token < tokens) R::fetch(from(n), l, D, ahead);
+    const bool is_q = u.h < L.Hq;
     float v[8], s = 0.0f;
-    R::load(from, l, D, v);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s = fmaf(v[j], v[j], s);
+    for (int j = 0; j < 8; ++j) {
+      v[j] = to_f32(x[j]);
+      s = fmaf(v[j], v[j], s);
+    }
     const float rstd = 1.0f / sqrtf(fmaf(group_sum<TEAM>(s), scale, L.eps));
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = v[j] * rstd * (is_q ? wq[j] : wk[j]);
-    rotate<TEAM, WIDE, MODE, R>(v, l, L.rotary, cs + token * (L.rotary / 2), sn + token * (L.rotary / 2), 1.0f, box);
-    R::store(to, l, D, v);
+    rotate<TEAM, WIDE, MODE, R>(v, l, L.rotary, cs + u.token * (L.rotary / 2), sn + u.token * (L.rotary / 2), 1.0f, box);
+    const int64_t row = first + u.token;
+    R::store(is_q ? static_cast<E*>(L.q_out) + (row * L.Hq + u.h) * D : static_cast<E*>(L.k_out) + (row * L.Hk + u.h - L.Hq) * D,
+             l, D, v);
+    u = n;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = ahead[j];
   }
 }
 
@@ -188,23 +226,27 @@ __global__ __launch_bounds__(THREADS) void qk_backward_kernel(QkLaunch L, float*
     }
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
-      const int heads = which ? L.Hk : L.Hq, units = tokens * heads;
+      const int heads = which ? L.Hk : L.Hq;
       const int64_t stride = which ? L.k_stride : L.q_stride;
-      const E* x = static_cast<const E*>(which ? L.k : L.q);
-      const E* dy = static_cast<const E*>(which ? L.dk_out : L.dq_out);
-      E* dx = static_cast<E*>(which ? L.dk : L.dq);
+      const E* x = static_cast<const E*>(which ? L.k : L.q) + first * stride;
+      const E* dy = static_cast<const E*>(which ? L.dk_out : L.dq_out) + first * heads * D;
+      E* dx = static_cast<E*>(which ? L.dk : L.dq) + first * heads * D;
       float w[8];
       R::weights(which ? L.k_weight : L.q_weight, l, D, w);
-      for (int u = team; u < units; u += TEAMS) {
-        const int token = u / heads, h = u % heads;
-        const int64_t row = first + token, at = (row * heads + h) * D;
+      Units u(team, heads);
+      for (; u.token < tokens; u.next(TEAMS, heads)) {
+        E x8[8], d8[8];
+        R::fetch(x + u.token * stride + u.h * D, l, D, x8);
+        R::fetch(dy + (u.token * heads + u.h) * D, l, D, d8);
         float v[8], d[8], s = 0.0f, inner = 0.0f;
-        R::load(x + row * stride + int64_t(h) * D, l, D, v);
-        R::load(dy + at, l, D, d);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s = fmaf(v[j], v[j], s);
+        for (int j = 0; j < 8; ++j) {
+          v[j] = to_f32(x8[j]);
+          d[j] = to_f32(d8[j]);
+          s = fmaf(v[j], v[j], s);
+        }
         const float rstd = 1.0f / sqrtf(fmaf(group_sum<TEAM>(s), scale, L.eps));
-        rotate<TEAM, WIDE, MODE, R>(d, l, L.rotary, cs + token * (L.rotary / 2), sn + token * (L.rotary / 2), -1.0f, box);
+        rotate<TEAM, WIDE, MODE, R>(d, l, L.rotary, cs + u.token * (L.rotary / 2), sn + u.token * (L.rotary / 2), -1.0f, box);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           v[j] *= rstd;
@@ -215,7 +257,7 @@ __global__ __launch_bounds__(THREADS) void qk_backward_kernel(QkLaunch L, float*
         inner = group_sum<TEAM>(inner) * scale;
 #pragma unroll
         for (int j = 0; j < 8; ++j) d[j] = rstd * fmaf(-v[j], inner, d[j]);
-        R::store(dx + at, l, D, d);
+        R::store(dx + (u.token * heads + u.h) * D, l, D, d);
       }
     }
   }
@@ -258,7 +300,7 @@ __global__ __launch_bounds__(1024) void qk_weights_kernel(const float* __restric
   if (r == 0 && c < cols) out[c] = part[0][i];
 }
 
-constexpr int MAX_GRID = 2048;  // of the backward pass: rows of partial sums
+constexpr int MAX_GRID = 1024;  // of the backward pass, as many as the CUs hold: rows of partial sums
 
 // Tokens of a workgroup: more share a launch's fixed costs and the table's
 // barrier, fewer spread a small call over the chip; the table fits 16 KB.
@@ -295,6 +337,7 @@ hipError_t by_mode(const QkLaunch& L, bool back, hipStream_t s) {
   if (L.rotary == 0) return go<E, TEAM, WIDE, NONE>(L, back, s);
   if (L.interleaved) return go<E, TEAM, WIDE, PAIRS>(L, back, s);
   if constexpr (WIDE) {
+    if (L.rotary == 8 * TEAM) return go<E, TEAM, WIDE, WHOLE>(L, back, s);
     if (L.rotary % 16 == 0) return go<E, TEAM, WIDE, LANES>(L, back, s);
   }
   return go<E, TEAM, WIDE, HALVES>(L, back, s);

@@ -9,6 +9,7 @@ raw pointers to the library.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -890,35 +891,46 @@ def mx_linear(x, w_codes, w_scales, *, out_dtype=None, y=None, workspace=None):
 # ---------------------------------------------------------------- the delta rule with its state in fp32
 
 
-def _delta_setup(q, k, v, alpha, beta, cu_seqlens, log_decay, out_dtype, dtypes=(torch.bfloat16,)):
+@functools.lru_cache(maxsize=512)
+def _delta_form(q_shape, v_shape, dtype, out_dtype, log_decay, sequences, step):
+    """What follows from sizes, types and flags alone: the call's parameters and
+    the shapes of its gates and states.  sequences: those of a packed call, else
+    None."""
+    if dtype not in _DT or not (step or dtype == torch.bfloat16):
+        raise ValueError(f"q must be bfloat16{' or float32' if step else ''}, got {dtype}")
+    if out_dtype not in _DT:
+        raise ValueError("out_dtype must be float32 or bfloat16")
+    dims = 3 if step or sequences is not None else 4
+    if len(q_shape) != dims or len(v_shape) != dims or q_shape[:-2] != v_shape[:-2]:
+        raise ValueError("q must be [B,T,G,d_k] and v [B,T,H,d_v], or [T,..] with cu_seqlens (one token: [B,..])")
+    (G, d_k), (H, d_v) = q_shape[-2:], v_shape[-2:]
+    B, T = (sequences, q_shape[0]) if sequences is not None else (q_shape[0], 1 if step else q_shape[1])
+    _sizes(B, T)
+    _sizes(G, H, max(d_k, d_v))
+    p = _lib.DeltaParams(B, T, G, H, d_k, d_v, _DT[dtype], _DT[out_dtype], _lib.GDNQ_DELTA_LOG if log_decay else 0)
+    return p, torch.Size(v_shape[:-1]), torch.Size((B, H, d_v, d_k))
+
+
+def _delta_setup(q, k, v, alpha, beta, cu_seqlens, log_decay, out_dtype, step=False):
     """The checks every delta rule call shares: its parameters and the shape
     of its states."""
     _need(q, "q", None, None)
+    if v is None:
+        raise ValueError("v is required")
     dev = q.device
-    if q.dtype not in dtypes:
-        raise ValueError(f"q must be one of {[str(d) for d in dtypes]}, got {q.dtype}")
-    if out_dtype not in _DT:
-        raise ValueError("out_dtype must be float32 or bfloat16")
-    step = len(dtypes) > 1
-    packed = cu_seqlens is not None
-    dims = 3 if step or packed else 4
-    if q.dim() != dims or v.dim() != dims:
-        raise ValueError("q must be [B,T,G,d_k] and v [B,T,H,d_v], or [T,..] with cu_seqlens (one token: [B,..])")
-    if packed:
+    sequences = None
+    if cu_seqlens is not None:
         _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
         if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
             raise ValueError("cu_seqlens: one dimension of B+1 offsets")
-    lead, (G, d_k), (H, d_v) = q.shape[:-2], q.shape[-2:], v.shape[-2:]
-    _checked(k, "k", q.dtype, dev, q.shape)
-    _checked(v, "v", q.dtype, dev, lead + (H, d_v))
-    _checked(alpha, "alpha", torch.float32, dev, lead + (H,))
-    _checked(beta, "beta", torch.float32, dev, lead + (H,))
-    B, T = (cu_seqlens.numel() - 1, q.shape[0]) if packed else (q.shape[0], 1 if step else q.shape[1])
-    _sizes(B, T)
-    _sizes(G, H, max(d_k, d_v))
-    p = _lib.DeltaParams(B, T, G, H, d_k, d_v, _DT[q.dtype], _DT[out_dtype],
-                         _lib.GDNQ_DELTA_LOG if log_decay else 0)
-    return p, (B, H, d_v, d_k), packed
+        sequences = cu_seqlens.numel() - 1
+    dtype, shape = q.dtype, q.shape
+    p, gates, states = _delta_form(shape, v.shape, dtype, out_dtype, log_decay, sequences, step)
+    _checked(k, "k", dtype, dev, shape)
+    _checked(v, "v", dtype, dev, v.shape)
+    _checked(alpha, "alpha", torch.float32, dev, gates)
+    _checked(beta, "beta", torch.float32, dev, gates)
+    return p, states, sequences is not None
 
 
 def delta_rule_workspace_size(q, v, cu_seqlens=None, *, backward=False):
@@ -996,7 +1008,7 @@ def delta_rule_step(q, k, v, alpha, beta, h, *, log_decay=False, out_dtype=None,
     in place unless h_out is given.  Returns o [B,H,d_v] like v, or of
     out_dtype."""
     out_dtype = out_dtype or (v.dtype if o is None else o.dtype)
-    p, states, _ = _delta_setup(q, k, v, alpha, beta, None, log_decay, out_dtype, (torch.float32, torch.bfloat16))
+    p, states, _ = _delta_setup(q, k, v, alpha, beta, None, log_decay, out_dtype, True)
     dev = q.device
     _checked(h, "h", torch.float32, dev, states)
     h_out = h if h_out is None else _checked(h_out, "h_out", torch.float32, dev, states)
@@ -1011,26 +1023,23 @@ def delta_rule_step(q, k, v, alpha, beta, h, *, log_decay=False, out_dtype=None,
 
 
 def _head_rows(t, name, dtype, dev):
-    """A tensor [..,heads,width] whose rows [heads,width] are dense and evenly
-    apart, as views of a fused projection's rows are: (leading shape, rows,
-    elements from row to row)."""
+    """Elements from row to row of a tensor [..,heads,width] whose rows
+    [heads,width] are dense and evenly apart, as views of a fused projection's
+    rows are."""
     if t is None:
         raise ValueError(f"{name} is required")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a GPU tensor")
     if t.dtype != dtype or t.device != dev:
         raise ValueError(f"{name} must be {dtype} on {dev}, got {t.dtype} on {t.device}")
     if t.dim() < 2:
         raise ValueError(f"{name} must be [..,heads,width]")
     H, D = t.shape[-2:]
-    lead, strides = t.shape[:-2], t.stride()
     if t.is_contiguous():
-        rows = 1
-        for s in lead:
-            rows *= s
-        return lead, rows, H * D
+        return H * D
+    strides = t.stride()
+    if (D > 1 and strides[-1] != 1) or (H > 1 and strides[-2] != D):
+        raise ValueError(f"{name}: its heads must be dense")
     rows, step = 1, None
-    for size, stride in zip(reversed(lead), reversed(strides[:-2])):
+    for size, stride in zip(reversed(t.shape[:-2]), reversed(strides[:-2])):
         if size == 1:
             continue
         if step is None:
@@ -1038,47 +1047,55 @@ def _head_rows(t, name, dtype, dev):
         elif stride != step * rows:
             raise ValueError(f"{name}: its rows must be evenly apart")
         rows *= size
-    if (D > 1 and strides[-1] != 1) or (H > 1 and strides[-2] != D):
-        raise ValueError(f"{name}: its heads must be dense")
-    return lead, rows, H * D if step is None else step
+    return H * D if step is None else step
+
+
+@functools.lru_cache(maxsize=512)
+def _qk_form(q_shape, k_shape, dtype, rotary, norm, eps, interleaved, pos64, q_stride, k_stride):
+    """What follows from sizes, types and flags alone."""
+    if dtype not in _DT:
+        raise ValueError("q must be float32 or bfloat16")
+    if norm not in ("rms", "l2"):
+        raise ValueError(f"norm must be 'rms' or 'l2', got {norm!r}")
+    if k_shape[:-2] != q_shape[:-2] or k_shape[-1] != q_shape[-1]:
+        raise ValueError(f"k must be {tuple(q_shape[:-2])} + [heads,{q_shape[-1]}], got {tuple(k_shape)}")
+    rows = 1
+    for s in q_shape[:-2]:
+        rows *= s
+    Hq, Hk, D = q_shape[-2], k_shape[-2], q_shape[-1]
+    _sizes(rows, Hq, Hk)
+    _sizes(D, rotary)
+    flags = ((_lib.GDNQ_QK_L2 if norm == "l2" else 0) | (_lib.GDNQ_QK_INTERLEAVED if interleaved else 0)
+             | (_lib.GDNQ_QK_POS64 if pos64 else 0))
+    return (_lib.QkParams(rows, Hq, Hk, D, rotary, _DT[dtype], eps, flags, q_stride, k_stride),
+            torch.Size(q_shape[:-2]), torch.Size((D,)))
 
 
 def _qk_setup(q, k, q_weight, k_weight, positions, inv_freq, norm, eps, interleaved):
     """The checks the forward and backward calls share."""
     if q is None or not q.is_cuda:
         raise ValueError("q must be a GPU tensor")
-    dev = q.device
-    if q.dtype not in _DT:
-        raise ValueError("q must be float32 or bfloat16")
-    if norm not in ("rms", "l2"):
-        raise ValueError(f"norm must be 'rms' or 'l2', got {norm!r}")
-    lead, rows, q_stride = _head_rows(q, "q", q.dtype, dev)
-    k_lead, _, k_stride = _head_rows(k, "k", q.dtype, dev)
-    D = q.shape[-1]
-    if k_lead != lead or k.shape[-1] != D:
-        raise ValueError(f"k must be {tuple(lead)} + [heads,{D}], got {tuple(k.shape)}")
-    for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
-        _optional(t, name, torch.float32, dev, (D,))
+    dev, dtype = q.device, q.dtype
+    q_stride, k_stride = _head_rows(q, "q", dtype, dev), _head_rows(k, "k", dtype, dev)
     if (positions is None) != (inv_freq is None):
         raise ValueError("positions and inv_freq: both or neither")
-    rotary = flags = 0
+    rotary, pos64 = 0, False
     if positions is not None:
-        if positions.dtype not in (torch.int32, torch.int64):
+        pos64 = positions.dtype == torch.int64
+        if not pos64 and positions.dtype != torch.int32:
             raise ValueError("positions must be int32 or int64")
-        _checked(positions, "positions", positions.dtype, dev, lead)
         _need(inv_freq, "inv_freq", torch.float32, dev)
         if inv_freq.dim() != 1:
             raise ValueError("inv_freq: one dimension, a value for every pair of rotated columns")
         rotary = 2 * inv_freq.numel()
-        if positions.dtype == torch.int64:
-            flags = _lib.GDNQ_QK_POS64
+    p, lead, width = _qk_form(q.shape, k.shape, dtype, rotary, norm, eps, interleaved, pos64, q_stride, k_stride)
+    if positions is not None:
+        _checked(positions, "positions", positions.dtype, dev, lead)
         if rotary == 0:  # nothing turns
             positions = inv_freq = None
-    flags |= (_lib.GDNQ_QK_L2 if norm == "l2" else 0) | (_lib.GDNQ_QK_INTERLEAVED if interleaved else 0)
-    _sizes(rows, q.shape[-2], k.shape[-2])
-    _sizes(D, rotary)
-    return _lib.QkParams(rows, q.shape[-2], k.shape[-2], D, rotary, _DT[q.dtype], eps, flags, q_stride, k_stride), \
-        positions, inv_freq
+    _optional(q_weight, "q_weight", torch.float32, dev, width)
+    _optional(k_weight, "k_weight", torch.float32, dev, width)
+    return p, positions, inv_freq
 
 
 def qk_norm(q, k, q_weight=None, k_weight=None, positions=None, inv_freq=None, *, norm="rms", eps=1e-6,
@@ -1160,14 +1177,30 @@ def int8_quantize(x, codes=None, scales=None):
     return codes, scales
 
 
-def _int8_weights(w_codes, w_scales, bias, depth, dev):
-    _need(w_codes, "w_codes", torch.int8, dev)
-    if w_codes.dim() != 2 or w_codes.shape[1] != depth:
-        raise ValueError(f"w_codes must be [cols,{depth}], got {tuple(w_codes.shape)}")
-    cols = w_codes.shape[0]
-    _checked(w_scales, "w_scales", torch.float32, dev, (cols,))
-    _optional(bias, "bias", torch.float32, dev, (cols,))
-    return cols
+@functools.lru_cache(maxsize=512)
+def _int8_form(x_shape, w_shape, in_dtype, out_dtype):
+    """What follows from sizes and types alone: parameters, y's and the scales'
+    shapes and int8_linear's workspace."""
+    if len(x_shape) < 1:
+        raise ValueError("rows must be [..,depth]")
+    if in_dtype is not None and in_dtype not in _DT:
+        raise ValueError("x must be float32 or bfloat16")
+    if out_dtype not in _DT:
+        raise ValueError("out_dtype must be float32 or bfloat16")
+    depth = x_shape[-1]
+    if len(w_shape) != 2 or w_shape[1] != depth:
+        raise ValueError(f"w_codes must be [cols,{depth}], got {tuple(w_shape)}")
+    rows, cols = 1, w_shape[0]
+    for s in x_shape[:-1]:
+        rows *= s
+    _sizes(rows, cols, depth)
+    p = _lib.Int8Params(rows, cols, depth, _DT.get(in_dtype, 0), _DT[out_dtype], 0)
+    return (p, torch.Size(x_shape[:-1] + (cols,)), torch.Size(x_shape[:-1]), torch.Size((cols,)),
+            int(_lib.int8_workspace_size(p)))
+
+
+def _int8_out(y, shape, out_dtype, dev):
+    return torch.empty(shape, dtype=out_dtype, device=dev) if y is None else _checked(y, "y", out_dtype, dev, shape)
 
 
 def int8_workspace_size(rows, cols, depth):
@@ -1181,16 +1214,13 @@ def int8_matmul(a_codes, a_scales, w_codes, w_scales, bias=None, *, out_dtype=to
     [cols,depth] as int8_quantize gives them, bias [cols] fp32 or None (see
     gdnq_int8_matmul in include/gdnq.h)."""
     _need(a_codes, "a_codes", torch.int8, None)
+    _need(w_codes, "w_codes", torch.int8, a_codes.device)
     dev = a_codes.device
-    if a_codes.dim() < 1:
-        raise ValueError("a_codes must be [..,depth]")
-    depth, lead = a_codes.shape[-1], a_codes.shape[:-1]
+    p, shape, lead, cols, _ = _int8_form(a_codes.shape, w_codes.shape, None, out_dtype)
     _checked(a_scales, "a_scales", torch.float32, dev, lead)
-    cols = _int8_weights(w_codes, w_scales, bias, depth, dev)
-    y = _mx_out(y, lead, cols, out_dtype, dev)
-    rows = _mx_rows(a_codes)
-    _sizes(rows, cols, depth)
-    p = _lib.Int8Params(rows, cols, depth, 0, _DT[out_dtype], 0)
+    _checked(w_scales, "w_scales", torch.float32, dev, cols)
+    _optional(bias, "bias", torch.float32, dev, cols)
+    y = _int8_out(y, shape, out_dtype, dev)
     _launch(dev, _lib.int8_matmul, p, _ptr(a_codes), _ptr(a_scales), _ptr(w_codes), _ptr(w_scales), _ptr(bias), _ptr(y))
     return y
 
@@ -1201,17 +1231,12 @@ def int8_linear(x, w_codes, w_scales, bias=None, *, out_dtype=None, y=None, work
     (default x's) float32 or bfloat16."""
     _need(x, "x", None, None)
     dev = x.device
-    if x.dtype not in _DT:
-        raise ValueError("x must be float32 or bfloat16")
-    if x.dim() < 1:
-        raise ValueError("x must be [..,depth]")
-    depth = x.shape[-1]
-    cols = _int8_weights(w_codes, w_scales, bias, depth, dev)
+    _need(w_codes, "w_codes", torch.int8, dev)
     out_dtype = out_dtype or (x.dtype if y is None else y.dtype)
-    y = _mx_out(y, x.shape[:-1], cols, out_dtype, dev)
-    rows = _mx_rows(x)
-    _sizes(rows, cols, depth)
-    p = _lib.Int8Params(rows, cols, depth, _DT[x.dtype], _DT[out_dtype], 0)
-    ws, ws_bytes = _space(workspace, int(_lib.int8_workspace_size(p)), dev)
+    p, shape, _, cols, need = _int8_form(x.shape, w_codes.shape, x.dtype, out_dtype)
+    _checked(w_scales, "w_scales", torch.float32, dev, cols)
+    _optional(bias, "bias", torch.float32, dev, cols)
+    y = _int8_out(y, shape, out_dtype, dev)
+    ws, ws_bytes = _space(workspace, need, dev)
     _launch(dev, _lib.int8_linear, p, _ptr(x), _ptr(w_codes), _ptr(w_scales), _ptr(bias), _ptr(y), _ptr(ws), ws_bytes)
     return y

@@ -188,7 +188,10 @@ __global__ __launch_bounds__(WAVES * 64) void int8_rows_kernel(Int8Launch L, int
 
 // ---------------------------------------------------------------- many rows
 //
-// A workgroup computes BM x BN of y, its WGM x WGN waves an equal part each, in
+// Bound by the matrix units: 16384 x 8192 x 4096 takes 491 us, 2.24 POPS (a large
+// library product of 8-bit integers reaches 2.18 on this card, 8192 x 8192 x 8192);
+// eight waves of 128 x 64 instead of four of 128 x 128 take 497.
+//   A workgroup computes BM x BN of y, its WGM x WGN waves an equal part each, in
 // steps of DEPTH values: the step's rows of both operands are loaded straight
 // into LDS, in two buffers.  The 32 x 32 x 32 instruction: lane l holds 16 bytes
 // of row l % 32, of two blocks h = l / 32, and the results 8 g + 4 h + 0 .. 3 of
@@ -258,7 +261,6 @@ __global__ __launch_bounds__(WGM* WGN * 64) void int8_tile_kernel(Int8Launch L, 
   constexpr int WAVES = WGM * WGN, THREADS = WAVES * 64;
   constexpr int TM = BM / WGM / 32, TN = BN / WGN / 32;  // 32 x 32 tiles of a wave
   constexpr int STEP_BLOCKS = DEPTH / 16, INSTRUCTIONS = STEP_BLOCKS / 2;
-  static_assert(BM * BN <= (BM + BN) * DEPTH, "the results of a pass fit the two buffers");
   __shared__ __attribute__((aligned(1024))) uint8_t codes[2][(BM + BN) * DEPTH];
 
   // Tiles in bands: the workgroups of one XCD (every eighth) take adjacent
@@ -360,7 +362,8 @@ __global__ __launch_bounds__(WGM* WGN * 64) void int8_tile_kernel(Int8Launch L, 
 
   // The results go through LDS, so that they leave in whole rows.  A row's
   // 16-byte pieces are permuted by its number.
-  constexpr int PASSES = sizeof(E) / 2, COLS = BN / PASSES, PITCH = COLS * sizeof(E), PIECES = PITCH / 16;
+  constexpr int PASSES = BM * BN * sizeof(E) <= sizeof(codes) ? 1 : 2, COLS = BN / PASSES, PITCH = COLS * sizeof(E), PIECES = PITCH / 16;
+  static_assert(BM * COLS * sizeof(E) <= sizeof(codes) && BN / WGN <= COLS, "a pass fits the two buffers, a wave's columns one pass");
   static_assert(BM * PIECES % THREADS == 0, "the loop below ends with whole rows of threads");
   typedef E e4 __attribute__((ext_vector_type(4)));
   float scale_a[TM];
@@ -370,6 +373,8 @@ __global__ __launch_bounds__(WGM* WGN * 64) void int8_tile_kernel(Int8Launch L, 
   E* y = static_cast<E*>(L.y);
   for (int pass = 0; pass < PASSES; ++pass) {
     __syncthreads();
+    int column = n0 + wn + h * 4;
+    asm volatile("" : "+v"(column));  // scales are read here, not kept from before the loop: that spilled
     if (wn / COLS == pass) {
 #pragma unroll
       for (int j = 0; j < TN; ++j)
@@ -378,7 +383,7 @@ __global__ __launch_bounds__(WGM* WGN * 64) void int8_tile_kernel(Int8Launch L, 
           f32x4 scale_w, bias = {0, 0, 0, 0};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int n = min(n0 + wn + j * 32 + g * 8 + h * 4 + e, L.N - 1);
+            const int n = min(column + j * 32 + g * 8 + e, L.N - 1);
             scale_w[e] = L.w_scales[n];
             if (L.bias) bias[e] = L.bias[n];
           }
@@ -430,12 +435,30 @@ hipError_t tile_product(const Int8Launch& L, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// Which kernel, by the number of workgroups each would have (us for a product of
+// M x N x K with the choice, and with the one it was taken over):
+//   few rows, 16 of them and 16 waves: at most one workgroup per CU (16 x 4096 x
+//     4096: 8.2, 32 x 32 tiles 10.2; 64 x 1024 x 8192: 9.5, 13.0 with 32 rows);
+//   few rows, 32 of them: also up to 448 where the depth is small enough that
+//     reading A in each of them costs little (64 x 2048 x 4096: 8.4, 32 x 32 tiles
+//     10.0; 192 x 1111 x 2064: 7.3, 8.2; but 48 x 4096 x 4096, 512 of them: 13.3,
+//     10.3);
+//   32 x 32 tiles of one wave: at most one per CU, since a CU takes about 25 to 45
+//     bytes a nanosecond and 64 x 64 tiles leave most of them idle (64 x 4096 x
+//     4096: 10.4, 12.1);
+//   64 x 64 tiles in steps of 256, of which a CU holds two: up to 512 (512 x 4096
+//     x 4096: 15.3, 128 x 128 tiles 22.7);
+//   128 x 128 tiles: up to 256 in steps of 256, one on a CU (1001 x 4096 x 4096:
+//     22.6, in steps of 128 24.7, 64 x 64 28.0), else in steps of 128, two on a CU
+//     (2048 x 4096 x 4096: 35.7, 256 x 256 tiles 46.8);
+//   256 x 256 tiles from 192 on (4096 x 4096 x 4096: 63.5, 71.0).
 template <typename E>
 hipError_t matmul(const Int8Launch& L, hipStream_t stream) {
   auto count = [&](int64_t m, int64_t n) { return (L.M + m - 1) / m * ((L.N + n - 1) / n); };
   if (count(16, 16) <= 256) return rows_product<1, 16, 4, E>(L, stream);
   const int64_t rows = count(32, 16);
-  if (rows <= 256 || (rows <= 448 && rows * L.K <= 1 << 19)) return rows_product<2, 8, 4, E>(L, stream);
+  if (rows <= 256 || (rows <= 448 && rows * L.K <= 1 << 20)) return rows_product<2, 8, 4, E>(L, stream);
+  if (count(32, 32) <= 256) return tile_product<32, 32, 1, 1, 256, E>(L, stream);
   if (count(64, 64) <= 512) return tile_product<64, 64, 2, 2, 256, E>(L, stream);
   if (count(256, 256) >= 192) return tile_product<256, 256, 2, 2, 128, E>(L, stream);
   if (count(128, 128) <= 256) return tile_product<128, 128, 2, 2, 256, E>(L, stream);

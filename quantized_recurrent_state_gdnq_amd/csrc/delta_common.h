@@ -182,9 +182,20 @@ __device__ __forceinline__ f32x4 mfma_split_split(const bf16x8& ah, const bf16x8
   return mfma16(ah, bh, mfma16(ah, bl, mfma16(al, bh, c)));
 }
 
+// Eight values in two parts; by pairs, six instructions each.
 __device__ __forceinline__ void split8(const f32x4& a, const f32x4& b, bf16x8& hi, bf16x8& lo) {
-  const float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-  split2(x, hi, lo);
+  u32x4 h, l;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const f32x2 x = i < 2 ? f32x2{a[2 * i], a[2 * i + 1]} : f32x2{b[2 * i - 4], b[2 * i - 3]};
+    h[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf16x2));
+    uint32_t word = h[i];
+    asm("" : "+v"(word));  // or the compiler rounds each value again to have it by itself
+    const f32x2 rest = {x[0] - __uint_as_float(word << 16), x[1] - __uint_as_float(word & 0xffff0000u)};
+    l[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(rest, bf16x2));
+  }
+  hi = __builtin_bit_cast(bf16x8, h);
+  lo = __builtin_bit_cast(bf16x8, l);
 }
 
 // 2^(a - b) of numbers given as whole part and rest.

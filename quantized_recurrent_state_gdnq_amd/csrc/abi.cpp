@@ -918,7 +918,7 @@ static gdnq_status delta_validate(const gdnq_delta_params* p, bool varlen, bool 
   if (L.N > 0x7fffffffLL) return fail(GDNQ_ERR_SHAPE, "%lld tokens: at most 2^31 - 1", (long long)L.N);
   // a workgroup of 256 threads per chunk and head, and per 64 rows of a state (a
   // step: per four), and a launch has fewer than 2^32 threads
-  const int64_t slots = varlen ? L.N / 64 + L.B : int64_t(L.B) * ((L.T + 63) / 64);
+  const int64_t slots = varlen ? L.N / 64 + L.B : int64_t(L.B) * ((int64_t(L.T) + 63) / 64);
   const int64_t groups = step ? (L.dv + 31) / 32 : (L.dv + 63) / 64;
   if (slots > (1 << 24) || slots * L.H >= 1 << 24 || int64_t(L.B) * L.H >= 1 << 24 || int64_t(L.B) * L.H * groups >= 1 << 24)
     return fail(GDNQ_ERR_SHAPE, "%lld chunks, %d sequences of %d heads: too large", (long long)slots, L.B, L.H);

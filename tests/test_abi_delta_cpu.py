@@ -282,3 +282,55 @@ def test_int8_quantize():
     refused(q(addr(1), 4, 64, 1, addr(1), addr(3), None), ALIAS, "overlaps")
     refused(q(addr(1), 4, 64, 1, addr(2) + 4, addr(3), None), ALIGN, "codes")
     assert q(None, 0, 64, 1, None, None, None) == 0
+
+
+# ---------------------------------------------------------------- the wrappers' own sizes
+
+BIG = 2 ** 32 + 10
+
+
+@pytest.fixture
+def meta(monkeypatch):
+    """Tensors of the given shape on no device, that pass for GPU tensors."""
+    monkeypatch.setattr(ops, "_need", lambda t, *a, **k: t)
+
+    def make(*shape, dtype=torch.bfloat16):
+        return torch.empty(shape, dtype=dtype, device="meta")
+    return make
+
+
+@pytest.mark.parametrize("lead", [(1, BIG), (BIG, 1)])
+def test_delta_sizes_beyond_32_bits(meta, lead):
+    q, gate = meta(*lead, 1, 8), meta(*lead, 1, dtype=torch.float32)
+    carry = meta(16, dtype=torch.uint8)
+    for call in (lambda: ops.delta_rule(q, q, q, gate, gate), lambda: ops.delta_rule_workspace_size(q, q),
+                 lambda: ops.delta_rule_backward(q, q, q, q, gate, gate, carry)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call()
+
+
+def test_packed_delta_and_step_sizes_beyond_32_bits(meta):
+    q, gate, cu = meta(BIG, 1, 8), meta(BIG, 1, dtype=torch.float32), meta(3, dtype=torch.int32)
+    for call in (lambda: ops.delta_rule(q, q, q, gate, gate, cu_seqlens=cu),
+                 lambda: ops.delta_rule_workspace_size(q, q, cu),
+                 lambda: ops.delta_rule_step(q, q, q, gate, gate, meta(BIG, 1, 8, 8, dtype=torch.float32))):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call()
+
+
+def test_int8_sizes_beyond_32_bits(meta):
+    few, many = meta(4, 16, dtype=torch.int8), meta(BIG, 16, dtype=torch.int8)
+    scales = lambda n: meta(n, dtype=torch.float32)  # noqa: E731
+    for call in (lambda: ops.int8_matmul(few, scales(4), many, scales(BIG)),
+                 lambda: ops.int8_matmul(many, scales(BIG), few, scales(4)),
+                 lambda: ops.int8_linear(meta(BIG, 16), few, scales(4)),
+                 lambda: ops.int8_quantize(meta(1, BIG + 6)), lambda: ops.int8_workspace_size(4, BIG, 32)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call()
+
+
+def test_qk_sizes_beyond_32_bits():
+    for lead, heads in (((BIG,), 1), ((2, BIG // 2), 1), ((1,), BIG)):
+        q = torch.empty((*lead, heads, 8), dtype=torch.bfloat16, device="meta")
+        with pytest.raises(ValueError, match="2\\^31"):
+            ops.qk_norm_workspace_size(q, q)

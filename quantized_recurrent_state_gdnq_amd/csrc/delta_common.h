@@ -119,6 +119,21 @@ __device__ __forceinline__ DeltaSpan delta_sequence(const DeltaLaunch& L, int b)
   return {first, first / DELTA_CHUNK + b, int(max(end - first, int64_t(0)))};
 }
 
+// The index-th longest of up to 64 packed sequences: chains of many chunks start
+// first, so that no long one starts beside the last short ones (12 sequences of
+// 16384 tokens, 16 heads: MEASURED_ORDER).  Other calls keep their order.
+__device__ __forceinline__ int delta_longest(const DeltaLaunch& L, int index) {
+  if (!L.cu_seqlens || L.B > 64) return index;
+  const int lane = threadIdx.x & 63;
+  const int tokens = lane < L.B ? delta_sequence(L, lane).tokens : -1;
+  int before = 0;
+  for (int i = 0; i < L.B; ++i) {
+    const int other = __builtin_amdgcn_readlane(tokens, i);
+    before += other > tokens || (other == tokens && i < lane);
+  }
+  return __builtin_ctzll(__builtin_amdgcn_ballot_w64(lane < L.B && before == index));
+}
+
 // The tokens of a slot: how many (0: none) and the first.
 __device__ __forceinline__ int delta_slot_tokens(const DeltaLaunch& L, int slot, int64_t& first) {
   int b;
@@ -216,9 +231,17 @@ __device__ __forceinline__ int chain_row(int tile, int row) {
 // decays.  All of it comes straight from memory, 16 bytes a lane and 1 KB a wave
 // at a time, in the order of LDS: the permutation of the blocks is in the address
 // that each lane loads from.
-template <int DK>
+// The first pass over segments of the forward call needs neither Q nor the second
+// triangle, and two of its workgroups fit a CU.
+template <int DK, bool BARE = false>
 struct ChainBuffer {
+  static constexpr int TRI_PIECES = 2 * TRI_BYTES / 1024;
   uint8_t k[64 * DK * 2], q[64 * DK * 2], tri[2 * TRI_BYTES], v[64 * 128], rows[1024];
+};
+template <int DK>
+struct ChainBuffer<DK, true> {
+  static constexpr int TRI_PIECES = TRI_BYTES / 1024;
+  uint8_t k[64 * DK * 2], tri[TRI_BYTES], v[64 * 128], rows[1024];
 };
 
 __device__ const uint8_t delta_zeros[16] __attribute__((aligned(16))) = {};
@@ -296,17 +319,17 @@ struct ChainLoader {
   // products of the chunk before: all at once they hold the wave up until the
   // queue has room (2600 of a chunk's 8100 cycles).
   static constexpr int STEPS = LOADS + 5;
-  template <int STEP>
-  __device__ __forceinline__ void step(ChainBuffer<DK>& to, const Next& x) const {
+  template <int STEP, bool BARE>
+  __device__ __forceinline__ void step(ChainBuffer<DK, BARE>& to, const Next& x) const {
     if constexpr (STEP < LOADS) {
       to_lds(x.k, at_k[STEP], to.k + (STEP * 4 + wave) * 1024);
-      to_lds(x.q, at_k[STEP], to.q + (STEP * 4 + wave) * 1024);
+      if constexpr (!BARE) to_lds(x.q, at_k[STEP], to.q + (STEP * 4 + wave) * 1024);
     } else if constexpr (STEP == LOADS) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) to_lds(x.v, at_v[i], to.v + (i * 4 + wave) * 1024);
     } else if constexpr (STEP < LOADS + 4) {
 #pragma unroll
-      for (int i = (STEP - LOADS - 1) * 2; i < (STEP - LOADS) * 2; ++i)
+      for (int i = (STEP - LOADS - 1) * 2; i < (STEP - LOADS) * 2 && i * 4 < to.TRI_PIECES; ++i)
         to_lds(x.ws, (i * 4 + wave) * 1024 + lane * 16, to.tri + (i * 4 + wave) * 1024);
     } else {
       if (wave == 0) to_lds(x.ws + DELTA_SCALARS, lane * 16, to.rows);
@@ -315,8 +338,8 @@ struct ChainLoader {
 
   // Any chunk at once.  Rows behind the last token are the last one's again (beta
   // is 0 there), or zeros where ZERO_V; columns behind the last are zero.
-  template <bool ZERO_V>
-  __device__ __forceinline__ void load(ChainBuffer<DK>& to, const Next& x) const {
+  template <bool ZERO_V, bool BARE>
+  __device__ __forceinline__ void load(ChainBuffer<DK, BARE>& to, const Next& x) const {
     step<LOADS + 1>(to, x);
     step<LOADS + 2>(to, x);
     step<LOADS + 3>(to, x);
@@ -327,7 +350,7 @@ struct ChainLoader {
       lds_place<DK>((i * 4 + wave) * 64 + lane, row, block);
       const int64_t at = min(row, x.n - 1) * krow + block * 16;
       to_lds(block * 8 < dk ? x.k + at : delta_zeros, to.k + (i * 4 + wave) * 1024);
-      to_lds(block * 8 < dk ? x.q + at : delta_zeros, to.q + (i * 4 + wave) * 1024);
+      if constexpr (!BARE) to_lds(block * 8 < dk ? x.q + at : delta_zeros, to.q + (i * 4 + wave) * 1024);
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {

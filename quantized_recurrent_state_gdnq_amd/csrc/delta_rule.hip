@@ -19,11 +19,12 @@ namespace {
 // this one's are used.
 //   PASS: the first pass over segments, which has no outputs.
 template <int DK, bool SAVE, bool PASS, typename O>
-__global__ __launch_bounds__(256, 1) void delta_chain_kernel(DeltaLaunch L, int row_groups) {
+__global__ __launch_bounds__(256, PASS ? 2 : 1) void delta_chain_kernel(DeltaLaunch L, int row_groups) {
   constexpr int KB = DK / 32, TILES = DK / 16;
-  __shared__ __attribute__((aligned(1024))) ChainBuffer<DK> buffers[2];
+  using Buffer = ChainBuffer<DK, PASS>;
+  __shared__ __attribute__((aligned(1024))) Buffer buffers[2];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-  const int per = row_groups * L.H * (L.segments - PASS), b = int(blockIdx.x) / per;
+  const int per = row_groups * L.H * (L.segments - PASS), b = delta_longest(L, int(blockIdx.x) / per);
   const DeltaSpan s = delta_sequence(L, b);
   const int chunks = (s.tokens + 63) / 64;
   const ChainPlace place = chain_place(L, row_groups, chunks, b, int(blockIdx.x) % per);
@@ -50,28 +51,30 @@ __global__ __launch_bounds__(256, 1) void delta_chain_kernel(DeltaLaunch L, int 
     chain_load_state<TILES>(S, start, L.dk, col, mine, g);
   }
   if (place.first < end)
-    loader.template load<false>(buffers[place.first & 1], loader.next(s.first + int64_t(place.first) * 64,
+    loader.template load<false, PASS>(buffers[place.first & 1], loader.next(s.first + int64_t(place.first) * 64,
                                                                      min(64, s.tokens - place.first * 64), s.slot + place.first));
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
   for (int chunk = place.first; chunk < end; ++chunk) {
-    const ChainBuffer<DK>& buf = buffers[chunk & 1];
+    const Buffer& buf = buffers[chunk & 1];
     const int64_t first = s.first + int64_t(chunk) * 64;
     const int n = min(64, s.tokens - chunk * 64);
-    ChainBuffer<DK>& following = buffers[(chunk + 1) & 1];
+    Buffer& following = buffers[(chunk + 1) & 1];
     const auto next = loader.next(first + 64, min(64, s.tokens - chunk * 64 - 64), s.slot + chunk + 1);
     const bool paced = chunk + 1 < end && next.whole;
-    if (chunk + 1 < end && !next.whole) loader.template load<false>(following, next);
+    if (chunk + 1 < end && !next.whole) loader.template load<false, PASS>(following, next);
     auto ahead = [&](auto step) {
       phase();
-      if (paced) loader.template step<step.value>(following, next);
+      if (paced) loader.template step<step.value, PASS>(following, next);
     };
     bf16* left = nullptr;  // this chunk's part of the carry
     if constexpr (SAVE)
       left = reinterpret_cast<bf16*>(static_cast<uint8_t*>(L.carry) + ((s.slot + chunk) * L.H + h) * delta_left_bytes(L));
     // K, then Q, 32 columns at a time, two ahead
     bf16x8 ring[3][4];
-    auto read = [&](auto i) { chain_rows<DK>(i.value < KB ? buf.k : buf.q, lane, i.value % KB, ring[i.value % 3]); };
+    const uint8_t* queries = nullptr;
+    if constexpr (!PASS) queries = buf.q;
+    auto read = [&](auto i) { chain_rows<DK>(i.value < KB ? buf.k : queries, lane, i.value % KB, ring[i.value % 3]); };
     read(Int<0>{});
     read(Int<1>{});
     phase();

@@ -21,7 +21,7 @@ __global__ __launch_bounds__(256, 1) void delta_chain_back_kernel(DeltaLaunch L,
   constexpr int KB = DK / 32, TILES = DK / 16;
   __shared__ __attribute__((aligned(1024))) ChainBuffer<DK> buffers[2];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-  const int per = row_groups * L.H * L.segments, b = int(blockIdx.x) / per;
+  const int per = row_groups * L.H * L.segments, b = delta_longest(L, int(blockIdx.x) / per);
   const DeltaSpan s = delta_sequence(L, b);
   const int chunks = (s.tokens + 63) / 64;
   const ChainPlace place = chain_place(L, row_groups, chunks, b, int(blockIdx.x) % per);
@@ -47,7 +47,7 @@ __global__ __launch_bounds__(256, 1) void delta_chain_back_kernel(DeltaLaunch L,
     chain_load_state<TILES>(S, start, L.dk, col, mine, g);
   }
   if (count > 0)
-    loader.template load<true>(buffers[0], loader.next(s.first + int64_t(last) * 64, min(64, s.tokens - last * 64), s.slot + last));
+    loader.template load<true, false>(buffers[0], loader.next(s.first + int64_t(last) * 64, min(64, s.tokens - last * 64), s.slot + last));
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
   for (int done = 0; done < count; ++done) {
@@ -56,10 +56,10 @@ __global__ __launch_bounds__(256, 1) void delta_chain_back_kernel(DeltaLaunch L,
     ChainBuffer<DK>& following = buffers[(done + 1) & 1];
     const auto next = loader.next(s.first + int64_t(chunk - 1) * 64, 64, s.slot + chunk - 1);
     const bool paced = chunk > place.first && next.whole;
-    if (chunk > place.first && !next.whole) loader.template load<true>(following, next);
+    if (chunk > place.first && !next.whole) loader.template load<true, false>(following, next);
     auto ahead = [&](auto step) {
       phase();
-      if (paced) loader.template step<step.value>(following, next);
+      if (paced) loader.template step<step.value, false>(following, next);
     };
     bf16* left = reinterpret_cast<bf16*>(static_cast<uint8_t*>(L.workspace) + left_at +
                                          ((s.slot + chunk) * L.H + h) * delta_left_bytes(L));

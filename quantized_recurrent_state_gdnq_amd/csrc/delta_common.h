@@ -49,10 +49,19 @@ inline int64_t delta_slots(const DeltaLaunch& L) {
   return L.cu_seqlens ? L.N / DELTA_CHUNK + L.B : int64_t(L.B) * ((int64_t(L.T) + DELTA_CHUNK - 1) / DELTA_CHUNK);
 }
 __host__ __device__ inline int64_t delta_align(int64_t n) { return (n + 255) / 256 * 256; }
-// A state in two bf16 parts, [2][d_v][d_k], and behind it a chunk's w or z,
-// [2][d_v][64]: what a chain leaves of a chunk and head.
-__host__ __device__ inline int64_t delta_state_bytes(const DeltaLaunch& L) { return int64_t(L.dv) * L.dk * 4; }
-__host__ __device__ inline int64_t delta_left_bytes(const DeltaLaunch& L) { return int64_t(L.dv) * (L.dk * 4 + DELTA_CHUNK * 4); }
+// What a chain leaves of a chunk and head: a state in two bf16 parts, and behind it
+// the chunk's w or z, [2][d_v][64].  Each part is in tiles of 16 rows and 32
+// columns, a kilobyte: a store of a wave (16 rows x 32 columns) is then whole lines
+// (rows as they are leave half a line each: 4 x 8192 tokens, 16 heads, chain 617 us,
+// with tiles 542).
+__host__ __device__ inline int64_t delta_part(const DeltaLaunch& L) { return int64_t((L.dv + 15) / 16) * ((L.dk + 31) / 32) * 512; }
+__host__ __device__ inline int64_t delta_left_bytes(const DeltaLaunch& L) {
+  return delta_part(L) * 4 + int64_t((L.dv + 15) / 16) * 4096;
+}
+// Where block `block` (8 columns) of a row is, in bf16, of rows of so many times 32 columns.
+__host__ __device__ inline int left_place(int row, int block, int times) {
+  return ((row >> 4) * times + (block >> 2)) * 512 + (row & 15) * 32 + (block & 3) * 8;
+}
 
 // Few chains of many chunks are cut into segments that run at once.  A segment
 // maps the state that enters it linearly, S' = S P + R: a first pass carries R

@@ -37,6 +37,7 @@ __global__ __launch_bounds__(256, PASS ? 2 : 1) void delta_chain_kernel(DeltaLau
   ChainLoader<DK> loader;
   loader.init(L, L.v, h, PASS && place.identity ? 0 : group, wave, lane);
   const int64_t vrow = int64_t(L.H) * L.dv;
+  const int times = (L.dk + 31) / 32, part_size = int(delta_part(L)), w_size = (L.dv + 15) / 16 * 1024;  // of what it leaves
 
   f32x4 S[TILES];
   const int64_t state_row = ((int64_t(b) * L.H + h) * L.dv + col) * L.dk;
@@ -85,8 +86,8 @@ __global__ __launch_bounds__(256, PASS ? 2 : 1) void delta_chain_kernel(DeltaLau
       if constexpr (SAVE) {
         const int at = j * 32 + g * 8;
         if (mine && at < L.dk) {
-          *reinterpret_cast<bf16x8*>(left + col * L.dk + at) = sh[j];
-          *reinterpret_cast<bf16x8*>(left + (L.dv + col) * L.dk + at) = sl[j];
+          *reinterpret_cast<bf16x8*>(left + left_place(col, j * 4 + g, times)) = sh[j];
+          *reinterpret_cast<bf16x8*>(left + part_size + left_place(col, j * 4 + g, times)) = sl[j];
         }
       }
     }
@@ -206,11 +207,11 @@ __global__ __launch_bounds__(256, PASS ? 2 : 1) void delta_chain_kernel(DeltaLau
     __syncthreads();
     if constexpr (SAVE) {
       if (mine) {
-        bf16* wp = left + 2 * L.dv * L.dk;
+        bf16* wp = left + 2 * part_size;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          *reinterpret_cast<bf16x8*>(wp + col * 64 + j * 32 + g * 8) = hi[j];
-          *reinterpret_cast<bf16x8*>(wp + (L.dv + col) * 64 + j * 32 + g * 8) = lo[j];
+          *reinterpret_cast<bf16x8*>(wp + left_place(col, j * 4 + g, 2)) = hi[j];
+          *reinterpret_cast<bf16x8*>(wp + w_size + left_place(col, j * 4 + g, 2)) = lo[j];
         }
       }
     }

@@ -34,6 +34,7 @@ __global__ __launch_bounds__(256, 1) void delta_chain_back_kernel(DeltaLaunch L,
   ChainLoader<DK> loader;
   loader.init(L, L.dout, h, PASS && place.identity ? 0 : group, wave, lane);
 
+  const int times = (L.dk + 31) / 32, part_size = int(delta_part(L)), w_size = (L.dv + 15) / 16 * 1024;  // of what it leaves
   f32x4 S[TILES];  // dS^T
   const int64_t state_row = ((int64_t(b) * L.H + h) * L.dv + col) * L.dk;
   if constexpr (PASS) {
@@ -74,8 +75,8 @@ __global__ __launch_bounds__(256, 1) void delta_chain_back_kernel(DeltaLaunch L,
       split8(S[2 * j], S[2 * j + 1], sh[j], sl[j]);
       const int at = j * 32 + g * 8;
       if (!PASS && mine && at < L.dk) {
-        *reinterpret_cast<bf16x8*>(left + col * L.dk + at) = sh[j];
-        *reinterpret_cast<bf16x8*>(left + (L.dv + col) * L.dk + at) = sl[j];
+        *reinterpret_cast<bf16x8*>(left + left_place(col, j * 4 + g, times)) = sh[j];
+        *reinterpret_cast<bf16x8*>(left + part_size + left_place(col, j * 4 + g, times)) = sl[j];
       }
     }
     const float* rows = reinterpret_cast<const float*>(buf.rows);
@@ -177,11 +178,11 @@ __global__ __launch_bounds__(256, 1) void delta_chain_back_kernel(DeltaLaunch L,
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     if (!PASS && mine) {
-      bf16* zp = left + 2 * L.dv * L.dk;
+      bf16* zp = left + 2 * part_size;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        *reinterpret_cast<bf16x8*>(zp + col * 64 + j * 32 + g * 8) = zh[j];
-        *reinterpret_cast<bf16x8*>(zp + (L.dv + col) * 64 + j * 32 + g * 8) = zl[j];
+        *reinterpret_cast<bf16x8*>(zp + left_place(col, j * 4 + g, 2)) = zh[j];
+        *reinterpret_cast<bf16x8*>(zp + w_size + left_place(col, j * 4 + g, 2)) = zl[j];
       }
     }
   }
@@ -227,7 +228,7 @@ struct GradientLoader {
   static constexpr int PIECES = 4 * 32 * DK * 2 / 1024;  // kilobytes of the states, of which a wave takes every 16th
   const uint8_t *left[2], *d, *rows;  // of the carry and the workspace at a chunk and head; dO of its first token; its decays
   int64_t vrow;
-  int dk, dv, n, wave, lane;
+  int dk, dv, part_size, n, wave, lane;
   bool exact;                  // whole columns and slabs
   uint32_t at_state, at_row, at_d;  // a lane's offsets then
   __device__ __forceinline__ void init(const DeltaLaunch& L, int wave_, int lane_) {
@@ -235,13 +236,14 @@ struct GradientLoader {
     lane = lane_;
     dk = L.dk;
     dv = L.dv;
+    part_size = int(delta_part(L));
     vrow = int64_t(L.H) * L.dv * 2;
     exact = L.dk == DK && L.dv % 32 == 0;
     int row, block;
     lds_place<DK>(wave % (PIECES / 4) * 64 + lane, row, block);  // 16 pieces on it is the same place of another part
-    at_state = uint32_t(row * DK + block * 8) * 2;
+    at_state = uint32_t(left_place(row, block, DK / 32)) * 2;
     lds_place<64>(wave % 4 * 64 + lane, row, block);
-    at_row = uint32_t(row * 64 + block * 8) * 2;
+    at_row = uint32_t(left_place(row, block, 2)) * 2;
     row = (wave % 4 * 64 + lane) / 4;
     block = (slab_block(row, lane & 3) >> 4) & 3;
     at_d = uint32_t(row) * uint32_t(vrow) + block * 16;
@@ -272,13 +274,13 @@ struct GradientLoader {
     for (int i = 0; i < PIECES / 16; ++i) {
       const int piece = i * 16 + wave, part = piece / (PIECES / 4);
       lds_place<DK>(piece % (PIECES / 4) * 64 + lane, row, block);
-      const uint8_t* p = (part < 2 ? left[0] : left[1]) + (int64_t((part & 1) * dv + v0 + row) * dk + block * 8) * 2;
+      const uint8_t* p = (part < 2 ? left[0] : left[1]) + ((part & 1) * part_size + left_place(v0 + row, block, (dk + 31) / 32)) * 2;
       to_lds(v0 + row < dv && block * 8 < dk ? p : delta_zeros, &to.states[0][0] + piece * 1024);
     }
     {
       const int part = wave / 4;
       lds_place<64>(wave % 4 * 64 + lane, row, block);
-      const uint8_t* p = (part < 2 ? left[0] : left[1]) + (int64_t(2 * dv) * dk + int64_t((part & 1) * dv + v0 + row) * 64 + block * 8) * 2;
+      const uint8_t* p = (part < 2 ? left[0] : left[1]) + (2 * part_size + (part & 1) * ((dv + 15) / 16 * 1024) + left_place(v0 + row, block, 2)) * 2;
       to_lds(v0 + row < dv ? p : delta_zeros, &to.tokens[0][0] + wave * 1024);
     }
     if (wave < 4) {

@@ -513,14 +513,22 @@ __global__ __launch_bounds__(256) void delta_join_kernel(DeltaLaunch L, int grou
   const float* start = BACK ? L.dh_last : L.h0;
   if (start) start += (int64_t(b) * L.H + h) * L.dv * L.dk;
   chain_load_state<TILES>(S, start, L.dk, row, mine, g);
+  auto segment = [&](int step) { return reinterpret_cast<float*>(delta_segment(L, b, BACK ? steps - step : step, h)); };
+  f32x4 next[TILES];  // R of the next step, loaded a step ahead as P is
+  chain_load_state<TILES>(next, segment(0), L.dk, row, mine, g);
   load(0);
   for (int step = 0; step < steps; ++step) {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    if (step + 1 < steps) load(step + 1);
-    float* state = reinterpret_cast<float*>(delta_segment(L, b, BACK ? steps - step : step, h));
+    float* state = segment(step);
     f32x4 R[TILES];
-    chain_load_state<TILES>(R, state, L.dk, row, mine, g);
+#pragma unroll
+    for (int t = 0; t < TILES; ++t) R[t] = next[t];
+    if (step + 1 < steps) {
+      chain_load_state<TILES>(next, segment(step + 1), L.dk, row, mine, g);
+      load(step + 1);
+    }
+    phase();
     bf16x8 sh[KB], sl[KB];
 #pragma unroll
     for (int j = 0; j < KB; ++j) split8(S[2 * j], S[2 * j + 1], sh[j], sl[j]);

@@ -38,6 +38,7 @@ __global__ __launch_bounds__(256, PASS ? 2 : 1) void delta_chain_kernel(DeltaLau
   loader.init(L, L.v, h, PASS && place.identity ? 0 : group, wave, lane);
   const int64_t vrow = int64_t(L.H) * L.dv;
   const int times = (L.dk + 31) / 32, part_size = int(delta_part(L)), w_size = (L.dv + 15) / 16 * 1024;  // of what it leaves
+  const bool exact = L.dk == DK && group * 64 + wave * 16 + 16 <= L.dv;  // all lanes leave something
 
   f32x4 S[TILES];
   const int64_t state_row = ((int64_t(b) * L.H + h) * L.dv + col) * L.dk;
@@ -83,13 +84,6 @@ __global__ __launch_bounds__(256, PASS ? 2 : 1) void delta_chain_kernel(DeltaLau
 #pragma unroll
     for (int j = 0; j < KB; ++j) {
       split8(S[2 * j], S[2 * j + 1], sh[j], sl[j]);
-      if constexpr (SAVE) {
-        const int at = j * 32 + g * 8;
-        if (mine && at < L.dk) {
-          *reinterpret_cast<bf16x8*>(left + left_place(col, j * 4 + g, times)) = sh[j];
-          *reinterpret_cast<bf16x8*>(left + part_size + left_place(col, j * 4 + g, times)) = sl[j];
-        }
-      }
     }
     const float* rows = reinterpret_cast<const float*>(buf.rows);
     auto row4 = [&](int which, int it) { return *reinterpret_cast<const f32x4*>(rows + which * 64 + chain_row(it, g * 4)); };
@@ -110,7 +104,22 @@ __global__ __launch_bounds__(256, PASS ? 2 : 1) void delta_chain_kernel(DeltaLau
         }
       split8(x[2 * half.value], x[2 * half.value + 1], hi[half.value], lo[half.value]);
     };
-    constexpr int PRODUCTS = PASS ? KB : 2 * KB;
+    // A part of the state that enters; behind the last load, so that the wait for
+    // the loads need not wait for these stores too.
+    auto leave = [&](auto j) {
+      phase();
+      if constexpr (SAVE && j.value < KB) {
+        bf16* to = left + left_place(col, j.value * 4 + g, times);
+        if (exact) {
+          *reinterpret_cast<bf16x8*>(to) = sh[j.value];
+          *reinterpret_cast<bf16x8*>(to + part_size) = sl[j.value];
+        } else if (mine && j.value * 32 + g * 8 < L.dk) {
+          *reinterpret_cast<bf16x8*>(to) = sh[j.value];
+          *reinterpret_cast<bf16x8*>(to + part_size) = sl[j.value];
+        }
+      }
+    };
+    constexpr int PRODUCTS = PASS ? KB : 2 * KB, STEPS = ChainLoader<DK>::STEPS;
     each<PRODUCTS>([&](auto i) {
       constexpr int j = i.value % KB;
       if constexpr (i.value + 2 < PRODUCTS) read(Int<i.value + 2>{});
@@ -136,15 +145,13 @@ __global__ __launch_bounds__(256, PASS ? 2 : 1) void delta_chain_kernel(DeltaLau
         for (int it = 0; it < 4; ++it) o[it] = mfma16(sh[j], f[it], o[it]);
       }
       if constexpr (!PASS && i.value >= 2 * KB - 2) errors(Int<i.value - (2 * KB - 2)>{});  // beside the last of these products
-      // the loader's first KB + 2 steps
-      if constexpr (i.value < KB) ahead(Int<i.value>{});
-      if constexpr (!PASS && i.value >= 2 * KB - 2) ahead(Int<i.value - KB + 2>{});
+      each<STEPS>([&](auto s) {
+        if constexpr (s.value * PRODUCTS / STEPS == i.value) ahead(s);
+      });
     });
     if constexpr (PASS) {
       errors(Int<0>{});
       errors(Int<1>{});
-      ahead(Int<KB>{});
-      ahead(Int<KB + 1>{});
     }
     phase();
     bf16x8 kt[2][4][2];
@@ -173,7 +180,7 @@ __global__ __launch_bounds__(256, PASS ? 2 : 1) void delta_chain_kernel(DeltaLau
     for (int t = 0; t < TILES; ++t) S[t] *= whole;
 #pragma unroll
     for (int it = 0; it < 4; ++it) o[it] *= decay_o[it];
-    ahead(Int<KB + 2>{});
+    leave(Int<0>{});
     phase();
     bf16x8 mh[TRI_BLOCKS], ml[TRI_BLOCKS], th[2], tl[2];
     if constexpr (TILES > 4) chain_columns<DK>(buf.k, lane, 1, kt[1]);
@@ -186,9 +193,10 @@ __global__ __launch_bounds__(256, PASS ? 2 : 1) void delta_chain_kernel(DeltaLau
 #pragma unroll
       for (int j = 0; j < 2; ++j) split8(w[2 * j], w[2 * j + 1], hi[j], lo[j]);
     }
-    ahead(Int<KB + 3>{});
+    leave(Int<1>{});
+    leave(Int<2>{});
     if constexpr (TILES > 4) chain_update(S + 4, kt[1], th, tl);
-    ahead(Int<KB + 4>{});
+    leave(Int<3>{});
     auto inside = [&](const bf16x8 (&y)[2], const bf16x8 (&m)[TRI_BLOCKS]) {
 #pragma unroll
       for (int it = 0; it < 4; ++it) o[it] = mfma16(y[0], m[it < 2 ? it : 2 * it - 2], o[it]);
@@ -203,7 +211,10 @@ __global__ __launch_bounds__(256, PASS ? 2 : 1) void delta_chain_kernel(DeltaLau
     phase();
     // the next chunk is in LDS, and nobody reads this one any more; the stores
     // below are behind this wait, so that the next chunk's covers them
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    if (SAVE && exact)
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * KB) : "memory");
+    else
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     if constexpr (SAVE) {
       if (mine) {

@@ -70,30 +70,55 @@ __host__ __device__ inline int left_place(int row, int block, int times) {
 // 2.3 times the work (without the outputs, 82 of 132 products a chunk and row),
 // so it pays where chains leave three in four of the 256 CUs idle: 65536 tokens,
 // 8 heads, 16 workgroups: the call takes 3.3 ms in one piece, 0.75 cut.
-//   In the workspace for each sequence, segment and head: R (then the state
-// behind the segment) [d_v][d_k] fp32, P [2][d_k][d_k] in two bf16 parts.
+//   Packed sequences differ: those of more than `split_above` chunks, three times what
+// a CU's share of all chunks would be, are cut into segments of that share (their
+// lengths are known on the device alone).  16384 tokens, 16 heads, forward: 16000 and 20 of
+// 200 723 -> 401 us; 10000, 4000, 1500 and 884 466 -> 361; where none is long enough
+// the two empty launches cost 8.  Twice and half the share: 425 for the second.
+//   In the workspace for each segment of a cut sequence and each head: R (then the
+// state behind the segment) [d_v][d_k] fp32, P [2][d_k][d_k] in two bf16 parts.
+constexpr int DELTA_ORDERED = 64;  // packed sequences that a wave puts in order
 inline void delta_split(DeltaLaunch& L, int64_t at) {
-  const int64_t chains = int64_t(L.B) * L.H * ((L.dv + 63) / 64);
+  const int64_t rows = int64_t(L.H) * ((L.dv + 63) / 64), chains = rows * L.B;
   const int64_t chunks = ((L.cu_seqlens ? L.N : int64_t(L.T)) + DELTA_CHUNK - 1) / DELTA_CHUNK;
   L.segments = 1;
-  L.seg_chunks = 0x7fffffff;
+  L.seg_chunks = L.split_above = 0x7fffffff;
+  L.seg_slots = 0;
   L.seg_at = delta_align(at);
-  if (chains == 0 || chains > 64) return;
-  const int64_t want = 256 / chains;
-  if (chunks < 8 * want) return;
-  L.seg_chunks = int((chunks + want - 1) / want);
-  L.segments = int((chunks + L.seg_chunks - 1) / L.seg_chunks);
+  if (chains == 0) return;
+  if (L.cu_seqlens) {
+    const int64_t share = chunks * rows / 256;
+    const int64_t above = share > 5 ? 3 * share : 16;
+    if (L.B > DELTA_ORDERED || chunks <= above) return;
+    L.split_above = int(above);
+    L.seg_chunks = int(share > 8 ? share : 8);
+    L.segments = int((chunks + L.seg_chunks - 1) / L.seg_chunks);
+    // every cut sequence has one more than its whole segments, and is longer than split_above
+    L.seg_slots = chunks / L.seg_chunks + chunks / above + 1;
+  } else {
+    if (chains > 64) return;
+    const int64_t want = 256 / chains;
+    if (chunks < 8 * want) return;
+    L.split_above = 0;
+    L.seg_chunks = int((chunks + want - 1) / want);
+    L.segments = int((chunks + L.seg_chunks - 1) / L.seg_chunks);
+    L.seg_slots = int64_t(L.B) * L.segments;
+  }
+}
+// Segments and whole sequences of a call, at most; of a first pass, the segments that another follows.
+inline int64_t delta_items(const DeltaLaunch& L, bool pass) {
+  if (L.segments == 1) return L.B;
+  if (!L.cu_seqlens) return int64_t(L.B) * (L.segments - pass);
+  return L.N / DELTA_CHUNK / L.seg_chunks + (pass ? 1 : L.B);
 }
 __host__ __device__ inline int64_t delta_segment_bytes(const DeltaLaunch& L) { return int64_t(L.dk) * (L.dv + L.dk) * 4; }
 // The bytes up to the end of what the segments take.
-inline int64_t delta_split_bytes(const DeltaLaunch& L) {
-  return L.segments > 1 ? L.seg_at + int64_t(L.B) * L.segments * L.H * delta_segment_bytes(L) : L.seg_at;
-}
+inline int64_t delta_split_bytes(const DeltaLaunch& L) { return L.seg_at + L.seg_slots * L.H * delta_segment_bytes(L); }
 
 #ifdef __HIPCC__
 
-__device__ __forceinline__ uint8_t* delta_segment(const DeltaLaunch& L, int b, int seg, int h) {
-  return static_cast<uint8_t*>(L.workspace) + L.seg_at + ((int64_t(b) * L.segments + seg) * L.H + h) * delta_segment_bytes(L);
+__device__ __forceinline__ uint8_t* delta_segment(const DeltaLaunch& L, int at, int h) {
+  return static_cast<uint8_t*>(L.workspace) + L.seg_at + (int64_t(at) * L.H + h) * delta_segment_bytes(L);
 }
 
 template <int V>
@@ -128,19 +153,47 @@ __device__ __forceinline__ DeltaSpan delta_sequence(const DeltaLaunch& L, int b)
   return {first, first / DELTA_CHUNK + b, int(max(end - first, int64_t(0)))};
 }
 
-// The index-th longest of up to 64 packed sequences: chains of many chunks start
-// first, so that no long one starts beside the last short ones (12 sequences of
-// 16384 tokens, 16 heads: MEASURED_ORDER).  Other calls keep their order.
-__device__ __forceinline__ int delta_longest(const DeltaLaunch& L, int index) {
-  if (!L.cu_seqlens || L.B > 64) return index;
+// What the workgroups of a chain take: a sequence, or a segment of one.
+struct DeltaItem {
+  int b, seg, segments;  // b < 0: none
+  int64_t at;            // its sequence's first segment in the workspace
+};
+// Of packed sequences (up to 64, a lane each) the longest come first, so that no
+// long chain starts beside the last short ones (12 sequences of 16384 tokens, 16
+// heads: 352 -> 340 us, and 325 -> 314 back).  Malformed offsets can ask for more
+// items or segments than there are: those beyond are left out.
+__device__ __forceinline__ DeltaItem delta_packed(const DeltaLaunch& L, int index, int b, bool pass) {
   const int lane = threadIdx.x & 63;
   const int tokens = lane < L.B ? delta_sequence(L, lane).tokens : -1;
+  const int chunks = (tokens + DELTA_CHUNK - 1) / DELTA_CHUNK;
+  const int segments = chunks > L.split_above ? (chunks + L.seg_chunks - 1) / L.seg_chunks : 1;
+  const int items = lane < L.B ? segments - pass : 0, slots = segments > 1 ? segments : 0;
   int before = 0;
+  int64_t at = 0;
   for (int i = 0; i < L.B; ++i) {
     const int other = __builtin_amdgcn_readlane(tokens, i);
-    before += other > tokens || (other == tokens && i < lane);
+    const bool first = other > tokens || (other == tokens && i < lane);
+    before += first ? __builtin_amdgcn_readlane(items, i) : 0;
+    at += first ? __builtin_amdgcn_readlane(slots, i) : 0;
   }
-  return __builtin_ctzll(__builtin_amdgcn_ballot_w64(lane < L.B && before == index));
+  const bool fits = at + slots <= L.seg_slots;
+  const bool here = b < 0 ? index >= before && index - before < items : lane == b;
+  const uint64_t found = __builtin_amdgcn_ballot_w64(here && fits);
+  if (!found) return {-1, 0, 1, 0};
+  const int from = __builtin_ctzll(found);
+  return {from, index - __builtin_amdgcn_readlane(before, from), __builtin_amdgcn_readlane(segments, from),
+          __builtin_amdgcn_readlane(int(at), from)};
+}
+// The index-th item.
+__device__ __forceinline__ DeltaItem delta_item(const DeltaLaunch& L, int index, bool pass) {
+  if (L.cu_seqlens && L.B <= DELTA_ORDERED) return delta_packed(L, index, -1, pass);
+  const int n = L.segments - pass;
+  return {index / n, index % n, L.segments, int64_t(index / n) * L.segments};
+}
+// All of sequence b.
+__device__ __forceinline__ DeltaItem delta_whole(const DeltaLaunch& L, int b) {
+  if (L.cu_seqlens && L.B <= DELTA_ORDERED) return delta_packed(L, 0, b, false);
+  return {b, 0, L.segments, int64_t(b) * L.segments};
 }
 
 // The tokens of a slot: how many (0: none) and the first.
@@ -421,23 +474,21 @@ __device__ __forceinline__ s16x4 chain_column(const uint8_t* v, int it, int wave
 }
 __device__ __forceinline__ float bf16_value(short x) { return __uint_as_float(uint32_t(uint16_t(x)) << 16); }
 
-// Where the workgroup of a chain is: rows [64 group, ..) of head h, segment seg of
-// sequence b.  Of a first pass the groups behind those of V carry the identity.
+// Where the workgroup of a chain is: rows [64 group, ..) of head h, an item's chunks.
+// Of a first pass the groups behind those of V carry the identity.
 struct ChainPlace {
-  int b, seg, h, group, first, end;  // chunks
+  int h, group, first, end;  // chunks
   bool identity;
 };
-__device__ __forceinline__ ChainPlace chain_place(const DeltaLaunch& L, int groups, int chunks, int b, int rest) {
+__device__ __forceinline__ ChainPlace chain_place(const DeltaLaunch& L, int groups, int chunks, const DeltaItem& item, int rest) {
   ChainPlace p;
-  p.b = b;
   p.group = rest % groups;
-  p.h = rest / groups % L.H;
-  p.seg = rest / groups / L.H;
+  p.h = rest / groups;
   const int dv_groups = (L.dv + 63) / 64;
   p.identity = p.group >= dv_groups;
   if (p.identity) p.group -= dv_groups;
-  p.first = int(min(int64_t(p.seg) * L.seg_chunks, int64_t(chunks)));
-  p.end = int(min(int64_t(p.first) + L.seg_chunks, int64_t(chunks)));
+  p.first = item.seg > 0 ? int(min(int64_t(item.seg) * L.seg_chunks, int64_t(chunks))) : 0;
+  p.end = item.seg + 1 < item.segments ? int(min(int64_t(p.first) + L.seg_chunks, int64_t(chunks))) : chunks;
   return p;
 }
 // A chain's state tiles from a matrix of fp32 rows (or none: zero), or the identity.
@@ -459,8 +510,8 @@ __device__ __forceinline__ void chain_identity(f32x4 (&S)[TILES], int row, int g
 }
 // What a first pass leaves: R in fp32, or P in two parts.
 template <int TILES>
-__device__ __forceinline__ void chain_leave(const DeltaLaunch& L, const ChainPlace& p, const f32x4 (&S)[TILES], int row, int g) {
-  uint8_t* to = delta_segment(L, p.b, p.seg, p.h);
+__device__ __forceinline__ void chain_leave(const DeltaLaunch& L, const DeltaItem& item, const ChainPlace& p, const f32x4 (&S)[TILES], int row, int g) {
+  uint8_t* to = delta_segment(L, int(item.at) + item.seg, p.h);
   if (!p.identity) {
     if (row >= L.dv) return;
 #pragma unroll
@@ -497,11 +548,11 @@ __global__ __launch_bounds__(256) void delta_join_kernel(DeltaLaunch L, int grou
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
   const int row = group * 64 + wave * 16 + c;
   const bool mine = row < L.dv;
-  const int chunks = (delta_sequence(L, b).tokens + 63) / 64;
-  const int steps = int((int64_t(chunks) + L.seg_chunks - 1) / L.seg_chunks) - 1;
-  if (steps <= 0) return;
+  const DeltaItem item = delta_whole(L, b);
+  const int steps = item.segments - 1;
+  if (item.b < 0 || steps <= 0) return;
   auto load = [&](int step) {
-    const uint8_t* from = delta_segment(L, b, BACK ? steps - step : step, h) + int64_t(L.dv) * L.dk * 4;
+    const uint8_t* from = delta_segment(L, int(item.at) + (BACK ? steps - step : step), h) + int64_t(L.dv) * L.dk * 4;
 #pragma unroll 4
     for (int i = 0; i < PIECES / 4; ++i) {
       const int piece = i * 4 + wave, part = piece / (PIECES / 2);
@@ -520,7 +571,7 @@ __global__ __launch_bounds__(256) void delta_join_kernel(DeltaLaunch L, int grou
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     if (step + 1 < steps) load(step + 1);
-    float* state = reinterpret_cast<float*>(delta_segment(L, b, BACK ? steps - step : step, h));
+    float* state = reinterpret_cast<float*>(delta_segment(L, int(item.at) + (BACK ? steps - step : step), h));
     f32x4 R[TILES];
     chain_load_state<TILES>(R, state, L.dk, row, mine, g);
     bf16x8 sh[KB], sl[KB];

@@ -24,13 +24,13 @@ __global__ __launch_bounds__(256, PASS ? 2 : 1) void delta_chain_kernel(DeltaLau
   using Buffer = ChainBuffer<DK, PASS>;
   __shared__ __attribute__((aligned(1024))) Buffer buffers[2];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-  const int per = row_groups * L.H * (L.segments - PASS), b = delta_longest(L, int(blockIdx.x) / per);
+  const int per = row_groups * L.H;
+  const DeltaItem item = delta_item(L, int(blockIdx.x) / per, PASS);
+  if (item.b < 0) return;
+  const int b = item.b;
   const DeltaSpan s = delta_sequence(L, b);
   const int chunks = (s.tokens + 63) / 64;
-  const ChainPlace place = chain_place(L, row_groups, chunks, b, int(blockIdx.x) % per);
-  // a segment without chunks, or one that no other follows
-  if (place.seg > 0 && place.first >= chunks) return;
-  if (PASS && place.end >= chunks) return;
+  const ChainPlace place = chain_place(L, row_groups, chunks, item, int(blockIdx.x) % per);
   const int h = place.h, group = place.group, end = place.end;
   const int col = group * 64 + wave * 16 + c;
   const bool mine = col < L.dv;
@@ -49,7 +49,7 @@ __global__ __launch_bounds__(256, PASS ? 2 : 1) void delta_chain_kernel(DeltaLau
       chain_load_state<TILES>(S, nullptr, L.dk, col, mine, g);
   } else {
     const float* start = L.h0 ? L.h0 + state_row - int64_t(col) * L.dk : nullptr;
-    if (place.seg > 0) start = reinterpret_cast<const float*>(delta_segment(L, b, place.seg - 1, h));
+    if (item.seg > 0) start = reinterpret_cast<const float*>(delta_segment(L, int(item.at) + item.seg - 1, h));
     chain_load_state<TILES>(S, start, L.dk, col, mine, g);
   }
   if (place.first < end)
@@ -237,7 +237,7 @@ __global__ __launch_bounds__(256, PASS ? 2 : 1) void delta_chain_kernel(DeltaLau
       }
     }
   }
-  if constexpr (PASS) chain_leave<TILES>(L, place, S, col, g);
+  if constexpr (PASS) chain_leave<TILES>(L, item, place, S, col, g);
   if (!PASS && L.h_last && mine && end == chunks) {
 #pragma unroll
     for (int t = 0; t < TILES; ++t) {
@@ -328,12 +328,12 @@ hipError_t forward(const DeltaLaunch& L, hipStream_t stream) {
   const int groups = (L.dv + 63) / 64;
   if (L.segments > 1) {
     const int all = groups + (L.dk + 63) / 64;
-    delta_chain_kernel<DK, false, true, bf16><<<uint32_t(all * L.H * (L.segments - 1) * L.B), 256, 0, stream>>>(L, all);
+    delta_chain_kernel<DK, false, true, bf16><<<uint32_t(all * L.H * delta_items(L, true)), 256, 0, stream>>>(L, all);
     if (hipError_t e = hipGetLastError()) return e;
     delta_join_kernel<DK, false><<<uint32_t(groups * L.H * L.B), 256, 0, stream>>>(L, groups);
     if (hipError_t e = hipGetLastError()) return e;
   }
-  const uint32_t grid = uint32_t(groups) * uint32_t(L.H) * uint32_t(L.B) * uint32_t(L.segments);
+  const uint32_t grid = uint32_t(groups * L.H * delta_items(L, false));
   if (L.carry)
     L.out_bf16 ? delta_chain_kernel<DK, true, false, bf16><<<grid, 256, 0, stream>>>(L, groups)
                : delta_chain_kernel<DK, true, false, float><<<grid, 256, 0, stream>>>(L, groups);

@@ -21,13 +21,14 @@ __global__ __launch_bounds__(256, 1) void delta_chain_back_kernel(DeltaLaunch L,
   constexpr int KB = DK / 32, TILES = DK / 16;
   __shared__ __attribute__((aligned(1024))) ChainBuffer<DK> buffers[2];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-  const int per = row_groups * L.H * L.segments, b = delta_longest(L, int(blockIdx.x) / per);
+  const int per = row_groups * L.H;
+  DeltaItem item = delta_item(L, int(blockIdx.x) / per, PASS);
+  if (item.b < 0) return;
+  item.seg += PASS;  // the segments that another comes before
+  const int b = item.b;
   const DeltaSpan s = delta_sequence(L, b);
   const int chunks = (s.tokens + 63) / 64;
-  const ChainPlace place = chain_place(L, row_groups, chunks, b, int(blockIdx.x) % per);
-  // a segment without chunks, or one that none comes before
-  if (place.seg > 0 && place.first >= chunks) return;
-  if (PASS && place.seg == 0) return;
+  const ChainPlace place = chain_place(L, row_groups, chunks, item, int(blockIdx.x) % per);
   const int h = place.h, group = place.group, count = place.end - place.first, last = place.end - 1;
   const int col = group * 64 + wave * 16 + c;
   const bool mine = col < L.dv && !(PASS && place.identity);
@@ -44,7 +45,7 @@ __global__ __launch_bounds__(256, 1) void delta_chain_back_kernel(DeltaLaunch L,
       chain_load_state<TILES>(S, nullptr, L.dk, col, mine, g);
   } else {
     const float* start = L.dh_last ? L.dh_last + state_row - int64_t(col) * L.dk : nullptr;
-    if (place.end < chunks) start = reinterpret_cast<const float*>(delta_segment(L, b, place.seg + 1, h));
+    if (place.end < chunks) start = reinterpret_cast<const float*>(delta_segment(L, int(item.at) + item.seg + 1, h));
     chain_load_state<TILES>(S, start, L.dk, col, mine, g);
   }
   if (count > 0)
@@ -186,8 +187,8 @@ __global__ __launch_bounds__(256, 1) void delta_chain_back_kernel(DeltaLaunch L,
       }
     }
   }
-  if constexpr (PASS) chain_leave<TILES>(L, place, S, col, g);
-  if (!PASS && L.dh0 && mine && place.seg == 0) {
+  if constexpr (PASS) chain_leave<TILES>(L, item, place, S, col, g);
+  if (!PASS && L.dh0 && mine && item.seg == 0) {
 #pragma unroll
     for (int t = 0; t < TILES; ++t) {
       const int at = chain_row(t, g * 4);
@@ -641,12 +642,12 @@ hipError_t backward(const DeltaLaunch& L, hipStream_t stream) {
   const int groups = (L.dv + 63) / 64;
   if (L.segments > 1) {
     const int all = groups + (L.dk + 63) / 64;
-    delta_chain_back_kernel<DK, true><<<uint32_t(all * L.H * L.segments * L.B), 256, 0, stream>>>(L, all, left_at);
+    delta_chain_back_kernel<DK, true><<<uint32_t(all * L.H * delta_items(L, true)), 256, 0, stream>>>(L, all, left_at);
     if (hipError_t e = hipGetLastError()) return e;
     delta_join_kernel<DK, true><<<uint32_t(groups * L.H * L.B), 256, 0, stream>>>(L, groups);
     if (hipError_t e = hipGetLastError()) return e;
   }
-  delta_chain_back_kernel<DK, false><<<uint32_t(groups * L.H * L.segments) * uint32_t(L.B), 256, 0, stream>>>(L, groups, left_at);
+  delta_chain_back_kernel<DK, false><<<uint32_t(groups * L.H * delta_items(L, false)), 256, 0, stream>>>(L, groups, left_at);
   if (hipError_t e = hipGetLastError()) return e;
   const int64_t items = slots * L.G;
   if (items > 0) delta_gradient_kernel<DK><<<uint32_t(items < 256 ? items : 256), 1024, 0, stream>>>(L, left_at, int(items));

@@ -172,9 +172,10 @@ struct DeltaLaunch {
   int B, T, G, H, dk, dv;
   int64_t N;        // tokens of the call
   int row_groups;
-  // Long sequences in few heads: SEG chunks a segment, up to `segments` of a sequence (1: not split),
-  // and where the workspace holds what passes between them.
-  int seg_chunks, segments;
+  // Long sequences in few heads: those of more than split_above chunks are cut into segments of seg_chunks, up to
+  // `segments` of a sequence (1: no call has any), seg_slots in all, at seg_at of the workspace
+  int seg_chunks, segments, split_above;
+  int64_t seg_slots;
   int64_t seg_at;
   bool in_bf16, out_bf16, log_decay;
 };

@@ -69,7 +69,7 @@ __host__ __device__ inline int left_place(int row, int block, int times) {
 // one joins them, and the chains then start from the states that enter.  That is
 // 2.3 times the work (without the outputs, 82 of 132 products a chunk and row),
 // so it pays where chains leave three in four of the 256 CUs idle: 65536 tokens,
-// 8 heads, 16 workgroups: the call takes 3.3 ms in one piece, 0.75 cut.
+// 8 heads, 16 workgroups: the call takes 3.3 ms in one piece, 0.59 cut.
 //   Packed sequences differ: those of more than `split_above` chunks, three times what
 // a CU's share of all chunks would be, are cut into segments of that share (their
 // lengths are known on the device alone).  16384 tokens, 16 heads, forward: 16000 and 20 of
@@ -151,6 +151,21 @@ __device__ __forceinline__ DeltaSpan delta_sequence(const DeltaLaunch& L, int b)
   }
   const int64_t first = delta_offset(L, b), end = delta_offset(L, b + 1);
   return {first, first / DELTA_CHUNK + b, int(max(end - first, int64_t(0)))};
+}
+
+// Workgroups that read the same (a key head's) on the same XCD, whose L2 they
+// share: of a grid of units of `size` workgroups, eight units at a time, one for each
+// XCD, as workgroups are dealt out; the last units, fewer than eight, in order.
+// 65536 tokens, 8 heads, first pass 222 -> 203 us; 16384 packed tokens, 16 heads, chain 290 -> 278.
+__device__ __forceinline__ int xcd_unit(int size, int& within) {
+  const int block = int(blockIdx.x), full = int(gridDim.x) / size & ~7;
+  if (block < full * size) {
+    const int r = block % (8 * size);
+    within = r >> 3;
+    return block / (8 * size) * 8 + (r & 7);
+  }
+  within = (block - full * size) % size;
+  return full + (block - full * size) / size;
 }
 
 // What the workgroups of a chain take: a sequence, or a segment of one.
@@ -480,10 +495,11 @@ struct ChainPlace {
   int h, group, first, end;  // chunks
   bool identity;
 };
-__device__ __forceinline__ ChainPlace chain_place(const DeltaLaunch& L, int groups, int chunks, const DeltaItem& item, int rest) {
+__device__ __forceinline__ ChainPlace chain_place(const DeltaLaunch& L, int groups, int chunks, const DeltaItem& item, int key_head,
+                                                 int within) {
   ChainPlace p;
-  p.group = rest % groups;
-  p.h = rest / groups;
+  p.group = within % groups;
+  p.h = key_head * (L.H / L.G) + within / groups;
   const int dv_groups = (L.dv + 63) / 64;
   p.identity = p.group >= dv_groups;
   if (p.identity) p.group -= dv_groups;

@@ -99,8 +99,8 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaLaunch L) {
   __shared__ __attribute__((aligned(16))) float a[PREP_FLOATS], n[PREP_FLOATS];
   __shared__ float rest[64], beta[64];
   __shared__ int whole[64];
-  const int slot = int(blockIdx.x) / L.H;
-  const int h = int(blockIdx.x) % L.H, kh = h / (L.H / L.G);
+  int within;
+  const int unit = xcd_unit(L.H / L.G, within), slot = unit / L.G, kh = unit % L.G, h = kh * (L.H / L.G) + within;
   int64_t first;
   const int tokens = delta_slot_tokens(L, slot, first);
   if (tokens == 0) return;

@@ -21,14 +21,15 @@ __global__ __launch_bounds__(256, 1) void delta_chain_back_kernel(DeltaLaunch L,
   constexpr int KB = DK / 32, TILES = DK / 16;
   __shared__ __attribute__((aligned(1024))) ChainBuffer<DK> buffers[2];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-  const int per = row_groups * L.H;
-  DeltaItem item = delta_item(L, int(blockIdx.x) / per, PASS);
+  int within;
+  const int unit = xcd_unit(row_groups * (L.H / L.G), within);
+  DeltaItem item = delta_item(L, unit / L.G, PASS);
   if (item.b < 0) return;
   item.seg += PASS;  // the segments that another comes before
   const int b = item.b;
   const DeltaSpan s = delta_sequence(L, b);
   const int chunks = (s.tokens + 63) / 64;
-  const ChainPlace place = chain_place(L, row_groups, chunks, item, int(blockIdx.x) % per);
+  const ChainPlace place = chain_place(L, row_groups, chunks, item, unit % L.G, within);
   const int h = place.h, group = place.group, count = place.end - place.first, last = place.end - 1;
   const int col = group * 64 + wave * 16 + c;
   const bool mine = col < L.dv && !(PASS && place.identity);

@@ -766,7 +766,7 @@ gdnq_status gdnq_qk_norm_backward(const gdnq_qk_params* p, const void* q, const 
                                   size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
- * gdnq_int8_* -- rows in 8-bit integers with a scale each, and the product of
+ * gdnq_int_* -- rows in 8-bit integers with a scale each, and the product of
  *   such rows: beside gdnq_mx_*, a projection whose weights have a scale for
  *   every channel and whose activations have one for every token.
  *
@@ -774,35 +774,35 @@ gdnq_status gdnq_qk_norm_backward(const gdnq_qk_params* p, const void* q, const 
  *   code = clamp(round_half_even(x / scale), -127, 127) (IEEE fp32 divisions);
  *   a row of zeros, or whose scale rounds to 0, has codes 0.  A row with a NaN
  *   or an infinity gets scale NaN and codes 0: products with it are NaN.
- *   gdnq_int8_quantize: x [rows, depth] (dtype GDNQ_F32 or GDNQ_BF16) to codes
+ *   gdnq_int_quantize: x [rows, depth] (dtype GDNQ_F32 or GDNQ_BF16) to codes
  *     [rows, depth] int8 and scales [rows] fp32.
- *   gdnq_int8_matmul: y[m,n] = (sum_k a[m,k] w[n,k]) a_scales[m] w_scales[n] +
+ *   gdnq_int_matmul: y[m,n] = (sum_k a[m,k] w[n,k]) a_scales[m] w_scales[n] +
  *     bias[n]: a [rows, depth], w [cols, depth] int8 (-128 is allowed), bias
  *     [cols] fp32 or NULL, y [rows, cols] out_dtype.  The sum is exact, the rest
  *     fp32, rounded once.
- *   gdnq_int8_linear: the same with a = the codes of x [rows, depth] in_dtype,
+ *   gdnq_int_linear: the same with a = the codes of x [rows, depth] in_dtype,
  *     quantized in the call's workspace.
  *   0 <= rows <= 2^30; 1 <= cols <= 2^25; depth a multiple of 16, 16 .. 2^17 - 16
  *   (the sums fit 32 bits); ceil(rows / 256) ceil(cols / 256) < 2^24.  in_dtype
- *   is not read by gdnq_int8_matmul.  flags must be 0.
- *   workspace: gdnq_int8_workspace_size(p) bytes for gdnq_int8_linear.
+ *   is not read by gdnq_int_matmul.  flags must be 0.
+ *   workspace: gdnq_int_workspace_size(p) bytes for gdnq_int_linear.
  *   Errors: NULL, SHAPE, DTYPE, ALIGN, ALIAS, FLAGS, WORKSPACE, HIP.
  * ------------------------------------------------------------------------ */
 typedef struct {
   int32_t rows, cols, depth, in_dtype, out_dtype;
   uint32_t flags;
-} gdnq_int8_params;
+} gdnq_int_params;
 
-gdnq_status gdnq_int8_quantize(const void* x, int64_t rows, int32_t depth, int32_t dtype, int8_t* codes,
+gdnq_status gdnq_int_quantize(const void* x, int64_t rows, int32_t depth, int32_t dtype, int8_t* codes,
                                float* scales, void* stream);
 
-gdnq_status gdnq_int8_matmul(const gdnq_int8_params* p, const int8_t* a_codes, const float* a_scales,
+gdnq_status gdnq_int_matmul(const gdnq_int_params* p, const int8_t* a_codes, const float* a_scales,
                              const int8_t* w_codes, const float* w_scales, const float* bias, void* y,
                              void* stream);
 
-size_t gdnq_int8_workspace_size(const gdnq_int8_params* p);
+size_t gdnq_int_workspace_size(const gdnq_int_params* p);
 
-gdnq_status gdnq_int8_linear(const gdnq_int8_params* p, const void* x, const int8_t* w_codes,
+gdnq_status gdnq_int_linear(const gdnq_int_params* p, const void* x, const int8_t* w_codes,
                              const float* w_scales, const float* bias, void* y, void* workspace,
                              size_t workspace_bytes, void* stream);
 

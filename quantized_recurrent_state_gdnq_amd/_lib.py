@@ -41,7 +41,7 @@ EXPORTS = ("gdnq_quantize_state", "gdnq_decode_step", "gdnq_prefill_workspace_si
            "gdnq_mx_quantize", "gdnq_mx_workspace_size", "gdnq_mx_matmul", "gdnq_mx_linear",
            "gdnq_delta_workspace_size", "gdnq_delta_carry_size", "gdnq_delta_forward", "gdnq_delta_backward",
            "gdnq_delta_step", "gdnq_qk_norm", "gdnq_qk_norm_workspace_size", "gdnq_qk_norm_backward",
-           "gdnq_int8_quantize", "gdnq_int8_matmul", "gdnq_int8_workspace_size", "gdnq_int8_linear",
+           "gdnq_int_quantize", "gdnq_int_matmul", "gdnq_int_workspace_size", "gdnq_int_linear",
            "gdnq_decode_set_schedule", "gdnq_status_string", "gdnq_last_error", "gdnq_version",
            "gdnq_sync_debug")
 
@@ -172,14 +172,14 @@ def _load():
     lib.gdnq_qk_norm_workspace_size.restype = sz
     lib.gdnq_qk_norm_backward.argtypes = [ctypes.POINTER(QkParams)] + [vp] * 13 + [sz, vp]
     lib.gdnq_qk_norm_backward.restype = i32
-    lib.gdnq_int8_quantize.argtypes = [vp, i64, i32, i32, vp, vp, vp]
-    lib.gdnq_int8_quantize.restype = i32
-    lib.gdnq_int8_matmul.argtypes = [ctypes.POINTER(Int8Params)] + [vp] * 7
-    lib.gdnq_int8_matmul.restype = i32
-    lib.gdnq_int8_workspace_size.argtypes = [ctypes.POINTER(Int8Params)]
-    lib.gdnq_int8_workspace_size.restype = sz
-    lib.gdnq_int8_linear.argtypes = [ctypes.POINTER(Int8Params)] + [vp] * 6 + [sz, vp]
-    lib.gdnq_int8_linear.restype = i32
+    lib.gdnq_int_quantize.argtypes = [vp, i64, i32, i32, vp, vp, vp]
+    lib.gdnq_int_quantize.restype = i32
+    lib.gdnq_int_matmul.argtypes = [ctypes.POINTER(Int8Params)] + [vp] * 7
+    lib.gdnq_int_matmul.restype = i32
+    lib.gdnq_int_workspace_size.argtypes = [ctypes.POINTER(Int8Params)]
+    lib.gdnq_int_workspace_size.restype = sz
+    lib.gdnq_int_linear.argtypes = [ctypes.POINTER(Int8Params)] + [vp] * 6 + [sz, vp]
+    lib.gdnq_int_linear.restype = i32
     lib.gdnq_decode_set_schedule.argtypes = [i32, i32]
     lib.gdnq_decode_set_schedule.restype = i32
     lib.gdnq_status_string.argtypes = [i32]
@@ -365,17 +365,17 @@ def qk_norm_backward(params, q, k, q_weight, k_weight, positions, inv_freq, dq_o
 
 
 def int8_quantize(x, rows, depth, dtype, codes, scales, stream):
-    return lib.gdnq_int8_quantize(x, rows, depth, dtype, codes, scales, stream)
+    return lib.gdnq_int_quantize(x, rows, depth, dtype, codes, scales, stream)
 
 
 def int8_matmul(params, a_codes, a_scales, w_codes, w_scales, bias, y, stream):
-    return lib.gdnq_int8_matmul(ctypes.byref(params), a_codes, a_scales, w_codes, w_scales, bias, y, stream)
+    return lib.gdnq_int_matmul(ctypes.byref(params), a_codes, a_scales, w_codes, w_scales, bias, y, stream)
 
 
 def int8_workspace_size(params):
-    return lib.gdnq_int8_workspace_size(ctypes.byref(params))
+    return lib.gdnq_int_workspace_size(ctypes.byref(params))
 
 
 def int8_linear(params, x, w_codes, w_scales, bias, y, workspace, workspace_bytes, stream):
-    return lib.gdnq_int8_linear(ctypes.byref(params), x, w_codes, w_scales, bias, y, workspace, workspace_bytes,
+    return lib.gdnq_int_linear(ctypes.byref(params), x, w_codes, w_scales, bias, y, workspace, workspace_bytes,
                                 stream)

@@ -1133,7 +1133,7 @@ static gdnq_status int8_depth_ok(int64_t rows, int32_t depth) {
   return GDNQ_OK;
 }
 
-static gdnq_status int8_validate(const gdnq_int8_params* p, bool linear, gdnq::Int8Launch& L) {
+static gdnq_status int8_validate(const gdnq_int_params* p, bool linear, gdnq::Int8Launch& L) {
   if (!p) return fail(GDNQ_ERR_NULL, "params is NULL");
   // at most 1024 threads per 16 columns of few rows, 256 per tile of 256 x 256, fewer than 2^32 in a launch
   if (p->rows < 0 || p->cols < 1 || p->rows > (1 << 30) || p->cols > (1 << 25))
@@ -1149,7 +1149,7 @@ static gdnq_status int8_validate(const gdnq_int8_params* p, bool linear, gdnq::I
   return GDNQ_OK;
 }
 
-gdnq_status gdnq_int8_quantize(const void* x, int64_t rows, int32_t depth, int32_t dtype, int8_t* codes,
+gdnq_status gdnq_int_quantize(const void* x, int64_t rows, int32_t depth, int32_t dtype, int8_t* codes,
                                float* scales, void* stream) {
   if (gdnq_status st = int8_depth_ok(rows, depth)) return st;
   if (!dtype_ok(dtype)) return fail(GDNQ_ERR_DTYPE, "dtype = %d", dtype);
@@ -1163,18 +1163,18 @@ gdnq_status gdnq_int8_quantize(const void* x, int64_t rows, int32_t depth, int32
                                              static_cast<hipStream_t>(stream)), "int8 quantize launch", stream);
 }
 
-// The quantized activations of gdnq_int8_linear.
+// The quantized activations of gdnq_int_linear.
 static size_t int8_quantized_bytes(const gdnq::Int8Launch& L) {
   return mx_align(size_t(L.M) * L.K) + mx_align(size_t(L.M) * 4);
 }
 
-size_t gdnq_int8_workspace_size(const gdnq_int8_params* p) {
+size_t gdnq_int_workspace_size(const gdnq_int_params* p) {
   gdnq::Int8Launch L;
   if (int8_validate(p, false, L) != GDNQ_OK) return 0;
   return int8_quantized_bytes(L);
 }
 
-gdnq_status gdnq_int8_matmul(const gdnq_int8_params* p, const int8_t* a_codes, const float* a_scales,
+gdnq_status gdnq_int_matmul(const gdnq_int_params* p, const int8_t* a_codes, const float* a_scales,
                              const int8_t* w_codes, const float* w_scales, const float* bias, void* y,
                              void* stream) {
   gdnq::Int8Launch L;
@@ -1192,7 +1192,7 @@ gdnq_status gdnq_int8_matmul(const gdnq_int8_params* p, const int8_t* a_codes, c
   return launched(gdnq::launch_int8_matmul(L, static_cast<hipStream_t>(stream)), "int8 product launch", stream);
 }
 
-gdnq_status gdnq_int8_linear(const gdnq_int8_params* p, const void* x, const int8_t* w_codes,
+gdnq_status gdnq_int_linear(const gdnq_int_params* p, const void* x, const int8_t* w_codes,
                              const float* w_scales, const float* bias, void* y, void* workspace,
                              size_t workspace_bytes, void* stream) {
   gdnq::Int8Launch L;

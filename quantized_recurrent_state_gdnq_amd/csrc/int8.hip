@@ -1,5 +1,5 @@
 // Matrix product in 8-bit integers with a scale for every token and channel
-// (see gdnq_int8_* in gdnq.h): y = (A W^T) sa sw + bias, A and W codes of the
+// (see gdnq_int_* in gdnq.h): y = (A W^T) sa sw + bias, A and W codes of the
 // library's row codec, their product in whole numbers.
 #include <hip/hip_runtime.h>
 

@@ -1158,7 +1158,7 @@ def qk_norm_backward(dq_out, dk_out, q, k, q_weight=None, k_weight=None, positio
 
 
 def int8_quantize(x, codes=None, scales=None):
-    """Rows in 8-bit integers with a scale each (see gdnq_int8_quantize in
+    """Rows in 8-bit integers with a scale each (see gdnq_int_quantize in
     include/gdnq.h): x [..,depth] fp32 or bf16, depth a multiple of 16.  Returns
     (codes [..,depth] int8, scales [..] fp32)."""
     _need(x, "x", None, None)
@@ -1212,7 +1212,7 @@ def int8_workspace_size(rows, cols, depth):
 def int8_matmul(a_codes, a_scales, w_codes, w_scales, bias=None, *, out_dtype=torch.bfloat16, y=None):
     """y [..,cols] = (A W^T) a_scales w_scales + bias for rows a [..,depth] and w
     [cols,depth] as int8_quantize gives them, bias [cols] fp32 or None (see
-    gdnq_int8_matmul in include/gdnq.h)."""
+    gdnq_int_matmul in include/gdnq.h)."""
     _need(a_codes, "a_codes", torch.int8, None)
     _need(w_codes, "w_codes", torch.int8, a_codes.device)
     dev = a_codes.device

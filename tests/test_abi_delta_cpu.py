@@ -1,4 +1,4 @@
-"""Host-only checks of gdnq_delta_*, gdnq_qk_norm_* and gdnq_int8_*: bad
+"""Host-only checks of gdnq_delta_*, gdnq_qk_norm_* and gdnq_int_*: bad
 arguments are refused, with a reason, before anything is launched.
 
 Pointers are fake addresses that the host code compares but never

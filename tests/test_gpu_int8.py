@@ -1,4 +1,4 @@
-"""8-bit rows and their product (gdnq_int8_*) on the GPU: the codes against the
+"""8-bit rows and their product (gdnq_int_*) on the GPU: the codes against the
 codec's definition in the library's oracle, exactly, and the product against whole
 numbers in 64 bits: a sum of whole numbers is exact, its conversion, two scales
 and the bias are four roundings of 2^-24 (of the terms' magnitudes), and a bf16

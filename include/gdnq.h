@@ -668,9 +668,10 @@ gdnq_status gdnq_mx_linear(const gdnq_mx_params* p, const void* x, const uint8_t
  *     v, o [B,H,d_v] (in_dtype and out_dtype GDNQ_F32 or GDNQ_BF16), alpha, beta
  *     [B,H] fp32, h read and h_out written [B,H,d_v,d_k] fp32 (h_out may be h
  *     itself: the state updated in place).
- *   in_dtype of the chunked calls must be GDNQ_BF16; gdnq_delta_backward does
- *   not read out_dtype.  Products of fp32 values take them in two bf16 parts (16
- *   bits and more), sums and states are fp32; o, dq, dk and dv are rounded once.
+ *   in_dtype of the chunked calls must be GDNQ_BF16; out_dtype is o's alone.
+ *   Products of fp32 values take them in two bf16 parts (16 bits and more), sums
+ *   and states are fp32: fp32 results of the chunked calls are good to about 1e-5
+ *   of their norm.  o, dq, dk and dv are rounded once.
  *   Results do not depend on the order in which workgroups run.  A NaN or
  *   infinity stays in its own sequence and head, and reaches back at most to the
  *   first token of its chunk of 64.

@@ -48,7 +48,8 @@ __device__ __forceinline__ void load8(const bf16* p, float (&v)[8]) {
 //
 // A row per workgroup of THREADS lanes, EIGHTS times eight values a lane held in
 // registers between the largest value and the codes (EIGHTS = 0: a row longer
-// than that is read twice, the second time out of cache).
+// than that is read twice, the second time out of cache).  Bound by memory: 16384
+// rows of 4096 bf16 take 36 to 40 us, 5.1 TB/s; 64 rows 3.6.
 __device__ __forceinline__ uint2 codes8(const float (&v)[8], float scale, bool finite) {
   float c[8];
   codec_codes<8>(v, scale, c);
@@ -133,7 +134,8 @@ __device__ __forceinline__ void store4(E* y, int M, int N, int m, int n, const f
 //
 // A workgroup computes 16 columns of 16 MT rows, the depth split over its
 // waves; every lane loads whole 16-byte blocks of the weights straight into the
-// instruction's operand (lane l: row l % 16, block l / 16 of 16 x 64).
+// instruction's operand (lane l: row l % 16, block l / 16 of 16 x 64).  Bound by the
+// latency of these loads: 16 x 4096 x 4096 takes 8.2 us, its weights 3.3 at a copy's rate.
 template <int MT, int WAVES, int N, typename E>
 __global__ __launch_bounds__(WAVES * 64) void int8_rows_kernel(Int8Launch L, int col_tiles) {
   __shared__ i32x4 sums[WAVES][MT][64];

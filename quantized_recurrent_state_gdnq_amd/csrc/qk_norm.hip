@@ -11,6 +11,9 @@
 // a team of 8 .. 64 lanes.  A workgroup takes a few tokens at a time, puts the
 // sines and cosines of their angles into LDS (one of each per token and pair, for
 // all its heads), and its teams take the tokens' rows in turn.
+//   Bound by memory where there is work: 32768 tokens of 40 heads of 128, all columns
+// turned, bf16, take 137 us forward (4.9 TB/s) and 222 back (4.5), a large copy
+// 5.14 TB/s; 64 tokens of 32 heads take 6.2, a launch and two dependent loads.
 //   WIDE: rows of a multiple of 8 columns, 16-byte aligned: a lane holds eight
 // adjacent columns, and partners half the rotated columns apart are in another
 // lane's same register where that half is a multiple of 8.  Else a lane holds

@@ -680,7 +680,8 @@ gdnq_status gdnq_mx_linear(const gdnq_mx_params* p, const void* x, const uint8_t
  *   need no initial value.  Calls that may overlap in time take workspaces of
  *   their own.
  *   B >= 0, T >= 0, at most 2^31 - 1 tokens, 64-token chunks (of all sequences;
- *   packed: T / 64 + B) times H < 2^24, B H ceil(d_v / 64) < 2^24.
+ *   packed: T / 64 + B) times H < 2^24, B H ceil(d_v / 64) < 2^24; chunked calls
+ *   G d_k < 2^25 and H d_v < 2^25.
  *   Errors: NULL, SHAPE, DTYPE, ALIGN (cu_seqlens: 4 bytes), ALIAS, FLAGS,
  *   WORKSPACE, HIP.
  * ------------------------------------------------------------------------ */

@@ -916,6 +916,9 @@ static gdnq_status delta_validate(const gdnq_delta_params* p, bool varlen, bool 
   L.out_bf16 = p->out_dtype == GDNQ_BF16;
   L.log_decay = (p->flags & GDNQ_DELTA_LOG) != 0;
   if (L.N > 0x7fffffffLL) return fail(GDNQ_ERR_SHAPE, "%lld tokens: at most 2^31 - 1", (long long)L.N);
+  // the kernels' offsets inside a chunk of 64 tokens are 32 bits
+  if (!step && (int64_t(L.G) * L.dk >= 1 << 25 || int64_t(L.H) * L.dv >= 1 << 25))
+    return fail(GDNQ_ERR_SHAPE, "%d key heads of %d, %d heads of %d: too large, fewer than 2^25 values a token", L.G, L.dk, L.H, L.dv);
   // a workgroup of 256 threads per chunk and head, and per 64 rows of a state (a
   // step: per four), and a launch has fewer than 2^32 threads
   const int64_t slots = varlen ? L.N / 64 + L.B : int64_t(L.B) * ((int64_t(L.T) + 63) / 64);

@@ -354,6 +354,7 @@ struct ChainLoader {
   int64_t krow, vrow, chunk_stride;
   int dk, cols, wave, lane;
   bool exact;                     // no columns of K to be zero
+  uint32_t beyond;                // else bit i: the lane's block of load i is such a column
 
   __device__ __forceinline__ void init(const DeltaLaunch& L, const void* values, int h, int group, int wave_, int lane_) {
     wave = wave_;
@@ -370,10 +371,12 @@ struct ChainLoader {
     space = static_cast<const uint8_t*>(L.workspace) + int64_t(h) * DELTA_CHUNK_BYTES;
     chunk_stride = int64_t(L.H) * DELTA_CHUNK_BYTES;
     int row, block;
+    beyond = 0;
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
       lds_place<DK>((i * 4 + wave) * 64 + lane, row, block);
       at_k[i] = uint32_t(row) * uint32_t(krow) + block * 16;
+      beyond |= uint32_t(block * 8 >= dk) << i;
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -389,7 +392,7 @@ struct ChainLoader {
     bool whole;
   };
   __device__ __forceinline__ Next next(int64_t first, int n, int64_t slot) const {
-    return {space + slot * chunk_stride, k + first * krow, q + first * krow, v + first * vrow, n, exact && n == 64};
+    return {space + slot * chunk_stride, k + first * krow, q + first * krow, v + first * vrow, n, n == 64};
   }
 
   // A whole chunk's loads are made in STEPS parts of one or two, between the
@@ -399,8 +402,10 @@ struct ChainLoader {
   template <int STEP, bool BARE>
   __device__ __forceinline__ void step(ChainBuffer<DK, BARE>& to, const Next& x) const {
     if constexpr (STEP < LOADS) {
-      to_lds(x.k, at_k[STEP], to.k + (STEP * 4 + wave) * 1024);
-      if constexpr (!BARE) to_lds(x.q, at_k[STEP], to.q + (STEP * 4 + wave) * 1024);
+      if (exact || !(beyond >> STEP & 1)) {  // lanes of columns beyond the last write nothing
+        to_lds(x.k, at_k[STEP], to.k + (STEP * 4 + wave) * 1024);
+        if constexpr (!BARE) to_lds(x.q, at_k[STEP], to.q + (STEP * 4 + wave) * 1024);
+      }
     } else if constexpr (STEP == LOADS) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) to_lds(x.v, at_v[i], to.v + (i * 4 + wave) * 1024);
@@ -411,6 +416,20 @@ struct ChainLoader {
     } else {
       if (wave == 0) to_lds(x.ws + DELTA_SCALARS, lane * 16, to.rows);
     }
+  }
+
+  // The columns beyond the last, zero in both buffers before the first load, so that
+  // their chunks too are loaded in steps (1003 tokens, heads of 72: chain 52 -> 49 us).
+  template <bool BARE>
+  __device__ __forceinline__ void clear(ChainBuffer<DK, BARE>& to) const {
+    if (exact) return;
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i)
+      if (beyond >> i & 1) {
+        const int at = (i * 4 + wave) * 1024 + lane * 16;
+        *reinterpret_cast<u32x4*>(to.k + at) = u32x4{0, 0, 0, 0};
+        if constexpr (!BARE) *reinterpret_cast<u32x4*>(to.q + at) = u32x4{0, 0, 0, 0};
+      }
   }
 
   // Any chunk at once.  Rows behind the last token are the last one's again (beta

@@ -60,6 +60,8 @@ __global__ __launch_bounds__(256, PASS ? 2 : 1) void delta_chain_kernel(DeltaLau
     if (item.seg > 0) start = reinterpret_cast<const float*>(delta_segment(L, int(item.at) + item.seg - 1, h));
     chain_load_state<TILES>(S, start, L.dk, col, mine, g);
   }
+  loader.clear(buffers[0]);
+  loader.clear(buffers[1]);
   if (place.first < end)
     loader.template load<false, PASS>(buffers[place.first & 1], loader.next(s.first + int64_t(place.first) * 64,
                                                                      min(64, s.tokens - place.first * 64), s.slot + place.first));

@@ -50,6 +50,8 @@ __global__ __launch_bounds__(256, 1) void delta_chain_back_kernel(DeltaLaunch L,
     if (place.end < chunks) start = reinterpret_cast<const float*>(delta_segment(L, int(item.at) + item.seg + 1, h));
     chain_load_state<TILES>(S, start, L.dk, col, mine, g);
   }
+  loader.clear(buffers[0]);
+  loader.clear(buffers[1]);
   if (count > 0)
     loader.template load<true, false>(buffers[0], loader.next(s.first + int64_t(last) * 64, min(64, s.tokens - last * 64), s.slot + last));
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");

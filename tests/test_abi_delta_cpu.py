@@ -147,6 +147,19 @@ def test_delta_launch_limit(B, T, H, dv, fits):
         refused(backward(p), SHAPE, "too large")
 
 
+@pytest.mark.parametrize("H,dk,dv,fits", [
+    (2 ** 18 - 1, 128, 8, True), (2 ** 18, 128, 8, False), (2 ** 15 - 1, 8, 1024, True), (2 ** 15, 8, 1024, False)])
+def test_delta_offsets_inside_a_chunk(H, dk, dv, fits):
+    """64 tokens of fewer than 2^25 bf16 values each are less than 2^32 bytes."""
+    p = delta_p(B=1, T=64, G=H, H=H, dk=dk, dv=dv)
+    if fits:
+        refused(forward(p, o=addr(20) + 8), ALIGN, "o")
+    else:
+        refused(forward(p), SHAPE, "2^25")
+        refused(backward(p), SHAPE, "2^25")
+    refused(step(delta_p(B=1, T=1, G=H, H=H, dk=dk, dv=dv), o=None), NULL, "o")
+
+
 # ---------------------------------------------------------------- norms of queries and keys
 
 def qk_p(R=10, Hq=4, Hk=2, D=64, rotary=32, dtype=1, eps=1e-6, flags=0, qs=None, ks=None):

@@ -69,7 +69,7 @@ __host__ __device__ inline int left_place(int row, int block, int times) {
 // one joins them, and the chains then start from the states that enter.  That is
 // 2.3 times the work (without the outputs, 82 of 132 products a chunk and row),
 // so it pays where chains leave three in four of the 256 CUs idle: 65536 tokens,
-// 8 heads, 16 workgroups: the call takes 3.3 ms in one piece, 0.59 cut.
+// 8 heads, 16 workgroups: the call takes 3.3 ms in one piece, 0.56 cut.
 //   Packed sequences differ: those of more than `split_above` chunks, three times what
 // a CU's share of all chunks would be, are cut into segments of that share (their
 // lengths are known on the device alone).  16384 tokens, 16 heads, forward: 16000 and 20 of

@@ -53,3 +53,63 @@ def test_workspace_alone_is_written():
     _, _, carry = ops.delta_rule(**d, cu_seqlens=cu, save=True, workspace=ws)
     ops.delta_rule_backward(more["do"], d["q"], d["k"], d["v"], d["alpha"], d["beta"], carry, d["h0"], cu_seqlens=cu, workspace=ws_back)
     assert (ws[need:] == 0xA5).all() and (ws_back[need_back:] == 0xA5).all()
+
+
+def test_arrays_beyond_32_bits():
+    """Values of more than 2^32 bytes, what is left of the chunks of more: the last
+    sequence's results are, bit for bit, those of a call of its own."""
+    N, n, G, H, d = 66000, 200, 2, 256, 128
+    g = torch.Generator(device=DEV).manual_seed(2)
+    rand = lambda *s: torch.rand(s, generator=g, device=DEV)  # noqa: E731
+    q, k = [torch.nn.functional.normalize(rand(N, G, d) - 0.5, dim=-1).bfloat16() for _ in range(2)]
+    v, do = [torch.empty((N, H, d), dtype=torch.bfloat16, device=DEV).normal_(generator=g) for _ in range(2)]
+    alpha, beta = 1 - 0.1 * rand(N, H), rand(N, H)
+    assert v.numel() * 2 > 2 ** 32
+
+    def call(first, offsets):
+        cu = torch.tensor(offsets, dtype=torch.int32, device=DEV)
+        a = [t[first:] for t in (q, k, v, alpha, beta)]
+        o, h, carry = ops.delta_rule(*a, cu_seqlens=cu, save=True)
+        grads = ops.delta_rule_backward(do[first:], *a, carry, cu_seqlens=cu)
+        return [t[-n:].clone() for t in (o, *grads[:5])] + [h[-1].clone()]
+
+    for x, y in zip(call(0, [0, N - n, N]), call(N - n, [0, n])):
+        assert torch.isfinite(x).all() and torch.equal(x, y)
+
+
+def test_replayed_with_other_offsets():
+    """The offsets are read on the device: a captured call follows what they hold, whatever is cut then."""
+    N = 2600
+    d, more = inputs((N,), 2, 4, 64, 64, 3)
+    offsets = [[0, 900, 1800, N], [0, 0, 2599, N], [10, 1200, 1201, 2500], [0, 100, 164, N]]
+    cu = torch.tensor(offsets[0], dtype=torch.int32, device=DEV)
+    out = {n: torch.zeros_like(t) for n, t in (("o", d["v"]), ("dq", d["q"]), ("dk", d["k"]), ("dv", d["v"]),
+                                               ("dalpha", d["alpha"]), ("dbeta", d["beta"]), ("dh0", d["h0"]), ("h_last", d["h0"]))}
+
+    def call():
+        _, _, carry = ops.delta_rule(**d, cu_seqlens=cu, save=True, o=out["o"], h_last=out["h_last"])
+        ops.delta_rule_backward(more["do"], d["q"], d["k"], d["v"], d["alpha"], d["beta"], carry, d["h0"], more["dh_last"], cu,
+                                **{n: out[n] for n in ("dq", "dk", "dv", "dalpha", "dbeta", "dh0")})
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for values in offsets + offsets[::-1]:
+        cu.copy_(torch.tensor(values, dtype=torch.int32))
+        for t in out.values():
+            t.zero_()
+        call()
+        want = {n: t.clone() for n, t in out.items()}
+        for t in out.values():
+            t.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for n, t in out.items():
+            assert torch.equal(t, want[n]), (values, n)

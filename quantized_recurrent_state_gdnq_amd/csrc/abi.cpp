@@ -1028,6 +1028,8 @@ static gdnq_status qk_validate(const gdnq_qk_params* p, gdnq::QkLaunch& L) {
   if (!p) return fail(GDNQ_ERR_NULL, "params is NULL");
   if (p->rows < 0 || p->q_heads < 1 || p->k_heads < 1 || p->width < 1 || p->width > 512)
     return fail(GDNQ_ERR_SHAPE, "rows = %d, q_heads = %d, k_heads = %d, width = %d (1 .. 512)", p->rows, p->q_heads, p->k_heads, p->width);
+  // a workgroup of 256 threads per eight tokens, fewer than 2^32 in a launch
+  if (p->rows > (1 << 27) - 8) return fail(GDNQ_ERR_SHAPE, "rows = %d: at most 2^27 - 8", p->rows);
   // in 64 bits: the heads' sum alone may pass 32
   const int64_t heads = int64_t(p->q_heads) + p->k_heads;
   if (heads > (1 << 20) || heads * p->rows > 0x7fffffffLL)

@@ -192,6 +192,15 @@ def test_qk_parameters(p, code):
     assert _lib.qk_norm_workspace_size(p) == 0
 
 
+@pytest.mark.parametrize("R,fits", [(2 ** 27 - 8, True), (2 ** 27 - 7, False), (2 ** 29, False)])
+def test_qk_launch_limit(R, fits):
+    """Fewer than 2^24 workgroups of 256 threads, eight tokens each."""
+    p = qk_p(R=R, Hq=1, Hk=1, D=1, rotary=0)
+    assert (_lib.qk_norm_workspace_size(p) > 0) == fits
+    for st in (qk(p, pos=None, freq=None, q_out=None), qk_backward(p, pos=None, freq=None, dq=None)):
+        assert st == (NULL if fits else SHAPE)
+
+
 def test_qk_pointers():
     p = qk_p()
     for name, word in (("q", "q"), ("k", "k"), ("pos", "positions"), ("freq", "inv_freq")):

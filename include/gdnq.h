@@ -721,10 +721,10 @@ gdnq_status gdnq_delta_step(const gdnq_delta_params* p, const void* q, const voi
  *   Pair i is columns (i, i + rotary / 2), or (2i, 2i + 1) with
  *   GDNQ_QK_INTERLEAVED.
  *
- *   p->rows R tokens, 0 .. 2^27 - 8, p->q_heads, p->k_heads >= 1, in all at most
- *   2^20, R (q_heads + k_heads) <= 2^31 - 1, p->width D in 1 .. 512 (a multiple of 8 is faster), p->rotary even,
- *   0 .. D (a multiple of 16 is faster); p->dtype (q, k, results and gradients)
- *   GDNQ_F32 or GDNQ_BF16; p->eps >= 0, finite.
+ *   p->rows R tokens, 0 .. 2^27 - 8; p->q_heads, p->k_heads >= 1, in all at most
+ *   2^20, R (q_heads + k_heads) <= 2^31 - 1; p->width D in 1 .. 512 (a multiple of
+ *   8 is faster); p->rotary even, 0 .. D (a multiple of 16 is faster); p->dtype
+ *   (q, k, results and gradients) GDNQ_F32 or GDNQ_BF16; p->eps >= 0, finite.
  *     q, k       rows of [q_heads, D] and [k_heads, D], dense, q_stride and
  *                k_stride elements apart (at least a row: views of a fused
  *                projection's rows).  These two need only their type's

@@ -438,7 +438,7 @@ def _codes(x):
     """Rows in 8 bits: the scale is a 127th of the largest value, a code the
     nearest whole number to value / scale, half-way ones to the even one."""
     x = x.float()
-    scales = x.abs().amax(-1) / 127.0
+    scales = x.abs().amax(-1) / torch.full((), 127.0, device=x.device)  # by a number it would be a product with 1 / 127
     codes = torch.round(x / torch.where(scales > 0, scales, torch.ones_like(scales)).unsqueeze(-1))
     return codes.clamp(-127, 127).to(torch.int8), scales
 

@@ -669,9 +669,13 @@ gdnq_status gdnq_mx_linear(const gdnq_mx_params* p, const void* x, const uint8_t
  *     [B,H] fp32, h read and h_out written [B,H,d_v,d_k] fp32 (h_out may be h
  *     itself: the state updated in place).
  *   in_dtype of the chunked calls must be GDNQ_BF16; out_dtype is o's alone.
- *   Products of fp32 values take them in two bf16 parts (16 bits and more), sums
- *   and states are fp32: fp32 results of the chunked calls are good to about 1e-5
- *   of their norm.  o, dq, dk and dv are rounded once.
+ *   Products of fp32 values take them in bf16 parts, sums and states are fp32.
+ *   Three parts (24 bits) where a state or a gradient of h0, alpha or beta comes of
+ *   it, but two (16 bits) for a chunk's inverse triangle: h_last, dh0, dalpha and
+ *   dbeta of the chunked calls are good to about 1e-6 of their norm (keys of length
+ *   1; times the norm of that inverse where it is large).  Two for o, dq,
+ *   dk and dv, rounded once (o in fp32: good to 5e-6), and for what enters a segment
+ *   where a call cuts long sequences: 5e-6.
  *   Results do not depend on the order in which workgroups run.  A NaN or
  *   infinity stays in its own sequence and head, and reaches back at most to the
  *   first token of its chunk of 64.

@@ -16,8 +16,11 @@
 // and each of their rows by itself: a wave carries 16 rows.
 //
 // Operands of the products are bf16: q, k, v and dO as they are, fp32 values in
-// two parts, hi = bf16(x) and lo = bf16(x - hi), 16 to 17 significant bits; the
-// product of two lo parts (2^-18 of the term) is left out.  Sums are fp32.
+// parts, bf16(x), bf16(x less that) and so on.  What passes to a state, a gate's
+// gradient or the next chunk has three, 24 bits and more; the inverse two, 16 to 17
+// bits, and so does what goes to a bf16 result alone (M, O's S and w, dM and dAt).
+// Products of parts beyond the longer operand's last (2^-25 of a term of three, 2^-18
+// of two) are left out.  Sums are fp32.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -36,45 +39,49 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int DELTA_CHUNK = 64;
 // A triangle of 64 x 64 as the first operand of a product: of its 16 x 32
-// blocks six are not zero.  A block is 64 lanes of 16 bytes; hi parts, then lo.
+// blocks six are not zero.  A block is 64 lanes of 16 bytes; a part lies behind another.
 constexpr int TRI_BLOCKS = 6, TRI_PART = TRI_BLOCKS * 1024, TRI_BYTES = 2 * TRI_PART;
-// Of one chunk of one value head in the workspace: two such triangles, then
-// rows of 64: c, beta c_64 / c, c_64 / c, beta c (the chains' kilobyte), beta, and
-// log2 c as a whole number and a rest.
-constexpr int DELTA_SCALARS = 2 * TRI_BYTES;
+// Of one chunk of one value head in the workspace: two such triangles (the backward
+// pass's second in three parts), then rows of 64: c, beta c_64 / c, c_64 / c, beta c
+// (the chains' kilobyte), beta, and log2 c as a whole number and a rest.
+__host__ __device__ constexpr int delta_scalars(bool back) { return (back ? 5 : 4) * TRI_PART; }
 enum { ROW_C, ROW_TAIL_BETA, ROW_TAIL, ROW_C_BETA, ROW_BETA, ROW_WHOLE, ROW_REST, ROWS };
-constexpr int DELTA_CHUNK_BYTES = DELTA_SCALARS + 8 * 256;
+__host__ __device__ constexpr int delta_chunk_bytes(bool back) { return delta_scalars(back) + 8 * 256; }
 
 inline int64_t delta_slots(const DeltaLaunch& L) {
   return L.cu_seqlens ? L.N / DELTA_CHUNK + L.B : int64_t(L.B) * ((int64_t(L.T) + DELTA_CHUNK - 1) / DELTA_CHUNK);
 }
 __host__ __device__ inline int64_t delta_align(int64_t n) { return (n + 255) / 256 * 256; }
-// What a chain leaves of a chunk and head: a state in two bf16 parts, and behind it
-// the chunk's w or z, [2][d_v][64].  Each part is in tiles of 16 rows and 32
-// columns, a kilobyte: a store of a wave (16 rows x 32 columns) is then whole lines
-// (rows as they are leave half a line each: 4 x 8192 tokens, 16 heads, chain 617 us,
-// with tiles 542).
-__host__ __device__ inline int64_t delta_part(const DeltaLaunch& L) { return int64_t((L.dv + 15) / 16) * ((L.dk + 31) / 32) * 512; }
-__host__ __device__ inline int64_t delta_left_bytes(const DeltaLaunch& L) {
-  return delta_part(L) * 4 + int64_t((L.dv + 15) / 16) * 4096;
+// What a chain leaves of a chunk and head, in fp32: a state, and behind it the
+// chunk's w or z, [d_v][64].  Both are in tiles of 16 rows and 16 columns, a kilobyte,
+// the columns those of a chain's tile (chain_row): a store of a wave is then whole
+// lines (rows as they are leave half a line each: 4 x 8192 tokens, 16 heads, chain 617
+// us, with tiles 542).
+__host__ __device__ inline int64_t delta_state_floats(const DeltaLaunch& L) {
+  return int64_t((L.dv + 15) / 16) * ((L.dk + 31) / 32) * 512;
 }
-// Where block `block` (8 columns) of a row is, in bf16, of rows of so many times 32 columns.
-__host__ __device__ inline int left_place(int row, int block, int times) {
-  return ((row >> 4) * times + (block >> 2)) * 512 + (row & 15) * 32 + (block & 3) * 8;
+__host__ __device__ inline int64_t delta_left_bytes(const DeltaLaunch& L) {
+  return delta_state_floats(L) * 4 + int64_t((L.dv + 15) / 16) * 4096;
+}
+// Where, in floats, a lane's four values of a tile are, of rows of so many tiles.
+__host__ __device__ inline int left_place(int row, int tile, int tiles, int g) {
+  return ((row >> 4) * tiles + tile) * 256 + (row & 15) * 16 + g * 4;
 }
 
 // Few chains of many chunks are cut into segments that run at once.  A segment
 // maps the state that enters it linearly, S' = S P + R: a first pass carries R
 // from zero and P from the identity (d_k more rows, without V and O), a second
 // one joins them, and the chains then start from the states that enter.  That is
-// 2.3 times the work (without the outputs, 82 of 132 products a chunk and row),
-// so it pays where chains leave three in four of the 256 CUs idle: 65536 tokens,
-// 8 heads, 16 workgroups: the call takes 3.3 ms in one piece, 0.56 cut.
+// 1.9 times the work (without the outputs, and with two parts of each value, 82 of
+// 176 products a chunk and row), so it pays where chains leave three in four of the
+// 256 CUs idle: 65536 tokens, 8 heads, 16 workgroups: the call takes 3.3 ms in one
+// piece, 0.65 cut.  What enters a segment is good to the two parts' bits, 5e-6 of its
+// norm; three would be half as many products again in both passes.
 //   Packed sequences differ: those of more than `split_above` chunks, three times what
 // a CU's share of all chunks would be, are cut into segments of that share (their
-// lengths are known on the device alone).  16384 tokens, 16 heads, forward: 16000 and 20 of
-// 200 723 -> 401 us; 10000, 4000, 1500 and 884 466 -> 361; where none is long enough
-// the two empty launches cost 8.  Twice and half the share: 425 for the second.
+// lengths are known on the device alone).  16384 tokens, 16 heads, forward: one of all
+// 873 -> 316 us; 10000, 4000, 1500 and 884 570 -> 371; where none is long enough the two
+// empty launches cost 8 to 10 of 230.  Twice and half the share: 356 and 455.
 //   In the workspace for each segment of a cut sequence and each head: R (then the
 // state behind the segment) [d_v][d_k] fp32, P [2][d_k][d_k] in two bf16 parts.
 constexpr int DELTA_ORDERED = 64;  // packed sequences that a wave puts in order
@@ -265,7 +272,7 @@ __device__ __forceinline__ bf16x8 lds_transposed(const uint8_t* a, const uint8_t
   return __builtin_bit_cast(bf16x8, s16x8{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]});
 }
 
-// Two products of fp32 values in parts.
+// Products of fp32 values in two parts.
 __device__ __forceinline__ f32x4 mfma_exact_split(const bf16x8& a, const bf16x8& bh, const bf16x8& bl, f32x4 c) {
   return mfma16(a, bh, mfma16(a, bl, c));
 }
@@ -274,20 +281,41 @@ __device__ __forceinline__ f32x4 mfma_split_split(const bf16x8& ah, const bf16x8
   return mfma16(ah, bh, mfma16(ah, bl, mfma16(al, bh, c)));
 }
 
-// Eight values in two parts; by pairs, six instructions each.
-__device__ __forceinline__ void split8(const f32x4& a, const f32x4& b, bf16x8& hi, bf16x8& lo) {
-  u32x4 h, l;
+// Two values in P parts, five instructions for each part but the last.
+template <int P>
+__device__ __forceinline__ void split_pair(f32x2 x, uint32_t (&parts)[P]) {
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    parts[p] = __builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf16x2));
+    if (p + 1 == P) break;
+    uint32_t word = parts[p];
+    asm("" : "+v"(word));  // or the compiler rounds each value again to have it by itself
+    x = f32x2{x[0] - __uint_as_float(word << 16), x[1] - __uint_as_float(word & 0xffff0000u)};
+  }
+}
+// Eight values in P parts.
+template <int P>
+__device__ __forceinline__ void split8(const f32x4& a, const f32x4& b, bf16x8 (&x)[P]) {
+  u32x4 words[P];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const f32x2 x = i < 2 ? f32x2{a[2 * i], a[2 * i + 1]} : f32x2{b[2 * i - 4], b[2 * i - 3]};
-    h[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf16x2));
-    uint32_t word = h[i];
-    asm("" : "+v"(word));  // or the compiler rounds each value again to have it by itself
-    const f32x2 rest = {x[0] - __uint_as_float(word << 16), x[1] - __uint_as_float(word & 0xffff0000u)};
-    l[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(rest, bf16x2));
+    uint32_t parts[P];
+    split_pair(i < 2 ? f32x2{a[2 * i], a[2 * i + 1]} : f32x2{b[2 * i - 4], b[2 * i - 3]}, parts);
+#pragma unroll
+    for (int p = 0; p < P; ++p) words[p][i] = parts[p];
   }
-  hi = __builtin_bit_cast(bf16x8, h);
-  lo = __builtin_bit_cast(bf16x8, l);
+#pragma unroll
+  for (int p = 0; p < P; ++p) x[p] = __builtin_bit_cast(bf16x8, words[p]);
+}
+// f(i, j) for the parts of a product of PA and PB that are not left out, the
+// smallest terms first.
+template <int PA, int PB, typename F>
+__device__ __forceinline__ void part_terms(F&& f) {
+  constexpr int N = PA > PB ? PA : PB;
+  each<N * PA>([&](auto n) {
+    constexpr int i = PA - 1 - n.value % PA, j = N - 1 - n.value / PA - i;
+    if constexpr (j >= 0 && j < PB) f(Int<i>{}, Int<j>{});
+  });
 }
 
 // 2^(a - b) of numbers given as whole part and rest.
@@ -310,13 +338,13 @@ __device__ __forceinline__ int chain_row(int tile, int row) {
 // that each lane loads from.
 // The first pass over segments of the forward call needs neither Q nor the second
 // triangle, and two of its workgroups fit a CU.
-template <int DK, bool BARE = false>
+template <int DK, bool BACK, bool BARE>
 struct ChainBuffer {
-  static constexpr int TRI_PIECES = 2 * TRI_BYTES / 1024;
-  uint8_t k[64 * DK * 2], q[64 * DK * 2], tri[2 * TRI_BYTES], v[64 * 128], rows[1024];
+  static constexpr int TRI_PIECES = delta_scalars(BACK) / 1024;
+  uint8_t k[64 * DK * 2], q[64 * DK * 2], tri[delta_scalars(BACK)], v[64 * 128], rows[1024];
 };
-template <int DK>
-struct ChainBuffer<DK, true> {
+template <int DK, bool BACK>
+struct ChainBuffer<DK, BACK, true> {
   static constexpr int TRI_PIECES = TRI_BYTES / 1024;
   uint8_t k[64 * DK * 2], tri[TRI_BYTES], v[64 * 128], rows[1024];
 };
@@ -345,9 +373,11 @@ __device__ __forceinline__ void lds_place(int p, int& row, int& block) {
   block = (lds_block<D>(row, p % (D / 8)) >> 4) % (D / 8);
 }
 
-template <int DK>
+template <int DK, bool BACK>
 struct ChainLoader {
   static constexpr int LOADS = 64 * (DK / 8) / 256;
+  template <bool BARE>
+  using Buffer = ChainBuffer<DK, BACK, BARE>;
   uint32_t at_k[LOADS], at_v[2];  // byte offsets in a whole chunk
   const uint8_t *k, *q, *v;       // of the call's first token, this head, this group of columns
   const uint8_t* space;           // the workspace at this head
@@ -368,8 +398,8 @@ struct ChainLoader {
     q = static_cast<const uint8_t*>(L.q) + int64_t(kh) * L.dk * 2;
     v = static_cast<const uint8_t*>(values) + (int64_t(h) * L.dv + group * 64) * 2;
     cols = min(64, L.dv - group * 64);
-    space = static_cast<const uint8_t*>(L.workspace) + int64_t(h) * DELTA_CHUNK_BYTES;
-    chunk_stride = int64_t(L.H) * DELTA_CHUNK_BYTES;
+    space = static_cast<const uint8_t*>(L.workspace) + int64_t(h) * delta_chunk_bytes(BACK);
+    chunk_stride = int64_t(L.H) * delta_chunk_bytes(BACK);
     int row, block;
     beyond = 0;
 #pragma unroll
@@ -398,9 +428,10 @@ struct ChainLoader {
   // A whole chunk's loads are made in STEPS parts of one or two, between the
   // products of the chunk before: all at once they hold the wave up until the
   // queue has room (2600 of a chunk's 8100 cycles).
-  static constexpr int STEPS = LOADS + 5;
+  static constexpr int TRI_STEPS = (delta_scalars(BACK) / 1024 + 7) / 8, STEPS = LOADS + 1 + TRI_STEPS + 1;
   template <int STEP, bool BARE>
-  __device__ __forceinline__ void step(ChainBuffer<DK, BARE>& to, const Next& x) const {
+  __device__ __forceinline__ void step(Buffer<BARE>& to, const Next& x) const {
+    constexpr int PIECES = Buffer<BARE>::TRI_PIECES;
     if constexpr (STEP < LOADS) {
       if (exact || !(beyond >> STEP & 1)) {  // lanes of columns beyond the last write nothing
         to_lds(x.k, at_k[STEP], to.k + (STEP * 4 + wave) * 1024);
@@ -409,19 +440,20 @@ struct ChainLoader {
     } else if constexpr (STEP == LOADS) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) to_lds(x.v, at_v[i], to.v + (i * 4 + wave) * 1024);
-    } else if constexpr (STEP < LOADS + 4) {
+    } else if constexpr (STEP < LOADS + 1 + TRI_STEPS) {
 #pragma unroll
-      for (int i = (STEP - LOADS - 1) * 2; i < (STEP - LOADS) * 2 && i * 4 < to.TRI_PIECES; ++i)
-        to_lds(x.ws, (i * 4 + wave) * 1024 + lane * 16, to.tri + (i * 4 + wave) * 1024);
+      for (int i = (STEP - LOADS - 1) * 2; i < (STEP - LOADS) * 2 && i * 4 < PIECES; ++i)
+        if (i * 4 + 4 <= PIECES || i * 4 + wave < PIECES)
+          to_lds(x.ws, (i * 4 + wave) * 1024 + lane * 16, to.tri + (i * 4 + wave) * 1024);
     } else {
-      if (wave == 0) to_lds(x.ws + DELTA_SCALARS, lane * 16, to.rows);
+      if (wave == 0) to_lds(x.ws + delta_scalars(BACK), lane * 16, to.rows);
     }
   }
 
   // The columns beyond the last, zero in both buffers before the first load, so that
   // their chunks too are loaded in steps (1003 tokens, heads of 72: chain 52 -> 49 us).
   template <bool BARE>
-  __device__ __forceinline__ void clear(ChainBuffer<DK, BARE>& to) const {
+  __device__ __forceinline__ void clear(Buffer<BARE>& to) const {
     if (exact) return;
 #pragma unroll
     for (int i = 0; i < LOADS; ++i)
@@ -435,11 +467,8 @@ struct ChainLoader {
   // Any chunk at once.  Rows behind the last token are the last one's again (beta
   // is 0 there), or zeros where ZERO_V; columns behind the last are zero.
   template <bool ZERO_V, bool BARE>
-  __device__ __forceinline__ void load(ChainBuffer<DK, BARE>& to, const Next& x) const {
-    step<LOADS + 1>(to, x);
-    step<LOADS + 2>(to, x);
-    step<LOADS + 3>(to, x);
-    step<LOADS + 4>(to, x);
+  __device__ __forceinline__ void load(Buffer<BARE>& to, const Next& x) const {
+    each<STEPS - LOADS - 1>([&](auto i) { step<LOADS + 1 + i.value, BARE>(to, x); });
     int row, block;
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
@@ -478,24 +507,23 @@ __device__ __forceinline__ void chain_columns(const uint8_t* m, int lane, int ti
       f[t][j] = lds_transposed(m + lds_block<DK>(row, block) + half, m + lds_block<DK>(row + 4, block) + half);
     }
 }
-// Four tiles of S^T += columns^T x, x in parts.
-__device__ __forceinline__ void chain_update(f32x4* S, const bf16x8 (&f)[4][2], const bf16x8 (&h)[2], const bf16x8 (&l)[2]) {
+// Four tiles of S^T += columns^T x, x in P parts, 32 tokens each.
+template <int P>
+__device__ __forceinline__ void chain_update(f32x4* S, const bf16x8 (&f)[4][2], const bf16x8 (&x)[2][P]) {
 #pragma unroll
-  for (int j = 0; j < 2; ++j)
+  for (int p = P - 1; p >= 0; --p)
 #pragma unroll
-    for (int t = 0; t < 4; ++t) S[t] = mfma16(f[t][j], l[j], S[t]);
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
-  for (int j = 0; j < 2; ++j)
-#pragma unroll
-    for (int t = 0; t < 4; ++t) S[t] = mfma16(f[t][j], h[j], S[t]);
+      for (int t = 0; t < 4; ++t) S[t] = mfma16(f[t][j], x[j][p], S[t]);
 }
-// The six blocks of a triangle, hi and lo.
-__device__ __forceinline__ void chain_triangle(const uint8_t* tri, int lane, bf16x8 (&h)[TRI_BLOCKS], bf16x8 (&l)[TRI_BLOCKS]) {
+// The six blocks of a triangle, in its first P parts.
+template <int P>
+__device__ __forceinline__ void chain_triangle(const uint8_t* tri, int lane, bf16x8 (&m)[P][TRI_BLOCKS]) {
 #pragma unroll
-  for (int i = 0; i < TRI_BLOCKS; ++i) {
-    h[i] = lds_frag(tri + i * 1024 + lane * 16);
-    l[i] = lds_frag(tri + TRI_PART + i * 1024 + lane * 16);
-  }
+  for (int i = 0; i < TRI_BLOCKS; ++i)
+#pragma unroll
+    for (int p = 0; p < P; ++p) m[p][i] = lds_frag(tri + p * TRI_PART + i * 1024 + lane * 16);
 }
 __device__ __forceinline__ void phase() { __builtin_amdgcn_sched_barrier(0); }
 
@@ -561,11 +589,11 @@ __device__ __forceinline__ void chain_leave(const DeltaLaunch& L, const DeltaIte
 #pragma unroll
   for (int j = 0; j < TILES / 2; ++j) {
     const int at = j * 32 + g * 8;
-    bf16x8 hi, lo;
-    split8(S[2 * j], S[2 * j + 1], hi, lo);
+    bf16x8 x[2];
+    split8(S[2 * j], S[2 * j + 1], x);
     if (at < L.dk) {
-      *reinterpret_cast<bf16x8*>(pm + row * L.dk + at) = hi;
-      *reinterpret_cast<bf16x8*>(pm + (L.dk + row) * L.dk + at) = lo;
+      *reinterpret_cast<bf16x8*>(pm + row * L.dk + at) = x[0];
+      *reinterpret_cast<bf16x8*>(pm + (L.dk + row) * L.dk + at) = x[1];
     }
   }
 }
@@ -609,9 +637,9 @@ __global__ __launch_bounds__(256) void delta_join_kernel(DeltaLaunch L, int grou
     float* state = reinterpret_cast<float*>(delta_segment(L, int(item.at) + (BACK ? steps - step : step), h));
     f32x4 R[TILES];
     chain_load_state<TILES>(R, state, L.dk, row, mine, g);
-    bf16x8 sh[KB], sl[KB];
+    bf16x8 s2[KB][2];
 #pragma unroll
-    for (int j = 0; j < KB; ++j) split8(S[2 * j], S[2 * j + 1], sh[j], sl[j]);
+    for (int j = 0; j < KB; ++j) split8(S[2 * j], S[2 * j + 1], s2[j]);
 #pragma unroll
     for (int t = 0; t < TILES; ++t) {
       f32x4 s = {0, 0, 0, 0};
@@ -620,7 +648,7 @@ __global__ __launch_bounds__(256) void delta_join_kernel(DeltaLaunch L, int grou
         const int r = j * 32 + g * 8 + (c >> 2), block = (t >> 1) * 4 + (c & 3), half = (t & 1) * 8;
         const int x = lds_block<DK>(r, block) + half, y = lds_block<DK>(r + 4, block) + half;
         const uint8_t *ph = ps[step & 1][0], *pl = ps[step & 1][1];
-        s = mfma_split_split(lds_transposed(ph + x, ph + y), lds_transposed(pl + x, pl + y), sh[j], sl[j], s);
+        s = mfma_split_split(lds_transposed(ph + x, ph + y), lds_transposed(pl + x, pl + y), s2[j][0], s2[j][1], s);
       }
       S[t] = R[t] + s;
     }

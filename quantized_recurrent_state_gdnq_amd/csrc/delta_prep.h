@@ -109,7 +109,7 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaLaunch L) {
   const int tokens = delta_slot_tokens(L, slot, first);
   if (tokens == 0) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-  uint8_t* out = static_cast<uint8_t*>(L.workspace) + (int64_t(slot) * L.H + h) * DELTA_CHUNK_BYTES;
+  uint8_t* out = static_cast<uint8_t*>(L.workspace) + (int64_t(slot) * L.H + h) * delta_chunk_bytes(BACK);
 
   // The decays, as log2 in 64 bits and then as a whole number and a rest, so
   // that the ratio of two tokens is good to fp32 whatever lies before them.  A
@@ -131,7 +131,7 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaLaunch L) {
     rest[lane] = r;
     whole[lane] = wi;
     beta[lane] = bt;
-    float* sc = reinterpret_cast<float*>(out + DELTA_SCALARS) + lane;
+    float* sc = reinterpret_cast<float*>(out + delta_scalars(BACK)) + lane;
     const float c1 = exp2_difference(r, wi, 0.0f, 0), tail = exp2_difference(__shfl(r, 63), __shfl(wi, 63), r, wi);
     sc[ROW_C * 64] = c1;
     sc[ROW_TAIL_BETA * 64] = tail * bt;
@@ -204,11 +204,12 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaLaunch L) {
       const int r = BACK ? at + e : row, k = BACK ? row : at + e;  // at + e all lie in one tile
       x[e] = (at >> 4) > (row >> 4) == BACK || (at >> 4) == (row >> 4) ? from[prep_tile(r >> 4, k >> 4) + (r & 15) * PREP_PITCH + (k & 15)] : 0.0f;
     }
-    bf16x8 hi, lo;
-    split2(x, hi, lo);
+    bf16x8 parts[3];
+    split3(x, parts[0], parts[1], parts[2]);
     uint8_t* to = out + (f < TRI_BLOCKS ? 0 : TRI_BYTES) + block * 1024 + lane * 16;
-    *reinterpret_cast<bf16x8*>(to) = hi;
-    *reinterpret_cast<bf16x8*>(to + TRI_PART) = lo;
+    *reinterpret_cast<bf16x8*>(to) = parts[0];
+    *reinterpret_cast<bf16x8*>(to + TRI_PART) = parts[1];
+    if (BACK && f >= TRI_BLOCKS) *reinterpret_cast<bf16x8*>(to + 2 * TRI_PART) = parts[2];
   }
 }
 

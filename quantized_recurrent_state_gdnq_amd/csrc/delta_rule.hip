@@ -18,17 +18,20 @@ namespace {
 // triangles) come from LDS, where the workgroup puts the next chunk's while
 // this one's are used: its loads are made between this chunk's products, its
 // operands read from LDS some products ahead of their own.
-//   Bound by one wave a SIMD: a chunk is 132 matrix instructions of 16 cycles and
-// about 670 others in a chain of products of which each needs the one before, 2.8
-// us a chunk of 128 x 128; with SAVE (96 KB more to store a chunk and head) 3.9.
-// 4 x 8192 tokens, 16 heads: 364 us, 755 MB of memory at 2.1 TB/s, with half of the
-// CUs idle: there are no more rows, and segments would be 2.3 times the work.
+//   Bound by one wave a SIMD: a chunk is 176 matrix instructions of 16 cycles and
+// about 900 others in a chain of products of which each needs the one before, 3.4
+// us a chunk of 128 x 128; with SAVE (96 KB more to store a chunk and head) 4.6.
+// 4 x 8192 tokens, 16 heads: 442 us, 755 MB of memory at 1.7 TB/s, with half of the
+// CUs idle: there are no more rows, and segments would be 1.9 times the work.  The
+// third part of S, x and w is 44 of the products and 70 of the microseconds: without
+// it the state is 4e-6 of its norm off, with it 1e-6.
 //   SAVE: S and w of every chunk are left in the carry.
 //   PASS: the first pass over segments, which has no outputs.
 template <int DK, bool SAVE, bool PASS, typename O>
 __global__ __launch_bounds__(256, PASS ? 2 : 1) void delta_chain_kernel(DeltaLaunch L, int row_groups) {
-  constexpr int KB = DK / 32, TILES = DK / 16;
-  using Buffer = ChainBuffer<DK, PASS>;
+  constexpr int KB = DK / 32, TILES = DK / 16, P = PASS ? 2 : 3;  // parts of what passes on
+  using Loader = ChainLoader<DK, false>;
+  using Buffer = ChainBuffer<DK, false, PASS>;
   __shared__ __attribute__((aligned(1024))) Buffer buffers[2];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
   int within;
@@ -42,10 +45,10 @@ __global__ __launch_bounds__(256, PASS ? 2 : 1) void delta_chain_kernel(DeltaLau
   const int h = place.h, group = place.group, end = place.end;
   const int col = group * 64 + wave * 16 + c;
   const bool mine = col < L.dv;
-  ChainLoader<DK> loader;
+  Loader loader;
   loader.init(L, L.v, h, PASS && place.identity ? 0 : group, wave, lane);
   const int64_t vrow = int64_t(L.H) * L.dv;
-  const int times = (L.dk + 31) / 32, part_size = int(delta_part(L)), w_size = (L.dv + 15) / 16 * 1024;  // of what it leaves
+  const int tiles = (L.dk + 31) / 32 * 2;  // of a row of the state that it leaves
   const bool exact = L.dk == DK && group * 64 + wave * 16 + 16 <= L.dv;  // all lanes leave something
 
   f32x4 S[TILES];
@@ -79,9 +82,9 @@ __global__ __launch_bounds__(256, PASS ? 2 : 1) void delta_chain_kernel(DeltaLau
       phase();
       if (paced) loader.template step<step.value, PASS>(following, next);
     };
-    bf16* left = nullptr;  // this chunk's part of the carry
+    float* left = nullptr;  // this chunk's part of the carry
     if constexpr (SAVE)
-      left = reinterpret_cast<bf16*>(static_cast<uint8_t*>(L.carry) + ((s.slot + chunk) * L.H + h) * delta_left_bytes(L));
+      left = reinterpret_cast<float*>(static_cast<uint8_t*>(L.carry) + ((s.slot + chunk) * L.H + h) * delta_left_bytes(L));
     // K, then Q, 32 columns at a time, two ahead
     bf16x8 ring[3][4];
     const uint8_t* queries = nullptr;
@@ -90,11 +93,9 @@ __global__ __launch_bounds__(256, PASS ? 2 : 1) void delta_chain_kernel(DeltaLau
     read(Int<0>{});
     read(Int<1>{});
     phase();
-    bf16x8 sh[KB], sl[KB];
+    bf16x8 sp[KB][P];
 #pragma unroll
-    for (int j = 0; j < KB; ++j) {
-      split8(S[2 * j], S[2 * j + 1], sh[j], sl[j]);
-    }
+    for (int j = 0; j < KB; ++j) split8(S[2 * j], S[2 * j + 1], sp[j]);
     const float* rows = reinterpret_cast<const float*>(buf.rows);
     auto row4 = [&](int which, int it) { return *reinterpret_cast<const f32x4*>(rows + which * 64 + chain_row(it, g * 4)); };
     phase();
@@ -103,7 +104,7 @@ __global__ __launch_bounds__(256, PASS ? 2 : 1) void delta_chain_kernel(DeltaLau
     // are the same registers, in the other order.
     f32x4 x[4] = {}, o[4] = {}, decay[4];
     s16x4 v[4];
-    bf16x8 hi[2], lo[2], nh[TRI_BLOCKS], nl[TRI_BLOCKS];
+    bf16x8 xp[2][P], n2[2][TRI_BLOCKS];
     auto errors = [&](auto half) {
 #pragma unroll
       for (int it = 2 * half.value; it < 2 * half.value + 2; ++it)
@@ -112,24 +113,22 @@ __global__ __launch_bounds__(256, PASS ? 2 : 1) void delta_chain_kernel(DeltaLau
           const float value = PASS && place.identity ? 0.0f : bf16_value(v[it][e]);
           x[it][e] = value - decay[it][e] * x[it][e];
         }
-      split8(x[2 * half.value], x[2 * half.value + 1], hi[half.value], lo[half.value]);
+      split8(x[2 * half.value], x[2 * half.value + 1], xp[half.value]);
     };
-    // A part of the state that enters; behind the last load, so that the wait for
+    // A quarter of the state that enters; behind the last load, so that the wait for
     // the loads need not wait for these stores too.
-    auto leave = [&](auto j) {
+    auto leave = [&](auto quarter) {
       phase();
-      if constexpr (SAVE && j.value < KB) {
-        bf16* to = left + left_place(col, j.value * 4 + g, times);
-        if (exact) {
-          *reinterpret_cast<bf16x8*>(to) = sh[j.value];
-          *reinterpret_cast<bf16x8*>(to + part_size) = sl[j.value];
-        } else if (mine && j.value * 32 + g * 8 < L.dk) {
-          *reinterpret_cast<bf16x8*>(to) = sh[j.value];
-          *reinterpret_cast<bf16x8*>(to + part_size) = sl[j.value];
+      if constexpr (SAVE) {
+#pragma unroll
+        for (int t = quarter.value * (TILES / 4); t < (quarter.value + 1) * (TILES / 4); ++t) {
+          float* to = left + left_place(col, t, tiles, g);
+          if (exact || (mine && chain_row(t, g * 4) < L.dk)) *reinterpret_cast<f32x4*>(to) = S[t];
         }
+        phase();
       }
     };
-    constexpr int PRODUCTS = PASS ? KB : 2 * KB, STEPS = ChainLoader<DK>::STEPS;
+    constexpr int PRODUCTS = PASS ? KB : 2 * KB, STEPS = Loader::STEPS;
     each<PRODUCTS>([&](auto i) {
       constexpr int j = i.value % KB;
       if constexpr (i.value + 2 < PRODUCTS) read(Int<i.value + 2>{});
@@ -140,19 +139,19 @@ __global__ __launch_bounds__(256, PASS ? 2 : 1) void delta_chain_kernel(DeltaLau
           decay[it] = row4(ROW_C, it);
         }
       }
-      if constexpr (i.value == PRODUCTS - 2) chain_triangle(buf.tri, lane, nh, nl);
+      if constexpr (i.value == PRODUCTS - 2) chain_triangle(buf.tri, lane, n2);
       phase();
       const bf16x8(&f)[4] = ring[i.value % 3];
       if constexpr (i.value < KB) {
 #pragma unroll
-        for (int it = 0; it < 4; ++it) x[it] = mfma16(f[it], sl[j], x[it]);
+        for (int p = P - 1; p >= 0; --p)
 #pragma unroll
-        for (int it = 0; it < 4; ++it) x[it] = mfma16(f[it], sh[j], x[it]);
+          for (int it = 0; it < 4; ++it) x[it] = mfma16(f[it], sp[j][p], x[it]);
       } else {
 #pragma unroll
-        for (int it = 0; it < 4; ++it) o[it] = mfma16(sl[j], f[it], o[it]);
+        for (int p = 1; p >= 0; --p)
 #pragma unroll
-        for (int it = 0; it < 4; ++it) o[it] = mfma16(sh[j], f[it], o[it]);
+          for (int it = 0; it < 4; ++it) o[it] = mfma16(sp[j][p], f[it], o[it]);
       }
       if constexpr (!PASS && i.value >= 2 * KB - 2) errors(Int<i.value - (2 * KB - 2)>{});  // beside the last of these products
       each<STEPS>([&](auto s) {
@@ -177,63 +176,57 @@ __global__ __launch_bounds__(256, PASS ? 2 : 1) void delta_chain_kernel(DeltaLau
     // The six blocks of a triangle: tiles 0 and 1 with the first 32 tokens, 2 and
     // 3 with both halves.
     f32x4 w[4] = {};
-    auto part = [&](const bf16x8 (&n)[TRI_BLOCKS], const bf16x8 (&y)[2]) {
+    part_terms<2, P>([&](auto i, auto j) {
+      const bf16x8(&n)[TRI_BLOCKS] = n2[i.value];
 #pragma unroll
-      for (int it = 0; it < 4; ++it) w[it] = mfma16(n[it < 2 ? it : 2 * it - 2], y[0], w[it]);
+      for (int it = 0; it < 4; ++it) w[it] = mfma16(n[it < 2 ? it : 2 * it - 2], xp[0][j.value], w[it]);
 #pragma unroll
-      for (int it = 2; it < 4; ++it) w[it] = mfma16(n[2 * it - 1], y[1], w[it]);
-    };
-    part(nl, hi);
-    part(nh, lo);
-    part(nh, hi);
+      for (int it = 2; it < 4; ++it) w[it] = mfma16(n[2 * it - 1], xp[1][j.value], w[it]);
+      if constexpr (SAVE && i.value == 0 && j.value > 0) {  // beside the products
+        leave(Int<(P - 1 - j.value) * 2>{});
+        leave(Int<(P - 1 - j.value) * 2 + 1>{});
+      }
+    });
 #pragma unroll
     for (int t = 0; t < TILES; ++t) S[t] *= whole;
 #pragma unroll
     for (int it = 0; it < 4; ++it) o[it] *= decay_o[it];
-    leave(Int<0>{});
     phase();
-    bf16x8 mh[TRI_BLOCKS], ml[TRI_BLOCKS], th[2], tl[2];
+    bf16x8 m2[2][TRI_BLOCKS], tp[2][P], wp[2][2];
     if constexpr (TILES > 4) chain_columns<DK>(buf.k, lane, 1, kt[1]);
-    if constexpr (!PASS) chain_triangle(buf.tri + TRI_BYTES, lane, mh, ml);
+    if constexpr (!PASS) chain_triangle(buf.tri + TRI_BYTES, lane, m2);
     phase();
 #pragma unroll
-    for (int j = 0; j < 2; ++j) split8(w[2 * j] * tail[2 * j], w[2 * j + 1] * tail[2 * j + 1], th[j], tl[j]);
-    chain_update(S, kt[0], th, tl);
+    for (int j = 0; j < 2; ++j) split8(w[2 * j] * tail[2 * j], w[2 * j + 1] * tail[2 * j + 1], tp[j]);
+    chain_update(S, kt[0], tp);
     if constexpr (!PASS) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) split8(w[2 * j], w[2 * j + 1], hi[j], lo[j]);
+      for (int j = 0; j < 2; ++j) split8(w[2 * j], w[2 * j + 1], wp[j]);
     }
-    leave(Int<1>{});
-    leave(Int<2>{});
-    if constexpr (TILES > 4) chain_update(S + 4, kt[1], th, tl);
-    leave(Int<3>{});
-    auto inside = [&](const bf16x8 (&y)[2], const bf16x8 (&m)[TRI_BLOCKS]) {
+    phase();
+    if constexpr (TILES > 4) chain_update(S + 4, kt[1], tp);
+    phase();
+    if constexpr (!PASS)
+      part_terms<2, 2>([&](auto i, auto j) {
+        const bf16x8(&m)[TRI_BLOCKS] = m2[i.value];
 #pragma unroll
-      for (int it = 0; it < 4; ++it) o[it] = mfma16(y[0], m[it < 2 ? it : 2 * it - 2], o[it]);
+        for (int it = 0; it < 4; ++it) o[it] = mfma16(wp[0][j.value], m[it < 2 ? it : 2 * it - 2], o[it]);
 #pragma unroll
-      for (int it = 2; it < 4; ++it) o[it] = mfma16(y[1], m[2 * it - 1], o[it]);
-    };
-    if constexpr (!PASS) {
-      inside(lo, mh);
-      inside(hi, ml);
-      inside(hi, mh);
-    }
+        for (int it = 2; it < 4; ++it) o[it] = mfma16(wp[1][j.value], m[2 * it - 1], o[it]);
+      });
     phase();
     // the next chunk is in LDS, and nobody reads this one any more; the stores
     // below are behind this wait, so that the next chunk's covers them
     if (SAVE && exact)
-      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * KB) : "memory");
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(TILES) : "memory");
     else
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     if constexpr (SAVE) {
       if (mine) {
-        bf16* wp = left + 2 * part_size;
+        float* to = left + delta_state_floats(L);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          *reinterpret_cast<bf16x8*>(wp + left_place(col, j * 4 + g, 2)) = hi[j];
-          *reinterpret_cast<bf16x8*>(wp + w_size + left_place(col, j * 4 + g, 2)) = lo[j];
-        }
+        for (int it = 0; it < 4; ++it) *reinterpret_cast<f32x4*>(to + left_place(col, it, 4, g)) = w[it];
       }
     }
     const int oc = group * 64 + wave * 16 + g * 4;
@@ -380,7 +373,7 @@ hipError_t step_of(const DeltaLaunch& L, hipStream_t stream) {
 
 size_t delta_carry_bytes(const DeltaLaunch& L) { return size_t(delta_slots(L)) * L.H * delta_left_bytes(L); }
 static DeltaLaunch forward_split(DeltaLaunch L) {
-  delta_split(L, delta_slots(L) * L.H * DELTA_CHUNK_BYTES);
+  delta_split(L, delta_slots(L) * L.H * delta_chunk_bytes(false));
   return L;
 }
 size_t delta_forward_workspace_bytes(const DeltaLaunch& L) { return size_t(delta_split_bytes(forward_split(L))); }

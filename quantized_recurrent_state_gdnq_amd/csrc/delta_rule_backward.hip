@@ -10,17 +10,20 @@ namespace {
 // The workspace goes on with dS' and z of every chunk and head, as the carry
 // holds S and w.
 __host__ __device__ inline int64_t backward_left_at(const DeltaLaunch& L, int64_t slots) {
-  return delta_align(slots * L.H * DELTA_CHUNK_BYTES);
+  return delta_align(slots * L.H * delta_chunk_bytes(true));
 }
 
 // ---------------------------------------------------------------- the chain of dS
 //
 // As the forward chain, from the last chunk to the first, dS' and z left for the
-// gradients as S and w are; bound as it is.  4 x 8192 tokens, 16 heads: 500 us.
+// gradients as S and w are; bound as it is, by 192 products a chunk.  4 x 8192
+// tokens, 16 heads: 590 us.
 template <int DK, bool PASS>
 __global__ __launch_bounds__(256, 1) void delta_chain_back_kernel(DeltaLaunch L, int row_groups, int64_t left_at) {
-  constexpr int KB = DK / 32, TILES = DK / 16;
-  __shared__ __attribute__((aligned(1024))) ChainBuffer<DK> buffers[2];
+  constexpr int KB = DK / 32, TILES = DK / 16, P = PASS ? 2 : 3;  // parts of what passes on
+  using Loader = ChainLoader<DK, true>;
+  using Buffer = ChainBuffer<DK, true, false>;
+  __shared__ __attribute__((aligned(1024))) Buffer buffers[2];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
   int within;
   const int unit = xcd_unit(row_groups * (L.H / L.G), within);
@@ -34,10 +37,10 @@ __global__ __launch_bounds__(256, 1) void delta_chain_back_kernel(DeltaLaunch L,
   const int h = place.h, group = place.group, count = place.end - place.first, last = place.end - 1;
   const int col = group * 64 + wave * 16 + c;
   const bool mine = col < L.dv && !(PASS && place.identity);
-  ChainLoader<DK> loader;
+  Loader loader;
   loader.init(L, L.dout, h, PASS && place.identity ? 0 : group, wave, lane);
 
-  const int times = (L.dk + 31) / 32, part_size = int(delta_part(L)), w_size = (L.dv + 15) / 16 * 1024;  // of what it leaves
+  const int tiles = (L.dk + 31) / 32 * 2;  // of a row of the state that it leaves
   f32x4 S[TILES];  // dS^T
   const int64_t state_row = ((int64_t(b) * L.H + h) * L.dv + col) * L.dk;
   if constexpr (PASS) {
@@ -58,8 +61,8 @@ __global__ __launch_bounds__(256, 1) void delta_chain_back_kernel(DeltaLaunch L,
   __syncthreads();
   for (int done = 0; done < count; ++done) {
     const int chunk = last - done;
-    const ChainBuffer<DK>& buf = buffers[done & 1];
-    ChainBuffer<DK>& following = buffers[(done + 1) & 1];
+    const Buffer& buf = buffers[done & 1];
+    Buffer& following = buffers[(done + 1) & 1];
     const auto next = loader.next(s.first + int64_t(chunk - 1) * 64, 64, s.slot + chunk - 1);
     const bool paced = chunk > place.first && next.whole;
     if (chunk > place.first && !next.whole) loader.template load<true, false>(following, next);
@@ -67,32 +70,31 @@ __global__ __launch_bounds__(256, 1) void delta_chain_back_kernel(DeltaLaunch L,
       phase();
       if (paced) loader.template step<step.value, false>(following, next);
     };
-    bf16* left = reinterpret_cast<bf16*>(static_cast<uint8_t*>(L.workspace) + left_at +
-                                         ((s.slot + chunk) * L.H + h) * delta_left_bytes(L));
+    float* left = reinterpret_cast<float*>(static_cast<uint8_t*>(L.workspace) + left_at +
+                                           ((s.slot + chunk) * L.H + h) * delta_left_bytes(L));
     bf16x8 ring[3][4];
     auto read = [&](auto i) { chain_rows<DK>(buf.k, lane, i.value, ring[i.value % 3]); };
     read(Int<0>{});
     read(Int<1>{});
     phase();
-    bf16x8 sh[KB], sl[KB];
+    bf16x8 sp[KB][P];
 #pragma unroll
     for (int j = 0; j < KB; ++j) {
-      split8(S[2 * j], S[2 * j + 1], sh[j], sl[j]);
-      const int at = j * 32 + g * 8;
-      if (!PASS && mine && at < L.dk) {
-        *reinterpret_cast<bf16x8*>(left + left_place(col, j * 4 + g, times)) = sh[j];
-        *reinterpret_cast<bf16x8*>(left + part_size + left_place(col, j * 4 + g, times)) = sl[j];
+      split8(S[2 * j], S[2 * j + 1], sp[j]);
+      if (!PASS && mine && j * 32 + g * 8 < L.dk) {
+        *reinterpret_cast<f32x4*>(left + left_place(col, 2 * j, tiles, g)) = S[2 * j];
+        *reinterpret_cast<f32x4*>(left + left_place(col, 2 * j + 1, tiles, g)) = S[2 * j + 1];
       }
     }
     const float* rows = reinterpret_cast<const float*>(buf.rows);
     auto row4 = [&](int which, int it) { return *reinterpret_cast<const f32x4*>(rows + which * 64 + chain_row(it, g * 4)); };
     phase();
     f32x4 u[4] = {}, tail[4], decay[4];
-    bf16x8 mh[TRI_BLOCKS], ml[TRI_BLOCKS], d[2];
+    bf16x8 m3[P][TRI_BLOCKS], d[2];
     each<KB>([&](auto i) {
       if constexpr (i.value + 2 < KB) read(Int<i.value + 2>{});
       if constexpr (i.value == KB - 2) {
-        chain_triangle(buf.tri + TRI_BYTES, lane, mh, ml);
+        chain_triangle(buf.tri + TRI_BYTES, lane, m3);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const s16x4 d0 = chain_column(buf.v, 2 * j, wave, lane), d1 = chain_column(buf.v, 2 * j + 1, wave, lane);
@@ -109,26 +111,26 @@ __global__ __launch_bounds__(256, 1) void delta_chain_back_kernel(DeltaLaunch L,
       phase();
       const bf16x8(&f)[4] = ring[i.value % 3];
 #pragma unroll
-      for (int it = 0; it < 4; ++it) u[it] = mfma16(f[it], sl[i.value], u[it]);
+      for (int p = P - 1; p >= 0; --p)
 #pragma unroll
-      for (int it = 0; it < 4; ++it) u[it] = mfma16(f[it], sh[i.value], u[it]);
+        for (int it = 0; it < 4; ++it) u[it] = mfma16(f[it], sp[i.value][p], u[it]);
       ahead(Int<i.value>{});  // the loader's first KB steps
     });
     const float whole = rows[ROW_C * 64 + 63];
-    bf16x8 kt[2][4][2], dh[2], dl[2], hi[2], lo[2];
+    bf16x8 kt[2][4][2], dp[2][P], up[2][P], zp[2][P];
     chain_columns<DK>(buf.q, lane, 0, kt[0]);
     phase();
     // transposed triangles: tiles 0 and 1 take both halves of the tokens, 2 and 3 the second
-    auto part = [&](f32x4 (&y)[4], const bf16x8 (&m)[TRI_BLOCKS], const bf16x8 (&x)[2]) {
+    auto part = [&](f32x4 (&y)[4], const bf16x8 (&m)[TRI_BLOCKS], const bf16x8& x0, const bf16x8& x1) {
 #pragma unroll
-      for (int it = 0; it < 4; ++it) y[it] = mfma16(m[it < 2 ? it * 2 + 1 : it + 2], x[1], y[it]);
+      for (int it = 0; it < 4; ++it) y[it] = mfma16(m[it < 2 ? it * 2 + 1 : it + 2], x1, y[it]);
 #pragma unroll
-      for (int it = 0; it < 2; ++it) y[it] = mfma16(m[it * 2], x[0], y[it]);
+      for (int it = 0; it < 2; ++it) y[it] = mfma16(m[it * 2], x0, y[it]);
     };
 #pragma unroll
     for (int it = 0; it < 4; ++it) u[it] *= tail[it];
-    part(u, ml, d);
-    part(u, mh, d);
+#pragma unroll
+    for (int p = P - 1; p >= 0; --p) part(u, m3[p], d[0], d[1]);
     // beside these products: c dO in parts
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -138,20 +140,20 @@ __global__ __launch_bounds__(256, 1) void delta_chain_back_kernel(DeltaLaunch L,
         a[e] = decay[2 * j][e] * float(d[j][e]);
         b4[e] = decay[2 * j + 1][e] * float(d[j][4 + e]);
       }
-      split8(a, b4, dh[j], dl[j]);
+      split8(a, b4, dp[j]);
     }
 #pragma unroll
     for (int t = 0; t < TILES; ++t) S[t] *= whole;
     ahead(Int<KB>{});
     phase();
-    bf16x8 nh[TRI_BLOCKS], nl[TRI_BLOCKS];
-    chain_triangle(buf.tri, lane, nh, nl);
+    bf16x8 n2[2][TRI_BLOCKS];
+    chain_triangle(buf.tri, lane, n2);
     if constexpr (TILES > 4) chain_columns<DK>(buf.q, lane, 1, kt[1]);
     phase();
     // the part of dS that does not wait for z, half of it while u is split
-    chain_update(S, kt[0], dh, dl);
-    split8(u[0], u[1], hi[0], lo[0]);
-    split8(u[2], u[3], hi[1], lo[1]);
+    chain_update(S, kt[0], dp);
+    split8(u[0], u[1], up[0]);
+    split8(u[2], u[3], up[1]);
     ahead(Int<KB + 1>{});
     phase();
     chain_columns<DK>(buf.k, lane, 0, kt[0]);
@@ -160,35 +162,28 @@ __global__ __launch_bounds__(256, 1) void delta_chain_back_kernel(DeltaLaunch L,
     for (int it = 0; it < 4; ++it) decay_beta[it] = row4(ROW_C_BETA, it);
     phase();
     f32x4 z[4] = {};
-    part(z, nl, hi);
-    part(z, nh, lo);
-    part(z, nh, hi);
+    part_terms<2, P>([&](auto i, auto j) { part(z, n2[i.value], up[0][j.value], up[1][j.value]); });
     ahead(Int<KB + 2>{});
-    bf16x8 zh[2], zl[2];
-    if constexpr (TILES > 4) chain_update(S + 4, kt[1], dh, dl);
+    if constexpr (TILES > 4) chain_update(S + 4, kt[1], dp);
 #pragma unroll
     for (int j = 0; j < 2; ++j)
-      split8(z[2 * j] * -decay_beta[2 * j], z[2 * j + 1] * -decay_beta[2 * j + 1], hi[j], lo[j]);
+      split8(z[2 * j] * -decay_beta[2 * j], z[2 * j + 1] * -decay_beta[2 * j + 1], zp[j]);
     ahead(Int<KB + 3>{});
     phase();
     if constexpr (TILES > 4) chain_columns<DK>(buf.k, lane, 1, kt[1]);
     phase();
-    chain_update(S, kt[0], hi, lo);
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      if constexpr (!PASS) split8(z[2 * j], z[2 * j + 1], zh[j], zl[j]);
+    chain_update(S, kt[0], zp);
     ahead(Int<KB + 4>{});
-    if constexpr (TILES > 4) chain_update(S + 4, kt[1], hi, lo);
+    if constexpr (TILES > 4) chain_update(S + 4, kt[1], zp);
+    ahead(Int<KB + 5>{});
+    static_assert(Loader::LOADS == KB && Loader::STEPS == KB + 6, "every step of the loader is taken");
     phase();
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     if (!PASS && mine) {
-      bf16* zp = left + 2 * part_size;
+      float* to = left + delta_state_floats(L);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        *reinterpret_cast<bf16x8*>(zp + left_place(col, j * 4 + g, 2)) = zh[j];
-        *reinterpret_cast<bf16x8*>(zp + w_size + left_place(col, j * 4 + g, 2)) = zl[j];
-      }
+      for (int it = 0; it < 4; ++it) *reinterpret_cast<f32x4*>(to + left_place(col, it, 4, g)) = z[it];
     }
   }
   if constexpr (PASS) chain_leave<TILES>(L, item, place, S, col, g);
@@ -216,98 +211,115 @@ __global__ __launch_bounds__(256, 1) void delta_chain_back_kernel(DeltaLaunch L,
 // the key head's value heads in turn (so that their sum needs no atomics and no
 // memory): wave (it, quarter) has the 16 tokens of tile it, a quarter of the
 // columns (d_k) and half of dM or of dAt.  S, dS', w, z and dO pass through LDS 32
-// rows (d_v) at a time, the next ones (of the next head, or chunk) loaded while
-// these are used; bound by these loads, 208 KB a chunk and head at 128 x 128, which
-// the products and sums of a slab hide in part: 16384 tokens, 16 heads take 316 us,
-// 1.22 GB at 3.9 TB/s, 18 us a chunk and head on each CU.  dQ
-// and dK are formed transposed (tokens in lanes), so that a token's factors are a
-// lane's and results leave four at a time.
+// rows (d_v) at a time, the first four by way of registers, where they are split
+// into three parts once for all sixteen waves; the next ones (of the next head, or
+// chunk) are loaded while these are used.  Bound by these loads, 208 KB a chunk and
+// head at 128 x 128, and the products that they wait for: 16384 tokens, 16 heads take
+// 400 us, 1.22 GB at 3.1 TB/s, 23 us a chunk and head on each CU; with two parts,
+// loaded as such, it was 316, and dbeta and dlog alpha 4e-6 to 6e-6 of their norm off
+// (now 1e-6), more where few large terms cancel.  dQ and dK are formed transposed
+// (tokens in lanes), so that a token's factors are a lane's and results leave four at
+// a time.
 template <int DK>
 struct GradientSlab {
-  uint8_t states[4][32 * DK * 2], tokens[4][4096], d[4096];  // S hi, lo, dS' hi, lo; w hi, lo, z hi, lo; dO
+  uint8_t states[6][32 * DK * 2], tokens[6][4096];  // S, dS' and w, z, three parts each
 };
 
 // Rows of 32 bf16 in LDS.
 __device__ __forceinline__ int slab_block(int row, int block) { return row * 64 + ((block ^ (row >> 2 & 3)) << 4); }
 
+// A slab passes through registers, where it is split: four values of S and of dS'
+// (with DK 64 in the first eight waves) and of w (waves 0 to 7) or z, loaded while
+// the slab before is used.  dO goes straight into LDS.
 template <int DK>
 struct GradientLoader {
-  static constexpr int PIECES = 4 * 32 * DK * 2 / 1024;  // kilobytes of the states, of which a wave takes every 16th
+  static constexpr int TILES = DK / 16;
   const uint8_t *left[2], *d, *rows;  // of the carry and the workspace at a chunk and head; dO of its first token; its decays
   int64_t vrow;
-  int dk, dv, part_size, n, wave, lane;
-  bool exact;                  // whole columns and slabs
-  uint32_t at_state, at_row, at_d;  // a lane's offsets then
+  int dk, dv, n, wave, lane, tiles, state_floats;
+  bool has_state;
+  struct Held {
+    f32x4 s, ds, t;
+  };
   __device__ __forceinline__ void init(const DeltaLaunch& L, int wave_, int lane_) {
     wave = wave_;
     lane = lane_;
     dk = L.dk;
     dv = L.dv;
-    part_size = int(delta_part(L));
     vrow = int64_t(L.H) * L.dv * 2;
-    exact = L.dk == DK && L.dv % 32 == 0;
-    int row, block;
-    lds_place<DK>(wave % (PIECES / 4) * 64 + lane, row, block);  // 16 pieces on it is the same place of another part
-    at_state = uint32_t(left_place(row, block, DK / 32)) * 2;
-    lds_place<64>(wave % 4 * 64 + lane, row, block);
-    at_row = uint32_t(left_place(row, block, 2)) * 2;
-    row = (wave % 4 * 64 + lane) / 4;
-    block = (slab_block(row, lane & 3) >> 4) & 3;
-    at_d = uint32_t(row) * uint32_t(vrow) + block * 16;
+    tiles = (dk + 31) / 32 * 2;
+    state_floats = int(delta_state_floats(L));
+    has_state = wave < 2 * TILES;
   }
   __device__ __forceinline__ void set(const DeltaLaunch& L, int64_t left_at, int64_t slot, int64_t first, int tokens, int h) {
     const int64_t chunk = slot * L.H + h;
     const uint8_t* space = static_cast<const uint8_t*>(L.workspace);
     left[0] = static_cast<const uint8_t*>(L.carry) + chunk * delta_left_bytes(L);
     left[1] = space + left_at + chunk * delta_left_bytes(L);
-    rows = space + chunk * DELTA_CHUNK_BYTES + DELTA_SCALARS;
+    rows = space + chunk * delta_chunk_bytes(true) + delta_scalars(true);
     d = static_cast<const uint8_t*>(L.dout) + (first * L.H + h) * int64_t(L.dv) * 2;
     n = tokens;
   }
-  __device__ __forceinline__ void load(GradientSlab<DK>& to, int v0) const {
-    if (exact && n == 64) {
-#pragma unroll
-      for (int i = 0; i < PIECES / 16; ++i) {
-        const int piece = i * 16 + wave, part = piece / (PIECES / 4);
-        to_lds((part < 2 ? left[0] : left[1]) + ((part & 1) * dv + v0) * (DK * 2), at_state, &to.states[0][0] + piece * 1024);
-      }
-      const int part = wave / 4;
-      to_lds((part < 2 ? left[0] : left[1]) + (2 * dv * DK + ((part & 1) * dv + v0) * 64) * 2, at_row, &to.tokens[0][0] + wave * 1024);
-      if (wave < 4) to_lds(d + v0 * 2, at_d, to.d + wave * 1024);
-      return;
+  // Row of the slab and tile of a wave's values; a lane has columns 4 (lane % 4) .. of
+  // the tile (chain_row) in row lane / 4 of the group's.
+  __device__ __forceinline__ int state_row() const { return wave / TILES * 16 + (lane >> 2); }
+  __device__ __forceinline__ int state_tile() const { return wave % TILES; }
+  __device__ __forceinline__ int token_row() const { return (wave >> 2 & 1) * 16 + (lane >> 2); }
+  __device__ __forceinline__ bool keep_state(int v0) const {
+    return v0 + state_row() < dv && chain_row(state_tile(), (lane & 3) * 4) < dk;
+  }
+  // From a clamped address where there is nothing: cut to zero in store().
+  __device__ __forceinline__ Held load(int v0, uint8_t* outs) const {
+    Held x = {};
+    if (has_state) {
+      const uint32_t at = keep_state(v0) ? uint32_t(((v0 + state_row()) >> 4) * tiles + state_tile()) * 1024 + lane * 16 : lane * 16;
+      x.s = *reinterpret_cast<const f32x4*>(left[0] + at);
+      x.ds = *reinterpret_cast<const f32x4*>(left[1] + at);
     }
-    int row, block;
-#pragma unroll 1
-    for (int i = 0; i < PIECES / 16; ++i) {
-      const int piece = i * 16 + wave, part = piece / (PIECES / 4);
-      lds_place<DK>(piece % (PIECES / 4) * 64 + lane, row, block);
-      const uint8_t* p = (part < 2 ? left[0] : left[1]) + ((part & 1) * part_size + left_place(v0 + row, block, (dk + 31) / 32)) * 2;
-      to_lds(v0 + row < dv && block * 8 < dk ? p : delta_zeros, &to.states[0][0] + piece * 1024);
-    }
-    {
-      const int part = wave / 4;
-      lds_place<64>(wave % 4 * 64 + lane, row, block);
-      const uint8_t* p = (part < 2 ? left[0] : left[1]) + (2 * part_size + (part & 1) * ((dv + 15) / 16 * 1024) + left_place(v0 + row, block, 2)) * 2;
-      to_lds(v0 + row < dv ? p : delta_zeros, &to.tokens[0][0] + wave * 1024);
-    }
+    const uint32_t group = v0 + token_row() < dv ? (v0 + token_row()) >> 4 : 0;
+    x.t = *reinterpret_cast<const f32x4*>((wave < 8 ? left[0] : left[1]) + state_floats * 4 + ((group * 4 + (wave & 3)) * 1024 + lane * 16));
     if (wave < 4) {
-      row = (wave * 64 + lane) / 4;
-      block = (slab_block(row, lane & 3) >> 4) & 3;
+      const int row = (wave * 64 + lane) / 4, block = (slab_block(row, lane & 3) >> 4) & 3;
       const uint8_t* p = d + row * vrow + (v0 + block * 8) * 2;
-      to_lds(row < n && v0 + block * 8 < dv ? p : delta_zeros, to.d + wave * 1024);
+      to_lds(row < n && v0 + block * 8 < dv ? p : delta_zeros, outs + wave * 1024);
     }
+    return x;
+  }
+  // Four values, in parts, to their place in each part's matrix.
+  __device__ __forceinline__ static void split_to(const f32x4& x, uint8_t* to, int part_bytes) {
+    uint32_t a[3], b[3];
+    split_pair(f32x2{x[0], x[1]}, a);
+    split_pair(f32x2{x[2], x[3]}, b);
+#pragma unroll
+    for (int p = 0; p < 3; ++p) *reinterpret_cast<uint2*>(to + p * part_bytes) = uint2{a[p], b[p]};
+  }
+  // The slab into LDS; the sum of this lane's products of S and dS'.
+  __device__ __forceinline__ float store(Held x, int v0, GradientSlab<DK>& to) const {
+    float sum = 0.0f;
+    auto cut = [](bool keep, const f32x4& v) { return __builtin_bit_cast(f32x4, only_if(keep, __builtin_bit_cast(u32x4, v))); };
+    if (has_state) {
+      const bool keep = keep_state(v0);
+      x.s = cut(keep, x.s);
+      x.ds = cut(keep, x.ds);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum = fmaf(x.s[e], x.ds[e], sum);
+      const int t = state_tile(), at = lds_block<DK>(state_row(), (t >> 1) * 4 + (lane & 3)) + (t & 1) * 8;
+      split_to(x.s, to.states[0] + at, sizeof(to.states[0]));
+      split_to(x.ds, to.states[3] + at, sizeof(to.states[0]));
+    }
+    const int t = wave & 3, at = lds_block<64>(token_row(), (t >> 1) * 4 + (lane & 3)) + (t & 1) * 8;
+    split_to(cut(v0 + token_row() < dv, x.t), to.tokens[wave < 8 ? 0 : 3] + at, sizeof(to.tokens[0]));
+    return sum;
   }
 };
 
-// The sum of eight products of values in two parts.
-__device__ __forceinline__ float dot8(const bf16x8& ah, const bf16x8& al, const bf16x8& bh, const bf16x8& bl, float s) {
+// The sum of eight products of values in three parts.
+__device__ __forceinline__ float dot8(const bf16x8 (&a)[3], const bf16x8 (&b)[3], float s) {
+  part_terms<3, 3>([&](auto i, auto j) {
 #pragma unroll
-  for (int e = 0; e < 8; e += 2) {
-    const bf16x2 a0 = {ah[e], ah[e + 1]}, a1 = {al[e], al[e + 1]}, b0 = {bh[e], bh[e + 1]}, b1 = {bl[e], bl[e + 1]};
-    s = __builtin_amdgcn_fdot2_f32_bf16(a1, b0, s, false);
-    s = __builtin_amdgcn_fdot2_f32_bf16(a0, b1, s, false);
-    s = __builtin_amdgcn_fdot2_f32_bf16(a0, b0, s, false);
-  }
+    for (int e = 0; e < 8; e += 2)
+      s = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{a[i.value][e], a[i.value][e + 1]}, bf16x2{b[j.value][e], b[j.value][e + 1]}, s, false);
+  });
   return s;
 }
 
@@ -315,9 +327,9 @@ template <int DK>
 __global__ __launch_bounds__(1024) void delta_gradient_kernel(DeltaLaunch L, int64_t left_at, int items) {
   constexpr int BLOCKS = DK / 8, KB = DK / 32, TILES = DK / 64;  // tiles of a wave
   constexpr int MAT = 64 * DK * 2;
-  static_assert(sizeof(GradientSlab<DK>) >= 4 * 8192, "the triangles take a slab's place");
-  __shared__ __attribute__((aligned(1024))) GradientSlab<DK> slabs[2];
-  __shared__ __attribute__((aligned(1024))) uint8_t ks[MAT], qs[MAT];
+  static_assert(sizeof(GradientSlab<DK>) >= 4 * 8192, "the triangles take the slab's place");
+  __shared__ __attribute__((aligned(1024))) GradientSlab<DK> slab;
+  __shared__ __attribute__((aligned(1024))) uint8_t outs[2][4096], ks[MAT], qs[MAT];  // dO of a slab, K, Q
   __shared__ __attribute__((aligned(1024))) float decays[3][512];
   __shared__ float below[2][4][64], row_in[4][64], row_out[4][64], pair_sum[4][64], dots[16];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -358,7 +370,7 @@ __global__ __launch_bounds__(1024) void delta_gradient_kernel(DeltaLaunch L, int
     return tokens;
   };
   n = find(item, first);
-  // of the decays (the head before's, this one's, the next one's), of the slabs
+  // of the decays (the head before's, this one's, the next one's), of dO
   int before = 2, now = 0, turn = 0;
   // d log alpha of the head before, whose sums lie in LDS until the next head's
   // slabs are done: by a wave with the least other work, while slabs are loaded.
@@ -384,9 +396,10 @@ __global__ __launch_bounds__(1024) void delta_gradient_kernel(DeltaLaunch L, int
       L.dalpha[at] = da;
     }
   };
+  typename GradientLoader<DK>::Held held = {};
   if (item < items) {
     loader.set(L, left_at, item / L.G, first, n, item % L.G * share);
-    loader.load(slabs[0], 0);
+    held = loader.load(0, outs[0]);
     if (wave < 2) to_lds(loader.rows, wave * 1024 + lane * 16, decays[0] + wave * 256);
   }
   while (item < items) {
@@ -403,25 +416,11 @@ __global__ __launch_bounds__(1024) void delta_gradient_kernel(DeltaLaunch L, int
       const float* row = decays[now];
       f32x4 ds[TILES] = {}, xs[TILES] = {}, ud[TILES] = {};  // dO S, z S, w dS'
       f32x4 pair[2] = {};                                    // dO w^T or z w^T
-      float db = 0.0f, dot = 0.0f;
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      __syncthreads();
-      if (hs == 0) {
-        const uint8_t* kp = static_cast<const uint8_t*>(L.k) + (first * krow + int64_t(kh) * L.dk) * 2;
-        const uint8_t* qp = static_cast<const uint8_t*>(L.q) + (first * krow + int64_t(kh) * L.dk) * 2;
-        int r, block;
-        lds_place<DK>(wave * 64 + lane, r, block);
-        if (wave < MAT / 1024) {
-          const int64_t at = (r * krow + block * 8) * 2;
-          const bool keep = r < n && block * 8 < L.dk;
-          to_lds(keep ? kp + at : delta_zeros, ks + wave * 1024);
-          to_lds(keep ? qp + at : delta_zeros, qs + wave * 1024);
-        }
-      }
-      if (wave == 3 && last_n > 0) finish(decays[before]);
-      const float bt = row[ROW_BETA * 64 + token];
+      float db = 0.0f, dot = 0.0f, bt = 0.0f;
       for (int v0 = 0; v0 < L.dv; v0 += 32, turn ^= 1) {
-        const GradientSlab<DK>& slab = slabs[turn];
+        asm volatile("s_waitcnt vmcnt(0)" : "+v"(loader.lane) : : "memory");  // with the slab dO and, before the first, the decays
+        __syncthreads();  // the slab before, or the triangles, have been read
+        dot += loader.store(held, v0, slab);
         // the next slab: of this head, of the next, or of the next chunk
         const bool more = v0 + 32 < L.dv;
         if (!more) {
@@ -431,46 +430,67 @@ __global__ __launch_bounds__(1024) void delta_gradient_kernel(DeltaLaunch L, int
             loader.set(L, left_at, next / L.G, next_first, next_n, next % L.G * share);
           if (wave < 2) to_lds(loader.rows, wave * 1024 + lane * 16, decays[after] + wave * 256);
         }
-        loader.load(slabs[turn ^ 1], more ? v0 + 32 : 0);  // behind the last chunk the same again
+        held = loader.load(more ? v0 + 32 : 0, outs[turn ^ 1]);  // behind the last chunk the same again
+        if (v0 == 0 && hs == 0 && wave < MAT / 1024) {
+          const uint8_t* kp = static_cast<const uint8_t*>(L.k) + (first * krow + int64_t(kh) * L.dk) * 2;
+          const uint8_t* qp = static_cast<const uint8_t*>(L.q) + (first * krow + int64_t(kh) * L.dk) * 2;
+          int r, block;
+          lds_place<DK>(wave * 64 + loader.lane, r, block);
+          const int64_t at = (r * krow + block * 8) * 2;
+          const bool keep = r < n && block * 8 < L.dk;
+          to_lds(keep ? kp + at : delta_zeros, ks + wave * 1024);
+          to_lds(keep ? qp + at : delta_zeros, qs + wave * 1024);
+        }
+        __syncthreads();
+        if (v0 == 0) {
+          if (wave == 3 && last_n > 0) finish(decays[before]);
+          bt = row[ROW_BETA * 64 + token];
+        }
         auto tokens16 = [&](int part, int tile) { return columns64(slab.tokens[part], tile); };
-        const bf16x8 wh = tokens16(0, it), wl = tokens16(1, it), zh = tokens16(2, it), zl = tokens16(3, it);
-        const bf16x8 o8 = lds_frag(slab.d + it * 1024 + slab_block(c, g));
+        const bf16x8 o8 = lds_frag(outs[turn] + it * 1024 + slab_block(c, g));
+        {
+          const bf16x8 z3[3] = {tokens16(3, it), tokens16(4, it), tokens16(5, it)};
+#pragma unroll
+          for (int t = 0; t < TILES; ++t) {
+            const bf16x8 s3[3] = {columns(slab.states[0], t), columns(slab.states[1], t), columns(slab.states[2], t)};
+#pragma unroll
+            for (int p = 2; p >= 0; --p) ds[t] = mfma16(s3[p], o8, ds[t]);
+            part_terms<3, 3>([&](auto i, auto j) { xs[t] = mfma16(s3[i.value], z3[j.value], xs[t]); });
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            if (jt0 + j > it) continue;
+            const bf16x8 w3[3] = {tokens16(0, jt0 + j), tokens16(1, jt0 + j), tokens16(2, jt0 + j)};
+            if (kind) {
+              part_terms<3, 3>([&](auto i, auto q) { pair[j] = mfma16(z3[i.value], w3[q.value], pair[j]); });
+            } else {
+#pragma unroll
+              for (int p = 2; p >= 0; --p) pair[j] = mfma16(o8, w3[p], pair[j]);
+            }
+          }
+          if (quarter == 3) {
+            const bf16x8 w3[3] = {tokens16(0, it), tokens16(1, it), tokens16(2, it)};
+            db = dot8(w3, z3, db);
+            bf16x8 dv8;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dv8[e] = bf16(bt * (float(z3[0][e]) + (float(z3[1][e]) + float(z3[2][e]))));
+            if (token < n && v0 + g * 8 < L.dv)
+              *reinterpret_cast<bf16x8*>(reinterpret_cast<uint8_t*>(static_cast<bf16*>(L.dv_out) + first * vrow + int64_t(h) * L.dv + v0) +
+                                         (uint32_t(token) * uint32_t(vrow * 2) + g * 16)) = dv8;
+          }
+        }
+        const bf16x8 w3[3] = {tokens16(0, it), tokens16(1, it), tokens16(2, it)};
 #pragma unroll
         for (int t = 0; t < TILES; ++t) {
-          const bf16x8 sh = columns(slab.states[0], t), sl = columns(slab.states[1], t);
-          ds[t] = mfma16(sh, o8, mfma16(sl, o8, ds[t]));
-          xs[t] = mfma_split_split(sh, sl, zh, zl, xs[t]);
-          const bf16x8 dh = columns(slab.states[2], t), dl = columns(slab.states[3], t);
-          ud[t] = mfma_split_split(dh, dl, wh, wl, ud[t]);
+          const bf16x8 d3[3] = {columns(slab.states[3], t), columns(slab.states[4], t), columns(slab.states[5], t)};
+          part_terms<3, 3>([&](auto i, auto j) { ud[t] = mfma16(d3[i.value], w3[j.value], ud[t]); });
         }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          if (jt0 + j > it) continue;
-          const bf16x8 h8 = tokens16(0, jt0 + j), l8 = tokens16(1, jt0 + j);
-          if (kind)
-            pair[j] = mfma_split_split(zh, zl, h8, l8, pair[j]);
-          else
-            pair[j] = mfma_exact_split(o8, h8, l8, pair[j]);
-        }
-        bf16x8 dv8;
-        if (quarter == 3) {
-          db = dot8(wh, wl, zh, zl, db);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) dv8[e] = bf16(bt * (float(zh[e]) + float(zl[e])));
-        }
-        // <S, dS'> of the slab's 32 rows
-        if (wave < 32 * BLOCKS / 64) {
-          const int p = wave * 1024 + lane * 16;
-          dot = dot8(lds_frag(slab.states[0] + p), lds_frag(slab.states[1] + p), lds_frag(slab.states[2] + p),
-                     lds_frag(slab.states[3] + p), dot);
-        }
-        if (more || v0 == 0) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // K and Q came with the first
-        __syncthreads();
-        if (quarter == 3 && token < n && v0 + g * 8 < L.dv) *reinterpret_cast<bf16x8*>(static_cast<bf16*>(L.dv_out) + (first + token) * vrow + int64_t(h) * L.dv + g * 8 + v0) = dv8;
       }
       part();
       token = it * 16 + c;
-      uint8_t* pairs = reinterpret_cast<uint8_t*>(&slabs[turn ^ 1]);  // the last slab's place
+      uint8_t* pairs = reinterpret_cast<uint8_t*>(&slab);
+      if (L.dv <= 32) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // K and Q, for which no other slab has waited
+      __syncthreads();
       if (quarter == 3) {
         db = xor32_sum(xor16_sum(db));
         if (token < n && g == 0) L.dbeta[(first + token) * L.H + h] = db;

@@ -215,8 +215,8 @@ __global__ __launch_bounds__(256, 1) void delta_chain_back_kernel(DeltaLaunch L,
 // into three parts once for all sixteen waves; the next ones (of the next head, or
 // chunk) are loaded while these are used.  Bound by these loads, 208 KB a chunk and
 // head at 128 x 128, and the products that they wait for: 16384 tokens, 16 heads take
-// 400 us, 1.22 GB at 3.1 TB/s, 23 us a chunk and head on each CU; with two parts,
-// loaded as such, it was 316, and dbeta and dlog alpha 4e-6 to 6e-6 of their norm off
+// 382 us, 1.22 GB at 3.2 TB/s, 22 us a chunk and head on each CU; with two parts,
+// loaded as such, it was 314, and dbeta and dlog alpha 4e-6 to 6e-6 of their norm off
 // (now 1e-6), more where few large terms cancel.  dQ and dK are formed transposed
 // (tokens in lanes), so that a token's factors are a lane's and results leave four at
 // a time.
@@ -377,21 +377,23 @@ __global__ __launch_bounds__(1024) void delta_gradient_kernel(DeltaLaunch L, int
   int64_t last_first = 0;
   int last_n = 0, last_h = 0;
   auto finish = [&](const float* row) {
+    int l = lane;
+    asm volatile("" : "+v"(l));  // or what follows from it is kept in registers through every slab
     // sums over i >= t, and over j < t (not of all up to t less the token's own:
     // its own is far larger where the token forgets much)
     float in = 0.0f, out = 0.0f, all = 0.0f, inside = 0.0f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      in += row_in[i][63 - lane];
-      out += lane ? row_out[i][lane - 1] : 0.0f;
-      inside += pair_sum[i][lane];
+      in += row_in[i][63 - l];
+      out += l ? row_out[i][l - 1] : 0.0f;
+      inside += pair_sum[i][l];
     }
 #pragma unroll
     for (int i = 0; i < 16; ++i) all += dots[i];
-    in = __shfl(wave_scan_incl(in), 63 - lane);
+    in = __shfl(wave_scan_incl(in), 63 - l);
     float da = inside + in + wave_scan_incl(out) + row[ROW_C * 64 + 63] * all;
-    if (lane < last_n) {
-      const int64_t at = (last_first + lane) * L.H + last_h;
+    if (l < last_n) {
+      const int64_t at = (last_first + l) * L.H + last_h;
       if (!L.log_decay) da /= fmaxf(L.alpha[at], 5.42101086e-20f);  // the least decay, 2^-64
       L.dalpha[at] = da;
     }
@@ -456,6 +458,7 @@ __global__ __launch_bounds__(1024) void delta_gradient_kernel(DeltaLaunch L, int
 #pragma unroll
             for (int p = 2; p >= 0; --p) ds[t] = mfma16(s3[p], o8, ds[t]);
             part_terms<3, 3>([&](auto i, auto j) { xs[t] = mfma16(s3[i.value], z3[j.value], xs[t]); });
+            phase();
           }
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
@@ -467,6 +470,7 @@ __global__ __launch_bounds__(1024) void delta_gradient_kernel(DeltaLaunch L, int
 #pragma unroll
               for (int p = 2; p >= 0; --p) pair[j] = mfma16(o8, w3[p], pair[j]);
             }
+            phase();
           }
           if (quarter == 3) {
             const bf16x8 w3[3] = {tokens16(0, it), tokens16(1, it), tokens16(2, it)};
@@ -484,6 +488,7 @@ __global__ __launch_bounds__(1024) void delta_gradient_kernel(DeltaLaunch L, int
         for (int t = 0; t < TILES; ++t) {
           const bf16x8 d3[3] = {columns(slab.states[3], t), columns(slab.states[4], t), columns(slab.states[5], t)};
           part_terms<3, 3>([&](auto i, auto j) { ud[t] = mfma16(d3[i.value], w3[j.value], ud[t]); });
+          phase();
         }
       }
       part();

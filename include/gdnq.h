@@ -677,8 +677,14 @@ gdnq_status gdnq_mx_linear(const gdnq_mx_params* p, const void* x, const uint8_t
  *   dk and dv, rounded once (o in fp32: good to 5e-6), and for what enters a segment
  *   where a call cuts long sequences: 5e-6.
  *   Results do not depend on the order in which workgroups run.  A NaN or
- *   infinity stays in its own sequence and head, and reaches back at most to the
- *   first token of its chunk of 64.
+ *   infinity stays in its own sequence and head (the gradients of q and k: its key
+ *   head), where an infinity may come back as a NaN.  In a forward call it reaches
+ *   back at most to the first token of its chunk of 64; in a backward call dS takes
+ *   it to every chunk before.
+ *   Of up to 64 packed sequences the longest start first, and those far longer than
+ *   the others are cut into segments that run at once; more than 64 run as they lie,
+ *   each 64 rows of a head one after another (16000 tokens beside 64 short sequences
+ *   take 1.9 times as long forward as beside 63).
  *   Outputs must not overlap inputs or each other (but h_out = h).
  *   workspace: gdnq_delta_workspace_size(p, varlen, backward) bytes; its contents
  *   need no initial value.  Calls that may overlap in time take workspaces of

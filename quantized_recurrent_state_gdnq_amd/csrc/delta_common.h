@@ -55,8 +55,8 @@ __host__ __device__ inline int64_t delta_align(int64_t n) { return (n + 255) / 2
 // What a chain leaves of a chunk and head, in fp32: a state, and behind it the
 // chunk's w or z, [d_v][64].  Both are in tiles of 16 rows and 16 columns, a kilobyte,
 // the columns those of a chain's tile (chain_row): a store of a wave is then whole
-// lines (rows as they are leave half a line each: 4 x 8192 tokens, 16 heads, chain 617
-// us, with tiles 542).
+// lines (rows as they are leave half a line each: 4 x 8192 tokens, 16 heads, chain 640
+// us, with tiles 583).
 __host__ __device__ inline int64_t delta_state_floats(const DeltaLaunch& L) {
   return int64_t((L.dv + 15) / 16) * ((L.dk + 31) / 32) * 512;
 }
@@ -163,7 +163,8 @@ __device__ __forceinline__ DeltaSpan delta_sequence(const DeltaLaunch& L, int b)
 // Workgroups that read the same (a key head's) on the same XCD, whose L2 they
 // share: of a grid of units of `size` workgroups, eight units at a time, one for each
 // XCD, as workgroups are dealt out; the last units, fewer than eight, in order.
-// 65536 tokens, 8 heads, first pass 222 -> 203 us; 16384 packed tokens, 16 heads, chain 290 -> 278.
+// 65536 tokens, 8 heads, first pass 216 -> 206 us; 16384 packed tokens, 16 heads, chains 328 -> 317
+// and 334 -> 323.
 __device__ __forceinline__ int xcd_unit(int size, int& within) {
   const int block = int(blockIdx.x), full = int(gridDim.x) / size & ~7;
   if (block < full * size) {
@@ -182,8 +183,10 @@ struct DeltaItem {
 };
 // Of packed sequences (up to 64, a lane each) the longest come first, so that no
 // long chain starts beside the last short ones (12 sequences of 16384 tokens, 16
-// heads: 352 -> 340 us, and 325 -> 314 back).  Malformed offsets can ask for more
-// items or segments than there are: those beyond are left out.
+// heads: 326 -> 317 us, and 336 -> 323 back).  Malformed offsets can ask for more
+// items or segments than there are: those beyond are left out.  More than 64 sequences
+// are taken as they lie, uncut: 16000 tokens and 64 short ones take 867 us forward and
+// 1486 back, with 63 short ones 463 and 1036.
 __device__ __forceinline__ DeltaItem delta_packed(const DeltaLaunch& L, int index, int b, bool pass) {
   const int lane = threadIdx.x & 63;
   const int tokens = lane < L.B ? delta_sequence(L, lane).tokens : -1;

@@ -5,8 +5,8 @@
 // One workgroup of four waves per chunk and value head, six on a CU.  Bound by
 // latency: loads, the scan of the decays, sixteen dependent rows of a
 // substitution and six tile products one after another (vector units 31% busy, LDS
-// 24%); 8192 chunks and heads of 128 take 142 to 149 us, 26 KB written and 16 to 32
-// KB read each at 2.6 to 3.8 TB/s.
+// 24%); 8192 chunks and heads of 128 take 140 to 148 us, 26 KB written (32 backward) and
+// 16 to 32 KB read each at 2.5 to 3.8 TB/s.
 #pragma once
 
 #include "delta_common.h"

@@ -253,7 +253,7 @@ __global__ __launch_bounds__(256, PASS ? 2 : 1) void delta_chain_kernel(DeltaLau
 // ---------------------------------------------------------------- one token
 //
 // Bound by the state's bytes: read once, written once (64 sequences, 32 heads of 128 x
-// 128: 51.5 us, 5.28 TB/s; one sequence of 16 heads: 3.3 us, the launch).  LANES lanes hold a row,
+// 128: 51.7 us, 5.26 TB/s; one sequence of 16 heads: 3.2 us, the launch).  LANES lanes hold a row,
 // eight columns each, and R rows are in flight in a lane.
 template <int LANES, int R, typename E>
 __global__ __launch_bounds__(256) void delta_step_kernel(DeltaLaunch L) {
@@ -347,6 +347,10 @@ hipError_t forward(const DeltaLaunch& L, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// Four rows a lane where that still is 1024 workgroups, four a CU, else one (us with
+// four rows, with one; 128 x 128 unless said): 256 workgroups of four rows 6.7, 6.3; 512
+// 10.2, 9.7; 768 14.0, 14.8; 1024 15.8, 17.6 (64 x 64 9.9, 9.7; 256 x 256 15.4, 17.4); 4096
+// 52.4, 55.4.
 template <int LANES, typename E>
 hipError_t step(DeltaLaunch L, hipStream_t stream) {
   constexpr int ROWS = 256 / LANES;

@@ -12,8 +12,9 @@
 // sines and cosines of their angles into LDS (one of each per token and pair, for
 // all its heads), and its teams take the tokens' rows in turn.
 //   Bound by memory where there is work: 32768 tokens of 40 heads of 128, all columns
-// turned, bf16, take 137 us forward (4.9 TB/s) and 222 back (4.5), a large copy
-// 5.14 TB/s; 64 tokens of 32 heads take 6.2, a launch and two dependent loads.
+// turned, bf16, take 146 us forward (4.6 TB/s) and 240 back (4.2), the medians of 20,
+// at best 137 (4.9) and 224 (4.5); a large copy 5.14 TB/s; 64 tokens of 32 heads take
+// 6.2, a launch and two dependent loads.
 //   WIDE: rows of a multiple of 8 columns, 16-byte aligned: a lane holds eight
 // adjacent columns, and partners half the rotated columns apart are in another
 // lane's same register where that half is a multiple of 8.  Else a lane holds
@@ -306,11 +307,14 @@ __global__ __launch_bounds__(1024) void qk_weights_kernel(const float* __restric
 constexpr int MAX_GRID = 1024;  // of the backward pass, as many as the CUs hold: rows of partial sums
 
 // Tokens of a workgroup: more share a launch's fixed costs and the table's
-// barrier, fewer spread a small call over the chip; the table fits 16 KB.
+// barrier, fewer spread a small call over the chip; the table is 16 KB at most (8
+// tokens, 512 columns).  As many as leave 1024 workgroups, up to 8 (us forward / back of
+// 32 heads of 128, all turned, with 1, 2, 4 and 8): 64 tokens 5.1 / 4.7, 6.4 / 6.2,
+// 8.8 / 9.1, 13.9 / 15.1; 2048 20.6 / 12.8, 15.1 / 11.7, 13.4 / 13.8, 16.0 / 21.1; 8192
+// 67.7 / 38.4, 42.2 / 34.7, 32.5 / 34.3, 30.1 / 35.2.
 int group_of(const QkLaunch& L) {
   int group = 8;
   while (group > 1 && (L.R + group - 1) / group < 1024) group /= 2;
-  while (group > 1 && group * L.rotary > 4096) group /= 2;
   return group;
 }
 

@@ -21,7 +21,7 @@ namespace {
 //   Bound by one wave a SIMD: a chunk is 176 matrix instructions of 16 cycles and
 // about 900 others in a chain of products of which each needs the one before, 3.4
 // us a chunk of 128 x 128; with SAVE (96 KB more to store a chunk and head) 4.6.
-// 4 x 8192 tokens, 16 heads: 442 us, 755 MB of memory at 1.7 TB/s, with half of the
+// 4 x 8192 tokens, 16 heads: 434 us, 755 MB of memory at 1.7 TB/s, with half of the
 // CUs idle: there are no more rows, and segments would be 1.9 times the work.  The
 // third part of S, x and w is 44 of the products and 70 of the microseconds: without
 // it the state is 4e-6 of its norm off, with it 1e-6.
@@ -253,7 +253,7 @@ __global__ __launch_bounds__(256, PASS ? 2 : 1) void delta_chain_kernel(DeltaLau
 // ---------------------------------------------------------------- one token
 //
 // Bound by the state's bytes: read once, written once (64 sequences, 32 heads of 128 x
-// 128: 51.7 us, 5.26 TB/s; one sequence of 16 heads: 3.2 us, the launch).  LANES lanes hold a row,
+// 128: 51.5 us, 5.29 TB/s; one sequence of 16 heads: 3.5 us, the launch).  LANES lanes hold a row,
 // eight columns each, and R rows are in flight in a lane.
 template <int LANES, int R, typename E>
 __global__ __launch_bounds__(256) void delta_step_kernel(DeltaLaunch L) {

@@ -215,8 +215,8 @@ __global__ __launch_bounds__(256, 1) void delta_chain_back_kernel(DeltaLaunch L,
 // into three parts once for all sixteen waves; the next ones (of the next head, or
 // chunk) are loaded while these are used.  Bound by these loads, 208 KB a chunk and
 // head at 128 x 128, and the products that they wait for: 16384 tokens, 16 heads take
-// 382 us, 1.22 GB at 3.2 TB/s, 22 us a chunk and head on each CU; with two parts,
-// loaded as such, it was 314, and dbeta and dlog alpha 4e-6 to 6e-6 of their norm off
+// 390 us, 1.17 GB at 3.0 TB/s, 22 us a chunk and head on each CU; with two parts,
+// loaded as such, it was 316, and dbeta and dlog alpha 4e-6 to 6e-6 of their norm off
 // (now 1e-6), more where few large terms cancel.  dQ and dK are formed transposed
 // (tokens in lanes), so that a token's factors are a lane's and results leave four at
 // a time.

@@ -49,8 +49,8 @@ __device__ __forceinline__ void load8(const bf16* p, float (&v)[8]) {
 // A row per workgroup of THREADS lanes, EIGHTS times eight values a lane held in
 // registers between the largest value and the codes (EIGHTS = 0: a row longer
 // than that is read twice, the second time in part out of cache).  Bound by memory:
-// 16384 rows of 4096 bf16 take 41 us (36 at best), 4.9 TB/s, of 8192 fp32 126 us, 5.3;
-// of 12288 fp32, read twice, 264 us, 3.8 TB/s of the bytes as read once; 64 rows 3.8.
+// 16384 rows of 4096 bf16 take 40 us (36 at best), 5.0 TB/s, of 8192 fp32 126 us, 5.3;
+// of 12288 fp32, read twice, 264 us, 3.8 TB/s of the bytes as read once; 64 rows 4.0.
 __device__ __forceinline__ uint2 codes8(const float (&v)[8], float scale, bool finite) {
   float c[8];
   codec_codes<8>(v, scale, c);
@@ -191,9 +191,9 @@ __global__ __launch_bounds__(WAVES * 64) void int8_rows_kernel(Int8Launch L, int
 
 // ---------------------------------------------------------------- many rows
 //
-// Bound by the matrix units: 16384 x 8192 x 4096 takes 498 us at best, 2.21 POPS (a
+// Bound by the matrix units: 16384 x 8192 x 4096 takes 492 us at best, 2.24 POPS (a
 // large library product of 8-bit integers reaches 2.18 on this card, 8192 x 8192 x
-// 8192), and 542, 2.03 POPS, as the median of 20 in a row; eight waves of 128 x 64
+// 8192), and 540, 2.04 POPS, as the median of 20 in a row; eight waves of 128 x 64
 // instead of four of 128 x 128 take 1% more.
 //   A workgroup computes BM x BN of y, its WGM x WGN waves an equal part each, in
 // steps of DEPTH values: the step's rows of both operands are loaded straight

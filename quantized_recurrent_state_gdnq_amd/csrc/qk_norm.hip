@@ -12,8 +12,8 @@
 // sines and cosines of their angles into LDS (one of each per token and pair, for
 // all its heads), and its teams take the tokens' rows in turn.
 //   Bound by memory where there is work: 32768 tokens of 40 heads of 128, all columns
-// turned, bf16, take 146 us forward (4.6 TB/s) and 240 back (4.2), the medians of 20,
-// at best 137 (4.9) and 224 (4.5); a large copy 5.14 TB/s; 64 tokens of 32 heads take
+// turned, bf16, take 149 us forward (4.5 TB/s) and 242 back (4.2), the medians of 20,
+// at best 138 (4.9) and 223 (4.5); a large copy 5.14 TB/s; 64 tokens of 32 heads take
 // 6.2, a launch and two dependent loads.
 //   WIDE: rows of a multiple of 8 columns, 16-byte aligned: a lane holds eight
 // adjacent columns, and partners half the rotated columns apart are in another

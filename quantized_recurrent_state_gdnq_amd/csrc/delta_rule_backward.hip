@@ -325,7 +325,7 @@ __device__ __forceinline__ float dot8(const bf16x8 (&a)[3], const bf16x8 (&b)[3]
 
 template <int DK>
 __global__ __launch_bounds__(1024) void delta_gradient_kernel(DeltaLaunch L, int64_t left_at, int items) {
-  constexpr int BLOCKS = DK / 8, KB = DK / 32, TILES = DK / 64;  // tiles of a wave
+  constexpr int KB = DK / 32, TILES = DK / 64;  // tiles of a wave
   constexpr int MAT = 64 * DK * 2;
   static_assert(sizeof(GradientSlab<DK>) >= 4 * 8192, "the triangles take the slab's place");
   __shared__ __attribute__((aligned(1024))) GradientSlab<DK> slab;
